@@ -11,6 +11,9 @@ raise.
 
 Layout BSHD, bf16: q/o/do [B,S,H,D], k/v [B,S,Hkv,D] with H % Hkv == 0 (GQA when
 Hkv < H); lse [B,H,S] fp32.
+
+The operators around it in a decoder block have modules of their own and the same manner:
+rotary positions (``rope``) and the norms joined with the residual stream (``norms``).
 """
 from __future__ import annotations
 
@@ -23,7 +26,8 @@ __all__ = ["fwd", "bwd", "bwd_workspace_bytes", "fwd_workspace_bytes", "status",
            "sched_workers",
            "sched_resolve", "packed_rank", "fwd_varlen", "bwd_varlen", "bwd_varlen_workspace_bytes",
            "bwd_varlen_order_log", "SCHEDULES", "lib",
-           "DashError"]
+           "DashError", "rope_freqs", "rope_fwd", "rope_bwd", "norm_fwd", "norm_bwd",
+           "join_fwd", "join_bwd"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libdash_attn.so")
@@ -42,7 +46,8 @@ EXPORTS = ["dash_attn_fwd_workspace_bytes", "dash_attn_fwd", "dash_attn_bwd_work
            "dash_status_string", "dash_sched_workers", "dash_sched_segments", "dash_sched_steps",
            "dash_sched_step", "dash_sched_grid", "dash_sched_packed_rank", "dash_sched_resolve",
            "dash_attn_bwd_noalloc", "dash_attn_bwd_varlen_workspace_bytes",
-           "dash_attn_fwd_varlen", "dash_attn_bwd_varlen", "dash_attn_bwd_varlen_order_log"]
+           "dash_attn_fwd_varlen", "dash_attn_bwd_varlen", "dash_attn_bwd_varlen_order_log",
+           "dash_rope", "dash_join_fwd", "dash_join_bwd", "dash_join_bwd_workspace_bytes"]
 
 
 class DashError(RuntimeError):
@@ -121,6 +126,18 @@ def lib() -> ctypes.CDLL:
         L.dash_sched_packed_rank.restype = i
         L.dash_sched_resolve.argtypes = [i, i, i, i, i]
         L.dash_sched_resolve.restype = i
+        ll = ctypes.c_longlong
+        L.dash_rope.argtypes = [vp, i, i, i, i, i, i, vp, f, vp, i, ll, ll, ll, i, vp]
+        L.dash_rope.restype = i
+        llp = ctypes.POINTER(ll)
+        L.dash_join_fwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, ll, i, ll, llp, f, f, f, i,
+                                    i, vp]
+        L.dash_join_fwd.restype = i
+        L.dash_join_bwd_workspace_bytes.argtypes = [ll, i, ll, i, i]
+        L.dash_join_bwd_workspace_bytes.restype = sz
+        L.dash_join_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ll, i,
+                                    ll, llp, f, f, i, i, vp, sz, vp]
+        L.dash_join_bwd.restype = i
         _lib = L
         return L
 
@@ -428,3 +445,7 @@ def bwd_varlen_order_log(q, k, v, o, do, lse, cu_seqlens, causal: bool = False,
                                       stream, None, None, None, None, order)
     status(ws, stream)
     return dq, dk, dv, order
+
+
+from .norms import join_bwd, join_fwd, norm_bwd, norm_fwd  # noqa: E402
+from .rope import rope_bwd, rope_freqs, rope_fwd  # noqa: E402

@@ -17,7 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdash_attn.so")
-SOURCES = ["api.cu", "bwd.cu", "bwd_varlen.cu", "fwd.cu", "aux.cu", "noalloc.cu"]
+SOURCES = ["api.cu", "bwd.cu", "bwd_varlen.cu", "fwd.cu", "aux.cu", "noalloc.cu",
+           "rope.cu", "norm.cu", "norm_bf16.cu", "norm_fp16.cu", "norm_fp32.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

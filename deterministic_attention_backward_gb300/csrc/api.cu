@@ -1,51 +1,25 @@
 // api.cu -- the extern "C" boundary of libdash_attn.so (declared in include/dash_attn.h):
 // argument validation, workspace carving, TMA descriptor construction and the launch
 // sequence of the forward and backward passes.  No device memory is allocated here.
-#include <cudaTypedefs.h>
-
-#include <atomic>
 #include <cmath>
-#include <mutex>
 
 #include "common.cuh"
 #include "dash_attn.h"
+#include "host.cuh"
 #include "sched.cuh"
 
 namespace {
 
+using dash::align256;
+using dash::aligned16;
+using dash::aligned4;
+using dash::device_info;
+using dash::DevInfo;
+using dash::g_wait_ns;
+using dash::kStatusBytes;
 using dash::kTile;
-
-// ------------------------------------------------------------------ driver entry point
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-std::once_flag g_encode_once;
-
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  std::call_once(g_encode_once, [] {
-    void *fn = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  });
-  return g_encode;
-}
-
-// [B, S, Hx, D] bf16 viewed as a 4-D tensor (D, Hx, S, B); box = 64 columns x 1 head x 128
-// rows x 1 batch, 128-byte swizzle: one box lands in shared memory as 128 rows of 128 bytes.
-// Rows of a tile past S (S not a multiple of 128) are outside the tensor and read as zeros.
-bool make_bshd_map(CUtensorMap *m, const void *base, int B, int S, int Hx, int D) {
-  auto enc = tensor_map_encoder();
-  if (!enc) return false;
-  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)Hx, (cuuint64_t)S, (cuuint64_t)B};
-  const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)Hx * D * 2,
-                                 (cuuint64_t)S * Hx * D * 2};
-  const cuuint32_t box[4] = {(cuuint32_t)dash::kBoxCols, 1, (cuuint32_t)kTile, 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box,
-             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
+using dash::make_bshd_map;
+using dash::tensor_map_encoder;
 
 // [T, Hx, D] bf16 packed tokens viewed as a 3-D tensor (D, Hx, T), same box and swizzle as
 // make_bshd_map.  Rows past T read as zeros; a sequence's rows past its end are the next
@@ -62,36 +36,8 @@ bool make_thd_map(CUtensorMap *m, const void *base, int T, int Hx, int D) {
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// ------------------------------------------------------------------ device properties
-struct DevInfo {
-  int sms = 0, major = 0, minor = 0;
-};
-std::mutex g_dev_mu;
-DevInfo g_dev[64];
-
-dash_status_t device_info(DevInfo *out) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DASH_ERR_CUDA;
-  std::lock_guard<std::mutex> lk(g_dev_mu);
-  DevInfo &d = g_dev[dev];
-  if (d.sms == 0) {
-    if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&d.major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&d.minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) {
-      d.sms = 0;
-      return DASH_ERR_CUDA;
-    }
-  }
-  *out = d;
-  // kernels are built for sm_103a only
-  return (d.major == 10 && d.minor == 3) ? DASH_OK : DASH_ERR_UNSUPPORTED;
-}
-
 // ------------------------------------------------------------------ validation / workspace
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 int tiles(int S) { return (S + kTile - 1) / kTile; }  // N: a last, partial tile counts
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 dash_status_t check_sizes(int B, int S, int H, int group, int D) {
   if (B <= 0 || S <= 0 || H <= 0 || group <= 0 || D <= 0) return DASH_ERR_INVALID;
@@ -103,8 +49,6 @@ dash_status_t check_sizes(int B, int S, int H, int group, int D) {
     return DASH_ERR_UNSUPPORTED;
   return DASH_OK;
 }
-
-constexpr size_t kStatusBytes = 256;
 
 struct BwdWorkspace {
   uint32_t *status;
@@ -141,9 +85,6 @@ BwdWorkspace carve_tiles(void *ws, size_t ntiles, int D) {
 BwdWorkspace carve_bwd(void *ws, int B, int S, int H, int D) {
   return carve_tiles(ws, (size_t)B * H * tiles(S), D);
 }
-
-// Limit of one bounded wait inside the kernels (dash_attn_set_wait_limit).
-std::atomic<unsigned long long> g_wait_ns{2000000000ull};
 
 #ifdef DASH_TRACE_BUILD
 unsigned long long *g_trace = nullptr;  // development trace build only

@@ -1,0 +1,170 @@
+// norm.cu -- the extern "C" entries of the row norms: argument checks, the partition of the
+// rows among CTAs, the choice of vector width.
+#include "norm.cuh"
+
+#include "common.cuh"
+#include "dash_attn.h"
+#include "elem.cuh"
+#include "host.cuh"
+
+namespace dash {
+
+// CTAs per gate group of the backward: about two 512-thread CTAs on each of 152 SMs in all,
+// more where a CTA is smaller; never more than there are rows for.
+int norm_bwd_ctas(long long rows, long long groups, int C, int elem_bytes, bool wide) {
+  const int n = wide ? C * elem_bytes / 16 : C;
+  const long long total = n <= 128 ? 2 * kNormSlots : n <= 256 ? 3 * kNormSlots
+                          : n <= 512 ? 2 * kNormSlots : kNormSlots;
+  const long long per = rows / groups, at_once = n <= 128 ? 8 : 1;
+  const long long most = (per + at_once - 1) / at_once;
+  const long long want = total / groups;
+  return (int)(want < 1 ? 1 : want < most ? want : most);
+}
+
+namespace {
+
+bool elem_ok(int t) { return t == DASH_BF16 || t == DASH_FP16 || t == DASH_FP32; }
+int elem_size(int t) { return t == DASH_FP32 ? 4 : 2; }
+
+// Whether every pointer (null ones aside) is aligned to `size` bytes.
+template <int N>
+bool all_aligned(const void *const (&ptrs)[N], uintptr_t size) {
+  uintptr_t any = 0;
+  for (const void *q : ptrs) any |= reinterpret_cast<uintptr_t>(q);
+  return (any & (size - 1)) == 0;
+}
+
+dash_status_t check_rows(long long rows, int C, long long gate_rows, bool gate, int dtype,
+                         int wdtype) {
+  if (rows <= 0 || C <= 0 || !elem_ok(dtype) || (wdtype != dtype && wdtype != DASH_FP32))
+    return DASH_ERR_INVALID;
+  if (gate && (gate_rows <= 0 || rows % gate_rows)) return DASH_ERR_INVALID;
+  if (rows >= (1LL << 31) || C > (1 << 24)) return DASH_ERR_UNSUPPORTED;
+  return DASH_OK;
+}
+
+struct Groups {
+  int groups, ctas, row_gate;
+  long long gate_rows;
+};
+Groups make_groups(long long rows, int C, long long gate_rows, bool gate, int dtype, bool wide) {
+  Groups g{1, 1, gate && gate_rows == 1 && rows > 1, rows};
+  if (gate && !g.row_gate) g.gate_rows = gate_rows;
+  g.groups = (int)(rows / g.gate_rows);
+  g.ctas = norm_bwd_ctas(rows, g.groups, C, elem_size(dtype), wide);
+  return g;
+}
+
+}  // namespace
+}  // namespace dash
+
+extern "C" {
+
+dash_status_t dash_join_fwd(const void *x, const void *a, const void *w_post, const void *gate,
+                            const void *w_next, void *y, void *h, float *rstd_a, float *rstd_y,
+                            long long rows, int C, long long gate_rows,
+                            const long long strides[4], float skip_scale, float branch_scale,
+                            float eps, dash_dtype_t dtype, dash_dtype_t wdtype,
+                            dash_stream_t stream) {
+  using namespace dash;
+  dash_status_t st = check_rows(rows, C, gate_rows, gate != nullptr, dtype, wdtype);
+  if (st != DASH_OK) return st;
+  const bool join = a != nullptr;
+  if (!x || !strides || (join ? !y : !w_next || w_post || gate)) return DASH_ERR_INVALID;
+  if ((w_next && (!h || !rstd_y)) || (w_post && !rstd_a)) return DASH_ERR_INVALID;
+  const int size = elem_size(dtype), vec = 16 / size;
+  const void *rowp[] = {x, a, y, w_next ? h : nullptr}, *wp[] = {w_post, gate, w_next};
+  const void *fp[] = {rstd_a, rstd_y};
+  if (!all_aligned(rowp, size) || !all_aligned(wp, elem_size(wdtype)) || !all_aligned(fp, 4))
+    return DASH_ERR_INVALID;
+  const bool wide = C % vec == 0 && all_aligned(rowp, 16) && all_aligned(wp, 16) &&
+                    (strides[0] | strides[1] | strides[2] | strides[3]) % vec == 0;
+  DevInfo dev;
+  if ((st = device_info(&dev)) != DASH_OK) return st;
+  NormFwdParams p{};
+  p.x = x, p.a = a, p.w_post = w_post, p.gate = gate, p.w_next = w_next;
+  p.y = y, p.h = h, p.rstd_a = rstd_a, p.rstd_y = rstd_y;
+  p.xs = strides[0], p.as = strides[1], p.ys = strides[2], p.hs = strides[3];
+  p.rows = rows;
+  p.gate_rows = gate ? gate_rows : rows;
+  p.C = C;
+  p.wf32 = wdtype == DASH_FP32 && dtype != DASH_FP32;
+  p.skip = skip_scale, p.branch = branch_scale, p.eps = eps;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == DASH_BF16   ? launch_norm_fwd<__nv_bfloat16>(p, join, wide, s)
+                        : dtype == DASH_FP16 ? launch_norm_fwd<__half>(p, join, wide, s)
+                                             : launch_norm_fwd<float>(p, join, wide, s);
+  return e == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+}
+
+size_t dash_join_bwd_workspace_bytes(long long rows, int C, long long gate_rows, int join,
+                                     dash_dtype_t dtype) {
+  using namespace dash;
+  if (check_rows(rows, C, gate_rows, gate_rows > 0, dtype, dtype) != DASH_OK) return 0;
+  size_t most = 0;
+  for (const bool wide : {false, true}) {
+    const Groups g = make_groups(rows, C, gate_rows, gate_rows > 0, dtype, wide);
+    const size_t n = align256((size_t)g.groups * g.ctas * (join ? 2 : 1) * C * sizeof(float));
+    most = n > most ? n : most;
+  }
+  return most;
+}
+
+dash_status_t dash_join_bwd(const void *dy, const void *dh, const void *y, const void *a,
+                            const void *w_post, const void *gate, const void *w_next,
+                            const float *rstd_a, const float *rstd_y, void *dx, void *da,
+                            void *dw_post, void *dgate, void *dw_next, long long rows, int C,
+                            long long gate_rows, const long long strides[6], float skip_scale,
+                            float branch_scale, dash_dtype_t dtype, dash_dtype_t wdtype,
+                            void *workspace, size_t workspace_bytes, dash_stream_t stream) {
+  using namespace dash;
+  dash_status_t st = check_rows(rows, C, gate_rows, gate != nullptr, dtype, wdtype);
+  if (st != DASH_OK) return st;
+  const bool join = a != nullptr;
+  if (!dx || !strides || (join ? !da || (!dy && !w_next) : !w_next || w_post || gate))
+    return DASH_ERR_INVALID;
+  if (w_next && (!dh || !y || !rstd_y || !dw_next)) return DASH_ERR_INVALID;
+  if ((w_post && (!rstd_a || !dw_post)) || (gate && !dgate)) return DASH_ERR_INVALID;
+  const int size = elem_size(dtype), vec = 16 / size;
+  const void *rowp[] = {dy, w_next ? dh : nullptr, w_next ? y : nullptr, a, dx, join ? da : nullptr};
+  const void *wp[] = {w_post, gate, w_next};
+  const void *dwp[] = {w_post ? dw_post : nullptr, gate ? dgate : nullptr,
+                       w_next ? dw_next : nullptr};
+  const void *fp[] = {rstd_a, rstd_y};
+  if (!all_aligned(rowp, size) || !all_aligned(wp, elem_size(wdtype)) ||
+      !all_aligned(dwp, elem_size(wdtype)) || !all_aligned(fp, 4))
+    return DASH_ERR_INVALID;
+  if (!workspace || !aligned16(workspace) ||
+      workspace_bytes < dash_join_bwd_workspace_bytes(rows, C, gate ? gate_rows : 0, join, dtype))
+    return DASH_ERR_WORKSPACE;
+  long long any = 0;
+  for (int i = 0; i < 6; ++i) any |= strides[i];
+  const bool wide = C % vec == 0 && all_aligned(rowp, 16) && all_aligned(wp, 16) && any % vec == 0;
+  DevInfo dev;
+  if ((st = device_info(&dev)) != DASH_OK) return st;
+  const Groups g = make_groups(rows, C, gate_rows, gate != nullptr, dtype, wide);
+  NormBwdParams p{};
+  p.dy = dy, p.dh = dh, p.y = y, p.a = a;
+  p.w_post = w_post, p.gate = gate, p.w_next = w_next;
+  p.rstd_a = rstd_a, p.rstd_y = rstd_y;
+  p.dx = dx, p.da = da;
+  p.dw_post = w_post ? dw_post : nullptr;
+  p.dgate = gate ? dgate : nullptr;
+  p.dw_next = w_next ? dw_next : nullptr;
+  p.part = static_cast<float *>(workspace);
+  p.dys = strides[0], p.dhs = strides[1], p.ys = strides[2], p.as = strides[3];
+  p.dxs = strides[4], p.das = strides[5];
+  p.rows = rows;
+  p.gate_rows = g.gate_rows;
+  p.groups = g.groups, p.ctas = g.ctas, p.row_gate = g.row_gate;
+  p.C = C;
+  p.wf32 = wdtype == DASH_FP32 && dtype != DASH_FP32;
+  p.skip = skip_scale, p.branch = branch_scale;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == DASH_BF16   ? launch_norm_bwd<__nv_bfloat16>(p, join, wide, s)
+                        : dtype == DASH_FP16 ? launch_norm_bwd<__half>(p, join, wide, s)
+                                             : launch_norm_bwd<float>(p, join, wide, s);
+  return e == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+}
+
+}  // extern "C"

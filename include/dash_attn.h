@@ -300,6 +300,76 @@ dash_status_t dash_attn_bwd_varlen_order_log(const void *q, const void *k, const
                                              void *workspace, size_t workspace_bytes,
                                              int *order_log, dash_stream_t stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Operators around the attention in a decoder block: rotary positions, norms joined with the
+ * residual stream, differential attention.  They keep the conventions above (caller-owned
+ * device memory, argument errors before anything is enqueued, work on `stream` of the current
+ * device), with these element types: */
+typedef enum { DASH_BF16 = 0, DASH_FP16 = 1, DASH_FP32 = 2 } dash_dtype_t;
+
+/* Rotary positions.  One part is a tensor [B, S, heads, D] (element strides of batch, token
+ * and head; the D elements of a head are contiguous), read at `in` and written at `out`.
+ * turn != 0: the head's first `rot` elements turn with the token's position, the others pass;
+ * turn == 0: the part is copied (the values of a qkv product, so that one call leaves q, k
+ * and v as the contiguous tensors attention reads).  `out` is `in` itself (with the same
+ * strides) or memory that no part reads, and no two of its elements share an address. */
+typedef struct {
+  const void *in;
+  void *out;
+  int heads, D, turn;
+  long long in_stride[3], out_stride[3]; /* batch, token, head */
+} dash_rope_part_t;
+/* Pair p of a head: elements p and p + rot/2 (half), or 2p and 2p + 1 (interleaved). */
+typedef enum { DASH_ROPE_HALF = 0, DASH_ROPE_INTERLEAVED = 1 } dash_rope_layout_t;
+
+/* Pair p (x, y) becomes magnitude * (x cos a - y sin a, y cos a + x sin a) with the angle
+ * a = position * inv_freq[p] (radians; device array of rot/2 doubles); backward != 0 turns by
+ * -a, which is the gradient.  The angle is formed in 64-bit fixed point modulo one turn, so
+ * far positions lose nothing.  Positions: device int32 (positions64 == 0) or int64, the
+ * token's at element b * pos_stride_b + s * pos_stride_t, or NULL for start + s.  Arithmetic
+ * in fp32, one rounding at the end.  1 to 3 parts of one element type; rot even, <= 1024. */
+dash_status_t dash_rope(const dash_rope_part_t *parts, int nparts, int B, int S, int rot,
+                        dash_rope_layout_t layout, dash_dtype_t dtype, const double *inv_freq,
+                        float magnitude, const void *positions, int positions64,
+                        long long pos_stride_b, long long pos_stride_t, long long start,
+                        int backward, dash_stream_t stream);
+
+/* Norm of rows, and the join of a residual stream with a branch between two norms.  With
+ * rstd(v) = (mean(v^2) + eps)^-1/2 over the C elements of a row:
+ *   y = skip_scale * x + branch_scale * gate * (a * rstd(a) * w_post)
+ *   h = y * rstd(y) * w_next                                        (y before its rounding)
+ * a NULL: a plain norm, y = x is not written and h = x rstd(x) w_next.  w_post NULL: the branch
+ * is not normed; gate NULL: 1; w_next NULL: no h.  Tensors are `rows` rows of C contiguous
+ * elements, the row strides (in elements) of x, a, y, h in `strides`; rstd_a and rstd_y
+ * [rows] fp32 are kept for the backward (each written only where its norm is asked for).  The
+ * weights [C] are of the rows' type or all fp32; gate is [rows / gate_rows, C], each row of it
+ * serving gate_rows consecutive rows.  y and h may each be x or a itself (with the same stride),
+ * not both the same.  fp32 arithmetic, one rounding per output. */
+dash_status_t dash_join_fwd(const void *x, const void *a, const void *w_post, const void *gate,
+                            const void *w_next, void *y, void *h, float *rstd_a, float *rstd_y,
+                            long long rows, int C, long long gate_rows,
+                            const long long strides[4], float skip_scale, float branch_scale,
+                            float eps, dash_dtype_t dtype, dash_dtype_t wdtype,
+                            dash_stream_t stream);
+/* Bytes of device workspace of dash_join_bwd (the CTAs' partial sums of the weight gradients);
+ * gate_rows 0 where there is no gate, join 0 for a plain norm; 0 on bad sizes. */
+size_t dash_join_bwd_workspace_bytes(long long rows, int C, long long gate_rows, int join,
+                                     dash_dtype_t dtype);
+/* Gradient of dash_join_fwd: dy, dh are the gradients of y and h (dy may be NULL where nothing
+ * else uses y; dh is read where w_next is given), y the forward's output (x for a plain norm,
+ * whose dy is added to dx: the gradient of the residual stream beside the norm), a the branch.
+ * Writes dx, da and, in the weights' type, dw_post, dgate, dw_next (each where its weight is
+ * given).  Row strides of dy, dh, y, a, dx, da in `strides`.  dx and da may each be an input
+ * itself, not both the same.  The weight gradients are summed in an order that the sizes alone fix: the
+ * same bits on every run. */
+dash_status_t dash_join_bwd(const void *dy, const void *dh, const void *y, const void *a,
+                            const void *w_post, const void *gate, const void *w_next,
+                            const float *rstd_a, const float *rstd_y, void *dx, void *da,
+                            void *dw_post, void *dgate, void *dw_next, long long rows, int C,
+                            long long gate_rows, const long long strides[6], float skip_scale,
+                            float branch_scale, dash_dtype_t dtype, dash_dtype_t wdtype,
+                            void *workspace, size_t workspace_bytes, dash_stream_t stream);
+
 /* Human-readable name of a status code (static storage). */
 const char *dash_status_string(dash_status_t status);
 
