@@ -13,7 +13,8 @@ Layout BSHD, bf16: q/o/do [B,S,H,D], k/v [B,S,Hkv,D] with H % Hkv == 0 (GQA when
 Hkv < H); lse [B,H,S] fp32.
 
 The operators around it in a decoder block have modules of their own and the same manner:
-rotary positions (``rope``) and the norms joined with the residual stream (``norms``).
+rotary positions (``rope``), the norms joined with the residual stream (``norms``) and
+differential attention, the difference of two softmax maps (``diff``).
 """
 from __future__ import annotations
 
@@ -27,7 +28,7 @@ __all__ = ["fwd", "bwd", "bwd_workspace_bytes", "fwd_workspace_bytes", "status",
            "sched_resolve", "packed_rank", "fwd_varlen", "bwd_varlen", "bwd_varlen_workspace_bytes",
            "bwd_varlen_order_log", "SCHEDULES", "lib",
            "DashError", "rope_freqs", "rope_fwd", "rope_bwd", "norm_fwd", "norm_bwd",
-           "join_fwd", "join_bwd"]
+           "join_fwd", "join_bwd", "diff_fwd", "diff_bwd", "diff_bwd_workspace_bytes"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libdash_attn.so")
@@ -47,7 +48,9 @@ EXPORTS = ["dash_attn_fwd_workspace_bytes", "dash_attn_fwd", "dash_attn_bwd_work
            "dash_sched_step", "dash_sched_grid", "dash_sched_packed_rank", "dash_sched_resolve",
            "dash_attn_bwd_noalloc", "dash_attn_bwd_varlen_workspace_bytes",
            "dash_attn_fwd_varlen", "dash_attn_bwd_varlen", "dash_attn_bwd_varlen_order_log",
-           "dash_rope", "dash_join_fwd", "dash_join_bwd", "dash_join_bwd_workspace_bytes"]
+           "dash_rope", "dash_join_fwd", "dash_join_bwd", "dash_join_bwd_workspace_bytes",
+           "dash_diff_fwd_workspace_bytes", "dash_diff_fwd", "dash_diff_bwd_workspace_bytes",
+           "dash_diff_bwd"]
 
 
 class DashError(RuntimeError):
@@ -138,6 +141,13 @@ def lib() -> ctypes.CDLL:
         L.dash_join_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ll, i,
                                     ll, llp, f, f, i, i, vp, sz, vp]
         L.dash_join_bwd.restype = i
+        for name in ("dash_diff_fwd_workspace_bytes", "dash_diff_bwd_workspace_bytes"):
+            getattr(L, name).argtypes = [i, i, i, i]
+            getattr(L, name).restype = sz
+        L.dash_diff_fwd.argtypes = [vp] * 7 + [i, i, i, i, i, f, i, i, i, vp, sz, vp]
+        L.dash_diff_fwd.restype = i
+        L.dash_diff_bwd.argtypes = [vp] * 12 + [i, i, i, i, i, f, i, i, i, vp, sz, vp]
+        L.dash_diff_bwd.restype = i
         _lib = L
         return L
 
@@ -447,5 +457,6 @@ def bwd_varlen_order_log(q, k, v, o, do, lse, cu_seqlens, causal: bool = False,
     return dq, dk, dv, order
 
 
+from .diff import diff_bwd, diff_bwd_workspace_bytes, diff_fwd  # noqa: E402
 from .norms import join_bwd, join_fwd, norm_bwd, norm_fwd  # noqa: E402
 from .rope import rope_bwd, rope_freqs, rope_fwd  # noqa: E402

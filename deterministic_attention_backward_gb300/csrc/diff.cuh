@@ -1,0 +1,103 @@
+// diff.cuh -- differential attention: parameters, launch interface and the small device
+// helpers its kernels share.
+//
+//   O = P1 V - lam P2 V,   Pm = softmax(c Qm Km^T + mask)
+// Head pair h holds the query maps 2h and 2h+1 (d elements each, neighbours in memory), the key
+// maps of its KV head likewise, and a value head of dv = 2d: every operand is a [B, S, heads,
+// 2d] tensor of the plain attention, so the same TMA boxes bring it in, and map m is columns
+// [m d, (m+1) d) of a Q or K tile.
+#pragma once
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace dash {
+
+struct DiffFwdParams {
+  __nv_bfloat16 *o, *o2;  // [B,S,H,2d]
+  float *lse;             // [B,2H,S]
+  const void *lam;        // [H] or [B,S,H], bf16 or fp32
+  uint32_t *status;
+  int B, S, H, Hkv, G, N, causal;
+  int lam_f32, lam_token;
+  unsigned long long wait_ns;
+  float scale_log2;       // softmax scale * log2(e)
+};
+
+// Row vectors of the backward, per (batch, head pair) padded to whole tiles:
+//   rowv = {LSE1 log2e, LSE2 log2e, D1, D2}, Dm = dO . Om, and lam; rows past S hold
+//   {inf, inf, 0, 0} and 0, which give them no weight.
+struct DiffBwdParams {
+  const __nv_bfloat16 *o, *o2, *dout;
+  const float *lse;
+  const void *lam;
+  float4 *rowv;           // [B,H,N*128]
+  float *lamv;            // [B,H,N*128]
+  float *dlam_part;       // [B,H,N] (weights per head only)
+  uint32_t *status;
+  __nv_bfloat16 *dq, *dk, *dv;
+  void *dlam;             // [H] or [B,S,H], lam's type
+  int B, S, H, Hkv, G, N, causal;
+  int lam_f32, lam_token;
+  unsigned long long wait_ns;
+  float scale_log2, scale;
+};
+
+cudaError_t launch_diff_fwd(int d, const CUtensorMap &tq, const CUtensorMap &tk,
+                            const CUtensorMap &tv, const DiffFwdParams &p, cudaStream_t s);
+cudaError_t launch_diff_bwd(int d, const CUtensorMap &tq, const CUtensorMap &tk,
+                            const CUtensorMap &tv, const CUtensorMap &tdo,
+                            const DiffBwdParams &p, cudaStream_t s);
+
+#ifdef __CUDACC__
+__device__ __forceinline__ float lam_at(const void *lam, int f32, size_t at) {
+  return f32 ? static_cast<const float *>(lam)[at]
+             : __bfloat162float(static_cast<const __nv_bfloat16 *>(lam)[at]);
+}
+
+// tcgen05.wait::ld that the 32 loaded registers depend on, so that no use moves above it.
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(
+          taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+      "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]),
+      "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
+      "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+
+// Byte offset of element column `col` (a multiple of 16) of row 0 in a [128 x 2d] operand tile
+// of 64-column boxes.
+__device__ __forceinline__ constexpr uint32_t col_bytes(int col) {
+  return (uint32_t)(col >> 6) * kBoxBytes + (uint32_t)(col & 63) * 2;
+}
+
+// 32 fp32 columns of this thread's row, scaled, as 32 bf16 at dst (16-byte aligned).
+__device__ __forceinline__ void store_row32(__nv_bfloat16 *dst, const uint32_t (&v)[32],
+                                            float scale) {
+  uint32_t pk[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    pk[i] = pack_bf16(__uint_as_float(v[2 * i]) * scale, __uint_as_float(v[2 * i + 1]) * scale);
+  uint4 *d4 = reinterpret_cast<uint4 *>(dst);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    d4[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+}
+#endif
+
+}  // namespace dash

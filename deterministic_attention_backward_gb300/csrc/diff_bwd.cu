@@ -1,0 +1,707 @@
+// diff_bwd.cu -- differential attention backward, deterministic without any ordering between
+// CTAs: one kernel stationary in queries accumulates dQ, one stationary in keys accumulates
+// dK and dV, each on chip in the order of its own loop.
+//
+// With dP = dO V^T (both maps share it), Dm = dO . Om, and ~ for the rounding to bf16 that the
+// tensor core asks for:
+//   dS1 = P1 (dP - D1)       dS2 = -lam P2 (dP - D2)        dlam_i = - sum_j P2 dP
+//   dQm = c ~dSm Km          dKm = c ~dSm^T Qm              dV = ~(P1 - lam P2)^T dO
+// Splitting the pass recomputes S1, S2 and dP (512 of then 1792 flops a pair at d = 64), and
+// avoids what a single key-stationary kernel pays on this GPU: fp32 dQ partials pushed into L2
+// at 16-20 bytes a cycle and SM, 64 KB a tile pair, longer than all of a tile pair's products,
+// and their ordering.
+#include "diff.cuh"
+
+namespace dash {
+namespace {
+
+constexpr int kThreads = 320;
+
+// -------------------------------------------------------------------- row vectors
+// One group of DV / 8 lanes per row of [B, S, H], rows in memory order (coalesced reads).
+template <int d>
+__global__ void __launch_bounds__(256) diff_rows_kernel(const DiffBwdParams p) {
+  constexpr int DV = 2 * d, kLanes = DV / 8;
+  const int lane = threadIdx.x % kLanes;
+  const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / kLanes;
+  const int Sp = p.N * kTile;
+  const long long rows = (long long)p.B * Sp * p.H;
+  const bool in = row < rows;
+  const int h = in ? (int)(row % p.H) : 0;
+  const long long t = in ? row / p.H : 0;
+  const int i = (int)(t % Sp), b = (int)(t / Sp);
+  const bool real = in && i < p.S;
+  float d1 = 0.f, d2 = 0.f;
+  const size_t at = (size_t)b * p.S + i;
+  float lam = 0.f;
+  if (real) {
+    lam = lam_at(p.lam, p.lam_f32, p.lam_token ? at * p.H + h : (size_t)h);
+    const size_t off = (at * p.H + h) * DV + lane * 8;
+    const uint4 g = *reinterpret_cast<const uint4 *>(p.dout + off);
+    const uint4 x = *reinterpret_cast<const uint4 *>(p.o + off);
+    const uint4 y = *reinterpret_cast<const uint4 *>(p.o2 + off);
+    const __nv_bfloat162 *g2 = reinterpret_cast<const __nv_bfloat162 *>(&g);
+    const __nv_bfloat162 *x2 = reinterpret_cast<const __nv_bfloat162 *>(&x);
+    const __nv_bfloat162 *y2 = reinterpret_cast<const __nv_bfloat162 *>(&y);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 a = __bfloat1622float2(g2[e]), u = __bfloat1622float2(x2[e]),
+                   w = __bfloat1622float2(y2[e]);
+      d1 = fmaf(a.x, u.x, fmaf(a.y, u.y, d1));
+      d2 = fmaf(a.x, w.x, fmaf(a.y, w.y, d2));
+    }
+  }
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) {
+    d1 += __shfl_xor_sync(0xffffffffu, d1, o);
+    d2 += __shfl_xor_sync(0xffffffffu, d2, o);
+  }
+  if (lane == 0 && in) {
+    const size_t to = ((size_t)b * p.H + h) * Sp + i;
+    float4 v = make_float4(INFINITY, INFINITY, 0.f, 0.f);
+    if (real) {
+      const size_t l = ((size_t)b * 2 * p.H + 2 * h) * p.S + i;
+      // O1 = O + lam O2
+      v = make_float4(p.lse[l] * kLog2e, p.lse[l + p.S] * kLog2e, fmaf(lam, d2, d1), d2);
+    }
+    p.rowv[to] = v;
+    p.lamv[to] = lam;
+  }
+}
+
+// -------------------------------------------------------------------- dQ
+// CTA: a 128-row query tile of one head pair; steps of 64 keys, double-buffered in TMEM so
+// that the tensor core forms step t+1's S1, S2, dP while the warpgroups turn step t's into dS:
+//   buffer u: S1 [192u, +64) S2 [+64) dP [+64);  dS_m bf16 over the first 32 columns of S_m
+//   dQ1 [384, 384+d)  dQ2 [384+d, 384+2d)
+// Warps 0-3 map 1, 4-7 map 2, 8 TMA producer, 9 MMA issuer.
+constexpr int kKeys = 64;  // keys of a step
+
+template <int d>
+struct DqL {
+  static constexpr int DV = 2 * d;
+  static constexpr int kStages = 2;
+  static constexpr int kTileBytes = DV * kTile * 2;
+  static constexpr int kBoxes = DV / kBoxCols;
+  static constexpr int kStageBytes = 2 * kTileBytes;  // K then V, 128 keys
+  static constexpr int offQ = 0, offDO = kTileBytes;
+  static constexpr int offStage = 2 * kTileBytes;
+  static constexpr int offBar = offStage + kStages * kStageBytes;
+  // q_full, kv_full[2], kv_empty[2], in_full[2], ds_full[2], acc_full, drain
+  static constexpr int kNumBars = 1 + 2 * kStages + 4 + 2;
+  static constexpr int offMisc = offBar + kNumBars * 8;  // tmem address, abort flag, 4 floats
+  static constexpr int kBytes = offMisc + 32;
+  static constexpr uint32_t tAcc = 384, kTmemCols = 512;
+  static_assert(kBytes <= 232448, "shared memory budget");
+};
+
+template <int d>
+__global__ void __launch_bounds__(kThreads, 1)
+    diff_dq_kernel(const __grid_constant__ CUtensorMap tm_q,
+                   const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v,
+                   const __grid_constant__ CUtensorMap tm_do, const DiffBwdParams p) {
+  using L = DqL<d>;
+  constexpr int DV = L::DV;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0) atomicOr(p.status, kErrSmemAlign);
+    return;
+  }
+  uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + L::offBar);
+  uint64_t *kv_full = q_full + 1, *kv_empty = kv_full + L::kStages;
+  uint64_t *in_full = kv_empty + L::kStages, *ds_full = in_full + 2, *acc_full = ds_full + 2;
+  uint64_t *drain = acc_full + 1;
+  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + L::offMisc);
+  int *s_abort = reinterpret_cast<int *>(smem + L::offMisc + 4);
+  float *s_part = reinterpret_cast<float *>(smem + L::offMisc + 16);
+  const Abort ab{s_abort, p.status, p.wait_ns};
+  const int warp = warp_id(), lane = lane_id();
+
+  const int i = p.N - 1 - (int)(blockIdx.x % p.N);  // heaviest causal tiles first
+  const int bh = blockIdx.x / p.N;
+  const int h = bh % p.H, b = bh / p.H;
+  const int hkv = h / p.G;
+  const int keys = p.causal ? min(p.S, (i + 1) * kTile) : p.S;
+  const int steps = (keys + kKeys - 1) / kKeys, stages = (steps + 1) / 2;
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(&kv_full[s], 1);
+      mbar_init(&kv_empty[s], 1);
+    }
+    for (int u = 0; u < 2; ++u) {
+      mbar_init(&in_full[u], 1);
+      mbar_init(&ds_full[u], 8);
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(drain, 1);
+    *s_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8 && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    tma_prefetch_desc(&tm_do);
+  }
+  if (warp == 9) {
+    tmem_alloc(s_tmem, L::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+
+  if (warp == 8 && lane == 0) {
+    // ------------------------------------------------------------------ TMA producer
+    int last[L::kStages];
+    for (int s = 0; s < L::kStages; ++s) last[s] = -1;
+    bool ok = true;
+    mbar_arrive_expect_tx(q_full, 2 * L::kTileBytes);
+    for (int bx = 0; bx < L::kBoxes; ++bx) {
+      tma_load_4d(smem + L::offQ + bx * kBoxBytes, &tm_q, q_full, bx * kBoxCols, h, i * kTile, b);
+      tma_load_4d(smem + L::offDO + bx * kBoxBytes, &tm_do, q_full, bx * kBoxCols, h, i * kTile,
+                  b);
+    }
+    for (int j = 0; j < stages; ++j) {
+      const int s = j % L::kStages;
+      const uint32_t ph = (j / L::kStages) & 1;
+      if (!mbar_wait(&kv_empty[s], ph ^ 1, ab)) {
+        ok = false;
+        break;
+      }
+      mbar_arrive_expect_tx(&kv_full[s], L::kStageBytes);
+      uint8_t *sk = smem + L::offStage + s * L::kStageBytes;
+      for (int bx = 0; bx < L::kBoxes; ++bx) {
+        tma_load_4d(sk + bx * kBoxBytes, &tm_k, &kv_full[s], bx * kBoxCols, hkv, j * kTile, b);
+        tma_load_4d(sk + L::kTileBytes + bx * kBoxBytes, &tm_v, &kv_full[s], bx * kBoxCols, hkv,
+                    j * kTile, b);
+      }
+      last[s] = (int)ph;
+    }
+    if (!ok) {
+      mbar_wait_drain(q_full, 0, 100000000ull);
+      for (int s = 0; s < L::kStages; ++s)
+        if (last[s] >= 0) mbar_wait_drain(&kv_full[s], (uint32_t)last[s], 100000000ull);
+    }
+  } else if (warp == 9 && lane == 0) {
+    // ------------------------------------------------------------------ MMA issuer
+    constexpr uint32_t kIdescIn = make_idesc_bf16(128, kKeys, false, false);
+    constexpr uint32_t kIdescQ = make_idesc_bf16(128, d, false, true);
+    const uint32_t sbase = smem_u32(smem);
+    auto stage_at = [&](int t) {
+      return sbase + L::offStage + ((t >> 1) % L::kStages) * L::kStageBytes;
+    };
+    // S1, S2 and dP of step t; keys (t & 1) * 64 on of its stage
+    auto issue_in = [&](int t) -> bool {
+      if (!(t & 1) && !mbar_wait(&kv_full[(t >> 1) % L::kStages],
+                                 ((t >> 1) / L::kStages) & 1, ab))
+        return false;
+      tc_fence_after();
+      const uint32_t aK = stage_at(t) + (t & 1) * (kKeys * 128), aV = aK + L::kTileBytes;
+      const uint32_t to = tmem + (t & 1) * 192;
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int k = 0; k < d / 16; ++k) {
+          const uint32_t off = col_bytes(m * d + 16 * k);
+          mma_ss(to + m * 64, make_sdesc_sw128(sbase + L::offQ + off, 16, 1024),
+                 make_sdesc_sw128(aK + off, 16, 1024), kIdescIn, k > 0);
+        }
+#pragma unroll
+      for (int k = 0; k < DV / 16; ++k) {
+        const uint32_t off = col_bytes(16 * k);
+        mma_ss(to + 128, make_sdesc_sw128(sbase + L::offDO + off, 16, 1024),
+               make_sdesc_sw128(aV + off, 16, 1024), kIdescIn, k > 0);
+      }
+      mma_commit(&in_full[t & 1]);
+      return true;
+    };
+    bool ok = mbar_wait(q_full, 0, ab) && issue_in(0);
+    if (ok && steps > 1) ok = issue_in(1);
+    for (int t = 0; ok && t < steps; ++t) {
+      if (!mbar_wait(&ds_full[t & 1], (t >> 1) & 1, ab)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t aK = stage_at(t) + (t & 1) * (kKeys * 128);
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int k = 0; k < kKeys / 16; ++k)
+          mma_ts(tmem + L::tAcc + m * d, tmem + (t & 1) * 192 + m * 64 + 8 * k,
+                 make_sdesc_sw128(aK + col_bytes(m * d) + k * 2048, kBoxBytes, 1024), kIdescQ,
+                 (t > 0 || k > 0) ? 1u : 0u);
+      if ((t & 1) || t == steps - 1) mma_commit(&kv_empty[(t >> 1) % L::kStages]);
+      if (t + 2 < steps && !issue_in(t + 2)) ok = false;
+    }
+    if (ok) mma_commit(acc_full);
+    mma_commit(drain);
+    mbar_wait_drain(drain, 0, 100000000ull);
+  } else if (warp < 8) {
+    // ------------------------------------------------------------------ dS of map m
+    const int m = warp >> 2;
+    const int quad = warp & 3;
+    const int r = quad * 32 + lane;  // query row within the tile = TMEM lane
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const int row = i * kTile + r;
+    const size_t vec = ((size_t)b * p.H + h) * (p.N * kTile) + row;
+    const float4 rv = p.rowv[vec];
+    const float neg_lse = m ? -rv.y : -rv.x, D = m ? rv.w : rv.z;
+    const float by = m ? -p.lamv[vec] : 1.f;
+    float along = 0.f;  // sum_j P dP of this row
+    bool ok = true;
+    for (int t = 0; t < steps; ++t) {
+      const int u = t & 1;
+      if (!mbar_wait_warp(&in_full[u], (t >> 1) & 1, ab)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t tS = tmem + lane_off + u * 192 + m * 64, tP = tmem + lane_off + u * 192 + 128;
+      // keys of this step that the row sees
+      const int limit = min(p.S, p.causal ? row + 1 : p.S) - t * kKeys;
+      const bool cut = __any_sync(0xffffffffu, limit < kKeys);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t s[32], g[32], pk[16];
+        tmem_ld32(tS + 32 * c, s);
+        tmem_ld32(tP + 32 * c, g);
+        tmem_ld_wait_for(s);
+        tmem_ld_wait_for(g);
+        if (cut) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (32 * c + e >= limit) s[e] = __float_as_uint(-INFINITY), g[e] = 0u;
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float v[2];
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const float P = ex2_approx(fmaf(__uint_as_float(s[2 * e + z]), p.scale_log2, neg_lse));
+            const float dP = __uint_as_float(g[2 * e + z]);
+            along = fmaf(P, dP, along);
+            v[z] = P * by * (dP - D);
+          }
+          pk[e] = pack_bf16(v[0], v[1]);
+        }
+        tmem_st16(tS + 16 * c, pk);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ds_full[u]);
+    }
+    // ------------------------------------------------------------------ epilogue
+    const bool row_ok = row < p.S;
+    if (ok && mbar_wait_warp(acc_full, 0, ab)) {
+      tc_fence_after();
+      __nv_bfloat16 *out = p.dq + (((size_t)b * p.S + row) * 2 * p.H + 2 * h + m) * d;
+#pragma unroll 1
+      for (int c = 0; c < d / 32; ++c) {
+        uint32_t v[32];
+        tmem_ld32(tmem + lane_off + L::tAcc + m * d + 32 * c, v);
+        tmem_ld_wait_for(v);
+        if (row_ok) store_row32(out + 32 * c, v, p.scale);
+      }
+    }
+    if (m == 1) {
+      if (!row_ok) along = 0.f;
+      if (p.lam_token) {
+        const size_t at = ((size_t)b * p.S + row) * p.H + h;
+        if (row_ok) {
+          if (p.lam_f32)
+            static_cast<float *>(p.dlam)[at] = -along;
+          else
+            static_cast<__nv_bfloat16 *>(p.dlam)[at] = __float2bfloat16_rn(-along);
+        }
+      } else {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) along += __shfl_xor_sync(0xffffffffu, along, o);
+        if (lane == 0) s_part[quad] = along;
+        named_bar_sync(1, 128);
+        if (threadIdx.x == 128)
+          p.dlam_part[((size_t)b * p.H + h) * p.N + i] =
+              -((s_part[0] + s_part[1]) + (s_part[2] + s_part[3]));
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::kTmemCols);
+  }
+}
+
+// Weights per head: the tiles' sums of one head, added in a fixed order.
+__global__ void __launch_bounds__(256) diff_dlam_kernel(const DiffBwdParams p) {
+  __shared__ float s[8];
+  const int h = blockIdx.x;
+  float v = 0.f;
+  for (int k = threadIdx.x; k < p.B * p.N; k += 256)
+    v += p.dlam_part[((size_t)(k / p.N) * p.H + h) * p.N + k % p.N];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    v = 0.f;
+    for (int k = 0; k < 8; ++k) v += s[k];
+    if (p.lam_f32)
+      static_cast<float *>(p.dlam)[h] = v;
+    else
+      static_cast<__nv_bfloat16 *>(p.dlam)[h] = __float2bfloat16_rn(v);
+  }
+}
+
+// -------------------------------------------------------------------- dK, dV
+// CTA: a 128-key block of one KV head, over the query heads of its group and their tiles in
+// ascending order, in steps of 64 queries with everything transposed (thread = key row, so
+// the bf16 operands P^T, dS1^T go back to TMEM where their rows are):
+//   dV [0,dv)  dK1 [128,128+d) dK2 [192,192+d)
+//   in: S1^T [256,320) S2^T [320,384) dP^T [384,448)   out: P^T [448,480) dS1^T [480,512)
+// The step's inputs go to registers at once, which frees their columns for the next step's
+// products; dS2^T finds no room in TMEM and goes through shared memory.  The two warpgroups
+// share a step's queries (32 each).
+constexpr int kQueries = 64;
+
+template <int d>
+struct DkvL {
+  static constexpr int DV = 2 * d;
+  static constexpr int kStages = 2;
+  static constexpr int kTileBytes = DV * kTile * 2;
+  static constexpr int kBoxes = DV / kBoxCols;
+  static constexpr int kRowBytes = kTile * 16, kLamBytes = kTile * 4;
+  static constexpr int offK = 0, offV = kTileBytes;
+  static constexpr int offStage = 2 * kTileBytes;  // per stage Q, dO
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int offDS = offStage + kStages * kStageBytes;  // dS2^T, one box
+  static constexpr int offRow = offDS + kBoxBytes;                // per stage row vectors
+  static constexpr int offLam = offRow + kStages * kRowBytes;
+  static constexpr int offBar = offLam + kStages * kLamBytes;
+  // kv_full, q_full[2], q_empty[2], in_full, in_free, out_full, out_free, acc_full, drain
+  static constexpr int kNumBars = 1 + 2 * kStages + 6;
+  static constexpr int offMisc = offBar + kNumBars * 8;
+  static constexpr int kBytes = offMisc + 16;
+  static constexpr uint32_t tV = 0, tK = 128, tIn = 256, tP = 448, tDS = 480, kTmemCols = 512;
+  static_assert(kBytes <= 232448, "shared memory budget");
+};
+
+template <int d>
+__global__ void __launch_bounds__(kThreads, 1)
+    diff_dkv_kernel(const __grid_constant__ CUtensorMap tm_q,
+                    const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v,
+                    const __grid_constant__ CUtensorMap tm_do, const DiffBwdParams p) {
+  using L = DkvL<d>;
+  constexpr int DV = L::DV;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0) atomicOr(p.status, kErrSmemAlign);
+    return;
+  }
+  uint64_t *kv_full = reinterpret_cast<uint64_t *>(smem + L::offBar);
+  uint64_t *q_full = kv_full + 1, *q_empty = q_full + L::kStages;
+  uint64_t *in_full = q_empty + L::kStages, *in_free = in_full + 1, *out_full = in_full + 2;
+  uint64_t *out_free = in_full + 3, *acc_full = in_full + 4, *drain = in_full + 5;
+  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + L::offMisc);
+  int *s_abort = reinterpret_cast<int *>(smem + L::offMisc + 4);
+  const Abort ab{s_abort, p.status, p.wait_ns};
+  const int warp = warp_id(), lane = lane_id();
+
+  const int heads = p.B * p.Hkv;
+  const int j = blockIdx.x / heads;  // causal: block 0 meets the most queries, first
+  const int bh = blockIdx.x % heads;
+  const int hkv = bh % p.Hkv, b = bh / p.Hkv;
+  const int i0 = p.causal ? j : 0, tiles = p.N - i0;
+  const int stages = p.G * tiles;
+  // the last tile has one step where S ends in its first half
+  const int last_steps = p.S - (p.N - 1) * kTile > kQueries ? 2 : 1;
+  const int steps = p.G * (2 * (tiles - 1) + last_steps);
+  // advances (tile, half) to the next step; true where a new stage begins
+  auto next = [&](int &i, int &u) {
+    if (++u < (i == p.N - 1 ? last_steps : 2)) return false;
+    u = 0;
+    if (++i == p.N) i = i0;
+    return true;
+  };
+
+  if (threadIdx.x == 0) {
+    mbar_init(kv_full, 1);
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(&q_full[s], 1);
+      mbar_init(&q_empty[s], 9);  // the products' commit and the eight warps that read row vectors
+    }
+    mbar_init(in_full, 1);
+    mbar_init(in_free, 8);
+    mbar_init(out_full, 8);
+    mbar_init(out_free, 1);
+    mbar_init(acc_full, 1);
+    mbar_init(drain, 1);
+    *s_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8 && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    tma_prefetch_desc(&tm_do);
+  }
+  if (warp == 9) {
+    tmem_alloc(s_tmem, L::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+
+  if (warp == 8 && lane == 0) {
+    // ------------------------------------------------------------------ TMA producer
+    int last[L::kStages];
+    for (int s = 0; s < L::kStages; ++s) last[s] = -1;
+    bool ok = true;
+    mbar_arrive_expect_tx(kv_full, 2 * L::kTileBytes);
+    for (int bx = 0; bx < L::kBoxes; ++bx) {
+      tma_load_4d(smem + L::offK + bx * kBoxBytes, &tm_k, kv_full, bx * kBoxCols, hkv, j * kTile,
+                  b);
+      tma_load_4d(smem + L::offV + bx * kBoxBytes, &tm_v, kv_full, bx * kBoxCols, hkv, j * kTile,
+                  b);
+    }
+    for (int n = 0; n < stages; ++n) {
+      const int s = n % L::kStages;
+      const uint32_t ph = (n / L::kStages) & 1;
+      if (!mbar_wait(&q_empty[s], ph ^ 1, ab)) {
+        ok = false;
+        break;
+      }
+      const int h = hkv * p.G + n / tiles, i = i0 + n % tiles;
+      mbar_arrive_expect_tx(&q_full[s], L::kStageBytes + L::kRowBytes + L::kLamBytes);
+      uint8_t *sq = smem + L::offStage + s * L::kStageBytes;
+      for (int bx = 0; bx < L::kBoxes; ++bx) {
+        tma_load_4d(sq + bx * kBoxBytes, &tm_q, &q_full[s], bx * kBoxCols, h, i * kTile, b);
+        tma_load_4d(sq + L::kTileBytes + bx * kBoxBytes, &tm_do, &q_full[s], bx * kBoxCols, h,
+                    i * kTile, b);
+      }
+      const size_t vec = (((size_t)b * p.H + h) * p.N + i) * kTile;
+      bulk_load(smem + L::offRow + s * L::kRowBytes, p.rowv + vec, L::kRowBytes, &q_full[s]);
+      bulk_load(smem + L::offLam + s * L::kLamBytes, p.lamv + vec, L::kLamBytes, &q_full[s]);
+      last[s] = (int)ph;
+    }
+    if (!ok) {
+      mbar_wait_drain(kv_full, 0, 100000000ull);
+      for (int s = 0; s < L::kStages; ++s)
+        if (last[s] >= 0) mbar_wait_drain(&q_full[s], (uint32_t)last[s], 100000000ull);
+    }
+  } else if (warp == 9 && lane == 0) {
+    // ------------------------------------------------------------------ MMA issuer
+    constexpr uint32_t kIdescIn = make_idesc_bf16(128, kQueries, false, false);
+    constexpr uint32_t kIdescV = make_idesc_bf16(128, DV, false, true);
+    constexpr uint32_t kIdescK = make_idesc_bf16(128, d, false, true);
+    const uint32_t sbase = smem_u32(smem);
+    auto stage_at = [&](int n) {
+      return sbase + L::offStage + (n % L::kStages) * L::kStageBytes;
+    };
+    // S1^T, S2^T and dP^T of half u of stage n
+    auto issue_in = [&](int n, int u) -> bool {
+      if (u == 0 && !mbar_wait(&q_full[n % L::kStages], (n / L::kStages) & 1, ab)) return false;
+      tc_fence_after();
+      const uint32_t aQ = stage_at(n) + u * (kQueries * 128), aO = aQ + L::kTileBytes;
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int k = 0; k < d / 16; ++k) {
+          const uint32_t off = col_bytes(m * d + 16 * k);
+          mma_ss(tmem + L::tIn + m * 64, make_sdesc_sw128(sbase + L::offK + off, 16, 1024),
+                 make_sdesc_sw128(aQ + off, 16, 1024), kIdescIn, k > 0);
+        }
+#pragma unroll
+      for (int k = 0; k < DV / 16; ++k) {
+        const uint32_t off = col_bytes(16 * k);
+        mma_ss(tmem + L::tIn + 128, make_sdesc_sw128(sbase + L::offV + off, 16, 1024),
+               make_sdesc_sw128(aO + off, 16, 1024), kIdescIn, k > 0);
+      }
+      mma_commit(in_full);
+      return true;
+    };
+    bool ok = mbar_wait(kv_full, 0, ab) && issue_in(0, 0);
+    int i = i0, u = 0, n = 0;        // step t
+    int i1 = i0, u1 = 0, n1 = 0;     // step t + 1
+    if (next(i1, u1)) ++n1;
+    for (int t = 0; ok && t < steps; ++t) {
+      if (t + 1 < steps && !(mbar_wait(in_free, t & 1, ab) && issue_in(n1, u1))) {
+        ok = false;
+        break;
+      }
+      if (!mbar_wait(out_full, t & 1, ab)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t aQ = stage_at(n) + u * (kQueries * 128), aO = aQ + L::kTileBytes;
+      const uint32_t first = t > 0 ? 1u : 0u;
+#pragma unroll
+      for (int k = 0; k < kQueries / 16; ++k)
+        mma_ts(tmem + L::tV, tmem + L::tP + 8 * k,
+               make_sdesc_sw128(aO + k * 2048, kBoxBytes, 1024), kIdescV, k > 0 ? 1u : first);
+#pragma unroll
+      for (int k = 0; k < kQueries / 16; ++k)
+        mma_ts(tmem + L::tK, tmem + L::tDS + 8 * k,
+               make_sdesc_sw128(aQ + k * 2048, kBoxBytes, 1024), kIdescK, k > 0 ? 1u : first);
+#pragma unroll
+      for (int k = 0; k < kQueries / 16; ++k)
+        mma_ss(tmem + L::tK + 64, make_sdesc_sw128(sbase + L::offDS + k * 32, 16, 1024),
+               make_sdesc_sw128(aQ + col_bytes(d) + k * 2048, kBoxBytes, 1024), kIdescK,
+               k > 0 ? 1u : first);
+      mma_commit(out_free);
+      const int s = n % L::kStages;
+      if (next(i, u)) {
+        ++n;
+        mma_commit(&q_empty[s]);
+      }
+      if (next(i1, u1)) ++n1;
+    }
+    if (ok) mma_commit(acc_full);
+    mma_commit(drain);
+    mbar_wait_drain(drain, 0, 100000000ull);
+  } else if (warp < 8) {
+    // ------------------------------------------------------------------ P, dS (transposed)
+    const int wg = warp >> 2;
+    const int quad = warp & 3;
+    const int r = quad * 32 + lane;  // key row within the block = TMEM lane
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const uint32_t tI = tmem + lane_off + L::tIn + 32 * wg;
+    const int key = j * kTile + r;
+    uint8_t *ds_row = smem + L::offDS + r * 128;
+    bool ok = true;
+    int i = i0, u = 0, n = 0;
+    for (int t = 0; t < steps; ++t) {
+      if (!mbar_wait_warp(in_full, t & 1, ab)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      uint32_t s1[32], s2[32], g[32];
+      tmem_ld32(tI, s1);
+      tmem_ld32(tI + 64, s2);
+      tmem_ld32(tI + 128, g);
+      tmem_ld_wait_for(s1);
+      tmem_ld_wait_for(s2);
+      tmem_ld_wait_for(g);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(in_free);
+      const int s = n % L::kStages;
+      const int q0 = u * kQueries + 32 * wg;  // first query within the tile
+      const float4 *rv = reinterpret_cast<const float4 *>(smem + L::offRow + s * L::kRowBytes) + q0;
+      const float *lm = reinterpret_cast<const float *>(smem + L::offLam + s * L::kLamBytes) + q0;
+      // queries before this key see nothing of it
+      const int from = p.causal && i == j ? r - q0 : 0;
+      if (__any_sync(0xffffffffu, from > 0)) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (e < from) s1[e] = s2[e] = __float_as_uint(-INFINITY), g[e] = 0u;
+      }
+      uint32_t pP[16], p1[16], p2[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        float P[2], x[2], y[2];
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const int c = 2 * e + z;
+          const float4 v = rv[c];
+          const float a = ex2_approx(fmaf(__uint_as_float(s1[c]), p.scale_log2, -v.x));
+          const float w = ex2_approx(fmaf(__uint_as_float(s2[c]), p.scale_log2, -v.y)) * lm[c];
+          const float dP = __uint_as_float(g[c]);
+          P[z] = a - w;
+          x[z] = a * (dP - v.z);
+          y[z] = w * (v.w - dP);
+        }
+        pP[e] = pack_bf16(P[0], P[1]);
+        p1[e] = pack_bf16(x[0], x[1]);
+        p2[e] = pack_bf16(y[0], y[1]);
+      }
+      if (t > 0 && !mbar_wait_warp(out_free, (t - 1) & 1, ab)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      tmem_st16(tmem + lane_off + L::tP + 16 * wg, pP);
+      tmem_st16(tmem + lane_off + L::tDS + 16 * wg, p1);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        *reinterpret_cast<uint4 *>(ds_row + (((4 * wg + c) ^ (r & 7)) << 4)) =
+            make_uint4(p2[4 * c], p2[4 * c + 1], p2[4 * c + 2], p2[4 * c + 3]);
+      tmem_st_wait();
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(out_full);
+      if (next(i, u)) {
+        ++n;
+        if (lane == 0) mbar_arrive(&q_empty[s]);
+      }
+    }
+    if (ok && mbar_wait_warp(acc_full, 0, ab)) {
+      tc_fence_after();
+      const bool row_ok = key < p.S;
+      const size_t at = (size_t)b * p.S + key;
+      __nv_bfloat16 *dk = p.dk + (at * 2 * p.Hkv + 2 * hkv + wg) * d;
+      __nv_bfloat16 *dv = p.dv + (at * p.Hkv + hkv) * DV + wg * d;
+#pragma unroll 1
+      for (int c = 0; c < d / 32; ++c) {
+        uint32_t v[32];
+        tmem_ld32(tmem + lane_off + L::tK + 64 * wg + 32 * c, v);
+        tmem_ld_wait_for(v);
+        if (row_ok) store_row32(dk + 32 * c, v, p.scale);
+        tmem_ld32(tmem + lane_off + L::tV + d * wg + 32 * c, v);
+        tmem_ld_wait_for(v);
+        if (row_ok) store_row32(dv + 32 * c, v, 1.f);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::kTmemCols);
+  }
+}
+
+template <int d>
+cudaError_t launch_t(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                     const CUtensorMap &tdo, const DiffBwdParams &p, cudaStream_t s) {
+  using LQ = DqL<d>;
+  using LK = DkvL<d>;
+  cudaError_t e = cudaFuncSetAttribute(diff_dq_kernel<d>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, LQ::kBytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(diff_dkv_kernel<d>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             LK::kBytes);
+  if (e != cudaSuccess) return e;
+  const long long threads = (long long)p.B * p.N * kTile * p.H * (2 * d / 8);
+  diff_rows_kernel<d><<<(unsigned)((threads + 255) / 256), 256, 0, s>>>(p);
+  diff_dq_kernel<d><<<(unsigned)p.B * p.H * p.N, kThreads, LQ::kBytes, s>>>(tq, tk, tv, tdo, p);
+  if (!p.lam_token) diff_dlam_kernel<<<p.H, 256, 0, s>>>(p);
+  diff_dkv_kernel<d>
+      <<<(unsigned)p.B * p.Hkv * p.N, kThreads, LK::kBytes, s>>>(tq, tk, tv, tdo, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_diff_bwd(int d, const CUtensorMap &tq, const CUtensorMap &tk,
+                            const CUtensorMap &tv, const CUtensorMap &tdo,
+                            const DiffBwdParams &p, cudaStream_t s) {
+  return d == 32 ? launch_t<32>(tq, tk, tv, tdo, p, s) : launch_t<64>(tq, tk, tv, tdo, p, s);
+}
+
+}  // namespace dash

@@ -1,0 +1,313 @@
+// diff_fwd.cu -- differential attention forward: O, O2 = P2 V (the backward's second row
+// product and the weight's gradient need it) and both maps' LSE.
+//
+// One CTA per (batch, head pair, 128-row query tile).  The two maps are two independent online
+// softmaxes over the same KV blocks; a warpgroup owns each (thread = query row), so that while
+// one turns its scores into probabilities the tensor core runs the other's products:
+//   Sm = Qm Km^T -> max, exp2, sum -> Pm (bf16, in TMEM over Sm) -> Om += Pm V
+// The running maximum of a row is only raised when a block exceeds it by 2^8 (the row's Om
+// and sum are then rescaled in place; no product on Om is in flight, the next Sm follows Pm V
+// in issue order).  P is rounded to bf16 for the tensor core, relative error 2^-9 per entry;
+// sums, maxima and accumulators are fp32.
+//
+// TMEM columns: S1 [0,128), S2 [128,256), O1 [256, 256+dv), O2 [256+dv, 256+2dv).
+// Warps 0-3 map 1, 4-7 map 2, 8 TMA producer, 9 MMA issuer.
+#include "diff.cuh"
+
+namespace dash {
+namespace {
+
+constexpr int kThreads = 320;
+constexpr float kRaise = 8.f;  // log2 of how far a row's scores may pass its running maximum
+
+template <int d>
+struct FwdL {
+  static constexpr int DV = 2 * d;
+  static constexpr int kStages = 2;
+  static constexpr int kTileBytes = DV * kTile * 2;
+  static constexpr int kBoxes = DV / kBoxCols;
+  static constexpr int kStageBytes = 2 * kTileBytes;  // K then V
+  static constexpr int offQ = 0;
+  static constexpr int offStage = kTileBytes;
+  static constexpr int offSum = offStage + kStages * kStageBytes;  // float [2][128]
+  static constexpr int offBar = offSum + 2 * kTile * 4;
+  // q_full, kv_full[2], kv_empty[2], s_full[2], p_full[2], o_full, drain
+  static constexpr int kNumBars = 1 + 2 * kStages + 4 + 2;
+  static constexpr int offMisc = offBar + kNumBars * 8;
+  static constexpr int kBytes = offMisc + 16;
+  static constexpr uint32_t tS = 0, tO = 256, kTmemCols = 512;
+  static_assert(kBytes <= 232448, "shared memory budget");
+};
+
+template <int d>
+__global__ void __launch_bounds__(kThreads, 1)
+    diff_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
+                    const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v, const DiffFwdParams p) {
+  using L = FwdL<d>;
+  constexpr int DV = L::DV;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0) atomicOr(p.status, kErrSmemAlign);
+    return;
+  }
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::offBar);
+  uint64_t *q_full = bars, *kv_full = bars + 1, *kv_empty = kv_full + L::kStages;
+  uint64_t *s_full = kv_empty + L::kStages, *p_full = s_full + 2, *o_full = p_full + 2;
+  uint64_t *drain = o_full + 1;
+  float *s_sum = reinterpret_cast<float *>(smem + L::offSum);
+  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + L::offMisc);
+  int *s_abort = reinterpret_cast<int *>(smem + L::offMisc + 4);
+  const Abort ab{s_abort, p.status, p.wait_ns};
+  const int warp = warp_id(), lane = lane_id();
+
+  // heaviest causal tiles first
+  const int i = p.N - 1 - (int)(blockIdx.x % p.N);
+  const int bh = blockIdx.x / p.N;
+  const int h = bh % p.H, b = bh / p.H;
+  const int hkv = h / p.G;
+  const int nkv = p.causal ? i + 1 : p.N;
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(&kv_full[s], 1);
+      mbar_init(&kv_empty[s], 1);
+    }
+    for (int m = 0; m < 2; ++m) {
+      mbar_init(&s_full[m], 1);
+      mbar_init(&p_full[m], 4);
+    }
+    mbar_init(o_full, 1);
+    mbar_init(drain, 1);
+    *s_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8 && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (warp == 9) {
+    tmem_alloc(s_tmem, L::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+
+  if (warp == 8 && lane == 0) {
+    // ------------------------------------------------------------------ TMA producer
+    int last[L::kStages];
+    for (int s = 0; s < L::kStages; ++s) last[s] = -1;
+    bool ok = true;
+    mbar_arrive_expect_tx(q_full, L::kTileBytes);
+    for (int bx = 0; bx < L::kBoxes; ++bx)
+      tma_load_4d(smem + L::offQ + bx * kBoxBytes, &tm_q, q_full, bx * kBoxCols, h, i * kTile, b);
+    for (int j = 0; j < nkv; ++j) {
+      const int s = j % L::kStages;
+      const uint32_t ph = (j / L::kStages) & 1;
+      if (!mbar_wait(&kv_empty[s], ph ^ 1, ab)) {
+        ok = false;
+        break;
+      }
+      mbar_arrive_expect_tx(&kv_full[s], L::kStageBytes);
+      uint8_t *sk = smem + L::offStage + s * L::kStageBytes;
+      for (int bx = 0; bx < L::kBoxes; ++bx)
+        tma_load_4d(sk + bx * kBoxBytes, &tm_k, &kv_full[s], bx * kBoxCols, hkv, j * kTile, b);
+      for (int bx = 0; bx < L::kBoxes; ++bx)
+        tma_load_4d(sk + L::kTileBytes + bx * kBoxBytes, &tm_v, &kv_full[s], bx * kBoxCols, hkv,
+                    j * kTile, b);
+      last[s] = (int)ph;
+    }
+    if (!ok) {
+      mbar_wait_drain(q_full, 0, 100000000ull);
+      for (int s = 0; s < L::kStages; ++s)
+        if (last[s] >= 0) mbar_wait_drain(&kv_full[s], (uint32_t)last[s], 100000000ull);
+    }
+  } else if (warp == 9 && lane == 0) {
+    // ------------------------------------------------------------------ MMA issuer
+    constexpr uint32_t kIdescS = make_idesc_bf16(128, 128, false, false);
+    constexpr uint32_t kIdescO = make_idesc_bf16(128, DV, false, true);
+    const uint32_t sbase = smem_u32(smem);
+    auto issue_s = [&](int j, int m) {
+      const uint32_t aK = sbase + L::offStage + (j % L::kStages) * L::kStageBytes;
+#pragma unroll
+      for (int k = 0; k < d / 16; ++k) {
+        const uint32_t off = col_bytes(m * d + 16 * k);
+        mma_ss(tmem + L::tS + m * 128, make_sdesc_sw128(sbase + L::offQ + off, 16, 1024),
+               make_sdesc_sw128(aK + off, 16, 1024), kIdescS, k > 0);
+      }
+      mma_commit(&s_full[m]);
+    };
+    bool ok = mbar_wait(q_full, 0, ab) && mbar_wait(&kv_full[0], 0, ab);
+    if (ok) {
+      tc_fence_after();
+      issue_s(0, 0);
+      issue_s(0, 1);
+    }
+    for (int j = 0; ok && j < nkv; ++j) {
+      const int s = j % L::kStages, j1 = j + 1;
+      const uint32_t aV = sbase + L::offStage + s * L::kStageBytes + L::kTileBytes;
+      for (int m = 0; ok && m < 2; ++m) {
+        if (!mbar_wait(&p_full[m], j & 1, ab)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_ts(tmem + L::tO + m * DV, tmem + L::tS + m * 128 + 8 * k,
+                 make_sdesc_sw128(aV + k * 2048, kBoxBytes, 1024), kIdescO,
+                 (j > 0 || k > 0) ? 1u : 0u);
+        if (m == 1) mma_commit(&kv_empty[s]);
+        if (j1 < nkv) {
+          if (m == 0 && !mbar_wait(&kv_full[j1 % L::kStages], (j1 / L::kStages) & 1, ab)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          issue_s(j1, m);
+        }
+      }
+    }
+    if (ok) mma_commit(o_full);
+    mma_commit(drain);
+    mbar_wait_drain(drain, 0, 100000000ull);
+  } else if (warp < 8) {
+    // ------------------------------------------------------------------ softmax of map m
+    const int m = warp >> 2;
+    const int quad = warp & 3;
+    const int r = quad * 32 + lane;  // query row within the tile = TMEM lane
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const uint32_t tS = tmem + lane_off + L::tS + m * 128, tO = tmem + lane_off + L::tO + m * DV;
+    float ref = -INFINITY, l = 0.f;  // running maximum (log2 units) and sum
+    bool ok = true;
+    for (int j = 0; j < nkv; ++j) {
+      if (!mbar_wait_warp(&s_full[m], j & 1, ab)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      uint32_t s[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, s[c]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld_wait_for(s[c]);
+      const int limit = min(p.S - j * kTile, p.causal && j == i ? r + 1 : kTile);  // keys seen
+      if (__any_sync(0xffffffffu, limit < kTile)) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (32 * c + e >= limit) s[c][e] = __float_as_uint(-INFINITY);
+      }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(s[c][e]));
+      mx *= p.scale_log2;
+      if (j == 0) {
+        ref = mx;
+      } else if (__any_sync(0xffffffffu, mx > ref + kRaise)) {
+        const float top = fmaxf(ref, mx);
+        const float by = ex2_approx(ref - top);
+        ref = top;
+        l *= by;
+#pragma unroll 1
+        for (int c = 0; c < DV / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tO + 32 * c, o);
+          tmem_ld_wait_for(o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
+          tmem_st32(tO + 32 * c, o);
+        }
+        tmem_st_wait();
+      }
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float a = ex2_approx(fmaf(__uint_as_float(s[c][2 * e]), p.scale_log2, -ref));
+          const float z = ex2_approx(fmaf(__uint_as_float(s[c][2 * e + 1]), p.scale_log2, -ref));
+          sum[(2 * e) & 3] += a;
+          sum[(2 * e + 1) & 3] += z;
+          pk[e] = pack_bf16(a, z);
+        }
+        tmem_st16(tS + 16 * c, pk);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[m]);
+    }
+    // ------------------------------------------------------------------ epilogue
+    const int row = i * kTile + r;
+    const bool row_ok = row < p.S;
+    s_sum[m * kTile + r] = 1.f / l;
+    if (ok && row_ok)
+      p.lse[((size_t)b * 2 * p.H + 2 * h + m) * p.S + row] = (ref + log2f(l)) * kLn2;
+    named_bar_sync(1, 256);
+    if (ok && mbar_wait_warp(o_full, 0, ab)) {
+      tc_fence_after();
+      // this warpgroup's half of the columns of both accumulators
+      const float n1 = s_sum[r], n2 = s_sum[kTile + r];
+      const size_t at = (size_t)b * p.S + row;
+      const float lam =
+          row_ok ? lam_at(p.lam, p.lam_f32, p.lam_token ? at * p.H + h : (size_t)h) : 0.f;
+      const uint32_t t1 = tmem + lane_off + L::tO + m * d;
+      const size_t out = (at * p.H + h) * DV + m * d;
+#pragma unroll 1
+      for (int c = 0; c < d / 32; ++c) {
+        uint32_t o1[32], o2[32];
+        tmem_ld32(t1 + 32 * c, o1);
+        tmem_ld32(t1 + DV + 32 * c, o2);
+        tmem_ld_wait_for(o1);
+        tmem_ld_wait_for(o2);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float z = __uint_as_float(o2[e]) * n2;
+          o2[e] = __float_as_uint(z);
+          o1[e] = __float_as_uint(fmaf(-lam, z, __uint_as_float(o1[e]) * n1));
+        }
+        if (row_ok) {
+          store_row32(p.o + out + 32 * c, o1, 1.f);
+          store_row32(p.o2 + out + 32 * c, o2, 1.f);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::kTmemCols);
+  }
+}
+
+template <int d>
+cudaError_t launch_t(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                     const DiffFwdParams &p, cudaStream_t s) {
+  using L = FwdL<d>;
+  const cudaError_t e = cudaFuncSetAttribute(
+      diff_fwd_kernel<d>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+  if (e != cudaSuccess) return e;
+  diff_fwd_kernel<d><<<(unsigned)p.B * p.H * p.N, kThreads, L::kBytes, s>>>(tq, tk, tv, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_diff_fwd(int d, const CUtensorMap &tq, const CUtensorMap &tk,
+                            const CUtensorMap &tv, const DiffFwdParams &p, cudaStream_t s) {
+  return d == 32 ? launch_t<32>(tq, tk, tv, p, s) : launch_t<64>(tq, tk, tv, p, s);
+}
+
+}  // namespace dash

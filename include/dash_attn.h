@@ -370,6 +370,34 @@ dash_status_t dash_join_bwd(const void *dy, const void *dh, const void *y, const
                             float branch_scale, dash_dtype_t dtype, dash_dtype_t wdtype,
                             void *workspace, size_t workspace_bytes, dash_stream_t stream);
 
+/* Differential attention, the difference of two softmax maps with a learned weight:
+ *   O = P1 V - lam P2 V,     Pm = softmax(scale * Qm Km^T + mask)
+ *   q [B,S,2H,d]   k [B,S,2Hkv,d]   v, o, o2, dout, dv like them with heads of 2d:
+ *   v [B,S,Hkv,2d]   o, o2, dout [B,S,H,2d]   dq like q, dk like k   (bf16, contiguous)
+ * Head pair h reads the query maps 2h and 2h+1; with n = h / group, group = H / Hkv, the key
+ * maps 2n and 2n+1 and the value head n.  lam: one weight per head pair [H], or per token and
+ * head pair [B,S,H] (lam_per_token), bf16 or fp32; any value.  d = 32 or 64 (value heads of 64
+ * or 128), any S >= 1, masks and scale as dash_attn_fwd (scale <= 0: 1/sqrt(d)).
+ * Forward: writes o, o2 = P2 V and lse [B,2H,S] fp32 (natural log, of map 2h+m at 2h+m), which
+ * the backward takes; workspace: its status word. */
+size_t dash_diff_fwd_workspace_bytes(int B, int S, int H, int d);
+dash_status_t dash_diff_fwd(const void *q, const void *k, const void *v, const void *lam, void *o,
+                            void *o2, float *lse, int B, int S, int H, int group, int d,
+                            float scale, dash_mask_t mask, dash_dtype_t lam_dtype,
+                            int lam_per_token, void *workspace, size_t workspace_bytes,
+                            dash_stream_t stream);
+/* Backward: dq, dk, dv and dlam (lam's shape and type).  Deterministic: every sum is formed in
+ * a fixed order without atomics, bit-identical on every run; dk and dv sum a group's query heads
+ * in ascending order.  Workspace: status block, row vectors of B*H*Sp*20 bytes, B*H*Sp/128
+ * partial sums (Sp = S rounded up to 128); dash_attn_status reads either status word. */
+size_t dash_diff_bwd_workspace_bytes(int B, int S, int H, int d);
+dash_status_t dash_diff_bwd(const void *q, const void *k, const void *v, const void *o,
+                            const void *o2, const void *dout, const float *lse, const void *lam,
+                            void *dq, void *dk, void *dv, void *dlam, int B, int S, int H,
+                            int group, int d, float scale, dash_mask_t mask,
+                            dash_dtype_t lam_dtype, int lam_per_token, void *workspace,
+                            size_t workspace_bytes, dash_stream_t stream);
+
 /* Human-readable name of a status code (static storage). */
 const char *dash_status_string(dash_status_t status);
 
