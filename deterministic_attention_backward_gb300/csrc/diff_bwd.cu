@@ -187,60 +187,63 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int s = 0; s < L::kStages; ++s)
         if (last[s] >= 0) mbar_wait_drain(&kv_full[s], (uint32_t)last[s], 100000000ull);
     }
-  } else if (warp == 9 && lane == 0) {
+  } else if (warp == 9) {
     // ------------------------------------------------------------------ MMA issuer
+    // The whole warp runs the loop, so that descriptors and control flow stay warp-uniform;
+    // one elected lane issues (one lane alone forms every descriptor in vector registers and
+    // moves it over: the issue then bounds these short products).
     constexpr uint32_t kIdescIn = make_idesc_bf16(128, kKeys, false, false);
     constexpr uint32_t kIdescQ = make_idesc_bf16(128, d, false, true);
     const uint32_t sbase = smem_u32(smem);
-    auto stage_at = [&](int t) {
-      return sbase + L::offStage + ((t >> 1) % L::kStages) * L::kStageBytes;
+    const uint32_t loQ = desc_lo(sbase + L::offQ, 16), loDO = desc_lo(sbase + L::offDO, 16);
+    auto step_at = [&](int t) {  // K rows of step t
+      return sbase + L::offStage + ((t >> 1) % L::kStages) * L::kStageBytes +
+             (t & 1) * (kKeys * 128);
     };
     // S1, S2 and dP of step t; keys (t & 1) * 64 on of its stage
     auto issue_in = [&](int t) -> bool {
-      if (!(t & 1) && !mbar_wait(&kv_full[(t >> 1) % L::kStages],
-                                 ((t >> 1) / L::kStages) & 1, ab))
+      if (!(t & 1) && !mbar_wait_warp(&kv_full[(t >> 1) % L::kStages],
+                                      ((t >> 1) / L::kStages) & 1, ab))
         return false;
       tc_fence_after();
-      const uint32_t aK = stage_at(t) + (t & 1) * (kKeys * 128), aV = aK + L::kTileBytes;
+      const uint32_t loK = desc_lo(step_at(t), 16), loV = desc_lo(step_at(t) + L::kTileBytes, 16);
       const uint32_t to = tmem + (t & 1) * 192;
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int k = 0; k < d / 16; ++k) {
-          const uint32_t off = col_bytes(m * d + 16 * k);
-          mma_ss(to + m * 64, make_sdesc_sw128(sbase + L::offQ + off, 16, 1024),
-                 make_sdesc_sw128(aK + off, 16, 1024), kIdescIn, k > 0);
+          const uint32_t off = col_bytes(m * d + 16 * k) >> 4;
+          mma_ss_e(to + m * 64, desc_of(loQ + off), desc_of(loK + off), kIdescIn, k > 0);
         }
 #pragma unroll
       for (int k = 0; k < DV / 16; ++k) {
-        const uint32_t off = col_bytes(16 * k);
-        mma_ss(to + 128, make_sdesc_sw128(sbase + L::offDO + off, 16, 1024),
-               make_sdesc_sw128(aV + off, 16, 1024), kIdescIn, k > 0);
+        const uint32_t off = col_bytes(16 * k) >> 4;
+        mma_ss_e(to + 128, desc_of(loDO + off), desc_of(loV + off), kIdescIn, k > 0);
       }
-      mma_commit(&in_full[t & 1]);
+      mma_commit_e(&in_full[t & 1]);
       return true;
     };
-    bool ok = mbar_wait(q_full, 0, ab) && issue_in(0);
+    bool ok = mbar_wait_warp(q_full, 0, ab) && issue_in(0);
     if (ok && steps > 1) ok = issue_in(1);
     for (int t = 0; ok && t < steps; ++t) {
-      if (!mbar_wait(&ds_full[t & 1], (t >> 1) & 1, ab)) {
+      if (!mbar_wait_warp(&ds_full[t & 1], (t >> 1) & 1, ab)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const uint32_t aK = stage_at(t) + (t & 1) * (kKeys * 128);
+      const uint32_t loK = desc_lo(step_at(t), kBoxBytes);
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int k = 0; k < kKeys / 16; ++k)
-          mma_ts(tmem + L::tAcc + m * d, tmem + (t & 1) * 192 + m * 64 + 8 * k,
-                 make_sdesc_sw128(aK + col_bytes(m * d) + k * 2048, kBoxBytes, 1024), kIdescQ,
-                 (t > 0 || k > 0) ? 1u : 0u);
-      if ((t & 1) || t == steps - 1) mma_commit(&kv_empty[(t >> 1) % L::kStages]);
+          mma_ts_e(tmem + L::tAcc + m * d, tmem + (t & 1) * 192 + m * 64 + 8 * k,
+                   desc_of(loK + ((col_bytes(m * d) + k * 2048) >> 4)), kIdescQ,
+                   (t > 0 || k > 0) ? 1u : 0u);
+      if ((t & 1) || t == steps - 1) mma_commit_e(&kv_empty[(t >> 1) % L::kStages]);
       if (t + 2 < steps && !issue_in(t + 2)) ok = false;
     }
-    if (ok) mma_commit(acc_full);
-    mma_commit(drain);
+    if (ok) mma_commit_e(acc_full);
+    mma_commit_e(drain);
     mbar_wait_drain(drain, 0, 100000000ull);
   } else if (warp < 8) {
     // ------------------------------------------------------------------ dS of map m
@@ -500,76 +503,79 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int s = 0; s < L::kStages; ++s)
         if (last[s] >= 0) mbar_wait_drain(&q_full[s], (uint32_t)last[s], 100000000ull);
     }
-  } else if (warp == 9 && lane == 0) {
+  } else if (warp == 9) {
     // ------------------------------------------------------------------ MMA issuer
+    // (a converged warp, one elected lane issues)
     constexpr uint32_t kIdescIn = make_idesc_bf16(128, kQueries, false, false);
     constexpr uint32_t kIdescV = make_idesc_bf16(128, DV, false, true);
     constexpr uint32_t kIdescK = make_idesc_bf16(128, d, false, true);
     const uint32_t sbase = smem_u32(smem);
-    auto stage_at = [&](int n) {
-      return sbase + L::offStage + (n % L::kStages) * L::kStageBytes;
+    const uint32_t loK = desc_lo(sbase + L::offK, 16), loV = desc_lo(sbase + L::offV, 16);
+    const uint32_t loDS = desc_lo(sbase + L::offDS, 16);
+    auto step_at = [&](int n, int u) {  // Q rows of half u of stage n
+      return sbase + L::offStage + (n % L::kStages) * L::kStageBytes + u * (kQueries * 128);
     };
     // S1^T, S2^T and dP^T of half u of stage n
     auto issue_in = [&](int n, int u) -> bool {
-      if (u == 0 && !mbar_wait(&q_full[n % L::kStages], (n / L::kStages) & 1, ab)) return false;
+      if (u == 0 && !mbar_wait_warp(&q_full[n % L::kStages], (n / L::kStages) & 1, ab))
+        return false;
       tc_fence_after();
-      const uint32_t aQ = stage_at(n) + u * (kQueries * 128), aO = aQ + L::kTileBytes;
+      const uint32_t loQ = desc_lo(step_at(n, u), 16);
+      const uint32_t loO = desc_lo(step_at(n, u) + L::kTileBytes, 16);
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int k = 0; k < d / 16; ++k) {
-          const uint32_t off = col_bytes(m * d + 16 * k);
-          mma_ss(tmem + L::tIn + m * 64, make_sdesc_sw128(sbase + L::offK + off, 16, 1024),
-                 make_sdesc_sw128(aQ + off, 16, 1024), kIdescIn, k > 0);
+          const uint32_t off = col_bytes(m * d + 16 * k) >> 4;
+          mma_ss_e(tmem + L::tIn + m * 64, desc_of(loK + off), desc_of(loQ + off), kIdescIn, k > 0);
         }
 #pragma unroll
       for (int k = 0; k < DV / 16; ++k) {
-        const uint32_t off = col_bytes(16 * k);
-        mma_ss(tmem + L::tIn + 128, make_sdesc_sw128(sbase + L::offV + off, 16, 1024),
-               make_sdesc_sw128(aO + off, 16, 1024), kIdescIn, k > 0);
+        const uint32_t off = col_bytes(16 * k) >> 4;
+        mma_ss_e(tmem + L::tIn + 128, desc_of(loV + off), desc_of(loO + off), kIdescIn, k > 0);
       }
-      mma_commit(in_full);
+      mma_commit_e(in_full);
       return true;
     };
-    bool ok = mbar_wait(kv_full, 0, ab) && issue_in(0, 0);
-    int i = i0, u = 0, n = 0;        // step t
-    int i1 = i0, u1 = 0, n1 = 0;     // step t + 1
+    bool ok = mbar_wait_warp(kv_full, 0, ab) && issue_in(0, 0);
+    int i = i0, u = 0, n = 0;     // step t
+    int i1 = i0, u1 = 0, n1 = 0;  // step t + 1
     if (next(i1, u1)) ++n1;
     for (int t = 0; ok && t < steps; ++t) {
-      if (t + 1 < steps && !(mbar_wait(in_free, t & 1, ab) && issue_in(n1, u1))) {
+      if (t + 1 < steps && !(mbar_wait_warp(in_free, t & 1, ab) && issue_in(n1, u1))) {
         ok = false;
         break;
       }
-      if (!mbar_wait(out_full, t & 1, ab)) {
+      if (!mbar_wait_warp(out_full, t & 1, ab)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const uint32_t aQ = stage_at(n) + u * (kQueries * 128), aO = aQ + L::kTileBytes;
+      const uint32_t loQ = desc_lo(step_at(n, u), kBoxBytes);
+      const uint32_t loO = desc_lo(step_at(n, u) + L::kTileBytes, kBoxBytes);
       const uint32_t first = t > 0 ? 1u : 0u;
 #pragma unroll
       for (int k = 0; k < kQueries / 16; ++k)
-        mma_ts(tmem + L::tV, tmem + L::tP + 8 * k,
-               make_sdesc_sw128(aO + k * 2048, kBoxBytes, 1024), kIdescV, k > 0 ? 1u : first);
+        mma_ts_e(tmem + L::tV, tmem + L::tP + 8 * k, desc_of(loO + ((k * 2048) >> 4)), kIdescV,
+                 k > 0 ? 1u : first);
 #pragma unroll
       for (int k = 0; k < kQueries / 16; ++k)
-        mma_ts(tmem + L::tK, tmem + L::tDS + 8 * k,
-               make_sdesc_sw128(aQ + k * 2048, kBoxBytes, 1024), kIdescK, k > 0 ? 1u : first);
+        mma_ts_e(tmem + L::tK, tmem + L::tDS + 8 * k, desc_of(loQ + ((k * 2048) >> 4)), kIdescK,
+                 k > 0 ? 1u : first);
 #pragma unroll
       for (int k = 0; k < kQueries / 16; ++k)
-        mma_ss(tmem + L::tK + 64, make_sdesc_sw128(sbase + L::offDS + k * 32, 16, 1024),
-               make_sdesc_sw128(aQ + col_bytes(d) + k * 2048, kBoxBytes, 1024), kIdescK,
-               k > 0 ? 1u : first);
-      mma_commit(out_free);
+        mma_ss_e(tmem + L::tK + 64, desc_of(loDS + ((k * 32) >> 4)),
+                 desc_of(loQ + ((col_bytes(d) + k * 2048) >> 4)), kIdescK, k > 0 ? 1u : first);
+      mma_commit_e(out_free);
       const int s = n % L::kStages;
       if (next(i, u)) {
         ++n;
-        mma_commit(&q_empty[s]);
+        mma_commit_e(&q_empty[s]);
       }
       if (next(i1, u1)) ++n1;
     }
-    if (ok) mma_commit(acc_full);
-    mma_commit(drain);
+    if (ok) mma_commit_e(acc_full);
+    mma_commit_e(drain);
     mbar_wait_drain(drain, 0, 100000000ull);
   } else if (warp < 8) {
     // ------------------------------------------------------------------ P, dS (transposed)

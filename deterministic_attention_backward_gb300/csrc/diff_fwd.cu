@@ -126,22 +126,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int s = 0; s < L::kStages; ++s)
         if (last[s] >= 0) mbar_wait_drain(&kv_full[s], (uint32_t)last[s], 100000000ull);
     }
-  } else if (warp == 9 && lane == 0) {
+  } else if (warp == 9) {
     // ------------------------------------------------------------------ MMA issuer
+    // The whole warp runs the loop, so that descriptors and control flow stay warp-uniform;
+    // one elected lane issues.
     constexpr uint32_t kIdescS = make_idesc_bf16(128, 128, false, false);
     constexpr uint32_t kIdescO = make_idesc_bf16(128, DV, false, true);
     const uint32_t sbase = smem_u32(smem);
+    const uint32_t loQ = desc_lo(sbase + L::offQ, 16);
     auto issue_s = [&](int j, int m) {
-      const uint32_t aK = sbase + L::offStage + (j % L::kStages) * L::kStageBytes;
+      const uint32_t loK = desc_lo(sbase + L::offStage + (j % L::kStages) * L::kStageBytes, 16);
 #pragma unroll
       for (int k = 0; k < d / 16; ++k) {
-        const uint32_t off = col_bytes(m * d + 16 * k);
-        mma_ss(tmem + L::tS + m * 128, make_sdesc_sw128(sbase + L::offQ + off, 16, 1024),
-               make_sdesc_sw128(aK + off, 16, 1024), kIdescS, k > 0);
+        const uint32_t off = col_bytes(m * d + 16 * k) >> 4;
+        mma_ss_e(tmem + L::tS + m * 128, desc_of(loQ + off), desc_of(loK + off), kIdescS, k > 0);
       }
-      mma_commit(&s_full[m]);
+      mma_commit_e(&s_full[m]);
     };
-    bool ok = mbar_wait(q_full, 0, ab) && mbar_wait(&kv_full[0], 0, ab);
+    bool ok = mbar_wait_warp(q_full, 0, ab) && mbar_wait_warp(&kv_full[0], 0, ab);
     if (ok) {
       tc_fence_after();
       issue_s(0, 0);
@@ -149,21 +151,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int j = 0; ok && j < nkv; ++j) {
       const int s = j % L::kStages, j1 = j + 1;
-      const uint32_t aV = sbase + L::offStage + s * L::kStageBytes + L::kTileBytes;
-      for (int m = 0; ok && m < 2; ++m) {
-        if (!mbar_wait(&p_full[m], j & 1, ab)) {
-          ok = false;
-          break;
-        }
+      const uint32_t loV =
+          desc_lo(sbase + L::offStage + s * L::kStageBytes + L::kTileBytes, kBoxBytes);
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        if (ok && !mbar_wait_warp(&p_full[m], j & 1, ab)) ok = false;
+        if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          mma_ts(tmem + L::tO + m * DV, tmem + L::tS + m * 128 + 8 * k,
-                 make_sdesc_sw128(aV + k * 2048, kBoxBytes, 1024), kIdescO,
-                 (j > 0 || k > 0) ? 1u : 0u);
-        if (m == 1) mma_commit(&kv_empty[s]);
+          mma_ts_e(tmem + L::tO + m * DV, tmem + L::tS + m * 128 + 8 * k,
+                   desc_of(loV + ((k * 2048) >> 4)), kIdescO, (j > 0 || k > 0) ? 1u : 0u);
+        if (m == 1) mma_commit_e(&kv_empty[s]);
         if (j1 < nkv) {
-          if (m == 0 && !mbar_wait(&kv_full[j1 % L::kStages], (j1 / L::kStages) & 1, ab)) {
+          if (m == 0 && !mbar_wait_warp(&kv_full[j1 % L::kStages], (j1 / L::kStages) & 1, ab)) {
             ok = false;
             break;
           }
@@ -172,8 +173,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (ok) mma_commit(o_full);
-    mma_commit(drain);
+    if (ok) mma_commit_e(o_full);
+    mma_commit_e(drain);
     mbar_wait_drain(drain, 0, 100000000ull);
   } else if (warp < 8) {
     // ------------------------------------------------------------------ softmax of map m
