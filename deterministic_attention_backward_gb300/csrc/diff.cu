@@ -23,21 +23,18 @@ dash_status_t check_diff(int B, int S, int H, int group, int d) {
 
 struct DiffWorkspace {
   uint32_t *status;
-  float4 *rowv;
-  float *lamv, *dlam_part;
+  float *rowv, *dlam_part;
   size_t total;
 };
 DiffWorkspace carve(void *ws, int B, int S, int H) {
-  const size_t ntiles = (size_t)B * H * tiles(S), rows = ntiles * kTile;
+  const size_t ntiles = (size_t)B * H * tiles(S);
   char *base = static_cast<char *>(ws);
   DiffWorkspace w{};
   size_t off = 0;
   w.status = reinterpret_cast<uint32_t *>(base);
   off += kStatusBytes;
-  w.rowv = reinterpret_cast<float4 *>(base + off);
-  off = align256(off + rows * sizeof(float4));
-  w.lamv = reinterpret_cast<float *>(base + off);
-  off = align256(off + rows * sizeof(float));
+  w.rowv = reinterpret_cast<float *>(base + off);
+  off = align256(off + ntiles * kRowVecs * kTile * sizeof(float));
   w.dlam_part = reinterpret_cast<float *>(base + off);
   w.total = align256(off + ntiles * sizeof(float));
   return w;
@@ -133,7 +130,6 @@ dash_status_t dash_diff_bwd(const void *q, const void *k, const void *v, const v
   p.lse = lse;
   p.lam = lam;
   p.rowv = w.rowv;
-  p.lamv = w.lamv;
   p.dlam_part = w.dlam_part;
   p.status = w.status;
   p.dq = static_cast<__nv_bfloat16 *>(dq);
@@ -147,7 +143,7 @@ dash_status_t dash_diff_bwd(const void *q, const void *k, const void *v, const v
   p.wait_ns = g_wait_ns.load();
   p.scale = scale > 0.f ? scale : 1.0f / std::sqrt((float)d);
   p.scale_log2 = p.scale * kLog2e;
-  return launch_diff_bwd(d, tq, tk, tv, tdo, p, s) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+  return launch_diff_bwd(d, tq, tk, tv, tdo, static_cast<const __nv_bfloat16 *>(q), p, s) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -23,15 +23,16 @@ struct DiffFwdParams {
   float scale_log2;       // softmax scale * log2(e)
 };
 
-// Row vectors of the backward, per (batch, head pair) padded to whole tiles:
-//   rowv = {LSE1 log2e, LSE2 log2e, D1, D2}, Dm = dO . Om, and lam; rows past S hold
-//   {inf, inf, 0, 0} and 0, which give them no weight.
+// Row vectors of the backward, per tile of a (batch, head pair) kRowVecs arrays of 128 floats,
+// each negated for the fused multiply-adds that take them:
+//   -LSE1 log2e, -LSE2 log2e, -D1, -D2, -lam       (Dm = dO . Om)
+// Rows past S hold -inf, -inf, 0, 0, 0, which give them no weight.
+constexpr int kRowVecs = 5;
 struct DiffBwdParams {
   const __nv_bfloat16 *o, *o2, *dout;
   const float *lse;
   const void *lam;
-  float4 *rowv;           // [B,H,N*128]
-  float *lamv;            // [B,H,N*128]
+  float *rowv;            // [B,H,N][kRowVecs][128]
   float *dlam_part;       // [B,H,N] (weights per head only)
   uint32_t *status;
   __nv_bfloat16 *dq, *dk, *dv;
@@ -45,7 +46,7 @@ struct DiffBwdParams {
 cudaError_t launch_diff_fwd(int d, const CUtensorMap &tq, const CUtensorMap &tk,
                             const CUtensorMap &tv, const DiffFwdParams &p, cudaStream_t s);
 cudaError_t launch_diff_bwd(int d, const CUtensorMap &tq, const CUtensorMap &tk,
-                            const CUtensorMap &tv, const CUtensorMap &tdo,
+                            const CUtensorMap &tv, const CUtensorMap &tdo, const __nv_bfloat16 *q,
                             const DiffBwdParams &p, cudaStream_t s);
 
 #ifdef __CUDACC__
@@ -54,7 +55,7 @@ __device__ __forceinline__ float lam_at(const void *lam, int f32, size_t at) {
              : __bfloat162float(static_cast<const __nv_bfloat16 *>(lam)[at]);
 }
 
-// tcgen05.wait::ld that the 32 loaded registers depend on, so that no use moves above it.
+// tcgen05.wait::ld that the loaded registers depend on, so that no use moves above it.
 __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
@@ -65,6 +66,29 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[32]) {
                  "+r"(r[30]), "+r"(r[31])
                :
                : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+      : "memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
   asm volatile(
@@ -80,22 +104,65 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
       : "memory");
 }
 
+// Two fp32 values in a register pair: one instruction for two fused multiply-adds (the
+// elementwise part of these kernels is bound by instruction issue).
+using f2 = uint64_t;
+__device__ __forceinline__ f2 f2_of(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ f2 f2_of(uint32_t a, uint32_t b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void f2_to(f2 v, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 ex2_2(f2 v) {
+  float a, b;
+  f2_to(v, a, b);
+  return f2_of(ex2_approx(a), ex2_approx(b));
+}
+__device__ __forceinline__ uint32_t pack_bf16(f2 v) {
+  float a, b;
+  f2_to(v, a, b);
+  return pack_bf16(a, b);
+}
+
 // Byte offset of element column `col` (a multiple of 16) of row 0 in a [128 x 2d] operand tile
 // of 64-column boxes.
 __device__ __forceinline__ constexpr uint32_t col_bytes(int col) {
   return (uint32_t)(col >> 6) * kBoxBytes + (uint32_t)(col & 63) * 2;
 }
 
-// 32 fp32 columns of this thread's row, scaled, as 32 bf16 at dst (16-byte aligned).
-__device__ __forceinline__ void store_row32(__nv_bfloat16 *dst, const uint32_t (&v)[32],
-                                            float scale) {
-  uint32_t pk[16];
+// C fp32 columns of this thread's row, scaled, as C bf16 at dst (16-byte aligned).
+template <int C>
+__device__ __forceinline__ void store_row(__nv_bfloat16 *dst, const uint32_t (&v)[C],
+                                          float scale) {
+  uint32_t pk[C / 2];
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
+  for (int i = 0; i < C / 2; ++i)
     pk[i] = pack_bf16(__uint_as_float(v[2 * i]) * scale, __uint_as_float(v[2 * i + 1]) * scale);
   uint4 *d4 = reinterpret_cast<uint4 *>(dst);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < C / 8; ++i)
     d4[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
 }
 #endif

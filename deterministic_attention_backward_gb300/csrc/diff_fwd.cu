@@ -278,8 +278,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           o1[e] = __float_as_uint(fmaf(-lam, z, __uint_as_float(o1[e]) * n1));
         }
         if (row_ok) {
-          store_row32(p.o + out + 32 * c, o1, 1.f);
-          store_row32(p.o2 + out + 32 * c, o2, 1.f);
+          store_row(p.o + out + 32 * c, o1, 1.f);
+          store_row(p.o2 + out + 32 * c, o2, 1.f);
         }
       }
     }

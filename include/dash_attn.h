@@ -388,8 +388,9 @@ dash_status_t dash_diff_fwd(const void *q, const void *k, const void *v, const v
                             dash_stream_t stream);
 /* Backward: dq, dk, dv and dlam (lam's shape and type).  Deterministic: every sum is formed in
  * a fixed order without atomics, bit-identical on every run; dk and dv sum a group's query heads
- * in ascending order.  Workspace: status block, row vectors of B*H*Sp*20 bytes, B*H*Sp/128
- * partial sums (Sp = S rounded up to 128); dash_attn_status reads either status word. */
+ * in ascending order.  The row terms D = dO . Om of dq come from o and o2 as they are given
+ * (rounded); those of dk, and dlam, from the fp32 sums of Pm dP.  Workspace: status block, row
+ * vectors of B*H*Sp*20 bytes, B*H*Sp/128 partial sums (Sp = S rounded up to 128); dash_attn_status reads either status word. */
 size_t dash_diff_bwd_workspace_bytes(int B, int S, int H, int d);
 dash_status_t dash_diff_bwd(const void *q, const void *k, const void *v, const void *o,
                             const void *o2, const void *dout, const float *lse, const void *lam,

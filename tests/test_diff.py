@@ -42,8 +42,9 @@ def make(B, S, H, Hkv, d, lam, seed=0, spread=2.0):
 
 
 class Exact:
-    """Everything in 64 bits, heads as [B, H, S, .]; P from the LSE and D from the outputs that
-    are given (the kernels' own), as the backward's contract has it."""
+    """Everything in 64 bits, heads as [B, H, S, .]; P from the LSE that is given (the forward's
+    own), D for dQ from the outputs that are given, for dK from P and dP, as the backward's
+    contract has it."""
 
     def __init__(self, q, k, v, lam, causal, scale=None):
         B, S, H2, d = q.shape
@@ -87,6 +88,8 @@ class Exact:
         by = torch.stack([torch.ones_like(lam), -lam])
         dS = by * P * (dP - D)
         tS = HALF * dS.abs() + 2 * R * by.abs() * P * (dPa + Da)
+        dSk = by * P * (dP - (P * dP).sum(-1, keepdim=True))
+        tSk = HALF * dSk.abs() + 2 * R * by.abs() * P * (dPa + (P * dPa).sum(-1, keepdim=True))
         both = P[0] - lam * P[1]
         tP = HALF * both.abs() + 2 * R * (P[0] + la * P[1])
 
@@ -100,8 +103,8 @@ class Exact:
         dl, tl = -(P[1] * dP).sum(-1), 2 * R * (P[1] * dPa).sum(-1)
         dl, tl = (x.sum((0, 2)) if self.per_head else x.transpose(1, 2) for x in (dl, tl))
         return {"dq": (heads(c * dS @ self.k, H), heads(c * tS @ self.k.abs(), H)),
-                "dk": (heads(c * dS.transpose(*tr) @ self.q, Hkv),
-                       heads(c * tS.transpose(*tr) @ self.q.abs(), Hkv)),
+                "dk": (heads(c * dSk.transpose(*tr) @ self.q, Hkv),
+                       heads(c * tSk.transpose(*tr) @ self.q.abs(), Hkv)),
                 "dv": (values(both.transpose(*tr) @ do), values(tP.transpose(*tr) @ do.abs())),
                 "dlam": (dl, tl)}
 
@@ -196,8 +199,7 @@ def test_gradient_against_differences(L, d):
         def heads(x, n):
             x = x.unflatten(2, (n, H // n)).sum(3)
             return x.permute(1, 3, 2, 0, 4).reshape(B, S, 2 * n, d)
-        more = {"dq": heads(tS @ e.k.abs(), H),
-                "dk": heads(tS.transpose(-1, -2) @ e.q.abs(), Hkv), "dv": 0.0, "dlam": 0.0}
+        more = {"dq": heads(tS @ e.k.abs(), H), "dk": 0.0, "dv": 0.0, "dlam": 0.0}
 
         def loss(q, k, v, w):
             x = Exact(q, k, v, w, causal)
