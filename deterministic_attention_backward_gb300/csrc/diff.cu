@@ -143,7 +143,7 @@ dash_status_t dash_diff_bwd(const void *q, const void *k, const void *v, const v
   p.wait_ns = g_wait_ns.load();
   p.scale = scale > 0.f ? scale : 1.0f / std::sqrt((float)d);
   p.scale_log2 = p.scale * kLog2e;
-  return launch_diff_bwd(d, tq, tk, tv, tdo, static_cast<const __nv_bfloat16 *>(q), p, s) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+  return launch_diff_bwd(d, tq, tk, tv, tdo, p, s) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -46,7 +46,7 @@ struct DiffBwdParams {
 cudaError_t launch_diff_fwd(int d, const CUtensorMap &tq, const CUtensorMap &tk,
                             const CUtensorMap &tv, const DiffFwdParams &p, cudaStream_t s);
 cudaError_t launch_diff_bwd(int d, const CUtensorMap &tq, const CUtensorMap &tk,
-                            const CUtensorMap &tv, const CUtensorMap &tdo, const __nv_bfloat16 *q,
+                            const CUtensorMap &tv, const CUtensorMap &tdo,
                             const DiffBwdParams &p, cudaStream_t s);
 
 #ifdef __CUDACC__
@@ -84,9 +84,24 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+// 16 lanes x 32 columns as matrix fragments: thread t holds of 8-column group j, in r[4j..4j+3],
+// columns 8j + 2 (t % 4) and the next one of lanes t / 4 and t / 4 + 8.  Four lanes' worth of rows
+// and eight columns a thread (two such loads cover the warp's 32 lanes), so that what goes by
+// column is read once for four rows.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// The fragments' pairs rounded to bf16: 16 lanes x 16 columns of two values each; v[2j] the
+// pair of group j of lane t / 4, v[2j+1] of lane t / 4 + 8.
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
       : "memory");
 }

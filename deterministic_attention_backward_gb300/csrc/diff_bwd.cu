@@ -73,41 +73,44 @@ __global__ void __launch_bounds__(256) diff_rows_kernel(const DiffBwdParams p) {
 }
 
 // -------------------------------------------------------------------- dQ
-// CTA: a 128-row query tile of one head pair; steps of 64 keys.  The stationary operands Q1, Q2
-// and dO live in TMEM as the A operands: a product of 64 columns with both operands in shared
-// memory reads 6 KB for 32 cycles of tensor work, more than the 128 bytes a cycle that shared
-// memory gives; with A in TMEM it reads 2 KB.  A step's S1, S2, dP go to registers at once,
-// which frees their columns for the next step's products while dS is formed.
-//   S1 [0,64) S2 [64,128) dP [128,192)   dS1 [192,224) dS2 [224,256)  (bf16)
-//   dQ1 [256,256+d) dQ2 [320,320+d)      Q1 [384,+d/2) Q2 [416,+d/2) dO [448,+d)  (bf16)
-// Warpgroup w: map w / 2, keys 32 (w % 2) on of the step; thread = query row.
+// CTA: a 128-row query tile of one head pair, over its 128-key blocks.  All four warpgroups
+// work on one map at a time (thread = query row, 32 keys each), so that the tensor core has the
+// other map's products to run meanwhile:
+//   elementwise   S1, dP -> dS1 |          S2, dP (kept) -> dS2      | ...
+//   tensor core   dP of the next block, dQ2 += , next S2 | dQ1 +=, next S1 | ...
+//   S1 [0,128) S2 [128,256) dP [256,384) dQ1 [384,384+d) dQ2 [448,448+d)
+// dS goes back as bf16 over the columns that the thread itself has read (the first 16 of every
+// 32); a product's 16-key steps address them one by one.  All products have 128 columns or take
+// A from TMEM: with both operands in shared memory, 64 columns would read 6 KB for 32 cycles of
+// tensor work, more than its 128 bytes a cycle.
 // D for dS comes from the rounded outputs; the exact sums over j of Pm dP fall out of this pass
 // and replace it for dK, and give dlam.
-constexpr int kKeys = 64;  // keys of a step
-
 template <int d>
 struct DqL {
   static constexpr int DV = 2 * d;
-  static constexpr int kStages = 3;
+  // K is read until a block's last product, V only by its dP, one block ahead of the others
+  static constexpr int kK = 3, kV = 2;
   static constexpr int kTileBytes = DV * kTile * 2;
   static constexpr int kBoxes = DV / kBoxCols;
-  static constexpr int kStageBytes = 2 * kTileBytes;  // K then V, 128 keys
-  static constexpr int offStage = 0;
-  static constexpr int offAlong = kStages * kStageBytes;  // float [4][128]
-  static constexpr int offBar = offAlong + 4 * kTile * 4;
-  // kv_full[], kv_empty[], in_full, in_free, out_full, out_free, drain
-  static constexpr int kNumBars = 2 * kStages + 5;
+  static constexpr int offQ = 0, offDO = kTileBytes;
+  static constexpr int offK = 2 * kTileBytes, offV = offK + kK * kTileBytes;
+  static constexpr int offAlong = offK;  // float [2][4][128], once K has been used
+  static constexpr int offBar = offV + kV * kTileBytes;
+  // q_full, k_full[], k_empty[], v_full[], v_empty[], s_full[2], dp_full, dp_free, ds_full[2],
+  // acc_full, drain
+  static constexpr int kNumBars = 1 + 2 * (kK + kV) + 8;
   static constexpr int offMisc = offBar + kNumBars * 8;  // tmem address, abort flag, 4 floats
   static constexpr int kBytes = offMisc + 32;
-  static constexpr uint32_t tOut = 192, tAcc = 256, tQ = 384, tDO = 448, kTmemCols = 512;
+  static constexpr uint32_t tP = 256, tAcc = 384, kTmemCols = 512;
   static_assert(kBytes <= 232448, "shared memory budget");
 };
 
 template <int d>
 __global__ void __launch_bounds__(kThreads, 1)
-    diff_dq_kernel(const __grid_constant__ CUtensorMap tm_k,
-                   const __grid_constant__ CUtensorMap tm_v, const __nv_bfloat16 *q,
-                   const DiffBwdParams p) {
+    diff_dq_kernel(const __grid_constant__ CUtensorMap tm_q,
+                   const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v,
+                   const __grid_constant__ CUtensorMap tm_do, const DiffBwdParams p) {
   using L = DqL<d>;
   constexpr int DV = L::DV;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -115,10 +118,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) atomicOr(p.status, kErrSmemAlign);
     return;
   }
-  uint64_t *kv_full = reinterpret_cast<uint64_t *>(smem + L::offBar);
-  uint64_t *kv_empty = kv_full + L::kStages, *in_full = kv_empty + L::kStages;
-  uint64_t *in_free = in_full + 1, *out_full = in_full + 2, *out_free = in_full + 3;
-  uint64_t *drain = in_full + 4;
+  uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + L::offBar);
+  uint64_t *k_full = q_full + 1, *k_empty = k_full + L::kK;
+  uint64_t *v_full = k_empty + L::kK, *v_empty = v_full + L::kV;
+  uint64_t *s_full = v_empty + L::kV, *dp_full = s_full + 2, *dp_free = s_full + 3;
+  uint64_t *ds_full = s_full + 4, *acc_full = s_full + 6, *drain = s_full + 7;
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + L::offMisc);
   int *s_abort = reinterpret_cast<int *>(smem + L::offMisc + 4);
   float *s_part = reinterpret_cast<float *>(smem + L::offMisc + 16);
@@ -130,25 +134,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int bh = blockIdx.x / p.N;
   const int h = bh % p.H, b = bh / p.H;
   const int hkv = h / p.G;
-  const int keys = p.causal ? min(p.S, (i + 1) * kTile) : p.S;
-  const int steps = (keys + kKeys - 1) / kKeys, stages = (steps + 1) / 2;
+  const int nkv = p.causal ? i + 1 : p.N;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < L::kStages; ++s) {
-      mbar_init(&kv_full[s], 1);
-      mbar_init(&kv_empty[s], 1);
+    mbar_init(q_full, 1);
+    for (int s = 0; s < L::kK; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
     }
-    mbar_init(in_full, 1);
-    mbar_init(in_free, kWarps);
-    mbar_init(out_full, kWarps);
-    mbar_init(out_free, 1);
+    for (int s = 0; s < L::kV; ++s) {
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    for (int m = 0; m < 2; ++m) {
+      mbar_init(&s_full[m], 1);
+      mbar_init(&ds_full[m], kWarps);
+    }
+    mbar_init(dp_full, 1);
+    mbar_init(dp_free, kWarps);
+    mbar_init(acc_full, 1);
     mbar_init(drain, 1);
     *s_abort = 0;
     fence_mbar_init();
   }
   if (warp == kWarps && lane == 0) {
+    tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
+    tma_prefetch_desc(&tm_do);
   }
   if (warp == kWarps + 1) {
     tmem_alloc(s_tmem, L::kTmemCols);
@@ -158,203 +171,222 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  const int wg = warp >> 2, quad = warp & 3;
-  const int r = quad * 32 + lane;  // query row within the tile = TMEM lane
-  const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-  const int row = i * kTile + r;
-  const bool row_ok = row < p.S;
-  if (warp < kWarps) {
-    // A quarter of this row's Q1 | Q2 | dO (both of d / 2 words, the latter in two parts) into
-    // TMEM, whose columns hold the row's memory words; rows past S are zeros.
-    const size_t at = (size_t)b * p.S + row;
-    const __nv_bfloat16 *src = (wg < 2 ? q : p.dout) + (at * p.H + h) * DV + (wg & 1) * d;
-    const uint32_t to = tmem + lane_off + (wg < 2 ? L::tQ + wg * 32 : L::tDO + (wg & 1) * (d / 2));
-#pragma unroll
-    for (int c = 0; c < d / 32; ++c) {
-      uint32_t v[16];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint4 x = row_ok ? reinterpret_cast<const uint4 *>(src)[4 * c + e]
-                               : make_uint4(0u, 0u, 0u, 0u);
-        v[4 * e] = x.x, v[4 * e + 1] = x.y, v[4 * e + 2] = x.z, v[4 * e + 3] = x.w;
-      }
-      tmem_st16(to + 16 * c, v);
-    }
-    tmem_st_wait();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
 
   if (warp == kWarps && lane == 0) {
     // ------------------------------------------------------------------ TMA producer
-    int last[L::kStages];
-    for (int s = 0; s < L::kStages; ++s) last[s] = -1;
     bool ok = true;
-    for (int j = 0; j < stages; ++j) {
-      const int s = j % L::kStages;
-      const uint32_t ph = (j / L::kStages) & 1;
-      if (!mbar_wait(&kv_empty[s], ph ^ 1, ab)) {
+    int nk = 0, nv = 0;  // blocks brought in
+    mbar_arrive_expect_tx(q_full, 2 * L::kTileBytes);
+    for (int bx = 0; bx < L::kBoxes; ++bx) {
+      tma_load_4d(smem + L::offQ + bx * kBoxBytes, &tm_q, q_full, bx * kBoxCols, h, i * kTile, b);
+      tma_load_4d(smem + L::offDO + bx * kBoxBytes, &tm_do, q_full, bx * kBoxCols, h, i * kTile,
+                  b);
+    }
+    for (int j = 0; j < nkv; ++j) {
+      const int sk = j % L::kK, sv = j % L::kV;
+      if (!mbar_wait(&v_empty[sv], ((j / L::kV) & 1) ^ 1, ab)) {
         ok = false;
         break;
       }
-      mbar_arrive_expect_tx(&kv_full[s], L::kStageBytes);
-      uint8_t *sk = smem + L::offStage + s * L::kStageBytes;
-      for (int bx = 0; bx < L::kBoxes; ++bx) {
-        tma_load_4d(sk + bx * kBoxBytes, &tm_k, &kv_full[s], bx * kBoxCols, hkv, j * kTile, b);
-        tma_load_4d(sk + L::kTileBytes + bx * kBoxBytes, &tm_v, &kv_full[s], bx * kBoxCols, hkv,
-                    j * kTile, b);
+      mbar_arrive_expect_tx(&v_full[sv], L::kTileBytes);
+      for (int bx = 0; bx < L::kBoxes; ++bx)
+        tma_load_4d(smem + L::offV + sv * L::kTileBytes + bx * kBoxBytes, &tm_v, &v_full[sv],
+                    bx * kBoxCols, hkv, j * kTile, b);
+      ++nv;
+      if (!mbar_wait(&k_empty[sk], ((j / L::kK) & 1) ^ 1, ab)) {
+        ok = false;
+        break;
       }
-      last[s] = (int)ph;
+      mbar_arrive_expect_tx(&k_full[sk], L::kTileBytes);
+      for (int bx = 0; bx < L::kBoxes; ++bx)
+        tma_load_4d(smem + L::offK + sk * L::kTileBytes + bx * kBoxBytes, &tm_k, &k_full[sk],
+                    bx * kBoxCols, hkv, j * kTile, b);
+      ++nk;
     }
-    if (!ok)
-      for (int s = 0; s < L::kStages; ++s)
-        if (last[s] >= 0) mbar_wait_drain(&kv_full[s], (uint32_t)last[s], 100000000ull);
+    if (!ok) {  // leave no copy in flight into shared memory
+      mbar_wait_drain(q_full, 0, 100000000ull);
+      for (int j = max(0, nv - L::kV); j < nv; ++j)
+        mbar_wait_drain(&v_full[j % L::kV], (j / L::kV) & 1, 100000000ull);
+      for (int j = max(0, nk - L::kK); j < nk; ++j)
+        mbar_wait_drain(&k_full[j % L::kK], (j / L::kK) & 1, 100000000ull);
+    }
   } else if (warp == kWarps + 1) {
     // ------------------------------------------------------------------ MMA issuer
     // The whole warp runs the loop, so that descriptors and control flow stay warp-uniform;
     // one elected lane issues (one lane alone forms every descriptor in vector registers and
-    // moves it over: the issue then bounds these short products).
-    constexpr uint32_t kIdescIn = make_idesc_bf16(128, kKeys, false, false);
+    // moves it over, which bounds short products).
+    constexpr uint32_t kIdescIn = make_idesc_bf16(128, 128, false, false);
     constexpr uint32_t kIdescQ = make_idesc_bf16(128, d, false, true);
     const uint32_t sbase = smem_u32(smem);
-    auto step_at = [&](int t) {  // K rows of step t
-      return sbase + L::offStage + ((t >> 1) % L::kStages) * L::kStageBytes +
-             (t & 1) * (kKeys * 128);
-    };
-    // S1, S2 and dP of step t; keys (t & 1) * 64 on of its stage
-    auto issue_in = [&](int t) -> bool {
-      if (!(t & 1) && !mbar_wait_warp(&kv_full[(t >> 1) % L::kStages],
-                                      ((t >> 1) / L::kStages) & 1, ab))
-        return false;
-      tc_fence_after();
-      const uint32_t loK = desc_lo(step_at(t), 16), loV = desc_lo(step_at(t) + L::kTileBytes, 16);
+    const uint32_t loQ = desc_lo(sbase + L::offQ, 16), loDO = desc_lo(sbase + L::offDO, 16);
+    auto k_at = [&](int j) { return sbase + L::offK + (j % L::kK) * L::kTileBytes; };
+    auto issue_s = [&](int j, int m) {
+      const uint32_t loK = desc_lo(k_at(j), 16);
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int k = 0; k < d / 16; ++k)
-          mma_ts_e(tmem + m * 64, tmem + L::tQ + m * 32 + 8 * k,
-                   desc_of(loK + (col_bytes(m * d + 16 * k) >> 4)), kIdescIn, k > 0);
-#pragma unroll
-      for (int k = 0; k < DV / 16; ++k)
-        mma_ts_e(tmem + 128, tmem + L::tDO + 8 * k, desc_of(loV + (col_bytes(16 * k) >> 4)),
-                 kIdescIn, k > 0);
-      mma_commit_e(in_full);
-      return true;
-    };
-    bool ok = issue_in(0);
-    for (int t = 0; ok && t < steps; ++t) {
-      if (t + 1 < steps && !(mbar_wait_warp(in_free, t & 1, ab) && issue_in(t + 1))) {
-        ok = false;
-        break;
+      for (int k = 0; k < d / 16; ++k) {
+        const uint32_t off = col_bytes(m * d + 16 * k) >> 4;
+        mma_ss_e(tmem + m * 128, desc_of(loQ + off), desc_of(loK + off), kIdescIn, k > 0);
       }
-      if (!mbar_wait_warp(out_full, t & 1, ab)) {
-        ok = false;
-        break;
+      mma_commit_e(&s_full[m]);
+    };
+    auto issue_dp = [&](int j) {
+      const uint32_t loV = desc_lo(sbase + L::offV + (j % L::kV) * L::kTileBytes, 16);
+#pragma unroll
+      for (int k = 0; k < DV / 16; ++k) {
+        const uint32_t off = col_bytes(16 * k) >> 4;
+        mma_ss_e(tmem + L::tP, desc_of(loDO + off), desc_of(loV + off), kIdescIn, k > 0);
       }
+      mma_commit_e(dp_full);
+      mma_commit_e(&v_empty[j % L::kV]);
+    };
+    auto k_there = [&](int j) { return mbar_wait_warp(&k_full[j % L::kK], (j / L::kK) & 1, ab); };
+    auto v_there = [&](int j) { return mbar_wait_warp(&v_full[j % L::kV], (j / L::kV) & 1, ab); };
+    bool ok = mbar_wait_warp(q_full, 0, ab) && k_there(0) && v_there(0);
+    if (ok) {
       tc_fence_after();
-      const uint32_t loK = desc_lo(step_at(t), kBoxBytes);
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k)
-          mma_ts_e(tmem + L::tAcc + m * 64, tmem + L::tOut + m * 32 + 8 * k,
-                   desc_of(loK + ((col_bytes(m * d) + k * 2048) >> 4)), kIdescQ,
-                   (t > 0 || k > 0) ? 1u : 0u);
-      mma_commit_e(out_free);
-      if (t & 1) mma_commit_e(&kv_empty[(t >> 1) % L::kStages]);
+      issue_s(0, 0);
+      issue_dp(0);
+      issue_s(0, 1);
     }
+    for (int j = 0; ok && j < nkv; ++j) {
+      const bool more = j + 1 < nkv;
+      if (!mbar_wait_warp(dp_free, j & 1, ab) || (more && !v_there(j + 1))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      if (more) issue_dp(j + 1);
+      const uint32_t loK = desc_lo(k_at(j), kBoxBytes);
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        if (ok && !mbar_wait_warp(&ds_full[m], j & 1, ab)) ok = false;
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          mma_ts_e(tmem + L::tAcc + m * 64, tmem + m * 128 + 32 * (k >> 1) + 8 * (k & 1),
+                   desc_of(loK + ((col_bytes(m * d) + k * 2048) >> 4)), kIdescQ,
+                   (j > 0 || k > 0) ? 1u : 0u);
+        if (m == 1) mma_commit_e(&k_empty[j % L::kK]);
+        if (more) {
+          if (m == 0 && !k_there(j + 1)) {
+            ok = false;
+            break;
+          }
+          issue_s(j + 1, m);
+        }
+      }
+    }
+    if (ok) mma_commit_e(acc_full);
     mma_commit_e(drain);
     mbar_wait_drain(drain, 0, 100000000ull);
   } else if (warp < kWarps) {
-    // ------------------------------------------------------------------ dS of map m
-    const int m = wg >> 1, k0 = 32 * (wg & 1);
+    // ------------------------------------------------------------------ dS
+    const int wg = warp >> 2, quad = warp & 3;
+    const int r = quad * 32 + lane;  // query row within the tile = TMEM lane
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const int row = i * kTile + r;
+    const bool row_ok = row < p.S;
     float *rowv = p.rowv + (((size_t)b * p.H + h) * p.N + i) * (kRowVecs * kTile) + r;
-    const float nlse = rowv[m * kTile], nD = rowv[(2 + m) * kTile];
-    const f2 c2 = f2_of(p.scale_log2, p.scale_log2), nl2 = f2_of(nlse, nlse), nD2 = f2_of(nD, nD);
-    f2 along2 = f2_of(0.f, 0.f);  // sum_j Pm dP of this row, even and odd keys
-    const uint32_t tS = tmem + lane_off + m * 64 + k0, tP = tmem + lane_off + 128 + k0;
-    const uint32_t tO = tmem + lane_off + L::tOut + m * 32 + k0 / 2;
+    const f2 c2 = f2_of(p.scale_log2, p.scale_log2);
+    float nl[2], nD[2];
+    f2 along[2];  // sum_j Pm dP of this row, even and odd keys
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      nl[m] = rowv[m * kTile];
+      nD[m] = rowv[(2 + m) * kTile];
+      along[m] = f2_of(0.f, 0.f);
+    }
+    const uint32_t t0 = tmem + lane_off + 32 * wg;
     bool ok = true;
-    for (int t = 0; t < steps; ++t) {
-      if (!mbar_wait_warp(in_full, t & 1, ab)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      uint32_t s[32], g[32];
-      tmem_ld32(tS, s);
-      tmem_ld32(tP, g);
-      tmem_ld_wait_for(s);
-      tmem_ld_wait_for(g);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(in_free);
-      // of these 32 keys, those that the row sees
-      const int limit = min(p.S, p.causal ? row + 1 : p.S) - t * kKeys - k0;
-      if (__any_sync(0xffffffffu, limit < 32)) {
+    for (int j = 0; ok && j < nkv; ++j) {
+      // of this thread's 32 keys, those that the row sees
+      const int limit = min(p.S, p.causal ? row + 1 : p.S) - j * kTile - 32 * wg;
+      const bool cut = __any_sync(0xffffffffu, limit < 32);
+      uint32_t g[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-          if (e >= limit) s[e] = __float_as_uint(-INFINITY), g[e] = 0u;
-      }
-      uint32_t pk[16];
+      for (int m = 0; m < 2; ++m) {
+        uint32_t s[32];
+        if (ok) ok = mbar_wait_warp(&s_full[m], j & 1, ab) &&
+                     (m == 1 || mbar_wait_warp(dp_full, j & 1, ab));
+        if (!ok) break;
+        tc_fence_after();
+        tmem_ld32(t0 + m * 128, s);
+        if (m == 0) tmem_ld32(t0 + L::tP, g);
+        tmem_ld_wait_for(s);
+        if (m == 0) {
+          tmem_ld_wait_for(g);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(dp_free);
+        }
+        if (cut) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const f2 P = ex2_2(fma2(f2_of(s[2 * e], s[2 * e + 1]), c2, nl2));
-        const f2 dP = f2_of(g[2 * e], g[2 * e + 1]);
-        along2 = fma2(P, dP, along2);
-        pk[e] = pack_bf16(mul2(P, add2(dP, nD2)));
+          for (int e = 0; e < 32; ++e)
+            if (e >= limit) s[e] = __float_as_uint(-INFINITY), g[e] = 0u;
+        }
+        const f2 nl2 = f2_of(nl[m], nl[m]), nD2 = f2_of(nD[m], nD[m]);
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const f2 P = ex2_2(fma2(f2_of(s[2 * e], s[2 * e + 1]), c2, nl2));
+          const f2 dP = f2_of(g[2 * e], g[2 * e + 1]);
+          along[m] = fma2(P, dP, along[m]);
+          pk[e] = pack_bf16(mul2(P, add2(dP, nD2)));
+        }
+        tmem_st16(t0 + m * 128, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ds_full[m]);
       }
-      if (t > 0 && !mbar_wait_warp(out_free, (t - 1) & 1, ab)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      tmem_st16(tO, pk);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(out_full);
     }
     // ------------------------------------------------------------------ epilogue
-    float along, odd;
-    f2_to(along2, along, odd);
-    s_along[wg * kTile + r] = along + odd;
-    named_bar_sync(1, kWarps * 32);
-    const float D = s_along[2 * m * kTile + r] + s_along[(2 * m + 1) * kTile + r];
-    if (wg & 1) {
-      if (row_ok) rowv[(2 + m) * kTile] = -D;
-    } else if (m == 1) {
-      if (p.lam_token) {
-        const size_t at = ((size_t)b * p.S + row) * p.H + h;
-        if (row_ok) {
-          if (p.lam_f32)
-            static_cast<float *>(p.dlam)[at] = -D;
-          else
-            static_cast<__nv_bfloat16 *>(p.dlam)[at] = __float2bfloat16_rn(-D);
-        }
-      } else {
-        float sum = row_ok ? D : 0.f;
+    ok = ok && mbar_wait_warp(acc_full, 0, ab);  // every product has run: K's memory is free
+    if (!ok) mbar_wait_drain(drain, 0, 100000000ull);
+    tc_fence_after();
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) s_part[quad] = sum;
-        named_bar_sync(2, 128);
-        if (quad == 0 && lane == 0)
-          p.dlam_part[((size_t)b * p.H + h) * p.N + i] =
-              -((s_part[0] + s_part[1]) + (s_part[2] + s_part[3]));
+    for (int m = 0; m < 2; ++m) {
+      float even, odd;
+      f2_to(along[m], even, odd);
+      s_along[(m * 4 + wg) * kTile + r] = even + odd;
+    }
+    named_bar_sync(1, kWarps * 32);
+    if (wg < 2) {
+      const float *al = s_along + wg * 4 * kTile + r;
+      const float D = (al[0] + al[kTile]) + (al[2 * kTile] + al[3 * kTile]);
+      if (row_ok) rowv[(2 + wg) * kTile] = -D;
+      if (wg == 1) {
+        if (p.lam_token) {
+          const size_t at = ((size_t)b * p.S + row) * p.H + h;
+          if (row_ok) {
+            if (p.lam_f32)
+              static_cast<float *>(p.dlam)[at] = -D;
+            else
+              static_cast<__nv_bfloat16 *>(p.dlam)[at] = __float2bfloat16_rn(-D);
+          }
+        } else {
+          float sum = row_ok ? D : 0.f;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          if (lane == 0) s_part[quad] = sum;
+          named_bar_sync(2, 128);
+          if (quad == 0 && lane == 0)
+            p.dlam_part[((size_t)b * p.H + h) * p.N + i] =
+                -((s_part[0] + s_part[1]) + (s_part[2] + s_part[3]));
+        }
       }
     }
-    if (ok && mbar_wait_warp(out_free, (steps - 1) & 1, ab)) {
-      tc_fence_after();
+    if (ok) {
       // half of dQm's columns; dS2 was formed without its weight, a factor of the row
+      const int m = wg >> 1, half = (wg & 1) * (d / 2);
       const float by = m ? rowv[4 * kTile] * p.scale : p.scale;
-      __nv_bfloat16 *out =
-          p.dq + (((size_t)b * p.S + row) * 2 * p.H + 2 * h + m) * d + (wg & 1) * (d / 2);
+      __nv_bfloat16 *out = p.dq + (((size_t)b * p.S + row) * 2 * p.H + 2 * h + m) * d + half;
       uint32_t v[d / 2];
       if constexpr (d == 64)
-        tmem_ld32(tmem + lane_off + L::tAcc + m * 64 + (wg & 1) * 32, v);
+        tmem_ld32(tmem + lane_off + L::tAcc + m * 64 + half, v);
       else
-        tmem_ld16(tmem + lane_off + L::tAcc + m * 64 + (wg & 1) * 16, v);
+        tmem_ld16(tmem + lane_off + L::tAcc + m * 64 + half, v);
       tmem_ld_wait_for(v);
       if (row_ok) store_row(out, v, by);
     }
@@ -390,16 +422,15 @@ __global__ void __launch_bounds__(256) diff_dlam_kernel(const DiffBwdParams p) {
 }
 
 // -------------------------------------------------------------------- dK, dV
-// CTA: a 128-key block of one KV head, over the query heads of its group and their tiles in
-// ascending order, in steps of 64 queries with everything transposed (thread = key row, so
-// the bf16 operands P^T, dS1^T go back to TMEM where their rows are):
-//   dV [0,dv)  dK1 [128,128+d) dK2 [192,192+d)
-//   in: S1^T [256,320) S2^T [320,384) dP^T [384,448)   out: P^T [448,480) dS1^T [480,512)
-// The step's inputs go to registers at once, which frees their columns for the next step's
-// products; dS2^T finds no room in TMEM and goes through shared memory.  The four warpgroups
-// share a step's queries (16 each).
-constexpr int kQueries = 64;
-
+// CTA: a 128-key block of one KV head, over the query heads of its group and their 128-row
+// tiles in ascending order, everything transposed (thread = key row, so that the bf16 operands
+// P^T and dS^T go back to TMEM where their rows are; 32 queries a warpgroup).  dV, dK1 and dK2
+// leave two blocks of 128 columns, X and Y, which the three inputs of a tile share in turn:
+//   elementwise   A: S1 (X) -> P1 | B: S2 (Y) -> P (over S2) | C: dP (X) -> dS1, dS2 | A ...
+//   tensor core   dK of the last tile, S2 | dP (X, once S1 is in registers) | dV, next S1 (X)
+// P over the first 16 of every 32 columns of Y, dS1 the other 16; dS2 takes P's place once the
+// product for dV has read it.
+//   dV [0,dv)  dK1 [128,128+d) dK2 [192,192+d)  X [256,384) Y [384,512)
 template <int d>
 struct DkvL {
   static constexpr int DV = 2 * d;
@@ -410,14 +441,14 @@ struct DkvL {
   static constexpr int offK = 0, offV = kTileBytes;
   static constexpr int offStage = 2 * kTileBytes;  // per stage Q, dO
   static constexpr int kStageBytes = 2 * kTileBytes;
-  static constexpr int offDS = offStage + kStages * kStageBytes;  // dS2^T, one box
-  static constexpr int offRow = offDS + kBoxBytes;                // per stage row vectors
+  static constexpr int offRow = offStage + kStages * kStageBytes;  // per stage row vectors
   static constexpr int offBar = offRow + kStages * kRowBytes;
-  // kv_full, q_full[2], q_empty[2], in_full, in_free, out_full, out_free, acc_full, drain
-  static constexpr int kNumBars = 1 + 2 * kStages + 6;
+  // kv_full, q_full[], q_empty[], s1_full, s2_full, dp_full, s1_free, dp_free, p_full, dv_done,
+  // ds_full, acc_full, drain
+  static constexpr int kNumBars = 1 + 2 * kStages + 10;
   static constexpr int offMisc = offBar + kNumBars * 8;
   static constexpr int kBytes = offMisc + 16;
-  static constexpr uint32_t tV = 0, tK = 128, tIn = 256, tP = 448, tDS = 480, kTmemCols = 512;
+  static constexpr uint32_t tV = 0, tK = 128, tX = 256, tY = 384, kTmemCols = 512;
   static_assert(kBytes <= 232448, "shared memory budget");
 };
 
@@ -436,8 +467,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   uint64_t *kv_full = reinterpret_cast<uint64_t *>(smem + L::offBar);
   uint64_t *q_full = kv_full + 1, *q_empty = q_full + L::kStages;
-  uint64_t *in_full = q_empty + L::kStages, *in_free = in_full + 1, *out_full = in_full + 2;
-  uint64_t *out_free = in_full + 3, *acc_full = in_full + 4, *drain = in_full + 5;
+  uint64_t *s1_full = q_empty + L::kStages, *s2_full = s1_full + 1, *dp_full = s1_full + 2;
+  uint64_t *s1_free = s1_full + 3, *dp_free = s1_full + 4, *p_full = s1_full + 5;
+  uint64_t *dv_done = s1_full + 6, *ds_full = s1_full + 7, *acc_full = s1_full + 8;
+  uint64_t *drain = s1_full + 9;
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + L::offMisc);
   int *s_abort = reinterpret_cast<int *>(smem + L::offMisc + 4);
   const Abort ab{s_abort, p.status, p.wait_ns};
@@ -449,16 +482,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int hkv = bh % p.Hkv, b = bh / p.Hkv;
   const int i0 = p.causal ? j : 0, tiles = p.N - i0;
   const int stages = p.G * tiles;
-  // the last tile has one step where S ends in its first half
-  const int last_steps = p.S - (p.N - 1) * kTile > kQueries ? 2 : 1;
-  const int steps = p.G * (2 * (tiles - 1) + last_steps);
-  // advances (tile, half) to the next step; true where a new stage begins
-  auto next = [&](int &i, int &u) {
-    if (++u < (i == p.N - 1 ? last_steps : 2)) return false;
-    u = 0;
-    if (++i == p.N) i = i0;
-    return true;
-  };
 
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
@@ -466,10 +489,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&q_full[s], 1);
       mbar_init(&q_empty[s], kWarps + 1);  // the products' commit, the readers of row vectors
     }
-    mbar_init(in_full, 1);
-    mbar_init(in_free, kWarps);
-    mbar_init(out_full, kWarps);
-    mbar_init(out_free, 1);
+    mbar_init(s1_full, 1);
+    mbar_init(s2_full, 1);
+    mbar_init(dp_full, 1);
+    mbar_init(s1_free, kWarps);
+    mbar_init(dp_free, kWarps);
+    mbar_init(p_full, kWarps);
+    mbar_init(dv_done, 1);
+    mbar_init(ds_full, kWarps);
     mbar_init(acc_full, 1);
     mbar_init(drain, 1);
     *s_abort = 0;
@@ -530,155 +557,219 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kWarps + 1) {
     // ------------------------------------------------------------------ MMA issuer
     // (a converged warp, one elected lane issues)
-    constexpr uint32_t kIdescIn = make_idesc_bf16(128, kQueries, false, false);
+    constexpr uint32_t kIdescIn = make_idesc_bf16(128, 128, false, false);
     constexpr uint32_t kIdescV = make_idesc_bf16(128, DV, false, true);
     constexpr uint32_t kIdescK = make_idesc_bf16(128, d, false, true);
     const uint32_t sbase = smem_u32(smem);
     const uint32_t loK = desc_lo(sbase + L::offK, 16), loV = desc_lo(sbase + L::offV, 16);
-    const uint32_t loDS = desc_lo(sbase + L::offDS, 16);
-    auto step_at = [&](int n, int u) {  // Q rows of half u of stage n
-      return sbase + L::offStage + (n % L::kStages) * L::kStageBytes + u * (kQueries * 128);
+    auto stage_at = [&](int n) {
+      return sbase + L::offStage + (n % L::kStages) * L::kStageBytes;
     };
-    // S1^T, S2^T and dP^T of half u of stage n
-    auto issue_in = [&](int n, int u) -> bool {
-      if (u == 0 && !mbar_wait_warp(&q_full[n % L::kStages], (n / L::kStages) & 1, ab))
-        return false;
+    auto issue_s = [&](int n, int m) {  // S1^T -> X, S2^T -> Y
+      const uint32_t loQ = desc_lo(stage_at(n), 16);
+#pragma unroll
+      for (int k = 0; k < d / 16; ++k) {
+        const uint32_t off = col_bytes(m * d + 16 * k) >> 4;
+        mma_ss_e(tmem + (m ? L::tY : L::tX), desc_of(loK + off), desc_of(loQ + off), kIdescIn,
+                 k > 0);
+      }
+      mma_commit_e(m ? s2_full : s1_full);
+    };
+    auto q_there = [&](int n) {
+      return mbar_wait_warp(&q_full[n % L::kStages], (n / L::kStages) & 1, ab);
+    };
+    bool ok = mbar_wait_warp(kv_full, 0, ab) && q_there(0);
+    if (ok) {
       tc_fence_after();
-      const uint32_t loQ = desc_lo(step_at(n, u), 16);
-      const uint32_t loO = desc_lo(step_at(n, u) + L::kTileBytes, 16);
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int k = 0; k < d / 16; ++k) {
-          const uint32_t off = col_bytes(m * d + 16 * k) >> 4;
-          mma_ss_e(tmem + L::tIn + m * 64, desc_of(loK + off), desc_of(loQ + off), kIdescIn, k > 0);
-        }
+      issue_s(0, 0);
+      issue_s(0, 1);
+    }
+    for (int n = 0; ok && n < stages; ++n) {
+      const bool more = n + 1 < stages;
+      const uint32_t ph = n & 1, first = n > 0 ? 1u : 0u;
+      const uint32_t aQ = stage_at(n), aO = aQ + L::kTileBytes;
+      const uint32_t loO = desc_lo(aO, 16), loOmn = desc_lo(aO, kBoxBytes);
+      const uint32_t loQmn = desc_lo(aQ, kBoxBytes);
+      if (!mbar_wait_warp(s1_free, ph, ab)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
 #pragma unroll
       for (int k = 0; k < DV / 16; ++k) {
         const uint32_t off = col_bytes(16 * k) >> 4;
-        mma_ss_e(tmem + L::tIn + 128, desc_of(loV + off), desc_of(loO + off), kIdescIn, k > 0);
+        mma_ss_e(tmem + L::tX, desc_of(loV + off), desc_of(loO + off), kIdescIn, k > 0);
       }
-      mma_commit_e(in_full);
-      return true;
-    };
-    bool ok = mbar_wait_warp(kv_full, 0, ab) && issue_in(0, 0);
-    int i = i0, u = 0, n = 0;     // step t
-    int i1 = i0, u1 = 0, n1 = 0;  // step t + 1
-    if (next(i1, u1)) ++n1;
-    for (int t = 0; ok && t < steps; ++t) {
-      if (t + 1 < steps && !(mbar_wait_warp(in_free, t & 1, ab) && issue_in(n1, u1))) {
-        ok = false;
-        break;
-      }
-      if (!mbar_wait_warp(out_full, t & 1, ab)) {
+      mma_commit_e(dp_full);
+      if (!mbar_wait_warp(p_full, ph, ab)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const uint32_t loQ = desc_lo(step_at(n, u), kBoxBytes);
-      const uint32_t loO = desc_lo(step_at(n, u) + L::kTileBytes, kBoxBytes);
-      const uint32_t first = t > 0 ? 1u : 0u;
 #pragma unroll
-      for (int k = 0; k < kQueries / 16; ++k)
-        mma_ts_e(tmem + L::tV, tmem + L::tP + 8 * k, desc_of(loO + ((k * 2048) >> 4)), kIdescV,
-                 k > 0 ? 1u : first);
-#pragma unroll
-      for (int k = 0; k < kQueries / 16; ++k)
-        mma_ts_e(tmem + L::tK, tmem + L::tDS + 8 * k, desc_of(loQ + ((k * 2048) >> 4)), kIdescK,
-                 k > 0 ? 1u : first);
-#pragma unroll
-      for (int k = 0; k < kQueries / 16; ++k)
-        mma_ss_e(tmem + L::tK + 64, desc_of(loDS + ((k * 32) >> 4)),
-                 desc_of(loQ + ((col_bytes(d) + k * 2048) >> 4)), kIdescK, k > 0 ? 1u : first);
-      mma_commit_e(out_free);
-      const int s = n % L::kStages;
-      if (next(i, u)) {
-        ++n;
-        mma_commit_e(&q_empty[s]);
+      for (int k = 0; k < kTile / 16; ++k)
+        mma_ts_e(tmem + L::tV, tmem + L::tY + 32 * (k >> 1) + 8 * (k & 1),
+                 desc_of(loOmn + ((k * 2048) >> 4)), kIdescV, k > 0 ? 1u : first);
+      mma_commit_e(dv_done);
+      if (!mbar_wait_warp(dp_free, ph, ab) || (more && !q_there(n + 1))) {
+        ok = false;
+        break;
       }
-      if (next(i1, u1)) ++n1;
+      tc_fence_after();
+      if (more) issue_s(n + 1, 0);
+      if (!mbar_wait_warp(ds_full, ph, ab)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          mma_ts_e(tmem + L::tK + 64 * m,
+                   tmem + L::tY + (m ? 0 : 16) + 32 * (k >> 1) + 8 * (k & 1),
+                   desc_of(loQmn + ((col_bytes(m * d) + k * 2048) >> 4)), kIdescK,
+                   k > 0 ? 1u : first);
+      mma_commit_e(&q_empty[n % L::kStages]);
+      if (more) issue_s(n + 1, 1);
     }
     if (ok) mma_commit_e(acc_full);
     mma_commit_e(drain);
     mbar_wait_drain(drain, 0, 100000000ull);
   } else if (warp < kWarps) {
     // ------------------------------------------------------------------ P, dS (transposed)
+    // In fragments (tmem_ld_frag): the row vectors go by query, a column here; read for every
+    // element they would cost 40 broadcast loads of 16 bytes a warp and tile on the memory that
+    // feeds the tensor core, in fragments 20 of 8 bytes.
     const int wg = warp >> 2;
     const int quad = warp & 3;
-    const int r = quad * 32 + lane;  // key row within the block = TMEM lane
+    const int r = quad * 32 + lane;  // key row of the epilogue = TMEM lane
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    const uint32_t tI = tmem + lane_off + L::tIn + 16 * wg;
+    const uint32_t tX = tmem + lane_off + L::tX + 32 * wg, tY = tmem + lane_off + L::tY + 32 * wg;
+    constexpr uint32_t kLanes16 = 16u << 16;
     const int key = j * kTile + r;
-    uint8_t *ds_row = smem + L::offDS + r * 128;
     const f2 c2 = f2_of(p.scale_log2, p.scale_log2);
+    // key of fragment row 0 less the query of its column 0, within the diagonal tile
+    const int ahead = quad * 32 + lane / 4 - (32 * wg + 2 * (lane & 3));
     bool ok = true;
-    int i = i0, u = 0, n = 0;
-    for (int t = 0; t < steps; ++t) {
-      if (!mbar_wait_warp(in_full, t & 1, ab)) {
+    for (int n = 0; n < stages; ++n) {
+      const uint32_t ph = n & 1;
+      const int s = n % L::kStages;
+      const float *rv = reinterpret_cast<const float *>(smem + L::offRow + s * L::kRowBytes) +
+                        32 * wg + 2 * (lane & 3);
+      auto vec = [&](int k, int g) {  // row vector k of this thread's columns of group g
+        return *reinterpret_cast<const f2 *>(rv + k * kTile + 8 * g);
+      };
+      // on the diagonal tile, queries before the key see nothing of it
+      const bool cut = p.causal && n % tiles == 0;
+      auto hide = [&](uint32_t (&x)[16], int half, uint32_t with) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)  // key - query of the element
+          if (ahead + 16 * half + 8 * ((e >> 1) & 1) - 8 * (e >> 2) - (e & 1) > 0) x[e] = with;
+      };
+      f2 P1[2][8], w[2][8];  // P1, -lam P2; [half of the lanes][2 * group + row]
+      // A
+      if (!mbar_wait_warp(s1_full, ph, ab)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      uint32_t s1[16], s2[16], g[16];
-      tmem_ld16(tI, s1);
-      tmem_ld16(tI + 64, s2);
-      tmem_ld16(tI + 128, g);
-      tmem_ld_wait_for(s1);
-      tmem_ld_wait_for(s2);
-      tmem_ld_wait_for(g);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(in_free);
-      const int s = n % L::kStages;
-      const int q0 = u * kQueries + 16 * wg;  // first query within the tile
-      const float *rv = reinterpret_cast<const float *>(smem + L::offRow + s * L::kRowBytes) + q0;
-      // queries before this key see nothing of it
-      const int from = p.causal && i == j ? r - q0 : 0;
-      if (__any_sync(0xffffffffu, from > 0)) {
+      {
+        uint32_t x[2][16];
+        tmem_ld_frag(tX, x[0]);
+        tmem_ld_frag(tX + kLanes16, x[1]);
+        tmem_ld_wait_for(x[0]);
+        tmem_ld_wait_for(x[1]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s1_free);
+        if (cut) {
+          hide(x[0], 0, __float_as_uint(-INFINITY));
+          hide(x[1], 1, __float_as_uint(-INFINITY));
+        }
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (e < from) s1[e] = s2[e] = __float_as_uint(-INFINITY), g[e] = 0u;
-      }
-      uint32_t pP[8], p1[8], p2[8];
+        for (int g = 0; g < 4; ++g) {
+          const f2 nl = vec(0, g);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        // row vectors of four queries, the same for every lane
-        ulonglong2 v[kRowVecs];
-#pragma unroll
-        for (int k = 0; k < kRowVecs; ++k)
-          v[k] = *reinterpret_cast<const ulonglong2 *>(rv + k * kTile + 4 * e);
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          const int c = 4 * e + 2 * z;
-          auto at = [&](int k) { return z ? v[k].y : v[k].x; };
-          const f2 P1 = ex2_2(fma2(f2_of(s1[c], s1[c + 1]), c2, at(0)));
-          const f2 w = mul2(ex2_2(fma2(f2_of(s2[c], s2[c + 1]), c2, at(1))), at(4));  // -lam P2
-          const f2 dP = f2_of(g[c], g[c + 1]);
-          pP[2 * e + z] = pack_bf16(add2(P1, w));
-          p1[2 * e + z] = pack_bf16(mul2(P1, add2(dP, at(2))));
-          p2[2 * e + z] = pack_bf16(mul2(w, add2(dP, at(3))));
+          for (int e = 0; e < 4; ++e) {
+            const int half = e >> 1, at = 2 * g + (e & 1);
+            P1[half][at] =
+                ex2_2(fma2(f2_of(x[half][2 * at], x[half][2 * at + 1]), c2, nl));
+          }
         }
       }
-      if (t > 0 && !mbar_wait_warp(out_free, (t - 1) & 1, ab)) {
+      // B
+      if (!mbar_wait_warp(s2_full, ph, ab)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      tmem_st8(tmem + lane_off + L::tP + 8 * wg, pP);
-      tmem_st8(tmem + lane_off + L::tDS + 8 * wg, p1);
+      {
+        f2 nl[4], nlam[4];
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-        *reinterpret_cast<uint4 *>(ds_row + (((2 * wg + c) ^ (r & 7)) << 4)) =
-            make_uint4(p2[4 * c], p2[4 * c + 1], p2[4 * c + 2], p2[4 * c + 3]);
+        for (int g = 0; g < 4; ++g) nl[g] = vec(1, g), nlam[g] = vec(4, g);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t x[16], pk[8];
+          tmem_ld_frag(tY + half * kLanes16, x);
+          tmem_ld_wait_for(x);
+          if (cut) hide(x, half, __float_as_uint(-INFINITY));
+#pragma unroll
+          for (int at = 0; at < 8; ++at) {
+            w[half][at] =
+                mul2(ex2_2(fma2(f2_of(x[2 * at], x[2 * at + 1]), c2, nl[at >> 1])), nlam[at >> 1]);
+            pk[at] = pack_bf16(add2(P1[half][at], w[half][at]));
+          }
+          tmem_st_frag(tY + half * kLanes16, pk);
+        }
+      }
       tmem_st_wait();
-      fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(out_full);
-      if (next(i, u)) {
-        ++n;
-        if (lane == 0) mbar_arrive(&q_empty[s]);
+      if (lane == 0) mbar_arrive(p_full);
+      // C
+      if (!mbar_wait_warp(dp_full, ph, ab)) {
+        ok = false;
+        break;
       }
+      tc_fence_after();
+      uint32_t pk2[2][8];
+      {
+        f2 nD1[4], nD2[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) nD1[g] = vec(2, g), nD2[g] = vec(3, g);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t x[16], pk[8];
+          tmem_ld_frag(tX + half * kLanes16, x);
+          tmem_ld_wait_for(x);
+          if (half) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(dp_free);
+          }
+          if (cut) hide(x, half, 0u);
+#pragma unroll
+          for (int at = 0; at < 8; ++at) {
+            const f2 dP = f2_of(x[2 * at], x[2 * at + 1]);
+            pk[at] = pack_bf16(mul2(P1[half][at], add2(dP, nD1[at >> 1])));
+            pk2[half][at] = pack_bf16(mul2(w[half][at], add2(dP, nD2[at >> 1])));
+          }
+          tmem_st_frag(tY + 16 + half * kLanes16, pk);
+        }
+      }
+      if (lane == 0) mbar_arrive(&q_empty[s]);
+      if (!mbar_wait_warp(dv_done, ph, ab)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      tmem_st_frag(tY, pk2[0]);
+      tmem_st_frag(tY + kLanes16, pk2[1]);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ds_full);
     }
     if (ok && mbar_wait_warp(acc_full, 0, ab)) {
       tc_fence_after();
@@ -707,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int d>
 cudaError_t launch_t(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
-                     const CUtensorMap &tdo, const __nv_bfloat16 *q,
+                     const CUtensorMap &tdo,
                      const DiffBwdParams &p, cudaStream_t s) {
   using LQ = DqL<d>;
   using LK = DkvL<d>;
@@ -719,7 +810,7 @@ cudaError_t launch_t(const CUtensorMap &tq, const CUtensorMap &tk, const CUtenso
   if (e != cudaSuccess) return e;
   const unsigned tiles = (unsigned)p.B * p.H * p.N;
   diff_rows_kernel<d><<<tiles, 256, 0, s>>>(p);
-  diff_dq_kernel<d><<<tiles, kThreads, LQ::kBytes, s>>>(tk, tv, q, p);
+  diff_dq_kernel<d><<<tiles, kThreads, LQ::kBytes, s>>>(tq, tk, tv, tdo, p);
   if (!p.lam_token) diff_dlam_kernel<<<p.H, 256, 0, s>>>(p);
   diff_dkv_kernel<d>
       <<<(unsigned)p.B * p.Hkv * p.N, kThreads, LK::kBytes, s>>>(tq, tk, tv, tdo, p);
@@ -729,9 +820,9 @@ cudaError_t launch_t(const CUtensorMap &tq, const CUtensorMap &tk, const CUtenso
 }  // namespace
 
 cudaError_t launch_diff_bwd(int d, const CUtensorMap &tq, const CUtensorMap &tk,
-                            const CUtensorMap &tv, const CUtensorMap &tdo, const __nv_bfloat16 *q,
+                            const CUtensorMap &tv, const CUtensorMap &tdo,
                             const DiffBwdParams &p, cudaStream_t s) {
-  return d == 32 ? launch_t<32>(tq, tk, tv, tdo, q, p, s) : launch_t<64>(tq, tk, tv, tdo, q, p, s);
+  return d == 32 ? launch_t<32>(tq, tk, tv, tdo, p, s) : launch_t<64>(tq, tk, tv, tdo, p, s);
 }
 
 }  // namespace dash
