@@ -118,8 +118,10 @@ dash_status_t dash_diff_bwd(const void *q, const void *k, const void *v, const v
   if ((st = device_info(&dev)) != DASH_OK) return st;
   const int Hkv = H / group;
   CUtensorMap tq, tk, tv, tdo;
-  if (!make_bshd_map(&tq, q, B, S, H, 2 * d) || !make_bshd_map(&tk, k, B, S, Hkv, 2 * d) ||
-      !make_bshd_map(&tv, v, B, S, Hkv, 2 * d) || !make_bshd_map(&tdo, dout, B, S, H, 2 * d))
+  // Q and dO stream through dK/dV's kernel by half tiles, K and V are read by whole ones
+  if (!make_bshd_map(&tq, q, B, S, H, 2 * d, kTile / 2) ||
+      !make_bshd_map(&tk, k, B, S, Hkv, 2 * d) || !make_bshd_map(&tv, v, B, S, Hkv, 2 * d) ||
+      !make_bshd_map(&tdo, dout, B, S, H, 2 * d, kTile / 2))
     return DASH_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (cudaMemsetAsync(workspace, 0, kStatusBytes, s) != cudaSuccess) return DASH_ERR_CUDA;
@@ -143,7 +145,9 @@ dash_status_t dash_diff_bwd(const void *q, const void *k, const void *v, const v
   p.wait_ns = g_wait_ns.load();
   p.scale = scale > 0.f ? scale : 1.0f / std::sqrt((float)d);
   p.scale_log2 = p.scale * kLog2e;
-  return launch_diff_bwd(d, tq, tk, tv, tdo, p, s) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+  const cudaError_t e =
+      launch_diff_bwd(d, tq, tk, tv, tdo, p, s);
+  return e == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -23,16 +23,20 @@ struct DiffFwdParams {
   float scale_log2;       // softmax scale * log2(e)
 };
 
-// Row vectors of the backward, per tile of a (batch, head pair) kRowVecs arrays of 128 floats,
-// each negated for the fused multiply-adds that take them:
+// Row vectors of the backward, per half tile (64 rows) of a (batch, head pair) kRowVecs arrays
+// of 64 floats, each negated for the fused multiply-adds that take them:
 //   -LSE1 log2e, -LSE2 log2e, -D1, -D2, -lam       (Dm = dO . Om)
 // Rows past S hold -inf, -inf, 0, 0, 0, which give them no weight.
 constexpr int kRowVecs = 5;
+// Where vector 0 of row r of `tile` lies; vector k follows 64 k further on.
+__host__ __device__ __forceinline__ size_t rowv_at(size_t tile, int r) {
+  return (tile * 2 + (r >> 6)) * (kRowVecs * 64) + (r & 63);
+}
 struct DiffBwdParams {
   const __nv_bfloat16 *o, *o2, *dout;
   const float *lse;
   const void *lam;
-  float *rowv;            // [B,H,N][kRowVecs][128]
+  float *rowv;            // [B,H,N][2][kRowVecs][64]
   float *dlam_part;       // [B,H,N] (weights per head only)
   uint32_t *status;
   __nv_bfloat16 *dq, *dk, *dv;
@@ -53,6 +57,34 @@ cudaError_t launch_diff_bwd(int d, const CUtensorMap &tq, const CUtensorMap &tk,
 __device__ __forceinline__ float lam_at(const void *lam, int f32, size_t at) {
   return f32 ? static_cast<const float *>(lam)[at]
              : __bfloat162float(static_cast<const __nv_bfloat16 *>(lam)[at]);
+}
+
+// mbar_wait_warp without a read of the global timer on the way of a wait that is short: the
+// read takes longer than most of these waits last.  The limit runs from the first look at the
+// timer, after 256 tries.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, const Abort &ab) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  uint64_t t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if ((it & 15u) == 0) {
+      int stop = 0;
+      if (lane_id() == 0) {
+        if (ab.set()) {
+          stop = 1;
+        } else if ((it & 255u) == 0) {
+          if (t0 == 0) t0 = globaltimer();
+          if (ab.poll_global()) {
+            stop = 1;
+          } else if (globaltimer() - t0 > ab.limit_ns) {
+            ab.raise(kErrMbarTimeout);
+            stop = 1;
+          }
+        }
+      }
+      if (__shfl_sync(0xffffffffu, stop, 0)) return false;
+    }
+  }
 }
 
 // tcgen05.wait::ld that the loaded registers depend on, so that no use moves above it.
@@ -84,24 +116,35 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-// 16 lanes x 32 columns as matrix fragments: thread t holds of 8-column group j, in r[4j..4j+3],
-// columns 8j + 2 (t % 4) and the next one of lanes t / 4 and t / 4 + 8.  Four lanes' worth of rows
-// and eight columns a thread (two such loads cover the warp's 32 lanes), so that what goes by
-// column is read once for four rows.
-__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
+// 16 lanes x 16 columns as matrix fragments: thread t holds of 8-column group g, in r[4g..4g+3],
+// columns 8g + 2 (t % 4) and the next one of lanes t / 4 and t / 4 + 8.  Four rows and four
+// columns a thread over the warp's 32 lanes (two such loads), so that what goes by column is
+// read once for four rows.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
+        "=r"(r[7])
       : "r"(taddr));
 }
-// The fragments' pairs rounded to bf16: 16 lanes x 16 columns of two values each; v[2j] the
-// pair of group j of lane t / 4, v[2j+1] of lane t / 4 + 8.
-__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&v)[8]) {
+// The fragments' pairs rounded to bf16: 16 lanes x 8 columns of two values each; v[2g] the
+// pair of group g of lane t / 4, v[2g+1] of lane t / 4 + 8.
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&v)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
+               "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7])
+               :
+               : "memory");
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
       : "memory");
 }
@@ -159,6 +202,39 @@ __device__ __forceinline__ uint32_t pack_bf16(f2 v) {
   float a, b;
   f2_to(v, a, b);
   return pack_bf16(a, b);
+}
+
+// tcgen05.mma and commit for a converged warp whose lane with `lead` set issues (elect_one(),
+// asked once: electing anew for every instruction costs a third of the issue rate; measured
+// 12.6 against 21 cycles an instruction, 18 against 32 beside busy warps).
+__device__ __forceinline__ void mma_ss_l(uint32_t lead, uint32_t d_tmem, uint64_t adesc,
+                                         uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\t"
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_l(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem,
+                                         uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\t"
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_l(uint32_t lead, uint64_t *bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::
+          "r"(smem_u32(bar)),
+      "r"(lead)
+      : "memory");
 }
 
 // Byte offset of element column `col` (a multiple of 16) of row 0 in a [128 x 2d] operand tile

@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(256) diff_rows_kernel(const DiffBwdParams p) {
     v[4] = -lam;
   }
 #pragma unroll
-  for (int k = 0; k < kRowVecs; ++k) p.rowv[((size_t)tile * kRowVecs + k) * kTile + r] = v[k];
+  for (int k = 0; k < kRowVecs; ++k) p.rowv[rowv_at(tile, r) + k * 64] = v[k];
 }
 
 // -------------------------------------------------------------------- dQ
@@ -177,10 +177,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int nk = 0, nv = 0;  // blocks brought in
     mbar_arrive_expect_tx(q_full, 2 * L::kTileBytes);
-    for (int bx = 0; bx < L::kBoxes; ++bx) {
-      tma_load_4d(smem + L::offQ + bx * kBoxBytes, &tm_q, q_full, bx * kBoxCols, h, i * kTile, b);
-      tma_load_4d(smem + L::offDO + bx * kBoxBytes, &tm_do, q_full, bx * kBoxCols, h, i * kTile,
-                  b);
+    for (int bx = 0; bx < 2 * L::kBoxes; ++bx) {  // boxes of Q and dO are half tiles
+      const int at = bx * (kBoxBytes / 2), col = (bx >> 1) * kBoxCols;
+      const int row = i * kTile + (bx & 1) * (kTile / 2);
+      tma_load_4d(smem + L::offQ + at, &tm_q, q_full, col, h, row, b);
+      tma_load_4d(smem + L::offDO + at, &tm_do, q_full, col, h, row, b);
     }
     for (int j = 0; j < nkv; ++j) {
       const int sk = j % L::kK, sv = j % L::kV;
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // moves it over, which bounds short products).
     constexpr uint32_t kIdescIn = make_idesc_bf16(128, 128, false, false);
     constexpr uint32_t kIdescQ = make_idesc_bf16(128, d, false, true);
-    const uint32_t sbase = smem_u32(smem);
+    const uint32_t sbase = smem_u32(smem), lead = elect_one();
     const uint32_t loQ = desc_lo(sbase + L::offQ, 16), loDO = desc_lo(sbase + L::offDO, 16);
     auto k_at = [&](int j) { return sbase + L::offK + (j % L::kK) * L::kTileBytes; };
     auto issue_s = [&](int j, int m) {
@@ -225,23 +226,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int k = 0; k < d / 16; ++k) {
         const uint32_t off = col_bytes(m * d + 16 * k) >> 4;
-        mma_ss_e(tmem + m * 128, desc_of(loQ + off), desc_of(loK + off), kIdescIn, k > 0);
+        mma_ss_l(lead, tmem + m * 128, desc_of(loQ + off), desc_of(loK + off), kIdescIn, k > 0);
       }
-      mma_commit_e(&s_full[m]);
+      mma_commit_l(lead, &s_full[m]);
     };
     auto issue_dp = [&](int j) {
       const uint32_t loV = desc_lo(sbase + L::offV + (j % L::kV) * L::kTileBytes, 16);
 #pragma unroll
       for (int k = 0; k < DV / 16; ++k) {
         const uint32_t off = col_bytes(16 * k) >> 4;
-        mma_ss_e(tmem + L::tP, desc_of(loDO + off), desc_of(loV + off), kIdescIn, k > 0);
+        mma_ss_l(lead, tmem + L::tP, desc_of(loDO + off), desc_of(loV + off), kIdescIn, k > 0);
       }
-      mma_commit_e(dp_full);
-      mma_commit_e(&v_empty[j % L::kV]);
+      mma_commit_l(lead, dp_full);
+      mma_commit_l(lead, &v_empty[j % L::kV]);
     };
-    auto k_there = [&](int j) { return mbar_wait_warp(&k_full[j % L::kK], (j / L::kK) & 1, ab); };
-    auto v_there = [&](int j) { return mbar_wait_warp(&v_full[j % L::kV], (j / L::kV) & 1, ab); };
-    bool ok = mbar_wait_warp(q_full, 0, ab) && k_there(0) && v_there(0);
+    auto k_there = [&](int j) { return wait_warp(&k_full[j % L::kK], (j / L::kK) & 1, ab); };
+    auto v_there = [&](int j) { return wait_warp(&v_full[j % L::kV], (j / L::kV) & 1, ab); };
+    bool ok = wait_warp(q_full, 0, ab) && k_there(0) && v_there(0);
     if (ok) {
       tc_fence_after();
       issue_s(0, 0);
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int j = 0; ok && j < nkv; ++j) {
       const bool more = j + 1 < nkv;
-      if (!mbar_wait_warp(dp_free, j & 1, ab) || (more && !v_there(j + 1))) {
+      if (!wait_warp(dp_free, j & 1, ab) || (more && !v_there(j + 1))) {
         ok = false;
         break;
       }
@@ -259,15 +260,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t loK = desc_lo(k_at(j), kBoxBytes);
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        if (ok && !mbar_wait_warp(&ds_full[m], j & 1, ab)) ok = false;
+        if (ok && !wait_warp(&ds_full[m], j & 1, ab)) ok = false;
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)
-          mma_ts_e(tmem + L::tAcc + m * 64, tmem + m * 128 + 32 * (k >> 1) + 8 * (k & 1),
+          mma_ts_l(lead, tmem + L::tAcc + m * 64, tmem + m * 128 + 32 * (k >> 1) + 8 * (k & 1),
                    desc_of(loK + ((col_bytes(m * d) + k * 2048) >> 4)), kIdescQ,
                    (j > 0 || k > 0) ? 1u : 0u);
-        if (m == 1) mma_commit_e(&k_empty[j % L::kK]);
+        if (m == 1) mma_commit_l(lead, &k_empty[j % L::kK]);
         if (more) {
           if (m == 0 && !k_there(j + 1)) {
             ok = false;
@@ -277,8 +278,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (ok) mma_commit_e(acc_full);
-    mma_commit_e(drain);
+    if (ok) mma_commit_l(lead, acc_full);
+    mma_commit_l(lead, drain);
     mbar_wait_drain(drain, 0, 100000000ull);
   } else if (warp < kWarps) {
     // ------------------------------------------------------------------ dS
@@ -287,14 +288,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     const int row = i * kTile + r;
     const bool row_ok = row < p.S;
-    float *rowv = p.rowv + (((size_t)b * p.H + h) * p.N + i) * (kRowVecs * kTile) + r;
+    float *rowv = p.rowv + rowv_at(((size_t)b * p.H + h) * p.N + i, r);
     const f2 c2 = f2_of(p.scale_log2, p.scale_log2);
     float nl[2], nD[2];
     f2 along[2];  // sum_j Pm dP of this row, even and odd keys
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-      nl[m] = rowv[m * kTile];
-      nD[m] = rowv[(2 + m) * kTile];
+      nl[m] = rowv[m * 64];
+      nD[m] = rowv[(2 + m) * 64];
       along[m] = f2_of(0.f, 0.f);
     }
     const uint32_t t0 = tmem + lane_off + 32 * wg;
@@ -307,8 +308,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         uint32_t s[32];
-        if (ok) ok = mbar_wait_warp(&s_full[m], j & 1, ab) &&
-                     (m == 1 || mbar_wait_warp(dp_full, j & 1, ab));
+        if (ok) ok = wait_warp(&s_full[m], j & 1, ab) &&
+                     (m == 1 || wait_warp(dp_full, j & 1, ab));
         if (!ok) break;
         tc_fence_after();
         tmem_ld32(t0 + m * 128, s);
@@ -342,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     // ------------------------------------------------------------------ epilogue
-    ok = ok && mbar_wait_warp(acc_full, 0, ab);  // every product has run: K's memory is free
+    ok = ok && wait_warp(acc_full, 0, ab);  // every product has run: K's memory is free
     if (!ok) mbar_wait_drain(drain, 0, 100000000ull);
     tc_fence_after();
 #pragma unroll
@@ -355,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (wg < 2) {
       const float *al = s_along + wg * 4 * kTile + r;
       const float D = (al[0] + al[kTile]) + (al[2 * kTile] + al[3 * kTile]);
-      if (row_ok) rowv[(2 + wg) * kTile] = -D;
+      if (row_ok) rowv[(2 + wg) * 64] = -D;
       if (wg == 1) {
         if (p.lam_token) {
           const size_t at = ((size_t)b * p.S + row) * p.H + h;
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) {
       // half of dQm's columns; dS2 was formed without its weight, a factor of the row
       const int m = wg >> 1, half = (wg & 1) * (d / 2);
-      const float by = m ? rowv[4 * kTile] * p.scale : p.scale;
+      const float by = m ? rowv[4 * 64] * p.scale : p.scale;
       __nv_bfloat16 *out = p.dq + (((size_t)b * p.S + row) * 2 * p.H + 2 * h + m) * d + half;
       uint32_t v[d / 2];
       if constexpr (d == 64)
@@ -422,33 +423,38 @@ __global__ void __launch_bounds__(256) diff_dlam_kernel(const DiffBwdParams p) {
 }
 
 // -------------------------------------------------------------------- dK, dV
-// CTA: a 128-key block of one KV head, over the query heads of its group and their 128-row
-// tiles in ascending order, everything transposed (thread = key row, so that the bf16 operands
-// P^T and dS^T go back to TMEM where their rows are; 32 queries a warpgroup).  dV, dK1 and dK2
-// leave two blocks of 128 columns, X and Y, which the three inputs of a tile share in turn:
-//   elementwise   A: S1 (X) -> P1 | B: S2 (Y) -> P (over S2) | C: dP (X) -> dS1, dS2 | A ...
-//   tensor core   dK of the last tile, S2 | dP (X, once S1 is in registers) | dV, next S1 (X)
-// P over the first 16 of every 32 columns of Y, dS1 the other 16; dS2 takes P's place once the
-// product for dV has read it.
-//   dV [0,dv)  dK1 [128,128+d) dK2 [192,192+d)  X [256,384) Y [384,512)
+// CTA: a 128-key block of one KV head, over the query heads of its group and their tiles in
+// ascending order, everything transposed (TMEM lane = key row, so that the bf16 operands P^T
+// and dS^T go back to TMEM where their rows are), in steps of 64 queries, 16 a warpgroup:
+//   A   S1, dP -> P1 and dP kept in registers, dS1 over S1
+//   B   S2 -> w = -lam P2, P = P1 + w and dS2 over S2
+// The accumulators (dV [0,dv), dK1 [128,+d), dK2 [192,+d)) leave four slots of 64 columns from
+// 256 on, which the steps pass around so that a step's inputs are formed beside the elementwise
+// work of the one before:
+//   dP(t)   slot 1, free again once A(t) has read it
+//   S1(t)   slots 0, 3, 2, 0, ...: that of S2(t-2), read for the last time by dV, dK2 of t-2
+//   S2(t)   slots 2, 0, 3, 2, ...: that of S1(t-1), read for the last time by dK1 of t-1
+// Q, dO and the row vectors come in by half tiles, a step each, in a ring of four.
+constexpr int kStep = 64;
+
 template <int d>
 struct DkvL {
   static constexpr int DV = 2 * d;
-  static constexpr int kStages = 2;
+  static constexpr int kStages = 4;  // half tiles
   static constexpr int kTileBytes = DV * kTile * 2;
+  static constexpr int kHalfBytes = kTileBytes / 2, kHalfBox = kBoxBytes / 2;
   static constexpr int kBoxes = DV / kBoxCols;
-  static constexpr int kRowBytes = kRowVecs * kTile * 4;
+  static constexpr int kRowBytes = kRowVecs * kStep * 4;
   static constexpr int offK = 0, offV = kTileBytes;
   static constexpr int offStage = 2 * kTileBytes;  // per stage Q, dO
-  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kStageBytes = 2 * kHalfBytes;
   static constexpr int offRow = offStage + kStages * kStageBytes;  // per stage row vectors
   static constexpr int offBar = offRow + kStages * kRowBytes;
-  // kv_full, q_full[], q_empty[], s1_full, s2_full, dp_full, s1_free, dp_free, p_full, dv_done,
-  // ds_full, acc_full, drain
-  static constexpr int kNumBars = 1 + 2 * kStages + 10;
+  // kv_full, q_full[], q_empty[], a_full, dp_free, ds1_full, s2_full, out_full, acc_full, drain
+  static constexpr int kNumBars = 1 + 2 * kStages + 7;
   static constexpr int offMisc = offBar + kNumBars * 8;
   static constexpr int kBytes = offMisc + 16;
-  static constexpr uint32_t tV = 0, tK = 128, tX = 256, tY = 384, kTmemCols = 512;
+  static constexpr uint32_t tV = 0, tK = 128, tSlots = 256, kTmemCols = 512;
   static_assert(kBytes <= 232448, "shared memory budget");
 };
 
@@ -467,10 +473,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   uint64_t *kv_full = reinterpret_cast<uint64_t *>(smem + L::offBar);
   uint64_t *q_full = kv_full + 1, *q_empty = q_full + L::kStages;
-  uint64_t *s1_full = q_empty + L::kStages, *s2_full = s1_full + 1, *dp_full = s1_full + 2;
-  uint64_t *s1_free = s1_full + 3, *dp_free = s1_full + 4, *p_full = s1_full + 5;
-  uint64_t *dv_done = s1_full + 6, *ds_full = s1_full + 7, *acc_full = s1_full + 8;
-  uint64_t *drain = s1_full + 9;
+  uint64_t *a_full = q_empty + L::kStages, *dp_free = a_full + 1, *ds1_full = a_full + 2;
+  uint64_t *s2_full = a_full + 3, *out_full = a_full + 4, *acc_full = a_full + 5;
+  uint64_t *drain = a_full + 6;
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + L::offMisc);
   int *s_abort = reinterpret_cast<int *>(smem + L::offMisc + 4);
   const Abort ab{s_abort, p.status, p.wait_ns};
@@ -481,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int bh = blockIdx.x % heads;
   const int hkv = bh % p.Hkv, b = bh / p.Hkv;
   const int i0 = p.causal ? j : 0, tiles = p.N - i0;
-  const int stages = p.G * tiles;
+  const int steps = 2 * p.G * tiles;
 
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
@@ -489,14 +494,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&q_full[s], 1);
       mbar_init(&q_empty[s], kWarps + 1);  // the products' commit, the readers of row vectors
     }
-    mbar_init(s1_full, 1);
-    mbar_init(s2_full, 1);
-    mbar_init(dp_full, 1);
-    mbar_init(s1_free, kWarps);
+    mbar_init(a_full, 1);
     mbar_init(dp_free, kWarps);
-    mbar_init(p_full, kWarps);
-    mbar_init(dv_done, 1);
-    mbar_init(ds_full, kWarps);
+    mbar_init(ds1_full, kWarps);
+    mbar_init(s2_full, 1);
+    mbar_init(out_full, kWarps);
     mbar_init(acc_full, 1);
     mbar_init(drain, 1);
     *s_abort = 0;
@@ -529,23 +531,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_load_4d(smem + L::offV + bx * kBoxBytes, &tm_v, kv_full, bx * kBoxCols, hkv, j * kTile,
                   b);
     }
-    for (int n = 0; n < stages; ++n) {
+    for (int n = 0; n < steps; ++n) {
       const int s = n % L::kStages;
       const uint32_t ph = (n / L::kStages) & 1;
       if (!mbar_wait(&q_empty[s], ph ^ 1, ab)) {
         ok = false;
         break;
       }
-      const int h = hkv * p.G + n / tiles, i = i0 + n % tiles;
+      const int h = hkv * p.G + (n >> 1) / tiles, i = i0 + (n >> 1) % tiles, u = n & 1;
       mbar_arrive_expect_tx(&q_full[s], L::kStageBytes + L::kRowBytes);
       uint8_t *sq = smem + L::offStage + s * L::kStageBytes;
       for (int bx = 0; bx < L::kBoxes; ++bx) {
-        tma_load_4d(sq + bx * kBoxBytes, &tm_q, &q_full[s], bx * kBoxCols, h, i * kTile, b);
-        tma_load_4d(sq + L::kTileBytes + bx * kBoxBytes, &tm_do, &q_full[s], bx * kBoxCols, h,
-                    i * kTile, b);
+        tma_load_4d(sq + bx * L::kHalfBox, &tm_q, &q_full[s], bx * kBoxCols, h,
+                    i * kTile + u * kStep, b);
+        tma_load_4d(sq + L::kHalfBytes + bx * L::kHalfBox, &tm_do, &q_full[s], bx * kBoxCols, h,
+                    i * kTile + u * kStep, b);
       }
       bulk_load(smem + L::offRow + s * L::kRowBytes,
-                p.rowv + (((size_t)b * p.H + h) * p.N + i) * (kRowVecs * kTile), L::kRowBytes,
+                p.rowv + rowv_at(((size_t)b * p.H + h) * p.N + i, u * kStep), L::kRowBytes,
                 &q_full[s]);
       last[s] = (int)ph;
     }
@@ -557,84 +560,100 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kWarps + 1) {
     // ------------------------------------------------------------------ MMA issuer
     // (a converged warp, one elected lane issues)
-    constexpr uint32_t kIdescIn = make_idesc_bf16(128, 128, false, false);
+    constexpr uint32_t kIdescIn = make_idesc_bf16(128, kStep, false, false);
     constexpr uint32_t kIdescV = make_idesc_bf16(128, DV, false, true);
     constexpr uint32_t kIdescK = make_idesc_bf16(128, d, false, true);
-    const uint32_t sbase = smem_u32(smem);
+    const uint32_t sbase = smem_u32(smem), lead = elect_one();
     const uint32_t loK = desc_lo(sbase + L::offK, 16), loV = desc_lo(sbase + L::offV, 16);
-    auto stage_at = [&](int n) {
+    auto q_at = [&](int n) {  // Q of step n; dO lies kHalfBytes on
       return sbase + L::offStage + (n % L::kStages) * L::kStageBytes;
     };
-    auto issue_s = [&](int n, int m) {  // S1^T -> X, S2^T -> Y
-      const uint32_t loQ = desc_lo(stage_at(n), 16);
-#pragma unroll
-      for (int k = 0; k < d / 16; ++k) {
-        const uint32_t off = col_bytes(m * d + 16 * k) >> 4;
-        mma_ss_e(tmem + (m ? L::tY : L::tX), desc_of(loK + off), desc_of(loQ + off), kIdescIn,
-                 k > 0);
-      }
-      mma_commit_e(m ? s2_full : s1_full);
+    auto half_bytes = [](int col) {  // col_bytes in a half tile's boxes
+      return (uint32_t)(col >> 6) * L::kHalfBox + (uint32_t)(col & 63) * 2;
     };
     auto q_there = [&](int n) {
-      return mbar_wait_warp(&q_full[n % L::kStages], (n / L::kStages) & 1, ab);
+      return wait_warp(&q_full[n % L::kStages], (n / L::kStages) & 1, ab);
     };
-    bool ok = mbar_wait_warp(kv_full, 0, ab) && q_there(0);
+    auto issue_s = [&](int n, int m, uint32_t to) {  // Sm^T -> slot `to`
+      const uint32_t loQ = desc_lo(q_at(n), 16);
+#pragma unroll
+      for (int k = 0; k < d / 16; ++k) {
+        const int col = m * d + 16 * k;
+        mma_ss_l(lead, to, desc_of(loK + (col_bytes(col) >> 4)),
+                 desc_of(loQ + (half_bytes(col) >> 4)), kIdescIn, k > 0);
+      }
+    };
+    auto issue_dp = [&](int n) {  // dP^T -> slot 1
+      const uint32_t loO = desc_lo(q_at(n) + L::kHalfBytes, 16);
+#pragma unroll
+      for (int k = 0; k < DV / 16; ++k)
+        mma_ss_l(lead, tmem + L::tSlots + 64, desc_of(loV + (col_bytes(16 * k) >> 4)),
+                 desc_of(loO + (half_bytes(16 * k) >> 4)), kIdescIn, k > 0);
+      mma_commit_l(lead, a_full);
+    };
+    // slots of S1 and S2 of this step, and of the next step's S1 (its S2 takes S1's of this)
+    uint32_t slot1 = tmem + L::tSlots, slot2 = slot1 + 128, spare = slot1 + 192;
+    bool ok = wait_warp(kv_full, 0, ab) && q_there(0);
     if (ok) {
       tc_fence_after();
-      issue_s(0, 0);
-      issue_s(0, 1);
+      issue_s(0, 0, slot1);
+      issue_dp(0);
+      issue_s(0, 1, slot2);
+      mma_commit_l(lead, s2_full);
     }
-    for (int n = 0; ok && n < stages; ++n) {
-      const bool more = n + 1 < stages;
+    for (int n = 0; ok && n < steps; ++n) {
+      const bool more = n + 1 < steps;
       const uint32_t ph = n & 1, first = n > 0 ? 1u : 0u;
-      const uint32_t aQ = stage_at(n), aO = aQ + L::kTileBytes;
-      const uint32_t loO = desc_lo(aO, 16), loOmn = desc_lo(aO, kBoxBytes);
-      const uint32_t loQmn = desc_lo(aQ, kBoxBytes);
-      if (!mbar_wait_warp(s1_free, ph, ab)) {
+      const uint32_t loQ = desc_lo(q_at(n), L::kHalfBox);
+      const uint32_t loO = desc_lo(q_at(n) + L::kHalfBytes, L::kHalfBox);
+      if (more) {
+        if (!q_there(n + 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        issue_s(n + 1, 0, spare);
+        if (!wait_warp(dp_free, ph, ab)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        issue_dp(n + 1);
+      }
+      if (!wait_warp(ds1_full, ph, ab)) {
         ok = false;
         break;
       }
       tc_fence_after();
 #pragma unroll
-      for (int k = 0; k < DV / 16; ++k) {
-        const uint32_t off = col_bytes(16 * k) >> 4;
-        mma_ss_e(tmem + L::tX, desc_of(loV + off), desc_of(loO + off), kIdescIn, k > 0);
+      for (int k = 0; k < kStep / 16; ++k)
+        mma_ts_l(lead, tmem + L::tK, slot1 + 16 * k, desc_of(loQ + ((k * 2048) >> 4)), kIdescK,
+                 k > 0 ? 1u : first);
+      if (more) {
+        issue_s(n + 1, 1, slot1);
+        mma_commit_l(lead, s2_full);
       }
-      mma_commit_e(dp_full);
-      if (!mbar_wait_warp(p_full, ph, ab)) {
+      if (!wait_warp(out_full, ph, ab)) {
         ok = false;
         break;
       }
       tc_fence_after();
 #pragma unroll
-      for (int k = 0; k < kTile / 16; ++k)
-        mma_ts_e(tmem + L::tV, tmem + L::tY + 32 * (k >> 1) + 8 * (k & 1),
-                 desc_of(loOmn + ((k * 2048) >> 4)), kIdescV, k > 0 ? 1u : first);
-      mma_commit_e(dv_done);
-      if (!mbar_wait_warp(dp_free, ph, ab) || (more && !q_there(n + 1))) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      if (more) issue_s(n + 1, 0);
-      if (!mbar_wait_warp(ds_full, ph, ab)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
+      for (int k = 0; k < kStep / 16; ++k)
+        mma_ts_l(lead, tmem + L::tV, slot2 + 16 * k, desc_of(loO + ((k * 2048) >> 4)), kIdescV,
+                 k > 0 ? 1u : first);
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          mma_ts_e(tmem + L::tK + 64 * m,
-                   tmem + L::tY + (m ? 0 : 16) + 32 * (k >> 1) + 8 * (k & 1),
-                   desc_of(loQmn + ((col_bytes(m * d) + k * 2048) >> 4)), kIdescK,
-                   k > 0 ? 1u : first);
-      mma_commit_e(&q_empty[n % L::kStages]);
-      if (more) issue_s(n + 1, 1);
+      for (int k = 0; k < kStep / 16; ++k)
+        mma_ts_l(lead, tmem + L::tK + 64, slot2 + 8 + 16 * k,
+                 desc_of(loQ + ((half_bytes(d) + k * 2048) >> 4)), kIdescK, k > 0 ? 1u : first);
+      mma_commit_l(lead, &q_empty[n % L::kStages]);
+      const uint32_t was2 = slot2;
+      slot2 = slot1;
+      slot1 = spare;
+      spare = was2;
     }
-    if (ok) mma_commit_e(acc_full);
-    mma_commit_e(drain);
+    if (ok) mma_commit_l(lead, acc_full);
+    mma_commit_l(lead, drain);
     mbar_wait_drain(drain, 0, 100000000ull);
   } else if (warp < kWarps) {
     // ------------------------------------------------------------------ P, dS (transposed)
@@ -644,134 +663,128 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int wg = warp >> 2;
     const int quad = warp & 3;
     const int r = quad * 32 + lane;  // key row of the epilogue = TMEM lane
+    const int q0 = 16 * wg;          // this warpgroup's queries within a step
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    const uint32_t tX = tmem + lane_off + L::tX + 32 * wg, tY = tmem + lane_off + L::tY + 32 * wg;
+    const uint32_t t0 = tmem + lane_off + L::tSlots + q0;
     constexpr uint32_t kLanes16 = 16u << 16;
     const int key = j * kTile + r;
     const f2 c2 = f2_of(p.scale_log2, p.scale_log2);
-    // key of fragment row 0 less the query of its column 0, within the diagonal tile
-    const int ahead = quad * 32 + lane / 4 - (32 * wg + 2 * (lane & 3));
-    bool ok = true;
-    for (int n = 0; n < stages; ++n) {
-      const uint32_t ph = n & 1;
-      const int s = n % L::kStages;
-      const float *rv = reinterpret_cast<const float *>(smem + L::offRow + s * L::kRowBytes) +
-                        32 * wg + 2 * (lane & 3);
-      auto vec = [&](int k, int g) {  // row vector k of this thread's columns of group g
-        return *reinterpret_cast<const f2 *>(rv + k * kTile + 8 * g);
-      };
-      // on the diagonal tile, queries before the key see nothing of it
-      const bool cut = p.causal && n % tiles == 0;
-      auto hide = [&](uint32_t (&x)[16], int half, uint32_t with) {
+    const float *rowv = reinterpret_cast<const float *>(smem + L::offRow) + q0 + 2 * (lane & 3);
+    auto vec = [&](int n, int k, int g) {  // vector k of this thread's columns of group g, step n
+      return *reinterpret_cast<const f2 *>(rowv + (n % L::kStages) * (L::kRowBytes / 4) +
+                                           k * kStep + 8 * g);
+    };
+    // On the diagonal tile, queries before the key see nothing of it.  Key of fragment row 0
+    // less the query of its column 0, of the tile's first step:
+    const int ahead = quad * 32 + lane / 4 - (q0 + 2 * (lane & 3));
+    auto hide = [&](uint32_t (&x)[8], int n, int half, uint32_t with) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e)  // key - query of the element
-          if (ahead + 16 * half + 8 * ((e >> 1) & 1) - 8 * (e >> 2) - (e & 1) > 0) x[e] = with;
-      };
-      f2 P1[2][8], w[2][8];  // P1, -lam P2; [half of the lanes][2 * group + row]
+      for (int e = 0; e < 8; ++e)  // key - query of the element
+        if (ahead - kStep * (n & 1) + 16 * half + 8 * ((e >> 1) & 1) - 8 * (e >> 2) - (e & 1) > 0)
+          x[e] = with;
+    };
+    auto diagonal = [&](int n) { return p.causal && (n >> 1) % tiles == 0; };
+    uint32_t slot1 = t0, slot2 = t0 + 128, spare = t0 + 192;
+    bool ok = true;
+    for (int n = 0; n < steps; ++n) {
+      const uint32_t ph = n & 1;
+      const bool cut = diagonal(n);
+      // [half of the lanes][2 * group + row]
+      f2 P1[2][4], dP[2][4];
       // A
-      if (!mbar_wait_warp(s1_full, ph, ab)) {
+      if (!wait_warp(&q_full[n % L::kStages], (n / L::kStages) & 1, ab) ||
+          !wait_warp(a_full, ph, ab)) {
         ok = false;
         break;
       }
       tc_fence_after();
       {
-        uint32_t x[2][16];
-        tmem_ld_frag(tX, x[0]);
-        tmem_ld_frag(tX + kLanes16, x[1]);
-        tmem_ld_wait_for(x[0]);
-        tmem_ld_wait_for(x[1]);
+        uint32_t x[2][8], y[2][8];
+        tmem_ld_frag(slot1, x[0]);
+        tmem_ld_frag(slot1 + kLanes16, x[1]);
+        tmem_ld_frag(t0 + 64, y[0]);
+        tmem_ld_frag(t0 + 64 + kLanes16, y[1]);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          tmem_ld_wait_for(x[half]);
+          tmem_ld_wait_for(y[half]);
+        }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(s1_free);
+        if (lane == 0) mbar_arrive(dp_free);
         if (cut) {
-          hide(x[0], 0, __float_as_uint(-INFINITY));
-          hide(x[1], 1, __float_as_uint(-INFINITY));
-        }
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const f2 nl = vec(0, g);
+          for (int half = 0; half < 2; ++half) {
+            hide(x[half], n, half, __float_as_uint(-INFINITY));
+            hide(y[half], n, half, 0u);
+          }
+        }
+        uint32_t pk[2][4];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const f2 nl = vec(n, 0, g), nD = vec(n, 2, g);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int half = e >> 1, at = 2 * g + (e & 1);
-            P1[half][at] =
-                ex2_2(fma2(f2_of(x[half][2 * at], x[half][2 * at + 1]), c2, nl));
+            P1[half][at] = ex2_2(fma2(f2_of(x[half][2 * at], x[half][2 * at + 1]), c2, nl));
+            dP[half][at] = f2_of(y[half][2 * at], y[half][2 * at + 1]);
+            pk[half][at] = pack_bf16(mul2(P1[half][at], add2(dP[half][at], nD)));
           }
         }
+        tmem_st_frag(slot1, pk[0]);
+        tmem_st_frag(slot1 + kLanes16, pk[1]);
       }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ds1_full);
       // B
-      if (!mbar_wait_warp(s2_full, ph, ab)) {
+      if (!wait_warp(s2_full, ph, ab)) {
         ok = false;
         break;
       }
       tc_fence_after();
       {
-        f2 nl[4], nlam[4];
+        uint32_t x[2][8], pP[2][4], pk[2][4];
+        tmem_ld_frag(slot2, x[0]);
+        tmem_ld_frag(slot2 + kLanes16, x[1]);
+        tmem_ld_wait_for(x[0]);
+        tmem_ld_wait_for(x[1]);
+        if (cut) {
+          hide(x[0], n, 0, __float_as_uint(-INFINITY));
+          hide(x[1], n, 1, __float_as_uint(-INFINITY));
+        }
 #pragma unroll
-        for (int g = 0; g < 4; ++g) nl[g] = vec(1, g), nlam[g] = vec(4, g);
+        for (int g = 0; g < 2; ++g) {
+          const f2 nl = vec(n, 1, g), nD = vec(n, 3, g), nlam = vec(n, 4, g);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int half = e >> 1, at = 2 * g + (e & 1);
+            const f2 w =
+                mul2(ex2_2(fma2(f2_of(x[half][2 * at], x[half][2 * at + 1]), c2, nl)), nlam);
+            pP[half][at] = pack_bf16(add2(P1[half][at], w));
+            pk[half][at] = pack_bf16(mul2(w, add2(dP[half][at], nD)));
+          }
+        }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          uint32_t x[16], pk[8];
-          tmem_ld_frag(tY + half * kLanes16, x);
-          tmem_ld_wait_for(x);
-          if (cut) hide(x, half, __float_as_uint(-INFINITY));
-#pragma unroll
-          for (int at = 0; at < 8; ++at) {
-            w[half][at] =
-                mul2(ex2_2(fma2(f2_of(x[2 * at], x[2 * at + 1]), c2, nl[at >> 1])), nlam[at >> 1]);
-            pk[at] = pack_bf16(add2(P1[half][at], w[half][at]));
-          }
-          tmem_st_frag(tY + half * kLanes16, pk);
+          tmem_st_frag(slot2 + half * kLanes16, pP[half]);
+          tmem_st_frag(slot2 + 8 + half * kLanes16, pk[half]);
         }
       }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_full);
-      // C
-      if (!mbar_wait_warp(dp_full, ph, ab)) {
-        ok = false;
-        break;
+      if (lane == 0) {
+        mbar_arrive(out_full);
+        mbar_arrive(&q_empty[n % L::kStages]);
       }
-      tc_fence_after();
-      uint32_t pk2[2][8];
-      {
-        f2 nD1[4], nD2[4];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) nD1[g] = vec(2, g), nD2[g] = vec(3, g);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t x[16], pk[8];
-          tmem_ld_frag(tX + half * kLanes16, x);
-          tmem_ld_wait_for(x);
-          if (half) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(dp_free);
-          }
-          if (cut) hide(x, half, 0u);
-#pragma unroll
-          for (int at = 0; at < 8; ++at) {
-            const f2 dP = f2_of(x[2 * at], x[2 * at + 1]);
-            pk[at] = pack_bf16(mul2(P1[half][at], add2(dP, nD1[at >> 1])));
-            pk2[half][at] = pack_bf16(mul2(w[half][at], add2(dP, nD2[at >> 1])));
-          }
-          tmem_st_frag(tY + 16 + half * kLanes16, pk);
-        }
-      }
-      if (lane == 0) mbar_arrive(&q_empty[s]);
-      if (!mbar_wait_warp(dv_done, ph, ab)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      tmem_st_frag(tY, pk2[0]);
-      tmem_st_frag(tY + kLanes16, pk2[1]);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(ds_full);
+      const uint32_t was2 = slot2;
+      slot2 = slot1;
+      slot1 = spare;
+      spare = was2;
     }
-    if (ok && mbar_wait_warp(acc_full, 0, ab)) {
+    if (ok && wait_warp(acc_full, 0, ab)) {
       tc_fence_after();
       // one of dK1, dK2 and the halves of dV
       const size_t at = (size_t)b * p.S + key;

@@ -132,18 +132,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     // one elected lane issues.
     constexpr uint32_t kIdescS = make_idesc_bf16(128, 128, false, false);
     constexpr uint32_t kIdescO = make_idesc_bf16(128, DV, false, true);
-    const uint32_t sbase = smem_u32(smem);
+    const uint32_t sbase = smem_u32(smem), lead = elect_one();
     const uint32_t loQ = desc_lo(sbase + L::offQ, 16);
     auto issue_s = [&](int j, int m) {
       const uint32_t loK = desc_lo(sbase + L::offStage + (j % L::kStages) * L::kStageBytes, 16);
 #pragma unroll
       for (int k = 0; k < d / 16; ++k) {
         const uint32_t off = col_bytes(m * d + 16 * k) >> 4;
-        mma_ss_e(tmem + L::tS + m * 128, desc_of(loQ + off), desc_of(loK + off), kIdescS, k > 0);
+        mma_ss_l(lead, tmem + L::tS + m * 128, desc_of(loQ + off), desc_of(loK + off), kIdescS, k > 0);
       }
-      mma_commit_e(&s_full[m]);
+      mma_commit_l(lead, &s_full[m]);
     };
-    bool ok = mbar_wait_warp(q_full, 0, ab) && mbar_wait_warp(&kv_full[0], 0, ab);
+    bool ok = wait_warp(q_full, 0, ab) && wait_warp(&kv_full[0], 0, ab);
     if (ok) {
       tc_fence_after();
       issue_s(0, 0);
@@ -155,16 +155,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           desc_lo(sbase + L::offStage + s * L::kStageBytes + L::kTileBytes, kBoxBytes);
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        if (ok && !mbar_wait_warp(&p_full[m], j & 1, ab)) ok = false;
+        if (ok && !wait_warp(&p_full[m], j & 1, ab)) ok = false;
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          mma_ts_e(tmem + L::tO + m * DV, tmem + L::tS + m * 128 + 8 * k,
+          mma_ts_l(lead, tmem + L::tO + m * DV, tmem + L::tS + m * 128 + 8 * k,
                    desc_of(loV + ((k * 2048) >> 4)), kIdescO, (j > 0 || k > 0) ? 1u : 0u);
-        if (m == 1) mma_commit_e(&kv_empty[s]);
+        if (m == 1) mma_commit_l(lead, &kv_empty[s]);
         if (j1 < nkv) {
-          if (m == 0 && !mbar_wait_warp(&kv_full[j1 % L::kStages], (j1 / L::kStages) & 1, ab)) {
+          if (m == 0 && !wait_warp(&kv_full[j1 % L::kStages], (j1 / L::kStages) & 1, ab)) {
             ok = false;
             break;
           }
@@ -173,8 +173,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (ok) mma_commit_e(o_full);
-    mma_commit_e(drain);
+    if (ok) mma_commit_l(lead, o_full);
+    mma_commit_l(lead, drain);
     mbar_wait_drain(drain, 0, 100000000ull);
   } else if (warp < 8) {
     // ------------------------------------------------------------------ softmax of map m
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float ref = -INFINITY, l = 0.f;  // running maximum (log2 units) and sum
     bool ok = true;
     for (int j = 0; j < nkv; ++j) {
-      if (!mbar_wait_warp(&s_full[m], j & 1, ab)) {
+      if (!wait_warp(&s_full[m], j & 1, ab)) {
         ok = false;
         break;
       }
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok && row_ok)
       p.lse[((size_t)b * 2 * p.H + 2 * h + m) * p.S + row] = (ref + log2f(l)) * kLn2;
     named_bar_sync(1, 256);
-    if (ok && mbar_wait_warp(o_full, 0, ab)) {
+    if (ok && wait_warp(o_full, 0, ab)) {
       tc_fence_after();
       // this warpgroup's half of the columns of both accumulators
       const float n1 = s_sum[r], n2 = s_sum[kTile + r];

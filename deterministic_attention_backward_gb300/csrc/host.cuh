@@ -28,15 +28,17 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 }
 
 // [B, S, Hx, D] bf16 viewed as a 4-D tensor (D, Hx, S, B); box = 64 columns x 1 head x 128
-// rows x 1 batch, 128-byte swizzle: one box lands in shared memory as 128 rows of 128 bytes.
+// (or `rows`) rows x 1 batch, 128-byte swizzle: one box lands in shared memory as that many rows
+// of 128 bytes.
 // Rows of a tile past S (S not a multiple of 128) are outside the tensor and read as zeros.
-inline bool make_bshd_map(CUtensorMap *m, const void *base, int B, int S, int Hx, int D) {
+inline bool make_bshd_map(CUtensorMap *m, const void *base, int B, int S, int Hx, int D,
+                          int rows = kTile) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
   const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)Hx, (cuuint64_t)S, (cuuint64_t)B};
   const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)Hx * D * 2,
                                  (cuuint64_t)S * Hx * D * 2};
-  const cuuint32_t box[4] = {(cuuint32_t)kBoxCols, 1, (cuuint32_t)kTile, 1};
+  const cuuint32_t box[4] = {(cuuint32_t)kBoxCols, 1, (cuuint32_t)rows, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box,
              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
