@@ -589,7 +589,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < DV / 16; ++k)
         mma_ss_l(lead, tmem + L::tSlots + 64, desc_of(loV + (col_bytes(16 * k) >> 4)),
                  desc_of(loO + (half_bytes(16 * k) >> 4)), kIdescIn, k > 0);
-      mma_commit_l(lead, a_full);
     };
     // slots of S1 and S2 of this step, and of the next step's S1 (its S2 takes S1's of this)
     uint32_t slot1 = tmem + L::tSlots, slot2 = slot1 + 128, spare = slot1 + 192;
@@ -598,9 +597,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       issue_s(0, 0, slot1);
       issue_dp(0);
+      mma_commit_l(lead, a_full);
       issue_s(0, 1, slot2);
       mma_commit_l(lead, s2_full);
     }
+    // A barrier's phase n + 1 must not complete before every waiter has seen its phase n, so the
+    // commits that let the elementwise warps go on stand behind the waits for what they did
+    // before: a_full(n+1) behind ds1_full(n), s2_full(n+1) behind out_full(n).
     for (int n = 0; ok && n < steps; ++n) {
       const bool more = n + 1 < steps;
       const uint32_t ph = n & 1, first = n > 0 ? 1u : 0u;
@@ -624,19 +627,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = false;
         break;
       }
+      if (more) mma_commit_l(lead, a_full);
       tc_fence_after();
 #pragma unroll
       for (int k = 0; k < kStep / 16; ++k)
         mma_ts_l(lead, tmem + L::tK, slot1 + 16 * k, desc_of(loQ + ((k * 2048) >> 4)), kIdescK,
                  k > 0 ? 1u : first);
-      if (more) {
-        issue_s(n + 1, 1, slot1);
-        mma_commit_l(lead, s2_full);
-      }
+      if (more) issue_s(n + 1, 1, slot1);
       if (!wait_warp(out_full, ph, ab)) {
         ok = false;
         break;
       }
+      if (more) mma_commit_l(lead, s2_full);
       tc_fence_after();
 #pragma unroll
       for (int k = 0; k < kStep / 16; ++k)
