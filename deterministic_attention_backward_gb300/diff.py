@@ -16,44 +16,37 @@ from __future__ import annotations
 import torch
 
 from . import _check, _workspace, lib, status
-from ._args import disjoint, placed, shaped, tensor
+from ._args import alike, contiguous, run, tensor
+
+_BF16 = (torch.bfloat16,)
 
 
 def _dims(q, k, v, lam):
-    for t, n in ((q, "q"), (k, "k"), (v, "v")):
-        _operand(t, n, q)
-        if t.dim() != 4:
-            raise ValueError(f"{n} must be [B, S, heads, d], got {tuple(t.shape)}")
+    tensor(q, "q", _BF16)
+    if q.dim() != 4 or not isinstance(v, torch.Tensor) or v.dim() != 4:
+        raise ValueError("q and v must be [B, S, heads, d]")
     B, S, H2, d = q.shape
     Hkv = v.shape[2]
     if H2 % 2 or Hkv == 0 or (H2 // 2) % Hkv:
         raise ValueError(f"q {tuple(q.shape)} has no whole group of head pairs for each head of "
                          f"v {tuple(v.shape)}")
-    shaped(k, "k", (B, S, 2 * Hkv, d))
-    shaped(v, "v", (B, S, Hkv, 2 * d))
+    alike(k, "k", q, (B, S, 2 * Hkv, d))
+    alike(v, "v", q, (B, S, Hkv, 2 * d))
     H = H2 // 2
-    tensor(lam, "lam", dtypes=(torch.bfloat16, torch.float32))
+    tensor(lam, "lam", (torch.bfloat16, torch.float32))
     if lam.device != q.device:
         raise ValueError(f"lam is on {lam.device}, expected {q.device}")
-    if tuple(lam.shape) not in ((H,), (B, S, H)):
+    if lam.shape != (H,) and lam.shape != (B, S, H):
         raise ValueError(f"lam must be {(H,)} or {(B, S, H)}, got {tuple(lam.shape)}")
-    if not lam.is_contiguous():
-        raise ValueError("lam must be contiguous")
+    for t, n in ((q, "q"), (k, "k"), (v, "v"), (lam, "lam")):
+        contiguous(t, n)
     return B, S, H, Hkv, d
 
 
-def _operand(t, name, like, dtype=torch.bfloat16):
-    tensor(t, name, like=like, dtypes=(dtype,))
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-
-
-def _given(t, name, like, shape, dtype=torch.bfloat16):
+def _given(t, name, like, shape, dtype=None):
     """An output or a saved tensor that the caller hands in."""
-    _operand(t, name, like, dtype)
-    shaped(t, name, shape)
-    if not disjoint(t):
-        raise ValueError(f"{name} has elements that share an address")
+    alike(t, name, like, shape, dtype)
+    contiguous(t, name)
 
 
 def diff_bwd_workspace_bytes(B: int, S: int, H: int, d: int) -> int:
@@ -66,29 +59,30 @@ def diff_fwd(q, k, v, lam, causal: bool = False, scale: float | None = None, out
     """Forward: returns (O [B,S,H,2d], O2 = softmax(Q2 K2^T) V of the same shape, LSE [B,2H,S])."""
     B, S, H, Hkv, d = _dims(q, k, v, lam)
     shape = (B, S, H, 2 * d)
-    for t, n in ((out, "out"), (out2, "out2")):
-        if t is not None:
-            _given(t, n, q, shape)
+    if out is not None:
+        _given(out, "out", q, shape)
+    if out2 is not None:
+        _given(out2, "out2", q, shape)
     if lse is not None:
         _given(lse, "lse", q, (B, 2 * H, S), torch.float32)
-    with placed(q, stream):
+
+    def launch(handle):
         o = torch.empty(shape, dtype=q.dtype, device=q.device) if out is None else out
-        o2 = torch.empty(shape, dtype=q.dtype, device=q.device) if out2 is None else out2
-        if lse is None:
-            lse = torch.empty((B, 2 * H, S), dtype=torch.float32, device=q.device)
+        o2 = torch.empty_like(o) if out2 is None else out2
+        l = lse if lse is not None else torch.empty((B, 2 * H, S), dtype=torch.float32,
+                                                    device=q.device)
         if B and S:
             ws = _workspace(256, q.device, workspace)
-            code = lib().dash_diff_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), lam.data_ptr(),
-                                       o.data_ptr(), o2.data_ptr(), lse.data_ptr(), B, S, H,
-                                       H // Hkv, d, float(scale) if scale else 0.0,
-                                       int(bool(causal)), 2 * int(lam.dtype == torch.float32),
-                                       int(lam.dim() == 3), ws.data_ptr(),
-                                       ws.numel() * ws.element_size(),
-                                       torch.cuda.current_stream().cuda_stream)
-            _check(code, "dash_diff_fwd")
+            _check(lib().dash_diff_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), lam.data_ptr(),
+                                       o.data_ptr(), o2.data_ptr(), l.data_ptr(), B, S, H,
+                                       H // Hkv, d, scale or 0.0, bool(causal),
+                                       2 * (lam.dtype == torch.float32), lam.dim() == 3,
+                                       ws.data_ptr(), ws.numel() * ws.element_size(), handle),
+                   "dash_diff_fwd")
             if check:
                 status(ws, torch.cuda.current_stream())
-    return o, o2, lse
+        return o, o2, l
+    return run(q, stream, launch)
 
 
 def diff_bwd(q, k, v, o, o2, do, lse, lam, causal: bool = False, scale: float | None = None,
@@ -96,30 +90,30 @@ def diff_bwd(q, k, v, o, o2, do, lse, lam, causal: bool = False, scale: float | 
              check: bool = False):
     """Backward: returns (dQ, dK, dV, dlam), bit-identical on every run."""
     B, S, H, Hkv, d = _dims(q, k, v, lam)
-    for t, n in ((o, "o"), (o2, "o2"), (do, "do")):
-        _operand(t, n, q)
-        shaped(t, n, (B, S, H, 2 * d))
-    _operand(lse, "lse", q, torch.float32)
-    shaped(lse, "lse", (B, 2 * H, S))
+    shape = (B, S, H, 2 * d)
+    _given(o, "o", q, shape)
+    _given(o2, "o2", q, shape)
+    _given(do, "do", q, shape)
+    _given(lse, "lse", q, (B, 2 * H, S), torch.float32)
     for t, n, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v), (dlam, "dlam", lam)):
         if t is not None:
             _given(t, n, q, like.shape, like.dtype)
-    with placed(q, stream):
-        dq, dk, dv, dlam = (torch.empty_like(like) if t is None else t
-                            for t, like in ((dq, q), (dk, k), (dv, v), (dlam, lam)))
+
+    def launch(handle):
+        gq, gk, gv, gl = (torch.empty_like(like) if t is None else t
+                          for t, like in ((dq, q), (dk, k), (dv, v), (dlam, lam)))
         if not (B and S):
-            dlam.zero_()
-            return dq, dk, dv, dlam
-        ws = _workspace(diff_bwd_workspace_bytes(B, S, H, d) or 256, q.device, workspace)
-        code = lib().dash_diff_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-                                   o2.data_ptr(), do.data_ptr(), lse.data_ptr(), lam.data_ptr(),
-                                   dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dlam.data_ptr(), B,
-                                   S, H, H // Hkv, d, float(scale) if scale else 0.0,
-                                   int(bool(causal)), 2 * int(lam.dtype == torch.float32),
-                                   int(lam.dim() == 3), ws.data_ptr(),
-                                   ws.numel() * ws.element_size(),
-                                   torch.cuda.current_stream().cuda_stream)
-        _check(code, "dash_diff_bwd")
+            gl.zero_()
+            return gq, gk, gv, gl
+        L = lib()
+        ws = _workspace(L.dash_diff_bwd_workspace_bytes(B, S, H, d) or 256, q.device, workspace)
+        _check(L.dash_diff_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                               o2.data_ptr(), do.data_ptr(), lse.data_ptr(), lam.data_ptr(),
+                               gq.data_ptr(), gk.data_ptr(), gv.data_ptr(), gl.data_ptr(), B, S,
+                               H, H // Hkv, d, scale or 0.0, bool(causal),
+                               2 * (lam.dtype == torch.float32), lam.dim() == 3, ws.data_ptr(),
+                               ws.numel() * ws.element_size(), handle), "dash_diff_bwd")
         if check:
             status(ws, torch.cuda.current_stream())
-    return dq, dk, dv, dlam
+        return gq, gk, gv, gl
+    return run(q, stream, launch)

@@ -20,54 +20,57 @@ import ctypes
 import torch
 
 from . import _check, _workspace, lib
-from ._args import DTYPES, disjoint, placed, shaped, tensor
+from ._args import DTYPES, alike, disjoint, run, tensor
+
+_Strides4, _Strides6 = ctypes.c_longlong * 4, ctypes.c_longlong * 6
 
 
-def _rows(t, name, like=None):
-    """``t`` as [rows, C] without a copy; ValueError where it has no such form."""
-    if like is None:
-        tensor(t, name, dtypes=DTYPES)
-        if t.dim() < 1 or t.shape[-1] == 0:
-            raise ValueError(f"{name} needs rows of at least one element")
-    else:
-        tensor(t, name, like=like)
-        shaped(t, name, like.shape)
+def _stride(t, name, like=None):
+    """The stride of ``t``'s rows (of ``like``'s type, device and shape); ValueError where the
+    dimensions before the last do not flatten to one."""
+    if like is not None:
+        alike(t, name, like, like.shape)
+    C = t.shape[-1]
+    if t.is_contiguous():
+        return C
     try:
-        r = t.view(-1, t.shape[-1]) if t.numel() else t.reshape(-1, t.shape[-1])
+        r = t.view(-1, C)
     except RuntimeError:
         r = None
-    if r is None or (r.shape[-1] > 1 and r.stride(-1) != 1):
+    if r is None or (C > 1 and r.stride(1) != 1):
         raise ValueError(f"{name} must have contiguous rows at one stride, got strides "
                          f"{tuple(t.stride())}")
-    return r
+    return r.stride(0)
 
 
-def _written(t, name, like):
-    r = _rows(t, name, like)
-    if not disjoint(r):
+def _out(t, name, like):
+    """``_stride`` of a tensor that is written, 0 where there is none."""
+    if t is None:
+        return 0
+    s = _stride(t, name, like)
+    if not disjoint(t):
         raise ValueError(f"{name} has elements that share an address")
-    return r
+    return s
 
 
-def _weights(x, rows, **weights):
+def _weights(x, rows, w_post, gate, w_next):
     """Check the weights against rows of x; returns (their type, rows per gate row)."""
     C, dtype, gate_rows = x.shape[-1], None, rows
-    for name, w in weights.items():
+    for name, w in (("w_post", w_post), ("gate", gate), ("w_next", w_next)):
         if w is None:
             continue
-        tensor(w, name, dtypes=(x.dtype, torch.float32))
-        if w.device != x.device:
-            raise ValueError(f"{name} is on {w.device}, expected {x.device}")
-        if dtype is not None and w.dtype != dtype:
-            raise ValueError(f"{name} is {w.dtype}, the other weights {dtype}")
-        dtype = w.dtype
+        if dtype is None:
+            dtype = w.dtype if isinstance(w, torch.Tensor) else None
+            if dtype != x.dtype and dtype != torch.float32:
+                raise ValueError(f"{name} must be {x.dtype} or torch.float32, got {dtype}")
+        alike(w, name, x, dtype=dtype)
         if name == "gate" and w.dim() > 1:
-            groups = w.numel() // C if C else 0
+            groups = w.numel() // C
             if w.shape[-1] != C or groups == 0 or rows % groups:
                 raise ValueError(f"gate {tuple(w.shape)} does not divide {rows} rows of {C}")
             gate_rows = rows // groups
-        else:
-            shaped(w, name, (C,))
+        elif w.dim() != 1 or w.shape[0] != C:
+            raise ValueError(f"{name} must have shape {(C,)}, got {tuple(w.shape)}")
         if not w.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
     return x.dtype if dtype is None else dtype, gate_rows
@@ -77,93 +80,99 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stride(r):
-    return 0 if r is None else r.stride(0)
+def _like(t):
+    """A new contiguous tensor of t's shape."""
+    return torch.empty_like(t) if t.is_contiguous() else \
+        torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def _forward(x, a, w_post, gate, w_next, skip_scale, branch_scale, eps, y, h, stream):
-    xr = _rows(x, "x")
-    ar = None if a is None else _rows(a, "branch", x)
-    rows, C = xr.shape
-    wdtype, gate_rows = _weights(x, rows, w_post=w_post, gate=gate, w_next=w_next)
-    for t, n in ((y, "y"), (h, "h" if a is not None else "out")):
-        if t is not None:
-            _written(t, n, x)
-    with placed(x, stream):
-        new = dict(dtype=x.dtype, device=x.device)
-        if a is not None and y is None:
-            y = torch.empty(x.shape, **new)
-        if w_next is not None and h is None:
-            h = torch.empty(x.shape, **new)
-        rstd = dict(dtype=torch.float32, device=x.device)
-        rstd_a = torch.empty(x.shape[:-1], **rstd) if w_post is not None else None
-        rstd_y = torch.empty(x.shape[:-1], **rstd) if w_next is not None else None
-        if w_next is None:
-            h = None
+    tensor(x, "x", DTYPES)
+    shape = x.shape
+    if len(shape) < 1 or shape[-1] == 0:
+        raise ValueError("x needs rows of at least one element")
+    C = shape[-1]
+    rows = x.numel() // C
+    join = a is not None
+    xs, as_ = _stride(x, "x"), _stride(a, "branch", x) if join else 0
+    wdtype, gate_rows = _weights(x, rows, w_post, gate, w_next)
+    if w_next is None:
+        h = None
+    ys, hs = _out(y, "y", x), _out(h, "h" if join else "out", x)
+
+    def launch(handle):
+        Y, H, ra, ry = y, h, None, None
+        if join and Y is None:
+            Y = _like(x)
+        if w_next is not None:
+            if H is None:
+                H = _like(x)
+            ry = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
+        if w_post is not None:
+            ra = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
         if rows:
-            yr = None if a is None else _rows(y, "y", x)
-            hr = None if h is None else _rows(h, "h", x)
-            strides = (ctypes.c_longlong * 4)(_stride(xr), _stride(ar), _stride(yr), _stride(hr))
-            code = lib().dash_join_fwd(x.data_ptr(), _ptr(a), _ptr(w_post), _ptr(gate),
-                                       _ptr(w_next), _ptr(yr), _ptr(hr), _ptr(rstd_a),
-                                       _ptr(rstd_y), rows, C, gate_rows, strides,
-                                       float(skip_scale), float(branch_scale), float(eps),
-                                       DTYPES[x.dtype], DTYPES[wdtype],
-                                       torch.cuda.current_stream().cuda_stream)
-            _check(code, "dash_join_fwd")
-    return y, h, rstd_a, rstd_y
+            _check(lib().dash_join_fwd(x.data_ptr(), _ptr(a), _ptr(w_post), _ptr(gate),
+                                       _ptr(w_next), _ptr(Y) if join else None, _ptr(H), _ptr(ra),
+                                       _ptr(ry), rows, C, gate_rows,
+                                       _Strides4(xs, as_, ys or C, hs or C), skip_scale,
+                                       branch_scale, eps, DTYPES[x.dtype], DTYPES[wdtype],
+                                       handle), "dash_join_fwd")
+        return Y, H, ra, ry
+    return run(x, stream, launch)
 
 
 def _backward(dy, dh, y, a, rstd_a, rstd_y, w_post, gate, w_next, skip_scale, branch_scale, dx,
               da, workspace, stream):
+    join, normed = a is not None, w_next is not None
     base = y if y is not None else a
-    yr = None if y is None else _rows(y, "y" if a is not None else "x")
-    ar = None if a is None else _rows(a, "branch", base)
-    rows, C = (yr if yr is not None else ar).shape
-    wdtype, gate_rows = _weights(base, rows, w_post=w_post, gate=gate, w_next=w_next)
-    dyr = None if dy is None else _rows(dy, "dy", base)
-    if w_next is not None and (dh is None or y is None or rstd_y is None):
+    tensor(base, "y" if join else "x", DTYPES)
+    shape = base.shape
+    if len(shape) < 1 or shape[-1] == 0:
+        raise ValueError("y needs rows of at least one element")
+    C = shape[-1]
+    rows = base.numel() // C
+    if normed and (dh is None or y is None or rstd_y is None):
         raise ValueError("the gradient of the norm needs dh, its rows and their rstd")
-    dhr = None if w_next is None else _rows(dh, "dh", base)
-    if w_next is None and dy is None:
+    if not normed and dy is None:
         raise ValueError("no gradient is given")
     if w_post is not None and rstd_a is None:
         raise ValueError("the gradient of the norm after the branch needs rstd_a")
+    ys = 0 if y is None else _stride(y, "y")
+    as_ = _stride(a, "branch", base) if join else 0
+    dys = 0 if dy is None else _stride(dy, "dy", base)
+    dhs = _stride(dh, "dh", base) if normed else 0
+    wdtype, gate_rows = _weights(base, rows, w_post, gate, w_next)
     for t, w, n in ((rstd_a, w_post, "rstd_a"), (rstd_y, w_next, "rstd_y")):
         if w is not None:
-            tensor(t, n, like=base, dtypes=(torch.float32,))
-            shaped(t, n, base.shape[:-1])
+            alike(t, n, base, shape[:-1], torch.float32)
             if not t.is_contiguous():
                 raise ValueError(f"{n} must be contiguous")
-    for t, n in ((dx, "dx"), (da, "da")):
-        if t is not None:
-            _written(t, n, base)
-    with placed(base, stream):
-        dx = torch.empty(base.shape, dtype=base.dtype, device=base.device) if dx is None else dx
-        if a is not None and da is None:
-            da = torch.empty(base.shape, dtype=base.dtype, device=base.device)
+    dxs, das = _out(dx, "dx", base), _out(da, "da", base)
+
+    def launch(handle):
+        DX, DA = _like(base) if dx is None else dx, da
+        if join and DA is None:
+            DA = _like(base)
         dw_post, dgate, dw_next = (None if w is None else torch.empty_like(w)
                                    for w in (w_post, gate, w_next))
-        if rows == 0:
+        if rows:
+            L, dtype = lib(), DTYPES[base.dtype]
+            need = L.dash_join_bwd_workspace_bytes(rows, C, gate_rows if gate is not None else 0,
+                                                   join, dtype)
+            ws = _workspace(need or 256, base.device, workspace)
+            _check(L.dash_join_bwd(_ptr(dy), _ptr(dh) if normed else None, _ptr(y), _ptr(a),
+                                   _ptr(w_post), _ptr(gate), _ptr(w_next), _ptr(rstd_a),
+                                   _ptr(rstd_y), DX.data_ptr(), _ptr(DA), _ptr(dw_post),
+                                   _ptr(dgate), _ptr(dw_next), rows, C, gate_rows,
+                                   _Strides6(dys, dhs, ys, as_, dxs or C, das or C), skip_scale,
+                                   branch_scale, dtype, DTYPES[wdtype], ws.data_ptr(),
+                                   ws.numel() * ws.element_size(), handle), "dash_join_bwd")
+        else:
             for w in (dw_post, dgate, dw_next):
                 if w is not None:
                     w.zero_()
-            return dx, da, dw_post, dgate, dw_next
-        dxr = _rows(dx, "dx", base)
-        dar = None if a is None else _rows(da, "da", base)
-        need = lib().dash_join_bwd_workspace_bytes(rows, C, gate_rows if gate is not None else 0,
-                                                   int(a is not None), DTYPES[base.dtype])
-        ws = _workspace(int(need) or 256, base.device, workspace)
-        strides = (ctypes.c_longlong * 6)(*(_stride(r) for r in (dyr, dhr, yr, ar, dxr, dar)))
-        code = lib().dash_join_bwd(_ptr(dy), _ptr(dh) if w_next is not None else None, _ptr(y),
-                                   _ptr(a), _ptr(w_post), _ptr(gate), _ptr(w_next), _ptr(rstd_a),
-                                   _ptr(rstd_y), dx.data_ptr(), _ptr(da), _ptr(dw_post),
-                                   _ptr(dgate), _ptr(dw_next), rows, C, gate_rows, strides,
-                                   float(skip_scale), float(branch_scale), DTYPES[base.dtype],
-                                   DTYPES[wdtype], ws.data_ptr(), ws.numel() * ws.element_size(),
-                                   torch.cuda.current_stream().cuda_stream)
-        _check(code, "dash_join_bwd")
-    return dx, da, dw_post, dgate, dw_next
+        return DX, DA if join else None, dw_post, dgate, dw_next
+    return run(base, stream, launch)
 
 
 def norm_bwd_workspace_bytes(rows: int, C: int, dtype) -> int:

@@ -9,22 +9,19 @@ fp32.  One kernel launch turns q and k and copies v.
 """
 from __future__ import annotations
 
-import ctypes
 import math
+import struct
 
 import torch
 
 from . import _check, lib
-from ._args import DTYPES, disjoint, placed, shaped, tensor
+from ._args import DTYPES, alike, disjoint, run, tensor
 
 LAYOUTS = {"half": 0, "interleaved": 1}
 SCALINGS = ("none", "linear", "base", "ramp")
 
-
-class _Part(ctypes.Structure):
-    _fields_ = [("inp", ctypes.c_void_p), ("out", ctypes.c_void_p), ("heads", ctypes.c_int),
-                ("D", ctypes.c_int), ("turn", ctypes.c_int), ("in_stride", ctypes.c_longlong * 3),
-                ("out_stride", ctypes.c_longlong * 3)]
+# dash_rope_part_t: in, out, heads, D, turn, in_stride[3], out_stride[3]
+_PART = struct.Struct("@PPiii4x6q")
 
 
 def rope_freqs(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -67,74 +64,77 @@ def rope_freqs(rot: int, base: float = 10000.0, scaling: str = "none", factor: f
 
 def _rope(parts, inv_freq, magnitude, positions, start, layout, out, stream, back):
     q = parts[0]
-    tensor(q, "q", dtypes=DTYPES)
-    if q.dim() not in (3, 4):
+    tensor(q, "q", DTYPES)
+    dims = q.dim()
+    if dims != 4 and dims != 3:
         raise ValueError(f"heads are [B, S, H, D] or [T, H, D], got {tuple(q.shape)}")
     if layout not in LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(LAYOUTS)}")
-    tensor(inv_freq, "inv_freq", dtypes=(torch.float64,))
-    if inv_freq.device != q.device or inv_freq.dim() != 1 or not inv_freq.is_contiguous() or \
-            not 0 < 2 * inv_freq.numel() <= 1024:
-        raise ValueError("inv_freq must be contiguous float64 [rot/2] on the heads' device, "
-                         "rot <= 1024")
+    alike(inv_freq, "inv_freq", q, dtype=torch.float64)
     rot = 2 * inv_freq.numel()
-    packed = q.dim() == 3
-    B, S = (1, q.shape[0]) if packed else q.shape[:2]
-    if out is not None and len(out) != len(parts):
+    if inv_freq.dim() != 1 or not inv_freq.is_contiguous() or not 0 < rot <= 1024:
+        raise ValueError("inv_freq must be contiguous float64 [rot/2], rot <= 1024")
+    tokens = q.shape[:-2]
+    B, S = tokens if dims == 4 else (1, tokens[0])
+    if out is None:
+        out = (None, None, None)
+    elif len(out) != len(parts):
         raise ValueError(f"out must hold {len(parts)} tensors")
+    res, packed = [], []
     for i, t in enumerate(parts):
-        name = "qkv"[i]
         if t is None:
             continue
-        tensor(t, name, like=q)
-        if t.shape[:-2] != q.shape[:-2] or t.dim() != q.dim():
-            raise ValueError(f"{name} {tuple(t.shape)} does not go with q {tuple(q.shape)}")
-        if i < 2 and t.shape[-1] < rot:
-            raise ValueError(f"{name} has heads of {t.shape[-1]}, fewer than the {rot} that turn")
-        for u, n in ((t, name), (out[i] if out is not None else None, f"out[{i}]")):
-            if u is None:
-                continue
-            tensor(u, n, like=q)
-            shaped(u, n, t.shape)
-            if u.shape[-1] > 1 and u.stride(-1) != 1:
-                raise ValueError(f"the elements of a head of {n} must be contiguous")
-        if out is not None and out[i] is not None and not disjoint(out[i]):
-            raise ValueError(f"out[{i}] has elements that share an address")
-    pb = pt = 0
+        name, shape = "qkv"[i], t.shape
+        if i:
+            alike(t, name, q)
+            if shape[:-2] != tokens or t.dim() != dims:
+                raise ValueError(f"{name} {tuple(shape)} does not go with q {tuple(q.shape)}")
+        if i < 2 and shape[-1] < rot:
+            raise ValueError(f"{name} has heads of {shape[-1]}, fewer than the {rot} that turn")
+        if shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"the elements of a head of {name} must be contiguous")
+        o = out[i]
+        if o is not None:
+            name = f"out[{i}]"
+            alike(o, name, q, shape)
+            if shape[-1] > 1 and o.stride(-1) != 1:
+                raise ValueError(f"the elements of a head of {name} must be contiguous")
+            if not disjoint(o):
+                raise ValueError(f"{name} has elements that share an address")
+    where, pos64, pb, pt = None, 0, 0, 0
     if positions is not None:
-        tensor(positions, "positions", dtypes=(torch.int32, torch.int64))
+        tensor(positions, "positions", (torch.int32, torch.int64))
         if positions.device != q.device:
             raise ValueError(f"positions are on {positions.device}, the heads on {q.device}")
-        want = (q.shape[0],) if packed else (B, S)
-        if tuple(positions.shape) not in (want, want[-1:]):
-            raise ValueError(f"positions must be {want} or {want[-1:]}, got "
+        if positions.shape != tokens and positions.shape != tokens[-1:]:
+            raise ValueError(f"positions must be {tuple(tokens)} or {tuple(tokens[-1:])}, got "
                              f"{tuple(positions.shape)}")
+        where, pos64 = positions.data_ptr(), int(positions.dtype == torch.int64)
         pt = positions.stride(-1)
         pb = positions.stride(0) if positions.dim() == 2 else 0
-    with placed(q, stream):
-        res = tuple(None if t is None else
-                    out[i] if out is not None and out[i] is not None else
-                    torch.empty(t.shape, dtype=t.dtype, device=t.device)
-                    for i, t in enumerate(parts))
-        arr, n = (_Part * 3)(), 0
-        for i, (t, r) in enumerate(zip(parts, res)):
-            if t is None or t.shape[-1] == 0 or t.shape[-2] == 0:
+
+    def launch(handle):
+        for t, o in zip(parts, out):
+            if t is None:
+                res.append(None)
                 continue
-            a = arr[n]
-            n += 1
-            a.inp, a.out = t.data_ptr(), r.data_ptr()
-            a.heads, a.D, a.turn = t.shape[-2], t.shape[-1], int(i < 2)
-            a.in_stride[:] = (0, *t.stride()[:2]) if packed else t.stride()[:3]
-            a.out_stride[:] = (0, *r.stride()[:2]) if packed else r.stride()[:3]
-        if n and B and S:
-            code = lib().dash_rope(arr, n, B, S, rot, LAYOUTS[layout], DTYPES[q.dtype],
-                                   inv_freq.data_ptr(), float(magnitude),
-                                   None if positions is None else positions.data_ptr(),
-                                   int(positions is not None and positions.dtype == torch.int64),
-                                   pb, pt, int(start), int(back),
-                                   torch.cuda.current_stream().cuda_stream)
-            _check(code, "dash_rope")
-    return res
+            if o is None:
+                o = torch.empty_like(t) if t.is_contiguous() else \
+                    torch.empty(t.shape, dtype=t.dtype, device=t.device)
+            res.append(o)
+            if t.numel():
+                ti, to = t.stride(), o.stride()
+                if dims == 3:
+                    ti, to = (0, *ti), (0, *to)
+                packed.append(_PART.pack(t.data_ptr(), o.data_ptr(), t.shape[-2], t.shape[-1],
+                                         int(len(res) < 3), ti[0], ti[1], ti[2], to[0], to[1],
+                                         to[2]))
+        if packed:
+            _check(lib().dash_rope(b"".join(packed), len(packed), B, S, rot, LAYOUTS[layout],
+                                   DTYPES[q.dtype], inv_freq.data_ptr(), magnitude, where, pos64,
+                                   pb, pt, start, back, handle), "dash_rope")
+        return tuple(res)
+    return run(q, stream, launch)
 
 
 def rope_fwd(q, k=None, v=None, *, inv_freq, magnitude: float = 1.0, positions=None,

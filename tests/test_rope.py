@@ -5,7 +5,6 @@ phase) and sincospif by two units in the last place, so cos and sin are off by l
 pi 2^-25 + 2^-22 < 2^-21; the turn of a pair of norm n then by 2 n 2^-21 with its own fp32
 rounding (three roundings of 2^-24 relative to n) below that: 2^-19 n m in all for magnitude m.
 Rounding to the output's type adds half a step, eps / 2 relative to the value."""
-import ctypes
 import math
 
 import pytest
@@ -13,7 +12,7 @@ import torch
 
 import deterministic_attention_backward_gb300 as dash
 from deterministic_attention_backward_gb300 import _build
-from deterministic_attention_backward_gb300.rope import _Part
+from deterministic_attention_backward_gb300.rope import _PART
 
 BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
 
@@ -75,12 +74,8 @@ def test_abi_refusals(L):
     fake = 1 << 20  # never dereferenced: every call below is refused first
 
     def call(nparts=1, B=1, S=1, rot=8, layout=0, dtype=0, freq=fake, pos=None, pos64=0, **part):
-        a = (_Part * 3)()
-        for q in a:
-            q.inp = q.out = fake
-            q.heads, q.D, q.turn = 2, 16, 1
-            for k, v in part.items():
-                setattr(q, k, v)
+        q = {**dict(inp=fake, out=fake, heads=2, D=16, turn=1), **part}
+        a = _PART.pack(q["inp"] or 0, q["out"] or 0, q["heads"], q["D"], q["turn"], *[16] * 6) * 4
         return L.dash_rope(a, nparts, B, S, rot, layout, dtype, freq, 1.0, pos, pos64, 0, 1, 0, 0,
                            None)
     for bad in (dict(nparts=0), dict(nparts=4), dict(B=0), dict(S=-1), dict(rot=7), dict(rot=0),
