@@ -6,6 +6,10 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include <type_traits>
+
+#include "f32x2.cuh"
+
 namespace dash {
 
 template <typename T>
@@ -63,6 +67,54 @@ __device__ __forceinline__ Pack<T, V> pack(const float (&f)[V]) {
 #pragma unroll
   for (int i = 0; i < V; ++i) r.e[i] = from_f32<T>(f[i]);
   return r;
+}
+
+// A 16-byte vector as pairs of fp32 values, and back.
+template <typename T>
+__device__ __forceinline__ void unpack2(const uint4 &v, f2 (&f)[8 / sizeof(T)]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if constexpr (sizeof(T) == 4) {
+    f[0] = f2_of(w[0], w[1]);
+    f[1] = f2_of(w[2], w[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const T *e = reinterpret_cast<const T *>(&w[i]);
+      f[i] = f2_of(to_f32<T>(e[0]), to_f32<T>(e[1]));
+    }
+  }
+}
+template <>
+__device__ __forceinline__ void unpack2<__nv_bfloat16>(const uint4 &v, f2 (&f)[4]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = f2_of(w[i] << 16, w[i] & 0xffff0000u);
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack2(const f2 (&f)[8 / sizeof(T)]) {
+  uint32_t w[4];
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float a, b;
+      f2_to(f[i], a, b);
+      w[2 * i] = __float_as_uint(a), w[2 * i + 1] = __float_as_uint(b);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float a, b;
+      f2_to(f[i], a, b);
+      if constexpr (std::is_same<T, __half>::value) {
+        const __half2 h = __floats2half2_rn(a, b);
+        w[i] = *reinterpret_cast<const uint32_t *>(&h);
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        w[i] = *reinterpret_cast<const uint32_t *>(&h);
+      }
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 }  // namespace dash

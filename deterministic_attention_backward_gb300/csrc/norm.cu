@@ -9,15 +9,31 @@
 
 namespace dash {
 
-// CTAs per gate group of the backward: about two 512-thread CTAs on each of 152 SMs in all,
-// more where a CTA is smaller; never more than there are rows for.
-int norm_bwd_ctas(long long rows, long long groups, int C, int elem_bytes, bool wide) {
+// CTAs per gate group of the backward: in all as many as 152 SMs hold at once (by the ring's
+// shared memory and the column sums' registers, see ring_shape), whatever the device, so that
+// the order of the weight gradients' sums depends on the sizes alone; never more than there are
+// rows for.
+int norm_bwd_ctas(long long rows, long long groups, int C, int elem_bytes, bool wide, bool join) {
   const int n = wide ? C * elem_bytes / 16 : C;
-  const long long total = n <= 128 ? 2 * kNormSlots : n <= 256 ? 3 * kNormSlots
-                          : n <= 512 ? 2 * kNormSlots : kNormSlots;
-  const long long per = rows / groups, at_once = n <= 128 ? 8 : 1;
+  int sms_share = 2, at_once = 1;  // CTAs on an SM, rows of a CTA at once
+  if (!wide) {
+    if (n <= 128) at_once = 8;
+  } else if (n <= 64) {
+    const int lanes = n <= 4 ? 4 : n <= 8 ? 8 : n <= 16 ? 16 : 32;
+    at_once = 256 / lanes;
+    sms_share = join ? 2 : n <= 32 ? 4 : 3;
+  } else if (n <= 128) {
+    sms_share = 8;
+  } else if (n <= 256) {
+    sms_share = 4;
+  } else if (n <= 512) {
+    sms_share = join ? 2 : 3;
+  } else if (n <= 2048) {
+    sms_share = 1;
+  }
+  const long long per = rows / groups;
   const long long most = (per + at_once - 1) / at_once;
-  const long long want = total / groups;
+  const long long want = 152LL * sms_share / groups;
   return (int)(want < 1 ? 1 : want < most ? want : most);
 }
 
@@ -47,11 +63,12 @@ struct Groups {
   int groups, ctas, row_gate;
   long long gate_rows;
 };
-Groups make_groups(long long rows, int C, long long gate_rows, bool gate, int dtype, bool wide) {
+Groups make_groups(long long rows, int C, long long gate_rows, bool gate, int dtype, bool wide,
+                   bool join) {
   Groups g{1, 1, gate && gate_rows == 1 && rows > 1, rows};
   if (gate && !g.row_gate) g.gate_rows = gate_rows;
   g.groups = (int)(rows / g.gate_rows);
-  g.ctas = norm_bwd_ctas(rows, g.groups, C, elem_size(dtype), wide);
+  g.ctas = norm_bwd_ctas(rows, g.groups, C, elem_size(dtype), wide, join);
   return g;
 }
 
@@ -103,7 +120,7 @@ size_t dash_join_bwd_workspace_bytes(long long rows, int C, long long gate_rows,
   if (check_rows(rows, C, gate_rows, gate_rows > 0, dtype, dtype) != DASH_OK) return 0;
   size_t most = 0;
   for (const bool wide : {false, true}) {
-    const Groups g = make_groups(rows, C, gate_rows, gate_rows > 0, dtype, wide);
+    const Groups g = make_groups(rows, C, gate_rows, gate_rows > 0, dtype, wide, join);
     const size_t n = align256((size_t)g.groups * g.ctas * (join ? 2 : 1) * C * sizeof(float));
     most = n > most ? n : most;
   }
@@ -142,7 +159,7 @@ dash_status_t dash_join_bwd(const void *dy, const void *dh, const void *y, const
   const bool wide = C % vec == 0 && all_aligned(rowp, 16) && all_aligned(wp, 16) && any % vec == 0;
   DevInfo dev;
   if ((st = device_info(&dev)) != DASH_OK) return st;
-  const Groups g = make_groups(rows, C, gate_rows, gate != nullptr, dtype, wide);
+  const Groups g = make_groups(rows, C, gate_rows, gate != nullptr, dtype, wide, join);
   NormBwdParams p{};
   p.dy = dy, p.dh = dh, p.y = y, p.a = a;
   p.w_post = w_post, p.gate = gate, p.w_next = w_next;

@@ -30,10 +30,7 @@ struct NormBwdParams {
   float skip, branch;
 };
 
-// CTAs that share the rows of one group: about `kNormSlots` in all, whatever the device, so
-// that the order of the weight gradients' sums depends on the sizes alone.
-constexpr int kNormSlots = 304;
-int norm_bwd_ctas(long long rows, long long groups, int C, int elem_bytes, bool wide);
+int norm_bwd_ctas(long long rows, long long groups, int C, int elem_bytes, bool wide, bool join);
 
 template <typename T>
 cudaError_t launch_norm_fwd(const NormFwdParams &p, bool join, bool wide, cudaStream_t s);

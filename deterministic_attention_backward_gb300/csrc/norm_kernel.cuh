@@ -16,6 +16,8 @@
 // `part`, and a second kernel adds the CTAs' sums in a fixed order -- no atomics, the same
 // bits on every run.
 #pragma once
+#include <type_traits>
+
 #include "common.cuh"
 #include "elem.cuh"
 #include "norm.cuh"
@@ -48,7 +50,7 @@ __device__ __forceinline__ void store_w(void *w, long long at, int wf32, float v
     static_cast<T *>(w)[at] = from_f32<T>(v);
 }
 
-// Sum over the kNT threads of a row, the same value in each.  `red` holds two buffers of
+// Sum over the kNT threads of a row (part of a warp, a warp, or a CTA), the same value in each.  `red` holds two buffers of
 // kNT / 32 floats used in turn, so one barrier per sum is enough.
 template <int kNT>
 struct RowSum {
@@ -56,7 +58,8 @@ struct RowSum {
   int turn = 0;
   __device__ __forceinline__ float operator()(float v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = (kNT < 32 ? kNT : 32) / 2; o > 0; o >>= 1)
+      v += __shfl_xor_sync(0xffffffffu, v, o);
     if constexpr (kNT > 32) {
       float *r = red + turn * (kNT / 32);
       turn ^= 1;
@@ -424,6 +427,429 @@ __global__ void __launch_bounds__(kNT * kRowsPerCta<kNT>)
   }
 }
 
+// ------------------------------------------------------------------------------- rings
+// Rows of 16-byte vectors come in through a ring of shared memory that every thread fills and
+// reads for itself (cp.async: no barrier, and a thread's loads for the next rows are in flight
+// while it works on this one without holding registers).  Slot (stage, array, vector) of a
+// thread is 16 bytes at thread * 16 of its own block of kThreads * 16.
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kLeft>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+template <int kNT>
+constexpr int kRingThreads = kNT < 256 ? (kNT > 32 ? kNT : 256) : kNT;
+
+template <typename T, int kThreads, int kNV, int kArrays>
+struct Ring {
+  static constexpr int P = 8 / sizeof(T);  // pairs of a vector
+  uint8_t *mine;                           // this thread's slots
+  __device__ __forceinline__ explicit Ring(void *smem)
+      : mine(static_cast<uint8_t *>(smem) + threadIdx.x * 16) {}
+  __device__ __forceinline__ uint8_t *slot(int stage, int array, int i) const {
+    return mine + (size_t)((stage * kArrays + array) * kNV + i) * (kThreads * 16);
+  }
+  __device__ __forceinline__ void fetch(int stage, int array, int i, const T *src) const {
+    cp_async16(slot(stage, array, i), src);
+  }
+  __device__ __forceinline__ void read(int stage, int array, int i, f2 (&f)[P]) const {
+    unpack2<T>(*reinterpret_cast<const uint4 *>(slot(stage, array, i)), f);
+  }
+};
+template <typename T>
+__device__ __forceinline__ void put(T *dst, const f2 (&f)[8 / sizeof(T)]) {
+  *reinterpret_cast<uint4 *>(dst) = pack2<T>(f);
+}
+// A weight vector in pairs (uniform branch on its type).
+template <typename T>
+__device__ __forceinline__ void load_w2(const void *w, long long at, int wf32,
+                                        f2 (&f)[8 / sizeof(T)]) {
+  if (sizeof(T) == 2 && wf32) {
+    const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const float *>(w) + at);
+#pragma unroll
+    for (int i = 0; i < (int)(4 / sizeof(T)); ++i) {
+      const uint4 v = q[i];
+      f[2 * i] = f2_of(v.x, v.y);
+      f[2 * i + 1] = f2_of(v.z, v.w);
+    }
+  } else {
+    unpack2<T>(*reinterpret_cast<const uint4 *>(static_cast<const T *>(w) + at), f);
+  }
+}
+// branch_scale gate w_post of one vector (factors that are not there: 1); of the gate's row
+// `grow`, in elements.
+template <typename T, typename Params>
+__device__ __forceinline__ void branch_factor(const Params &p, int c, long long grow,
+                                              f2 (&f)[8 / sizeof(T)]) {
+  constexpr int P = 8 / sizeof(T);
+#pragma unroll
+  for (int e = 0; e < P; ++e) f[e] = f2_of(p.branch, p.branch);
+  if (p.w_post) {
+    f2 w[P];
+    load_w2<T>(p.w_post, c, p.wf32, w);
+#pragma unroll
+    for (int e = 0; e < P; ++e) f[e] = mul2(f[e], w[e]);
+  }
+  if (p.gate) {
+    f2 w[P];
+    load_w2<T>(p.gate, grow + c, p.wf32, w);
+#pragma unroll
+    for (int e = 0; e < P; ++e) f[e] = mul2(f[e], w[e]);
+  }
+}
+
+// Weights stay in registers over a CTA's rows (up to two vectors a thread): read again for
+// every row they come from L2, whose latency then stands between the two sums of each row.
+template <typename T, int kNT, int kNV, bool kJoin, int kDepth>
+__global__ void __launch_bounds__(kRingThreads<kNT>) fwd_ring(const NormFwdParams p) {
+  constexpr int V = 16 / sizeof(T), P = V / 2, kThreads = kRingThreads<kNT>;
+  constexpr int kRows = kThreads / kNT;
+  constexpr bool kKeep = kNV <= 2;
+  extern __shared__ float4 dyn4[];
+  __shared__ float red[2 * (kNT / 32 ? kNT / 32 : 1)];
+  RowSum<kNT> row_sum{red};
+  const Ring<T, kThreads, kNV, kJoin ? 2 : 1> ring(dyn4);
+  const int lane = threadIdx.x % kNT;
+  const long long step = (long long)gridDim.x * kRows;
+  long long row = (long long)blockIdx.x * kRows + threadIdx.x / kNT;
+  const float inv_c = 1.f / (float)p.C;
+  auto fetch = [&](int stage, long long r) {
+    if (r < p.rows) {
+#pragma unroll
+      for (int i = 0; i < kNV; ++i) {
+        const int c = (i * kNT + lane) * V;
+        if (c < p.C) {
+          if constexpr (kJoin)
+            ring.fetch(stage, 1, i, static_cast<const T *>(p.a) + r * p.as + c);
+          ring.fetch(stage, 0, i, static_cast<const T *>(p.x) + r * p.xs + c);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < kDepth; ++s) fetch(s, row + s * step);
+  f2 wn[kKeep ? kNV : 1][P], fac[kKeep && kJoin ? kNV : 1][P];
+  long long held = -1;  // the gate row that `fac` holds
+  if constexpr (kKeep) {
+    if (p.w_next)
+#pragma unroll
+      for (int i = 0; i < kNV; ++i)
+        if ((i * kNT + lane) * V < p.C) load_w2<T>(p.w_next, (i * kNT + lane) * V, p.wf32, wn[i]);
+  }
+  const f2 skip = f2_of(p.skip, p.skip);
+  int stage = 0;
+  // a warp stays until its last row is done: the sums of rows take part in full
+  for (long long first = row - threadIdx.x % 32 / kNT; first < p.rows; first += step, row += step) {
+    const bool in = row < p.rows;
+    const long long gate = kJoin && p.gate && in ? (unsigned)row / (unsigned)p.gate_rows : 0;
+    if (kKeep && kJoin && gate != held) {
+      held = gate;
+#pragma unroll
+      for (int i = 0; i < kNV; ++i) {
+        const int c = (i * kNT + lane) * V;
+        if (c < p.C) branch_factor<T>(p, c, gate * p.C, fac[kJoin && kKeep ? i : 0]);
+      }
+    }
+    cp_async_wait<kDepth - 1>();
+    f2 y[kNV][P];  // the branch, then the joined row
+    f2 ss2 = f2_of(0.f, 0.f);
+    float rstd_a = 1.f;
+    if constexpr (kJoin) {
+#pragma unroll
+      for (int i = 0; i < kNV; ++i)
+        if (in && (i * kNT + lane) * V < p.C) {
+          ring.read(stage, 1, i, y[i]);
+#pragma unroll
+          for (int e = 0; e < P; ++e) ss2 = fma2(y[i][e], y[i][e], ss2);
+        }
+      if (p.w_post) {
+        rstd_a = rsqrtf(row_sum(f2_sum(ss2)) * inv_c + p.eps);
+        if (lane == 0 && in) p.rstd_a[row] = rstd_a;
+      }
+      ss2 = f2_of(0.f, 0.f);
+    }
+    const f2 rstd_a2 = f2_of(rstd_a, rstd_a);
+#pragma unroll
+    for (int i = 0; i < kNV; ++i) {
+      const int c = (i * kNT + lane) * V;
+      if (in && c < p.C) {
+        f2 x[P];
+        ring.read(stage, 0, i, x);
+        if constexpr (kJoin) {
+          f2 f[P];
+          if constexpr (!kKeep) branch_factor<T>(p, c, gate * p.C, f);
+#pragma unroll
+          for (int e = 0; e < P; ++e)
+            y[i][e] = fma2(mul2(y[i][e], rstd_a2), kKeep ? fac[kKeep ? i : 0][e] : f[e],
+                           mul2(skip, x[e]));
+          put<T>(static_cast<T *>(p.y) + row * p.ys + c, y[i]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < P; ++e) y[i][e] = x[e];
+        }
+#pragma unroll
+        for (int e = 0; e < P; ++e) ss2 = fma2(y[i][e], y[i][e], ss2);
+      }
+    }
+    fetch(stage, row + kDepth * step);  // everything of this stage has been read
+    stage = stage + 1 == kDepth ? 0 : stage + 1;
+    if (!p.w_next) continue;
+    // the norm takes the joined row before its rounding
+    const float rstd = rsqrtf(row_sum(f2_sum(ss2)) * inv_c + p.eps);
+    if (lane == 0 && in) p.rstd_y[row] = rstd;
+    const f2 rstd2 = f2_of(rstd, rstd);
+#pragma unroll
+    for (int i = 0; i < kNV; ++i) {
+      const int c = (i * kNT + lane) * V;
+      if (in && c < p.C) {
+        f2 w[P];
+        if constexpr (!kKeep) load_w2<T>(p.w_next, c, p.wf32, w);
+#pragma unroll
+        for (int e = 0; e < P; ++e)
+          w[e] = mul2(mul2(y[i][e], rstd2), kKeep ? wn[kKeep ? i : 0][e] : w[e]);
+        put<T>(static_cast<T *>(p.h) + row * p.hs + c, w);
+      }
+    }
+  }
+}
+
+template <typename T, int kNT, int kNV, bool kJoin, int kDepth>
+__global__ void __launch_bounds__(kRingThreads<kNT>, kRingThreads<kNT> <= 256 ? 512 / kRingThreads<kNT> : 1)
+    bwd_ring(const NormBwdParams p) {
+  constexpr int V = 16 / sizeof(T), P = V / 2, kThreads = kRingThreads<kNT>;
+  constexpr int kRows = kThreads / kNT;
+  constexpr int kSums = kJoin ? 2 : 1;
+  constexpr bool kKeep = kNV <= 2;
+  enum { kDh, kY, kDy, kA };
+  extern __shared__ float4 dyn4[];
+  __shared__ float red[2 * (kNT / 32 ? kNT / 32 : 1)];
+  RowSum<kNT> row_sum{red};
+  const Ring<T, kThreads, kNV, kJoin ? 4 : 3> ring(dyn4);
+  const int lane = threadIdx.x % kNT, sub = threadIdx.x / kNT;
+  const int group = blockIdx.x / p.ctas, cta = blockIdx.x % p.ctas;
+  const long long row1 = (group + 1) * p.gate_rows, step = (long long)p.ctas * kRows;
+  long long row = group * p.gate_rows + (long long)cta * kRows + sub;
+  const float inv_c = 1.f / (float)p.C;
+  const f2 zero = f2_of(0.f, 0.f);
+  f2 accN[kNV][P], accA[kJoin ? kNV : 1][P];
+#pragma unroll
+  for (int i = 0; i < kNV; ++i)
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      accN[i][e] = zero;
+      if constexpr (kJoin) accA[i][e] = zero;
+    }
+  float next_y = 0.f, next_a = 1.f;  // rstd of the next row, a row ahead of their use
+  auto stats = [&](long long r) {
+    if (r < row1) {
+      if (p.w_next) next_y = p.rstd_y[r];
+      if (kJoin && p.w_post) next_a = p.rstd_a[r];
+    }
+  };
+  auto fetch = [&](int stage, long long r) {
+    if (r < row1) {
+#pragma unroll
+      for (int i = 0; i < kNV; ++i) {
+        const int c = (i * kNT + lane) * V;
+        if (c < p.C) {
+          if (p.w_next) {
+            ring.fetch(stage, kDh, i, static_cast<const T *>(p.dh) + r * p.dhs + c);
+            ring.fetch(stage, kY, i, static_cast<const T *>(p.y) + r * p.ys + c);
+          }
+          if (p.dy) ring.fetch(stage, kDy, i, static_cast<const T *>(p.dy) + r * p.dys + c);
+          if constexpr (kJoin)
+            ring.fetch(stage, kA, i, static_cast<const T *>(p.a) + r * p.as + c);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < kDepth; ++s) fetch(s, row + s * step);
+  f2 wn[kKeep ? kNV : 1][P], fac[kKeep && kJoin ? kNV : 1][P];
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int i = 0; i < kNV; ++i) {
+      const int c = (i * kNT + lane) * V;
+      if (c < p.C) {
+        if (p.w_next) load_w2<T>(p.w_next, c, p.wf32, wn[i]);
+        if (kJoin && !p.row_gate)
+          branch_factor<T>(p, c, (long long)group * p.C, fac[kJoin ? i : 0]);
+      }
+    }
+  }
+  stats(row);
+  const f2 skip = f2_of(p.skip, p.skip), branch = f2_of(p.branch, p.branch);
+  int stage = 0;
+  for (long long first = row - threadIdx.x % 32 / kNT; first < row1; first += step, row += step) {
+    const bool in = row < row1;
+    const float rstd_y = next_y, rstd_a = next_a;
+    const f2 rstd_y2 = f2_of(rstd_y, rstd_y), rstd_a2 = f2_of(rstd_a, rstd_a);
+    stats(row + step);
+    cp_async_wait<kDepth - 1>();
+    f2 D[kNV][P];  // dh w_next, then Dy, then branch gate Dy w_post
+    float c1 = 0.f;
+    if (p.w_next) {
+      f2 c1_2 = zero;
+#pragma unroll
+      for (int i = 0; i < kNV; ++i) {
+        const int c = (i * kNT + lane) * V;
+        if (in && c < p.C) {
+          f2 q[P], w[P];
+          ring.read(stage, kDh, i, D[i]);
+          ring.read(stage, kY, i, q);
+          if constexpr (!kKeep) load_w2<T>(p.w_next, c, p.wf32, w);
+#pragma unroll
+          for (int e = 0; e < P; ++e) {
+            q[e] = mul2(q[e], rstd_y2);
+            accN[i][e] = fma2(D[i][e], q[e], accN[i][e]);
+            D[i][e] = mul2(D[i][e], kKeep ? wn[kKeep ? i : 0][e] : w[e]);
+            c1_2 = fma2(D[i][e], q[e], c1_2);
+          }
+        }
+      }
+      c1 = row_sum(f2_sum(c1_2)) * inv_c;
+    }
+    const float nc1 = -c1 * rstd_y;
+    const f2 nc1_2 = f2_of(nc1, nc1);
+    f2 c2_2 = zero;
+#pragma unroll
+    for (int i = 0; i < kNV; ++i) {
+      const int c = (i * kNT + lane) * V;
+      if (in && c < p.C) {
+        f2 t[P];
+        if (p.dy) {
+          ring.read(stage, kDy, i, t);
+        } else {
+#pragma unroll
+          for (int e = 0; e < P; ++e) t[e] = zero;
+        }
+        if (p.w_next) {
+          f2 y[P];
+          ring.read(stage, kY, i, y);
+#pragma unroll
+          for (int e = 0; e < P; ++e)
+            D[i][e] = fma2(rstd_y2, fma2(y[e], nc1_2, D[i][e]), t[e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < P; ++e) D[i][e] = t[e];
+        }
+        if constexpr (!kJoin) {
+          put<T>(static_cast<T *>(p.dx) + row * p.dxs + c, D[i]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < P; ++e) t[e] = mul2(D[i][e], skip);
+          put<T>(static_cast<T *>(p.dx) + row * p.dxs + c, t);
+          f2 z[P], f[P];
+          ring.read(stage, kA, i, z);
+          if (!kKeep || p.row_gate)
+            branch_factor<T>(p, c, (p.row_gate ? row : (long long)group) * p.C, f);
+          else
+#pragma unroll
+            for (int e = 0; e < P; ++e) f[e] = fac[kKeep ? i : 0][e];
+#pragma unroll
+          for (int e = 0; e < P; ++e) {
+            z[e] = mul2(z[e], rstd_a2);
+            t[e] = mul2(D[i][e], z[e]);  // what A sums, or with the row's own gate below
+            D[i][e] = mul2(D[i][e], f[e]);
+            c2_2 = fma2(D[i][e], z[e], c2_2);
+          }
+          if (p.row_gate) {
+            f2 g[P], w[P];
+            load_w2<T>(p.gate, row * p.C + c, p.wf32, g);
+#pragma unroll
+            for (int e = 0; e < P; ++e) w[e] = f2_of(1.f, 1.f);
+            if (p.w_post) load_w2<T>(p.w_post, c, p.wf32, w);
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+              t[e] = mul2(t[e], branch);
+              float d0, d1;
+              f2_to(mul2(t[e], w[e]), d0, d1);
+              store_w<T>(p.dgate, row * p.C + c + 2 * e, p.wf32, d0);
+              store_w<T>(p.dgate, row * p.C + c + 2 * e + 1, p.wf32, d1);
+              t[e] = mul2(t[e], g[e]);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < P; ++e) accA[kJoin ? i : 0][e] = add2(accA[kJoin ? i : 0][e], t[e]);
+        }
+      }
+    }
+    if constexpr (kJoin) {
+      const float c2 = p.w_post ? row_sum(f2_sum(c2_2)) * inv_c : 0.f;
+      const float nc2 = -c2 * rstd_a;
+      const f2 nc2_2 = f2_of(nc2, nc2);
+#pragma unroll
+      for (int i = 0; i < kNV; ++i) {
+        const int c = (i * kNT + lane) * V;
+        if (in && c < p.C) {
+          if (p.w_post) {
+            f2 a[P];
+            ring.read(stage, kA, i, a);
+#pragma unroll
+            for (int e = 0; e < P; ++e)
+              D[i][e] = mul2(rstd_a2, fma2(a[e], nc2_2, D[i][e]));
+          }
+          put<T>(static_cast<T *>(p.da) + row * p.das + c, D[i]);
+        }
+      }
+    }
+    fetch(stage, row + kDepth * step);
+    stage = stage + 1 == kDepth ? 0 : stage + 1;
+  }
+  // this CTA's sums, one slot per CTA: the rows of a thread added in order, then the row groups
+  float *out = p.part + (size_t)blockIdx.x * kSums * p.C;
+  if constexpr (kRows == 1) {
+#pragma unroll
+    for (int i = 0; i < kNV; ++i) {
+      const int c = (i * kNT + lane) * V;
+      if (c < p.C)
+#pragma unroll
+        for (int e = 0; e < P; e += 2) {
+          *reinterpret_cast<ulonglong2 *>(out + c + 2 * e) =
+              make_ulonglong2(accN[i][e], accN[i][e + 1]);
+          if constexpr (kJoin)
+            *reinterpret_cast<ulonglong2 *>(out + p.C + c + 2 * e) =
+                make_ulonglong2(accA[i][e], accA[i][e + 1]);
+        }
+    }
+  } else {
+    float *dyn = reinterpret_cast<float *>(dyn4);
+    cp_async_wait<0>();
+#pragma unroll
+    for (int k = 0; k < kSums; ++k) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kNV; ++i) {
+        const int c = (i * kNT + lane) * V;
+        if (c < p.C)
+#pragma unroll
+          for (int e = 0; e < P; e += 2)
+            *reinterpret_cast<ulonglong2 *>(dyn + sub * p.C + c + 2 * e) =
+                k ? make_ulonglong2(accA[kJoin ? i : 0][e], accA[kJoin ? i : 0][e + 1])
+                  : make_ulonglong2(accN[i][e], accN[i][e + 1]);
+      }
+      __syncthreads();
+      for (int c = threadIdx.x; c < p.C; c += kThreads) {
+        float s = 0.f;
+#pragma unroll 8
+        for (int r = 0; r < kRows; ++r) s += dyn[r * p.C + c];
+        out[k * p.C + c] = s;
+      }
+    }
+  }
+}
+
 // Rows too long for registers and shared memory: passes over the row in the caches, the
 // column sums in this CTA's slot of `part`, each column always by the same thread.
 template <typename T, int V, bool kJoin>
@@ -601,9 +1027,33 @@ __global__ void __launch_bounds__(1024) bwd_sums(const NormBwdParams p) {
 }
 
 // ------------------------------------------------------------------------------- dispatch
-// Threads per row and vectors per thread by the number of vectors in a row: a warp up to 128
-// vectors (no exchange through shared memory), then as few threads as hold the row with at
-// most two vectors each, so that several rows are in flight on an SM.
+// Rows of n 16-byte vectors: as few lanes as hold a row with one vector each up to a warp, then
+// more vectors a lane up to 128 (no exchange through shared memory), then a CTA with two (four
+// past 1024) vectors a thread.  Rows that only elements address (V = 1) take the register form,
+// longer ones the long form.
+template <typename T, bool kJoin, typename F>
+cudaError_t ring_shape(int n, F go) {
+  if (n <= 4) return go(std::integral_constant<int, 4>(), std::integral_constant<int, 1>());
+  if (n <= 8) return go(std::integral_constant<int, 8>(), std::integral_constant<int, 1>());
+  if (n <= 16) return go(std::integral_constant<int, 16>(), std::integral_constant<int, 1>());
+  if (n <= 32) return go(std::integral_constant<int, 32>(), std::integral_constant<int, 1>());
+  if (n <= 64) return go(std::integral_constant<int, 32>(), std::integral_constant<int, 2>());
+  if (n <= 128) return go(std::integral_constant<int, 64>(), std::integral_constant<int, 2>());
+  if (n <= 256) return go(std::integral_constant<int, 128>(), std::integral_constant<int, 2>());
+  if (n <= 512) return go(std::integral_constant<int, 256>(), std::integral_constant<int, 2>());
+  if (n <= 1024) return go(std::integral_constant<int, 512>(), std::integral_constant<int, 2>());
+  return go(std::integral_constant<int, 512>(), std::integral_constant<int, 4>());
+}
+
+template <typename K>
+cudaError_t ring_smem(K kernel, size_t smem) {
+  if (smem <= 32 * 1024) return cudaSuccess;  // (48 KB less what is static)
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+}
+
+// A forward's CTAs walk over the rows: about 1024 threads on each of 152 SMs.
+constexpr long long kRingCtas = 152;
+
 template <typename T, int V, bool kJoin>
 cudaError_t fwd(const NormFwdParams &p, cudaStream_t s) {
   const int n = (p.C + V - 1) / V;
@@ -611,29 +1061,26 @@ cudaError_t fwd(const NormFwdParams &p, cudaStream_t s) {
     kernel<<<(unsigned)((p.rows + rows - 1) / rows), threads, 0, s>>>(p);
     return cudaGetLastError();
   };
-  if (n <= 32) return go(fwd_rows<T, V, 32, 1, kJoin>, 256, 8);
-  if (n <= 64) return go(fwd_rows<T, V, 32, 2, kJoin>, 256, 8);
-  if (n <= 128) return go(fwd_rows<T, V, 32, 4, kJoin>, 256, 8);
-  if (n <= 256) return go(fwd_rows<T, V, 128, 2, kJoin>, 128, 1);
-  if (n <= 512) return go(fwd_rows<T, V, 256, 2, kJoin>, 256, 1);
-  if (n <= 1024) return go(fwd_rows<T, V, 512, 2, kJoin>, 512, 1);
-  if (n <= 2048) return go(fwd_rows<T, V, 512, 4, kJoin>, 512, 1);
-  return go(fwd_long<T, V, kJoin>, 512, 1);
-}
-
-// Shape of the backward for rows of n vectors: threads per row (0: the long form).
-struct BwdShape {
-  int nt, nv, smem;
-};
-inline BwdShape bwd_shape(int n) {
-  if (n <= 32) return {32, 1, 0};
-  if (n <= 64) return {32, 2, 0};
-  if (n <= 128) return {32, 4, 0};
-  if (n <= 256) return {128, 2, 0};
-  if (n <= 512) return {256, 2, 0};
-  if (n <= 1024) return {512, 2, 0};
-  if (n <= 2048) return {512, 4, 1};
-  return {0, 0, 0};
+  if (n > 2048) return go(fwd_long<T, V, kJoin>, 512, 1);
+  if constexpr (V > 1) {
+    return ring_shape<T, kJoin>(n, [&](auto nt, auto nv) {
+      constexpr int kNT = decltype(nt)::value, kNV = decltype(nv)::value;
+      constexpr int kThreads = kRingThreads<kNT>, kRows = kThreads / kNT;
+      constexpr int kDepth = kNV == 4 ? 2 : 3;
+      const auto kernel = fwd_ring<T, kNT, kNV, kJoin, kDepth>;
+      const size_t smem = (size_t)kDepth * (kJoin ? 2 : 1) * kNV * kThreads * 16;
+      const cudaError_t e = ring_smem(kernel, smem);
+      if (e != cudaSuccess) return e;
+      const long long need = (p.rows + kRows - 1) / kRows;
+      const long long most = kRingCtas * (1024 / kThreads > 0 ? 1024 / kThreads : 1);
+      kernel<<<(unsigned)(need < most ? need : most), kThreads, smem, s>>>(p);
+      return cudaGetLastError();
+    });
+  } else {
+    if (n <= 128) return go(fwd_rows<T, V, 32, 4, kJoin>, 256, 8);
+    if (n <= 512) return go(fwd_rows<T, V, 256, 2, kJoin>, 256, 1);
+    return go(fwd_rows<T, V, 512, 4, kJoin>, 512, 1);
+  }
 }
 
 template <typename T, int V, bool kJoin>
@@ -641,33 +1088,31 @@ cudaError_t bwd(const NormBwdParams &p, cudaStream_t s) {
   const unsigned grid = (unsigned)(p.groups * p.ctas);
   constexpr int kSums = kJoin ? 2 : 1;
   auto go = [&](auto kernel, int threads, size_t smem) {
-    if (smem > 48 * 1024) {
-      const cudaError_t e =
-          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-      if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = ring_smem(kernel, smem);
+    if (e != cudaSuccess) return e;
     kernel<<<grid, threads, smem, s>>>(p);
     return cudaGetLastError();
   };
   const int n = (p.C + V - 1) / V;
-  const size_t warps = (size_t)8 * p.C * 4;  // the rows of a CTA side by side
   cudaError_t e;
-  if (n <= 32)
-    e = go(bwd_rows<T, V, 32, 1, kJoin, false>, 256, warps);
-  else if (n <= 64)
-    e = go(bwd_rows<T, V, 32, 2, kJoin, false>, 256, warps);
-  else if (n <= 128)
-    e = go(bwd_rows<T, V, 32, 4, kJoin, false>, 256, warps);
-  else if (n <= 256)
-    e = go(bwd_rows<T, V, 128, 2, kJoin, false>, 128, 0);
-  else if (n <= 512)
-    e = go(bwd_rows<T, V, 256, 2, kJoin, false>, 256, 0);
-  else if (n <= 1024)
-    e = go(bwd_rows<T, V, 512, 2, kJoin, false>, 512, 0);
-  else if (n <= 2048)
-    e = go(bwd_rows<T, V, 512, 4, kJoin, true>, 512, (size_t)kSums * p.C * 4);
-  else
+  if (n > 2048) {
     e = go(bwd_long<T, V, kJoin>, 512, 0);
+  } else if constexpr (V > 1) {
+    e = ring_shape<T, kJoin>(n, [&](auto nt, auto nv) {
+      constexpr int kNT = decltype(nt)::value, kNV = decltype(nv)::value;
+      constexpr int kThreads = kRingThreads<kNT>;
+      constexpr int kDepth = kNV == 4 ? 1 : 3;
+      const size_t ring = (size_t)kDepth * (kJoin ? 4 : 3) * kNV * kThreads * 16;
+      const size_t sums = kThreads > kNT ? (size_t)(kThreads / kNT) * p.C * 4 : 0;
+      return go(bwd_ring<T, kNT, kNV, kJoin, kDepth>, kThreads, ring > sums ? ring : sums);
+    });
+  } else if (n <= 128) {
+    e = go(bwd_rows<T, V, 32, 4, kJoin, false>, 256, (size_t)8 * p.C * 4);
+  } else if (n <= 512) {
+    e = go(bwd_rows<T, V, 256, 2, kJoin, false>, 256, 0);
+  } else {
+    e = go(bwd_rows<T, V, 512, 4, kJoin, true>, 512, (size_t)kSums * p.C * 4);
+  }
   if (e != cudaSuccess) return e;
   bwd_sums<T, kJoin><<<(p.C + 31) / 32, 1024, 0, s>>>(p);
   return cudaGetLastError();
