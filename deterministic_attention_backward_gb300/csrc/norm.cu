@@ -18,16 +18,14 @@ int norm_bwd_ctas(long long rows, long long groups, int C, int elem_bytes, bool 
   int sms_share = 2, at_once = 1;  // CTAs on an SM, rows of a CTA at once
   if (!wide) {
     if (n <= 128) at_once = 8;
+  } else if (n <= 32) {
+    at_once = n <= 4 ? 64 : n <= 8 ? 32 : n <= 16 ? 16 : 8;
+    sms_share = join ? 2 : 4;
   } else if (n <= 64) {
-    const int lanes = n <= 4 ? 4 : n <= 8 ? 8 : n <= 16 ? 16 : 32;
-    at_once = 256 / lanes;
-    sms_share = join ? 2 : n <= 32 ? 4 : 3;
-  } else if (n <= 128) {
-    sms_share = 8;
-  } else if (n <= 256) {
-    sms_share = 4;
+    at_once = join ? 8 : 1;
+    sms_share = join ? 2 : 16;
   } else if (n <= 512) {
-    sms_share = join ? 2 : 3;
+    sms_share = n <= 128 ? 8 : n <= 256 ? 4 : 2;
   } else if (n <= 2048) {
     sms_share = 1;
   }

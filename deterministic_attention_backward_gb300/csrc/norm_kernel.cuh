@@ -519,11 +519,11 @@ __global__ void __launch_bounds__(kRingThreads<kNT>) fwd_ring(const NormFwdParam
   RowSum<kNT> row_sum{red};
   const Ring<T, kThreads, kNV, kJoin ? 2 : 1> ring(dyn4);
   const int lane = threadIdx.x % kNT;
-  const long long step = (long long)gridDim.x * kRows;
+  const long long step = (long long)gridDim.x * kRows, row1 = p.rows;
   long long row = (long long)blockIdx.x * kRows + threadIdx.x / kNT;
   const float inv_c = 1.f / (float)p.C;
   auto fetch = [&](int stage, long long r) {
-    if (r < p.rows) {
+    if (r < row1) {
 #pragma unroll
       for (int i = 0; i < kNV; ++i) {
         const int c = (i * kNT + lane) * V;
@@ -549,8 +549,8 @@ __global__ void __launch_bounds__(kRingThreads<kNT>) fwd_ring(const NormFwdParam
   const f2 skip = f2_of(p.skip, p.skip);
   int stage = 0;
   // a warp stays until its last row is done: the sums of rows take part in full
-  for (long long first = row - threadIdx.x % 32 / kNT; first < p.rows; first += step, row += step) {
-    const bool in = row < p.rows;
+  for (long long first = row - threadIdx.x % 32 / kNT; first < row1; first += step, row += step) {
+    const bool in = row < row1;
     const long long gate = kJoin && p.gate && in ? (unsigned)row / (unsigned)p.gate_rows : 0;
     if (kKeep && kJoin && gate != held) {
       held = gate;
@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(kRingThreads<kNT>) fwd_ring(const NormFwdParam
 }
 
 template <typename T, int kNT, int kNV, bool kJoin, int kDepth>
-__global__ void __launch_bounds__(kRingThreads<kNT>, kRingThreads<kNT> <= 256 ? 512 / kRingThreads<kNT> : 1)
+__global__ void __launch_bounds__(kRingThreads<kNT>, kJoin ? 512 / kRingThreads<kNT> : kNV == 1 ? 1024 / kRingThreads<kNT> : 1)
     bwd_ring(const NormBwdParams p) {
   constexpr int V = 16 / sizeof(T), P = V / 2, kThreads = kRingThreads<kNT>;
   constexpr int kRows = kThreads / kNT;
@@ -1027,22 +1027,32 @@ __global__ void __launch_bounds__(1024) bwd_sums(const NormBwdParams p) {
 }
 
 // ------------------------------------------------------------------------------- dispatch
-// Rows of n 16-byte vectors: as few lanes as hold a row with one vector each up to a warp, then
-// more vectors a lane up to 128 (no exchange through shared memory), then a CTA with two (four
-// past 1024) vectors a thread.  Rows that only elements address (V = 1) take the register form,
-// longer ones the long form.
-template <typename T, bool kJoin, typename F>
+// Rows of n 16-byte vectors: as few lanes as hold a row with one vector each up to a warp; then
+// two vectors a thread, but one for a plain norm's backward.  Rows that only elements address
+// (V = 1) take the register form, longer ones the long form.
+template <int kNT, int kNV>
+struct Shape {
+  static constexpr int nt = kNT, nv = kNV;
+};
+template <bool kOne, typename F>
 cudaError_t ring_shape(int n, F go) {
-  if (n <= 4) return go(std::integral_constant<int, 4>(), std::integral_constant<int, 1>());
-  if (n <= 8) return go(std::integral_constant<int, 8>(), std::integral_constant<int, 1>());
-  if (n <= 16) return go(std::integral_constant<int, 16>(), std::integral_constant<int, 1>());
-  if (n <= 32) return go(std::integral_constant<int, 32>(), std::integral_constant<int, 1>());
-  if (n <= 64) return go(std::integral_constant<int, 32>(), std::integral_constant<int, 2>());
-  if (n <= 128) return go(std::integral_constant<int, 64>(), std::integral_constant<int, 2>());
-  if (n <= 256) return go(std::integral_constant<int, 128>(), std::integral_constant<int, 2>());
-  if (n <= 512) return go(std::integral_constant<int, 256>(), std::integral_constant<int, 2>());
-  if (n <= 1024) return go(std::integral_constant<int, 512>(), std::integral_constant<int, 2>());
-  return go(std::integral_constant<int, 512>(), std::integral_constant<int, 4>());
+  if (n <= 4) return go(Shape<4, 1>());
+  if (n <= 8) return go(Shape<8, 1>());
+  if (n <= 16) return go(Shape<16, 1>());
+  if (n <= 32) return go(Shape<32, 1>());
+  if constexpr (kOne) {
+    if (n <= 64) return go(Shape<64, 1>());
+    if (n <= 128) return go(Shape<128, 1>());
+    if (n <= 256) return go(Shape<256, 1>());
+    if (n <= 512) return go(Shape<512, 1>());
+  } else {
+    if (n <= 64) return go(Shape<32, 2>());
+    if (n <= 128) return go(Shape<64, 2>());
+    if (n <= 256) return go(Shape<128, 2>());
+    if (n <= 512) return go(Shape<256, 2>());
+  }
+  if (n <= 1024) return go(Shape<512, 2>());
+  return go(Shape<512, 4>());
 }
 
 template <typename K>
@@ -1051,8 +1061,17 @@ cudaError_t ring_smem(K kernel, size_t smem) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
 }
 
-// A forward's CTAs walk over the rows: about 1024 threads on each of 152 SMs.
-constexpr long long kRingCtas = 152;
+// CTAs of `kernel` that the device holds at once (asked once: the same on every sm_103 device).
+template <typename K>
+int resident(K kernel, int threads, size_t smem) {
+  int dev = 0, sms = 0, each = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&each, kernel, threads, smem) != cudaSuccess ||
+      each < 1)
+    return 152;
+  return sms * each;
+}
 
 template <typename T, int V, bool kJoin>
 cudaError_t fwd(const NormFwdParams &p, cudaStream_t s) {
@@ -1063,8 +1082,8 @@ cudaError_t fwd(const NormFwdParams &p, cudaStream_t s) {
   };
   if (n > 2048) return go(fwd_long<T, V, kJoin>, 512, 1);
   if constexpr (V > 1) {
-    return ring_shape<T, kJoin>(n, [&](auto nt, auto nv) {
-      constexpr int kNT = decltype(nt)::value, kNV = decltype(nv)::value;
+    return ring_shape<false>(n, [&](auto shape) {
+      constexpr int kNT = decltype(shape)::nt, kNV = decltype(shape)::nv;
       constexpr int kThreads = kRingThreads<kNT>, kRows = kThreads / kNT;
       constexpr int kDepth = kNV == 4 ? 2 : 3;
       const auto kernel = fwd_ring<T, kNT, kNV, kJoin, kDepth>;
@@ -1072,7 +1091,7 @@ cudaError_t fwd(const NormFwdParams &p, cudaStream_t s) {
       const cudaError_t e = ring_smem(kernel, smem);
       if (e != cudaSuccess) return e;
       const long long need = (p.rows + kRows - 1) / kRows;
-      const long long most = kRingCtas * (1024 / kThreads > 0 ? 1024 / kThreads : 1);
+      static const int most = resident(kernel, kThreads, smem);
       kernel<<<(unsigned)(need < most ? need : most), kThreads, smem, s>>>(p);
       return cudaGetLastError();
     });
@@ -1098,8 +1117,8 @@ cudaError_t bwd(const NormBwdParams &p, cudaStream_t s) {
   if (n > 2048) {
     e = go(bwd_long<T, V, kJoin>, 512, 0);
   } else if constexpr (V > 1) {
-    e = ring_shape<T, kJoin>(n, [&](auto nt, auto nv) {
-      constexpr int kNT = decltype(nt)::value, kNV = decltype(nv)::value;
+    e = ring_shape<!kJoin>(n, [&](auto shape) {
+      constexpr int kNT = decltype(shape)::nt, kNV = decltype(shape)::nv;
       constexpr int kThreads = kRingThreads<kNT>;
       constexpr int kDepth = kNV == 4 ? 1 : 3;
       const size_t ring = (size_t)kDepth * (kJoin ? 4 : 3) * kNV * kThreads * 16;
