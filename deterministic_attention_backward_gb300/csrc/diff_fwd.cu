@@ -2,22 +2,25 @@
 // product and the weight's gradient need it) and both maps' LSE.
 //
 // One CTA per (batch, head pair, 128-row query tile).  The two maps are two independent online
-// softmaxes over the same KV blocks; a warpgroup owns each (thread = query row), so that while
-// one turns its scores into probabilities the tensor core runs the other's products:
+// softmaxes over the same KV blocks, two warpgroups each (thread = query row, 64 keys of a
+// block; they exchange their halves of the row's maximum through shared memory), so that while
+// one map's scores become probabilities the tensor core runs the other's products:
 //   Sm = Qm Km^T -> max, exp2, sum -> Pm (bf16, in TMEM over Sm) -> Om += Pm V
 // The running maximum of a row is only raised when a block exceeds it by 2^8 (the row's Om
 // and sum are then rescaled in place; no product on Om is in flight, the next Sm follows Pm V
-// in issue order).  P is rounded to bf16 for the tensor core, relative error 2^-9 per entry;
-// sums, maxima and accumulators are fp32.
+// in issue order).  P is rounded to bf16 for the tensor core, relative error 2^-8 at most per
+// entry; sums, maxima and accumulators are fp32.
 //
-// TMEM columns: S1 [0,128), S2 [128,256), O1 [256, 256+dv), O2 [256+dv, 256+2dv).
-// Warps 0-3 map 1, 4-7 map 2, 8 TMA producer, 9 MMA issuer.
+// TMEM columns: S1 [0,128), S2 [128,256), O1 [256, 256+dv), O2 [256+dv, 256+2dv); P over the
+// first half of the columns that its warpgroup reads.
+// Warps 0-7 map 1, 8-15 map 2, 16 TMA producer, 17 MMA issuer.
 #include "diff.cuh"
 
 namespace dash {
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kWarps = 16;
+constexpr int kThreads = (kWarps + 2) * 32;
 constexpr float kRaise = 8.f;  // log2 of how far a row's scores may pass its running maximum
 
 template <int d>
@@ -29,8 +32,9 @@ struct FwdL {
   static constexpr int kStageBytes = 2 * kTileBytes;  // K then V
   static constexpr int offQ = 0;
   static constexpr int offStage = kTileBytes;
-  static constexpr int offSum = offStage + kStages * kStageBytes;  // float [2][128]
-  static constexpr int offBar = offSum + 2 * kTile * 4;
+  static constexpr int offSum = offStage + kStages * kStageBytes;  // float [2][2][128]
+  static constexpr int offMax = offSum + 4 * kTile * 4;            // float [2][2][2][128]
+  static constexpr int offBar = offMax + 8 * kTile * 4;
   // q_full, kv_full[2], kv_empty[2], s_full[2], p_full[2], o_full, drain
   static constexpr int kNumBars = 1 + 2 * kStages + 4 + 2;
   static constexpr int offMisc = offBar + kNumBars * 8;
@@ -76,19 +80,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int m = 0; m < 2; ++m) {
       mbar_init(&s_full[m], 1);
-      mbar_init(&p_full[m], 4);
+      mbar_init(&p_full[m], kWarps / 2);
     }
     mbar_init(o_full, 1);
     mbar_init(drain, 1);
     *s_abort = 0;
     fence_mbar_init();
   }
-  if (warp == 8 && lane == 0) {
+  if (warp == kWarps && lane == 0) {
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
-  if (warp == 9) {
+  if (warp == kWarps + 1) {
     tmem_alloc(s_tmem, L::kTmemCols);
     tmem_relinquish();
   }
@@ -97,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
 
-  if (warp == 8 && lane == 0) {
+  if (warp == kWarps && lane == 0) {
     // ------------------------------------------------------------------ TMA producer
     int last[L::kStages];
     for (int s = 0; s < L::kStages; ++s) last[s] = -1;
@@ -126,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int s = 0; s < L::kStages; ++s)
         if (last[s] >= 0) mbar_wait_drain(&kv_full[s], (uint32_t)last[s], 100000000ull);
     }
-  } else if (warp == 9) {
+  } else if (warp == kWarps + 1) {
     // ------------------------------------------------------------------ MMA issuer
     // The whole warp runs the loop, so that descriptors and control flow stay warp-uniform;
     // one elected lane issues.
@@ -160,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          mma_ts_l(lead, tmem + L::tO + m * DV, tmem + L::tS + m * 128 + 8 * k,
+          mma_ts_l(lead, tmem + L::tO + m * DV, tmem + L::tS + m * 128 + 64 * (k >> 2) + 8 * (k & 3),
                    desc_of(loV + ((k * 2048) >> 4)), kIdescO, (j > 0 || k > 0) ? 1u : 0u);
         if (m == 1) mma_commit_l(lead, &kv_empty[s]);
         if (j1 < nkv) {
@@ -176,14 +180,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) mma_commit_l(lead, o_full);
     mma_commit_l(lead, drain);
     mbar_wait_drain(drain, 0, 100000000ull);
-  } else if (warp < 8) {
+  } else if (warp < kWarps) {
     // ------------------------------------------------------------------ softmax of map m
-    const int m = warp >> 2;
+    const int wg = warp >> 2, m = wg >> 1, half = wg & 1;
     const int quad = warp & 3;
     const int r = quad * 32 + lane;  // query row within the tile = TMEM lane
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    const uint32_t tS = tmem + lane_off + L::tS + m * 128, tO = tmem + lane_off + L::tO + m * DV;
-    float ref = -INFINITY, l = 0.f;  // running maximum (log2 units) and sum
+    const uint32_t tS = tmem + lane_off + L::tS + m * 128 + 64 * half;
+    const uint32_t tO = tmem + lane_off + L::tO + m * DV + half * d;  // this warpgroup's columns
+    float *s_max = reinterpret_cast<float *>(smem + L::offMax) + m * 4 * kTile + r;
+    const f2 c2 = f2_of(p.scale_log2, p.scale_log2);
+    float ref = -INFINITY;                            // running maximum (log2 units)
+    f2 l[2] = {f2_of(0.f, 0.f), f2_of(0.f, 0.f)};  // sum over this warpgroup's keys
     bool ok = true;
     for (int j = 0; j < nkv; ++j) {
       if (!wait_warp(&s_full[m], j & 1, ab)) {
@@ -191,34 +199,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      uint32_t s[4][32];
+      // of this thread's 64 keys, those that the row sees
+      const int limit = min(p.S - j * kTile, p.causal && j == i ? r + 1 : kTile) - 64 * half;
+      const bool cut = __any_sync(0xffffffffu, limit < 64);
+      // The scores are read twice, by 32 columns: once for the maximum, once for the
+      // probabilities (held between, they would not fit the registers of 18 warps).
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, s[c]);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld_wait_for(s[c]);
-      const int limit = min(p.S - j * kTile, p.causal && j == i ? r + 1 : kTile);  // keys seen
-      if (__any_sync(0xffffffffu, limit < kTile)) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
+      for (int c = 0; c < 2; ++c) {
+        uint32_t s[32];
+        tmem_ld32(tS + 32 * c, s);
+        tmem_ld_wait_for(s);
+        if (cut) {
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            if (32 * c + e >= limit) s[c][e] = __float_as_uint(-INFINITY);
+            if (32 * c + e >= limit) s[e] = __float_as_uint(-INFINITY);
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e]));
       }
-      float mx = -INFINITY;
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(s[c][e]));
-      mx *= p.scale_log2;
+      float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+      s_max[((j & 1) * 2 + half) * kTile] = top;
+      named_bar_sync(1 + m, kWarps * 16);
+      top = fmaxf(top, s_max[((j & 1) * 2 + (half ^ 1)) * kTile]);
       if (j == 0) {
-        ref = mx;
-      } else if (__any_sync(0xffffffffu, mx > ref + kRaise)) {
-        const float top = fmaxf(ref, mx);
-        const float by = ex2_approx(ref - top);
         ref = top;
-        l *= by;
+      } else if (__any_sync(0xffffffffu, top > ref + kRaise)) {
+        // (both warpgroups of a map take the same decision from the same values)
+        top = fmaxf(ref, top);
+        const float by = ex2_approx(ref - top);
+        const f2 by2 = f2_of(by, by);
+        ref = top;
+        l[0] = mul2(l[0], by2);
+        l[1] = mul2(l[1], by2);
 #pragma unroll 1
-        for (int c = 0; c < DV / 32; ++c) {
+        for (int c = 0; c < d / 32; ++c) {
           uint32_t o[32];
           tmem_ld32(tO + 32 * c, o);
           tmem_ld_wait_for(o);
@@ -228,21 +243,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_st_wait();
       }
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      const f2 nref2 = f2_of(-ref, -ref);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t pk[16];
+      for (int c = 0; c < 2; ++c) {
+        uint32_t s[32], pk[16];
+        tmem_ld32(tS + 32 * c, s);
+        tmem_ld_wait_for(s);
+        if (cut) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (32 * c + e >= limit) s[e] = __float_as_uint(-INFINITY);
+        }
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float a = ex2_approx(fmaf(__uint_as_float(s[c][2 * e]), p.scale_log2, -ref));
-          const float z = ex2_approx(fmaf(__uint_as_float(s[c][2 * e + 1]), p.scale_log2, -ref));
-          sum[(2 * e) & 3] += a;
-          sum[(2 * e + 1) & 3] += z;
-          pk[e] = pack_bf16(a, z);
+          const f2 P = ex2_2(fma2(f2_of(s[2 * e], s[2 * e + 1]), c2, nref2));
+          l[e & 1] = add2(l[e & 1], P);
+          pk[e] = pack_bf16(P);
         }
         tmem_st16(tS + 16 * c, pk);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -251,43 +270,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------ epilogue
     const int row = i * kTile + r;
     const bool row_ok = row < p.S;
-    s_sum[m * kTile + r] = 1.f / l;
-    if (ok && row_ok)
-      p.lse[((size_t)b * 2 * p.H + 2 * h + m) * p.S + row] = (ref + log2f(l)) * kLn2;
-    named_bar_sync(1, 256);
+    s_sum[(m * 2 + half) * kTile + r] = f2_sum(add2(l[0], l[1]));
+    named_bar_sync(3, kWarps * 32);
+    const float l1 = s_sum[r] + s_sum[kTile + r], l2 = s_sum[2 * kTile + r] + s_sum[3 * kTile + r];
+    if (ok && row_ok && half == 0)
+      p.lse[((size_t)b * 2 * p.H + 2 * h + m) * p.S + row] = (ref + log2f(m ? l2 : l1)) * kLn2;
     if (ok && wait_warp(o_full, 0, ab)) {
       tc_fence_after();
-      // this warpgroup's half of the columns of both accumulators
-      const float n1 = s_sum[r], n2 = s_sum[kTile + r];
+      // this warpgroup's quarter of the columns of both accumulators
+      const float n1 = 1.f / l1, n2 = 1.f / l2;
       const size_t at = (size_t)b * p.S + row;
       const float lam =
           row_ok ? lam_at(p.lam, p.lam_f32, p.lam_token ? at * p.H + h : (size_t)h) : 0.f;
-      const uint32_t t1 = tmem + lane_off + L::tO + m * d;
-      const size_t out = (at * p.H + h) * DV + m * d;
-#pragma unroll 1
-      for (int c = 0; c < d / 32; ++c) {
-        uint32_t o1[32], o2[32];
-        tmem_ld32(t1 + 32 * c, o1);
-        tmem_ld32(t1 + DV + 32 * c, o2);
-        tmem_ld_wait_for(o1);
-        tmem_ld_wait_for(o2);
+      const uint32_t t1 = tmem + lane_off + L::tO + wg * (d / 2);
+      const size_t out = (at * p.H + h) * DV + wg * (d / 2);
+      uint32_t o1[d / 2], o2[d / 2];
+      if constexpr (d == 64) {
+        tmem_ld32(t1, o1);
+        tmem_ld32(t1 + DV, o2);
+      } else {
+        tmem_ld16(t1, o1);
+        tmem_ld16(t1 + DV, o2);
+      }
+      tmem_ld_wait_for(o1);
+      tmem_ld_wait_for(o2);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float z = __uint_as_float(o2[e]) * n2;
-          o2[e] = __float_as_uint(z);
-          o1[e] = __float_as_uint(fmaf(-lam, z, __uint_as_float(o1[e]) * n1));
-        }
-        if (row_ok) {
-          store_row(p.o + out + 32 * c, o1, 1.f);
-          store_row(p.o2 + out + 32 * c, o2, 1.f);
-        }
+      for (int e = 0; e < d / 2; ++e) {
+        const float z = __uint_as_float(o2[e]) * n2;
+        o2[e] = __float_as_uint(z);
+        o1[e] = __float_as_uint(fmaf(-lam, z, __uint_as_float(o1[e]) * n1));
+      }
+      if (row_ok) {
+        store_row(p.o + out, o1, 1.f);
+        store_row(p.o2 + out, o2, 1.f);
       }
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kWarps + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, L::kTmemCols);
   }
