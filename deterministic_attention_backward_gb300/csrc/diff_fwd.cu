@@ -35,8 +35,8 @@ struct FwdL {
   static constexpr int offSum = offStage + kStages * kStageBytes;  // float [2][2][128]
   static constexpr int offMax = offSum + 4 * kTile * 4;            // float [2][2][2][128]
   static constexpr int offBar = offMax + 8 * kTile * 4;
-  // q_full, kv_full[2], kv_empty[2], s_full[2], p_full[2], o_full, drain
-  static constexpr int kNumBars = 1 + 2 * kStages + 4 + 2;
+  // q_full, k_full[], k_empty[], v_full[], v_empty[], s_full[2], p_full[2], o_full, drain
+  static constexpr int kNumBars = 1 + 4 * kStages + 4 + 2;
   static constexpr int offMisc = offBar + kNumBars * 8;
   static constexpr int kBytes = offMisc + 16;
   static constexpr uint32_t tS = 0, tO = 256, kTmemCols = 512;
@@ -55,9 +55,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) atomicOr(p.status, kErrSmemAlign);
     return;
   }
-  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::offBar);
-  uint64_t *q_full = bars, *kv_full = bars + 1, *kv_empty = kv_full + L::kStages;
-  uint64_t *s_full = kv_empty + L::kStages, *p_full = s_full + 2, *o_full = p_full + 2;
+  uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + L::offBar);
+  uint64_t *k_full = q_full + 1, *k_empty = k_full + L::kStages;
+  uint64_t *v_full = k_empty + L::kStages, *v_empty = v_full + L::kStages;
+  uint64_t *s_full = v_empty + L::kStages, *p_full = s_full + 2, *o_full = p_full + 2;
   uint64_t *drain = o_full + 1;
   float *s_sum = reinterpret_cast<float *>(smem + L::offSum);
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + L::offMisc);
@@ -75,8 +76,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
     for (int s = 0; s < L::kStages; ++s) {
-      mbar_init(&kv_full[s], 1);
-      mbar_init(&kv_empty[s], 1);
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
     }
     for (int m = 0; m < 2; ++m) {
       mbar_init(&s_full[m], 1);
@@ -103,32 +106,40 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kWarps && lane == 0) {
     // ------------------------------------------------------------------ TMA producer
-    int last[L::kStages];
-    for (int s = 0; s < L::kStages; ++s) last[s] = -1;
+    // K is free again once S2 of its block is formed, long before V
     bool ok = true;
+    int nk = 0, nv = 0;  // blocks brought in
     mbar_arrive_expect_tx(q_full, L::kTileBytes);
     for (int bx = 0; bx < L::kBoxes; ++bx)
       tma_load_4d(smem + L::offQ + bx * kBoxBytes, &tm_q, q_full, bx * kBoxCols, h, i * kTile, b);
     for (int j = 0; j < nkv; ++j) {
       const int s = j % L::kStages;
       const uint32_t ph = (j / L::kStages) & 1;
-      if (!mbar_wait(&kv_empty[s], ph ^ 1, ab)) {
+      uint8_t *sk = smem + L::offStage + s * L::kStageBytes;
+      if (!mbar_wait(&k_empty[s], ph ^ 1, ab)) {
         ok = false;
         break;
       }
-      mbar_arrive_expect_tx(&kv_full[s], L::kStageBytes);
-      uint8_t *sk = smem + L::offStage + s * L::kStageBytes;
+      mbar_arrive_expect_tx(&k_full[s], L::kTileBytes);
       for (int bx = 0; bx < L::kBoxes; ++bx)
-        tma_load_4d(sk + bx * kBoxBytes, &tm_k, &kv_full[s], bx * kBoxCols, hkv, j * kTile, b);
+        tma_load_4d(sk + bx * kBoxBytes, &tm_k, &k_full[s], bx * kBoxCols, hkv, j * kTile, b);
+      ++nk;
+      if (!mbar_wait(&v_empty[s], ph ^ 1, ab)) {
+        ok = false;
+        break;
+      }
+      mbar_arrive_expect_tx(&v_full[s], L::kTileBytes);
       for (int bx = 0; bx < L::kBoxes; ++bx)
-        tma_load_4d(sk + L::kTileBytes + bx * kBoxBytes, &tm_v, &kv_full[s], bx * kBoxCols, hkv,
+        tma_load_4d(sk + L::kTileBytes + bx * kBoxBytes, &tm_v, &v_full[s], bx * kBoxCols, hkv,
                     j * kTile, b);
-      last[s] = (int)ph;
+      ++nv;
     }
-    if (!ok) {
+    if (!ok) {  // leave no copy in flight into shared memory
       mbar_wait_drain(q_full, 0, 100000000ull);
-      for (int s = 0; s < L::kStages; ++s)
-        if (last[s] >= 0) mbar_wait_drain(&kv_full[s], (uint32_t)last[s], 100000000ull);
+      for (int j = max(0, nk - L::kStages); j < nk; ++j)
+        mbar_wait_drain(&k_full[j % L::kStages], (j / L::kStages) & 1, 100000000ull);
+      for (int j = max(0, nv - L::kStages); j < nv; ++j)
+        mbar_wait_drain(&v_full[j % L::kStages], (j / L::kStages) & 1, 100000000ull);
     }
   } else if (warp == kWarps + 1) {
     // ------------------------------------------------------------------ MMA issuer
@@ -146,8 +157,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_ss_l(lead, tmem + L::tS + m * 128, desc_of(loQ + off), desc_of(loK + off), kIdescS, k > 0);
       }
       mma_commit_l(lead, &s_full[m]);
+      if (m == 1) mma_commit_l(lead, &k_empty[j % L::kStages]);
     };
-    bool ok = wait_warp(q_full, 0, ab) && wait_warp(&kv_full[0], 0, ab);
+    auto k_there = [&](int j) {
+      return wait_warp(&k_full[j % L::kStages], (j / L::kStages) & 1, ab);
+    };
+    bool ok = wait_warp(q_full, 0, ab) && k_there(0);
     if (ok) {
       tc_fence_after();
       issue_s(0, 0);
@@ -157,6 +172,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int s = j % L::kStages, j1 = j + 1;
       const uint32_t loV =
           desc_lo(sbase + L::offStage + s * L::kStageBytes + L::kTileBytes, kBoxBytes);
+      // what the products read first: it is there long before the probabilities
+      ok = wait_warp(&v_full[s], (j / L::kStages) & 1, ab) && (j1 == nkv || k_there(j1));
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         if (ok && !wait_warp(&p_full[m], j & 1, ab)) ok = false;
@@ -166,15 +183,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < 8; ++k)
           mma_ts_l(lead, tmem + L::tO + m * DV, tmem + L::tS + m * 128 + 64 * (k >> 2) + 8 * (k & 3),
                    desc_of(loV + ((k * 2048) >> 4)), kIdescO, (j > 0 || k > 0) ? 1u : 0u);
-        if (m == 1) mma_commit_l(lead, &kv_empty[s]);
-        if (j1 < nkv) {
-          if (m == 0 && !wait_warp(&kv_full[j1 % L::kStages], (j1 / L::kStages) & 1, ab)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          issue_s(j1, m);
-        }
+        if (j1 < nkv) issue_s(j1, m);
+        if (m == 1) mma_commit_l(lead, &v_empty[s]);
       }
     }
     if (ok) mma_commit_l(lead, o_full);
