@@ -35,8 +35,8 @@ struct FwdL {
   static constexpr int offSum = offStage + kStages * kStageBytes;  // float [2][2][128]
   static constexpr int offMax = offSum + 4 * kTile * 4;            // float [2][2][2][128]
   static constexpr int offBar = offMax + 8 * kTile * 4;
-  // q_full, k_full[], k_empty[], v_full[], v_empty[], s_full[2], p_full[2], o_full, drain
-  static constexpr int kNumBars = 1 + 4 * kStages + 4 + 2;
+  // q_full, k_full[], k_empty[], v_full[], v_empty[], s_full[2], p_full[2][2], o_full, drain
+  static constexpr int kNumBars = 1 + 4 * kStages + 6 + 2;
   static constexpr int offMisc = offBar + kNumBars * 8;
   static constexpr int kBytes = offMisc + 16;
   static constexpr uint32_t tS = 0, tO = 256, kTmemCols = 512;
@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + L::offBar);
   uint64_t *k_full = q_full + 1, *k_empty = k_full + L::kStages;
   uint64_t *v_full = k_empty + L::kStages, *v_empty = v_full + L::kStages;
-  uint64_t *s_full = v_empty + L::kStages, *p_full = s_full + 2, *o_full = p_full + 2;
+  uint64_t *s_full = v_empty + L::kStages, *p_full = s_full + 2, *o_full = p_full + 4;
   uint64_t *drain = o_full + 1;
   float *s_sum = reinterpret_cast<float *>(smem + L::offSum);
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + L::offMisc);
@@ -83,7 +83,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int m = 0; m < 2; ++m) {
       mbar_init(&s_full[m], 1);
-      mbar_init(&p_full[m], kWarps / 2);
+      mbar_init(&p_full[2 * m], kWarps / 2);
+      mbar_init(&p_full[2 * m + 1], kWarps / 2);
     }
     mbar_init(o_full, 1);
     mbar_init(drain, 1);
@@ -176,13 +177,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = wait_warp(&v_full[s], (j / L::kStages) & 1, ab) && (j1 == nkv || k_there(j1));
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        if (ok && !wait_warp(&p_full[m], j & 1, ab)) ok = false;
-        if (!ok) break;
-        tc_fence_after();
+        // the first 32 keys of both warpgroups as soon as they are there, then the others
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_ts_l(lead, tmem + L::tO + m * DV, tmem + L::tS + m * 128 + 64 * (k >> 2) + 8 * (k & 3),
-                   desc_of(loV + ((k * 2048) >> 4)), kIdescO, (j > 0 || k > 0) ? 1u : 0u);
+        for (int c = 0; c < 2; ++c) {
+          if (ok) ok = wait_warp(&p_full[2 * m + c], j & 1, ab);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int k = 4 * (e >> 1) + 2 * c + (e & 1);
+            mma_ts_l(lead, tmem + L::tO + m * DV,
+                     tmem + L::tS + m * 128 + 64 * (k >> 2) + 8 * (k & 3),
+                     desc_of(loV + ((k * 2048) >> 4)), kIdescO, (j > 0 || c > 0 || e > 0) ? 1u : 0u);
+          }
+        }
+        if (!ok) break;
         if (j1 < nkv) issue_s(j1, m);
         if (m == 1) mma_commit_l(lead, &v_empty[s]);
       }
@@ -271,11 +280,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           pk[e] = pack_bf16(P);
         }
         tmem_st16(tS + 16 * c, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[2 * m + c]);
       }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[m]);
     }
     // ------------------------------------------------------------------ epilogue
     const int row = i * kTile + r;
