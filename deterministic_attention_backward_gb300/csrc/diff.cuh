@@ -46,6 +46,10 @@ struct DiffBwdParams {
   int lam_f32, lam_token;
   unsigned long long wait_ns;
   float scale_log2, scale;
+  // dK/dV's kernel: the first kv_whole tiles are a CTA each, the others kv_pieces CTAs each,
+  // whose fp32 sums [piece][4d/4][128][4] of kv_part diff_join_kernel adds
+  int kv_whole, kv_pieces;
+  float *kv_part;
 };
 
 cudaError_t launch_diff_fwd(int d, const CUtensorMap &tq, const CUtensorMap &tk,
@@ -143,12 +147,6 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[8]) {
                : "memory");
 }
 
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "

@@ -482,11 +482,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = warp_id(), lane = lane_id();
 
   const int heads = p.B * p.Hkv;
-  const int j = blockIdx.x / heads;  // causal: block 0 meets the most queries, first
-  const int bh = blockIdx.x % heads;
+  int tile = blockIdx.x, part = -1;  // part: where a piece's sums go
+  if (tile >= p.kv_whole) {
+    part = tile - p.kv_whole;
+    tile = p.kv_whole + part / p.kv_pieces;
+  }
+  const int j = tile / heads;  // causal: block 0 meets the most queries, first
+  const int bh = tile % heads;
   const int hkv = bh % p.Hkv, b = bh / p.Hkv;
   const int i0 = p.causal ? j : 0, tiles = p.N - i0;
-  const int steps = 2 * p.G * tiles;
+  int first_step = 0, steps = 2 * p.G * tiles;  // of the tile, and how many from there
+  if (part >= 0) {
+    const int piece = part % p.kv_pieces, all = steps;
+    first_step = all * piece / p.kv_pieces;
+    steps = all * (piece + 1) / p.kv_pieces - first_step;
+  }
+  if (steps == 0) return;  // (diff_join_kernel leaves such a piece out)
 
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
@@ -538,7 +549,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = false;
         break;
       }
-      const int h = hkv * p.G + (n >> 1) / tiles, i = i0 + (n >> 1) % tiles, u = n & 1;
+      const int at = first_step + n;
+      const int h = hkv * p.G + (at >> 1) / tiles, i = i0 + (at >> 1) % tiles, u = at & 1;
       mbar_arrive_expect_tx(&q_full[s], L::kStageBytes + L::kRowBytes);
       uint8_t *sq = smem + L::offStage + s * L::kStageBytes;
       for (int bx = 0; bx < L::kBoxes; ++bx) {
@@ -682,10 +694,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto hide = [&](uint32_t (&x)[8], int n, int half, uint32_t with) {
 #pragma unroll
       for (int e = 0; e < 8; ++e)  // key - query of the element
-        if (ahead - kStep * (n & 1) + 16 * half + 8 * ((e >> 1) & 1) - 8 * (e >> 2) - (e & 1) > 0)
+        if (ahead - kStep * ((first_step + n) & 1) + 16 * half + 8 * ((e >> 1) & 1) - 8 * (e >> 2) - (e & 1) > 0)
           x[e] = with;
     };
-    auto diagonal = [&](int n) { return p.causal && (n >> 1) % tiles == 0; };
+    auto diagonal = [&](int n) { return p.causal && ((first_step + n) >> 1) % tiles == 0; };
     uint32_t slot1 = t0, slot2 = t0 + 128, spare = t0 + 192;
     bool ok = true;
     for (int n = 0; n < steps; ++n) {
@@ -798,7 +810,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t v[32];
         tmem_ld32(from + 32 * c, v);
         tmem_ld_wait_for(v);
-        if (key < p.S) store_row(out + 32 * c, v, wg < 2 ? p.scale : 1.f);
+        if (part >= 0) {  // dK1, dK2, dV side by side
+          float4 *sum = reinterpret_cast<float4 *>(p.kv_part) +
+                        ((size_t)part * d + wg * (d / 4) + 8 * c) * kTile + r;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            sum[e * kTile] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
+                                         __uint_as_float(v[4 * e + 2]),
+                                         __uint_as_float(v[4 * e + 3]));
+        } else if (key < p.S) {
+          store_row(out + 32 * c, v, wg < 2 ? p.scale : 1.f);
+        }
       }
     }
   }
@@ -809,6 +831,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, L::kTmemCols);
   }
+}
+
+// dK and dV of the tiles that were cut: their pieces' sums, added in order.  One CTA per tile and
+// 8 columns, thread = key row.
+template <int d>
+__global__ void __launch_bounds__(kTile) diff_join_kernel(const DiffBwdParams p) {
+  const int heads = p.B * p.Hkv, tile = p.kv_whole + blockIdx.x, c8 = blockIdx.y;
+  const int j = tile / heads, bh = tile % heads, hkv = bh % p.Hkv, b = bh / p.Hkv;
+  const int all = 2 * p.G * (p.N - (p.causal ? j : 0));
+  const int key = j * kTile + threadIdx.x;
+  const float4 *part = reinterpret_cast<const float4 *>(p.kv_part) +
+                       ((size_t)blockIdx.x * p.kv_pieces * d + 2 * c8) * kTile + threadIdx.x;
+  float v[8] = {};
+#pragma unroll 4
+  for (int k = 0; k < p.kv_pieces; ++k) {
+    if (all * k / p.kv_pieces == all * (k + 1) / p.kv_pieces) continue;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const float4 x = part[((size_t)k * d + u) * kTile];
+      v[4 * u] += x.x, v[4 * u + 1] += x.y, v[4 * u + 2] += x.z, v[4 * u + 3] += x.w;
+    }
+  }
+  if (key >= p.S) return;
+  const int col = 8 * c8, m = col / d;  // dK1, dK2 and the halves of dV
+  const size_t at = (size_t)b * p.S + key;
+  __nv_bfloat16 *out = m < 2 ? p.dk + (at * 2 * p.Hkv + 2 * hkv) * d + col
+                             : p.dv + (at * p.Hkv + hkv) * 2 * d + (col - 2 * d);
+  uint32_t bits[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) bits[e] = __float_as_uint(v[e]);
+  store_row(out, bits, m < 2 ? p.scale : 1.f);
 }
 
 template <int d>
@@ -827,8 +880,10 @@ cudaError_t launch_t(const CUtensorMap &tq, const CUtensorMap &tk, const CUtenso
   diff_rows_kernel<d><<<tiles, 256, 0, s>>>(p);
   diff_dq_kernel<d><<<tiles, kThreads, LQ::kBytes, s>>>(tq, tk, tv, tdo, p);
   if (!p.lam_token) diff_dlam_kernel<<<p.H, 256, 0, s>>>(p);
-  diff_dkv_kernel<d>
-      <<<(unsigned)p.B * p.Hkv * p.N, kThreads, LK::kBytes, s>>>(tq, tk, tv, tdo, p);
+  const unsigned cut = (unsigned)p.B * p.Hkv * p.N - p.kv_whole;  // tiles in pieces
+  diff_dkv_kernel<d><<<p.kv_whole + cut * p.kv_pieces, kThreads, LK::kBytes, s>>>(tq, tk, tv,
+                                                                                  tdo, p);
+  if (cut) diff_join_kernel<d><<<dim3(cut, d / 2), kTile, 0, s>>>(p);
   return cudaGetLastError();
 }
 

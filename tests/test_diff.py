@@ -154,6 +154,16 @@ def test_heads_and_weights(L, lam, B, S, H, Hkv, causal, d):
 @pytest.mark.gpu
 @pytest.mark.parametrize("d", [32, 64])
 @pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("B,S,H,Hkv", [(1, 1300, 16, 16), (1, 2600, 1, 1), (1, 1500, 12, 3),
+                                       (2, 900, 20, 20)])
+def test_tiles_in_pieces(L, B, S, H, Hkv, causal, d):
+    """Key tiles of which some or all are cut, into more pieces than the last ones have steps."""
+    run(B, S, H, Hkv, d, causal, "head-bf16", seed=S)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [32, 64])
+@pytest.mark.parametrize("causal", [False, True])
 def test_scale_and_spread(L, causal, d):
     """A scale of one's own, flat and peaked maps: the running maximum stays and is raised."""
     run(1, 300, 2, 1, d, causal, "head-bf16", scale=0.07)
