@@ -137,13 +137,14 @@ dash_status_t dash_diff_fwd(const void *q, const void *k, const void *v, const v
   p.lse = lse;
   p.lam = lam;
   p.status = static_cast<uint32_t *>(workspace);
+  p.taken = p.status + 32;  // a sector of its own in the status block
   p.B = B, p.S = S, p.H = H, p.Hkv = Hkv, p.G = group, p.N = tiles(S);
   p.causal = mask == DASH_MASK_CAUSAL;
   p.lam_f32 = lam_dtype == DASH_FP32;
   p.lam_token = lam_per_token != 0;
   p.wait_ns = g_wait_ns.load();
   p.scale_log2 = (scale > 0.f ? scale : 1.0f / std::sqrt((float)d)) * kLog2e;
-  return launch_diff_fwd(d, tq, tk, tv, p, s) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+  return launch_diff_fwd(d, tq, tk, tv, p, dev.sms, s) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
 }
 
 dash_status_t dash_diff_bwd(const void *q, const void *k, const void *v, const void *o,

@@ -18,6 +18,7 @@ struct DiffFwdParams {
   float *lse;             // [B,2H,S]
   const void *lam;        // [H] or [B,S,H], bf16 or fp32
   uint32_t *status;
+  uint32_t *taken;        // tiles that CTAs have taken beside their first (cleared)
   int B, S, H, Hkv, G, N, causal;
   int lam_f32, lam_token;
   unsigned long long wait_ns;
@@ -53,7 +54,8 @@ struct DiffBwdParams {
 };
 
 cudaError_t launch_diff_fwd(int d, const CUtensorMap &tq, const CUtensorMap &tk,
-                            const CUtensorMap &tv, const DiffFwdParams &p, cudaStream_t s);
+                            const CUtensorMap &tv, const DiffFwdParams &p, int sms,
+                            cudaStream_t s);
 cudaError_t launch_diff_bwd(int d, const CUtensorMap &tq, const CUtensorMap &tk,
                             const CUtensorMap &tv, const CUtensorMap &tdo,
                             const DiffBwdParams &p, cudaStream_t s);
