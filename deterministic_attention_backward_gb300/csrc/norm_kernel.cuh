@@ -15,6 +15,12 @@
 // over rows of one gate group with one fp32 sum per column in registers, writes its sums to
 // `part`, and a second kernel adds the CTAs' sums in a fixed order -- no atomics, the same
 // bits on every run.
+//
+// Measured in bf16 (of a plain copy's rate): the join of 16384 rows of 4096 forward 92 us, 5.8 TB/s
+// (86 %); backward 172 us, 4.7 TB/s (69 %): three factors and three column sums of 16 columns a
+// thread fill the registers, so two CTAs of 8 warps share an SM, and each row's two sums stand
+// between its loads and its stores.  Norms of 4.2 M heads of 128: forward 46 us, backward 69 us
+// (86 %).  3711 rows of 1001 in fp32, addressed by elements: 13 us and 22 us.
 #pragma once
 #include <type_traits>
 
@@ -50,8 +56,8 @@ __device__ __forceinline__ void store_w(void *w, long long at, int wf32, float v
     static_cast<T *>(w)[at] = from_f32<T>(v);
 }
 
-// Sum over the kNT threads of a row (part of a warp, a warp, or a CTA), the same value in each.  `red` holds two buffers of
-// kNT / 32 floats used in turn, so one barrier per sum is enough.
+// Sum over the kNT threads of a row (part of a warp, a warp, or a CTA), the same value in each.
+// `red` holds two buffers of kNT / 32 floats used in turn, so one barrier per sum is enough.
 template <int kNT>
 struct RowSum {
   float *red;
@@ -1140,7 +1146,8 @@ cudaError_t bwd(const NormBwdParams &p, cudaStream_t s) {
 }  // namespace norm
 }  // namespace dash
 
-// The launches of one element type (inside namespace dash); `wide`: rows, strides and addresses allow 16-byte vectors.
+// The launches of one element type (inside namespace dash); `wide`: rows, strides and addresses
+// allow 16-byte vectors.
 #define DASH_NORM_TYPE(T)                                                                       \
   template <>                                                                                   \
   cudaError_t launch_norm_fwd<T>(const NormFwdParams &p, bool join, bool wide, cudaStream_t s) { \

@@ -12,7 +12,8 @@
 // Bound by memory: every element is read and written once.  A CTA takes kTok tokens, forms
 // each (token, pair) phase once in shared memory and uses it for all heads of the token; q, k
 // and v go in one launch (v unturned), so that strided views of a qkv product become the
-// contiguous tensors attention reads in a single pass.
+// contiguous tensors attention reads in a single pass.  Measured on 2 x 8192 tokens of 32 + 8 + 8
+// heads of 128 in bf16: 65 us, 6.2 TB/s, 91 % of a plain copy's rate; one token 3.5 us, a launch.
 #include "common.cuh"
 #include "dash_attn.h"
 #include "elem.cuh"

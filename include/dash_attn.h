@@ -379,7 +379,7 @@ dash_status_t dash_join_bwd(const void *dy, const void *dh, const void *y, const
  * head pair [B,S,H] (lam_per_token), bf16 or fp32; any value.  d = 32 or 64 (value heads of 64
  * or 128), any S >= 1, masks and scale as dash_attn_fwd (scale <= 0: 1/sqrt(d)).
  * Forward: writes o, o2 = P2 V and lse [B,2H,S] fp32 (natural log, of map 2h+m at 2h+m), which
- * the backward takes; workspace: its status word. */
+ * the backward takes; workspace: its status block. */
 size_t dash_diff_fwd_workspace_bytes(int B, int S, int H, int d);
 dash_status_t dash_diff_fwd(const void *q, const void *k, const void *v, const void *lam, void *o,
                             void *o2, float *lse, int B, int S, int H, int group, int d,
@@ -388,9 +388,11 @@ dash_status_t dash_diff_fwd(const void *q, const void *k, const void *v, const v
                             dash_stream_t stream);
 /* Backward: dq, dk, dv and dlam (lam's shape and type).  Deterministic: every sum is formed in
  * a fixed order without atomics, bit-identical on every run; dk and dv sum a group's query heads
- * in ascending order.  The row terms D = dO . Om of dq come from o and o2 as they are given
+ * in ascending order (key tiles that the sizes put into pieces: within a piece, then the pieces).
+ * The row terms D = dO . Om of dq come from o and o2 as they are given
  * (rounded); those of dk, and dlam, from the fp32 sums of Pm dP.  Workspace: status block, row
- * vectors of B*H*Sp*20 bytes, B*H*Sp/128 partial sums (Sp = S rounded up to 128); dash_attn_status reads either status word. */
+ * vectors of B*H*Sp*20 bytes (Sp = S rounded up to 128), partial sums of dlam and, 80 MB at most,
+ * of key tiles that are formed in pieces; dash_attn_status reads either status word. */
 size_t dash_diff_bwd_workspace_bytes(int B, int S, int H, int d);
 dash_status_t dash_diff_bwd(const void *q, const void *k, const void *v, const void *o,
                             const void *o2, const void *dout, const float *lse, const void *lam,
