@@ -44,6 +44,28 @@ def contiguous(t, name):
         raise ValueError(f"{name} must be contiguous")
 
 
+def apart(outs, others=()):
+    """Raise ValueError where two of the tensors ``outs`` that a call writes begin at one address,
+    or one of them where one of ``others`` does that it reads."""
+    at = [t.data_ptr() for t in outs if t is not None and t.numel()]
+    if len(set(at)) < len(at):
+        raise ValueError("two outputs are the same memory")
+    if not set(at).isdisjoint(t.data_ptr() for t in others if t is not None):
+        raise ValueError("an output is the memory of an input")
+
+
+def scratch(nbytes, like, given):
+    """A workspace on ``like``'s device: ``given``, checked, or a new one."""
+    if given is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    if not isinstance(given, Tensor) or given.device != like.device:
+        raise ValueError(f"workspace must be a tensor on {like.device}")
+    contiguous(given, "workspace")
+    if given.numel() * given.element_size() < nbytes:
+        raise ValueError(f"workspace too small: {nbytes} bytes are needed")
+    return given
+
+
 def disjoint(t) -> bool:
     """Whether no two elements of ``t`` share an address (it can be written)."""
     if t.is_contiguous():

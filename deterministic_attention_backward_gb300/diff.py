@@ -15,8 +15,8 @@ from __future__ import annotations
 
 import torch
 
-from . import _check, _workspace, lib, status
-from ._args import alike, contiguous, run, tensor
+from . import _check, lib, status
+from ._args import alike, apart, contiguous, run, scratch, tensor
 
 _BF16 = (torch.bfloat16,)
 
@@ -56,7 +56,8 @@ def diff_bwd_workspace_bytes(B: int, S: int, H: int, d: int) -> int:
 
 def diff_fwd(q, k, v, lam, causal: bool = False, scale: float | None = None, out=None, out2=None,
              lse=None, workspace=None, stream=None, check: bool = False):
-    """Forward: returns (O [B,S,H,2d], O2 = softmax(Q2 K2^T) V of the same shape, LSE [B,2H,S])."""
+    """Forward: returns (O [B,S,H,2d], O2 = softmax(Q2 K2^T) V of the same shape, LSE [B,2H,S]).
+    A ``workspace`` serves one call at a time."""
     B, S, H, Hkv, d = _dims(q, k, v, lam)
     shape = (B, S, H, 2 * d)
     if out is not None:
@@ -65,6 +66,8 @@ def diff_fwd(q, k, v, lam, causal: bool = False, scale: float | None = None, out
         _given(out2, "out2", q, shape)
     if lse is not None:
         _given(lse, "lse", q, (B, 2 * H, S), torch.float32)
+    if out is not None or out2 is not None or lse is not None:
+        apart((out, out2, lse), (q, k, v, lam))
 
     def launch(handle):
         o = torch.empty(shape, dtype=q.dtype, device=q.device) if out is None else out
@@ -72,7 +75,7 @@ def diff_fwd(q, k, v, lam, causal: bool = False, scale: float | None = None, out
         l = lse if lse is not None else torch.empty((B, 2 * H, S), dtype=torch.float32,
                                                     device=q.device)
         if B and S:
-            ws = _workspace(256, q.device, workspace)
+            ws = scratch(256, q, workspace)
             _check(lib().dash_diff_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), lam.data_ptr(),
                                        o.data_ptr(), o2.data_ptr(), l.data_ptr(), B, S, H,
                                        H // Hkv, d, scale or 0.0, bool(causal),
@@ -98,6 +101,8 @@ def diff_bwd(q, k, v, o, o2, do, lse, lam, causal: bool = False, scale: float | 
     for t, n, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v), (dlam, "dlam", lam)):
         if t is not None:
             _given(t, n, q, like.shape, like.dtype)
+    if dq is not None or dk is not None or dv is not None or dlam is not None:
+        apart((dq, dk, dv, dlam), (q, k, v, o, o2, do, lse, lam))
 
     def launch(handle):
         gq, gk, gv, gl = (torch.empty_like(like) if t is None else t
@@ -106,7 +111,7 @@ def diff_bwd(q, k, v, o, o2, do, lse, lam, causal: bool = False, scale: float | 
             gl.zero_()
             return gq, gk, gv, gl
         L = lib()
-        ws = _workspace(L.dash_diff_bwd_workspace_bytes(B, S, H, d) or 256, q.device, workspace)
+        ws = scratch(L.dash_diff_bwd_workspace_bytes(B, S, H, d) or 256, q, workspace)
         _check(L.dash_diff_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
                                o2.data_ptr(), do.data_ptr(), lse.data_ptr(), lam.data_ptr(),
                                gq.data_ptr(), gk.data_ptr(), gv.data_ptr(), gl.data_ptr(), B, S,

@@ -19,8 +19,8 @@ import ctypes
 
 import torch
 
-from . import _check, _workspace, lib
-from ._args import DTYPES, alike, disjoint, run, tensor
+from . import _check, lib
+from ._args import DTYPES, alike, disjoint, run, scratch, tensor
 
 _Strides4, _Strides6 = ctypes.c_longlong * 4, ctypes.c_longlong * 6
 
@@ -53,6 +53,19 @@ def _out(t, name, like):
     return s
 
 
+def _in_place(outs, ins):
+    """Raise ValueError where an output is the memory of another, or of an input whose rows lie at
+    another stride; both are (tensor, stride of its rows)."""
+    for n, (o, so) in enumerate(outs):
+        if o is None:
+            continue
+        at = o.data_ptr()
+        if any(u is not None and u.data_ptr() == at for u, _ in outs[:n]) or \
+                any(t is not None and t.data_ptr() == at and st != so for t, st in ins):
+            raise ValueError("an output is the memory of another output, or of an input with "
+                             "another stride")
+
+
 def _weights(x, rows, w_post, gate, w_next):
     """Check the weights against rows of x; returns (their type, rows per gate row)."""
     C, dtype, gate_rows = x.shape[-1], None, rows
@@ -66,8 +79,13 @@ def _weights(x, rows, w_post, gate, w_next):
         alike(w, name, x, dtype=dtype)
         if name == "gate" and w.dim() > 1:
             groups = w.numel() // C
-            if w.shape[-1] != C or groups == 0 or rows % groups:
-                raise ValueError(f"gate {tuple(w.shape)} does not divide {rows} rows of {C}")
+            lead = list(w.shape[:-1])
+            while lead and lead[-1] == 1:
+                lead.pop()
+            if w.shape[-1] != C or groups == 0 or rows % groups or \
+                    (x.dim() > 2 and list(x.shape[:len(lead)]) != lead):
+                raise ValueError(f"gate {tuple(w.shape)} has no row for each run of consecutive "
+                                 f"rows of {tuple(x.shape)}")
             gate_rows = rows // groups
         elif w.dim() != 1 or w.shape[0] != C:
             raise ValueError(f"{name} must have shape {(C,)}, got {tuple(w.shape)}")
@@ -99,6 +117,8 @@ def _forward(x, a, w_post, gate, w_next, skip_scale, branch_scale, eps, y, h, st
     if w_next is None:
         h = None
     ys, hs = _out(y, "y", x), _out(h, "h" if join else "out", x)
+    if y is not None or h is not None:
+        _in_place(((y, ys), (h, hs)), ((x, xs), (a, as_)))
 
     def launch(handle):
         Y, H, ra, ry = y, h, None, None
@@ -148,6 +168,8 @@ def _backward(dy, dh, y, a, rstd_a, rstd_y, w_post, gate, w_next, skip_scale, br
             if not t.is_contiguous():
                 raise ValueError(f"{n} must be contiguous")
     dxs, das = _out(dx, "dx", base), _out(da, "da", base)
+    if dx is not None or da is not None:
+        _in_place(((dx, dxs), (da, das)), ((dy, dys), (dh, dhs), (y, ys), (a, as_)))
 
     def launch(handle):
         DX, DA = _like(base) if dx is None else dx, da
@@ -159,7 +181,7 @@ def _backward(dy, dh, y, a, rstd_a, rstd_y, w_post, gate, w_next, skip_scale, br
             L, dtype = lib(), DTYPES[base.dtype]
             need = L.dash_join_bwd_workspace_bytes(rows, C, gate_rows if gate is not None else 0,
                                                    join, dtype)
-            ws = _workspace(need or 256, base.device, workspace)
+            ws = scratch(need or 256, base, workspace)
             _check(L.dash_join_bwd(_ptr(dy), _ptr(dh) if normed else None, _ptr(y), _ptr(a),
                                    _ptr(w_post), _ptr(gate), _ptr(w_next), _ptr(rstd_a),
                                    _ptr(rstd_y), DX.data_ptr(), _ptr(DA), _ptr(dw_post),
@@ -209,7 +231,7 @@ def join_fwd(x, a, *, w_post=None, gate=None, w_next=None, skip_scale: float = 1
     """y = skip_scale x + branch_scale gate (a rstd(a) w_post), h = y rstd(y) w_next: returns
     (y, h, rstd_a, rstd_y).  Without ``w_post`` the branch is not normed, without ``gate`` it is
     not gated, without ``w_next`` there is no h.  ``gate`` is [C], or [..., C] with every row of
-    it serving the same number of consecutive rows of x ([B, C] for x [B, S, C])."""
+    it serving the same number of consecutive rows of x ([B, C] or [B, 1, C] for x [B, S, C])."""
     if a is None:
         raise ValueError("join_fwd needs a branch")
     return _forward(x, a, w_post, gate, w_next, skip_scale, branch_scale, eps, y, h, stream)

@@ -76,9 +76,9 @@ def _rope(parts, inv_freq, magnitude, positions, start, layout, out, stream, bac
         raise ValueError("inv_freq must be contiguous float64 [rot/2], rot <= 1024")
     tokens = q.shape[:-2]
     B, S = tokens if dims == 4 else (1, tokens[0])
-    if out is None:
-        out = (None, None, None)
-    elif len(out) != len(parts):
+    given = out is not None
+    out = tuple(out) if given else (None, None, None)
+    if len(out) != len(parts):
         raise ValueError(f"out must hold {len(parts)} tensors")
     res, packed = [], []
     for i, t in enumerate(parts):
@@ -101,6 +101,13 @@ def _rope(parts, inv_freq, magnitude, positions, start, layout, out, stream, bac
                 raise ValueError(f"the elements of a head of {name} must be contiguous")
             if not disjoint(o):
                 raise ValueError(f"{name} has elements that share an address")
+    if given:  # in place: its own input, as it lies
+        at = [t.data_ptr() if t is not None and t.numel() else None for t in parts + out]
+        for i, o in enumerate(out, len(parts)):
+            if at[i] is not None and at[i] in at[:i] + at[i + 1:] and (
+                    at.count(at[i]) > 2 or at[i - len(parts)] != at[i] or
+                    o.stride() != parts[i - len(parts)].stride()):
+                raise ValueError(f"out[{i - len(parts)}] is the memory of another tensor")
     where, pos64, pb, pt = None, 0, 0, 0
     if positions is not None:
         tensor(positions, "positions", (torch.int32, torch.int64))

@@ -379,7 +379,8 @@ dash_status_t dash_join_bwd(const void *dy, const void *dh, const void *y, const
  * head pair [B,S,H] (lam_per_token), bf16 or fp32; any value.  d = 32 or 64 (value heads of 64
  * or 128), any S >= 1, masks and scale as dash_attn_fwd (scale <= 0: 1/sqrt(d)).
  * Forward: writes o, o2 = P2 V and lse [B,2H,S] fp32 (natural log, of map 2h+m at 2h+m), which
- * the backward takes; workspace: its status block. */
+ * the backward takes; workspace: its status block, of one call at a time.  No output overlaps an
+ * input or another output. */
 size_t dash_diff_fwd_workspace_bytes(int B, int S, int H, int d);
 dash_status_t dash_diff_fwd(const void *q, const void *k, const void *v, const void *lam, void *o,
                             void *o2, float *lse, int B, int S, int H, int group, int d,

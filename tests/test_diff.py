@@ -375,6 +375,13 @@ def test_refusals(L):
         a.update(bad)
         with pytest.raises(ValueError):
             dash.diff_bwd(q, k, v, a["o"], a["o2"], a["do"], a["lse"], w)
+    no(q, k, v, w, out=o, out2=o)
+    host = torch.zeros(1 << 20, dtype=torch.uint8)
+    no(q, k, v, w, workspace=host)
+    no(q, k, v, w, workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"))
+    for bad in (dict(dq=q), dict(dk=k), dict(dlam=w), dict(workspace=host)):
+        with pytest.raises(ValueError):
+            dash.diff_bwd(q, k, v, o, o2, do, lse, w, **bad)
     x, y, z, u, _ = make(1, 8, 2, 2, 16, "head-bf16")
     with pytest.raises(dash.DashError) as err:
         dash.diff_fwd(x, y, z, u)

@@ -319,6 +319,18 @@ def test_refusals(L):
     no(dash.join_bwd, x, x, x, x, None, rstd[:2], w_next=w)
     no(dash.norm_bwd, x, x, rstd.half(), w)
     no(dash.norm_bwd, x[:, :3], x, rstd, w)
+    g = torch.ones(6, 64, dtype=BF, device="cuda")
+    no(dash.join_fwd, x, x, gate=g)                      # torch would take a row for each token
+    no(dash.join_fwd, x, x, gate=g[None])
+    y = torch.zeros_like(x)
+    no(dash.join_fwd, x, x, w_next=w, y=y, h=y)
+    no(dash.join_bwd, x, x, x, x, None, rstd, w_next=w, dx=y, da=y)
+    wide = torch.zeros(4, 6, 128, dtype=BF, device="cuda")
+    no(dash.norm_fwd, wide[..., :64], w, out=wide.view(-1)[:1536].view(4, 6, 64))
+    no(dash.norm_bwd, wide[..., :64], x, rstd, w, dx=wide.view(-1)[:1536].view(4, 6, 64))
+    for ws in (torch.zeros(1 << 20, dtype=torch.uint8), torch.zeros(8, device="cuda"),
+               torch.zeros(1 << 20, 2, dtype=torch.uint8, device="cuda")[:, 0]):
+        no(dash.norm_bwd, x, x, rstd, w, workspace=ws)
 
 
 def test_abi_refusals(L):

@@ -245,3 +245,9 @@ def test_refusals(L):
     no(q, out=(q,))
     no(q, out=(q[:, :3], None, None))
     no(q, out=(q[:1].expand(2, 4, 2, 64), None, None))   # shared addresses
+    k, o = torch.zeros_like(q), torch.zeros_like(q)
+    no(q, k, out=(o, o, None))
+    no(q, k, out=(k, o, None))
+    no(q, k, out=(o, q, None))
+    wide = torch.zeros(2, 8, 2, 64, dtype=BF, device="cuda")
+    no(wide[:, :4], out=(wide.view(-1)[:1024].view(2, 4, 2, 64), None, None))  # other strides
