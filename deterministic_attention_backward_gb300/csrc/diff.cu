@@ -174,7 +174,6 @@ dash_status_t dash_diff_bwd(const void *q, const void *k, const void *v, const v
       !make_bshd_map(&tdo, dout, B, S, H, 2 * d, kTile / 2))
     return DASH_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(workspace, 0, kStatusBytes, s) != cudaSuccess) return DASH_ERR_CUDA;
   DiffBwdParams p{};
   p.o = static_cast<const __nv_bfloat16 *>(o);
   p.o2 = static_cast<const __nv_bfloat16 *>(o2);

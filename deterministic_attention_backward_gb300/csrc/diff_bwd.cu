@@ -12,9 +12,13 @@
 // and their ordering.
 #include "diff.cuh"
 
+#include "dash_attn.h"
+#include "host.cuh"
+
 namespace dash {
 namespace {
 
+constexpr int kStatusWords = kStatusBytes / 4;
 constexpr int kWarps = 16;                   // warps of elementwise work: four warpgroups
 constexpr int kThreads = (kWarps + 2) * 32;  // and the TMA producer, the MMA issuer
 
@@ -27,6 +31,7 @@ __global__ void __launch_bounds__(256) diff_rows_kernel(const DiffBwdParams p) {
   __shared__ float s_d[2][kTile];
   const int lane = threadIdx.x % kLanes, sub = threadIdx.x / kLanes;
   const int tile = blockIdx.x, i = tile % p.N, h = (tile / p.N) % p.H, b = tile / p.N / p.H;
+  if (tile == 0 && threadIdx.x < kStatusWords) p.status[threadIdx.x] = 0;  // for what follows
 #pragma unroll 4
   for (int r = sub; r < kTile; r += kRows) {
     const int row = i * kTile + r;
@@ -408,25 +413,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Weights per head: the tiles' sums of one head, added in a fixed order.
-__global__ void __launch_bounds__(256) diff_dlam_kernel(const DiffBwdParams p) {
-  __shared__ float s[8];
-  const int h = blockIdx.x;
+// Weights per head: the tiles' sums of head h, added in a fixed order by one warp.
+__device__ __forceinline__ void sum_dlam(const DiffBwdParams &p, int h, int lane) {
   float v = 0.f;
-  for (int k = threadIdx.x; k < p.B * p.N; k += 256)
+#pragma unroll 4
+  for (int k = lane; k < p.B * p.N; k += 32)
     v += p.dlam_part[((size_t)(k / p.N) * p.H + h) * p.N + k % p.N];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    v = 0.f;
-    for (int k = 0; k < 8; ++k) v += s[k];
-    if (p.lam_f32)
-      static_cast<float *>(p.dlam)[h] = v;
-    else
-      static_cast<__nv_bfloat16 *>(p.dlam)[h] = __float2bfloat16_rn(v);
-  }
+  if (lane > 0) return;
+  if (p.lam_f32)
+    static_cast<float *>(p.dlam)[h] = v;
+  else
+    static_cast<__nv_bfloat16 *>(p.dlam)[h] = __float2bfloat16_rn(v);
 }
 
 // -------------------------------------------------------------------- dK, dV
@@ -507,7 +506,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     first_step = all * piece / p.kv_pieces;
     steps = all * (piece + 1) / p.kv_pieces - first_step;
   }
-  if (steps == 0) return;  // (diff_join_kernel leaves such a piece out)
+  auto heads_dlam = [&]() {  // by the producer's warp, behind its work
+    if (!p.lam_token)
+      for (int h = blockIdx.x; h < p.H; h += gridDim.x) sum_dlam(p, h, lane);
+  };
+  if (steps == 0) {  // (diff_join_kernel leaves such a piece out)
+    if (warp == kWarps) heads_dlam();
+    return;
+  }
 
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
@@ -540,45 +546,49 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
 
-  if (warp == kWarps && lane == 0) {
-    // ------------------------------------------------------------------ TMA producer
-    int last[L::kStages];
-    for (int s = 0; s < L::kStages; ++s) last[s] = -1;
-    bool ok = true;
-    mbar_arrive_expect_tx(kv_full, 2 * L::kTileBytes);
-    for (int bx = 0; bx < L::kBoxes; ++bx) {
-      tma_load_4d(smem + L::offK + bx * kBoxBytes, &tm_k, kv_full, bx * kBoxCols, hkv, j * kTile,
-                  b);
-      tma_load_4d(smem + L::offV + bx * kBoxBytes, &tm_v, kv_full, bx * kBoxCols, hkv, j * kTile,
-                  b);
-    }
-    for (int n = 0; n < steps; ++n) {
-      const int s = n % L::kStages;
-      const uint32_t ph = (n / L::kStages) & 1;
-      if (!mbar_wait(&q_empty[s], ph ^ 1, ab)) {
-        ok = false;
-        break;
-      }
-      const int at = first_step + n;
-      const int h = hkv * p.G + (at >> 1) / tiles, i = i0 + (at >> 1) % tiles, u = at & 1;
-      mbar_arrive_expect_tx(&q_full[s], L::kStageBytes + L::kRowBytes);
-      uint8_t *sq = smem + L::offStage + s * L::kStageBytes;
+  if (warp == kWarps) {
+    if (lane == 0) {
+      // ------------------------------------------------------------------ TMA producer
+      int last[L::kStages];
+      for (int s = 0; s < L::kStages; ++s) last[s] = -1;
+      bool ok = true;
+      mbar_arrive_expect_tx(kv_full, 2 * L::kTileBytes);
       for (int bx = 0; bx < L::kBoxes; ++bx) {
-        tma_load_4d(sq + bx * L::kHalfBox, &tm_q, &q_full[s], bx * kBoxCols, h,
-                    i * kTile + u * kStep, b);
-        tma_load_4d(sq + L::kHalfBytes + bx * L::kHalfBox, &tm_do, &q_full[s], bx * kBoxCols, h,
-                    i * kTile + u * kStep, b);
+        tma_load_4d(smem + L::offK + bx * kBoxBytes, &tm_k, kv_full, bx * kBoxCols, hkv, j * kTile,
+                    b);
+        tma_load_4d(smem + L::offV + bx * kBoxBytes, &tm_v, kv_full, bx * kBoxCols, hkv, j * kTile,
+                    b);
       }
-      bulk_load(smem + L::offRow + s * L::kRowBytes,
-                p.rowv + rowv_at(((size_t)b * p.H + h) * p.N + i, u * kStep), L::kRowBytes,
-                &q_full[s]);
-      last[s] = (int)ph;
+      for (int n = 0; n < steps; ++n) {
+        const int s = n % L::kStages;
+        const uint32_t ph = (n / L::kStages) & 1;
+        if (!mbar_wait(&q_empty[s], ph ^ 1, ab)) {
+          ok = false;
+          break;
+        }
+        const int at = first_step + n;
+        const int h = hkv * p.G + (at >> 1) / tiles, i = i0 + (at >> 1) % tiles, u = at & 1;
+        mbar_arrive_expect_tx(&q_full[s], L::kStageBytes + L::kRowBytes);
+        uint8_t *sq = smem + L::offStage + s * L::kStageBytes;
+        for (int bx = 0; bx < L::kBoxes; ++bx) {
+          tma_load_4d(sq + bx * L::kHalfBox, &tm_q, &q_full[s], bx * kBoxCols, h,
+                      i * kTile + u * kStep, b);
+          tma_load_4d(sq + L::kHalfBytes + bx * L::kHalfBox, &tm_do, &q_full[s], bx * kBoxCols, h,
+                      i * kTile + u * kStep, b);
+        }
+        bulk_load(smem + L::offRow + s * L::kRowBytes,
+                  p.rowv + rowv_at(((size_t)b * p.H + h) * p.N + i, u * kStep), L::kRowBytes,
+                  &q_full[s]);
+        last[s] = (int)ph;
+      }
+      if (!ok) {
+        mbar_wait_drain(kv_full, 0, 100000000ull);
+        for (int s = 0; s < L::kStages; ++s)
+          if (last[s] >= 0) mbar_wait_drain(&q_full[s], (uint32_t)last[s], 100000000ull);
+      }
     }
-    if (!ok) {
-      mbar_wait_drain(kv_full, 0, 100000000ull);
-      for (int s = 0; s < L::kStages; ++s)
-        if (last[s] >= 0) mbar_wait_drain(&q_full[s], (uint32_t)last[s], 100000000ull);
-    }
+    __syncwarp();
+    heads_dlam();
   } else if (warp == kWarps + 1) {
     // ------------------------------------------------------------------ MMA issuer
     // (a converged warp, one elected lane issues)
@@ -880,16 +890,13 @@ cudaError_t launch_t(const CUtensorMap &tq, const CUtensorMap &tk, const CUtenso
                      const DiffBwdParams &p, cudaStream_t s) {
   using LQ = DqL<d>;
   using LK = DkvL<d>;
-  cudaError_t e = cudaFuncSetAttribute(diff_dq_kernel<d>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, LQ::kBytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(diff_dkv_kernel<d>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             LK::kBytes);
+  static std::atomic<uint64_t> dq_set{0}, dkv_set{0};
+  cudaError_t e = allow_smem(diff_dq_kernel<d>, LQ::kBytes, dq_set);
+  if (e == cudaSuccess) e = allow_smem(diff_dkv_kernel<d>, LK::kBytes, dkv_set);
   if (e != cudaSuccess) return e;
   const unsigned tiles = (unsigned)p.B * p.H * p.N;
   diff_rows_kernel<d><<<tiles, 256, 0, s>>>(p);
   diff_dq_kernel<d><<<tiles, kThreads, LQ::kBytes, s>>>(tq, tk, tv, tdo, p);
-  if (!p.lam_token) diff_dlam_kernel<<<p.H, 256, 0, s>>>(p);
   const unsigned cut = (unsigned)p.B * p.Hkv * p.N - p.kv_whole;  // tiles in pieces
   diff_dkv_kernel<d><<<p.kv_whole + cut * p.kv_pieces, kThreads, LK::kBytes, s>>>(tq, tk, tv,
                                                                                   tdo, p);

@@ -26,6 +26,9 @@
 // Warps 0-7 map 1, 8-15 map 2, 16 TMA producer, 17 MMA issuer.
 #include "diff.cuh"
 
+#include "dash_attn.h"
+#include "host.cuh"
+
 namespace dash {
 namespace {
 
@@ -409,8 +412,8 @@ template <int d>
 cudaError_t launch_t(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                      const DiffFwdParams &p, int sms, cudaStream_t s) {
   using L = FwdL<d>;
-  const cudaError_t e = cudaFuncSetAttribute(
-      diff_fwd_kernel<d>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+  static std::atomic<uint64_t> set{0};
+  const cudaError_t e = allow_smem(diff_fwd_kernel<d>, L::kBytes, set);
   if (e != cudaSuccess) return e;
   const int tiles = p.B * p.H * p.N;
   diff_fwd_kernel<d><<<tiles < sms ? tiles : sms, kThreads, L::kBytes, s>>>(tq, tk, tv, p);

@@ -70,6 +70,18 @@ inline dash_status_t device_info(DevInfo *out) {
   return (d.major == 10 && d.minor == 3) ? DASH_OK : DASH_ERR_UNSUPPORTED;
 }
 
+// Dynamic shared memory of `kernel` on the current device, set once per device (`set`: its bits).
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t> &set) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (set.load() >> dev & 1)) return e;
+  const cudaError_t f =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (f == cudaSuccess) set.fetch_or(1ull << dev);
+  return f;
+}
+
 // ------------------------------------------------------------------ checks
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
