@@ -11,10 +11,12 @@ namespace dash {
 
 // CTAs per gate group of the backward: in all as many as 152 SMs hold at once (by the ring's
 // shared memory and the column sums' registers, see ring_shape), whatever the device, so that
-// the order of the weight gradients' sums depends on the sizes alone; never more than there are
-// rows for.
-int norm_bwd_ctas(long long rows, long long groups, int C, int elem_bytes, bool wide, bool join) {
-  const int n = wide ? C * elem_bytes / 16 : C;
+// the order of the weight gradients' sums does not depend on it; never more than there are
+// rows for.  Rows off the 16-byte grid: as many for each of `period` alignments.
+int norm_bwd_ctas(long long rows, long long groups, int C, int elem_bytes, bool wide, int period,
+                  bool join) {
+  const int vec = 16 / elem_bytes;
+  const int n = wide ? (C + (period ? vec - 1 : 0) + vec - 1) / vec : C;
   int sms_share = 2, at_once = 1;  // CTAs on an SM, rows of a CTA at once
   if (!wide) {
     if (n <= 128) at_once = 8;
@@ -29,10 +31,11 @@ int norm_bwd_ctas(long long rows, long long groups, int C, int elem_bytes, bool 
   } else if (n <= 2048) {
     sms_share = 1;
   }
-  const long long per = rows / groups;
+  const int kinds = period ? period : 1;
+  const long long per = (rows / groups + kinds - 1) / kinds;
   const long long most = (per + at_once - 1) / at_once;
-  const long long want = 152LL * sms_share / groups;
-  return (int)(want < 1 ? 1 : want < most ? want : most);
+  const long long want = 152LL * sms_share / groups / kinds;
+  return (int)(want < 1 ? 1 : want < most ? want : most) * kinds;
 }
 
 namespace {
@@ -57,16 +60,51 @@ dash_status_t check_rows(long long rows, int C, long long gate_rows, bool gate, 
   return DASH_OK;
 }
 
+// How rows lie on the grid of 16-byte vectors: on it (wide, period 0), off it but in the same way
+// in every tensor (wide, period the rows after which they lie the same again), or neither.
+struct Lie {
+  bool wide = false;
+  int period = 0, off = 0, stride_mod = 0;
+};
+template <int N, int M>
+Lie lie_of(const void *const (&ptrs)[N], const long long *strides, const void *const (&weights)[M],
+           int C, int size, long long group_rows) {
+  const int vec = 16 / size;
+  Lie l;
+  bool first = true, same = true;
+  for (int i = 0; i < N; ++i) {
+    if (!ptrs[i]) continue;
+    const int off = (int)(reinterpret_cast<uintptr_t>(ptrs[i]) & 15) / size;
+    const int mod = (int)(strides[i] & (vec - 1));
+    if (first) l.off = off, l.stride_mod = mod;
+    same = same && off == l.off && mod == l.stride_mod;
+    first = false;
+  }
+  if (same && l.off == 0 && l.stride_mod == 0 && C % vec == 0 && all_aligned(weights, 16)) {
+    l.wide = true;
+    return l;
+  }
+  l.period = 1;
+  while ((l.period * l.stride_mod) & (vec - 1)) l.period *= 2;
+  // A CTA takes rows of one alignment: with few rows of each, or rows of a few vectors, it would
+  // stand half empty, and element by element they take a launch's time as well.  At 22324 rows of
+  // 1503 in bf16 the join takes 62 us forward, 126 backward (by elements 146, 212), at 124275 rows
+  // of 270 97 and 199 (244, 599).  Rows beyond the ring's go element by element.
+  l.wide = same && C >= 2 * vec && group_rows >= 8 * l.period && (C + 2 * vec - 2) / vec <= 2048;
+  if (!l.wide) l.period = 0;
+  return l;
+}
+
 struct Groups {
   int groups, ctas, row_gate;
   long long gate_rows;
 };
 Groups make_groups(long long rows, int C, long long gate_rows, bool gate, int dtype, bool wide,
-                   bool join) {
+                   int period, bool join) {
   Groups g{1, 1, gate && gate_rows == 1 && rows > 1, rows};
   if (gate && !g.row_gate) g.gate_rows = gate_rows;
   g.groups = (int)(rows / g.gate_rows);
-  g.ctas = norm_bwd_ctas(rows, g.groups, C, elem_size(dtype), wide, join);
+  g.ctas = norm_bwd_ctas(rows, g.groups, C, elem_size(dtype), wide, period, join);
   return g;
 }
 
@@ -87,13 +125,14 @@ dash_status_t dash_join_fwd(const void *x, const void *a, const void *w_post, co
   const bool join = a != nullptr;
   if (!x || !strides || (join ? !y : !w_next || w_post || gate)) return DASH_ERR_INVALID;
   if ((w_next && (!h || !rstd_y)) || (w_post && !rstd_a)) return DASH_ERR_INVALID;
-  const int size = elem_size(dtype), vec = 16 / size;
-  const void *rowp[] = {x, a, y, w_next ? h : nullptr}, *wp[] = {w_post, gate, w_next};
+  const int size = elem_size(dtype);
+  const void *rowp[] = {x, a, join ? y : nullptr, w_next ? h : nullptr};
+  const void *wp[] = {w_post, gate, w_next};
   const void *fp[] = {rstd_a, rstd_y};
   if (!all_aligned(rowp, size) || !all_aligned(wp, elem_size(wdtype)) || !all_aligned(fp, 4))
     return DASH_ERR_INVALID;
-  const bool wide = C % vec == 0 && all_aligned(rowp, 16) && all_aligned(wp, 16) &&
-                    (strides[0] | strides[1] | strides[2] | strides[3]) % vec == 0;
+  const Lie lie = lie_of(rowp, strides, wp, C, size, rows);
+  const bool wide = lie.wide;
   DevInfo dev;
   if ((st = device_info(&dev)) != DASH_OK) return st;
   NormFwdParams p{};
@@ -104,6 +143,7 @@ dash_status_t dash_join_fwd(const void *x, const void *a, const void *w_post, co
   p.gate_rows = gate ? gate_rows : rows;
   p.C = C;
   p.wf32 = wdtype == DASH_FP32 && dtype != DASH_FP32;
+  p.period = lie.period, p.off = lie.off, p.stride_mod = lie.stride_mod;
   p.skip = skip_scale, p.branch = branch_scale, p.eps = eps;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = dtype == DASH_BF16   ? launch_norm_fwd<__nv_bfloat16>(p, join, wide, s)
@@ -117,8 +157,10 @@ size_t dash_join_bwd_workspace_bytes(long long rows, int C, long long gate_rows,
   using namespace dash;
   if (check_rows(rows, C, gate_rows, gate_rows > 0, dtype, dtype) != DASH_OK) return 0;
   size_t most = 0;
-  for (const bool wide : {false, true}) {
-    const Groups g = make_groups(rows, C, gate_rows, gate_rows > 0, dtype, wide, join);
+  for (int form = 0; form < 6; ++form) {  // by elements, on the grid, off it in 1 to 8 ways
+    const int period = form < 2 ? 0 : 1 << (form - 2);
+    const Groups g = make_groups(rows, C, gate_rows, gate_rows > 0, dtype, form > 0, period, join);
+    if (period && g.gate_rows < 8 * period) break;
     const size_t n = align256((size_t)g.groups * g.ctas * (join ? 2 : 1) * C * sizeof(float));
     most = n > most ? n : most;
   }
@@ -140,8 +182,9 @@ dash_status_t dash_join_bwd(const void *dy, const void *dh, const void *y, const
     return DASH_ERR_INVALID;
   if (w_next && (!dh || !y || !rstd_y || !dw_next)) return DASH_ERR_INVALID;
   if ((w_post && (!rstd_a || !dw_post)) || (gate && !dgate)) return DASH_ERR_INVALID;
-  const int size = elem_size(dtype), vec = 16 / size;
-  const void *rowp[] = {dy, w_next ? dh : nullptr, w_next ? y : nullptr, a, dx, join ? da : nullptr};
+  const int size = elem_size(dtype);
+  const void *rowp[] = {dy, w_next ? dh : nullptr, w_next ? y : nullptr, a, dx,
+                        join ? da : nullptr};
   const void *wp[] = {w_post, gate, w_next};
   const void *dwp[] = {w_post ? dw_post : nullptr, gate ? dgate : nullptr,
                        w_next ? dw_next : nullptr};
@@ -152,12 +195,13 @@ dash_status_t dash_join_bwd(const void *dy, const void *dh, const void *y, const
   if (!workspace || !aligned16(workspace) ||
       workspace_bytes < dash_join_bwd_workspace_bytes(rows, C, gate ? gate_rows : 0, join, dtype))
     return DASH_ERR_WORKSPACE;
-  long long any = 0;
-  for (int i = 0; i < 6; ++i) any |= strides[i];
-  const bool wide = C % vec == 0 && all_aligned(rowp, 16) && all_aligned(wp, 16) && any % vec == 0;
+  const bool own_gates = gate && gate_rows == 1 && rows > 1;
+  const Lie lie = lie_of(rowp, strides, wp, C, size, gate && !own_gates ? gate_rows : rows);
+  const bool wide = lie.wide;
   DevInfo dev;
   if ((st = device_info(&dev)) != DASH_OK) return st;
-  const Groups g = make_groups(rows, C, gate_rows, gate != nullptr, dtype, wide, join);
+  const Groups g =
+      make_groups(rows, C, gate_rows, gate != nullptr, dtype, wide, lie.period, join);
   NormBwdParams p{};
   p.dy = dy, p.dh = dh, p.y = y, p.a = a;
   p.w_post = w_post, p.gate = gate, p.w_next = w_next;
@@ -174,6 +218,7 @@ dash_status_t dash_join_bwd(const void *dy, const void *dh, const void *y, const
   p.groups = g.groups, p.ctas = g.ctas, p.row_gate = g.row_gate;
   p.C = C;
   p.wf32 = wdtype == DASH_FP32 && dtype != DASH_FP32;
+  p.period = lie.period, p.off = lie.off, p.stride_mod = lie.stride_mod;
   p.skip = skip_scale, p.branch = branch_scale;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = dtype == DASH_BF16   ? launch_norm_bwd<__nv_bfloat16>(p, join, wide, s)

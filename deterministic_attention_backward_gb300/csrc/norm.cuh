@@ -14,6 +14,7 @@ struct NormFwdParams {
   long long xs, as, ys, hs;
   long long rows, gate_rows;             // gate row of row r: r / gate_rows
   int C, wf32;
+  int period, off, stride_mod;           // rows off the 16-byte grid (period 0: on it)
   float skip, branch, eps;
 };
 struct NormBwdParams {
@@ -27,10 +28,12 @@ struct NormBwdParams {
   int groups, ctas;                      // CTAs per group
   int row_gate;                          // every row has a gate row of its own
   int C, wf32;
+  int period, off, stride_mod;
   float skip, branch;
 };
 
-int norm_bwd_ctas(long long rows, long long groups, int C, int elem_bytes, bool wide, bool join);
+int norm_bwd_ctas(long long rows, long long groups, int C, int elem_bytes, bool wide, int period,
+                  bool join);
 
 template <typename T>
 cudaError_t launch_norm_fwd(const NormFwdParams &p, bool join, bool wide, cudaStream_t s);

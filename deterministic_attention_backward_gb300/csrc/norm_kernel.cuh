@@ -491,9 +491,77 @@ __device__ __forceinline__ void load_w2(const void *w, long long at, int wf32,
     unpack2<T>(*reinterpret_cast<const uint4 *>(static_cast<const T *>(w) + at), f);
   }
 }
+// Rows off the 16-byte grid.  Where all tensors lie on it in the same way, row r begins
+// (off + r stride) mod V elements behind a boundary, the same for every `period`-th row: a CTA
+// that takes such rows has its vectors at the same columns throughout, from `shift` columns before
+// the row on, and works as with aligned rows, but for the ends, where a vector holds columns of
+// the rows beside it: they count as zero and are not written.  (Each row read by itself, element
+// by element, took 2 to 6 times as long.)
+template <typename T>
+__device__ __forceinline__ bool inside(int c, int C) {  // whether the whole vector is
+  return c >= 0 && c + (int)(16 / sizeof(T)) <= C;
+}
+template <typename T>
+__device__ __forceinline__ void zero_outside(f2 (&f)[8 / sizeof(T)], int c, int C) {
+#pragma unroll
+  for (int e = 0; e < (int)(8 / sizeof(T)); ++e) {
+    float a, b;
+    f2_to(f[e], a, b);
+    f[e] = f2_of((unsigned)(c + 2 * e) < (unsigned)C ? a : 0.f,
+                 (unsigned)(c + 2 * e + 1) < (unsigned)C ? b : 0.f);
+  }
+}
+template <typename T, bool kShift>
+__device__ __forceinline__ void put_at(T *row, int c, int C, const f2 (&f)[8 / sizeof(T)]) {
+  if (!kShift || inside<T>(c, C)) {
+    put<T>(row + c, f);
+  } else {
+#pragma unroll
+    for (int e = 0; e < (int)(8 / sizeof(T)); ++e) {
+      float a, b;
+      f2_to(f[e], a, b);
+      if ((unsigned)(c + 2 * e) < (unsigned)C) row[c + 2 * e] = from_f32<T>(a);
+      if ((unsigned)(c + 2 * e + 1) < (unsigned)C) row[c + 2 * e + 1] = from_f32<T>(b);
+    }
+  }
+}
+// Columns c.. of the weights' row at `base`.
+template <typename T, bool kShift>
+__device__ __forceinline__ void weights_at(const void *w, long long base, int c, int C, int wf32,
+                                           f2 (&f)[8 / sizeof(T)]) {
+  if constexpr (!kShift) {
+    load_w2<T>(w, base + c, wf32, f);
+  } else {
+#pragma unroll
+    for (int e = 0; e < (int)(8 / sizeof(T)); ++e) {
+      float v[2][1] = {{0.f}, {0.f}};
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        if ((unsigned)(c + 2 * e + u) < (unsigned)C)
+          load_w<T, 1>(w, base + c + 2 * e + u, wf32, v[u]);
+      f[e] = f2_of(v[0][0], v[1][0]);
+    }
+  }
+}
+template <bool kShift, int P>
+__device__ __forceinline__ void put_sums(float *out, int c, int C, const f2 (&acc)[P]) {
+  if constexpr (!kShift) {
+#pragma unroll
+    for (int e = 0; e < P; e += 2)
+      *reinterpret_cast<ulonglong2 *>(out + c + 2 * e) = make_ulonglong2(acc[e], acc[e + 1]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      float a, b;
+      f2_to(acc[e], a, b);
+      if ((unsigned)(c + 2 * e) < (unsigned)C) out[c + 2 * e] = a;
+      if ((unsigned)(c + 2 * e + 1) < (unsigned)C) out[c + 2 * e + 1] = b;
+    }
+  }
+}
 // branch_scale gate w_post of one vector (factors that are not there: 1); of the gate's row
 // `grow`, in elements.
-template <typename T, typename Params>
+template <typename T, bool kShift, typename Params>
 __device__ __forceinline__ void branch_factor(const Params &p, int c, long long grow,
                                               f2 (&f)[8 / sizeof(T)]) {
   constexpr int P = 8 / sizeof(T);
@@ -501,13 +569,13 @@ __device__ __forceinline__ void branch_factor(const Params &p, int c, long long 
   for (int e = 0; e < P; ++e) f[e] = f2_of(p.branch, p.branch);
   if (p.w_post) {
     f2 w[P];
-    load_w2<T>(p.w_post, c, p.wf32, w);
+    weights_at<T, kShift>(p.w_post, 0, c, p.C, p.wf32, w);
 #pragma unroll
     for (int e = 0; e < P; ++e) f[e] = mul2(f[e], w[e]);
   }
   if (p.gate) {
     f2 w[P];
-    load_w2<T>(p.gate, grow + c, p.wf32, w);
+    weights_at<T, kShift>(p.gate, grow, c, p.C, p.wf32, w);
 #pragma unroll
     for (int e = 0; e < P; ++e) f[e] = mul2(f[e], w[e]);
   }
@@ -515,7 +583,7 @@ __device__ __forceinline__ void branch_factor(const Params &p, int c, long long 
 
 // Weights stay in registers over a CTA's rows (up to two vectors a thread): read again for
 // every row they come from L2, whose latency then stands between the two sums of each row.
-template <typename T, int kNT, int kNV, bool kJoin, int kDepth>
+template <typename T, int kNT, int kNV, bool kJoin, int kDepth, bool kShift>
 __global__ void __launch_bounds__(kRingThreads<kNT>) fwd_ring(const NormFwdParams p) {
   constexpr int V = 16 / sizeof(T), P = V / 2, kThreads = kRingThreads<kNT>;
   constexpr int kRows = kThreads / kNT;
@@ -525,14 +593,16 @@ __global__ void __launch_bounds__(kRingThreads<kNT>) fwd_ring(const NormFwdParam
   RowSum<kNT> row_sum{red};
   const Ring<T, kThreads, kNV, kJoin ? 2 : 1> ring(dyn4);
   const int lane = threadIdx.x % kNT;
-  const long long step = (long long)gridDim.x * kRows, row1 = p.rows;
-  long long row = (long long)blockIdx.x * kRows + threadIdx.x / kNT;
+  const int period = kShift ? p.period : 1, kind = kShift ? blockIdx.x % period : 0;
+  const int shift = kShift ? (p.off + kind * p.stride_mod) & (V - 1) : 0;
+  const long long step = (long long)gridDim.x * kRows, row1 = p.rows;  // (CTAs of a kind: / period)
+  long long row = ((long long)(blockIdx.x / period) * kRows + threadIdx.x / kNT) * period + kind;
   const float inv_c = 1.f / (float)p.C;
   auto fetch = [&](int stage, long long r) {
     if (r < row1) {
 #pragma unroll
       for (int i = 0; i < kNV; ++i) {
-        const int c = (i * kNT + lane) * V;
+        const int c = (i * kNT + lane) * V - shift;
         if (c < p.C) {
           if constexpr (kJoin)
             ring.fetch(stage, 1, i, static_cast<const T *>(p.a) + r * p.as + c);
@@ -550,20 +620,26 @@ __global__ void __launch_bounds__(kRingThreads<kNT>) fwd_ring(const NormFwdParam
     if (p.w_next)
 #pragma unroll
       for (int i = 0; i < kNV; ++i)
-        if ((i * kNT + lane) * V < p.C) load_w2<T>(p.w_next, (i * kNT + lane) * V, p.wf32, wn[i]);
+        if ((i * kNT + lane) * V - shift < p.C)
+        weights_at<T, kShift>(p.w_next, 0, (i * kNT + lane) * V - shift, p.C, p.wf32, wn[i]);
   }
   const f2 skip = f2_of(p.skip, p.skip);
   int stage = 0;
+  auto read = [&](int array, int i, f2 (&f)[P]) {
+    ring.read(stage, array, i, f);
+    const int c = (i * kNT + lane) * V - shift;
+    if (kShift && !inside<T>(c, p.C)) zero_outside<T>(f, c, p.C);
+  };
   // a warp stays until its last row is done: the sums of rows take part in full
-  for (long long first = row - threadIdx.x % 32 / kNT; first < row1; first += step, row += step) {
+  for (long long first = row - threadIdx.x % 32 / kNT * period; first < row1; first += step, row += step) {
     const bool in = row < row1;
     const long long gate = kJoin && p.gate && in ? (unsigned)row / (unsigned)p.gate_rows : 0;
     if (kKeep && kJoin && gate != held) {
       held = gate;
 #pragma unroll
       for (int i = 0; i < kNV; ++i) {
-        const int c = (i * kNT + lane) * V;
-        if (c < p.C) branch_factor<T>(p, c, gate * p.C, fac[kJoin && kKeep ? i : 0]);
+        const int c = (i * kNT + lane) * V - shift;
+        if (c < p.C) branch_factor<T, kShift>(p, c, gate * p.C, fac[kJoin && kKeep ? i : 0]);
       }
     }
     cp_async_wait<kDepth - 1>();
@@ -573,8 +649,8 @@ __global__ void __launch_bounds__(kRingThreads<kNT>) fwd_ring(const NormFwdParam
     if constexpr (kJoin) {
 #pragma unroll
       for (int i = 0; i < kNV; ++i)
-        if (in && (i * kNT + lane) * V < p.C) {
-          ring.read(stage, 1, i, y[i]);
+        if (in && (i * kNT + lane) * V - shift < p.C) {
+          read(1, i, y[i]);
 #pragma unroll
           for (int e = 0; e < P; ++e) ss2 = fma2(y[i][e], y[i][e], ss2);
         }
@@ -587,18 +663,18 @@ __global__ void __launch_bounds__(kRingThreads<kNT>) fwd_ring(const NormFwdParam
     const f2 rstd_a2 = f2_of(rstd_a, rstd_a);
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
-      const int c = (i * kNT + lane) * V;
+      const int c = (i * kNT + lane) * V - shift;
       if (in && c < p.C) {
         f2 x[P];
-        ring.read(stage, 0, i, x);
+        read(0, i, x);
         if constexpr (kJoin) {
           f2 f[P];
-          if constexpr (!kKeep) branch_factor<T>(p, c, gate * p.C, f);
+          if constexpr (!kKeep) branch_factor<T, kShift>(p, c, gate * p.C, f);
 #pragma unroll
           for (int e = 0; e < P; ++e)
             y[i][e] = fma2(mul2(y[i][e], rstd_a2), kKeep ? fac[kKeep ? i : 0][e] : f[e],
                            mul2(skip, x[e]));
-          put<T>(static_cast<T *>(p.y) + row * p.ys + c, y[i]);
+          put_at<T, kShift>(static_cast<T *>(p.y) + row * p.ys, c, p.C, y[i]);
         } else {
 #pragma unroll
           for (int e = 0; e < P; ++e) y[i][e] = x[e];
@@ -616,20 +692,20 @@ __global__ void __launch_bounds__(kRingThreads<kNT>) fwd_ring(const NormFwdParam
     const f2 rstd2 = f2_of(rstd, rstd);
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
-      const int c = (i * kNT + lane) * V;
+      const int c = (i * kNT + lane) * V - shift;
       if (in && c < p.C) {
         f2 w[P];
-        if constexpr (!kKeep) load_w2<T>(p.w_next, c, p.wf32, w);
+        if constexpr (!kKeep) weights_at<T, kShift>(p.w_next, 0, c, p.C, p.wf32, w);
 #pragma unroll
         for (int e = 0; e < P; ++e)
           w[e] = mul2(mul2(y[i][e], rstd2), kKeep ? wn[kKeep ? i : 0][e] : w[e]);
-        put<T>(static_cast<T *>(p.h) + row * p.hs + c, w);
+        put_at<T, kShift>(static_cast<T *>(p.h) + row * p.hs, c, p.C, w);
       }
     }
   }
 }
 
-template <typename T, int kNT, int kNV, bool kJoin, int kDepth>
+template <typename T, int kNT, int kNV, bool kJoin, int kDepth, bool kShift>
 __global__ void __launch_bounds__(kRingThreads<kNT>, kJoin ? 512 / kRingThreads<kNT> : kNV == 1 ? 1024 / kRingThreads<kNT> : 1)
     bwd_ring(const NormBwdParams p) {
   constexpr int V = 16 / sizeof(T), P = V / 2, kThreads = kRingThreads<kNT>;
@@ -643,8 +719,12 @@ __global__ void __launch_bounds__(kRingThreads<kNT>, kJoin ? 512 / kRingThreads<
   const Ring<T, kThreads, kNV, kJoin ? 4 : 3> ring(dyn4);
   const int lane = threadIdx.x % kNT, sub = threadIdx.x / kNT;
   const int group = blockIdx.x / p.ctas, cta = blockIdx.x % p.ctas;
-  const long long row1 = (group + 1) * p.gate_rows, step = (long long)p.ctas * kRows;
-  long long row = group * p.gate_rows + (long long)cta * kRows + sub;
+  const int period = kShift ? p.period : 1, kind = kShift ? cta % period : 0;
+  const int shift = kShift ? (p.off + kind * p.stride_mod) & (V - 1) : 0;
+  const long long row0 = group * p.gate_rows;
+  const long long row1 = row0 + p.gate_rows, step = (long long)p.ctas * kRows;
+  long long row = row0 + ((long long)(cta / period) * kRows + sub) * period;
+  if constexpr (kShift) row += ((kind - row0) % period + period) % period;  // the group's first
   const float inv_c = 1.f / (float)p.C;
   const f2 zero = f2_of(0.f, 0.f);
   f2 accN[kNV][P], accA[kJoin ? kNV : 1][P];
@@ -666,7 +746,7 @@ __global__ void __launch_bounds__(kRingThreads<kNT>, kJoin ? 512 / kRingThreads<
     if (r < row1) {
 #pragma unroll
       for (int i = 0; i < kNV; ++i) {
-        const int c = (i * kNT + lane) * V;
+        const int c = (i * kNT + lane) * V - shift;
         if (c < p.C) {
           if (p.w_next) {
             ring.fetch(stage, kDh, i, static_cast<const T *>(p.dh) + r * p.dhs + c);
@@ -686,18 +766,23 @@ __global__ void __launch_bounds__(kRingThreads<kNT>, kJoin ? 512 / kRingThreads<
   if constexpr (kKeep) {
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
-      const int c = (i * kNT + lane) * V;
+      const int c = (i * kNT + lane) * V - shift;
       if (c < p.C) {
-        if (p.w_next) load_w2<T>(p.w_next, c, p.wf32, wn[i]);
+        if (p.w_next) weights_at<T, kShift>(p.w_next, 0, c, p.C, p.wf32, wn[i]);
         if (kJoin && !p.row_gate)
-          branch_factor<T>(p, c, (long long)group * p.C, fac[kJoin ? i : 0]);
+          branch_factor<T, kShift>(p, c, (long long)group * p.C, fac[kJoin ? i : 0]);
       }
     }
   }
   stats(row);
   const f2 skip = f2_of(p.skip, p.skip), branch = f2_of(p.branch, p.branch);
   int stage = 0;
-  for (long long first = row - threadIdx.x % 32 / kNT; first < row1; first += step, row += step) {
+  auto read = [&](int array, int i, f2 (&f)[P]) {
+    ring.read(stage, array, i, f);
+    const int c = (i * kNT + lane) * V - shift;
+    if (kShift && !inside<T>(c, p.C)) zero_outside<T>(f, c, p.C);
+  };
+  for (long long first = row - threadIdx.x % 32 / kNT * period; first < row1; first += step, row += step) {
     const bool in = row < row1;
     const float rstd_y = next_y, rstd_a = next_a;
     const f2 rstd_y2 = f2_of(rstd_y, rstd_y), rstd_a2 = f2_of(rstd_a, rstd_a);
@@ -709,12 +794,12 @@ __global__ void __launch_bounds__(kRingThreads<kNT>, kJoin ? 512 / kRingThreads<
       f2 c1_2 = zero;
 #pragma unroll
       for (int i = 0; i < kNV; ++i) {
-        const int c = (i * kNT + lane) * V;
+        const int c = (i * kNT + lane) * V - shift;
         if (in && c < p.C) {
           f2 q[P], w[P];
-          ring.read(stage, kDh, i, D[i]);
-          ring.read(stage, kY, i, q);
-          if constexpr (!kKeep) load_w2<T>(p.w_next, c, p.wf32, w);
+          read(kDh, i, D[i]);
+          read(kY, i, q);
+          if constexpr (!kKeep) weights_at<T, kShift>(p.w_next, 0, c, p.C, p.wf32, w);
 #pragma unroll
           for (int e = 0; e < P; ++e) {
             q[e] = mul2(q[e], rstd_y2);
@@ -731,18 +816,18 @@ __global__ void __launch_bounds__(kRingThreads<kNT>, kJoin ? 512 / kRingThreads<
     f2 c2_2 = zero;
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
-      const int c = (i * kNT + lane) * V;
+      const int c = (i * kNT + lane) * V - shift;
       if (in && c < p.C) {
         f2 t[P];
         if (p.dy) {
-          ring.read(stage, kDy, i, t);
+          read(kDy, i, t);
         } else {
 #pragma unroll
           for (int e = 0; e < P; ++e) t[e] = zero;
         }
         if (p.w_next) {
           f2 y[P];
-          ring.read(stage, kY, i, y);
+          read(kY, i, y);
 #pragma unroll
           for (int e = 0; e < P; ++e)
             D[i][e] = fma2(rstd_y2, fma2(y[e], nc1_2, D[i][e]), t[e]);
@@ -751,15 +836,15 @@ __global__ void __launch_bounds__(kRingThreads<kNT>, kJoin ? 512 / kRingThreads<
           for (int e = 0; e < P; ++e) D[i][e] = t[e];
         }
         if constexpr (!kJoin) {
-          put<T>(static_cast<T *>(p.dx) + row * p.dxs + c, D[i]);
+          put_at<T, kShift>(static_cast<T *>(p.dx) + row * p.dxs, c, p.C, D[i]);
         } else {
 #pragma unroll
           for (int e = 0; e < P; ++e) t[e] = mul2(D[i][e], skip);
-          put<T>(static_cast<T *>(p.dx) + row * p.dxs + c, t);
+          put_at<T, kShift>(static_cast<T *>(p.dx) + row * p.dxs, c, p.C, t);
           f2 z[P], f[P];
-          ring.read(stage, kA, i, z);
+          read(kA, i, z);
           if (!kKeep || p.row_gate)
-            branch_factor<T>(p, c, (p.row_gate ? row : (long long)group) * p.C, f);
+            branch_factor<T, kShift>(p, c, (p.row_gate ? row : (long long)group) * p.C, f);
           else
 #pragma unroll
             for (int e = 0; e < P; ++e) f[e] = fac[kKeep ? i : 0][e];
@@ -772,17 +857,19 @@ __global__ void __launch_bounds__(kRingThreads<kNT>, kJoin ? 512 / kRingThreads<
           }
           if (p.row_gate) {
             f2 g[P], w[P];
-            load_w2<T>(p.gate, row * p.C + c, p.wf32, g);
+            weights_at<T, kShift>(p.gate, row * p.C, c, p.C, p.wf32, g);
 #pragma unroll
             for (int e = 0; e < P; ++e) w[e] = f2_of(1.f, 1.f);
-            if (p.w_post) load_w2<T>(p.w_post, c, p.wf32, w);
+            if (p.w_post) weights_at<T, kShift>(p.w_post, 0, c, p.C, p.wf32, w);
 #pragma unroll
             for (int e = 0; e < P; ++e) {
               t[e] = mul2(t[e], branch);
               float d0, d1;
               f2_to(mul2(t[e], w[e]), d0, d1);
-              store_w<T>(p.dgate, row * p.C + c + 2 * e, p.wf32, d0);
-              store_w<T>(p.dgate, row * p.C + c + 2 * e + 1, p.wf32, d1);
+              if (!kShift || (unsigned)(c + 2 * e) < (unsigned)p.C)
+                store_w<T>(p.dgate, row * p.C + c + 2 * e, p.wf32, d0);
+              if (!kShift || (unsigned)(c + 2 * e + 1) < (unsigned)p.C)
+                store_w<T>(p.dgate, row * p.C + c + 2 * e + 1, p.wf32, d1);
               t[e] = mul2(t[e], g[e]);
             }
           }
@@ -797,16 +884,16 @@ __global__ void __launch_bounds__(kRingThreads<kNT>, kJoin ? 512 / kRingThreads<
       const f2 nc2_2 = f2_of(nc2, nc2);
 #pragma unroll
       for (int i = 0; i < kNV; ++i) {
-        const int c = (i * kNT + lane) * V;
+        const int c = (i * kNT + lane) * V - shift;
         if (in && c < p.C) {
           if (p.w_post) {
             f2 a[P];
-            ring.read(stage, kA, i, a);
+            read(kA, i, a);
 #pragma unroll
             for (int e = 0; e < P; ++e)
               D[i][e] = mul2(rstd_a2, fma2(a[e], nc2_2, D[i][e]));
           }
-          put<T>(static_cast<T *>(p.da) + row * p.das + c, D[i]);
+          put_at<T, kShift>(static_cast<T *>(p.da) + row * p.das, c, p.C, D[i]);
         }
       }
     }
@@ -818,16 +905,11 @@ __global__ void __launch_bounds__(kRingThreads<kNT>, kJoin ? 512 / kRingThreads<
   if constexpr (kRows == 1) {
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
-      const int c = (i * kNT + lane) * V;
-      if (c < p.C)
-#pragma unroll
-        for (int e = 0; e < P; e += 2) {
-          *reinterpret_cast<ulonglong2 *>(out + c + 2 * e) =
-              make_ulonglong2(accN[i][e], accN[i][e + 1]);
-          if constexpr (kJoin)
-            *reinterpret_cast<ulonglong2 *>(out + p.C + c + 2 * e) =
-                make_ulonglong2(accA[i][e], accA[i][e + 1]);
-        }
+      const int c = (i * kNT + lane) * V - shift;
+      if (c < p.C) {
+        put_sums<kShift>(out, c, p.C, accN[i]);
+        if constexpr (kJoin) put_sums<kShift>(out + p.C, c, p.C, accA[i]);
+      }
     }
   } else {
     float *dyn = reinterpret_cast<float *>(dyn4);
@@ -837,13 +919,8 @@ __global__ void __launch_bounds__(kRingThreads<kNT>, kJoin ? 512 / kRingThreads<
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < kNV; ++i) {
-        const int c = (i * kNT + lane) * V;
-        if (c < p.C)
-#pragma unroll
-          for (int e = 0; e < P; e += 2)
-            *reinterpret_cast<ulonglong2 *>(dyn + sub * p.C + c + 2 * e) =
-                k ? make_ulonglong2(accA[kJoin ? i : 0][e], accA[kJoin ? i : 0][e + 1])
-                  : make_ulonglong2(accN[i][e], accN[i][e + 1]);
+        const int c = (i * kNT + lane) * V - shift;
+        if (c < p.C) put_sums<kShift>(dyn + sub * p.C, c, p.C, k ? accA[kJoin ? i : 0] : accN[i]);
       }
       __syncthreads();
       for (int c = threadIdx.x; c < p.C; c += kThreads) {
@@ -1035,7 +1112,8 @@ __global__ void __launch_bounds__(1024) bwd_sums(const NormBwdParams p) {
 // ------------------------------------------------------------------------------- dispatch
 // Rows of n 16-byte vectors: as few lanes as hold a row with one vector each up to a warp; then
 // two vectors a thread, but one for a plain norm's backward.  Rows that only elements address
-// (V = 1) take the register form, longer ones the long form.
+// (V = 1: tensors that lie on the grid of vectors in different ways, few rows of one alignment)
+// take the register form, longer ones the long form.
 template <int kNT, int kNV>
 struct Shape {
   static constexpr int nt = kNT, nv = kNV;
@@ -1081,7 +1159,8 @@ int resident(K kernel, int threads, size_t smem) {
 
 template <typename T, int V, bool kJoin>
 cudaError_t fwd(const NormFwdParams &p, cudaStream_t s) {
-  const int n = (p.C + V - 1) / V;
+  // a shifted row covers V - 1 columns more at most
+  const int n = (p.C + (p.period ? V - 1 : 0) + V - 1) / V;
   auto go = [&](auto kernel, int threads, int rows) {
     kernel<<<(unsigned)((p.rows + rows - 1) / rows), threads, 0, s>>>(p);
     return cudaGetLastError();
@@ -1092,14 +1171,20 @@ cudaError_t fwd(const NormFwdParams &p, cudaStream_t s) {
       constexpr int kNT = decltype(shape)::nt, kNV = decltype(shape)::nv;
       constexpr int kThreads = kRingThreads<kNT>, kRows = kThreads / kNT;
       constexpr int kDepth = kNV == 4 ? 2 : 3;
-      const auto kernel = fwd_ring<T, kNT, kNV, kJoin, kDepth>;
       const size_t smem = (size_t)kDepth * (kJoin ? 2 : 1) * kNV * kThreads * 16;
-      const cudaError_t e = ring_smem(kernel, smem);
-      if (e != cudaSuccess) return e;
-      const long long need = (p.rows + kRows - 1) / kRows;
-      static const int most = resident(kernel, kThreads, smem);
-      kernel<<<(unsigned)(need < most ? need : most), kThreads, smem, s>>>(p);
-      return cudaGetLastError();
+      auto launch = [&](auto shifted) {
+        constexpr bool kShift = decltype(shifted)::value;
+        const auto kernel = fwd_ring<T, kNT, kNV, kJoin, kDepth, kShift>;
+        const cudaError_t e = ring_smem(kernel, smem);
+        if (e != cudaSuccess) return e;
+        static const int most = resident(kernel, kThreads, smem);
+        const int kinds = kShift ? p.period : 1;
+        const long long each = (p.rows + kinds - 1) / kinds, need = (each + kRows - 1) / kRows;
+        kernel<<<(unsigned)((need < most / kinds ? need : most / kinds) * kinds), kThreads, smem,
+                 s>>>(p);
+        return cudaGetLastError();
+      };
+      return p.period ? launch(std::true_type()) : launch(std::false_type());
     });
   } else {
     if (n <= 128) return go(fwd_rows<T, V, 32, 4, kJoin>, 256, 8);
@@ -1118,7 +1203,7 @@ cudaError_t bwd(const NormBwdParams &p, cudaStream_t s) {
     kernel<<<grid, threads, smem, s>>>(p);
     return cudaGetLastError();
   };
-  const int n = (p.C + V - 1) / V;
+  const int n = (p.C + (p.period ? V - 1 : 0) + V - 1) / V;
   cudaError_t e;
   if (n > 2048) {
     e = go(bwd_long<T, V, kJoin>, 512, 0);
@@ -1129,7 +1214,9 @@ cudaError_t bwd(const NormBwdParams &p, cudaStream_t s) {
       constexpr int kDepth = kNV == 4 ? 1 : 3;
       const size_t ring = (size_t)kDepth * (kJoin ? 4 : 3) * kNV * kThreads * 16;
       const size_t sums = kThreads > kNT ? (size_t)(kThreads / kNT) * p.C * 4 : 0;
-      return go(bwd_ring<T, kNT, kNV, kJoin, kDepth>, kThreads, ring > sums ? ring : sums);
+      const size_t smem = ring > sums ? ring : sums;
+      return p.period ? go(bwd_ring<T, kNT, kNV, kJoin, kDepth, true>, kThreads, smem)
+                      : go(bwd_ring<T, kNT, kNV, kJoin, kDepth, false>, kThreads, smem);
     });
   } else if (n <= 128) {
     e = go(bwd_rows<T, V, 32, 4, kJoin, false>, 256, (size_t)8 * p.C * 4);

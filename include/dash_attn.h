@@ -360,8 +360,8 @@ size_t dash_join_bwd_workspace_bytes(long long rows, int C, long long gate_rows,
  * whose dy is added to dx: the gradient of the residual stream beside the norm), a the branch.
  * Writes dx, da and, in the weights' type, dw_post, dgate, dw_next (each where its weight is
  * given).  Row strides of dy, dh, y, a, dx, da in `strides`.  dx and da may each be an input
- * itself, not both the same.  The weight gradients are summed in an order that the sizes alone fix: the
- * same bits on every run. */
+ * itself, not both the same.  The weight gradients are summed in an order that the sizes, strides
+ * and alignments fix: the same bits on every run. */
 dash_status_t dash_join_bwd(const void *dy, const void *dh, const void *y, const void *a,
                             const void *w_post, const void *gate, const void *w_next,
                             const float *rstd_a, const float *rstd_y, void *dx, void *da,

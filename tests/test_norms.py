@@ -190,6 +190,81 @@ def test_norm(L, shape, dtype, res):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+@pytest.mark.parametrize("C", [17, 33, 65, 126, 250, 270, 499, 1001, 1503, 2052, 2731, 5003, 12271,
+                               16361])
+def test_rows_off_the_grid(L, C, dtype):
+    """Enough rows of a length that 16 bytes do not divide, gated per sequence."""
+    run_join((2, 70, C), dtype, dtype, (2, C))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape,gate,wdtype", [((2, 70, 1001), (2, 70, 1001), BF),  # own gates
+                                               ((131, 257), (257,), F32), ((9, 8, 99), (9, 99), F32),
+                                               ((3000, 65), None, BF), ((1, 66, 4099), (4099,), BF)],
+                         ids=str)
+def test_rows_off_the_grid_gates(L, shape, gate, wdtype):
+    run_join(shape, BF, wdtype, gate)
+    run_join(shape, BF, wdtype, gate, post=False, use_dy=False)
+    run_join(shape, BF, wdtype, gate, nxt=False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,C,offset,stride,weights", [
+    (90, 251, 3, 251, 0), (90, 251, 3, 258, 1), (90, 256, 1, 256, 0), (90, 256, 0, 261, 0),
+    (90, 256, 0, 256, 1), (77, 1030, 5, 1036, 3), (77, 64, 7, 71, 0), (70, 9000, 1, 9003, 1)])
+@pytest.mark.parametrize("alike", [True, False])
+def test_rows_off_the_grid_lie(L, dtype, rows, C, offset, stride, weights, alike):
+    """Rows at any offset and stride, the same for all tensors or not, NaN in everything around
+    them: the outputs are right and what lies around them stays."""
+    def lay(t, k=0):  # t's rows at the offset and stride, in a buffer of NaN
+        if not alike:
+            k *= 2
+        else:
+            k = 0
+        buf = torch.full((offset + k + rows * (stride + k) + 64,), float("nan"), dtype=dtype,
+                         device="cuda")
+        v = buf.as_strided((rows, C), (stride + k, 1), offset + k)
+        if t is not None:
+            v.copy_(t)
+        return v, buf
+
+    def around(v, buf):  # all NaN but the rows
+        o = buf.clone()
+        assert not v.isnan().any()
+        o.as_strided(v.shape, v.stride(), v.storage_offset()).fill_(float("nan"))
+        return o.isnan().all()
+
+    def weight(seed):
+        return make((C + weights,), dtype, seed, 0.2, 1.0)[weights:]
+    wp, g, wn = weight(3), weight(4), weight(5)
+    x, a = make((rows, C), dtype, 1, 2.0), make((rows, C), dtype, 2, 0.5)
+    w = dict(w_post=wp, gate=g, w_next=wn)
+    (xv, _), (av, _), (yv, yb), (hv, hb) = lay(x), lay(a, 1), lay(None, 2), lay(None, 3)
+    y, h, ra, ry = dash.join_fwd(xv, av, **w, eps=EPS, y=yv, h=hv)
+    Y, H, RA, RY, ty, th = forward(x, a, wp, g, wn, 1.0, 1.0)
+    near("y", y, Y, ty)
+    near("h", h, H, th)
+    assert around(yv, yb) and around(hv, hb)
+    dy, dh = make((rows, C), dtype, 6), make((rows, C), dtype, 7)
+    (dyv, _), (dhv, _), (dxv, dxb), (dav, dab) = lay(dy), lay(dh, 1), lay(None, 2), lay(None, 3)
+    got = dash.join_bwd(dyv, dhv, yv, av, ra, ry, **w, dx=dxv, da=dav)
+    want = backward(dy, dh, y, a, ra.double()[..., None], ry.double()[..., None], wp, g, wn, 1.0,
+                    1.0)
+    for n, t in zip(("dx", "da", "dw_post", "dgate", "dw_next"), got):
+        near(n, t, *want[n])
+    assert around(dxv, dxb) and around(dav, dab)
+    # in place
+    first, yv[:] = y.clone(), x
+    dash.join_fwd(yv, av, **w, eps=EPS, y=yv, h=av)
+    near("y in place", yv, Y, ty)
+    near("h in place", av, H, th)
+    if alike:
+        assert torch.equal(yv, first) and torch.equal(av, h)
+
+
+@pytest.mark.gpu
 def test_join_gradient_against_differences(L):
     """<gradient, direction> against central differences of the definition in 64 bits, fp32
     rows.  The difference quotient is off by h^2 / 6 of the third derivative, at h = 1e-4 below
