@@ -890,9 +890,8 @@ cudaError_t launch_t(const CUtensorMap &tq, const CUtensorMap &tk, const CUtenso
                      const DiffBwdParams &p, cudaStream_t s) {
   using LQ = DqL<d>;
   using LK = DkvL<d>;
-  static std::atomic<uint64_t> dq_set{0}, dkv_set{0};
-  cudaError_t e = allow_smem(diff_dq_kernel<d>, LQ::kBytes, dq_set);
-  if (e == cudaSuccess) e = allow_smem(diff_dkv_kernel<d>, LK::kBytes, dkv_set);
+  cudaError_t e = allow_smem<diff_dq_kernel<d>>(LQ::kBytes);
+  if (e == cudaSuccess) e = allow_smem<diff_dkv_kernel<d>>(LK::kBytes);
   if (e != cudaSuccess) return e;
   const unsigned tiles = (unsigned)p.B * p.H * p.N;
   diff_rows_kernel<d><<<tiles, 256, 0, s>>>(p);

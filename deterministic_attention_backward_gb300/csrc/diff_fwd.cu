@@ -412,8 +412,7 @@ template <int d>
 cudaError_t launch_t(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                      const DiffFwdParams &p, int sms, cudaStream_t s) {
   using L = FwdL<d>;
-  static std::atomic<uint64_t> set{0};
-  const cudaError_t e = allow_smem(diff_fwd_kernel<d>, L::kBytes, set);
+  const cudaError_t e = allow_smem<diff_fwd_kernel<d>>(L::kBytes);
   if (e != cudaSuccess) return e;
   const int tiles = p.B * p.H * p.N;
   diff_fwd_kernel<d><<<tiles < sms ? tiles : sms, kThreads, L::kBytes, s>>>(tq, tk, tv, p);

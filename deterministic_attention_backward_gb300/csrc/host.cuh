@@ -70,14 +70,15 @@ inline dash_status_t device_info(DevInfo *out) {
   return (d.major == 10 && d.minor == 3) ? DASH_OK : DASH_ERR_UNSUPPORTED;
 }
 
-// Dynamic shared memory of `kernel` on the current device, set once per device (`set`: its bits).
-template <typename K>
-cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t> &set) {
+// Lets kKernel have `bytes` of dynamic shared memory on the current device; asked once per device.
+template <auto kKernel>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> set{0};
   int dev = 0;
   const cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || (set.load() >> dev & 1)) return e;
   const cudaError_t f =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (f == cudaSuccess) set.fetch_or(1ull << dev);
   return f;
 }

@@ -26,6 +26,7 @@
 
 #include "common.cuh"
 #include "elem.cuh"
+#include "host.cuh"
 #include "norm.cuh"
 
 namespace dash {
@@ -1139,19 +1140,26 @@ cudaError_t ring_shape(int n, F go) {
   return go(Shape<512, 4>());
 }
 
-template <typename K>
-cudaError_t ring_smem(K kernel, size_t smem) {
-  if (smem <= 32 * 1024) return cudaSuccess;  // (48 KB less what is static)
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+// A launch with `smem` bytes of dynamic shared memory.
+constexpr int kMostSmem = 226 * 1024;
+template <auto kKernel, typename Params>
+cudaError_t launch_smem(unsigned grid, int threads, size_t smem, cudaStream_t s, const Params &p) {
+  if (smem > 32 * 1024) {  // (48 KB less what is static)
+    const cudaError_t e = allow_smem<kKernel>(kMostSmem);
+    if (e != cudaSuccess) return e;
+  }
+  kKernel<<<grid, threads, smem, s>>>(p);
+  return cudaGetLastError();
 }
 
-// CTAs of `kernel` that the device holds at once (asked once: the same on every sm_103 device).
-template <typename K>
-int resident(K kernel, int threads, size_t smem) {
+// CTAs of a kernel that the device holds at once (asked once: the same on every sm_103 device).
+template <auto kKernel>
+int resident(int threads, size_t smem) {
   int dev = 0, sms = 0, each = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
+  if (cudaGetDevice(&dev) != cudaSuccess || allow_smem<kKernel>(kMostSmem) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&each, kernel, threads, smem) != cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&each, kKernel, threads, smem) !=
+          cudaSuccess ||
       each < 1)
     return 152;
   return sms * each;
@@ -1174,15 +1182,12 @@ cudaError_t fwd(const NormFwdParams &p, cudaStream_t s) {
       const size_t smem = (size_t)kDepth * (kJoin ? 2 : 1) * kNV * kThreads * 16;
       auto launch = [&](auto shifted) {
         constexpr bool kShift = decltype(shifted)::value;
-        const auto kernel = fwd_ring<T, kNT, kNV, kJoin, kDepth, kShift>;
-        const cudaError_t e = ring_smem(kernel, smem);
-        if (e != cudaSuccess) return e;
-        static const int most = resident(kernel, kThreads, smem);
+        constexpr auto kKernel = fwd_ring<T, kNT, kNV, kJoin, kDepth, kShift>;
+        static const int most = resident<kKernel>(kThreads, smem);
         const int kinds = kShift ? p.period : 1;
         const long long each = (p.rows + kinds - 1) / kinds, need = (each + kRows - 1) / kRows;
-        kernel<<<(unsigned)((need < most / kinds ? need : most / kinds) * kinds), kThreads, smem,
-                 s>>>(p);
-        return cudaGetLastError();
+        return launch_smem<kKernel>(
+            (unsigned)((need < most / kinds ? need : most / kinds) * kinds), kThreads, smem, s, p);
       };
       return p.period ? launch(std::true_type()) : launch(std::false_type());
     });
@@ -1197,16 +1202,10 @@ template <typename T, int V, bool kJoin>
 cudaError_t bwd(const NormBwdParams &p, cudaStream_t s) {
   const unsigned grid = (unsigned)(p.groups * p.ctas);
   constexpr int kSums = kJoin ? 2 : 1;
-  auto go = [&](auto kernel, int threads, size_t smem) {
-    const cudaError_t e = ring_smem(kernel, smem);
-    if (e != cudaSuccess) return e;
-    kernel<<<grid, threads, smem, s>>>(p);
-    return cudaGetLastError();
-  };
   const int n = (p.C + (p.period ? V - 1 : 0) + V - 1) / V;
   cudaError_t e;
   if (n > 2048) {
-    e = go(bwd_long<T, V, kJoin>, 512, 0);
+    e = launch_smem<bwd_long<T, V, kJoin>>(grid, 512, 0, s, p);
   } else if constexpr (V > 1) {
     e = ring_shape<!kJoin>(n, [&](auto shape) {
       constexpr int kNT = decltype(shape)::nt, kNV = decltype(shape)::nv;
@@ -1215,15 +1214,17 @@ cudaError_t bwd(const NormBwdParams &p, cudaStream_t s) {
       const size_t ring = (size_t)kDepth * (kJoin ? 4 : 3) * kNV * kThreads * 16;
       const size_t sums = kThreads > kNT ? (size_t)(kThreads / kNT) * p.C * 4 : 0;
       const size_t smem = ring > sums ? ring : sums;
-      return p.period ? go(bwd_ring<T, kNT, kNV, kJoin, kDepth, true>, kThreads, smem)
-                      : go(bwd_ring<T, kNT, kNV, kJoin, kDepth, false>, kThreads, smem);
+      return p.period ? launch_smem<bwd_ring<T, kNT, kNV, kJoin, kDepth, true>>(grid, kThreads,
+                                                                                smem, s, p)
+                      : launch_smem<bwd_ring<T, kNT, kNV, kJoin, kDepth, false>>(grid, kThreads,
+                                                                                 smem, s, p);
     });
   } else if (n <= 128) {
-    e = go(bwd_rows<T, V, 32, 4, kJoin, false>, 256, (size_t)8 * p.C * 4);
+    e = launch_smem<bwd_rows<T, V, 32, 4, kJoin, false>>(grid, 256, (size_t)8 * p.C * 4, s, p);
   } else if (n <= 512) {
-    e = go(bwd_rows<T, V, 256, 2, kJoin, false>, 256, 0);
+    e = launch_smem<bwd_rows<T, V, 256, 2, kJoin, false>>(grid, 256, 0, s, p);
   } else {
-    e = go(bwd_rows<T, V, 512, 4, kJoin, true>, 512, (size_t)kSums * p.C * 4);
+    e = launch_smem<bwd_rows<T, V, 512, 4, kJoin, true>>(grid, 512, (size_t)kSums * p.C * 4, s, p);
   }
   if (e != cudaSuccess) return e;
   bwd_sums<T, kJoin><<<(p.C + 31) / 32, 1024, 0, s>>>(p);
