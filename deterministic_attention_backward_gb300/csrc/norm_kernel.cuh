@@ -42,7 +42,8 @@ __device__ __forceinline__ void load_w(const void *w, long long at, int wf32, fl
     } else {
 #pragma unroll
       for (int i = 0; i < V / 4; ++i) {
-        const float4 t = *reinterpret_cast<const float4 *>(static_cast<const float *>(w) + at + 4 * i);
+        const float4 t =
+            *reinterpret_cast<const float4 *>(static_cast<const float *>(w) + at + 4 * i);
         f[4 * i] = t.x, f[4 * i + 1] = t.y, f[4 * i + 2] = t.z, f[4 * i + 3] = t.w;
       }
     }
@@ -422,7 +423,8 @@ __global__ void __launch_bounds__(kNT * kRowsPerCta<kNT>)
         const int c = (i * kNT + lane) * V;
         if (c < p.C)
 #pragma unroll
-          for (int e = 0; e < V; ++e) dyn[sub * p.C + c + e] = k ? accA[kJoin ? i : 0][e] : accN[i][e];
+          for (int e = 0; e < V; ++e)
+            dyn[sub * p.C + c + e] = k ? accA[kJoin ? i : 0][e] : accN[i][e];
       }
       __syncthreads();
       for (int c = threadIdx.x; c < p.C; c += kNT * kRows) {
@@ -440,11 +442,8 @@ __global__ void __launch_bounds__(kNT * kRowsPerCta<kNT>)
 // reads for itself (cp.async: no barrier, and a thread's loads for the next rows are in flight
 // while it works on this one without holding registers).  Slot (stage, array, vector) of a
 // thread is 16 bytes at thread * 16 of its own block of kThreads * 16.
-__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
-               "l"(src)
-               : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -460,17 +459,17 @@ constexpr int kRingThreads = kNT < 256 ? (kNT > 32 ? kNT : 256) : kNT;
 template <typename T, int kThreads, int kNV, int kArrays>
 struct Ring {
   static constexpr int P = 8 / sizeof(T);  // pairs of a vector
-  uint8_t *mine;                           // this thread's slots
+  static constexpr uint32_t kStage = kArrays * kNV * kThreads * 16;
+  uint32_t first;  // this thread's slots of stage 0; `at` below: those of a stage
   __device__ __forceinline__ explicit Ring(void *smem)
-      : mine(static_cast<uint8_t *>(smem) + threadIdx.x * 16) {}
-  __device__ __forceinline__ uint8_t *slot(int stage, int array, int i) const {
-    return mine + (size_t)((stage * kArrays + array) * kNV + i) * (kThreads * 16);
+      : first(static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + threadIdx.x * 16) {}
+  __device__ __forceinline__ void fetch(uint32_t at, int array, int i, const T *src) const {
+    cp_async16(at + (array * kNV + i) * (kThreads * 16), src);
   }
-  __device__ __forceinline__ void fetch(int stage, int array, int i, const T *src) const {
-    cp_async16(slot(stage, array, i), src);
-  }
-  __device__ __forceinline__ void read(int stage, int array, int i, f2 (&f)[P]) const {
-    unpack2<T>(*reinterpret_cast<const uint4 *>(slot(stage, array, i)), f);
+  __device__ __forceinline__ void read(uint32_t at, int array, int i, f2 (&f)[P]) const {
+    unpack2<T>(*static_cast<const uint4 *>(
+                   __cvta_shared_to_generic(at + (array * kNV + i) * (kThreads * 16))),
+               f);
   }
 };
 template <typename T>
@@ -593,29 +592,35 @@ __global__ void __launch_bounds__(kRingThreads<kNT>) fwd_ring(const NormFwdParam
   extern __shared__ float4 dyn4[];
   __shared__ float red[2 * (kNT / 32 ? kNT / 32 : 1)];
   RowSum<kNT> row_sum{red};
-  const Ring<T, kThreads, kNV, kJoin ? 2 : 1> ring(dyn4);
+  using R = Ring<T, kThreads, kNV, kJoin ? 2 : 1>;
+  const R ring(dyn4);
+  int stage = 0;
   const int lane = threadIdx.x % kNT;
   const int period = kShift ? p.period : 1, kind = kShift ? blockIdx.x % period : 0;
   const int shift = kShift ? (p.off + kind * p.stride_mod) & (V - 1) : 0;
   const long long step = (long long)gridDim.x * kRows, row1 = p.rows;  // (CTAs of a kind: / period)
   long long row = ((long long)(blockIdx.x / period) * kRows + threadIdx.x / kNT) * period + kind;
   const float inv_c = 1.f / (float)p.C;
-  auto fetch = [&](int stage, long long r) {
-    if (r < row1) {
+  long long ahead = row;  // the row to fetch
+  auto fetch = [&]() {
+    const uint32_t at = ring.first + stage * R::kStage;
+    if (ahead < row1) {
 #pragma unroll
       for (int i = 0; i < kNV; ++i) {
         const int c = (i * kNT + lane) * V - shift;
         if (c < p.C) {
           if constexpr (kJoin)
-            ring.fetch(stage, 1, i, static_cast<const T *>(p.a) + r * p.as + c);
-          ring.fetch(stage, 0, i, static_cast<const T *>(p.x) + r * p.xs + c);
+            ring.fetch(at, 1, i, static_cast<const T *>(p.a) + ahead * p.as + c);
+          ring.fetch(at, 0, i, static_cast<const T *>(p.x) + ahead * p.xs + c);
         }
       }
     }
     cp_async_commit();
+    stage = stage + 1 == kDepth ? 0 : stage + 1;
+    ahead += step;
   };
 #pragma unroll
-  for (int s = 0; s < kDepth; ++s) fetch(s, row + s * step);
+  for (int s = 0; s < kDepth; ++s) fetch();
   f2 wn[kKeep ? kNV : 1][P], fac[kKeep && kJoin ? kNV : 1][P];
   long long held = -1;  // the gate row that `fac` holds
   if constexpr (kKeep) {
@@ -626,14 +631,14 @@ __global__ void __launch_bounds__(kRingThreads<kNT>) fwd_ring(const NormFwdParam
         weights_at<T, kShift>(p.w_next, 0, (i * kNT + lane) * V - shift, p.C, p.wf32, wn[i]);
   }
   const f2 skip = f2_of(p.skip, p.skip);
-  int stage = 0;
   auto read = [&](int array, int i, f2 (&f)[P]) {
-    ring.read(stage, array, i, f);
+    ring.read(ring.first + stage * R::kStage, array, i, f);
     const int c = (i * kNT + lane) * V - shift;
     if (kShift && !inside<T>(c, p.C)) zero_outside<T>(f, c, p.C);
   };
   // a warp stays until its last row is done: the sums of rows take part in full
-  for (long long first = row - threadIdx.x % 32 / kNT * period; first < row1; first += step, row += step) {
+  for (long long first = row - threadIdx.x % 32 / kNT * period; first < row1;
+       first += step, row += step) {
     const bool in = row < row1;
     const long long gate = kJoin && p.gate && in ? (unsigned)row / (unsigned)p.gate_rows : 0;
     if (kKeep && kJoin && gate != held) {
@@ -685,8 +690,7 @@ __global__ void __launch_bounds__(kRingThreads<kNT>) fwd_ring(const NormFwdParam
         for (int e = 0; e < P; ++e) ss2 = fma2(y[i][e], y[i][e], ss2);
       }
     }
-    fetch(stage, row + kDepth * step);  // everything of this stage has been read
-    stage = stage + 1 == kDepth ? 0 : stage + 1;
+    fetch();  // everything of this stage has been read
     if (!p.w_next) continue;
     // the norm takes the joined row before its rounding
     const float rstd = rsqrtf(row_sum(f2_sum(ss2)) * inv_c + p.eps);
@@ -708,7 +712,8 @@ __global__ void __launch_bounds__(kRingThreads<kNT>) fwd_ring(const NormFwdParam
 }
 
 template <typename T, int kNT, int kNV, bool kJoin, int kDepth, bool kShift>
-__global__ void __launch_bounds__(kRingThreads<kNT>, kJoin ? 512 / kRingThreads<kNT> : kNV == 1 ? 1024 / kRingThreads<kNT> : 1)
+__global__ void __launch_bounds__(kRingThreads<kNT>, kJoin ? 512 / kRingThreads<kNT>
+                                                     : kNV == 1 ? 1024 / kRingThreads<kNT> : 1)
     bwd_ring(const NormBwdParams p) {
   constexpr int V = 16 / sizeof(T), P = V / 2, kThreads = kRingThreads<kNT>;
   constexpr int kRows = kThreads / kNT;
@@ -718,7 +723,9 @@ __global__ void __launch_bounds__(kRingThreads<kNT>, kJoin ? 512 / kRingThreads<
   extern __shared__ float4 dyn4[];
   __shared__ float red[2 * (kNT / 32 ? kNT / 32 : 1)];
   RowSum<kNT> row_sum{red};
-  const Ring<T, kThreads, kNV, kJoin ? 4 : 3> ring(dyn4);
+  using R = Ring<T, kThreads, kNV, kJoin ? 4 : 3>;
+  const R ring(dyn4);
+  uint32_t at = ring.first;  // of the stage in turn
   const int lane = threadIdx.x % kNT, sub = threadIdx.x / kNT;
   const int group = blockIdx.x / p.ctas, cta = blockIdx.x % p.ctas;
   const int period = kShift ? p.period : 1, kind = kShift ? cta % period : 0;
@@ -744,26 +751,29 @@ __global__ void __launch_bounds__(kRingThreads<kNT>, kJoin ? 512 / kRingThreads<
       if (kJoin && p.w_post) next_a = p.rstd_a[r];
     }
   };
-  auto fetch = [&](int stage, long long r) {
-    if (r < row1) {
+  long long ahead = row;  // the row to fetch
+  auto fetch = [&]() {
+    if (ahead < row1) {
 #pragma unroll
       for (int i = 0; i < kNV; ++i) {
         const int c = (i * kNT + lane) * V - shift;
         if (c < p.C) {
           if (p.w_next) {
-            ring.fetch(stage, kDh, i, static_cast<const T *>(p.dh) + r * p.dhs + c);
-            ring.fetch(stage, kY, i, static_cast<const T *>(p.y) + r * p.ys + c);
+            ring.fetch(at, kDh, i, static_cast<const T *>(p.dh) + ahead * p.dhs + c);
+            ring.fetch(at, kY, i, static_cast<const T *>(p.y) + ahead * p.ys + c);
           }
-          if (p.dy) ring.fetch(stage, kDy, i, static_cast<const T *>(p.dy) + r * p.dys + c);
+          if (p.dy) ring.fetch(at, kDy, i, static_cast<const T *>(p.dy) + ahead * p.dys + c);
           if constexpr (kJoin)
-            ring.fetch(stage, kA, i, static_cast<const T *>(p.a) + r * p.as + c);
+            ring.fetch(at, kA, i, static_cast<const T *>(p.a) + ahead * p.as + c);
         }
       }
     }
     cp_async_commit();
+    at = at + R::kStage == ring.first + kDepth * R::kStage ? ring.first : at + R::kStage;
+    ahead += step;
   };
 #pragma unroll
-  for (int s = 0; s < kDepth; ++s) fetch(s, row + s * step);
+  for (int s = 0; s < kDepth; ++s) fetch();
   f2 wn[kKeep ? kNV : 1][P], fac[kKeep && kJoin ? kNV : 1][P];
   if constexpr (kKeep) {
 #pragma unroll
@@ -778,13 +788,13 @@ __global__ void __launch_bounds__(kRingThreads<kNT>, kJoin ? 512 / kRingThreads<
   }
   stats(row);
   const f2 skip = f2_of(p.skip, p.skip), branch = f2_of(p.branch, p.branch);
-  int stage = 0;
   auto read = [&](int array, int i, f2 (&f)[P]) {
-    ring.read(stage, array, i, f);
+    ring.read(at, array, i, f);
     const int c = (i * kNT + lane) * V - shift;
     if (kShift && !inside<T>(c, p.C)) zero_outside<T>(f, c, p.C);
   };
-  for (long long first = row - threadIdx.x % 32 / kNT * period; first < row1; first += step, row += step) {
+  for (long long first = row - threadIdx.x % 32 / kNT * period; first < row1;
+       first += step, row += step) {
     const bool in = row < row1;
     const float rstd_y = next_y, rstd_a = next_a;
     const f2 rstd_y2 = f2_of(rstd_y, rstd_y), rstd_a2 = f2_of(rstd_a, rstd_a);
@@ -899,8 +909,7 @@ __global__ void __launch_bounds__(kRingThreads<kNT>, kJoin ? 512 / kRingThreads<
         }
       }
     }
-    fetch(stage, row + kDepth * step);
-    stage = stage + 1 == kDepth ? 0 : stage + 1;
+    fetch();
   }
   // this CTA's sums, one slot per CTA: the rows of a thread added in order, then the row groups
   float *out = p.part + (size_t)blockIdx.x * kSums * p.C;
