@@ -88,8 +88,8 @@ Lie lie_of(const void *const (&ptrs)[N], const long long *strides, const void *c
   while ((l.period * l.stride_mod) & (vec - 1)) l.period *= 2;
   // A CTA takes rows of one alignment: with few rows of each, or rows of a few vectors, it would
   // stand half empty, and element by element they take a launch's time as well.  At 22324 rows of
-  // 1503 in bf16 the join takes 62 us forward, 126 backward (by elements 146, 212), at 124275 rows
-  // of 270 97 and 199 (244, 599).  Rows beyond the ring's go element by element.
+  // 1503 in bf16 the join takes 60 us forward, 128 backward (by elements 146, 212), at 124275 rows
+  // of 270 98 and 200 (244, 599).  Rows beyond the ring's go element by element.
   l.wide = same && C >= 2 * vec && group_rows >= 8 * l.period && (C + 2 * vec - 2) / vec <= 2048;
   if (!l.wide) l.period = 0;
   return l;

@@ -16,12 +16,12 @@
 // `part`, and a second kernel adds the CTAs' sums in a fixed order -- no atomics, the same
 // bits on every run.
 //
-// Measured in bf16 (of a plain copy's rate): the join of 16384 rows of 4096 forward 92 us, 5.8 TB/s
-// (86 %); backward 172 us, 4.7 TB/s (69 %): three factors and three column sums of 16 columns a
-// thread fill the registers, so two CTAs of 8 warps share an SM, and each row's two sums stand
-// between its loads and its stores.  Norms of 4.2 M heads of 128: forward 46 us, backward 69 us
-// (86 %).  Rows off the 16-byte grid cost little more: 22324 rows of 1503 in bf16 the join forward
-// 62 us, backward 126 us (of 1504: 54 and 110).
+// Measured in bf16 (of a plain copy's rate): the join of 16384 rows of 4096 forward 89 us, 6.0 TB/s
+// (89 %); backward 162 us, 5.0 TB/s (73 %): 570 instructions a thread and row of 16 columns, 131 us
+// without its loads, and its factors and column sums fill the registers, so that two CTAs of 8
+// warps share an SM.  Norms of 524288 heads of 128: forward 43 us, backward 68 us (88 %).  Rows off
+// the 16-byte grid cost little more: 22324 rows of 1503 in bf16 the join forward 60 us, backward
+// 128 us (of 1504: 50 and 102).
 #pragma once
 #include <type_traits>
 
