@@ -344,7 +344,8 @@ dash_status_t dash_rope(const dash_rope_part_t *parts, int nparts, int B, int S,
  * [rows] fp32 are kept for the backward (each written only where its norm is asked for).  The
  * weights [C] are of the rows' type or all fp32; gate is [rows / gate_rows, C], each row of it
  * serving gate_rows consecutive rows.  y and h may each be x or a itself (with the same stride),
- * not both the same.  fp32 arithmetic, one rounding per output. */
+ * not both the same.  fp32 arithmetic, one rounding per output.  Tensors are read by whole
+ * aligned words of 16 bytes: of rows that 16 bytes do not divide, with up to 15 bytes beside. */
 dash_status_t dash_join_fwd(const void *x, const void *a, const void *w_post, const void *gate,
                             const void *w_next, void *y, void *h, float *rstd_a, float *rstd_y,
                             long long rows, int C, long long gate_rows,
