@@ -457,6 +457,23 @@ def bwd_varlen_order_log(q, k, v, o, do, lse, cu_seqlens, causal: bool = False,
     return dq, dk, dv, order
 
 
-from .diff import diff_bwd, diff_bwd_workspace_bytes, diff_fwd  # noqa: E402
-from .norms import join_bwd, join_fwd, norm_bwd, norm_fwd  # noqa: E402
-from .rope import rope_bwd, rope_freqs, rope_fwd  # noqa: E402
+# The operators' modules import torch, which the schedule queries and the C ABI do without: they
+# are loaded with the first name that is asked of them.
+_MODULES = {"rope_freqs": "rope", "rope_fwd": "rope", "rope_bwd": "rope", "norm_fwd": "norms",
+            "norm_bwd": "norms", "join_fwd": "norms", "join_bwd": "norms", "diff_fwd": "diff",
+            "diff_bwd": "diff", "diff_bwd_workspace_bytes": "diff"}
+
+
+def __getattr__(name):
+    import importlib
+    if name in _MODULES.values():  # which sets the attribute
+        return importlib.import_module("." + name, __name__)
+    if name not in _MODULES:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    value = getattr(importlib.import_module("." + _MODULES[name], __name__), name)
+    globals()[name] = value
+    return value
+
+
+def __dir__():
+    return sorted({*globals(), *_MODULES, *_MODULES.values()})

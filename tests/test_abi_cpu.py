@@ -239,3 +239,33 @@ def test_varlen_workspace_spans_the_largest_packed_launch(L):
     arr2 = (ct.c_int * len(cu2))(*cu2)
     want = dash.bwd_workspace_bytes(1, (10 * 3 + 2 * 125) * 128, H, D) + table
     assert L.dash_attn_bwd_varlen_workspace_bytes(arr2, len(lens2), H, D) == want
+
+
+def test_package_works_without_torch(L):
+    """The schedule queries need the library alone: no call before the first on tensors loads
+    torch, and what the package offers is listed without it."""
+    import subprocess
+    import sys
+    code = """
+import sys
+sys.modules["torch"] = None  # an import of torch raises
+import deterministic_attention_backward_gb300 as dash
+assert dash.sched_resolve("auto", True, 8) in dash.SCHEDULES
+assert dash.sched_workers("shift", True, 4) > 0 and dash.sched_table("shift", True, 4)
+assert set(dash.__all__) <= set(dir(dash))
+try:
+    dash.no_such_name
+except AttributeError:
+    pass
+else:
+    raise SystemExit("a name that is not there")
+"""
+    subprocess.run([sys.executable, "-c", code], cwd=ROOT, check=True)
+    code = """
+import deterministic_attention_backward_gb300 as dash
+from deterministic_attention_backward_gb300 import *
+assert rope_fwd is dash.rope.rope_fwd and dash.norms.join_bwd is join_bwd
+assert dash.diff.diff_bwd is diff_bwd is dash.diff_bwd
+assert all(callable(getattr(dash, n)) for n in dash.__all__ if n != "SCHEDULES")
+"""
+    subprocess.run([sys.executable, "-c", code], cwd=ROOT, check=True)
