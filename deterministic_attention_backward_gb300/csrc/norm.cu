@@ -51,6 +51,20 @@ bool all_aligned(const void *const (&ptrs)[N], uintptr_t size) {
   return (any & (size - 1)) == 0;
 }
 
+// Whether no two of the outputs begin at one address, nor one of them where one of `reads` does
+// (null ones aside).
+template <int N, int M>
+bool apart(const void *const (&outs)[N], const void *const (&reads)[M]) {
+  for (int i = 0; i < N; ++i) {
+    if (!outs[i]) continue;
+    for (int k = 0; k < i; ++k)
+      if (outs[k] == outs[i]) return false;
+    for (const void *q : reads)
+      if (q == outs[i]) return false;
+  }
+  return true;
+}
+
 dash_status_t check_rows(long long rows, int C, long long gate_rows, bool gate, int dtype,
                          int wdtype) {
   if (rows <= 0 || C <= 0 || !elem_ok(dtype) || (wdtype != dtype && wdtype != DASH_FP32))
@@ -131,6 +145,11 @@ dash_status_t dash_join_fwd(const void *x, const void *a, const void *w_post, co
   const void *fp[] = {rstd_a, rstd_y};
   if (!all_aligned(rowp, size) || !all_aligned(wp, elem_size(wdtype)) || !all_aligned(fp, 4))
     return DASH_ERR_INVALID;
+  // y and h may be x or a; rows written early would be read as weights, or as x by other CTAs, later
+  const void *rows_out[] = {join ? y : nullptr, w_next ? h : nullptr};
+  const void *stats_out[] = {w_post ? rstd_a : nullptr, w_next ? rstd_y : nullptr};
+  const void *stats_reads[] = {x, a, w_post, gate, w_next, rows_out[0], rows_out[1]};
+  if (!apart(rows_out, wp) || !apart(stats_out, stats_reads)) return DASH_ERR_INVALID;
   const Lie lie = lie_of(rowp, strides, wp, C, size, rows);
   const bool wide = lie.wide;
   DevInfo dev;
@@ -195,6 +214,11 @@ dash_status_t dash_join_bwd(const void *dy, const void *dh, const void *y, const
   if (!workspace || !aligned16(workspace) ||
       workspace_bytes < dash_join_bwd_workspace_bytes(rows, C, gate ? gate_rows : 0, join, dtype))
     return DASH_ERR_WORKSPACE;
+  // dx and da may be dy, dh, y or a; the weights are read again after rows have been written
+  const void *outs[] = {dx, join ? da : nullptr, dwp[0], dwp[1], dwp[2], workspace};
+  const void *reads[] = {w_post, gate, w_next, w_post ? rstd_a : nullptr,
+                         w_next ? rstd_y : nullptr};
+  if (!apart(outs, reads)) return DASH_ERR_INVALID;
   const bool own_gates = gate && gate_rows == 1 && rows > 1;
   const Lie lie = lie_of(rowp, strides, wp, C, size, gate && !own_gates ? gate_rows : rows);
   const bool wide = lie.wide;

@@ -12,6 +12,8 @@ norms, forward and backward.
 
 Rows are the last dimension of tensors of any shape (the rest must flatten to one row stride),
 bf16, fp16 or fp32; weights of the rows' type or fp32.  The weight gradients are deterministic.
+Outputs may be row operands themselves (y and h: x or a; dx and da: dy, dh, y or a), at the same
+row stride; no output is a weight, a gate or an rstd.
 """
 from __future__ import annotations
 
@@ -53,9 +55,10 @@ def _out(t, name, like):
     return s
 
 
-def _in_place(outs, ins):
-    """Raise ValueError where an output is the memory of another, or of an input whose rows lie at
-    another stride; both are (tensor, stride of its rows)."""
+def _in_place(outs, ins, weights):
+    """Raise ValueError where an output is the memory of another, of an input whose rows lie at
+    another stride (both are (tensor, stride of its rows)), or of one of ``weights``, which are
+    read after rows have been written."""
     for n, (o, so) in enumerate(outs):
         if o is None:
             continue
@@ -64,6 +67,8 @@ def _in_place(outs, ins):
                 any(t is not None and t.data_ptr() == at and st != so for t, st in ins):
             raise ValueError("an output is the memory of another output, or of an input with "
                              "another stride")
+        if any(w is not None and w.data_ptr() == at for w in weights):
+            raise ValueError("an output is the memory of a weight, a gate or an rstd")
 
 
 def _weights(x, rows, w_post, gate, w_next):
@@ -118,7 +123,7 @@ def _forward(x, a, w_post, gate, w_next, skip_scale, branch_scale, eps, y, h, st
         h = None
     ys, hs = _out(y, "y", x), _out(h, "h" if join else "out", x)
     if y is not None or h is not None:
-        _in_place(((y, ys), (h, hs)), ((x, xs), (a, as_)))
+        _in_place(((y, ys), (h, hs)), ((x, xs), (a, as_)), (w_post, gate, w_next))
 
     def launch(handle):
         Y, H, ra, ry = y, h, None, None
@@ -169,7 +174,8 @@ def _backward(dy, dh, y, a, rstd_a, rstd_y, w_post, gate, w_next, skip_scale, br
                 raise ValueError(f"{n} must be contiguous")
     dxs, das = _out(dx, "dx", base), _out(da, "da", base)
     if dx is not None or da is not None:
-        _in_place(((dx, dxs), (da, das)), ((dy, dys), (dh, dhs), (y, ys), (a, as_)))
+        _in_place(((dx, dxs), (da, das)), ((dy, dys), (dh, dhs), (y, ys), (a, as_)),
+                  (w_post, gate, w_next, rstd_a, rstd_y))
 
     def launch(handle):
         DX, DA = _like(base) if dx is None else dx, da

@@ -436,3 +436,52 @@ def test_abi_refusals(L):
     assert norms.join_bwd_workspace_bytes(6, 8, BF, 4) == 0
     a = norms.join_bwd_workspace_bytes(6, 4096, BF)
     assert a >= 6 * 2 * 4096 * 4 and norms.norm_bwd_workspace_bytes(6, 4096, BF) < a
+
+
+def test_abi_refuses_outputs_in_memory_that_is_read(L):
+    """An output may be a row operand itself, not a weight, a gate, a row's rstd or another
+    output: rows written early would be read as weights later."""
+    ll = ctypes.c_longlong
+    far = {n: (i + 1) << 24 for i, n in enumerate(  # never dereferenced: no device, or refused
+        ("x", "a", "wp", "g", "wn", "y", "h", "ra", "ry"))}
+
+    def fwd(**same):
+        p = {**far, **{n: far[m] for n, m in same.items()}}
+        return L.dash_join_fwd(*p.values(), 6, 8, 3, (ll * 4)(8, 8, 8, 8), 1.0, 1.0, 1e-5, 0, 0,
+                               None)
+    for out in ("y", "h"):
+        for m in ("wp", "g", "wn"):
+            assert fwd(**{out: m}) == 1, (out, m)
+    assert fwd(y="h") == 1 and fwd(ra="ry") == 1 and fwd(ra="x") == 1 and fwd(ry="g") == 1
+    far = {n: (i + 1) << 24 for i, n in enumerate(
+        ("dy", "dh", "y", "a", "wp", "g", "wn", "ra", "ry", "dx", "da", "dwp", "dg", "dwn"))}
+
+    def bwd(**same):
+        p = {**far, **{n: far[m] for n, m in same.items()}}
+        return L.dash_join_bwd(*p.values(), 6, 8, 1, (ll * 6)(*[8] * 6), 1.0, 1.0, 0, 0, 1 << 20,
+                               1 << 30, None)
+    for out in ("dx", "da", "dwp", "dg", "dwn"):
+        for m in ("wp", "g", "wn", "ra", "ry"):
+            assert bwd(**{out: m}) == 1, (out, m)
+    assert bwd(dx="da") == 1 and bwd(dwp="dx") == 1 and bwd(dwn="dg") == 1
+
+
+@pytest.mark.gpu
+def test_refuses_outputs_that_are_weights(L):
+    x = torch.ones(4, 6, 64, dtype=BF, device="cuda")
+    one = torch.ones(1, 64, dtype=BF, device="cuda")
+    w, rstd, gate = one[0], torch.ones(4, 6, device="cuda"), x.clone()
+
+    def no(f, *a, **k):
+        with pytest.raises(ValueError):
+            f(*a, **k)
+    no(dash.join_fwd, x, x, gate=gate, w_next=w, y=gate)
+    no(dash.join_fwd, x, x, gate=gate, w_next=w, h=gate)
+    no(dash.norm_fwd, one, w, out=one)                      # a row that is its weight
+    for out in ("dx", "da"):
+        no(dash.join_bwd, x, x, x, x, rstd, rstd, w_post=w, gate=gate, w_next=w, **{out: gate})
+        no(dash.join_bwd, one, one, one, one, rstd[0, :1], rstd[0, :1], w_post=w, w_next=w.clone(),
+           **{out: one})
+    r = torch.ones(6, 1, device="cuda")                     # rows of one element in fp32
+    no(dash.norm_bwd, r, r, r[:, 0], torch.ones(1, device="cuda"), dx=r)
+    dash.join_bwd(x, x, x.clone(), x.clone(), rstd, rstd, w_post=w, gate=gate, w_next=w, dx=x)
