@@ -94,6 +94,14 @@ bool lam_ok(const void *lam, int dtype) {
          (reinterpret_cast<uintptr_t>(lam) & (dtype == DASH_FP32 ? 3 : 1)) == 0;
 }
 
+// The bytes of a bf16 tensor of `heads` heads of 2d, and of the weights.
+Bytes heads_of(const void *p, int B, int S, int heads, int d) {
+  return bytes_of(p, 2, (long long)B * S * heads * 2 * d);
+}
+Bytes weights_of(const void *p, int B, int S, int H, int dtype, bool per_token) {
+  return bytes_of(p, dtype == DASH_FP32 ? 4 : 2, per_token ? (long long)B * S * H : H);
+}
+
 }  // namespace
 }  // namespace dash
 
@@ -122,9 +130,16 @@ dash_status_t dash_diff_fwd(const void *q, const void *k, const void *v, const v
   if (!lse || !aligned4(lse) || !lam_ok(lam, lam_dtype)) return DASH_ERR_INVALID;
   if (!workspace || workspace_bytes < kStatusBytes || !aligned16(workspace))
     return DASH_ERR_WORKSPACE;
+  const int Hkv = H / group;
+  const Bytes outs[] = {heads_of(o, B, S, H, d), heads_of(o2, B, S, H, d),
+                        bytes_of(lse, 4, (long long)B * 2 * H * S),
+                        bytes_of(workspace, 1, kStatusBytes)};
+  const Bytes reads[] = {heads_of(q, B, S, H, d), heads_of(k, B, S, Hkv, d),
+                         heads_of(v, B, S, Hkv, d),
+                         weights_of(lam, B, S, H, lam_dtype, lam_per_token)};
+  if (!apart(outs, reads)) return DASH_ERR_INVALID;
   DevInfo dev;
   if ((st = device_info(&dev)) != DASH_OK) return st;
-  const int Hkv = H / group;
   CUtensorMap tq, tk, tv;
   if (!make_bshd_map(&tq, q, B, S, H, 2 * d) || !make_bshd_map(&tk, k, B, S, Hkv, 2 * d) ||
       !make_bshd_map(&tv, v, B, S, Hkv, 2 * d))
@@ -164,9 +179,19 @@ dash_status_t dash_diff_bwd(const void *q, const void *k, const void *v, const v
     return DASH_ERR_INVALID;
   const DiffWorkspace w = carve(workspace, B, S, H, d);
   if (!workspace || !aligned16(workspace) || workspace_bytes < w.total) return DASH_ERR_WORKSPACE;
+  const int Hkv = H / group;
+  const Bytes outs[] = {heads_of(dq, B, S, H, d), heads_of(dk, B, S, Hkv, d),
+                        heads_of(dv, B, S, Hkv, d),
+                        weights_of(dlam, B, S, H, lam_dtype, lam_per_token),
+                        bytes_of(workspace, 1, (long long)w.total)};
+  const Bytes reads[] = {heads_of(q, B, S, H, d), heads_of(k, B, S, Hkv, d),
+                         heads_of(v, B, S, Hkv, d), heads_of(o, B, S, H, d),
+                         heads_of(o2, B, S, H, d), heads_of(dout, B, S, H, d),
+                         bytes_of(lse, 4, (long long)B * 2 * H * S),
+                         weights_of(lam, B, S, H, lam_dtype, lam_per_token)};
+  if (!apart(outs, reads)) return DASH_ERR_INVALID;
   DevInfo dev;
   if ((st = device_info(&dev)) != DASH_OK) return st;
-  const int Hkv = H / group;
   CUtensorMap tq, tk, tv, tdo;
   // Q and dO stream through dK/dV's kernel by half tiles, K and V are read by whole ones
   if (!make_bshd_map(&tq, q, B, S, H, 2 * d, kTile / 2) ||

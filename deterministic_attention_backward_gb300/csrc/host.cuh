@@ -88,6 +88,98 @@ inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 
 inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
+// The bytes of a tensor, as runs of `run` bytes whose begins lie on up to three steps, the
+// narrowest first.
+struct Bytes {
+  uintptr_t at = 0;
+  long long run = 0;
+  int dims = 0;
+  long long step[3] = {}, count[3] = {};
+  long long span() const {  // from the first byte to behind the last
+    long long s = run;
+    for (int i = 0; i < dims; ++i) s += step[i] * (count[i] - 1);
+    return s;
+  }
+};
+// One block, or `count` runs of `run` elements at a stride of `stride` elements, and so on outwards.
+// A null pointer has no bytes.
+inline Bytes bytes_of(const void *p, int size, long long run) {
+  Bytes b;
+  b.at = reinterpret_cast<uintptr_t>(p);
+  b.run = p ? run * size : 0;
+  return b;
+}
+inline Bytes along(Bytes b, int size, long long stride, long long count) {
+  long long step = stride * size;
+  if (count <= 1 || step == 0) return b;
+  if (step < 0) b.at += (uintptr_t)(step * (count - 1)), step = -step;
+  int i = b.dims++;
+  for (; i > 0 && b.step[i - 1] > step; --i)
+    b.step[i] = b.step[i - 1], b.count[i] = b.count[i - 1];
+  b.step[i] = step, b.count[i] = count;
+  return b;
+}
+// Steps that continue what lies inside them become longer runs, or more of them.
+inline Bytes flat(const Bytes &b) {
+  Bytes r = b;
+  r.dims = 0;
+  for (int i = 0; i < b.dims; ++i) {
+    const int k = r.dims - 1;
+    if (k < 0 && b.step[i] == r.run)
+      r.run *= b.count[i];
+    else if (k >= 0 && b.step[i] == r.step[k] * r.count[k])
+      r.count[k] *= b.count[i];
+    else
+      r.step[k + 1] = b.step[i], r.count[k + 1] = b.count[i], r.dims = k + 2;
+  }
+  return r;
+}
+// Whether two tensors have a byte in common.  Gives up (false) after `tries` comparisons of parts,
+// which takes strides that hardly occur.
+inline bool share_parts(const Bytes &a, const Bytes &b, int &tries) {
+  if (a.at + a.span() <= b.at || b.at + b.span() <= a.at || !a.run || !b.run) return false;
+  if (a.at == b.at || (a.dims == 0 && b.dims == 0)) return true;
+  if (a.dims == 1 && b.dims == 1 && a.step[0] == b.step[0] && a.step[0] >= a.run &&
+      a.step[0] >= b.run) {
+    // run i of a begins `behind` bytes after run i + by of b
+    const long long step = a.step[0], d = (long long)(a.at - b.at);
+    const long long behind = (d % step + step) % step, by = (d - behind) / step;
+    auto meet = [&](long long k) {  // whether a run i of a has a run i + k of b
+      return (k < 0 ? -k : 0) < (a.count[0] < b.count[0] - k ? a.count[0] : b.count[0] - k);
+    };
+    return (behind < b.run && meet(by)) || (behind + a.run > step && meet(by + 1));
+  }
+  if (a.dims < b.dims || (a.dims == b.dims && a.step[a.dims - 1] < b.step[b.dims - 1]))
+    return share_parts(b, a, tries);
+  Bytes part = a;  // a's parts along its widest step, those that reach b
+  const long long step = a.step[a.dims - 1], n = a.count[a.dims - 1];
+  part.dims = a.dims - 1;
+  const long long below = (long long)(b.at - a.at) - part.span();
+  const long long last = ((long long)(b.at - a.at) + b.span() - 1) / step;
+  for (long long i = below < 0 ? 0 : below / step + 1; i < n && i <= last; ++i) {
+    if (--tries < 0) return false;
+    part.at = a.at + (uintptr_t)(i * step);
+    if (share_parts(part, b, tries)) return true;
+  }
+  return false;
+}
+inline bool share(const Bytes &a, const Bytes &b) {
+  if (a.at + a.span() <= b.at || b.at + b.span() <= a.at) return false;
+  int tries = 4096;
+  return share_parts(flat(a), flat(b), tries);
+}
+// Whether none of the outputs shares memory with another or with one of `reads`.
+template <int N, int M>
+bool apart(const Bytes (&outs)[N], const Bytes (&reads)[M]) {
+  for (int i = 0; i < N; ++i) {
+    for (int k = 0; k < i; ++k)
+      if (share(outs[i], outs[k])) return false;
+    for (const Bytes &r : reads)
+      if (share(outs[i], r)) return false;
+  }
+  return true;
+}
+
 constexpr size_t kStatusBytes = 256;  // a workspace's status block
 
 // Limit of one bounded wait inside the kernels (dash_attn_set_wait_limit).

@@ -51,16 +51,27 @@ bool all_aligned(const void *const (&ptrs)[N], uintptr_t size) {
   return (any & (size - 1)) == 0;
 }
 
-// Whether no two of the outputs begin at one address, nor one of them where one of `reads` does
-// (null ones aside).
-template <int N, int M>
-bool apart(const void *const (&outs)[N], const void *const (&reads)[M]) {
+// Row tensors: outputs may each be an input as it lies, or what no other tensor of the call is.
+struct Rows {
+  const void *at;
+  long long stride;
+};
+Bytes lies(const Rows &r, long long rows, int C, int size) {
+  return along(bytes_of(r.at, size, C), size, r.stride, rows);
+}
+template <int N, int M, int K>
+bool rows_apart(const Rows (&outs)[N], const Rows (&ins)[M], const Bytes (&others)[K],
+                long long rows, int C, int size) {
   for (int i = 0; i < N; ++i) {
-    if (!outs[i]) continue;
+    const Bytes out = lies(outs[i], rows, C, size);
     for (int k = 0; k < i; ++k)
-      if (outs[k] == outs[i]) return false;
-    for (const void *q : reads)
-      if (q == outs[i]) return false;
+      if (share(out, lies(outs[k], rows, C, size))) return false;
+    for (const Rows &r : ins)
+      if (!(r.at == outs[i].at && r.stride == outs[i].stride) &&
+          share(out, lies(r, rows, C, size)))
+        return false;
+    for (const Bytes &o : others)
+      if (share(out, o)) return false;
   }
   return true;
 }
@@ -145,11 +156,19 @@ dash_status_t dash_join_fwd(const void *x, const void *a, const void *w_post, co
   const void *fp[] = {rstd_a, rstd_y};
   if (!all_aligned(rowp, size) || !all_aligned(wp, elem_size(wdtype)) || !all_aligned(fp, 4))
     return DASH_ERR_INVALID;
-  // y and h may be x or a; rows written early would be read as weights, or as x by other CTAs, later
-  const void *rows_out[] = {join ? y : nullptr, w_next ? h : nullptr};
-  const void *stats_out[] = {w_post ? rstd_a : nullptr, w_next ? rstd_y : nullptr};
-  const void *stats_reads[] = {x, a, w_post, gate, w_next, rows_out[0], rows_out[1]};
-  if (!apart(rows_out, wp) || !apart(stats_out, stats_reads)) return DASH_ERR_INVALID;
+  const int wsize = elem_size(wdtype);
+  const Bytes stats[] = {bytes_of(w_post ? rstd_a : nullptr, 4, rows),
+                         bytes_of(w_next ? rstd_y : nullptr, 4, rows)};
+  const Bytes weights[] = {bytes_of(w_post, wsize, C),
+                           bytes_of(gate, wsize, gate ? rows / gate_rows * C : 0),
+                           bytes_of(w_next, wsize, C)};
+  const Rows outs[] = {{rowp[2], strides[2]}, {rowp[3], strides[3]}};
+  const Rows ins[] = {{x, strides[0]}, {a, strides[1]}};
+  const Bytes beside[] = {weights[0], weights[1], weights[2], stats[0], stats[1]};
+  const Bytes reads[] = {lies(ins[0], rows, C, size), lies(ins[1], rows, C, size),
+                         weights[0], weights[1], weights[2]};
+  if (!rows_apart(outs, ins, beside, rows, C, size) || !apart(stats, reads))
+    return DASH_ERR_INVALID;
   const Lie lie = lie_of(rowp, strides, wp, C, size, rows);
   const bool wide = lie.wide;
   DevInfo dev;
@@ -214,11 +233,26 @@ dash_status_t dash_join_bwd(const void *dy, const void *dh, const void *y, const
   if (!workspace || !aligned16(workspace) ||
       workspace_bytes < dash_join_bwd_workspace_bytes(rows, C, gate ? gate_rows : 0, join, dtype))
     return DASH_ERR_WORKSPACE;
-  // dx and da may be dy, dh, y or a; the weights are read again after rows have been written
-  const void *outs[] = {dx, join ? da : nullptr, dwp[0], dwp[1], dwp[2], workspace};
-  const void *reads[] = {w_post, gate, w_next, w_post ? rstd_a : nullptr,
-                         w_next ? rstd_y : nullptr};
-  if (!apart(outs, reads)) return DASH_ERR_INVALID;
+  const int wsize = elem_size(wdtype);
+  const long long gates = gate ? rows / gate_rows * C : 0;
+  const Bytes sums[] = {bytes_of(dwp[0], wsize, C), bytes_of(dwp[1], wsize, gates),
+                        bytes_of(dwp[2], wsize, C),
+                        bytes_of(workspace, 1,
+                                 dash_join_bwd_workspace_bytes(rows, C, gate ? gate_rows : 0, join,
+                                                               dtype))};
+  const Bytes weights[] = {bytes_of(w_post, wsize, C), bytes_of(gate, wsize, gates),
+                           bytes_of(w_next, wsize, C), bytes_of(w_post ? rstd_a : nullptr, 4, rows),
+                           bytes_of(w_next ? rstd_y : nullptr, 4, rows)};
+  const Rows outs[] = {{dx, strides[4]}, {rowp[5], strides[5]}};
+  const Rows ins[] = {{rowp[0], strides[0]}, {rowp[1], strides[1]}, {rowp[2], strides[2]},
+                      {a, strides[3]}};
+  const Bytes beside[] = {weights[0], weights[1], weights[2], weights[3], weights[4],
+                          sums[0],    sums[1],    sums[2],    sums[3]};
+  const Bytes reads[] = {weights[0], weights[1], weights[2], weights[3], weights[4],
+                         lies(ins[0], rows, C, size), lies(ins[1], rows, C, size),
+                         lies(ins[2], rows, C, size), lies(ins[3], rows, C, size)};
+  if (!rows_apart(outs, ins, beside, rows, C, size) || !apart(sums, reads))
+    return DASH_ERR_INVALID;
   const bool own_gates = gate && gate_rows == 1 && rows > 1;
   const Lie lie = lie_of(rowp, strides, wp, C, size, gate && !own_gates ? gate_rows : rows);
   const bool wide = lie.wide;

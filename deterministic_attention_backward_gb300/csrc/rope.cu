@@ -155,14 +155,37 @@ extern "C" dash_status_t dash_rope(const dash_rope_part_t *parts, int nparts, in
   if (dtype != DASH_BF16 && dtype != DASH_FP16 && dtype != DASH_FP32) return DASH_ERR_INVALID;
   if (!inv_freq || (reinterpret_cast<uintptr_t>(inv_freq) & 7)) return DASH_ERR_INVALID;
   if (reinterpret_cast<uintptr_t>(positions) & (positions64 ? 7 : 3)) return DASH_ERR_INVALID;
-  if (rot > kMaxRot || (long long)B * S >= (1LL << 31) - 4) return DASH_ERR_UNSUPPORTED;
-  const int size = dtype == DASH_FP32 ? 4 : 2, vec = 16 / size;
-  bool wide = rot % (2 * vec) == 0;
-  long long units = 0;
+  Bytes in[3], out[3];
+  const int size = dtype == DASH_FP32 ? 4 : 2, vec = 16 / size, psize = positions64 ? 8 : 4;
   for (int i = 0; i < nparts; ++i) {
     const dash_rope_part_t &q = parts[i];
     if (!q.in || !q.out || q.heads <= 0 || q.D <= 0 || (q.turn && q.D < rot))
       return DASH_ERR_INVALID;
+    auto lies = [&](const void *at, const long long *stride) {
+      const long long count[3] = {B, S, q.heads};
+      Bytes b = bytes_of(at, size, q.D);
+      for (int k = 0; k < 3; ++k) b = along(b, size, stride[k], count[k]);
+      return b;
+    };
+    in[i] = lies(q.in, q.in_stride), out[i] = lies(q.out, q.out_stride);
+  }
+  if (rot > kMaxRot || (long long)B * S >= (1LL << 31) - 4) return DASH_ERR_UNSUPPORTED;
+  const Bytes angles[2] = {
+      bytes_of(inv_freq, 8, rot / 2),
+      along(along(bytes_of(positions, psize, 1), psize, pos_stride_t, S), psize, pos_stride_b, B)};
+  for (int i = 0; i < nparts; ++i) {  // an output is its input, as it lies, or what nothing else is
+    const dash_rope_part_t &q = parts[i];
+    bool in_place = q.in == q.out;
+    for (int k = 0; k < 3; ++k) in_place = in_place && q.in_stride[k] == q.out_stride[k];
+    for (int k = 0; k < nparts; ++k)
+      if ((k < i && share(out[i], out[k])) || ((k != i || !in_place) && share(out[i], in[k])))
+        return DASH_ERR_INVALID;
+    if (share(out[i], angles[0]) || share(out[i], angles[1])) return DASH_ERR_INVALID;
+  }
+  bool wide = rot % (2 * vec) == 0;
+  long long units = 0;
+  for (int i = 0; i < nparts; ++i) {
+    const dash_rope_part_t &q = parts[i];
     const uintptr_t at = reinterpret_cast<uintptr_t>(q.in) | reinterpret_cast<uintptr_t>(q.out);
     if (at & (size - 1)) return DASH_ERR_INVALID;
     const long long any = q.in_stride[0] | q.in_stride[1] | q.in_stride[2] | q.out_stride[0] |

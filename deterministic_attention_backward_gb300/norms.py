@@ -13,7 +13,7 @@ norms, forward and backward.
 Rows are the last dimension of tensors of any shape (the rest must flatten to one row stride),
 bf16, fp16 or fp32; weights of the rows' type or fp32.  The weight gradients are deterministic.
 Outputs may be row operands themselves (y and h: x or a; dx and da: dy, dh, y or a), at the same
-row stride; no output is a weight, a gate or an rstd.
+row stride; beside that no output shares memory with another tensor of the call.
 """
 from __future__ import annotations
 

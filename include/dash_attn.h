@@ -304,7 +304,8 @@ dash_status_t dash_attn_bwd_varlen_order_log(const void *q, const void *k, const
  * Operators around the attention in a decoder block: rotary positions, norms joined with the
  * residual stream, differential attention.  They keep the conventions above (caller-owned
  * device memory, argument errors before anything is enqueued, work on `stream` of the current
- * device), with these element types: */
+ * device).  Outputs and workspaces that share memory with an operand or with one another, where
+ * that is not allowed below, are argument errors too.  Element types: */
 typedef enum { DASH_BF16 = 0, DASH_FP16 = 1, DASH_FP32 = 2 } dash_dtype_t;
 
 /* Rotary positions.  One part is a tensor [B, S, heads, D] (element strides of batch, token
@@ -344,8 +345,8 @@ dash_status_t dash_rope(const dash_rope_part_t *parts, int nparts, int B, int S,
  * [rows] fp32 are kept for the backward (each written only where its norm is asked for).  The
  * weights [C] are of the rows' type or all fp32; gate is [rows / gate_rows, C], each row of it
  * serving gate_rows consecutive rows.  y and h may each be x or a itself (with the same stride),
- * not both the same; no output is a weight or a gate.  fp32 arithmetic, one rounding per output.  Tensors are read by whole
- * aligned words of 16 bytes: of rows that 16 bytes do not divide, with up to 15 bytes beside. */
+ * not both the same.  fp32 arithmetic, one rounding per output.  Tensors are read by whole aligned
+ * words of 16 bytes: of rows that 16 bytes do not divide, with up to 15 bytes beside. */
 dash_status_t dash_join_fwd(const void *x, const void *a, const void *w_post, const void *gate,
                             const void *w_next, void *y, void *h, float *rstd_a, float *rstd_y,
                             long long rows, int C, long long gate_rows,
@@ -361,8 +362,8 @@ size_t dash_join_bwd_workspace_bytes(long long rows, int C, long long gate_rows,
  * whose dy is added to dx: the gradient of the residual stream beside the norm), a the branch.
  * Writes dx, da and, in the weights' type, dw_post, dgate, dw_next (each where its weight is
  * given).  Row strides of dy, dh, y, a, dx, da in `strides`.  dx and da may each be dy, dh, y or a
- * itself (with the same stride), not both the same; no output is a weight, a gate or an rstd.  The weight gradients are summed in an order that the sizes, strides
- * and alignments fix: the same bits on every run. */
+ * itself (with the same stride), not both the same.  The weight gradients are summed in an order
+ * that the sizes, strides and alignments fix: the same bits on every run. */
 dash_status_t dash_join_bwd(const void *dy, const void *dh, const void *y, const void *a,
                             const void *w_post, const void *gate, const void *w_next,
                             const float *rstd_a, const float *rstd_y, void *dx, void *da,
