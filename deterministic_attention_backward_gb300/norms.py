@@ -60,7 +60,7 @@ def _in_place(outs, ins, weights):
     another stride (both are (tensor, stride of its rows)), or of one of ``weights``, which are
     read after rows have been written."""
     for n, (o, so) in enumerate(outs):
-        if o is None:
+        if o is None or o.numel() == 0:
             continue
         at = o.data_ptr()
         if any(u is not None and u.data_ptr() == at for u, _ in outs[:n]) or \
@@ -87,11 +87,11 @@ def _weights(x, rows, w_post, gate, w_next):
             lead = list(w.shape[:-1])
             while lead and lead[-1] == 1:
                 lead.pop()
-            if w.shape[-1] != C or groups == 0 or rows % groups or \
+            if w.shape[-1] != C or (rows % groups if groups else rows) or \
                     (x.dim() > 2 and list(x.shape[:len(lead)]) != lead):
                 raise ValueError(f"gate {tuple(w.shape)} has no row for each run of consecutive "
                                  f"rows of {tuple(x.shape)}")
-            gate_rows = rows // groups
+            gate_rows = rows // max(groups, 1)
         elif w.dim() != 1 or w.shape[0] != C:
             raise ValueError(f"{name} must have shape {(C,)}, got {tuple(w.shape)}")
         if not w.is_contiguous():

@@ -485,3 +485,25 @@ def test_refuses_outputs_that_are_weights(L):
     r = torch.ones(6, 1, device="cuda")                     # rows of one element in fp32
     no(dash.norm_bwd, r, r, r[:, 0], torch.ones(1, device="cuda"), dx=r)
     dash.join_bwd(x, x, x.clone(), x.clone(), rstd, rstd, w_post=w, gate=gate, w_next=w, dx=x)
+
+
+@pytest.mark.gpu
+def test_empty_batches_with_gates_and_outputs(L):
+    """No sequences, or none of their tokens: a gate for every sequence goes with them, and so do
+    outputs that the caller hands in (all at no address)."""
+    w = make((64,), BF, 1)
+    for shape, gate in (((0, 5, 64), (0, 64)), ((0, 5, 64), (0, 1, 64)), ((2, 0, 64), (2, 64)),
+                        ((0, 64), (0, 64)), ((0, 5, 64), (0, 5, 64)), ((0, 5, 64), (64,))):
+        x, g = torch.empty(shape, dtype=BF, device="cuda"), make(gate, BF, 2)
+        kw = dict(w_post=w, gate=g, w_next=w)
+        y, h, ra, ry = dash.join_fwd(x, x, **kw, y=torch.empty_like(x), h=torch.empty_like(x))
+        assert y.shape == h.shape == x.shape and ra.shape == ry.shape == shape[:-1]
+        dx, da, dwp, dg, dwn = dash.join_bwd(y, h, y, x, ra, ry, **kw, dx=torch.empty_like(x),
+                                             da=torch.empty_like(x))
+        assert dx.shape == da.shape == x.shape and dg.shape == g.shape
+        assert (dwp == 0).all() and (dwn == 0).all() and (dg == 0).all()
+    x = torch.empty(0, 5, 64, dtype=BF, device="cuda")
+    with pytest.raises(ValueError):
+        dash.join_fwd(x, x, gate=make((0, 32), BF, 1))
+    with pytest.raises(ValueError):
+        dash.join_fwd(make((2, 5, 64), BF, 1), make((2, 5, 64), BF, 1), gate=make((0, 64), BF, 1))
