@@ -5,9 +5,10 @@
 //
 // The angle of a far position does not survive fp32 (position 2^20 at one radian a position is
 // off by 0.03 rad) and fp64 runs at 1/64 of the fp32 rate here, so the phase is an integer:
-// inv_freq / (2 pi) becomes a 64-bit fraction of a turn, the product with the position is
-// taken modulo 2^64 -- whole turns fall off exactly, for negative positions too -- and the top
-// 32 bits, as a signed fraction of half turns, go through sincospif.
+// inv_freq / (2 pi) becomes a 128-bit fraction of a turn, the product with the position is
+// taken modulo 2^128 -- whole turns fall off exactly, for negative positions too -- and the top
+// 32 bits, as a signed fraction of half turns, go through sincospif: over all 64-bit positions the
+// angle is off by the rounding of that fraction to fp32, 2^-25 half turns, and what it is cut by.
 //
 // Bound by memory: every element is read and written once.  A CTA takes kTok tokens, forms
 // each (token, pair) phase once in shared memory and uses it for all heads of the token; q, k
@@ -44,15 +45,22 @@ struct RopeParams {
   unsigned magic;  // ceil(2^32 / units)
 };
 
-// A frequency in radians per position as a 64-bit fraction of a turn (integer part dropped).
-// Shifts the bits of the double: the truncation is below 2^-64 turns.
-__device__ __forceinline__ uint64_t turns_of(double f) {
-  const double d = f * 0.15915494309189535;  // 1 / (2 pi)
+// A frequency in radians per position as a 128-bit fraction of a turn (whole turns fall off):
+// f / (2 pi) as a sum of two doubles, 1 / (2 pi) being one too, good to 2^-105 of itself; each
+// one's bits are moved to their place, which cuts off less than 2^-128 turns.  One double would
+// leave 53 bits: 2e-7 radians at position 2^31, 6e-6 at 2^36.
+using u128 = unsigned __int128;
+__device__ __forceinline__ u128 fraction_of(double d) {
   const uint64_t b = (uint64_t)__double_as_longlong(d);
-  const int sh = (int)((b >> 52) & 0x7FF) - 1023 + 12;  // mantissa's last bit at 2^(e-52)
-  const uint64_t m = (b & 0xFFFFFFFFFFFFFull) | (1ull << 52);
-  const uint64_t u = sh >= 64 ? 0 : sh >= 0 ? m << sh : sh > -64 ? m >> -sh : 0;
+  const int sh = (int)((b >> 52) & 0x7FF) - 1023 + 76;  // mantissa's last bit at 2^(e-52)
+  const u128 m = (b & 0xFFFFFFFFFFFFFull) | (1ull << 52);
+  const u128 u = sh >= 128 ? 0 : sh >= 0 ? m << sh : sh > -64 ? m >> -sh : 0;
   return (b >> 63) ? 0 - u : u;
+}
+__device__ __forceinline__ u128 turns_of(double f) {
+  constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;  // 1 / (2 pi)
+  const double hi = f * kHi;
+  return fraction_of(hi) + fraction_of(fma(f, kLo, fma(f, kHi, -hi)));
 }
 
 // n / d by the magic ceil(2^32 / d): exact while n d < 2^32.
@@ -75,9 +83,9 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
       pos = p.pos64 ? static_cast<const long long *>(p.pos)[at]
                     : (long long)static_cast<const int *>(p.pos)[at];
     }
-    const uint64_t phase = (uint64_t)pos * turns_of(p.inv_freq[pair]);
+    const int phase = (int)(uint32_t)(((u128)(__int128)pos * turns_of(p.inv_freq[pair])) >> 96);
     float sn, c;
-    sincospif((float)(int)(phase >> 32) * (1.0f / 2147483648.0f), &sn, &c);
+    sincospif((float)phase * (1.0f / 2147483648.0f), &sn, &c);
     cs[i] = make_float2(c * p.magnitude, (p.back ? -sn : sn) * p.magnitude);
   }
   __syncthreads();

@@ -251,3 +251,39 @@ def test_refusals(L):
     no(q, k, out=(o, q, None))
     wide = torch.zeros(2, 8, 2, 64, dtype=BF, device="cuda")
     no(wide[:, :4], out=(wide.view(-1)[:1024].view(2, 4, 2, 64), None, None))  # other strides
+
+
+def turns(inv_freq, pos):
+    """pos inv_freq / (2 pi) modulo 1, exact up to 2^-200: pi by Machin's formula in integers."""
+    from fractions import Fraction
+
+    def arctan(n, bits=400):  # of 1 / n
+        term = total = (1 << bits) // n
+        k = 1
+        while term:
+            term //= -n * n
+            k += 2
+            total += term // k
+        return total
+    two_pi = Fraction(8 * (4 * arctan(5) - arctan(239)), 1 << 400)
+    return float(Fraction(inv_freq) * pos / two_pi % 1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("base", [10000.0, 500000.0])
+def test_far_positions(L, base):
+    """Positions over all of 64 bits.  The pair (1, 0) becomes (cos a, sin a), each off by less than
+    2^-21 as above: nothing of the angle is lost on the way to its last fp32 rounding."""
+    f, _ = dash.rope_freqs(128, base=base)
+    far = [2 ** 31 - 1, 2 ** 36 + 5, 2 ** 40 - 3, 2 ** 53 + 1, 2 ** 62 + 12345, 2 ** 63 - 1, -2 ** 63,
+           -2 ** 45 - 1, 0]
+    pos = torch.tensor([far], device="cuda")
+    x = torch.zeros(1, len(far), 1, 128, device="cuda")
+    x[..., :64] = 1.0
+    got = dash.rope_fwd(x, inv_freq=f, positions=pos)[0][0, :, 0].double().cpu()
+    for row, p in zip(got, far):
+        a = torch.tensor([2 * math.pi * turns(w, p) for w in f.tolist()], dtype=torch.float64)
+        err = (row - torch.cat([a.cos(), a.sin()])).abs().max().item()
+        assert err < 2.0 ** -21, (p, err)
+        alone = dash.rope_fwd(x[:, :1], inv_freq=f, start=p)[0][0, 0, 0].double().cpu()
+        assert torch.equal(alone, row)
