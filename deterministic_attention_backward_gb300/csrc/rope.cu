@@ -83,9 +83,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
       pos = p.pos64 ? static_cast<const long long *>(p.pos)[at]
                     : (long long)static_cast<const int *>(p.pos)[at];
     }
-    const int phase = (int)(uint32_t)(((u128)(__int128)pos * turns_of(p.inv_freq[pair])) >> 96);
+    const double f = p.inv_freq[pair];
+    const int phase = (int)(uint32_t)(((u128)(__int128)pos * turns_of(f)) >> 96);
     float sn, c;
     sincospif((float)phase * (1.0f / 2147483648.0f), &sn, &c);
+    if (!isfinite(f)) c = sn = NAN;
     cs[i] = make_float2(c * p.magnitude, (p.back ? -sn : sn) * p.magnitude);
   }
   __syncthreads();

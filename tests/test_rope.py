@@ -287,3 +287,19 @@ def test_far_positions(L, base):
         assert err < 2.0 ** -21, (p, err)
         alone = dash.rope_fwd(x[:, :1], inv_freq=f, start=p)[0][0, 0, 0].double().cpu()
         assert torch.equal(alone, row)
+
+
+@pytest.mark.gpu
+def test_frequencies_that_are_no_numbers(L):
+    """A frequency that is infinite or NaN has no angle: its pair is NaN, the others are turned."""
+    f, _ = dash.rope_freqs(64)
+    x = make(1, 3, 2, 64, BF, 0)
+    want = dash.rope_fwd(x, inv_freq=f, start=5)[0]
+    for p, bad in ((0, math.nan), (7, math.inf), (31, -math.inf)):
+        g = f.clone()
+        g[p] = bad
+        for start in (5, 0):
+            y = dash.rope_fwd(x, inv_freq=g, start=start)[0]
+            assert y[..., [p, p + 32]].isnan().all()
+            keep = [i for i in range(64) if i not in (p, p + 32)]
+            assert start == 0 or torch.equal(y[..., keep], want[..., keep])
