@@ -109,7 +109,10 @@ def _rope(parts, inv_freq, magnitude, positions, start, layout, out, stream, bac
                     o.stride() != parts[i - len(parts)].stride()):
                 raise ValueError(f"out[{i - len(parts)}] is the memory of another tensor")
     where, pos64, pb, pt = None, 0, 0, 0
-    if positions is not None:
+    if positions is None:
+        if not -2 ** 63 <= start <= 2 ** 63 - S:
+            raise ValueError(f"positions from {start} on do not fit 64 bits")
+    else:
         tensor(positions, "positions", (torch.int32, torch.int64))
         if positions.device != q.device:
             raise ValueError(f"positions are on {positions.device}, the heads on {q.device}")

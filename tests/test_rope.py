@@ -303,3 +303,14 @@ def test_frequencies_that_are_no_numbers(L):
             assert y[..., [p, p + 32]].isnan().all()
             keep = [i for i in range(64) if i not in (p, p + 32)]
             assert start == 0 or torch.equal(y[..., keep], want[..., keep])
+
+
+@pytest.mark.gpu
+def test_start_beyond_64_bits(L):
+    f, _ = dash.rope_freqs(64)
+    x = make(1, 3, 2, 64, BF, 0)
+    for start in (2 ** 63, -2 ** 63 - 1, 2 ** 70, 2 ** 63 - 2):
+        with pytest.raises(ValueError):
+            dash.rope_fwd(x, inv_freq=f, start=start)
+    dash.rope_fwd(x, inv_freq=f, start=2 ** 63 - 3)
+    dash.rope_fwd(x, inv_freq=f, positions=torch.zeros(3, dtype=torch.int64, device="cuda"))
