@@ -35,7 +35,8 @@ def rope_freqs(rot: int, base: float = 10000.0, scaling: str = "none", factor: f
       by ``factor`` and the fastest kept
     - ``"ramp"``: pairs that turn more than ``fast`` times over ``original_len`` positions kept,
       pairs that turn less than ``slow`` times divided by ``factor``, a linear ramp over the pair
-      index between; magnitude 0.1 ln(factor) + 1
+      index between, from the floor of the index at ``fast`` turns to the ceiling of that at
+      ``slow`` (YaRN, arXiv 2309.00071); magnitude 0.1 ln(factor) + 1, 1 for factors below one
     """
     if rot <= 0 or rot % 2:
         raise ValueError(f"rot must be positive and even, got {rot}")
@@ -50,15 +51,19 @@ def rope_freqs(rot: int, base: float = 10000.0, scaling: str = "none", factor: f
     if scaling == "linear":
         f = f / factor
     elif scaling == "ramp":
-        if original_len <= 0 or not fast > slow:
-            raise ValueError("ramp wants original_len > 0 and fast > slow")
-        turns = f * original_len / (2.0 * math.pi)
-        first = float((turns > fast).sum())
-        last = max(first + 1.0, float((turns > slow).sum()))
+        if original_len <= 0 or not fast > slow or not base > 1:
+            raise ValueError("ramp wants original_len > 0, fast > slow and base > 1")
+
+        def index(turns):  # of the pair that turns so often over original_len positions
+            if turns <= 0:
+                return rot - 1
+            return rot * math.log(original_len / (2.0 * math.pi * turns)) / (2.0 * math.log(base))
+        first = max(math.floor(index(fast)), 0)
+        last = min(math.ceil(index(slow)), rot - 1)
         p = torch.arange(rot // 2, dtype=torch.float64)
-        keep = 1.0 - ((p - first) / (last - first)).clamp(0.0, 1.0)
-        f = f * keep + f / factor * (1.0 - keep)
-        magnitude = 0.1 * math.log(factor) + 1.0
+        by = ((p - first) / max(last - first, 1e-3)).clamp(0.0, 1.0)
+        f = f * (1.0 - by) + f / factor * by
+        magnitude = 0.1 * math.log(max(factor, 1.0)) + 1.0
     return f.to(device), magnitude
 
 

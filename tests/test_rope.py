@@ -314,3 +314,36 @@ def test_start_beyond_64_bits(L):
             dash.rope_fwd(x, inv_freq=f, start=start)
     dash.rope_fwd(x, inv_freq=f, start=2 ** 63 - 3)
     dash.rope_fwd(x, inv_freq=f, positions=torch.zeros(3, dtype=torch.int64, device="cuda"))
+
+
+def test_ramp_is_the_published_one():
+    """Frequencies for longer contexts by parts (YaRN, arXiv 2309.00071, with its ramp over the pair
+    index): a pair n turns around L / (2 pi) base^(-2n/rot) times, the ramp runs from the floor of
+    the index at which that is `fast` to the ceiling of that at which it is `slow`."""
+    for rot, base, L, factor in ((128, 1e4, 4096, 4.0), (128, 1e4, 4096, 32.0), (64, 5e5, 8192, 8.0),
+                                 (32, 1e4, 131072, 2.0), (128, 1e4, 4096, 1.0), (8, 1e6, 100, 4.0)):
+        fr, m = dash.rope_freqs(rot, base=base, scaling="ramp", factor=factor, original_len=L,
+                                device="cpu")
+
+        def index(turns):
+            return rot * math.log(L / (turns * 2 * math.pi)) / (2 * math.log(base))
+        first, last = max(math.floor(index(32)), 0), min(math.ceil(index(1)), rot - 1)
+        for n, got in enumerate(fr.tolist()):
+            f = base ** (-2 * n / rot)
+            by = min(max((n - first) / (last - first), 0), 1)
+            assert math.isclose(got, f * (1 - by) + f / factor * by, rel_tol=1e-12), (rot, n)
+        assert math.isclose(m, 0.1 * math.log(factor) + 1)
+    # 4096 positions, base 10000: pair 20 turns 36.7 times, pair 21 31.8, so the ramp begins at 20
+    fr, _ = dash.rope_freqs(128, scaling="ramp", factor=4.0, device="cpu")
+    f, _ = dash.rope_freqs(128, device="cpu")
+    assert fr[20] == f[20] and math.isclose(fr[21] / f[21], 1 - 0.75 / 26, rel_tol=1e-12)
+
+
+def test_ramp_shortened_and_refusals():
+    """A factor below one leaves the magnitude at one; the ramp needs a base above one."""
+    assert dash.rope_freqs(64, scaling="ramp", factor=0.5, device="cpu")[1] == 1.0
+    for base in (1.0, 0.5):
+        with pytest.raises(ValueError):
+            dash.rope_freqs(64, base=base, scaling="ramp", factor=2.0, device="cpu")
+    fr, _ = dash.rope_freqs(64, scaling="ramp", factor=2.0, slow=0.0, device="cpu")
+    assert (fr > dash.rope_freqs(64, device="cpu")[0] / 2).all()   # no pair turns less than never
