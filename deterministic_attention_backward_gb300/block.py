@@ -125,16 +125,17 @@ def _operator_functions():
     class Differential(torch.autograd.Function):
         @staticmethod
         def forward(ctx, q, k, v, lam, causal):
-            o, o2, lse = dash.diff_fwd(q, k, v, lam, causal=causal)
-            ctx.save_for_backward(q, k, v, o, o2, lse, lam)
+            rest = q.new_empty(2, *v.shape[:2], q.shape[2] // 2, v.shape[3])
+            o, o2, lse = dash.diff_fwd(q, k, v, lam, causal=causal, rest=rest)
+            ctx.save_for_backward(q, k, v, o, o2, lse, lam, rest)
             ctx.causal = causal
             return o
 
         @staticmethod
         def backward(ctx, do):
-            q, k, v, o, o2, lse, lam = ctx.saved_tensors
-            return *dash.diff_bwd(q, k, v, o, o2, dense(do), lse, lam,
-                                  causal=ctx.causal), None
+            q, k, v, o, o2, lse, lam, rest = ctx.saved_tensors
+            return *dash.diff_bwd(q, k, v, o, o2, dense(do), lse, lam, causal=ctx.causal,
+                                  rest=rest), None
 
     return Rotary, Norm, PreNorm, Join, Differential
 

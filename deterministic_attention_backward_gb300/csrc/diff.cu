@@ -120,6 +120,15 @@ dash_status_t dash_diff_fwd(const void *q, const void *k, const void *v, const v
                             float scale, dash_mask_t mask, dash_dtype_t lam_dtype,
                             int lam_per_token, void *workspace, size_t workspace_bytes,
                             dash_stream_t stream) {
+  return dash_diff_fwd_rest(q, k, v, lam, o, o2, nullptr, lse, B, S, H, group, d, scale, mask,
+                            lam_dtype, lam_per_token, workspace, workspace_bytes, stream);
+}
+
+dash_status_t dash_diff_fwd_rest(const void *q, const void *k, const void *v, const void *lam,
+                                 void *o, void *o2, void *rest, float *lse, int B, int S, int H,
+                                 int group, int d, float scale, dash_mask_t mask,
+                                 dash_dtype_t lam_dtype, int lam_per_token, void *workspace,
+                                 size_t workspace_bytes, dash_stream_t stream) {
   using namespace dash;
   dash_status_t st = check_diff(B, S, H, group, d);
   if (st != DASH_OK) return st;
@@ -127,11 +136,13 @@ dash_status_t dash_diff_fwd(const void *q, const void *k, const void *v, const v
   const void *ptrs[] = {q, k, v, o, o2};
   for (const void *ptr : ptrs)
     if (!ptr || !aligned16(ptr)) return DASH_ERR_INVALID;
-  if (!lse || !aligned4(lse) || !lam_ok(lam, lam_dtype)) return DASH_ERR_INVALID;
+  if (!lse || !aligned4(lse) || !lam_ok(lam, lam_dtype) || !aligned16(rest))
+    return DASH_ERR_INVALID;
   if (!workspace || workspace_bytes < kStatusBytes || !aligned16(workspace))
     return DASH_ERR_WORKSPACE;
   const int Hkv = H / group;
   const Bytes outs[] = {heads_of(o, B, S, H, d), heads_of(o2, B, S, H, d),
+                        heads_of(rest, 2 * B, S, H, d),
                         bytes_of(lse, 4, (long long)B * 2 * H * S),
                         bytes_of(workspace, 1, kStatusBytes)};
   const Bytes reads[] = {heads_of(q, B, S, H, d), heads_of(k, B, S, Hkv, d),
@@ -149,6 +160,7 @@ dash_status_t dash_diff_fwd(const void *q, const void *k, const void *v, const v
   DiffFwdParams p{};
   p.o = static_cast<__nv_bfloat16 *>(o);
   p.o2 = static_cast<__nv_bfloat16 *>(o2);
+  p.rest = static_cast<__nv_bfloat16 *>(rest);
   p.lse = lse;
   p.lam = lam;
   p.status = static_cast<uint32_t *>(workspace);
@@ -168,6 +180,17 @@ dash_status_t dash_diff_bwd(const void *q, const void *k, const void *v, const v
                             int group, int d, float scale, dash_mask_t mask,
                             dash_dtype_t lam_dtype, int lam_per_token, void *workspace,
                             size_t workspace_bytes, dash_stream_t stream) {
+  return dash_diff_bwd_rest(q, k, v, o, o2, nullptr, dout, lse, lam, dq, dk, dv, dlam, B, S, H,
+                            group, d, scale, mask, lam_dtype, lam_per_token, workspace,
+                            workspace_bytes, stream);
+}
+
+dash_status_t dash_diff_bwd_rest(const void *q, const void *k, const void *v, const void *o,
+                                 const void *o2, const void *rest, const void *dout,
+                                 const float *lse, const void *lam, void *dq, void *dk, void *dv,
+                                 void *dlam, int B, int S, int H, int group, int d, float scale,
+                                 dash_mask_t mask, dash_dtype_t lam_dtype, int lam_per_token,
+                                 void *workspace, size_t workspace_bytes, dash_stream_t stream) {
   using namespace dash;
   dash_status_t st = check_diff(B, S, H, group, d);
   if (st != DASH_OK) return st;
@@ -175,7 +198,8 @@ dash_status_t dash_diff_bwd(const void *q, const void *k, const void *v, const v
   const void *ptrs[] = {q, k, v, o, o2, dout, dq, dk, dv};
   for (const void *ptr : ptrs)
     if (!ptr || !aligned16(ptr)) return DASH_ERR_INVALID;
-  if (!lse || !aligned4(lse) || !lam_ok(lam, lam_dtype) || !lam_ok(dlam, lam_dtype))
+  if (!lse || !aligned4(lse) || !lam_ok(lam, lam_dtype) || !lam_ok(dlam, lam_dtype) ||
+      !aligned16(rest))
     return DASH_ERR_INVALID;
   const DiffWorkspace w = carve(workspace, B, S, H, d);
   if (!workspace || !aligned16(workspace) || workspace_bytes < w.total) return DASH_ERR_WORKSPACE;
@@ -186,7 +210,8 @@ dash_status_t dash_diff_bwd(const void *q, const void *k, const void *v, const v
                         bytes_of(workspace, 1, (long long)w.total)};
   const Bytes reads[] = {heads_of(q, B, S, H, d), heads_of(k, B, S, Hkv, d),
                          heads_of(v, B, S, Hkv, d), heads_of(o, B, S, H, d),
-                         heads_of(o2, B, S, H, d), heads_of(dout, B, S, H, d),
+                         heads_of(o2, B, S, H, d), heads_of(rest, 2 * B, S, H, d),
+                         heads_of(dout, B, S, H, d),
                          bytes_of(lse, 4, (long long)B * 2 * H * S),
                          weights_of(lam, B, S, H, lam_dtype, lam_per_token)};
   if (!apart(outs, reads)) return DASH_ERR_INVALID;
@@ -202,6 +227,7 @@ dash_status_t dash_diff_bwd(const void *q, const void *k, const void *v, const v
   DiffBwdParams p{};
   p.o = static_cast<const __nv_bfloat16 *>(o);
   p.o2 = static_cast<const __nv_bfloat16 *>(o2);
+  p.rest = static_cast<const __nv_bfloat16 *>(rest);
   p.dout = static_cast<const __nv_bfloat16 *>(dout);
   p.lse = lse;
   p.lam = lam;

@@ -15,6 +15,7 @@ namespace dash {
 
 struct DiffFwdParams {
   __nv_bfloat16 *o, *o2;  // [B,S,H,2d]
+  __nv_bfloat16 *rest;    // [2,B,S,H,2d], what o and o2 lose by their rounding (may be null)
   float *lse;             // [B,2H,S]
   const void *lam;        // [H] or [B,S,H], bf16 or fp32
   uint32_t *status;
@@ -36,6 +37,7 @@ __host__ __device__ __forceinline__ size_t rowv_at(size_t tile, int r) {
 }
 struct DiffBwdParams {
   const __nv_bfloat16 *o, *o2, *dout;
+  const __nv_bfloat16 *rest;  // the forward's, may be null
   const float *lse;
   const void *lam;
   float *rowv;            // [B,H,N][2][kRowVecs][64]
@@ -211,6 +213,12 @@ __device__ __forceinline__ void mma_commit_l(uint32_t lead, uint64_t *bar) {
 // of 64-column boxes.
 __device__ __forceinline__ constexpr uint32_t col_bytes(int col) {
   return (uint32_t)(col >> 6) * kBoxBytes + (uint32_t)(col & 63) * 2;
+}
+
+// What an fp32 value loses when it is rounded to bf16.
+__device__ __forceinline__ uint32_t rest_of(uint32_t v) {
+  const float x = __uint_as_float(v);
+  return __float_as_uint(x - __bfloat162float(__float2bfloat16_rn(x)));
 }
 
 // C fp32 columns of this thread's row, scaled, as C bf16 at dst (16-byte aligned).

@@ -25,7 +25,7 @@ constexpr int kThreads = (kWarps + 2) * 32;  // and the TMA producer, the MMA is
 // -------------------------------------------------------------------- row vectors
 // One CTA per tile of a (batch, head pair); DV / 8 lanes per row.  Bound by memory: 8 sequences of
 // 2048, 32 heads of 128, 66 us for 403 MB, 6.1 TB/s.
-template <int d>
+template <int d, bool kRest>
 __global__ void __launch_bounds__(256) diff_rows_kernel(const DiffBwdParams p) {
   constexpr int DV = 2 * d, kLanes = DV / 8, kRows = 256 / kLanes;
   __shared__ float s_d[2][kTile];
@@ -44,10 +44,21 @@ __global__ void __launch_bounds__(256) diff_rows_kernel(const DiffBwdParams p) {
       const __nv_bfloat162 *g2 = reinterpret_cast<const __nv_bfloat162 *>(&g);
       const __nv_bfloat162 *x2 = reinterpret_cast<const __nv_bfloat162 *>(&x);
       const __nv_bfloat162 *y2 = reinterpret_cast<const __nv_bfloat162 *>(&y);
+      uint4 xr, yr;
+      if constexpr (kRest) {
+        xr = *reinterpret_cast<const uint4 *>(p.rest + off);
+        yr = *reinterpret_cast<const uint4 *>(p.rest + (size_t)p.B * p.S * p.H * DV + off);
+      }
+      const __nv_bfloat162 *xr2 = reinterpret_cast<const __nv_bfloat162 *>(&xr);
+      const __nv_bfloat162 *yr2 = reinterpret_cast<const __nv_bfloat162 *>(&yr);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float2 a = __bfloat1622float2(g2[e]), u = __bfloat1622float2(x2[e]),
-                     w = __bfloat1622float2(y2[e]);
+        const float2 a = __bfloat1622float2(g2[e]);
+        float2 u = __bfloat1622float2(x2[e]), w = __bfloat1622float2(y2[e]);
+        if constexpr (kRest) {
+          const float2 ur = __bfloat1622float2(xr2[e]), wr = __bfloat1622float2(yr2[e]);
+          u.x += ur.x, u.y += ur.y, w.x += wr.x, w.y += wr.y;
+        }
         d1 = fmaf(a.x, u.x, fmaf(a.y, u.y, d1));
         d2 = fmaf(a.x, w.x, fmaf(a.y, w.y, d2));
       }
@@ -89,10 +100,12 @@ __global__ void __launch_bounds__(256) diff_rows_kernel(const DiffBwdParams p) {
 // 32); a product's 16-key steps address them one by one.  All products have 128 columns or take
 // A from TMEM: with both operands in shared memory, 64 columns would read 6 KB for 32 cycles of
 // tensor work, more than its 128 bytes a cycle.
-// D for dS comes from the rounded outputs; the exact sums over j of Pm dP fall out of this pass
-// and replace it for dK, and give dlam.  That and dS's own rounding leave dQ off by 2.7e-3 of its
-// norm where the rounding of dQ alone leaves 1.7e-3; with dS as two bf16 terms it is 2.4e-3, for a
-// kernel that takes 1.3 times as long, and an exact D would need the scores formed once more.
+// D for dS comes from the outputs, rounded or with what they lost added (rest); the exact sums over
+// j of Pm dP fall out of this pass and replace it for dK, and give dlam.  Of its norm dQ is off by,
+// at queries of spread 1, 2, 4, 8 (the more peaked the maps, the more dP - D cancels): with rest
+// 2.4e-3, 2.5e-3, 3.0e-3, 3.0e-3, from rounded outputs 2.5e-3, 2.9e-3, 4.7e-3, 7.5e-3.  The rounding
+// of dQ alone is 1.7e-3, with that of dS 2.4e-3; what is left with rest is P's in the forward.  dS as
+// two bf16 terms took a tenth off, for a kernel 1.3 times as long.
 // Measured at 8192 tokens, 32 head pairs of 64 with 8 KV heads: causal 633 us, full 1200 us.  A
 // block's products take 1570 cycles of the tensor core, a block 2650: the wait for a product, the
 // 64 exponentials a thread and the stores follow one another, 4 warps a scheduler cover them in
@@ -894,7 +907,10 @@ cudaError_t launch_t(const CUtensorMap &tq, const CUtensorMap &tk, const CUtenso
   if (e == cudaSuccess) e = allow_smem<diff_dkv_kernel<d>>(LK::kBytes);
   if (e != cudaSuccess) return e;
   const unsigned tiles = (unsigned)p.B * p.H * p.N;
-  diff_rows_kernel<d><<<tiles, 256, 0, s>>>(p);
+  if (p.rest)
+    diff_rows_kernel<d, true><<<tiles, 256, 0, s>>>(p);
+  else
+    diff_rows_kernel<d, false><<<tiles, 256, 0, s>>>(p);
   diff_dq_kernel<d><<<tiles, kThreads, LQ::kBytes, s>>>(tq, tk, tv, tdo, p);
   const unsigned cut = (unsigned)p.B * p.Hkv * p.N - p.kv_whole;  // tiles in pieces
   diff_dkv_kernel<d><<<p.kv_whole + cut * p.kv_pieces, kThreads, LK::kBytes, s>>>(tq, tk, tv,

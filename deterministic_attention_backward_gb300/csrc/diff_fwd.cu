@@ -396,6 +396,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (row_ok) {
         store_row(p.o + out, o1, 1.f);
         store_row(p.o2 + out, o2, 1.f);
+        if (p.rest) {
+#pragma unroll
+          for (int e = 0; e < d / 2; ++e) o1[e] = rest_of(o1[e]), o2[e] = rest_of(o2[e]);
+          store_row(p.rest + out, o1, 1.f);
+          store_row(p.rest + (size_t)p.B * p.S * p.H * DV + out, o2, 1.f);
+        }
       }
     }
   }

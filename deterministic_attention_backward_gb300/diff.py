@@ -10,6 +10,15 @@ q [B,S,2H,d], k [B,S,2Hkv,d], v [B,S,Hkv,2d] bf16 with d = 32 or 64: head pair h
 maps 2h and 2h+1 and shares the keys and values of pair h // (H / Hkv).  These are the projections
 of attention with H heads of 2d, viewed with heads of d for q and k.  lam [H] or [B,S,H], bf16
 or fp32.  o2 (the second map's output) and lse [B,2H,S] are what the backward needs besides o.
+
+A training step should keep what o and o2 lose by their rounding too, two bf16 tensors more:
+
+    rest = torch.empty(2, *o_shape, dtype=torch.bfloat16, device=q.device)
+    o, o2, lse = diff_fwd(q, k, v, lam, causal=True, rest=rest)
+    dq, dk, dv, dlam = diff_bwd(q, k, v, o, o2, do, lse, lam, causal=True, rest=rest)
+
+for the row terms D = dO . Om of dQ: off by 2.4e-3 to 3.2e-3 of its norm with rest, without it by
+2.5e-3 for flat maps and up to 8e-3 where a few keys dominate them.
 """
 from __future__ import annotations
 
@@ -55,8 +64,9 @@ def diff_bwd_workspace_bytes(B: int, S: int, H: int, d: int) -> int:
 
 
 def diff_fwd(q, k, v, lam, causal: bool = False, scale: float | None = None, out=None, out2=None,
-             lse=None, workspace=None, stream=None, check: bool = False):
+             lse=None, workspace=None, stream=None, check: bool = False, rest=None):
     """Forward: returns (O [B,S,H,2d], O2 = softmax(Q2 K2^T) V of the same shape, LSE [B,2H,S]).
+    ``rest`` ([2,B,S,H,2d] bf16) receives what O and O2 lose by their rounding, for ``diff_bwd``.
     A ``workspace`` serves one call at a time."""
     B, S, H, Hkv, d = _dims(q, k, v, lam)
     shape = (B, S, H, 2 * d)
@@ -66,8 +76,10 @@ def diff_fwd(q, k, v, lam, causal: bool = False, scale: float | None = None, out
         _given(out2, "out2", q, shape)
     if lse is not None:
         _given(lse, "lse", q, (B, 2 * H, S), torch.float32)
-    if out is not None or out2 is not None or lse is not None:
-        apart((out, out2, lse), (q, k, v, lam))
+    if rest is not None:
+        _given(rest, "rest", q, (2, *shape))
+    if out is not None or out2 is not None or lse is not None or rest is not None:
+        apart((out, out2, lse, rest), (q, k, v, lam))
 
     def launch(handle):
         o = torch.empty(shape, dtype=q.dtype, device=q.device) if out is None else out
@@ -76,11 +88,13 @@ def diff_fwd(q, k, v, lam, causal: bool = False, scale: float | None = None, out
                                                     device=q.device)
         if B and S:
             ws = scratch(256, q, workspace)
-            _check(lib().dash_diff_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), lam.data_ptr(),
-                                       o.data_ptr(), o2.data_ptr(), l.data_ptr(), B, S, H,
-                                       H // Hkv, d, scale or 0.0, bool(causal),
-                                       2 * (lam.dtype == torch.float32), lam.dim() == 3,
-                                       ws.data_ptr(), ws.numel() * ws.element_size(), handle),
+            _check(lib().dash_diff_fwd_rest(q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                            lam.data_ptr(), o.data_ptr(), o2.data_ptr(),
+                                            None if rest is None else rest.data_ptr(),
+                                            l.data_ptr(), B, S, H, H // Hkv, d, scale or 0.0,
+                                            bool(causal), 2 * (lam.dtype == torch.float32),
+                                            lam.dim() == 3, ws.data_ptr(),
+                                            ws.numel() * ws.element_size(), handle),
                    "dash_diff_fwd")
             if check:
                 status(ws, torch.cuda.current_stream())
@@ -90,19 +104,22 @@ def diff_fwd(q, k, v, lam, causal: bool = False, scale: float | None = None, out
 
 def diff_bwd(q, k, v, o, o2, do, lse, lam, causal: bool = False, scale: float | None = None,
              dq=None, dk=None, dv=None, dlam=None, workspace=None, stream=None,
-             check: bool = False):
-    """Backward: returns (dQ, dK, dV, dlam), bit-identical on every run."""
+             check: bool = False, rest=None):
+    """Backward: returns (dQ, dK, dV, dlam), bit-identical on every run.  ``rest``: what the
+    forward wrote there."""
     B, S, H, Hkv, d = _dims(q, k, v, lam)
     shape = (B, S, H, 2 * d)
     _given(o, "o", q, shape)
     _given(o2, "o2", q, shape)
     _given(do, "do", q, shape)
     _given(lse, "lse", q, (B, 2 * H, S), torch.float32)
+    if rest is not None:
+        _given(rest, "rest", q, (2, *shape))
     for t, n, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v), (dlam, "dlam", lam)):
         if t is not None:
             _given(t, n, q, like.shape, like.dtype)
     if dq is not None or dk is not None or dv is not None or dlam is not None:
-        apart((dq, dk, dv, dlam), (q, k, v, o, o2, do, lse, lam))
+        apart((dq, dk, dv, dlam), (q, k, v, o, o2, do, lse, lam, rest))
 
     def launch(handle):
         gq, gk, gv, gl = (torch.empty_like(like) if t is None else t
@@ -112,12 +129,14 @@ def diff_bwd(q, k, v, o, o2, do, lse, lam, causal: bool = False, scale: float | 
             return gq, gk, gv, gl
         L = lib()
         ws = scratch(L.dash_diff_bwd_workspace_bytes(B, S, H, d) or 256, q, workspace)
-        _check(L.dash_diff_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-                               o2.data_ptr(), do.data_ptr(), lse.data_ptr(), lam.data_ptr(),
-                               gq.data_ptr(), gk.data_ptr(), gv.data_ptr(), gl.data_ptr(), B, S,
-                               H, H // Hkv, d, scale or 0.0, bool(causal),
-                               2 * (lam.dtype == torch.float32), lam.dim() == 3, ws.data_ptr(),
-                               ws.numel() * ws.element_size(), handle), "dash_diff_bwd")
+        _check(L.dash_diff_bwd_rest(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                                    o2.data_ptr(), None if rest is None else rest.data_ptr(),
+                                    do.data_ptr(), lse.data_ptr(), lam.data_ptr(), gq.data_ptr(),
+                                    gk.data_ptr(), gv.data_ptr(), gl.data_ptr(), B, S, H,
+                                    H // Hkv, d, scale or 0.0, bool(causal),
+                                    2 * (lam.dtype == torch.float32), lam.dim() == 3,
+                                    ws.data_ptr(), ws.numel() * ws.element_size(), handle),
+               "dash_diff_bwd")
         if check:
             status(ws, torch.cuda.current_stream())
         return gq, gk, gv, gl

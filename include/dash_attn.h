@@ -389,11 +389,19 @@ dash_status_t dash_diff_fwd(const void *q, const void *k, const void *v, const v
                             float scale, dash_mask_t mask, dash_dtype_t lam_dtype,
                             int lam_per_token, void *workspace, size_t workspace_bytes,
                             dash_stream_t stream);
+/* The same for a forward whose backward follows: also writes rest [2,B,S,H,2d] bf16, what o and o2
+ * lose by their rounding (NULL: not written). */
+dash_status_t dash_diff_fwd_rest(const void *q, const void *k, const void *v, const void *lam,
+                                 void *o, void *o2, void *rest, float *lse, int B, int S, int H,
+                                 int group, int d, float scale, dash_mask_t mask,
+                                 dash_dtype_t lam_dtype, int lam_per_token, void *workspace,
+                                 size_t workspace_bytes, dash_stream_t stream);
 /* Backward: dq, dk, dv and dlam (lam's shape and type).  Deterministic: every sum is formed in
  * a fixed order without atomics, bit-identical on every run; dk and dv sum a group's query heads
  * in ascending order (key tiles that the sizes put into pieces: within a piece, then the pieces).
- * The row terms D = dO . Om of dq come from o and o2 as they are given
- * (rounded); those of dk, and dlam, from the fp32 sums of Pm dP.  Workspace: status block, row
+ * The row terms D = dO . Om of dq come from o and o2 as they are given (rounded, which the more
+ * peaked the maps are the more of dq's error it makes; dash_diff_bwd_rest adds what the rounding
+ * lost); those of dk, and dlam, from the fp32 sums of Pm dP.  Workspace: status block, row
  * vectors of B*H*Sp*20 bytes (Sp = S rounded up to 128), partial sums of dlam and, 80 MB at most,
  * of key tiles that are formed in pieces; dash_attn_status reads either status word. */
 size_t dash_diff_bwd_workspace_bytes(int B, int S, int H, int d);
@@ -403,6 +411,14 @@ dash_status_t dash_diff_bwd(const void *q, const void *k, const void *v, const v
                             int group, int d, float scale, dash_mask_t mask,
                             dash_dtype_t lam_dtype, int lam_per_token, void *workspace,
                             size_t workspace_bytes, dash_stream_t stream);
+/* The same with the forward's rest (NULL: none). */
+dash_status_t dash_diff_bwd_rest(const void *q, const void *k, const void *v, const void *o,
+                                 const void *o2, const void *rest, const void *dout,
+                                 const float *lse, const void *lam, void *dq, void *dk, void *dv,
+                                 void *dlam, int B, int S, int H, int group, int d, float scale,
+                                 dash_mask_t mask, dash_dtype_t lam_dtype, int lam_per_token,
+                                 void *workspace, size_t workspace_bytes, dash_stream_t stream);
+
 
 /* Human-readable name of a status code (static storage). */
 const char *dash_status_string(dash_status_t status);

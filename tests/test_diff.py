@@ -414,3 +414,104 @@ def test_abi_refusals(L):
     assert bwd(ws=None) == 5 and bwd(n=n - 1) == 5
     assert n >= 256 + 4 * 128 * 20 and dash.diff_bwd_workspace_bytes(1, 8, 4, 96) == 0
     assert L.dash_diff_fwd_workspace_bytes(1, 8, 4, 32) == 256
+
+
+def with_rest(q, k, v, w, do, causal, **kw):
+    rest = torch.full((2, *do.shape), math.nan, dtype=BF, device="cuda")
+    o, o2, lse = dash.diff_fwd(q, k, v, w, causal=causal, check=True, rest=rest, **kw)
+    return (o, o2, lse, rest), dash.diff_bwd(q, k, v, o, o2, do, lse, w, causal=causal, check=True,
+                                             rest=rest, **kw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [32, 64])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("S,H,Hkv,lam", [(1, 1, 1, "head-bf16"), (17, 2, 1, "token-fp32"),
+                                         (129, 4, 2, "head-fp32"), (300, 2, 2, "token-bf16"),
+                                         (1030, 3, 1, "head-bf16")])
+def test_rest_of_the_outputs(L, S, H, Hkv, lam, causal, d):
+    """rest adds what O and O2 lose: the sum is off by what P's rounding gives, (2^-8 + r) of the
+    terms, and twice a rounding, 2^-16 of the value.  All else is what the calls give without it,
+    bit for bit, but dQ."""
+    q, k, v, w, do = make(2, S, H, Hkv, d, lam, seed=S)
+    (o, o2, lse, rest), grads = with_rest(q, k, v, w, do, causal)
+    f = Exact(q, k, v, w, causal).forward()
+    for n, x, y in (("o", o, rest[0]), ("o2", o2, rest[1])):
+        ref, tol = f[n]
+        both = x.double() + y.double()
+        assert (y.double().abs() <= HALF * x.double().abs() * (1 + HALF)).all()
+        assert ((both - ref).abs() <= tol * (1 + 2 * HALF) + 2.0 ** -16 * ref.abs()).all()
+    p = dash.diff_fwd(q, k, v, w, causal=causal)
+    assert all(torch.equal(a, b) for a, b in zip((o, o2, lse), p))
+    plain = dash.diff_bwd(q, k, v, o, o2, do, lse, w, causal=causal)
+    assert all(torch.equal(a, b) for a, b in zip(grads[1:], plain[1:]))
+    zero = dash.diff_bwd(q, k, v, o, o2, do, lse, w, causal=causal, rest=torch.zeros_like(rest))
+    assert all(torch.equal(a, b) for a, b in zip(zero, plain))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [32, 64])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("spread", [1.0, 2.0, 4.0, 8.0])
+def test_dq_with_rest(L, spread, causal, d):
+    """dQ against its definition in 64 bits, D from P and dP, in the Euclidean norm.  Roundings are
+    off by 2^-8 of the value at most, evenly spread, 2^-8 / sqrt(3) in the root mean square, each
+    its own way.  Three reach dQ: its own; dS's, through dS K; P's in the forward, through
+    D = sum P dP and P K.  Their squares add up (two more of D's, 2^-16, and r do not count)."""
+    S, H = 700, 2
+    q, k, v, w, do = make(1, S, H, H, d, "head-fp32", seed=7, spread=spread)
+    w = torch.tensor([0.8, 1.0], device="cuda")
+    _, (dq, *_) = with_rest(q, k, v, w, do, causal)
+    e = Exact(q, k, v, w, causal)
+    P = (e.s - e.lse[..., None]).exp()
+    dP = do.double().transpose(1, 2) @ e.v.transpose(-1, -2)
+    by = torch.stack([torch.ones_like(e.lam), -e.lam])
+    dS = by * P * (dP - (P * dP).sum(-1, keepdim=True))
+    offD = (P * dP).square().sum(-1, keepdim=True)
+    for m in range(2):
+        want = e.c * dS[m] @ e.k[m]
+        got = dq.double().view(1, S, H, 2, d)[:, :, :, m].transpose(1, 2)
+        inner = e.c ** 2 * (dS[m].square() @ e.k[m].square() +
+                            by[m].square() * offD[m] * (P[m] @ e.k[m]).square())
+        tol = HALF / 3 ** 0.5 * (want.square().sum() + inner.sum()).sqrt()
+        assert (got - want).norm() <= tol, ((got - want).norm() / want.norm()).item()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [32, 64])
+def test_dq_of_a_row_that_sees_one_key(L, d):
+    """dQ is zero: P = 1, and D = dO . V1 comes back from O + lam O2 with two roundings of 2^-16 of
+    the terms (2^-15 with the fp32 sums), times one key."""
+    q, k, v, w, do = make(3, 200, 4, 2, d, "token-fp32", seed=2, spread=4.0)
+    (o, o2, *_), (dq, *_) = with_rest(q, k, v, w, do, True)
+    a = do[:, 0].double().abs()
+    own = v[:, 0].double().abs().repeat_interleave(2, 1)
+    lam = w[:, 0].double().abs()[..., None]
+    terms = (a * (o[:, 0].double().abs() + lam * o2[:, 0].double().abs() + own)).sum(-1)
+    key = k[:, 0].double().abs().view(3, 2, 2, d).repeat_interleave(2, 1)  # [B, H, 2, d]
+    tol = 2.0 ** -15 * terms[..., None, None] * key / math.sqrt(d)
+    tol[:, :, 1] *= lam
+    assert (dq[:, 0].double().abs().view(3, 4, 2, d) <= tol * (1 + HALF)).all()
+
+
+@pytest.mark.gpu
+def test_rest_refusals(L):
+    q, k, v, w, do = make(1, 8, 4, 2, 64, "head-bf16")
+    o, o2, lse = dash.diff_fwd(q, k, v, w)
+    rest = torch.empty(2, *do.shape, dtype=BF, device="cuda")
+    both = torch.empty(3, *do.shape, dtype=BF, device="cuda")
+    for bad in (rest[0], rest[:1], rest.float(), rest.cpu(), rest.transpose(0, 1)):
+        with pytest.raises(ValueError):
+            dash.diff_fwd(q, k, v, w, rest=bad)
+        with pytest.raises(ValueError):
+            dash.diff_bwd(q, k, v, o, o2, do, lse, w, rest=bad)
+    for kw in (dict(out=rest[0], rest=rest), dict(out2=both[1], rest=both[:2])):
+        with pytest.raises((ValueError, dash.DashError)):
+            dash.diff_fwd(q, k, v, w, **kw)
+    with pytest.raises((ValueError, dash.DashError)):
+        dash.diff_bwd(q, k, v, o, o2, do, lse, w, rest=both[:2], dv=both.view(-1)[:v.numel()].view(
+            v.shape))
+    for B, S in ((0, 5), (2, 0)):
+        x, y, z, u, g = make(B, S, 2, 1, 64, "head-bf16")
+        out, grads = with_rest(x, y, z, u, g, True)
+        assert out[0].shape == g.shape and (grads[3] == 0).all()
