@@ -515,3 +515,12 @@ def test_rest_refusals(L):
         x, y, z, u, g = make(B, S, 2, 1, 64, "head-bf16")
         out, grads = with_rest(x, y, z, u, g, True)
         assert out[0].shape == g.shape and (grads[3] == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,causal", [(64, True), (64, False), (32, True)])
+def test_long_sequence_backward(L, d, causal):
+    """64 key blocks and query tiles: every gradient against 64 bits.  dK sums 16384 queries in
+    1024 additions of 16, which is within 2^-14 of the terms, so within r as before."""
+    run(1, 8192, 2, 1, d, causal, "head-bf16", seed=4)
+    torch.cuda.empty_cache()

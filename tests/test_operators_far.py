@@ -68,3 +68,23 @@ def test_diff():
         y = y.double()
         diff = (x[-1:].double() - y).abs()
         assert (diff <= 2 * 2.0 ** -8 * y.abs() + 2.0 ** -10 * y.abs().mean()).all()
+
+
+def test_diff_weights_gradient():
+    """dlam of more than 2^31 elements, summed from every sequence's tiles, against the sum of
+    dO . O2 in 64 bits, O2 with what its rounding lost.  Values and dO are positive, so no terms
+    cancel: a row's sum is off by P's rounding, 2^-8 / sqrt(3) of it in the root mean square, those
+    of 532480 rows together by 2^-17, ten times less than the bound; one tile of the 4160 of a head
+    that were left out or taken twice would be two times the bound."""
+    B, S, H, Hkv, d = 65, 8192, 32, 8, 64
+    q, k = big(B, S, 2 * H, d, seed=1), big(B, S, 2 * Hkv, d, seed=2)
+    v, do = big(B, S, Hkv, 2 * d, seed=3).abs_(), big(B, S, H, 2 * d, seed=4).abs_()
+    lam = torch.linspace(0.1, 0.9, H, device="cuda")
+    rest = torch.empty(2, B, S, H, 2 * d, dtype=BF, device="cuda")
+    o, o2, lse = dash.diff_fwd(q, k, v, lam, causal=True, check=True, rest=rest)
+    *_, dlam = dash.diff_bwd(q, k, v, o, o2, do, lse, lam, causal=True, check=True, rest=rest)
+    want = torch.zeros(H, dtype=torch.float64, device="cuda")
+    for b in range(B):
+        want -= (do[b].double() * (o2[b].double() + rest[1, b].double())).sum((0, 2))
+    assert ((dlam.double() - want).abs() <= 2.0 ** -13 * want.abs()).all(), \
+        (dlam.double() / want - 1).abs().max().item()
