@@ -50,7 +50,7 @@ EXPORTS = ["dash_attn_fwd_workspace_bytes", "dash_attn_fwd", "dash_attn_bwd_work
            "dash_attn_fwd_varlen", "dash_attn_bwd_varlen", "dash_attn_bwd_varlen_order_log",
            "dash_rope", "dash_join_fwd", "dash_join_bwd", "dash_join_bwd_workspace_bytes",
            "dash_diff_fwd_workspace_bytes", "dash_diff_fwd", "dash_diff_bwd_workspace_bytes",
-           "dash_diff_bwd", "dash_diff_fwd_rest", "dash_diff_bwd_rest"]
+           "dash_diff_bwd", "dash_diff_fwd_rest", "dash_diff_bwd_rest", "dash_diff_withhold"]
 
 
 class DashError(RuntimeError):
@@ -148,6 +148,8 @@ def lib() -> ctypes.CDLL:
                               ("dash_diff_bwd", 12), ("dash_diff_bwd_rest", 13)):
             getattr(L, name).argtypes = [vp] * tensors + [i, i, i, i, i, f, i, i, i, vp, sz, vp]
             getattr(L, name).restype = i
+        L.dash_diff_withhold.argtypes = [i, i]
+        L.dash_diff_withhold.restype = i
         _lib = L
         return L
 

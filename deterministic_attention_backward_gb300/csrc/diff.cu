@@ -94,6 +94,13 @@ bool lam_ok(const void *lam, int dtype) {
          (reinterpret_cast<uintptr_t>(lam) & (dtype == DASH_FP32 ? 3 : 1)) == 0;
 }
 
+// dash_diff_withhold: the kernel (0: none), and above it the block.
+std::atomic<long long> g_withhold{0};
+int withheld(int kernel) {
+  const long long w = g_withhold.load();
+  return (w & 3) == kernel ? (int)(w >> 2) : -1;
+}
+
 // The bytes of a bf16 tensor of `heads` heads of 2d, and of the weights.
 Bytes heads_of(const void *p, int B, int S, int heads, int d) {
   return bytes_of(p, 2, (long long)B * S * heads * 2 * d);
@@ -106,6 +113,12 @@ Bytes weights_of(const void *p, int B, int S, int H, int dtype, bool per_token) 
 }  // namespace dash
 
 extern "C" {
+
+dash_status_t dash_diff_withhold(int kernel, int block) {
+  if (kernel < 0 || kernel > 3 || block < 0) return DASH_ERR_INVALID;
+  dash::g_withhold.store((long long)block << 2 | kernel);
+  return DASH_OK;
+}
 
 size_t dash_diff_fwd_workspace_bytes(int B, int S, int H, int d) {
   return dash::check_diff(B, S, H, 1, d) == DASH_OK ? dash::kStatusBytes : 0;
@@ -170,6 +183,7 @@ dash_status_t dash_diff_fwd_rest(const void *q, const void *k, const void *v, co
   p.lam_f32 = lam_dtype == DASH_FP32;
   p.lam_token = lam_per_token != 0;
   p.wait_ns = g_wait_ns.load();
+  p.withhold = withheld(1);
   p.scale_log2 = (scale > 0.f ? scale : 1.0f / std::sqrt((float)d)) * kLog2e;
   return launch_diff_fwd(d, tq, tk, tv, p, dev.sms, s) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
 }
@@ -243,6 +257,7 @@ dash_status_t dash_diff_bwd_rest(const void *q, const void *k, const void *v, co
   p.lam_f32 = lam_dtype == DASH_FP32;
   p.lam_token = lam_per_token != 0;
   p.wait_ns = g_wait_ns.load();
+  p.withhold_dq = withheld(2), p.withhold_dkv = withheld(3);
   p.scale = scale > 0.f ? scale : 1.0f / std::sqrt((float)d);
   p.scale_log2 = p.scale * kLog2e;
   const Cut cut = cut_tiles(B, S, Hkv, group, d, p.causal);

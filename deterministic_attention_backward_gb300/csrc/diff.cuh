@@ -22,6 +22,7 @@ struct DiffFwdParams {
   uint32_t *taken;        // tiles that CTAs have taken beside their first (cleared)
   int B, S, H, Hkv, G, N, causal;
   int lam_f32, lam_token;
+  int withhold;           // block at which a CTA's loads end (dash_diff_withhold), else -1
   unsigned long long wait_ns;
   float scale_log2;       // softmax scale * log2(e)
 };
@@ -47,6 +48,7 @@ struct DiffBwdParams {
   void *dlam;             // [H] or [B,S,H], lam's type
   int B, S, H, Hkv, G, N, causal;
   int lam_f32, lam_token;
+  int withhold_dq, withhold_dkv;  // as in the forward
   unsigned long long wait_ns;
   float scale_log2, scale;
   // dK/dV's kernel: the first kv_whole tiles are a CTA each, the others kv_pieces CTAs each,

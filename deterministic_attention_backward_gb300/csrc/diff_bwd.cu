@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int j = 0; j < nkv; ++j) {
       const int sk = j % L::kK, sv = j % L::kV;
-      if (!mbar_wait(&v_empty[sv], ((j / L::kV) & 1) ^ 1, ab)) {
+      if (j == p.withhold_dq || !mbar_wait(&v_empty[sv], ((j / L::kV) & 1) ^ 1, ab)) {
         ok = false;
         break;
       }
@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int n = 0; n < steps; ++n) {
         const int s = n % L::kStages;
         const uint32_t ph = (n / L::kStages) & 1;
-        if (!mbar_wait(&q_empty[s], ph ^ 1, ab)) {
+        if (n == p.withhold_dkv || !mbar_wait(&q_empty[s], ph ^ 1, ab)) {
           ok = false;
           break;
         }

@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = nk % L::kStages;
         const uint32_t ph = (nk / L::kStages) & 1;
         uint8_t *sk = smem + L::offStage + s * L::kStageBytes;
-        if (!mbar_wait(&k_empty[s], ph ^ 1, ab)) {
+        if (nk == p.withhold || !mbar_wait(&k_empty[s], ph ^ 1, ab)) {
           ok = false;
           break;
         }

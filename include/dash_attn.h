@@ -420,6 +420,11 @@ dash_status_t dash_diff_bwd_rest(const void *q, const void *k, const void *v, co
                                  void *workspace, size_t workspace_bytes, dash_stream_t stream);
 
 
+/* For tests of failure detection, process-wide: from the next call on the loads of every CTA of one
+ * kernel (1: the forward, 2: dQ's, 3: dK/dV's; 0: of none any more) end before its block `block`
+ * (128 keys; 64 queries in dK/dV's), so that the waits for it run out. */
+dash_status_t dash_diff_withhold(int kernel, int block);
+
 /* Human-readable name of a status code (static storage). */
 const char *dash_status_string(dash_status_t status);
 
