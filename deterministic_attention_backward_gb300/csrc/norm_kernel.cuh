@@ -52,6 +52,12 @@ __device__ __forceinline__ void load_w(const void *w, long long at, int wf32, fl
   }
 }
 template <typename T>
+__device__ __forceinline__ float load_w(const void *w, long long at, int wf32) {
+  float f[1];
+  load_w<T, 1>(w, at, wf32, f);
+  return f[0];
+}
+template <typename T>
 __device__ __forceinline__ void store_w(void *w, long long at, int wf32, float v) {
   if (wf32)
     static_cast<float *>(w)[at] = v;
@@ -85,7 +91,8 @@ struct RowSum {
 template <int kNT>
 constexpr int kRowsPerCta = kNT == 32 ? 8 : 1;
 
-template <typename T, int V, int kNT, int kNV, bool kJoin>
+// Rows element by element, in registers.
+template <typename T, int kNT, int kNV, bool kJoin>
 __global__ void __launch_bounds__(kNT * kRowsPerCta<kNT>) fwd_rows(const NormFwdParams p) {
   constexpr int kRows = kRowsPerCta<kNT>;
   __shared__ float red[2 * (kNT / 32)];
@@ -95,13 +102,14 @@ __global__ void __launch_bounds__(kNT * kRowsPerCta<kNT>) fwd_rows(const NormFwd
   if (row >= p.rows) return;  // whole rows: every thread of the row's sums, or none
   const float inv_c = 1.f / (float)p.C;
   const T *x = static_cast<const T *>(p.x) + row * p.xs;
-  Pack<T, V> px[kNV], pa[kNV];
+  const T *a = static_cast<const T *>(p.a) + row * p.as;
+  T px[kNV], pa[kNV];
 #pragma unroll
   for (int i = 0; i < kNV; ++i) {
-    const int c = (i * kNT + lane) * V;
+    const int c = i * kNT + lane;
     if (c < p.C) {
-      px[i] = load_pack<T, V>(x + c);
-      if constexpr (kJoin) pa[i] = load_pack<T, V>(static_cast<const T *>(p.a) + row * p.as + c);
+      px[i] = x[c];
+      if constexpr (kJoin) pa[i] = a[c];
     }
   }
   float rstd_a = 1.f;
@@ -110,45 +118,30 @@ __global__ void __launch_bounds__(kNT * kRowsPerCta<kNT>) fwd_rows(const NormFwd
       float ss = 0.f;
 #pragma unroll
       for (int i = 0; i < kNV; ++i)
-        if ((i * kNT + lane) * V < p.C) {
-          float a[V];
-          unpack<T, V>(pa[i], a);
-#pragma unroll
-          for (int e = 0; e < V; ++e) ss = fmaf(a[e], a[e], ss);
+        if (i * kNT + lane < p.C) {
+          const float v = to_f32<T>(pa[i]);
+          ss = fmaf(v, v, ss);
         }
       rstd_a = rsqrtf(row_sum(ss) * inv_c + p.eps);
       if (lane == 0) p.rstd_a[row] = rstd_a;
     }
   }
   const long long grow = (row / p.gate_rows) * p.C;
-  float y[kNV][V];
+  float y[kNV];
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < kNV; ++i) {
-    const int c = (i * kNT + lane) * V;
+    const int c = i * kNT + lane;
     if (c < p.C) {
-      unpack<T, V>(px[i], y[i]);
+      y[i] = to_f32<T>(px[i]);
       if constexpr (kJoin) {
-        float a[V], w[V];
-        unpack<T, V>(pa[i], a);
-#pragma unroll
-        for (int e = 0; e < V; ++e) a[e] *= p.branch * rstd_a;
-        if (p.w_post) {
-          load_w<T, V>(p.w_post, c, p.wf32, w);
-#pragma unroll
-          for (int e = 0; e < V; ++e) a[e] *= w[e];
-        }
-        if (p.gate) {
-          load_w<T, V>(p.gate, grow + c, p.wf32, w);
-#pragma unroll
-          for (int e = 0; e < V; ++e) a[e] *= w[e];
-        }
-#pragma unroll
-        for (int e = 0; e < V; ++e) y[i][e] = fmaf(p.skip, y[i][e], a[e]);
-        store_pack<T, V>(static_cast<T *>(p.y) + row * p.ys + c, pack<T, V>(y[i]));
+        float v = to_f32<T>(pa[i]) * (p.branch * rstd_a);
+        if (p.w_post) v *= load_w<T>(p.w_post, c, p.wf32);
+        if (p.gate) v *= load_w<T>(p.gate, grow + c, p.wf32);
+        y[i] = fmaf(p.skip, y[i], v);
+        static_cast<T *>(p.y)[row * p.ys + c] = from_f32<T>(y[i]);
       }
-#pragma unroll
-      for (int e = 0; e < V; ++e) ss = fmaf(y[i][e], y[i][e], ss);
+      ss = fmaf(y[i], y[i], ss);
     }
   }
   if (!p.w_next) return;
@@ -157,14 +150,10 @@ __global__ void __launch_bounds__(kNT * kRowsPerCta<kNT>) fwd_rows(const NormFwd
   if (lane == 0) p.rstd_y[row] = rstd;
 #pragma unroll
   for (int i = 0; i < kNV; ++i) {
-    const int c = (i * kNT + lane) * V;
-    if (c < p.C) {
-      float w[V];
-      load_w<T, V>(p.w_next, c, p.wf32, w);
-#pragma unroll
-      for (int e = 0; e < V; ++e) w[e] *= y[i][e] * rstd;
-      store_pack<T, V>(static_cast<T *>(p.h) + row * p.hs + c, pack<T, V>(w));
-    }
+    const int c = i * kNT + lane;
+    if (c < p.C)
+      static_cast<T *>(p.h)[row * p.hs + c] =
+          from_f32<T>(load_w<T>(p.w_next, c, p.wf32) * (y[i] * rstd));
   }
 }
 
@@ -239,8 +228,9 @@ __global__ void __launch_bounds__(512) fwd_long(const NormFwdParams p) {
 }
 
 // ------------------------------------------------------------------------------- backward
-// kSmem: the column sums live in shared memory instead of registers (long rows).
-template <typename T, int V, int kNT, int kNV, bool kJoin, bool kSmem>
+// Rows element by element, in registers; kSmem: the column sums live in shared memory instead
+// (long rows).
+template <typename T, int kNT, int kNV, bool kJoin, bool kSmem>
 __global__ void __launch_bounds__(kNT * kRowsPerCta<kNT>)
     bwd_rows(const NormBwdParams p) {
   constexpr int kRows = kRowsPerCta<kNT>;
@@ -253,33 +243,30 @@ __global__ void __launch_bounds__(kNT * kRowsPerCta<kNT>)
   const int group = blockIdx.x / p.ctas, cta = blockIdx.x % p.ctas;
   const long long row0 = group * p.gate_rows, row1 = row0 + p.gate_rows;
   const float inv_c = 1.f / (float)p.C;
-  float accN[kSmem ? 1 : kNV][V], accA[kSmem || !kJoin ? 1 : kNV][V];
+  float accN[kSmem ? 1 : kNV], accA[kSmem || !kJoin ? 1 : kNV];
   if constexpr (kSmem) {
     for (int c = threadIdx.x; c < kSums * p.C; c += kNT) dyn[c] = 0.f;
     __syncthreads();
   } else {
 #pragma unroll
-    for (int i = 0; i < kNV; ++i)
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        accN[i][e] = 0.f;
-        if constexpr (kJoin) accA[i][e] = 0.f;
-      }
+    for (int i = 0; i < kNV; ++i) {
+      accN[i] = 0.f;
+      if constexpr (kJoin) accA[i] = 0.f;
+    }
   }
   for (long long row = row0 + (long long)cta * kRows + sub; row < row1;
        row += (long long)p.ctas * kRows) {
-    Pack<T, V> pdh[kNV], py[kNV], pdy[kNV], pa[kNV];
+    T pdh[kNV], py[kNV], pdy[kNV], pa[kNV];
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
-      const int c = (i * kNT + lane) * V;
+      const int c = i * kNT + lane;
       if (c < p.C) {
         if (p.w_next) {
-          pdh[i] = load_pack<T, V>(static_cast<const T *>(p.dh) + row * p.dhs + c);
-          py[i] = load_pack<T, V>(static_cast<const T *>(p.y) + row * p.ys + c);
+          pdh[i] = static_cast<const T *>(p.dh)[row * p.dhs + c];
+          py[i] = static_cast<const T *>(p.y)[row * p.ys + c];
         }
-        if (p.dy) pdy[i] = load_pack<T, V>(static_cast<const T *>(p.dy) + row * p.dys + c);
-        if constexpr (kJoin)
-          pa[i] = load_pack<T, V>(static_cast<const T *>(p.a) + row * p.as + c);
+        if (p.dy) pdy[i] = static_cast<const T *>(p.dy)[row * p.dys + c];
+        if constexpr (kJoin) pa[i] = static_cast<const T *>(p.a)[row * p.as + c];
       }
     }
     const float rstd_y = p.w_next ? p.rstd_y[row] : 0.f;
@@ -288,112 +275,65 @@ __global__ void __launch_bounds__(kNT * kRowsPerCta<kNT>)
     if (p.w_next) {
 #pragma unroll
       for (int i = 0; i < kNV; ++i) {
-        const int c = (i * kNT + lane) * V;
+        const int c = i * kNT + lane;
         if (c < p.C) {
-          float dh[V], q[V], w[V];
-          unpack<T, V>(pdh[i], dh);
-          unpack<T, V>(py[i], q);
-          load_w<T, V>(p.w_next, c, p.wf32, w);
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            const float dq = dh[e] * (q[e] * rstd_y);
-            c1 = fmaf(dq, w[e], c1);
-            if constexpr (kSmem)
-              dyn[c + e] += dq;
-            else
-              accN[i][e] += dq;
-          }
+          const float dq = to_f32<T>(pdh[i]) * (to_f32<T>(py[i]) * rstd_y);
+          c1 = fmaf(dq, load_w<T>(p.w_next, c, p.wf32), c1);
+          if constexpr (kSmem)
+            dyn[c] += dq;
+          else
+            accN[i] += dq;
         }
       }
       c1 = row_sum(c1) * inv_c;
     }
-    // Dy of one vector of columns
-    auto joined = [&](int i, int c, float (&D)[V]) {
-      if (p.dy)
-        unpack<T, V>(pdy[i], D);
-      else
-#pragma unroll
-        for (int e = 0; e < V; ++e) D[e] = 0.f;
-      if (p.w_next) {
-        float dh[V], q[V], w[V];
-        unpack<T, V>(pdh[i], dh);
-        unpack<T, V>(py[i], q);
-        load_w<T, V>(p.w_next, c, p.wf32, w);
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-          D[e] = fmaf(rstd_y, fmaf(-(q[e] * rstd_y), c1, dh[e] * w[e]), D[e]);
-      }
+    // Dy of one column
+    auto joined = [&](int i, int c) {
+      float D = p.dy ? to_f32<T>(pdy[i]) : 0.f;
+      if (p.w_next)
+        D = fmaf(rstd_y,
+                 fmaf(-(to_f32<T>(py[i]) * rstd_y), c1,
+                      to_f32<T>(pdh[i]) * load_w<T>(p.w_next, c, p.wf32)),
+                 D);
+      return D;
     };
     if constexpr (!kJoin) {
 #pragma unroll
       for (int i = 0; i < kNV; ++i) {
-        const int c = (i * kNT + lane) * V;
-        if (c < p.C) {
-          float D[V];
-          joined(i, c, D);
-          store_pack<T, V>(static_cast<T *>(p.dx) + row * p.dxs + c, pack<T, V>(D));
-        }
+        const int c = i * kNT + lane;
+        if (c < p.C) static_cast<T *>(p.dx)[row * p.dxs + c] = from_f32<T>(joined(i, c));
       }
     } else {
       const long long grow = (p.row_gate ? row : group) * p.C;
-      // t = branch gate Dy of one vector of columns (and the sums it feeds, the first time)
+      // t = branch gate Dy w_post of one column
       float c2 = 0.f;
-      float t[kNV][V];
+      float t[kNV];
 #pragma unroll
       for (int i = 0; i < kNV; ++i) {
-        const int c = (i * kNT + lane) * V;
+        const int c = i * kNT + lane;
         if (c < p.C) {
-          float D[V], z[V], w[V];
-          joined(i, c, D);
-          unpack<T, V>(pa[i], z);
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            z[e] *= rstd_a;
-            t[i][e] = D[e] * p.skip;
-          }
-          store_pack<T, V>(static_cast<T *>(p.dx) + row * p.dxs + c, pack<T, V>(t[i]));
-#pragma unroll
-          for (int e = 0; e < V; ++e) t[i][e] = D[e] * p.branch;
-          if (p.gate) {
-            load_w<T, V>(p.gate, grow + c, p.wf32, w);
-#pragma unroll
-            for (int e = 0; e < V; ++e) t[i][e] *= w[e];
-          }
-          if (p.w_post) {
-            load_w<T, V>(p.w_post, c, p.wf32, w);
-          } else {
-#pragma unroll
-            for (int e = 0; e < V; ++e) w[e] = 1.f;
-          }
-          if (p.row_gate)
-#pragma unroll
-            for (int e = 0; e < V; ++e)
-              store_w<T>(p.dgate, row * p.C + c + e, p.wf32, p.branch * D[e] * w[e] * z[e]);
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            const float A = (p.row_gate ? t[i][e] : D[e]) * z[e];
-            if constexpr (kSmem)
-              dyn[p.C + c + e] += A;
-            else
-              accA[i][e] += A;
-            t[i][e] *= w[e];
-            c2 = fmaf(t[i][e], z[e], c2);
-          }
+          const float D = joined(i, c), z = to_f32<T>(pa[i]) * rstd_a;
+          static_cast<T *>(p.dx)[row * p.dxs + c] = from_f32<T>(D * p.skip);
+          t[i] = D * p.branch;
+          if (p.gate) t[i] *= load_w<T>(p.gate, grow + c, p.wf32);
+          const float w = p.w_post ? load_w<T>(p.w_post, c, p.wf32) : 1.f;
+          if (p.row_gate) store_w<T>(p.dgate, row * p.C + c, p.wf32, p.branch * D * w * z);
+          const float A = (p.row_gate ? t[i] : D) * z;
+          if constexpr (kSmem)
+            dyn[p.C + c] += A;
+          else
+            accA[i] += A;
+          t[i] *= w;
+          c2 = fmaf(t[i], z, c2);
         }
       }
       if (p.w_post) c2 = row_sum(c2) * inv_c;
 #pragma unroll
       for (int i = 0; i < kNV; ++i) {
-        const int c = (i * kNT + lane) * V;
+        const int c = i * kNT + lane;
         if (c < p.C) {
-          if (p.w_post) {
-            float z[V];
-            unpack<T, V>(pa[i], z);
-#pragma unroll
-            for (int e = 0; e < V; ++e)
-              t[i][e] = rstd_a * fmaf(-(z[e] * rstd_a), c2, t[i][e]);
-          }
-          store_pack<T, V>(static_cast<T *>(p.da) + row * p.das + c, pack<T, V>(t[i]));
+          if (p.w_post) t[i] = rstd_a * fmaf(-(to_f32<T>(pa[i]) * rstd_a), c2, t[i]);
+          static_cast<T *>(p.da)[row * p.das + c] = from_f32<T>(t[i]);
         }
       }
     }
@@ -406,13 +346,11 @@ __global__ void __launch_bounds__(kNT * kRowsPerCta<kNT>)
   } else if constexpr (kRows == 1) {
 #pragma unroll
     for (int i = 0; i < kNV; ++i) {
-      const int c = (i * kNT + lane) * V;
-      if (c < p.C)
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          out[c + e] = accN[i][e];
-          if constexpr (kJoin) out[p.C + c + e] = accA[i][e];
-        }
+      const int c = i * kNT + lane;
+      if (c < p.C) {
+        out[c] = accN[i];
+        if constexpr (kJoin) out[p.C + c] = accA[i];
+      }
     }
   } else {
 #pragma unroll
@@ -420,11 +358,8 @@ __global__ void __launch_bounds__(kNT * kRowsPerCta<kNT>)
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < kNV; ++i) {
-        const int c = (i * kNT + lane) * V;
-        if (c < p.C)
-#pragma unroll
-          for (int e = 0; e < V; ++e)
-            dyn[sub * p.C + c + e] = k ? accA[kJoin ? i : 0][e] : accN[i][e];
+        const int c = i * kNT + lane;
+        if (c < p.C) dyn[sub * p.C + c] = k ? accA[kJoin ? i : 0] : accN[i];
       }
       __syncthreads();
       for (int c = threadIdx.x; c < p.C; c += kNT * kRows) {
@@ -1215,9 +1150,9 @@ cudaError_t fwd(const NormFwdParams &p, cudaStream_t s) {
       return p.period ? launch(std::true_type()) : launch(std::false_type());
     });
   } else {
-    if (n <= 128) return go(fwd_rows<T, V, 32, 4, kJoin>, 256, 8);
-    if (n <= 512) return go(fwd_rows<T, V, 256, 2, kJoin>, 256, 1);
-    return go(fwd_rows<T, V, 512, 4, kJoin>, 512, 1);
+    if (n <= 128) return go(fwd_rows<T, 32, 4, kJoin>, 256, 8);
+    if (n <= 512) return go(fwd_rows<T, 256, 2, kJoin>, 256, 1);
+    return go(fwd_rows<T, 512, 4, kJoin>, 512, 1);
   }
 }
 
@@ -1243,11 +1178,11 @@ cudaError_t bwd(const NormBwdParams &p, cudaStream_t s) {
                                                                                  smem, s, p);
     });
   } else if (n <= 128) {
-    e = launch_smem<bwd_rows<T, V, 32, 4, kJoin, false>>(grid, 256, (size_t)8 * p.C * 4, s, p);
+    e = launch_smem<bwd_rows<T, 32, 4, kJoin, false>>(grid, 256, (size_t)8 * p.C * 4, s, p);
   } else if (n <= 512) {
-    e = launch_smem<bwd_rows<T, V, 256, 2, kJoin, false>>(grid, 256, 0, s, p);
+    e = launch_smem<bwd_rows<T, 256, 2, kJoin, false>>(grid, 256, 0, s, p);
   } else {
-    e = launch_smem<bwd_rows<T, V, 512, 4, kJoin, true>>(grid, 512, (size_t)kSums * p.C * 4, s, p);
+    e = launch_smem<bwd_rows<T, 512, 4, kJoin, true>>(grid, 512, (size_t)kSums * p.C * 4, s, p);
   }
   if (e != cudaSuccess) return e;
   bwd_sums<T, kJoin><<<(p.C + 31) / 32, 1024, 0, s>>>(p);
