@@ -28,7 +28,8 @@ __all__ = ["fwd", "bwd", "bwd_workspace_bytes", "fwd_workspace_bytes", "status",
            "sched_resolve", "packed_rank", "fwd_varlen", "bwd_varlen", "bwd_varlen_workspace_bytes",
            "bwd_varlen_order_log", "SCHEDULES", "lib",
            "DashError", "rope_freqs", "rope_fwd", "rope_bwd", "norm_fwd", "norm_bwd",
-           "join_fwd", "join_bwd", "diff_fwd", "diff_bwd", "diff_bwd_workspace_bytes"]
+           "join_fwd", "join_bwd", "diff_fwd", "diff_bwd", "diff_fwd_workspace_bytes",
+           "diff_bwd_workspace_bytes"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libdash_attn.so")
@@ -463,7 +464,8 @@ def bwd_varlen_order_log(q, k, v, o, do, lse, cu_seqlens, causal: bool = False,
 # are loaded with the first name that is asked of them.
 _MODULES = {"rope_freqs": "rope", "rope_fwd": "rope", "rope_bwd": "rope", "norm_fwd": "norms",
             "norm_bwd": "norms", "join_fwd": "norms", "join_bwd": "norms", "diff_fwd": "diff",
-            "diff_bwd": "diff", "diff_bwd_workspace_bytes": "diff"}
+            "diff_bwd": "diff", "diff_fwd_workspace_bytes": "diff",
+            "diff_bwd_workspace_bytes": "diff"}
 
 
 def __getattr__(name):

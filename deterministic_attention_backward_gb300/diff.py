@@ -58,6 +58,11 @@ def _given(t, name, like, shape, dtype=None):
     contiguous(t, name)
 
 
+def diff_fwd_workspace_bytes(B: int, S: int, H: int, d: int) -> int:
+    """Workspace bytes of ``diff_fwd`` for H head pairs of maps of d elements (0: unsupported)."""
+    return int(lib().dash_diff_fwd_workspace_bytes(B, S, H, d))
+
+
 def diff_bwd_workspace_bytes(B: int, S: int, H: int, d: int) -> int:
     """Workspace bytes of ``diff_bwd`` for H head pairs of maps of d elements (0: unsupported)."""
     return int(lib().dash_diff_bwd_workspace_bytes(B, S, H, d))
@@ -87,14 +92,14 @@ def diff_fwd(q, k, v, lam, causal: bool = False, scale: float | None = None, out
         l = lse if lse is not None else torch.empty((B, 2 * H, S), dtype=torch.float32,
                                                     device=q.device)
         if B and S:
-            ws = scratch(256, q, workspace)
-            _check(lib().dash_diff_fwd_rest(q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                            lam.data_ptr(), o.data_ptr(), o2.data_ptr(),
-                                            None if rest is None else rest.data_ptr(),
-                                            l.data_ptr(), B, S, H, H // Hkv, d, scale or 0.0,
-                                            bool(causal), 2 * (lam.dtype == torch.float32),
-                                            lam.dim() == 3, ws.data_ptr(),
-                                            ws.numel() * ws.element_size(), handle),
+            L = lib()
+            ws = scratch(L.dash_diff_fwd_workspace_bytes(B, S, H, d) or 256, q, workspace)
+            _check(L.dash_diff_fwd_rest(q.data_ptr(), k.data_ptr(), v.data_ptr(), lam.data_ptr(),
+                                        o.data_ptr(), o2.data_ptr(),
+                                        None if rest is None else rest.data_ptr(), l.data_ptr(),
+                                        B, S, H, H // Hkv, d, scale or 0.0, bool(causal),
+                                        2 * (lam.dtype == torch.float32), lam.dim() == 3,
+                                        ws.data_ptr(), ws.numel() * ws.element_size(), handle),
                    "dash_diff_fwd")
             if check:
                 status(ws, torch.cuda.current_stream())

@@ -524,3 +524,11 @@ def test_long_sequence_backward(L, d, causal):
     1024 additions of 16, which is within 2^-14 of the terms, so within r as before."""
     run(1, 8192, 2, 1, d, causal, "head-bf16", seed=4)
     torch.cuda.empty_cache()
+
+
+def test_forward_workspace_bytes(L):
+    """The size that a caller's own workspace of the forward needs, and no size where it has none."""
+    n = dash.diff_fwd_workspace_bytes(2, 300, 4, 64)
+    assert n == L.dash_diff_fwd_workspace_bytes(2, 300, 4, 64) == 256
+    assert dash.diff_fwd_workspace_bytes(2, 300, 4, 96) == 0
+    assert "diff_fwd_workspace_bytes" in dash.__all__
