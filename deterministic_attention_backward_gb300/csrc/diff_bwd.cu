@@ -6,10 +6,13 @@
 // tensor core asks for:
 //   dS1 = P1 (dP - D1)       dS2 = -lam P2 (dP - D2)        dlam_i = - sum_j P2 dP
 //   dQm = c ~dSm Km          dKm = c ~dSm^T Qm              dV = ~(P1 - lam P2)^T dO
-// Splitting the pass recomputes S1, S2 and dP (512 of then 1792 flops a pair at d = 64), and
-// avoids what a single key-stationary kernel pays on this GPU: fp32 dQ partials pushed into L2
-// at 16-20 bytes a cycle and SM, 64 KB a tile pair, longer than all of a tile pair's products,
-// and their ordering.
+// Two passes form S1, S2, dP and both maps' exponentials twice (512 of then 1792 flops a pair at
+// d = 64), so that no sum leaves the chip and nothing waits for another CTA.  One pass would be
+// stationary in keys and add 64 KB of fp32 dQ partials a tile pair in global memory in a fixed order,
+// as this library's main backward does at D = 128 with the same products: that reaches 1216 TFLOP/s
+// full and 937 to 975 causal at 8192, these two 959 and 872 of the same useful flops.  So one pass is
+// the faster form as far as products and partials go; the two exponentials a pair in place of its one
+// have not been weighed.
 #include "diff.cuh"
 
 #include "dash_attn.h"
@@ -24,7 +27,8 @@ constexpr int kThreads = (kWarps + 2) * 32;  // and the TMA producer, the MMA is
 
 // -------------------------------------------------------------------- row vectors
 // One CTA per tile of a (batch, head pair); DV / 8 lanes per row.  Bound by memory: 8 sequences of
-// 2048, 32 heads of 128, 66 us for 403 MB, 6.1 TB/s.
+// 2048, 32 heads of 128, 66 us for 403 MB, 6.1 TB/s.  kRest: with what the outputs lost by rounding,
+// 17 us more at 8192 tokens of 32 heads.
 template <int d, bool kRest>
 __global__ void __launch_bounds__(256) diff_rows_kernel(const DiffBwdParams p) {
   constexpr int DV = 2 * d, kLanes = DV / 8, kRows = 256 / kLanes;

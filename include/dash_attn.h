@@ -359,7 +359,8 @@ size_t dash_join_bwd_workspace_bytes(long long rows, int C, long long gate_rows,
                                      dash_dtype_t dtype);
 /* Gradient of dash_join_fwd: dy, dh are the gradients of y and h (dy may be NULL where nothing
  * else uses y; dh is read where w_next is given), y the forward's output (x for a plain norm,
- * whose dy is added to dx: the gradient of the residual stream beside the norm), a the branch.
+ * whose dy is added to dx: the gradient of the residual stream beside the norm), a the branch.  y
+ * is taken as it is, rounded, where the forward's h came from it unrounded.
  * Writes dx, da and, in the weights' type, dw_post, dgate, dw_next (each where its weight is
  * given).  Row strides of dy, dh, y, a, dx, da in `strides`.  dx and da may each be dy, dh, y or a
  * itself (with the same stride), not both the same.  The weight gradients are summed in an order
