@@ -139,15 +139,22 @@ inline Bytes flat(const Bytes &b) {
 inline bool share_parts(const Bytes &a, const Bytes &b, int &tries) {
   if (a.at + a.span() <= b.at || b.at + b.span() <= a.at || !a.run || !b.run) return false;
   if (a.at == b.at || (a.dims == 0 && b.dims == 0)) return true;
-  if (a.dims == 1 && b.dims == 1 && a.step[0] == b.step[0] && a.step[0] >= a.run &&
-      a.step[0] >= b.run) {
-    // run i of a begins `behind` bytes after run i + by of b
-    const long long step = a.step[0], d = (long long)(a.at - b.at);
-    const long long behind = (d % step + step) % step, by = (d - behind) / step;
-    auto meet = [&](long long k) {  // whether a run i of a has a run i + k of b
-      return (k < 0 ? -k : 0) < (a.count[0] < b.count[0] - k ? a.count[0] : b.count[0] - k);
-    };
-    return (behind < b.run && meet(by)) || (behind + a.run > step && meet(by + 1));
+  if (a.dims > 0 && b.dims > 0 && a.step[a.dims - 1] == b.step[b.dims - 1]) {
+    const long long step = a.step[a.dims - 1], n = a.count[a.dims - 1], m = b.count[b.dims - 1];
+    Bytes pa = a, pb = b;
+    --pa.dims, --pb.dims;
+    if (pa.span() <= step && pb.span() <= step) {
+      // part i of a begins `behind` bytes after part i + by of b, and may reach part i + by + 1
+      const long long d = (long long)(a.at - b.at);
+      const long long behind = (d % step + step) % step, by = (d - behind) / step;
+      auto meet = [&](long long k) {  // whether a part i of a has a part i + k of b
+        return (k < 0 ? -k : 0) < (n < m - k ? n : m - k);
+      };
+      pa.at = b.at + (uintptr_t)behind;
+      if (meet(by) && share_parts(pa, pb, tries)) return true;
+      pb.at = b.at + (uintptr_t)step;
+      return meet(by + 1) && share_parts(pa, pb, tries);
+    }
   }
   if (a.dims < b.dims || (a.dims == b.dims && a.step[a.dims - 1] < b.step[b.dims - 1]))
     return share_parts(b, a, tries);

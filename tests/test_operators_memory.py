@@ -207,3 +207,30 @@ def test_outputs_between_and_in_place(L):
     want = dash.join_fwd(x, a, w_post=w, w_next=w)
     got = dash.join_fwd(x, a, w_post=w, w_next=w, y=a, h=x)  # each in the other's place
     assert all(torch.equal(p, q) for p, q in zip(want, got))
+
+
+def test_long_tensors_of_padded_heads(L):
+    """Parts of heads of one buffer, whose strides do not flatten: told apart and together over any
+    number of tokens."""
+    S, W = 200000, 40 * 128 + 24
+    strides = (S * W, W, 128)
+
+    def call(at, out):
+        parts = [(at, 1 << 50, 0), (out, out, 0)]
+        packed = b"".join(_PART.pack(i, o, 3, 64, 0, *strides, *strides) for i, o, _ in parts)
+        packed += _PART.pack(1 << 55, 1 << 55, 1, 1 << 28, 0, *[1 << 29] * 6)
+        return L.dash_rope(packed, 3, 1, S, 2, 0, 0, 1 << 45, 1.0, None, 1, 0, 1, 0, 0, None)
+    base = 1 << 30
+    assert call(base, base + 128) == 2              # the other halves of the same heads
+    assert call(base, base + 3 * 256) == 2          # the next heads
+    assert call(base, base + 126) == 1 and call(base, base + 2 * 256 + 126) == 1
+    far = 2 * W * (S - 1)                           # the last token of the one, the first of the other
+    assert call(base, base + far + 128) == 2 and call(base, base + far + 256) == 1
+    assert call(base + far, base + 128) == 2 and call(base + far, base + 256 - 126) == 1
+    import time
+    least = 1.0
+    for _ in range(50):  # and in a time that does not grow with them (2 us; a walk over tokens 130)
+        t = time.perf_counter()
+        call(base, base + 128)
+        least = min(least, time.perf_counter() - t)
+    assert least < 40e-6, least
