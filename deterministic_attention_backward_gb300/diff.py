@@ -17,7 +17,7 @@ A training step should keep what o and o2 lose by their rounding too, two bf16 t
     o, o2, lse = diff_fwd(q, k, v, lam, causal=True, rest=rest)
     dq, dk, dv, dlam = diff_bwd(q, k, v, o, o2, do, lse, lam, causal=True, rest=rest)
 
-for the row terms D = dO . Om of dQ: off by 2.4e-3 to 3.2e-3 of its norm with rest, without it by
+for the row terms D = dO . Om of dQ: off by 2.4e-3 to 3.3e-3 of its norm with rest, without it by
 2.5e-3 for flat maps and up to 8e-3 where a few keys dominate them.
 """
 from __future__ import annotations

@@ -532,3 +532,27 @@ def test_forward_workspace_bytes(L):
     assert n == L.dash_diff_fwd_workspace_bytes(2, 300, 4, 64) == 256
     assert dash.diff_fwd_workspace_bytes(2, 300, 4, 96) == 0
     assert "diff_fwd_workspace_bytes" in dash.__all__
+
+
+@pytest.mark.gpu
+def test_rest_on_another_stream_and_captured(L):
+    q, k, v, w, do = make(2, 333, 4, 2, 64, "head-bf16")
+    (o, o2, lse, rest), want = with_rest(q, k, v, w, do, True)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    other = torch.empty_like(rest)
+    a = dash.diff_fwd(q, k, v, w, causal=True, stream=s, rest=other)
+    got = dash.diff_bwd(q, k, v, a[0], a[1], do, a[2], w, causal=True, stream=s, rest=other)
+    s.synchronize()
+    assert torch.equal(other, rest) and all(torch.equal(x, y) for x, y in zip(got, want))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        x = dash.diff_fwd(q, k, v, w, causal=True, rest=other)
+        got = dash.diff_bwd(q, k, v, x[0], x[1], do, x[2], w, causal=True, rest=other)
+    new = make(2, 333, 4, 2, 64, "head-bf16", 9)
+    (_, _, _, rest), want = with_rest(*new, True)
+    for t, u in zip((q, k, v, w, do), new):
+        t.copy_(u)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(other, rest) and all(torch.equal(x, y) for x, y in zip(got, want))
