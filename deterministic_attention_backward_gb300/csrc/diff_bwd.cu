@@ -8,11 +8,11 @@
 //   dQm = c ~dSm Km          dKm = c ~dSm^T Qm              dV = ~(P1 - lam P2)^T dO
 // Two passes form S1, S2, dP and both maps' exponentials twice (512 of then 1792 flops a pair at
 // d = 64), so that no sum leaves the chip and nothing waits for another CTA.  One pass would be
-// stationary in keys and add 64 KB of fp32 dQ partials a tile pair in global memory in a fixed order,
-// as this library's main backward does at D = 128 with the same products: that reaches 1216 TFLOP/s
-// full and 937 to 975 causal at 8192, these two 959 and 872 of the same useful flops.  So one pass is
-// the faster form as far as products and partials go; the two exponentials a pair in place of its one
-// have not been weighed.
+// stationary in keys and add 64 KB of fp32 dQ partials a tile pair in global memory in a fixed
+// order, as this library's main backward does at D = 128 with the same products: that reaches 1216
+// TFLOP/s full and 937 to 975 causal at 8192, these two 959 and 872 of the same useful flops.  So
+// one pass is the faster form as far as products and partials go; the two exponentials a pair in
+// place of its one have not been weighed.
 #include "diff.cuh"
 
 #include "dash_attn.h"
@@ -27,8 +27,8 @@ constexpr int kThreads = (kWarps + 2) * 32;  // and the TMA producer, the MMA is
 
 // -------------------------------------------------------------------- row vectors
 // One CTA per tile of a (batch, head pair); DV / 8 lanes per row.  Bound by memory: 8 sequences of
-// 2048, 32 heads of 128, 66 us for 403 MB, 6.1 TB/s.  kRest: with what the outputs lost by rounding,
-// 17 us more at 8192 tokens of 32 heads.
+// 2048, 32 heads of 128, 66 us for 403 MB, 6.1 TB/s.  kRest: with what the outputs lost by
+// rounding, 17 us more at 8192 tokens of 32 heads.
 template <int d, bool kRest>
 __global__ void __launch_bounds__(256) diff_rows_kernel(const DiffBwdParams p) {
   constexpr int DV = 2 * d, kLanes = DV / 8, kRows = 256 / kLanes;
@@ -104,12 +104,12 @@ __global__ void __launch_bounds__(256) diff_rows_kernel(const DiffBwdParams p) {
 // 32); a product's 16-key steps address them one by one.  All products have 128 columns or take
 // A from TMEM: with both operands in shared memory, 64 columns would read 6 KB for 32 cycles of
 // tensor work, more than its 128 bytes a cycle.
-// D for dS comes from the outputs, rounded or with what they lost added (rest); the exact sums over
-// j of Pm dP fall out of this pass and replace it for dK, and give dlam.  Of its norm dQ is off by,
-// at queries of spread 1, 2, 4, 8 (the more peaked the maps, the more dP - D cancels): with rest
-// 2.4e-3, 2.5e-3, 3.0e-3, 3.0e-3, from rounded outputs 2.5e-3, 2.9e-3, 4.7e-3, 7.5e-3.  The rounding
-// of dQ alone is 1.7e-3, with that of dS 2.4e-3; what is left with rest is P's in the forward.  dS as
-// two bf16 terms took a tenth off, for a kernel 1.3 times as long.
+// D for dS comes from the outputs, rounded or with what they lost added (rest); the exact sums
+// over j of Pm dP fall out of this pass and replace it for dK, and give dlam.  Of its norm dQ is
+// off by, at queries of spread 1, 2, 4, 8 (the more peaked the maps, the more dP - D cancels): with
+// rest 2.4e-3, 2.5e-3, 3.0e-3, 3.0e-3, from rounded outputs 2.5e-3, 2.9e-3, 4.7e-3, 7.5e-3.  The
+// rounding of dQ alone is 1.7e-3, with that of dS 2.4e-3; what is left with rest is P's in the
+// forward.  dS as two bf16 terms took a tenth off, for a kernel 1.3 times as long.
 // Measured at 8192 tokens, 32 head pairs of 64 with 8 KV heads: causal 633 us, full 1200 us.  A
 // block's products take 1570 cycles of the tensor core, a block 2650: the wait for a product, the
 // 64 exponentials a thread and the stores follow one another, 4 warps a scheduler cover them in

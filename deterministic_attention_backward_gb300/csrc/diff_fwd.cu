@@ -19,8 +19,8 @@
 // 1120 us, 1475 TFLOP/s (78 % of cuBLAS's bf16 rate).  A block's products take 1560 cycles of the
 // tensor core and its 32768 exponentials 1024 cycles; a block takes 2450, as each map's softmax
 // (wait, maximum, exchange, exponentials, stores) is a chain that the other map's products hide in
-// part only: tensor pipe 61 % busy.  16 sequences of 1024, full: 390 us (442 us with a CTA a tile).  With
-// the outputs' rest 661 us causal, 1220 us full: two more bf16 stores an output element.
+// part only: tensor pipe 61 % busy.  16 sequences of 1024, full: 390 us (442 us with a CTA a tile).
+// With the outputs' rest 661 us causal, 1220 us full: two more bf16 stores an output element.
 //
 // TMEM columns: S1 [0,128), S2 [128,256), O1 [256, 256+dv), O2 [256+dv, 256+2dv); P over the
 // first half of the columns that its warpgroup reads.

@@ -101,8 +101,8 @@ struct Bytes {
     return s;
   }
 };
-// One block, or `count` runs of `run` elements at a stride of `stride` elements, and so on outwards.
-// A null pointer has no bytes.
+// One block, or `count` runs of `run` elements at a stride of `stride` elements, and so on
+// outwards.  A null pointer has no bytes.
 inline Bytes bytes_of(const void *p, int size, long long run) {
   Bytes b;
   b.at = reinterpret_cast<uintptr_t>(p);

@@ -17,13 +17,13 @@
 // bits on every run.
 //
 // Measured in bf16 (of a plain copy's rate): the join of 16384 rows of 4096 forward 89 us, 6.0 TB/s
-// (89 %); backward 162 us, 5.0 TB/s (73 %).  The backward is bound by latency: its factors and column
-// sums fill the registers, so that two CTAs of 8 warps share an SM, 24 % of its warps, and they wait
-// for the ring's rows and at the two sums of a row that depend on one another (issue slots 40 % busy;
-// without its loads it takes 131 us).  Norms of 524288 heads of 128: forward 43 us, backward 68 us
-// (88 %).  Rows off the 16-byte grid: 22324 of 1503 in bf16 the join forward 60 us, backward 128 us, 1.5
-// and 2.2 times a copy's time; of 1504 columns, on the grid, 50 and 102 us (188 vectors leave a quarter
-// of the lanes of their shape idle).
+// (89 %); backward 162 us, 5.0 TB/s (73 %).  The backward is bound by latency: its factors and
+// column sums fill the registers, so that two CTAs of 8 warps share an SM, 24 % of its warps, and
+// they wait for the ring's rows and at the two sums of a row that depend on one another (issue slots
+// 40 % busy; without its loads it takes 131 us).  Norms of 524288 heads of 128: forward 43 us,
+// backward 68 us (88 %).  Rows off the 16-byte grid: 22324 of 1503 in bf16 the join forward 60 us,
+// backward 128 us, 1.5 and 2.2 times a copy's time; of 1504 columns, on the grid, 50 and 102 us (188
+// vectors leave a quarter of the lanes of their shape idle).
 #pragma once
 #include <type_traits>
 

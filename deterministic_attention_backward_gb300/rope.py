@@ -157,7 +157,8 @@ def rope_fwd(q, k=None, v=None, *, inv_freq, magnitude: float = 1.0, positions=N
     """Turn the heads of q (and k) with their tokens' positions and copy v: returns (q, k, v),
     contiguous unless ``out`` gives the tensors to write (strided ones too; an input itself is
     turned in place; beside that they share no memory with a tensor of the call).  Position of
-    token s: ``positions`` (int32 or int64, [B, S] or [S]; [T] for packed heads), or ``start`` + s."""
+    token s: ``positions`` (int32 or int64, [B, S] or [S]; [T] for packed heads), or
+    ``start`` + s."""
     return _rope((q, k, v), inv_freq, magnitude, positions, start, layout, out, stream, False)
 
 

@@ -326,9 +326,10 @@ typedef enum { DASH_ROPE_HALF = 0, DASH_ROPE_INTERLEAVED = 1 } dash_rope_layout_
 /* Pair p (x, y) becomes magnitude * (x cos a - y sin a, y cos a + x sin a) with the angle
  * a = position * inv_freq[p] (radians; device array of rot/2 doubles); backward != 0 turns by
  * -a, which is the gradient.  The angle is formed in 128-bit fixed point modulo one turn and
- * rounded to fp32 there: off by pi 2^-25 at any position.  Positions: device int32 (positions64 == 0) or int64, the
- * token's at element b * pos_stride_b + s * pos_stride_t, or NULL for start + s.  Arithmetic
- * in fp32, one rounding at the end.  1 to 3 parts of one element type; rot even, <= 1024. */
+ * rounded to fp32 there: off by pi 2^-25 at any position.  Positions: device int32
+ * (positions64 == 0) or int64, the token's at element b * pos_stride_b + s * pos_stride_t, or NULL
+ * for start + s.  Arithmetic in fp32, one rounding at the end.  1 to 3 parts of one element type;
+ * rot even, <= 1024. */
 dash_status_t dash_rope(const dash_rope_part_t *parts, int nparts, int B, int S, int rot,
                         dash_rope_layout_t layout, dash_dtype_t dtype, const double *inv_freq,
                         float magnitude, const void *positions, int positions64,
