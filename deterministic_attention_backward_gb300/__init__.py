@@ -29,7 +29,8 @@ __all__ = ["fwd", "bwd", "bwd_workspace_bytes", "fwd_workspace_bytes", "status",
            "bwd_varlen_order_log", "SCHEDULES", "lib",
            "DashError", "rope_freqs", "rope_fwd", "rope_bwd", "norm_fwd", "norm_bwd",
            "join_fwd", "join_bwd", "diff_fwd", "diff_bwd", "diff_fwd_workspace_bytes",
-           "diff_bwd_workspace_bytes"]
+           "diff_bwd_workspace_bytes", "dense_fwd", "dense_bwd", "dense_fwd_workspace_bytes",
+           "dense_bwd_workspace_bytes"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libdash_attn.so")
@@ -51,7 +52,9 @@ EXPORTS = ["dash_attn_fwd_workspace_bytes", "dash_attn_fwd", "dash_attn_bwd_work
            "dash_attn_fwd_varlen", "dash_attn_bwd_varlen", "dash_attn_bwd_varlen_order_log",
            "dash_rope", "dash_join_fwd", "dash_join_bwd", "dash_join_bwd_workspace_bytes",
            "dash_diff_fwd_workspace_bytes", "dash_diff_fwd", "dash_diff_bwd_workspace_bytes",
-           "dash_diff_bwd", "dash_diff_fwd_rest", "dash_diff_bwd_rest", "dash_diff_withhold"]
+           "dash_diff_bwd", "dash_diff_fwd_rest", "dash_diff_bwd_rest", "dash_diff_withhold",
+           "dash_dense_fwd_workspace_bytes", "dash_dense_fwd", "dash_dense_bwd_workspace_bytes",
+           "dash_dense_bwd", "dash_dense_withhold"]
 
 
 class DashError(RuntimeError):
@@ -151,6 +154,14 @@ def lib() -> ctypes.CDLL:
             getattr(L, name).restype = i
         L.dash_diff_withhold.argtypes = [i, i]
         L.dash_diff_withhold.restype = i
+        cp = ctypes.c_char_p  # a packed argument structure
+        for name in ("dash_dense_fwd", "dash_dense_bwd"):
+            getattr(L, name + "_workspace_bytes").argtypes = [cp]
+            getattr(L, name + "_workspace_bytes").restype = sz
+            getattr(L, name).argtypes = [cp, vp, sz, vp]
+            getattr(L, name).restype = i
+        L.dash_dense_withhold.argtypes = [i]
+        L.dash_dense_withhold.restype = i
         _lib = L
         return L
 
@@ -465,7 +476,8 @@ def bwd_varlen_order_log(q, k, v, o, do, lse, cu_seqlens, causal: bool = False,
 _MODULES = {"rope_freqs": "rope", "rope_fwd": "rope", "rope_bwd": "rope", "norm_fwd": "norms",
             "norm_bwd": "norms", "join_fwd": "norms", "join_bwd": "norms", "diff_fwd": "diff",
             "diff_bwd": "diff", "diff_fwd_workspace_bytes": "diff",
-            "diff_bwd_workspace_bytes": "diff"}
+            "diff_bwd_workspace_bytes": "diff", "dense_fwd": "dense", "dense_bwd": "dense",
+            "dense_fwd_workspace_bytes": "dense", "dense_bwd_workspace_bytes": "dense"}
 
 
 def __getattr__(name):

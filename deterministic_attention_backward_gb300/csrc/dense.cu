@@ -1,0 +1,367 @@
+// dense.cu -- the extern "C" entries of products with their epilogue: argument checks, the choice
+// of tiles and splits, workspace carving, tensor maps, launches.
+#include "dense.cuh"
+
+#include "dash_attn.h"
+#include "host.cuh"
+
+namespace dash {
+namespace {
+
+std::atomic<int> g_dense_withhold{-1};
+
+bool aligned2(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
+long long up(long long n, long long to) { return (n + to - 1) / to * to; }
+int ceil_div(long long n, long long d) { return (int)((n + d - 1) / d); }
+
+// An operand as rows of `cols` contiguous elements; `pad`: copied to an aligned place first.
+struct Rows {
+  const void *at = nullptr;
+  long long stride = 0;
+  int rows = 0, cols = 0;
+  bool pad = false;
+  Rows() = default;
+  Rows(const void *at, long long stride, int rows, int cols)
+      : at(at), stride(rows > 1 ? stride : up(cols, 8)), rows(rows), cols(cols) {
+    pad = at && (!aligned16(at) || this->stride % 8 || this->stride < cols);
+  }
+  size_t bytes() const { return pad ? align256((size_t)rows * up(cols, 8) * 2) : 0; }
+  Bytes lies() const { return along(bytes_of(at, 2, cols), 2, stride, rows); }
+};
+
+// A tensor map over rows: boxes of 64 contiguous elements x `box` rows.
+bool make_rows_map(CUtensorMap *m, const Rows &r, int box, bool f16) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)r.cols, (cuuint64_t)r.rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)r.stride * 2};
+  const cuuint32_t boxes[2] = {(cuuint32_t)kDenseK, (cuuint32_t)box};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+             const_cast<void *>(r.at), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// One product: its sizes, and the tiles and splits chosen for them.
+struct Product {
+  int M, N, K, parts, outs;
+  bool gated;
+  int bn, splits;
+  int cols() const { return gated ? bn / 2 : bn; }
+  int mt() const { return ceil_div(M, kDenseM); }
+  int nt() const { return ceil_div(N, cols()); }
+  int nk() const { return ceil_div(K, kDenseK); }
+  size_t part_bytes() const {
+    return splits > 1 ? align256((size_t)splits * outs * M * nt() * bn * 4) : 0;
+  }
+};
+
+// The choice follows from the sizes alone, as the order of the sums does (the pairs of SMs are those
+// of a GB300, not of the GPU that runs).  Time is counted in blocks of 64 of a 256-column tile
+// (0.27 us): a block of 128 columns costs 0.7, a tile 3 beside its blocks, a second kernel 8 and the
+// partial sums their way to memory and back.
+constexpr int kPairs = 76, kMaxSplits = 32;
+Product plan(int M, int N, int K, int parts, int outs, bool gated) {
+  Product best{M, N, K, parts, outs, gated, 256, 1};
+  double least = 0;
+  for (int bn = 256; bn >= 128; bn -= 128) {
+    Product p{M, N, K, parts, outs, gated, bn, 1};
+    const long long tiles = (long long)p.mt() * p.nt() * outs;
+    const int blocks = p.nk() * parts;
+    for (int s = 1; s <= kMaxSplits && s <= blocks; ++s) {
+      if (s > 1 && tiles * s > 4 * kPairs) break;
+      const int per = ceil_div(blocks, s);
+      if (ceil_div(blocks, per) != s) continue;  // no split is empty
+      double t = (double)((tiles * s + kPairs - 1) / kPairs) * (per * (bn == 256 ? 1.0 : 0.7) + 3);
+      if (s > 1) t += 8 + 8.0 * s * outs * M * p.nt() * bn / 1.8e6;
+      if (least == 0 || t < 0.97 * least) {
+        least = t;
+        best = p;
+        best.splits = s;
+      }
+    }
+  }
+  return best;
+}
+
+bool sizes_ok(const Product &p) {
+  return (long long)p.mt() * p.nt() * p.outs * p.splits < (1LL << 30) && p.M < (1 << 30) &&
+         p.N < (1 << 30) && p.K < (1 << 30);
+}
+
+struct Arena {
+  char *base;
+  size_t off = kStatusBytes;
+  explicit Arena(void *ws) : base(static_cast<char *>(ws)) {}
+  void *take(size_t bytes) {
+    void *p = bytes ? base + off : nullptr;
+    off += align256(bytes);
+    return p;
+  }
+};
+
+// Copies an operand that the copy engine cannot read where it lies.
+bool place(Rows &r, Arena &arena, cudaStream_t s) {
+  if (!r.pad) return true;
+  const long long stride = up(r.cols, 8);
+  void *to = arena.take(r.bytes());
+  if (launch_dense_copy(r.at, r.stride, to, stride, r.rows, r.cols, s) != cudaSuccess) return false;
+  r = Rows(to, stride, r.rows, r.cols);
+  return true;
+}
+
+// Launches a product of rows a[0..1], b[0..1] (the second ones where `parts` or `outs` or a gate
+// ask for them, otherwise empty).
+dash_status_t launch(const Product &p, const Rows (&a)[2], const Rows (&b)[2], bool a_mn, bool b_mn,
+                     bool a_out, bool b_out, const DenseEpilogue &e, void *y1, long long y1s,
+                     float *part, void *workspace, bool f16, int sms, cudaStream_t s) {
+  CUtensorMap ta[2], tb[2];
+  for (int i = 0; i < 2; ++i)
+    if (!make_rows_map(&ta[i], a[i].at ? a[i] : a[0], a_mn ? 64 : 128, f16) ||
+        !make_rows_map(&tb[i], b[i].at ? b[i] : b[0], b_mn ? 64 : p.bn / 2, f16))
+      return DASH_ERR_CUDA;
+  DenseParams d{};
+  d.e = e;
+  d.y1 = y1, d.y1s = y1s;
+  d.part = part;
+  d.status = static_cast<uint32_t *>(workspace);
+  d.wait_ns = g_wait_ns.load();
+  d.M = p.M, d.N = p.N;
+  d.mt = p.mt(), d.nt = p.nt(), d.bn = p.bn;
+  d.part_cols = (long long)d.nt * d.bn;
+  d.nk = p.nk(), d.parts = p.parts, d.outs = p.outs;
+  d.splits = p.splits, d.per = ceil_div(d.nk * d.parts, p.splits);
+  d.a_mn = a_mn, d.b_mn = b_mn, d.a_out = a_out, d.b_out = b_out;
+  d.withhold = g_dense_withhold.load();
+  return launch_dense(f16, ta, tb, d, sms, s) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+}
+
+bool vec_rows(const void *p, long long stride) { return !p || (aligned16(p) && stride % 8 == 0); }
+
+// ------------------------------------------------------------------ forward
+dash_status_t check_fwd(const dash_dense_fwd_t *a, Product &p, Rows &x, Rows (&w)[2]) {
+  if (!a || !a->x || !a->w || !a->y || a->M <= 0 || a->K <= 0 || a->N <= 0) return DASH_ERR_INVALID;
+  if (a->order != DASH_DENSE_KN && a->order != DASH_DENSE_NK) return DASH_ERR_INVALID;
+  if (a->act < DASH_ACT_NONE || a->act > DASH_ACT_SILU) return DASH_ERR_INVALID;
+  if (a->dtype != DASH_BF16 && a->dtype != DASH_FP16)
+    return a->dtype == DASH_FP32 ? DASH_ERR_UNSUPPORTED : DASH_ERR_INVALID;
+  const void *all[] = {a->x, a->w, a->w_gate, a->bias, a->bias_gate, a->residual, a->y, a->z,
+                       a->gate};
+  for (const void *t : all)
+    if (!aligned2(t)) return DASH_ERR_INVALID;
+  if ((a->bias_gate || a->gate) && !a->w_gate) return DASH_ERR_INVALID;
+  if (a->M > 1 && a->y_stride < a->N) return DASH_ERR_INVALID;
+  const bool kn = a->order == DASH_DENSE_KN;
+  p = plan(a->M, a->N, a->K, 1, 1, a->w_gate != nullptr);
+  if (!sizes_ok(p)) return DASH_ERR_UNSUPPORTED;
+  x = Rows(a->x, a->x_stride, a->M, a->K);
+  w[0] = Rows(a->w, a->w_stride, kn ? a->K : a->N, kn ? a->N : a->K);
+  w[1] = Rows(a->w_gate, a->w_gate_stride, w[0].rows, w[0].cols);
+  return DASH_OK;
+}
+size_t need_fwd(const Product &p, const Rows &x, const Rows (&w)[2]) {
+  return kStatusBytes + x.bytes() + w[0].bytes() + w[1].bytes() + p.part_bytes();
+}
+
+// ------------------------------------------------------------------ backward
+struct Bwd {
+  Product dx, dw;
+  Rows dy, x, w[2];
+  bool grads, pad_dy;  // dz (and dgate) are formed; dy is copied
+  int chunks, chunk;
+  size_t dz_bytes, sum_bytes, part_bytes, need;
+};
+dash_status_t check_bwd(const dash_dense_bwd_t *a, Bwd &b) {
+  if (!a || !a->dy || a->M < 0 || a->K <= 0 || a->N <= 0) return DASH_ERR_INVALID;
+  if (a->order != DASH_DENSE_KN && a->order != DASH_DENSE_NK) return DASH_ERR_INVALID;
+  if (a->act < DASH_ACT_NONE || a->act > DASH_ACT_SILU) return DASH_ERR_INVALID;
+  if (a->dtype != DASH_BF16 && a->dtype != DASH_FP16)
+    return a->dtype == DASH_FP32 ? DASH_ERR_UNSUPPORTED : DASH_ERR_INVALID;
+  const void *all[] = {a->dy, a->x, a->w, a->w_gate, a->z, a->gate, a->dx, a->dw, a->dw_gate,
+                       a->dbias, a->dbias_gate};
+  for (const void *t : all)
+    if (!aligned2(t)) return DASH_ERR_INVALID;
+  const bool kn = a->order == DASH_DENSE_KN, gated = a->gate != nullptr;
+  b.grads = a->act != DASH_ACT_NONE || gated;
+  if (b.grads && !a->z) return DASH_ERR_INVALID;
+  if ((a->dx && !a->w) || (a->dw && !a->x)) return DASH_ERR_INVALID;
+  if (gated ? (a->dx && !a->w_gate) || !a->dw != !a->dw_gate : a->dw_gate || a->dbias_gate)
+    return DASH_ERR_INVALID;
+  const int wr = kn ? a->K : a->N, wc = kn ? a->N : a->K;
+  if ((a->dx && a->M > 1 && a->dx_stride < a->K) ||
+      (a->dw && wr > 1 && (a->dw_stride < wc || (gated && a->dw_gate_stride < wc))))
+    return DASH_ERR_INVALID;
+  b.dy = Rows(a->dy, a->dy_stride, a->M, a->N);
+  b.x = Rows(a->dw ? a->x : nullptr, a->x_stride, a->M, a->K);
+  b.w[0] = Rows(a->dx ? a->w : nullptr, a->w_stride, wr, wc);
+  b.w[1] = Rows(a->dx && gated ? a->w_gate : nullptr, a->w_gate_stride, wr, wc);
+  const int M = a->M ? a->M : 1;
+  b.dx = plan(M, a->K, a->N, gated ? 2 : 1, 1, false);
+  b.dw = kn ? plan(a->K, a->N, M, 1, gated ? 2 : 1, false)
+            : plan(a->N, a->K, M, 1, gated ? 2 : 1, false);
+  if (!sizes_ok(b.dx) || !sizes_ok(b.dw)) return DASH_ERR_UNSUPPORTED;
+  // rows of a chunk: enough chunks for every SM, 64 rows at least
+  const int strips = ceil_div(a->N, 256);
+  b.chunk = ceil_div(M, ceil_div(152 * 8, strips));
+  b.chunk = (int)up(b.chunk < 64 ? 64 : b.chunk, 8);
+  b.chunks = ceil_div(M, b.chunk);
+  b.dz_bytes = b.grads && (a->dx || a->dw) ? align256((size_t)M * up(a->N, 8) * 2) : 0;
+  b.sum_bytes = align256((size_t)b.chunks * a->N * 4);
+  b.part_bytes = 0;
+  if (a->dx) b.part_bytes = b.dx.part_bytes();
+  if (a->dw && b.dw.part_bytes() > b.part_bytes) b.part_bytes = b.dw.part_bytes();
+  b.pad_dy = !b.grads && (a->dx || a->dw) && b.dy.pad;
+  b.need = kStatusBytes + (gated ? 2 : 1) * b.dz_bytes + (a->dbias ? b.sum_bytes : 0) +
+           (a->dbias_gate ? b.sum_bytes : 0) + b.part_bytes + (b.pad_dy ? b.dy.bytes() : 0) +
+           b.x.bytes() + b.w[0].bytes() + b.w[1].bytes();
+  return DASH_OK;
+}
+
+}  // namespace
+}  // namespace dash
+
+extern "C" {
+
+dash_status_t dash_dense_withhold(int block) {
+  dash::g_dense_withhold.store(block < 0 ? -1 : block);
+  return DASH_OK;
+}
+
+size_t dash_dense_fwd_workspace_bytes(const dash_dense_fwd_t *args) {
+  dash::Product p;
+  dash::Rows x, w[2];
+  return dash::check_fwd(args, p, x, w) == DASH_OK ? dash::need_fwd(p, x, w) : 0;
+}
+
+dash_status_t dash_dense_fwd(const dash_dense_fwd_t *a, void *workspace, size_t workspace_bytes,
+                             dash_stream_t stream) {
+  using namespace dash;
+  Product p;
+  Rows xs, w[2];
+  dash_status_t st = check_fwd(a, p, xs, w);
+  if (st != DASH_OK) return st;
+  const size_t need = need_fwd(p, xs, w);
+  if (!workspace || !aligned16(workspace) || workspace_bytes < need) return DASH_ERR_WORKSPACE;
+  const Rows y(a->y, a->y_stride, a->M, a->N), res(a->residual, a->residual_stride, a->M, a->N);
+  const long long kept = (long long)a->M * a->N;
+  const Bytes outs[] = {y.lies(), bytes_of(a->z, 2, kept), bytes_of(a->gate, 2, kept),
+                        bytes_of(workspace, 1, (long long)need)};
+  const Bytes reads[] = {xs.lies(), w[0].lies(), w[1].lies(), bytes_of(a->bias, 2, a->N),
+                         bytes_of(a->bias_gate, 2, a->N)};
+  if (!apart(outs, reads)) return DASH_ERR_INVALID;
+  const bool in_place = a->y == a->residual && (a->M == 1 || a->y_stride == a->residual_stride);
+  for (int i = in_place ? 1 : 0; i < 4; ++i)
+    if (share(outs[i], res.lies())) return DASH_ERR_INVALID;
+  DevInfo dev;
+  if ((st = device_info(&dev)) != DASH_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (cudaMemsetAsync(workspace, 0, kStatusBytes, s) != cudaSuccess) return DASH_ERR_CUDA;
+  Arena arena(workspace);
+  if (!place(xs, arena, s) || !place(w[0], arena, s) || !place(w[1], arena, s))
+    return DASH_ERR_CUDA;
+  float *part = static_cast<float *>(arena.take(p.part_bytes()));
+  DenseEpilogue e{};
+  e.y = a->y, e.z = a->z, e.g = a->gate;
+  e.bias = a->bias, e.bias_gate = a->bias_gate, e.residual = a->residual;
+  e.ys = a->y_stride, e.zs = e.gs = a->N, e.rs = a->residual_stride;
+  e.act = a->act, e.gated = p.gated;
+  e.vec = vec_rows(e.y, e.ys) && vec_rows(e.z, a->N) && vec_rows(e.g, a->N) &&
+          vec_rows(e.residual, e.rs) && vec_rows(e.bias, 0) && vec_rows(e.bias_gate, 0);
+  const Rows x[2] = {xs, Rows()};
+  return launch(p, x, w, false, a->order == DASH_DENSE_KN, false, false, e, nullptr, 0, part,
+                workspace, a->dtype == DASH_FP16, dev.sms, s);
+}
+
+size_t dash_dense_bwd_workspace_bytes(const dash_dense_bwd_t *args) {
+  dash::Bwd b;
+  return dash::check_bwd(args, b) == DASH_OK ? b.need : 0;
+}
+
+dash_status_t dash_dense_bwd(const dash_dense_bwd_t *a, void *workspace, size_t workspace_bytes,
+                             dash_stream_t stream) {
+  using namespace dash;
+  Bwd b;
+  dash_status_t st = check_bwd(a, b);
+  if (st != DASH_OK) return st;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < b.need) return DASH_ERR_WORKSPACE;
+  const bool kn = a->order == DASH_DENSE_KN, gated = a->gate != nullptr,
+             f16 = a->dtype == DASH_FP16;
+  const int wr = kn ? a->K : a->N, wc = kn ? a->N : a->K;
+  const long long kept = (long long)a->M * a->N;
+  const Rows dw(a->dw, a->dw_stride, wr, wc), dwg(a->dw_gate, a->dw_gate_stride, wr, wc);
+  const Bytes outs[] = {Rows(a->dx, a->dx_stride, a->M, a->K).lies(), dw.lies(), dwg.lies(),
+                        bytes_of(a->dbias, 2, a->N), bytes_of(a->dbias_gate, 2, a->N),
+                        bytes_of(workspace, 1, (long long)b.need)};
+  const Bytes reads[] = {b.dy.lies(), Rows(a->x, a->x_stride, a->M, a->K).lies(),
+                         Rows(a->w, a->w_stride, wr, wc).lies(),
+                         Rows(a->w_gate, a->w_gate_stride, wr, wc).lies(),
+                         bytes_of(a->z, 2, kept), bytes_of(a->gate, 2, kept)};
+  if (!apart(outs, reads)) return DASH_ERR_INVALID;
+  DevInfo dev;
+  if ((st = device_info(&dev)) != DASH_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (a->M == 0) {
+    const Rows *const w[2] = {&dw, &dwg};
+    for (const Rows *r : w)
+      if (r->at && cudaMemset2DAsync(const_cast<void *>(r->at), r->stride * 2, 0, (size_t)wc * 2,
+                                     wr, s) != cudaSuccess)
+        return DASH_ERR_CUDA;
+    for (void *d : {a->dbias, a->dbias_gate})
+      if (d && cudaMemsetAsync(d, 0, (size_t)a->N * 2, s) != cudaSuccess) return DASH_ERR_CUDA;
+    return cudaMemsetAsync(workspace, 0, kStatusBytes, s) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+  }
+  Arena arena(workspace);
+  Rows dz[2] = {b.dy, Rows()};
+  void *dz_at = arena.take(b.dz_bytes), *dg_at = gated ? arena.take(b.dz_bytes) : nullptr;
+  float *sum = static_cast<float *>(arena.take(a->dbias ? b.sum_bytes : 0));
+  float *sum_gate = static_cast<float *>(arena.take(a->dbias_gate ? b.sum_bytes : 0));
+  float *part = static_cast<float *>(arena.take(b.part_bytes));
+  if (b.grads || a->dbias) {
+    DenseGradParams g{};
+    g.dy = a->dy;
+    if (b.grads) g.z = a->z, g.g = a->gate;
+    g.dz = dz_at, g.dg = dg_at;
+    g.part = sum, g.part_gate = sum_gate;
+    g.status = static_cast<uint32_t *>(workspace);
+    g.dys = b.dy.stride, g.zs = g.gs = a->N, g.ds = up(a->N, 8);
+    g.M = a->M, g.N = a->N, g.act = a->act, g.chunk = b.chunk;
+    g.vec = a->N % 8 == 0 && vec_rows(a->dy, b.dy.stride) && vec_rows(a->z, a->N) &&
+            vec_rows(a->gate, a->N);
+    if (launch_dense_grad(f16, g, b.chunks, s) != cudaSuccess) return DASH_ERR_CUDA;
+    if ((sum || sum_gate) && launch_dense_sums(f16, sum, sum_gate, a->dbias, a->dbias_gate,
+                                               b.chunks, a->N, s) != cudaSuccess)
+      return DASH_ERR_CUDA;
+    if (b.grads) {
+      dz[0] = Rows(dz_at, g.ds, a->M, a->N);
+      dz[1] = Rows(dg_at, g.ds, a->M, a->N);
+    }
+  } else if (cudaMemsetAsync(workspace, 0, kStatusBytes, s) != cudaSuccess) {
+    return DASH_ERR_CUDA;
+  }
+  if (!a->dx && !a->dw) return DASH_OK;
+  if (!place(dz[0], arena, s) || !place(b.x, arena, s) || !place(b.w[0], arena, s) ||
+      !place(b.w[1], arena, s))
+    return DASH_ERR_CUDA;
+  if (a->dx) {
+    DenseEpilogue e{};
+    e.y = a->dx, e.ys = a->dx_stride;
+    e.vec = vec_rows(e.y, e.ys);
+    st = launch(b.dx, dz, b.w, false, !kn, false, false, e, nullptr, 0, part, workspace, f16,
+                dev.sms, s);
+    if (st != DASH_OK) return st;
+  }
+  if (a->dw) {
+    DenseEpilogue e{};
+    e.y = a->dw, e.ys = a->dw_stride;
+    e.vec = vec_rows(e.y, e.ys) && vec_rows(a->dw_gate, a->dw_gate_stride);
+    const Rows x[2] = {b.x, Rows()};
+    st = kn ? launch(b.dw, x, dz, true, true, false, gated, e, a->dw_gate, a->dw_gate_stride, part,
+                     workspace, f16, dev.sms, s)
+            : launch(b.dw, dz, x, true, true, gated, false, e, a->dw_gate, a->dw_gate_stride, part,
+                     workspace, f16, dev.sms, s);
+  }
+  return st;
+}
+
+}  // extern "C"

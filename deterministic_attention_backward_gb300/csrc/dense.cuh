@@ -1,0 +1,65 @@
+// dense.cuh -- products with their epilogue: parameters and launch interface of the kernels.
+//
+//   C[m, n] = sum over parts p, sum over k:  A_p[m, k] B_p[n, k]
+// with either dimension of an operand contiguous.  Forward, dx and dw are this one product with
+// other operands:
+//   forward  A = x, B = w^T; gated: B tiles of w and of w_gate side by side in one accumulator
+//   dx       A = dz (and dgate as second part), B = w (and w_gate)
+//   dw       A = x^T, B = dz^T (and dgate^T for a second output); w stored [N, K]: A and B change
+//            places
+#pragma once
+#include "common.cuh"
+
+namespace dash {
+
+constexpr int kDenseM = 256;   // rows of a tile, of a pair of CTAs
+constexpr int kDenseK = 64;    // contraction elements of a stage
+
+// What follows the product: y = residual + act(z) * g, with z = product + bias (and g likewise,
+// gated); z and g kept where asked for.
+struct DenseEpilogue {
+  void *y, *z, *g;
+  const void *bias, *bias_gate, *residual;
+  long long ys, zs, gs, rs;  // row strides in elements
+  int act, gated;
+  int vec;                   // all of them by 16-byte vectors
+};
+struct DenseParams {
+  DenseEpilogue e;
+  void *y1;                  // the second output (outs == 2)
+  long long y1s;
+  float *part;               // splits > 1: [splits][outs][M][cols] fp32 sums
+  uint32_t *status;
+  unsigned long long wait_ns;
+  long long part_cols;       // nt * bn
+  int M, N;
+  int mt, nt, bn;            // tiles; bn columns of a tile's accumulator (gated: half z, half g)
+  int nk, parts, outs;       // blocks of kDenseK of a part
+  int splits, per;           // splits of the parts' blocks, blocks of a split
+  int a_mn, b_mn;            // the contiguous dimension is M (N), not the contraction
+  int a_out, b_out;          // the second output takes the second A (B)
+  int withhold;              // block at which a CTA's loads end, else -1
+};
+
+// dz = dy g act'(z), dgate = dy act(z) and their sums over rows.
+struct DenseGradParams {
+  const void *dy, *z, *g;    // z null: dz = dy (and is not written); g null: not gated
+  void *dz, *dg;             // null where only the sums are wanted
+  float *part, *part_gate;   // [chunks][N]; null where the sums are not wanted
+  uint32_t *status;          // cleared
+  long long dys, zs, gs, ds;
+  int M, N, act, chunk;      // rows of a chunk
+  int vec;
+};
+
+cudaError_t launch_dense(bool f16, const CUtensorMap (&ta)[2], const CUtensorMap (&tb)[2],
+                         const DenseParams &p, int sms, cudaStream_t s);
+cudaError_t launch_dense_grad(bool f16, const DenseGradParams &p, int chunks, cudaStream_t s);
+// out[n] = sum over chunks, in order (gate: a second row of sums and its output)
+cudaError_t launch_dense_sums(bool f16, const float *part, const float *part_gate, void *out,
+                              void *out_gate, int chunks, int N, cudaStream_t s);
+// rows of cols elements of two bytes to rows at another stride, cleared up to there
+cudaError_t launch_dense_copy(const void *in, long long is, void *out, long long os,
+                              long long rows, int cols, cudaStream_t s);
+
+}  // namespace dash

@@ -427,6 +427,56 @@ dash_status_t dash_diff_bwd_rest(const void *q, const void *k, const void *v, co
  * (128 keys; 64 queries in dK/dV's), so that the waits for it run out. */
 dash_status_t dash_diff_withhold(int kernel, int block);
 
+/* Matrix product with its epilogue, in bf16 or fp16 with fp32 sums:
+ *   z = x w + bias      g = x w_gate + bias_gate      y = residual + act(z) g
+ * without w_gate y = residual + act(z); bias, bias_gate, residual may be NULL.  x [M, K] and y,
+ * residual [M, N] are rows at a stride (in elements); w and w_gate are [K, N] rows (DASH_DENSE_KN)
+ * or [N, K] rows (DASH_DENSE_NK); biases [N] contiguous, of the rows' type.  z and gate, where not
+ * NULL, receive z and g as contiguous [M, N] rows for the backward.  y may be the residual itself
+ * (at its stride); beside that no output shares memory with another tensor of the call.  Sums run
+ * in an order that the sizes fix, one rounding at the end.  Operands that do not begin on 16 bytes,
+ * or whose stride is no multiple of that, are copied into the workspace first.
+ * The workspace holds a status block (dash_attn_status) and serves one call at a time.  Its size
+ * follows from the same arguments as the call (pointers' alignment and strides among them); 0 where
+ * the call would be refused. */
+typedef enum {
+  DASH_ACT_NONE = 0,
+  DASH_ACT_RELU = 1,
+  DASH_ACT_GELU = 2,      /* z/2 (1 + erf(z / sqrt 2)) */
+  DASH_ACT_GELU_TANH = 3, /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+  DASH_ACT_SILU = 4
+} dash_act_t;
+typedef enum { DASH_DENSE_KN = 0, DASH_DENSE_NK = 1 } dash_dense_order_t;
+typedef struct {
+  const void *x, *w, *w_gate, *bias, *bias_gate, *residual;
+  void *y, *z, *gate;
+  long long x_stride, w_stride, w_gate_stride, residual_stride, y_stride;
+  int M, K, N, order, act, dtype;
+} dash_dense_fwd_t;
+size_t dash_dense_fwd_workspace_bytes(const dash_dense_fwd_t *args);
+dash_status_t dash_dense_fwd(const dash_dense_fwd_t *args, void *workspace, size_t workspace_bytes,
+                             dash_stream_t stream);
+/* Gradient: from dy [M, N], x, the weights and what the forward kept (z where act is not NONE or
+ * there is a gate, gate with it; both as the forward rounded them)
+ *   dz = dy g act'(z)   dgate = dy act(z)
+ *   dx = dz w^T + dgate w_gate^T   dw = x^T dz   dw_gate = x^T dgate   dbias, dbias_gate = sums
+ * each where its pointer is not NULL (dw and dw_gate in the weights' order).  dz and dgate are
+ * rounded to the rows' type for the tensor core, the biases' gradients are sums of the unrounded
+ * ones.  The residual's gradient is dy.  Deterministic; M = 0 clears the weights' gradients. */
+typedef struct {
+  const void *dy, *x, *w, *w_gate, *z, *gate;
+  void *dx, *dw, *dw_gate, *dbias, *dbias_gate;
+  long long dy_stride, x_stride, w_stride, w_gate_stride, dx_stride, dw_stride, dw_gate_stride;
+  int M, K, N, order, act, dtype;
+} dash_dense_bwd_t;
+size_t dash_dense_bwd_workspace_bytes(const dash_dense_bwd_t *args);
+dash_status_t dash_dense_bwd(const dash_dense_bwd_t *args, void *workspace, size_t workspace_bytes,
+                             dash_stream_t stream);
+/* For tests of failure detection, process-wide: from the next call on the loads of every CTA of the
+ * product kernel end before its block `block` of 64 contraction elements (-1: of none any more), so
+ * that the waits for it run out. */
+dash_status_t dash_dense_withhold(int block);
+
 /* Human-readable name of a status code (static storage). */
 const char *dash_status_string(dash_status_t status);
 

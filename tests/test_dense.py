@@ -1,0 +1,438 @@
+"""Products with their epilogue against the definition in 64 bits.
+
+Tolerances.  Products of 16-bit values are exact in fp32.  The tensor core adds 16 of them to an
+accumulator at a time; an addition that aligns its terms to the largest and cuts them off errs by less
+than 2^-22 of the sum of their magnitudes, over K / 16 steps and the additions of splits and parts
+behind them: (K / 16 + 40) 2^-22 S with S = sum |x| |w|.  The activations' slopes are below 1.13 and
+their functions good to 2^-20 of |z| + 1.  A rounding to the type is off by eps / 2 of the value.  The
+backward rounds dz (and dgate) once before its products, which enters as eps / 2 sum |dz| |w|.
+
+That bound holds for every element, but roundings rarely all point one way: in the norm over a tensor a
+rounding counts as its root mean square, eps / 2 / sqrt 3 of the values' norm, so dx and dw, with two
+roundings one behind the other, are held to twice that, and the sums' own error, as well."""
+import math
+
+import pytest
+import torch
+
+import deterministic_attention_backward_gb300 as dash
+from deterministic_attention_backward_gb300 import _build
+from deterministic_attention_backward_gb300.dense import _BWD, _FWD
+
+BF, HF = torch.bfloat16, torch.float16
+gpu = pytest.mark.gpu
+ACTS = ["none", "relu", "gelu", "gelu_tanh", "silu"]
+
+
+def act_of(z, act):
+    """act(z) and its derivative."""
+    if act == "none":
+        return z, torch.ones_like(z)
+    if act == "relu":
+        return z.clamp(min=0), (z > 0).to(z.dtype)
+    if act == "silu":
+        s = torch.sigmoid(z)
+        return z * s, s + z * s * (1 - s)
+    if act == "gelu":
+        c = 0.5 * (1 + torch.erf(z / math.sqrt(2)))
+        return z * c, c + z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    u = math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)
+    t = torch.tanh(u)
+    return z * (1 + t) / 2, (1 + t) / 2 + z / 2 * (1 - t * t) * math.sqrt(2 / math.pi) * (
+        1 + 3 * 0.044715 * z * z)
+
+
+def step(t):
+    return torch.finfo(t).eps / 2
+
+
+def rounded(ref, tol, dtype):
+    return tol + step(dtype) * (ref.abs() + tol) + torch.finfo(dtype).smallest_normal * \
+        torch.finfo(dtype).eps
+
+
+def sums(K):
+    return (K / 16 + 40) * 2.0 ** -22
+
+
+def inside(got, ref, tol, name=""):
+    err = (got.double() - ref).abs()
+    assert (err <= tol).all(), (name, (err - tol).max().item(), err.max().item())
+
+
+@pytest.fixture(scope="module")
+def L():
+    _build.build()
+    return dash.lib()
+
+
+def make(shape, dtype, seed, by=1.0, device="cuda"):
+    g = torch.Generator(device=device).manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device=device) * by).to(dtype)
+
+
+def weight(K, N, order, dtype, seed):
+    w = make((K, N), dtype, seed, K ** -0.5)
+    return w if order == "kn" else w.t().contiguous().t()
+
+
+def check_forward(x, w, y, kept, act, bias=None, w_gate=None, bias_gate=None, residual=None):
+    dt, K = x.dtype, x.shape[-1]
+    X = x.double()
+
+    def product(w, b):
+        z = X @ w.double()
+        tol = sums(K) * (X.abs() @ w.double().abs())
+        if b is not None:
+            z = z + b.double()
+            tol = tol + 2.0 ** -23 * z.abs()
+        return z, tol
+    z, tz = product(w, bias)
+    a, _ = act_of(z, act)
+    ta = 1.13 * tz + 2.0 ** -20 * (z.abs() + 1) * (act != "none")
+    if w_gate is not None:
+        g, tg = product(w_gate, bias_gate)
+        ta = ta * (g.abs() + tg) + a.abs() * tg + 2.0 ** -23 * (a * g).abs()
+        a = a * g
+    if residual is not None:
+        a = a + residual.double()
+        ta = ta + 2.0 ** -23 * a.abs()
+    inside(y, a, rounded(a, ta, dt), "y")
+    if kept is not None:
+        inside(kept[0] if w_gate is not None else kept, z, rounded(z, tz, dt), "z")
+        if w_gate is not None:
+            inside(kept[1], g, rounded(g, tg, dt), "g")
+
+
+def check_backward(dy, x, w, kept, grads, act, bias=None, w_gate=None, bias_gate=None):
+    dt, (K, N), M = x.dtype, w.shape, x.numel() // x.shape[-1]
+    D, X, W = dy.double().reshape(-1, N), x.double().reshape(-1, K), w.double()
+    dx, dw, db, dwg, dbg = grads
+    e = step(dt)
+    parts = []  # (dz, what fp32 loses of it, weights, gradients)
+    if act == "none" and w_gate is None:
+        parts.append((D, torch.zeros_like(D), W, dw, db))
+        e = 0.0
+    else:
+        z = (kept[0] if w_gate is not None else kept).double().reshape(-1, N)
+        a, slope = act_of(z, act)
+        lost = 2.0 ** -19 * D.abs() * (z.abs() + 1) * (act != "none")
+        if w_gate is None:
+            parts.append((D * slope, lost, W, dw, db))
+        else:
+            g = kept[1].double().reshape(-1, N)
+            parts.append((D * slope * g, lost * g.abs() + 2.0 ** -22 * (D * slope * g).abs(), W, dw,
+                          db))
+            parts.append((D * a, lost + 2.0 ** -23 * (D * a).abs(), w_gate.double(), dwg, dbg))
+    tiny = torch.finfo(dt).smallest_normal * torch.finfo(dt).eps
+    ref = sum(dz @ w.t() for dz, _, w, _, _ in parts)
+    size = sum(dz.abs() @ w.abs().t() for dz, _, w, _, _ in parts)
+    loss = sum((t + (tiny if e else 0)) @ w.abs().t() for _, t, w, _, _ in parts)
+
+    def hold(got, ref, size, loss, n, name):
+        tol = e * size * (1 + 2.0 ** -8) + loss * (1 + e) + sums(n) * size
+        inside(got, ref, rounded(ref, tol, dt), name)
+        rms = 2 * step(dt) / 3 ** 0.5 * ref.norm() + (sums(n) * size + loss).norm() + \
+            tiny * ref.numel() ** 0.5
+        assert (got.double() - ref).norm() <= rms or ref.numel() < 1000, name
+
+    if dx is not None:
+        hold(dx.reshape(-1, K), ref, size, loss, N * len(parts), "dx")
+    for i, (dz, t, _, dw, db) in enumerate(parts):
+        if dw is not None:
+            lost = X.abs().t() @ (t + (tiny if e else 0))
+            hold(dw, X.t() @ dz, X.abs().t() @ dz.abs(), lost, M, f"dw{i}")
+        if db is not None:
+            # fp32 sums of M terms in any order: M 2^-24 of the terms' magnitudes at most
+            r = dz.sum(0)
+            inside(db, r, rounded(r, M * 2.0 ** -23 * dz.abs().sum(0) + t.sum(0), dt), f"db{i}")
+
+
+def test_reference_slopes():
+    """The derivatives above against central differences."""
+    z = torch.linspace(-6, 6, 1201, dtype=torch.float64) + 1e-3
+    for act in ACTS:
+        up, down = act_of(z + 1e-5, act)[0], act_of(z - 1e-5, act)[0]
+        assert ((up - down) / 2e-5 - act_of(z, act)[1]).abs().max() < 1e-8, act
+
+
+def test_abi_refusals(L):
+    at = 1 << 20  # never dereferenced: every call below is refused first
+
+    def fwd(x=at, w=2 * at, wg=0, b=0, bg=0, r=0, y=3 * at, z=0, g=0, strides=(64, 64, 64, 64, 64),
+            M=4, K=64, N=64, order=0, act=0, dtype=0, ws=64 * at, bytes=1 << 30):
+        a = _FWD.pack(x, w, wg, b, bg, r, y, z, g, *strides, M, K, N, order, act, dtype)
+        return L.dash_dense_fwd(a, ws, bytes, None)
+    for bad in (dict(x=0), dict(w=0), dict(y=0), dict(M=0), dict(K=0), dict(N=-1), dict(order=2),
+                dict(act=5), dict(act=-1), dict(dtype=3), dict(x=at + 1), dict(bg=at), dict(g=at),
+                dict(strides=(64, 64, 64, 64, 63)), dict(y=at), dict(y=2 * at), dict(y=64 * at),
+                dict(z=3 * at), dict(b=3 * at), dict(r=3 * at, strides=(64, 64, 64, 72, 64)),
+                dict(r=3 * at + 64)):
+        assert fwd(**bad) == 1, bad
+    assert fwd(dtype=2) == 2 and fwd(M=(1 << 31) - 1) == 2
+    assert fwd(ws=0) == 5 and fwd(bytes=255) == 5 and fwd(ws=64 * at + 8) == 5
+    assert L.dash_dense_fwd(None, at, 1 << 30, None) == 1
+    assert L.dash_dense_fwd_workspace_bytes(None) == 0
+
+    def bwd(dy=at, x=2 * at, w=3 * at, wg=0, z=0, g=0, dx=4 * at, dw=5 * at, dwg=0, db=0, dbg=0,
+            strides=(64,) * 7, M=4, K=64, N=64, order=0, act=0, dtype=0, ws=64 * at, bytes=1 << 30):
+        a = _BWD.pack(dy, x, w, wg, z, g, dx, dw, dwg, db, dbg, *strides, M, K, N, order, act, dtype)
+        return L.dash_dense_bwd(a, ws, bytes, None)
+    for bad in (dict(dy=0), dict(M=-1), dict(K=0), dict(N=0), dict(order=-1), dict(act=9),
+                dict(dtype=7), dict(x=0), dict(w=0), dict(act=1), dict(g=at), dict(dwg=at),
+                dict(dbg=at), dict(z=6 * at, g=7 * at), dict(z=6 * at, g=7 * at, wg=8 * at),
+                dict(dx=at), dict(dw=2 * at), dict(dw=4 * at), dict(db=4 * at), dict(dw=5 * at + 1),
+                dict(strides=(64, 64, 64, 64, 63, 64, 64)),
+                dict(strides=(64, 64, 64, 64, 64, 63, 64))):
+        assert bwd(**bad) == 1, bad
+    assert bwd(dtype=2) == 2 and bwd(M=(1 << 31) - 1) == 2
+    assert bwd(ws=0) == 5 and bwd(bytes=255) == 5
+    assert L.dash_dense_bwd(None, at, 1 << 30, None) == 1
+
+
+def test_workspace_sizes(L):
+    """A part of the workspace for each operand that has to be copied, and for partial sums."""
+    at = 1 << 20
+
+    def need(x=at, w=2 * at, xs=64, ws=64, M=4, K=64, N=64, order=0):
+        return L.dash_dense_fwd_workspace_bytes(
+            _FWD.pack(x, w, 0, 0, 0, 0, 3 * at, 0, 0, xs, ws, 0, 0, N, M, K, N, order, 0, 0))
+    assert need() == 256
+    assert need(x=at + 2) == 256 + 4 * 128 and need(xs=65) == 256 + 4 * 128
+    assert need(w=2 * at + 2) == 256 + 64 * 128 and need(ws=68) == 256 + 64 * 128
+    assert need(K=7, xs=7) == 256 + 256  # 4 rows of 8, as a block of 256
+    assert need(N=64, K=64, ws=70, order=1) == 256 + 64 * 128
+    assert need(M=1, K=16384, N=256, ws=256) > 256 + 2 * 256 * 4
+    assert need(M=1, x=at, xs=3) == 256  # the stride of a single row has no meaning
+
+
+# M, K, N: one row and element up; tile edges; odd; several tiles a CTA; long sums
+SIZES = [(1, 1, 1), (1, 64, 256), (3, 8, 40), (17, 200, 96), (129, 65, 130), (256, 64, 256),
+         (257, 128, 513), (300, 1001, 77), (1, 4096, 1000), (33, 8192, 264), (1237, 96, 1000),
+         (2100, 192, 8200)]
+# what stands in the epilogue: act, bias, gate, residual
+EPILOGUES = [("none", False, False, False), ("silu", False, True, False), ("gelu", True, False, True),
+             ("gelu_tanh", True, True, True), ("relu", True, False, False)]
+
+
+def case(M, K, N, order, dtype, epilogue, seed=0):
+    act, b, g, r = epilogue
+    x, w = make((M, K), dtype, seed), weight(K, N, order, dtype, seed + 1)
+    a = dict(act=act, bias=make((N,), dtype, seed + 2, 0.5) if b else None,
+             w_gate=weight(K, N, order, dtype, seed + 3) if g else None,
+             bias_gate=make((N,), dtype, seed + 4, 0.5) if b and g else None)
+    return x, w, a, make((M, N), dtype, seed + 5) if r else None
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("order", ["kn", "nk"])
+@pytest.mark.parametrize("epilogue", EPILOGUES, ids=lambda e: e[0])
+@pytest.mark.parametrize("size", SIZES, ids=str)
+def test_forward(L, size, epilogue, order, dtype):
+    x, w, a, r = case(*size, order, dtype, epilogue)
+    y, kept = dash.dense_fwd(x, w, residual=r, check=True, **a)
+    check_forward(x, w, y, kept, residual=r, **a)
+    assert (kept is None) == (a["act"] == "none" and a["w_gate"] is None)
+    again, none = dash.dense_fwd(x, w, residual=r, keep=False, **a)
+    assert none is None and torch.equal(again, y)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("order", ["kn", "nk"])
+@pytest.mark.parametrize("epilogue", EPILOGUES, ids=lambda e: e[0])
+@pytest.mark.parametrize("size", SIZES, ids=str)
+def test_backward(L, size, epilogue, order, dtype):
+    M, K, N = size
+    x, w, a, r = case(*size, order, dtype, epilogue)
+    _, kept = dash.dense_fwd(x, w, **a)
+    dy = make((M, N), dtype, 9)
+    grads = dash.dense_bwd(dy, x, w, kept, check=True, **a)
+    assert grads[1].stride() == w.stride() or 1 in (K, N)
+    check_backward(dy, x, w, kept, grads, **a)
+    again = dash.dense_bwd(dy, x, w, kept, **a)
+    assert all(p is q or torch.equal(p, q) for p, q in zip(grads, again))
+    dx = dash.dense_bwd(dy, x, w, kept, need_dw=False, **a)
+    assert torch.equal(dx[0], grads[0]) and dx[1] is None and dx[3] is None
+    dw = dash.dense_bwd(dy, x, w, kept, need_dx=False, **a)
+    assert dw[0] is None and torch.equal(dw[1], grads[1])
+
+
+@gpu
+@pytest.mark.parametrize("offset", [0, 1, 8])
+@pytest.mark.parametrize("order", ["kn", "nk"])
+def test_views(L, order, offset):
+    """Rows at wider strides, off 16 bytes too, outputs into views whose surroundings stay."""
+    M, K, N, dt = 137, 72, 136, BF
+    x, w, a, r = case(M, K, N, order, dt, ("silu", True, True, True))
+    dy = make((M, N), dt, 9)
+    y, kept = dash.dense_fwd(x, w, residual=r, **a)
+    grads = dash.dense_bwd(dy, x, w, kept, **a)
+
+    def wide(t):
+        big = torch.full((t.shape[0] + 2, t.shape[1] + 24), 7.0, dtype=dt, device="cuda")
+        v = big[1:-1, offset:offset + t.shape[1]]
+        v.copy_(t)
+        return big, v
+
+    def wide_w(t):
+        big, v = wide(t if order == "kn" else t.t())
+        return big, v if order == "kn" else v.t()
+    xv, rv, dv = wide(x)[1], wide(r)[1], wide(dy)[1]
+    wv = wide_w(w)[1]
+    a["w_gate"] = wide_w(a["w_gate"])[1]
+    big, out = wide(torch.zeros_like(y))
+    got, kept2 = dash.dense_fwd(xv, wv, residual=rv, out=out, check=True, **a)
+    assert got is out and torch.equal(out, y) and torch.equal(kept2, kept)
+    assert (big == 7).sum() == big.numel() - out.numel() + (out == 7).sum()
+    bx, dx = wide(torch.zeros_like(x))
+    bw, dw = wide_w(torch.zeros_like(w))
+    bg, dg = wide_w(torch.zeros_like(w))
+    res = dash.dense_bwd(dv, xv, wv, kept, dx=dx, dw=dw, dw_gate=dg, **a)
+    assert res[0] is dx and res[1] is dw and res[3] is dg
+    assert all(torch.equal(p, q) for p, q in zip(res, grads))
+    for b, o in ((bx, dx), (bw, dw), (bg, dg)):
+        assert (b == 7).sum() == b.numel() - o.numel() + (o == 7).sum()
+    # onto the residual stream itself, from rows of a [B, S, K] tensor, one row for all
+    same = r.clone()
+    dash.dense_fwd(x, w, residual=same, out=same, **a)
+    assert torch.equal(same, y)
+    x3 = x[:136].view(2, 68, K).transpose(0, 1).contiguous().transpose(0, 1)
+    y3 = dash.dense_fwd(x[:136].view(2, 68, K), w, **a)[0]
+    with pytest.raises(ValueError):
+        dash.dense_fwd(x3, w, **a)
+    assert y3.shape == (2, 68, N)
+    one = dash.dense_bwd(dy[:1].expand(M, N), x, w, kept, **a)
+    ref = dash.dense_bwd(dy[:1].repeat(M, 1), x, w, kept, **a)
+    assert all(torch.equal(p, q) for p, q in zip(one, ref))
+
+
+@gpu
+def test_no_rows(L):
+    x, w, a, _ = case(1, 40, 24, "kn", BF, ("gelu", True, True, False))
+    x, dy = x[:0], torch.empty(0, 24, dtype=BF, device="cuda")
+    y, kept = dash.dense_fwd(x, w, **a)
+    assert y.shape == (0, 24) and kept.shape == (2, 0, 24)
+    dx, *rest = dash.dense_bwd(dy, x, w, kept, **a)
+    assert dx.shape == (0, 40) and all((t == 0).all() for t in rest)
+
+
+@gpu
+@pytest.mark.parametrize("bad", [math.inf, math.nan])
+def test_special_values_stay_in_their_row(L, bad):
+    """A row of x that is not finite spoils its own row of y and dx only; a split long sum too."""
+    for M, K, N in ((300, 72, 200), (2, 8192, 64)):
+        x, w, a, _ = case(M, K, N, "kn", BF, ("silu", False, True, False))
+        y, kept = dash.dense_fwd(x, w, **a)
+        dy = make((M, N), BF, 3)
+        dx = dash.dense_bwd(dy, x, w, kept, need_dw=False, **a)[0]
+        x[M // 2, K - 1] = bad
+        y2, _ = dash.dense_fwd(x, w, **a)
+        assert not y2[M // 2].isfinite().any()
+        y2[M // 2] = y[M // 2]
+        assert torch.equal(y2, y)
+        dy[M // 2, 5] = bad
+        dx2 = dash.dense_bwd(dy, x, w, kept, need_dw=False, **a)[0]
+        assert not dx2[M // 2].isfinite().any()
+        dx2[M // 2] = dx[M // 2]
+        assert torch.equal(dx2, dx)
+
+
+@gpu
+def test_activations_at_the_ends(L):
+    """Far arguments: the activations and their slopes go to 0 and 1, without NaN."""
+    z = torch.tensor([[-3e4, -200.0, -90.0, -30.0, -1e-4, 0.0, 1e-4, 30.0, 90.0, 3e4]], dtype=BF,
+                     device="cuda")
+    eye = torch.eye(10, dtype=BF, device="cuda")
+    for act in ACTS:
+        y, kept = dash.dense_fwd(z, eye, act=act)
+        check_forward(z, eye, y, kept, act)
+        dx, dw, *_ = dash.dense_bwd(torch.ones_like(z), z, eye, kept, act=act)
+        assert torch.allclose(dx.double(), act_of(z.double(), act)[1], atol=2.0 ** -8, rtol=2.0 ** -8)
+        assert dx.isfinite().all() and dw.isfinite().all()
+
+
+@gpu
+def test_streams_graphs_and_workspaces(L):
+    """On another stream, into captured graphs (replayed with new inputs), workspaces handed in."""
+    M, K, N = 200, 1024, 320
+    x, w, a, r = case(M, K, N, "kn", BF, ("silu", False, True, True))
+    dy = make((M, N), BF, 9)
+    ref = dash.dense_fwd(x, w, residual=r, **a)
+    want = dash.dense_bwd(dy, x, w, ref[1], **a)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    y, kept = dash.dense_fwd(x, w, residual=r, stream=s, **a)
+    got = dash.dense_bwd(dy, x, w, kept, stream=s, **a)
+    s.synchronize()
+    assert torch.equal(y, ref[0])
+    assert all(p is q or torch.equal(p, q) for p, q in zip(got, want))
+    ws1 = torch.empty(dash.dense_fwd_workspace_bytes(x, w, w_gate=a["w_gate"]), dtype=torch.uint8,
+                      device="cuda").fill_(255)
+    ws2 = torch.empty(dash.dense_bwd_workspace_bytes(dy, x, w, kept, **a), dtype=torch.uint8,
+                      device="cuda").fill_(255)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y, kept = dash.dense_fwd(x, w, residual=r, workspace=ws1, **a)
+        got = dash.dense_bwd(dy, x, w, kept, workspace=ws2, **a)
+    for seed in (20, 21):
+        x.copy_(make((M, K), BF, seed))
+        dy.copy_(make((M, N), BF, seed + 5))
+        g.replay()
+        y1, k1 = dash.dense_fwd(x, w, residual=r, **a)
+        assert torch.equal(y, y1) and torch.equal(kept, k1)
+        assert all(p is q or torch.equal(p, q)
+                   for p, q in zip(got, dash.dense_bwd(dy, x, w, k1, **a)))
+    dash.status(ws1), dash.status(ws2)
+
+
+@gpu
+def test_refusals(L):
+    x, w, a, r = case(4, 64, 32, "kn", BF, ("silu", True, True, True))
+    _, kept = dash.dense_fwd(x, w, **a)
+    dy = make((4, 32), BF, 9)
+    for bad in (lambda: dash.dense_fwd(x.cpu(), w), lambda: dash.dense_fwd(x.float(), w.float()),
+                lambda: dash.dense_fwd(x, w.half()), lambda: dash.dense_fwd(x, w[:63]),
+                lambda: dash.dense_fwd(x, w, act="tanh"), lambda: dash.dense_fwd(x, w, w[0, :31]),
+                lambda: dash.dense_fwd(x, w, residual=x), lambda: dash.dense_fwd(x, w, out=dy[:3]),
+                lambda: dash.dense_fwd(x, w[::2, ::2].contiguous()),
+                lambda: dash.dense_fwd(x[:, ::2], w[:32]), lambda: dash.dense_fwd(x[:, :32], w[::2, ::2]),
+                lambda: dash.dense_fwd(x, w, w_gate=w.t().contiguous().t()),
+                lambda: dash.dense_fwd(x, w, bias_gate=a["bias"]),
+                lambda: dash.dense_fwd(x, w, out=dy[:1].expand(4, 32)),
+                lambda: dash.dense_fwd(x, w, workspace=torch.empty(8, device="cuda")),
+                lambda: dash.dense_fwd(x, w[:, :0]), lambda: dash.dense_fwd(x[:, :0], w[:0]),
+                lambda: dash.dense_bwd(dy, x, w, act="silu"),
+                lambda: dash.dense_bwd(dy, x, w, kept[0], act="silu", w_gate=w),
+                lambda: dash.dense_bwd(dy[:3], x, w), lambda: dash.dense_bwd(dy, x, w, dw_gate=w),
+                lambda: dash.dense_bwd(dy, x, w, dw=torch.empty_like(w).t().contiguous().t()),
+                lambda: dash.dense_bwd(dy.half(), x, w)):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: dash.dense_fwd(x, w, residual=dy, out=w[:4]),
+                lambda: dash.dense_fwd(x[:2], w, out=r[:2], bias=r[1]),
+                lambda: dash.dense_bwd(dy, x, w, dx=x), lambda: dash.dense_bwd(dy, x, w, dw=w)):
+        with pytest.raises(dash.DashError):
+            bad()
+
+
+@gpu
+def test_failure_detection(L):
+    """Loads that end early: the waits for them run out, the call is reported, the next one is right."""
+    M, K, N = 700, 640, 1000
+    x, w, a, r = case(M, K, N, "nk", BF, ("gelu", True, False, True))
+    y, _ = dash.dense_fwd(x, w, residual=r, **a)
+    limit = dash.wait_limit()
+    dash.set_wait_limit(0.2)
+    try:
+        for block in (0, 7):
+            assert L.dash_dense_withhold(block) == 0
+            with pytest.raises(dash.DashError) as e:
+                dash.dense_fwd(x, w, residual=r, check=True, **a)
+            assert e.value.code == 4
+    finally:
+        L.dash_dense_withhold(-1)
+        dash.set_wait_limit(limit)
+    again, _ = dash.dense_fwd(x, w, residual=r, check=True, **a)
+    assert torch.equal(again, y)
