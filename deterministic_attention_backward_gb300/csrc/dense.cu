@@ -10,6 +10,7 @@ namespace {
 
 std::atomic<int> g_dense_withhold{-1};
 
+constexpr int kMaxSize = 1 << 30;  // coordinates and row numbers are 32-bit
 bool aligned2(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
 long long up(long long n, long long to) { return (n + to - 1) / to * to; }
 int ceil_div(long long n, long long d) { return (int)((n + d - 1) / d); }
@@ -47,35 +48,41 @@ bool make_rows_map(CUtensorMap *m, const Rows &r, int box, bool f16) {
 struct Product {
   int M, N, K, parts, outs;
   bool gated;
-  int bn, splits;
+  int bn = 256, whole = 0, splits = 1, per = 0;
   int cols() const { return gated ? bn / 2 : bn; }
   int mt() const { return ceil_div(M, kDenseM); }
   int nt() const { return ceil_div(N, cols()); }
   int nk() const { return ceil_div(K, kDenseK); }
+  long long tiles() const { return (long long)mt() * nt() * outs; }
   size_t part_bytes() const {
-    return splits > 1 ? align256((size_t)splits * outs * M * nt() * bn * 4) : 0;
+    return splits > 1 ? (size_t)(tiles() - whole) * splits * kDenseM * bn * 4 : 0;
   }
 };
 
 // The choice follows from the sizes alone, as the order of the sums does (the pairs of SMs are those
-// of a GB300, not of the GPU that runs).  Time is counted in blocks of 64 of a 256-column tile
-// (0.27 us): a block of 128 columns costs 0.7, a tile 3 beside its blocks, a second kernel 8 and the
-// partial sums their way to memory and back.
-constexpr int kPairs = 76, kMaxSplits = 32;
+// of a GB300, not of the GPU that runs).  Tiles that fill whole rounds of the pairs stay whole; the
+// rest, which would leave pairs idle, are split along the contraction where that is shorter.  Time is
+// counted in blocks of 64 of a 256-column tile (0.27 us): a block of 128 columns costs 0.7, an item 3
+// beside its blocks, the kernel that adds the splits 10 and the partial sums their way to memory.
+constexpr int kPairs = 76, kMaxSplits = 64;
 Product plan(int M, int N, int K, int parts, int outs, bool gated) {
-  Product best{M, N, K, parts, outs, gated, 256, 1};
+  Product best;
   double least = 0;
   for (int bn = 256; bn >= 128; bn -= 128) {
-    Product p{M, N, K, parts, outs, gated, bn, 1};
-    const long long tiles = (long long)p.mt() * p.nt() * outs;
+    Product p{M, N, K, parts, outs, gated, bn};
+    const long long tiles = p.tiles(), rounds = tiles / kPairs, rest = tiles - rounds * kPairs;
+    if (tiles >= (1LL << 28)) continue;
     const int blocks = p.nk() * parts;
+    const double block = bn == 256 ? 1.0 : 0.7;
+    p.whole = (int)(rounds * kPairs);
     for (int s = 1; s <= kMaxSplits && s <= blocks; ++s) {
-      if (s > 1 && tiles * s > 4 * kPairs) break;
-      const int per = ceil_div(blocks, s);
-      if (ceil_div(blocks, per) != s) continue;  // no split is empty
-      double t = (double)((tiles * s + kPairs - 1) / kPairs) * (per * (bn == 256 ? 1.0 : 0.7) + 3);
-      if (s > 1) t += 8 + 8.0 * s * outs * M * p.nt() * bn / 1.8e6;
-      if (least == 0 || t < 0.97 * least) {
+      p.per = ceil_div(blocks, s);
+      if (ceil_div(blocks, p.per) != s) continue;  // no split is empty
+      if (s > 1 && (rest == 0 || rest * s > 4 * kPairs)) break;
+      double t = rounds * (blocks * block + 3);
+      t += (rest * s + kPairs - 1) / kPairs * (p.per * block + 3);
+      if (s > 1) t += 10 + 8.0 * rest * s * (M < kDenseM ? M : kDenseM) * bn / 1.8e6;
+      if (least == 0 || t < 0.98 * least) {
         least = t;
         best = p;
         best.splits = s;
@@ -85,10 +92,7 @@ Product plan(int M, int N, int K, int parts, int outs, bool gated) {
   return best;
 }
 
-bool sizes_ok(const Product &p) {
-  return (long long)p.mt() * p.nt() * p.outs * p.splits < (1LL << 30) && p.M < (1 << 30) &&
-         p.N < (1 << 30) && p.K < (1 << 30);
-}
+bool sizes_ok(const Product &p) { return p.per > 0; }
 
 struct Arena {
   char *base;
@@ -129,9 +133,8 @@ dash_status_t launch(const Product &p, const Rows (&a)[2], const Rows (&b)[2], b
   d.wait_ns = g_wait_ns.load();
   d.M = p.M, d.N = p.N;
   d.mt = p.mt(), d.nt = p.nt(), d.bn = p.bn;
-  d.part_cols = (long long)d.nt * d.bn;
   d.nk = p.nk(), d.parts = p.parts, d.outs = p.outs;
-  d.splits = p.splits, d.per = ceil_div(d.nk * d.parts, p.splits);
+  d.whole = p.whole, d.splits = p.splits, d.per = p.per;
   d.a_mn = a_mn, d.b_mn = b_mn, d.a_out = a_out, d.b_out = b_out;
   d.withhold = g_dense_withhold.load();
   return launch_dense(f16, ta, tb, d, sms, s) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
@@ -153,6 +156,7 @@ dash_status_t check_fwd(const dash_dense_fwd_t *a, Product &p, Rows &x, Rows (&w
   if ((a->bias_gate || a->gate) && !a->w_gate) return DASH_ERR_INVALID;
   if (a->M > 1 && a->y_stride < a->N) return DASH_ERR_INVALID;
   const bool kn = a->order == DASH_DENSE_KN;
+  if (a->M > kMaxSize || a->K > kMaxSize || a->N > kMaxSize) return DASH_ERR_UNSUPPORTED;
   p = plan(a->M, a->N, a->K, 1, 1, a->w_gate != nullptr);
   if (!sizes_ok(p)) return DASH_ERR_UNSUPPORTED;
   x = Rows(a->x, a->x_stride, a->M, a->K);
@@ -196,6 +200,7 @@ dash_status_t check_bwd(const dash_dense_bwd_t *a, Bwd &b) {
   b.x = Rows(a->dw ? a->x : nullptr, a->x_stride, a->M, a->K);
   b.w[0] = Rows(a->dx ? a->w : nullptr, a->w_stride, wr, wc);
   b.w[1] = Rows(a->dx && gated ? a->w_gate : nullptr, a->w_gate_stride, wr, wc);
+  if (a->M > kMaxSize || a->K > kMaxSize || a->N > kMaxSize) return DASH_ERR_UNSUPPORTED;
   const int M = a->M ? a->M : 1;
   b.dx = plan(M, a->K, a->N, gated ? 2 : 1, 1, false);
   b.dw = kn ? plan(a->K, a->N, M, 1, gated ? 2 : 1, false)

@@ -28,14 +28,13 @@ struct DenseParams {
   DenseEpilogue e;
   void *y1;                  // the second output (outs == 2)
   long long y1s;
-  float *part;               // splits > 1: [splits][outs][M][cols] fp32 sums
+  float *part;               // fp32 sums of the split tiles: [tile][split][256][bn]
   uint32_t *status;
   unsigned long long wait_ns;
-  long long part_cols;       // nt * bn
   int M, N;
   int mt, nt, bn;            // tiles; bn columns of a tile's accumulator (gated: half z, half g)
   int nk, parts, outs;       // blocks of kDenseK of a part
-  int splits, per;           // splits of the parts' blocks, blocks of a split
+  int whole, splits, per;    // tiles that are whole; splits of each other tile, blocks of a split
   int a_mn, b_mn;            // the contiguous dimension is M (N), not the contraction
   int a_out, b_out;          // the second output takes the second A (B)
   int withhold;              // block at which a CTA's loads end, else -1

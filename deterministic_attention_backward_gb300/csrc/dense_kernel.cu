@@ -14,7 +14,9 @@ constexpr int kABytes = 128 * kDenseK * 2;  // one CTA's half of a tile's rows
 constexpr int kStageBytes = 2 * kABytes;    // and its half of the columns (128 at most)
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = (4 + kEpiWarps) * 32;
-constexpr int kOffBar = kStages * kStageBytes;
+constexpr int kTurnBytes = 32 * 64;         // 32 rows of 32 two-byte elements
+constexpr int kOffTurn = kStages * kStageBytes;  // two of them for each epilogue warp
+constexpr int kOffBar = kOffTurn + 2 * kEpiWarps * kTurnBytes;
 // full[], empty[], acc_full[2], acc_empty[2], drain
 constexpr int kNumBars = 2 * kStages + 5;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;  // tmem address, abort flag
@@ -77,13 +79,24 @@ __device__ __forceinline__ bool wait_pair(uint64_t *bar, uint32_t parity, const 
     }
   }
 }
-// One box into this CTA's shared memory, its bytes counted on a barrier of either CTA.
-__device__ __forceinline__ void load_box(void *dst, const CUtensorMap *map, uint32_t bar, int c0,
-                                         int c1) {
+// One box into this CTA's shared memory, its bytes counted on a barrier of either CTA; issued by the
+// lane of a converged warp with `lead` set (a lane on its own takes 85 cycles a box).
+__device__ __forceinline__ void load_box(uint32_t lead, uint32_t dst, const CUtensorMap *map,
+                                         uint32_t bar, int c0, int c1) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "@e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile"
+      ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];\n\t}\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void expect_l(uint32_t lead, uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.b32 e, %2, 0;\n\t"
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}\n" ::"r"(bar),
+      "r"(bytes), "r"(lead)
       : "memory");
 }
 __device__ __forceinline__ void alloc_pair(uint32_t *dst) {
@@ -121,105 +134,173 @@ __device__ __forceinline__ void commit_pair(uint32_t lead, uint64_t *bar) {
 }
 
 // ------------------------------------------------------------------ activations
-// act(z); the slope too where asked for.  expf, erff and tanhf are within a few units in the
-// last place, far below the rounding of the outputs to 16 bits.
-__device__ __forceinline__ float activation(float z, int act) {
-  switch (act) {
-    case DASH_ACT_RELU: return z > 0.f || z != z ? z : 0.f;
-    case DASH_ACT_SILU: return z / (1.f + expf(-z));
-    case DASH_ACT_GELU: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-    case DASH_ACT_GELU_TANH:
-      return 0.5f * z * (1.f + tanhf(0.79788456080286536f * fmaf(0.044715f * z * z, z, z)));
-    default: return z;
-  }
+// 1 / (1 + e^-z), within a few units in the last place where it is not tiny: far below the rounding
+// of the outputs to 16 bits.
+__device__ __forceinline__ float sigmoid(float z) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2_approx(-kLog2e * z)));
+  return r;
 }
-__device__ __forceinline__ float activation(float z, int act, float &slope) {
+// z/2 (1 + tanh u) = z sigmoid(2u)
+__device__ __forceinline__ float tanh_sigmoid(float z) {
+  return sigmoid(1.5957691216057308f * fmaf(0.044715f * z * z, z, z));
+}
+template <int kAct>
+__device__ __forceinline__ float activation(float z) {
+  if constexpr (kAct == DASH_ACT_RELU) return z > 0.f || z != z ? z : 0.f;
+  if constexpr (kAct == DASH_ACT_SILU) return z * sigmoid(z);
+  if constexpr (kAct == DASH_ACT_GELU)
+    return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+  if constexpr (kAct == DASH_ACT_GELU_TANH) return z * tanh_sigmoid(z);
+  return z;
+}
+// act(z) and its slope
+template <int kAct>
+__device__ __forceinline__ float activation(float z, float &slope) {
+  if constexpr (kAct == DASH_ACT_RELU) {
+    slope = z > 0.f ? 1.f : z != z ? z : 0.f;
+    return activation<kAct>(z);
+  }
+  if constexpr (kAct == DASH_ACT_SILU) {
+    const float s = sigmoid(z);
+    slope = s * fmaf(z, 1.f - s, 1.f);
+    return z * s;
+  }
+  if constexpr (kAct == DASH_ACT_GELU) {
+    const float c = 0.5f * (1.f + erff(z * 0.70710678118654752f));
+    slope = fmaf(z, 0.39894228040143268f * ex2_approx(-0.5f * kLog2e * z * z), c);
+    return z * c;
+  }
+  if constexpr (kAct == DASH_ACT_GELU_TANH) {
+    const float s = tanh_sigmoid(z);
+    slope = fmaf(s * (1.f - s), 1.5957691216057308f * z * fmaf(0.134145f * z, z, 1.f), s);
+    return z * s;
+  }
+  slope = 1.f;
+  return z;
+}
+template <int kAct, int C>
+__device__ __forceinline__ void activate(float (&z)[C]) {
+#pragma unroll
+  for (int e = 0; e < C; ++e) z[e] = activation<kAct>(z[e]);
+}
+template <int C>
+__device__ __forceinline__ void activate(int act, float (&z)[C]) {
   switch (act) {
-    case DASH_ACT_RELU:
-      slope = z > 0.f ? 1.f : z != z ? z : 0.f;
-      return z > 0.f || z != z ? z : 0.f;
-    case DASH_ACT_SILU: {
-      const float s = 1.f / (1.f + expf(-z));
-      slope = s * fmaf(z, 1.f - s, 1.f);
-      return z * s;
-    }
-    case DASH_ACT_GELU: {
-      const float c = 0.5f * (1.f + erff(z * 0.70710678118654752f));
-      slope = fmaf(z, 0.39894228040143268f * expf(-0.5f * z * z), c);
-      return z * c;
-    }
-    case DASH_ACT_GELU_TANH: {
-      const float t = tanhf(0.79788456080286536f * fmaf(0.044715f * z * z, z, z));
-      slope = fmaf(0.5f * z * (1.f - t * t), 0.79788456080286536f * fmaf(0.134145f * z, z, 1.f),
-                   0.5f * (1.f + t));
-      return 0.5f * z * (1.f + t);
-    }
-    default: slope = 1.f; return z;
+    case DASH_ACT_RELU: return activate<DASH_ACT_RELU>(z);
+    case DASH_ACT_GELU: return activate<DASH_ACT_GELU>(z);
+    case DASH_ACT_GELU_TANH: return activate<DASH_ACT_GELU_TANH>(z);
+    case DASH_ACT_SILU: return activate<DASH_ACT_SILU>(z);
+    default: return;
   }
 }
 
-// C values of a row from element `at` on, `left` of them inside the row.
+// C values from column n of a row on, `left` of them inside it.
 template <typename T, int C>
-__device__ __forceinline__ void store_cols(void *base, long long at, const float (&v)[C], int left,
-                                           bool vec) {
+__device__ __forceinline__ void store_cols(void *base, long long at, const float (&v)[C], int left) {
   T *dst = static_cast<T *>(base) + at;
-  if (vec) {
 #pragma unroll
-    for (int i = 0; i < C / 8; ++i)
-      if (8 * i + 8 <= left) {
-        float f[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = v[8 * i + e];
-        store_pack<T, 8>(dst + 8 * i, pack<T, 8>(f));
-      }
-    if (left >= C) return;
-#pragma unroll
-    for (int e = 0; e < C; ++e)
-      if (e < left && e >= (left & ~7)) dst[e] = from_f32<T>(v[e]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < C; ++e)
-      if (e < left) dst[e] = from_f32<T>(v[e]);
-  }
+  for (int e = 0; e < C; ++e)
+    if (e < left) dst[e] = from_f32<T>(v[e]);
 }
 template <typename T, int C>
-__device__ __forceinline__ void add_cols(const void *base, long long at, float (&v)[C], int left,
-                                         bool vec) {
+__device__ __forceinline__ void add_cols(const void *base, long long at, float (&v)[C], int left) {
   const T *src = static_cast<const T *>(base) + at;
-  if (vec && left >= C) {
 #pragma unroll
-    for (int i = 0; i < C / 8; ++i) {
+  for (int e = 0; e < C; ++e)
+    if (e < left) v[e] += to_f32<T>(src[e]);
+}
+// A bias, the same for all rows of a warp.
+template <typename T>
+__device__ __forceinline__ void add_bias(const void *base, int n, float (&v)[32], int left,
+                                         bool vec) {
+  if (vec && left >= 32) {
+    const T *src = static_cast<const T *>(base) + n;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
       float f[8];
       unpack<T, 8>(load_pack<T, 8>(src + 8 * i), f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[8 * i + e] += f[e];
     }
   } else {
-#pragma unroll
-    for (int e = 0; e < C; ++e)
-      if (e < left) v[e] += to_f32<T>(src[e]);
+    add_cols<T, 32>(base, n, v, left);
   }
 }
-// The epilogue of C columns of one row, from column n on.
-template <typename T, int C>
-__device__ __forceinline__ void finish(const DenseEpilogue &p, void *y, long long ys, long long row,
-                                       int n, int N, float (&z)[C], float (&g)[C]) {
-  const int left = N - n;
-  const bool vec = p.vec;
-  if (p.bias) add_cols<T, C>(p.bias, n, z, left, vec);
-  if (p.z) store_cols<T, C>(p.z, row * p.zs + n, z, left, vec);
-  if (p.act != DASH_ACT_NONE) {
+
+// ------------------------------------------------------------------ rows and columns change places
+// A thread of the epilogue holds 32 columns of a row; memory wants the lanes of a warp along a
+// row.  A turn buffer holds 32 rows of 64 bytes, the 16-byte pieces of a row permuted so that
+// neither way meets a bank twice.
+__device__ __forceinline__ uint8_t *turn_at(uint8_t *buf, int row, int piece) {
+  return buf + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
+}
+// (out of) this thread's row
+template <typename T>
+__device__ __forceinline__ void turn_put(uint8_t *buf, int lane, const float (&v)[32]) {
 #pragma unroll
-    for (int e = 0; e < C; ++e) z[e] = activation(z[e], p.act);
-  }
-  if (p.gated) {
-    if (p.bias_gate) add_cols<T, C>(p.bias_gate, n, g, left, vec);
-    if (p.g) store_cols<T, C>(p.g, row * p.gs + n, g, left, vec);
+  for (int i = 0; i < 4; ++i) {
+    float f[8];
 #pragma unroll
-    for (int e = 0; e < C; ++e) z[e] *= g[e];
+    for (int e = 0; e < 8; ++e) f[e] = v[8 * i + e];
+    store_pack<T, 8>(reinterpret_cast<T *>(turn_at(buf, lane, i)), pack<T, 8>(f));
   }
-  if (p.residual) add_cols<T, C>(p.residual, row * p.rs + n, z, left, vec);
-  store_cols<T, C>(y, row * ys + n, z, left, vec);
+}
+template <typename T>
+__device__ __forceinline__ void turn_add(uint8_t *buf, int lane, float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float f[8];
+    unpack<T, 8>(load_pack<T, 8>(reinterpret_cast<const T *>(turn_at(buf, lane, i))), f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[8 * i + e] += f[e];
+  }
+}
+// The buffer to rows [row0, row0 + 32) of a tensor, columns [n, n + left): by 16-byte pieces, four
+// lanes a row, or by elements, a row at a time.
+template <typename T>
+__device__ __forceinline__ void turn_store(uint8_t *buf, void *base, long long stride, long long row0,
+                                           int rows, int n, int left, int lane, bool vec) {
+  T *dst = static_cast<T *>(base) + row0 * stride + n;
+  if (vec && left >= 32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + (lane >> 2), c = lane & 3;
+      if (r < rows)
+        store_pack<T, 8>(dst + r * stride + 8 * c,
+                         load_pack<T, 8>(reinterpret_cast<const T *>(turn_at(buf, r, c))));
+    }
+  } else if (lane < left) {
+    const int c = lane >> 3, e = lane & 7;
+    for (int r = 0; r < rows; ++r)
+      dst[r * stride + lane] = reinterpret_cast<const T *>(turn_at(buf, r, c))[e];
+  }
+}
+// Rows of a tensor into the buffer, the pieces that `fetch` has brought in.
+template <typename T>
+__device__ __forceinline__ void turn_fetch(uint4 (&v)[4], const void *base, long long stride,
+                                           long long row0, int rows, int n, int lane) {
+  const T *src = static_cast<const T *>(base) + row0 * stride + n;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 2), c = lane & 3;
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (r < rows) v[i] = *reinterpret_cast<const uint4 *>(src + r * stride + 8 * c);
+  }
+}
+__device__ __forceinline__ void turn_fill(uint8_t *buf, const uint4 (&v)[4], int lane) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<uint4 *>(turn_at(buf, 8 * i + (lane >> 2), lane & 3)) = v[i];
+}
+template <typename T>
+__device__ __forceinline__ void turn_load(uint8_t *buf, const void *base, long long stride,
+                                          long long row0, int rows, int n, int left, int lane) {
+  const T *src = static_cast<const T *>(base) + row0 * stride + n;
+  const int c = lane >> 3, e = lane & 7;
+  if (lane < left)
+    for (int r = 0; r < rows; ++r)
+      reinterpret_cast<T *>(turn_at(buf, r, c))[e] = src[r * stride + lane];
 }
 
 __device__ __forceinline__ void load32(uint32_t taddr, float (&v)[32]) {
@@ -238,21 +319,30 @@ __device__ __forceinline__ void load32(uint32_t taddr, float (&v)[32]) {
   for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
 }
 
-// Work items: (split, output, tile), tiles in groups of 8 rows of tiles, so that those in flight
-// share their operands in L2.
+// Work items: the first `whole` tiles, then `splits` items for each of the others.  Tiles go in
+// groups of 8 rows of tiles, so that those in flight share their operands in L2.
 struct Item {
-  int m, n, out, split, k0, k1;
+  int m, n, out, k0, k1;
+  int cut;  // of a split tile: its place in the partial sums, else -1
 };
 __device__ __forceinline__ Item item_of(const DenseParams &p, int t) {
-  const int tiles = p.mt * p.nt, r = t % tiles, q = t / tiles;
   Item w;
-  w.out = p.outs == 2 ? q & 1 : 0;
-  w.split = p.outs == 2 ? q >> 1 : q;
+  w.cut = -1;
+  w.k0 = 0, w.k1 = p.nk * p.parts;
+  if (t >= p.whole) {
+    const int j = t - p.whole, tile = j / p.splits;
+    if (p.splits > 1) {
+      w.cut = j;
+      w.k0 = (j - tile * p.splits) * p.per;
+      w.k1 = min(w.k0 + p.per, w.k1);
+    }
+    t = p.whole + tile;
+  }
+  const int tiles = p.mt * p.nt, r = t % tiles;
+  w.out = t / tiles;
   const int per = 8 * p.nt, g = r / per, in = r - g * per, rows = min(8, p.mt - 8 * g);
   w.m = (8 * g + in % rows) * kDenseM;
   w.n = in / rows;
-  w.k0 = w.split * p.per;
-  w.k1 = min(w.k0 + p.per, p.nk * p.parts);
   return w;
 }
 
@@ -261,7 +351,7 @@ __device__ __forceinline__ Item item_of(const DenseParams &p, int t) {
 // Each CTA brings in its half of the rows and of the columns; the leader's tensor core instruction
 // reads both halves and leaves each CTA its 128 rows in its own TMEM, where two accumulators
 // alternate so that a tile's epilogue runs beside the next one's products.
-// Warp 0 TMA producer, 1 MMA issuer (leader), 2 TMEM, 4-11 epilogue (thread = row; the two
+// Warps 0 and 3 TMA producers, 1 MMA issuer (leader), 2 TMEM, 4-11 epilogue (thread = row; the two
 // warpgroups share the columns).
 template <typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -284,11 +374,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
-  const int items = p.mt * p.nt * p.outs * p.splits;
+  const int tiles = p.mt * p.nt * p.outs, items = p.whole + (tiles - p.whole) * p.splits;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 2);
       mbar_init(&empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -310,50 +400,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      const int half = p.bn / 2;  // columns that this CTA brings in
-      const uint32_t bytes = 2 * (kABytes + half * kDenseK * 2);
-      bool ok = true;
-      int it = 0;
-      for (int t = first; ok && t < items; t += step) {
-        const Item w = item_of(p, t);
-        const int m = w.m + (int)rank * 128;
-        // gated: the leader brings w's columns of the tile, the other CTA w_gate's
-        const int n = p.e.gated ? w.n * half : w.n * p.bn + (int)rank * half;
-        for (int k = w.k0; k < w.k1; ++k, ++it) {
-          const int s = it % kStages;
-          if (it == p.withhold || !mbar_wait(&empty[s], ((it / kStages) & 1) ^ 1, ab)) {
-            ok = false;
-            break;
-          }
-          const int part = k >= p.nk ? 1 : 0, kk = (k - part * p.nk) * kDenseK;
-          const CUtensorMap *ma = part || (w.out && p.a_out) ? &ta1 : &ta0;
-          const CUtensorMap *mb =
-              part || (w.out && p.b_out) || (p.e.gated && rank) ? &tb1 : &tb0;
-          const uint32_t bar = in_leader(&full[s]);
-          if (leader) mbar_arrive_expect_tx(&full[s], bytes);
-          uint8_t *sa = smem + s * kStageBytes, *sb = sa + kABytes;
-          if (p.a_mn) {
-            load_box(sa, ma, bar, m, kk);
-            load_box(sa + kMnBox, ma, bar, m + 64, kk);
-          } else {
-            load_box(sa, ma, bar, kk, m);
-          }
-          if (p.b_mn) {
-            load_box(sb, mb, bar, n, kk);
-            if (half > 64) load_box(sb + kMnBox, mb, bar, n + 64, kk);
-          } else {
-            load_box(sb, mb, bar, kk, n);
-          }
+  if (warp == 0 || warp == 3) {
+    // ------------------------------------------------------------------ TMA producers
+    // Warp 0 brings in A, warp 3 B, so that neither's instructions hold up the tensor core.
+    const bool isb = warp == 3;
+    const int half = p.bn / 2;  // columns that this CTA brings in
+    const bool mn = isb ? p.b_mn : p.a_mn;
+    const int boxes = mn ? (isb ? half / 64 : 2) : 1;
+    const uint32_t bytes = 2 * (isb ? half * kDenseK * 2 : kABytes);
+    const uint32_t lead = elect_one(), base = smem_u32(smem) + (isb ? kABytes : 0);
+    const uint32_t bar0 = in_leader(full), own0 = smem_u32(full), signals = leader ? lead : 0;
+    bool ok = true;
+    int it = 0, s = 0;
+    uint32_t ph = 1;
+    for (int t = first; ok && t < items; t += step) {
+      const Item w = item_of(p, t);
+      // gated: the leader brings w's columns of the tile, the other CTA w_gate's
+      const int at = !isb         ? w.m + (int)rank * 128
+                     : p.e.gated ? w.n * half
+                                 : w.n * p.bn + (int)rank * half;
+      const bool second = isb ? (w.out && p.b_out) || (p.e.gated && rank) : w.out && p.a_out;
+      for (int k = w.k0; k < w.k1; ++k, ++it) {
+        if (it == p.withhold || !wait_pair(&empty[s], ph, ab)) {
+          ok = false;
+          break;
         }
+        const bool part = k >= p.nk;
+        const int kk = (part ? k - p.nk : k) * kDenseK;
+        const CUtensorMap *map = part || second ? (isb ? &tb1 : &ta1) : (isb ? &tb0 : &ta0);
+        const uint32_t bar = bar0 + 8 * s, dst = base + s * kStageBytes;
+        expect_l(signals, own0 + 8 * s, bytes);
+        if (mn) {
+          load_box(lead, dst, map, bar, at, kk);
+          if (boxes > 1) load_box(lead, dst + kMnBox, map, bar, at + 64, kk);
+        } else {
+          load_box(lead, dst, map, bar, kk, at);
+        }
+        if (++s == kStages) s = 0, ph ^= 1;
       }
-      if (!ok && leader)  // leave no copy in flight into shared memory
-        for (int j = max(0, it - kStages); j < it; ++j)
-          mbar_wait_drain(&full[j % kStages], (j / kStages) & 1, 100000000ull);
     }
-    __syncwarp();
+    if (!ok && leader && !isb)  // leave no copy in flight into shared memory
+      for (int j = max(0, it - kStages); j < it; ++j)
+        mbar_wait_drain(&full[j % kStages], (j / kStages) & 1, 100000000ull);
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
     if (leader) {
@@ -392,39 +480,82 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp >= 4) {
     // ------------------------------------------------------------------ epilogue
     const int quad = warp & 3, wg = (warp - 4) >> 2;
-    const int r = quad * 32 + lane;
-    const int cols = p.e.gated ? p.bn / 2 : p.bn;  // output columns of a tile
+    uint8_t *turn = smem + kOffTurn + (warp - 4) * 2 * kTurnBytes, *turn2 = turn + kTurnBytes;
+    const DenseEpilogue &e = p.e;
+    const bool vec = e.vec;
+    const int cols = e.gated ? p.bn / 2 : p.bn;  // output columns of a tile
+    const int c0 = wg * (cols / 2), c1 = c0 + cols / 2;
     int n = 0;
     for (int t = first; t < items; t += step, ++n) {
       const Item w = item_of(p, t);
+      const long long row0 = w.m + (int)rank * 128 + quad * 32;
+      const int rows = (int)max(0ll, min(32ll, p.M - row0));
+      const int n0 = w.n * cols;
+      // the residual's pieces are under way while the products are formed
+      const bool fetch = e.residual && vec && w.cut < 0;
+      uint4 next[4];
+      if (fetch && n0 + c0 + 32 <= p.N)
+        turn_fetch<T>(next, e.residual, e.rs, row0, rows, n0 + c0, lane);
       if (!wait_pair(&acc_full[n & 1], (n >> 1) & 1, ab)) break;
       tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16) + (n & 1) * 256;
-      const long long row = w.m + (int)rank * 128 + r;
-      const bool in = row < p.M;
-      if (p.splits > 1) {
-        float *dst = p.part + ((long long)(w.split * p.outs + w.out) * p.M + row) * p.part_cols +
-                     (long long)w.n * p.bn;
+      if (w.cut >= 0) {
+        float *dst = p.part + (((long long)w.cut * 2 + rank) * 128 + quad * 32 + lane) * p.bn;
         for (int c = wg * (p.bn / 2); c < (wg + 1) * (p.bn / 2); c += 32) {
           float v[32];
           load32(acc + c, v);
-          if (in) {
+          if (lane < rows) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              *reinterpret_cast<float4 *>(dst + c + 4 * e) =
-                  make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float4 *>(dst + c + 4 * i) =
+                  make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           }
         }
       } else {
-        void *y = w.out ? p.y1 : p.e.y;
-        const long long ys = w.out ? p.y1s : p.e.ys;
-        const int n0 = w.n * cols;
-        for (int c = wg * (cols / 2); c < (wg + 1) * (cols / 2); c += 32) {
-          if (n0 + c >= p.N) break;
+        void *y = w.out ? p.y1 : e.y;
+        const long long ys = w.out ? p.y1s : e.ys;
+        for (int c = c0; c < c1; c += 32) {
+          const int at = n0 + c, left = p.N - at;
+          if (left <= 0) break;
+          // (the buffers alternate: a barrier lies between a buffer's reads and its next filling)
           float z[32], g[32];
           load32(acc + c, z);
-          if (p.e.gated) load32(acc + p.bn / 2 + c, g);
-          if (in) finish<T, 32>(p.e, y, ys, row, n0 + c, p.N, z, g);
+          if (e.gated) load32(acc + p.bn / 2 + c, g);
+          if (e.bias) add_bias<T>(e.bias, at, z, left, vec);
+          if (e.z) {
+            turn_put<T>(turn, lane, z);
+            __syncwarp();
+            turn_store<T>(turn, e.z, e.zs, row0, rows, at, left, lane, vec);
+          }
+          if (e.gated) {
+            if (e.bias_gate) add_bias<T>(e.bias_gate, at, g, left, vec);
+            if (e.g) {
+              turn_put<T>(turn2, lane, g);
+              __syncwarp();
+              turn_store<T>(turn2, e.g, e.gs, row0, rows, at, left, lane, vec);
+            }
+          }
+          activate(e.act, z);
+          if (e.gated) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) z[i] *= g[i];
+          }
+          __syncwarp();
+          if (e.residual) {
+            if (fetch && left >= 32) {
+              turn_fill(turn, next, lane);
+              if (c + 32 < c1 && left >= 64)
+                turn_fetch<T>(next, e.residual, e.rs, row0, rows, at + 32, lane);
+            } else {
+              turn_load<T>(turn, e.residual, e.rs, row0, rows, at, left, lane);
+            }
+            __syncwarp();
+            turn_add<T>(turn, lane, z);
+          }
+          turn_put<T>(turn2, lane, z);
+          __syncwarp();
+          turn_store<T>(turn2, y, ys, row0, rows, at, left, lane, vec);
+          __syncwarp();
         }
       }
       tc_fence_before();
@@ -445,36 +576,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-// The splits' sums, added in order, and the epilogue; a thread takes 4 columns of a row.
+// The splits' sums of the tiles that were split, added in order, and the epilogue; a thread takes 4
+// columns of a row, a CTA's y one tile.
 template <typename T>
 __global__ void __launch_bounds__(256) dense_finish_kernel(const __grid_constant__ DenseParams p) {
-  const int groups = (p.N + 3) / 4;
-  const long long i = blockIdx.x * 256ll + threadIdx.x;
-  const long long row = i / groups;
-  if (row >= p.M) return;
-  const int n = (int)(i - row * groups) * 4, out = blockIdx.y;
-  const int cols = p.e.gated ? p.bn / 2 : p.bn;
-  const long long c = (long long)(n / cols) * p.bn + n % cols;
+  const DenseEpilogue &e = p.e;
+  const int cols = e.gated ? p.bn / 2 : p.bn, groups = cols / 4;
+  const int i = blockIdx.x * 256 + threadIdx.x, r = i / groups, c = (i - r * groups) * 4;
+  const Item w = item_of(p, p.whole + blockIdx.y * p.splits);
+  const long long row = w.m + r;
+  const int n = w.n * cols + c;
+  if (row >= p.M || n >= p.N) return;
   float z[4] = {}, g[4] = {};
-  const float *src = p.part + (out * (long long)p.M + row) * p.part_cols + c;
-  const long long stride = (long long)p.outs * p.M * p.part_cols;
+  const long long stride = (long long)kDenseM * p.bn;
+  const float *src = p.part + w.cut * stride + (long long)r * p.bn + c;
   for (int s = 0; s < p.splits; ++s, src += stride) {
     const float4 v = *reinterpret_cast<const float4 *>(src);
     z[0] += v.x, z[1] += v.y, z[2] += v.z, z[3] += v.w;
-    if (p.e.gated) {
+    if (e.gated) {
       const float4 u = *reinterpret_cast<const float4 *>(src + p.bn / 2);
       g[0] += u.x, g[1] += u.y, g[2] += u.z, g[3] += u.w;
     }
   }
-  DenseEpilogue e = p.e;
-  e.vec = 0;
-  finish<T, 4>(e, out ? p.y1 : e.y, out ? p.y1s : e.ys, row, n, p.N, z, g);
+  const int left = p.N - n;
+  if (e.bias) add_cols<T, 4>(e.bias, n, z, left);
+  if (e.z) store_cols<T, 4>(e.z, row * e.zs + n, z, left);
+  activate(e.act, z);
+  if (e.gated) {
+    if (e.bias_gate) add_cols<T, 4>(e.bias_gate, n, g, left);
+    if (e.g) store_cols<T, 4>(e.g, row * e.gs + n, g, left);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) z[k] *= g[k];
+  }
+  if (e.residual) add_cols<T, 4>(e.residual, row * e.rs + n, z, left);
+  store_cols<T, 4>(w.out ? p.y1 : e.y, row * (w.out ? p.y1s : e.ys) + n, z, left);
 }
 
 // ------------------------------------------------------------------ dz, dgate and their sums
 // 32 threads a strip of 32 V columns, 8 rows at a time over a chunk of rows; the eight rows'
 // sums are added in order through shared memory.
-template <typename T, int V>
+template <typename T, int V, int kAct>
 __global__ void __launch_bounds__(256) dense_grad_kernel(const DenseGradParams p) {
   __shared__ float sums[2][8][32 * V + 1];
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < kStatusBytes / 4)
@@ -493,7 +634,7 @@ __global__ void __launch_bounds__(256) dense_grad_kernel(const DenseGradParams p
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           float slope;
-          const float a = activation(z[e], p.act, slope);
+          const float a = activation<kAct>(z[e], slope);
           z[e] = dy[e] * slope;
           if (p.g) {
             z[e] *= g[e];
@@ -559,13 +700,26 @@ cudaError_t launch_t(const CUtensorMap (&ta)[2], const CUtensorMap (&tb)[2], con
                      int sms, cudaStream_t s) {
   const cudaError_t e = allow_smem<dense_kernel<T>>(kSmem);
   if (e != cudaSuccess) return e;
-  const long long items = (long long)p.mt * p.nt * p.outs * p.splits;
-  const int pairs = (int)(items < sms / 2 ? items : sms / 2);
+  const int rest = p.mt * p.nt * p.outs - p.whole, items = p.whole + rest * p.splits;
+  const int pairs = items < sms / 2 ? items : sms / 2;
   dense_kernel<T><<<2 * pairs, kThreads, kSmem, s>>>(ta[0], ta[1], tb[0], tb[1], p);
-  if (p.splits > 1) {
-    const long long threads = (long long)p.M * ((p.N + 3) / 4);
-    dense_finish_kernel<T><<<dim3((unsigned)((threads + 255) / 256), p.outs), 256, 0, s>>>(p);
+  if (rest > 0 && p.splits > 1) {
+    const int rows = p.M < kDenseM ? p.M : kDenseM, cols = p.e.gated ? p.bn / 2 : p.bn;
+    dense_finish_kernel<T><<<dim3((rows * (cols / 4) + 255) / 256, rest), 256, 0, s>>>(p);
   }
+  return cudaGetLastError();
+}
+
+template <int kAct>
+cudaError_t launch_grad(bool f16, const DenseGradParams &p, int chunks, cudaStream_t s) {
+  const int strip = 32 * (p.vec ? 8 : 1);
+  const dim3 grid((p.N + strip - 1) / strip, chunks);
+  if (f16)
+    p.vec ? dense_grad_kernel<__half, 8, kAct><<<grid, 256, 0, s>>>(p)
+          : dense_grad_kernel<__half, 1, kAct><<<grid, 256, 0, s>>>(p);
+  else
+    p.vec ? dense_grad_kernel<__nv_bfloat16, 8, kAct><<<grid, 256, 0, s>>>(p)
+          : dense_grad_kernel<__nv_bfloat16, 1, kAct><<<grid, 256, 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -577,15 +731,13 @@ cudaError_t launch_dense(bool f16, const CUtensorMap (&ta)[2], const CUtensorMap
 }
 
 cudaError_t launch_dense_grad(bool f16, const DenseGradParams &p, int chunks, cudaStream_t s) {
-  const int strip = 32 * (p.vec ? 8 : 1);
-  const dim3 grid((p.N + strip - 1) / strip, chunks);
-  if (f16)
-    p.vec ? dense_grad_kernel<__half, 8><<<grid, 256, 0, s>>>(p)
-          : dense_grad_kernel<__half, 1><<<grid, 256, 0, s>>>(p);
-  else
-    p.vec ? dense_grad_kernel<__nv_bfloat16, 8><<<grid, 256, 0, s>>>(p)
-          : dense_grad_kernel<__nv_bfloat16, 1><<<grid, 256, 0, s>>>(p);
-  return cudaGetLastError();
+  switch (p.act) {
+    case DASH_ACT_RELU: return launch_grad<DASH_ACT_RELU>(f16, p, chunks, s);
+    case DASH_ACT_GELU: return launch_grad<DASH_ACT_GELU>(f16, p, chunks, s);
+    case DASH_ACT_GELU_TANH: return launch_grad<DASH_ACT_GELU_TANH>(f16, p, chunks, s);
+    case DASH_ACT_SILU: return launch_grad<DASH_ACT_SILU>(f16, p, chunks, s);
+    default: return launch_grad<DASH_ACT_NONE>(f16, p, chunks, s);
+  }
 }
 
 cudaError_t launch_dense_sums(bool f16, const float *part, const float *part_gate, void *out,
