@@ -27,10 +27,11 @@ __all__ = ["fwd", "bwd", "bwd_workspace_bytes", "fwd_workspace_bytes", "status",
            "sched_workers",
            "sched_resolve", "packed_rank", "fwd_varlen", "bwd_varlen", "bwd_varlen_workspace_bytes",
            "bwd_varlen_order_log", "SCHEDULES", "lib",
-           "DashError", "rope_freqs", "rope_fwd", "rope_bwd", "norm_fwd", "norm_bwd",
+           "DashError", "rope_freqs", "rope_fwd", "rope_bwd", "rope_norm_fwd",
+           "rope_norm_bwd", "rope_norm_bwd_workspace_bytes", "norm_fwd", "norm_bwd",
            "join_fwd", "join_bwd", "diff_fwd", "diff_bwd", "diff_fwd_workspace_bytes",
            "diff_bwd_workspace_bytes", "dense_fwd", "dense_bwd", "dense_fwd_workspace_bytes",
-           "dense_bwd_workspace_bytes"]
+           "dense_bwd_workspace_bytes", "grad_norm", "grad_clip", "grad_norm_workspace_bytes"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libdash_attn.so")
@@ -50,11 +51,13 @@ EXPORTS = ["dash_attn_fwd_workspace_bytes", "dash_attn_fwd", "dash_attn_bwd_work
            "dash_sched_step", "dash_sched_grid", "dash_sched_packed_rank", "dash_sched_resolve",
            "dash_attn_bwd_noalloc", "dash_attn_bwd_varlen_workspace_bytes",
            "dash_attn_fwd_varlen", "dash_attn_bwd_varlen", "dash_attn_bwd_varlen_order_log",
-           "dash_rope", "dash_join_fwd", "dash_join_bwd", "dash_join_bwd_workspace_bytes",
+           "dash_rope", "dash_rope_norm_fwd", "dash_rope_norm_bwd",
+           "dash_rope_norm_bwd_workspace_bytes", "dash_join_fwd", "dash_join_bwd", "dash_join_bwd_workspace_bytes",
            "dash_diff_fwd_workspace_bytes", "dash_diff_fwd", "dash_diff_bwd_workspace_bytes",
            "dash_diff_bwd", "dash_diff_fwd_rest", "dash_diff_bwd_rest", "dash_diff_withhold",
            "dash_dense_fwd_workspace_bytes", "dash_dense_fwd", "dash_dense_bwd_workspace_bytes",
-           "dash_dense_bwd", "dash_dense_withhold"]
+           "dash_dense_bwd", "dash_dense_withhold", "dash_grad_norm_workspace_bytes",
+           "dash_grad_norm", "dash_grad_clip"]
 
 
 class DashError(RuntimeError):
@@ -136,6 +139,14 @@ def lib() -> ctypes.CDLL:
         ll = ctypes.c_longlong
         L.dash_rope.argtypes = [vp, i, i, i, i, i, i, vp, f, vp, i, ll, ll, ll, i, vp]
         L.dash_rope.restype = i
+        vpp = ctypes.POINTER(vp)
+        L.dash_rope_norm_fwd.argtypes = [vp, i, vpp, i, i, i, i, i, i, vp, f, f, vp, i, ll, ll, ll, vp]
+        L.dash_rope_norm_fwd.restype = i
+        L.dash_rope_norm_bwd_workspace_bytes.argtypes = [i]
+        L.dash_rope_norm_bwd_workspace_bytes.restype = sz
+        L.dash_rope_norm_bwd.argtypes = [vp, vp, i, vpp, vpp, i, i, i, i, i, i, vp, f, f, vp, i, ll,
+                                         ll, ll, vp, sz, vp]
+        L.dash_rope_norm_bwd.restype = i
         llp = ctypes.POINTER(ll)
         L.dash_join_fwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, ll, i, ll, llp, f, f, f, i,
                                     i, vp]
@@ -162,6 +173,12 @@ def lib() -> ctypes.CDLL:
             getattr(L, name).restype = i
         L.dash_dense_withhold.argtypes = [i]
         L.dash_dense_withhold.restype = i
+        L.dash_grad_norm_workspace_bytes.argtypes = [i]
+        L.dash_grad_norm_workspace_bytes.restype = sz
+        L.dash_grad_norm.argtypes = [cp, i, vp, vp, sz, vp]
+        L.dash_grad_norm.restype = i
+        L.dash_grad_clip.argtypes = [cp, i, f, f, vp, vp, vp, sz, vp]
+        L.dash_grad_clip.restype = i
         _lib = L
         return L
 
@@ -473,11 +490,13 @@ def bwd_varlen_order_log(q, k, v, o, do, lse, cu_seqlens, causal: bool = False,
 
 # The operators' modules import torch, which the schedule queries and the C ABI do without: they
 # are loaded with the first name that is asked of them.
-_MODULES = {"rope_freqs": "rope", "rope_fwd": "rope", "rope_bwd": "rope", "norm_fwd": "norms",
+_MODULES = {"rope_freqs": "rope", "rope_fwd": "rope", "rope_bwd": "rope", "rope_norm_fwd": "rope",
+            "rope_norm_bwd": "rope", "rope_norm_bwd_workspace_bytes": "rope", "norm_fwd": "norms",
             "norm_bwd": "norms", "join_fwd": "norms", "join_bwd": "norms", "diff_fwd": "diff",
             "diff_bwd": "diff", "diff_fwd_workspace_bytes": "diff",
             "diff_bwd_workspace_bytes": "diff", "dense_fwd": "dense", "dense_bwd": "dense",
-            "dense_fwd_workspace_bytes": "dense", "dense_bwd_workspace_bytes": "dense"}
+            "dense_fwd_workspace_bytes": "dense", "dense_bwd_workspace_bytes": "dense",
+            "grad_norm": "grads", "grad_clip": "grads", "grad_norm_workspace_bytes": "grads"}
 
 
 def __getattr__(name):

@@ -18,8 +18,9 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdash_attn.so")
 SOURCES = ["api.cu", "bwd.cu", "bwd_varlen.cu", "fwd.cu", "aux.cu", "noalloc.cu",
-           "rope.cu", "norm.cu", "norm_bf16.cu", "norm_fp16.cu", "norm_fp32.cu",
-           "diff.cu", "diff_fwd.cu", "diff_bwd.cu", "dense.cu", "dense_kernel.cu"]
+           "rope.cu", "rope_norm.cu", "norm.cu", "norm_bf16.cu", "norm_fp16.cu", "norm_fp32.cu",
+           "diff.cu", "diff_fwd.cu", "diff_bwd.cu", "dense.cu", "dense_kernel.cu",
+           "grads.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -15,6 +15,7 @@
 // and v go in one launch (v unturned), so that strided views of a qkv product become the
 // contiguous tensors attention reads in a single pass.  Measured on 2 x 8192 tokens of 32 + 8 + 8
 // heads of 128 in bf16: 65 us, 6.2 TB/s, 91 % of a plain copy's rate; one token 3.5 us, a launch.
+#include "angle.cuh"
 #include "common.cuh"
 #include "dash_attn.h"
 #include "elem.cuh"
@@ -44,24 +45,6 @@ struct RopeParams {
   int pos64, S, tokens, rot, back, nparts, units;
   unsigned magic;  // ceil(2^32 / units)
 };
-
-// A frequency in radians per position as a 128-bit fraction of a turn (whole turns fall off):
-// f / (2 pi) as a sum of two doubles, 1 / (2 pi) being one too, good to 2^-105 of itself; each
-// one's bits are moved to their place, which cuts off less than 2^-128 turns.  One double would
-// leave 53 bits: 2e-7 radians at position 2^31, 6e-6 at 2^36.
-using u128 = unsigned __int128;
-__device__ __forceinline__ u128 fraction_of(double d) {
-  const uint64_t b = (uint64_t)__double_as_longlong(d);
-  const int sh = (int)((b >> 52) & 0x7FF) - 1023 + 76;  // mantissa's last bit at 2^(e-52)
-  const u128 m = (b & 0xFFFFFFFFFFFFFull) | (1ull << 52);
-  const u128 u = sh >= 128 ? 0 : sh >= 0 ? m << sh : sh > -64 ? m >> -sh : 0;
-  return (b >> 63) ? 0 - u : u;
-}
-__device__ __forceinline__ u128 turns_of(double f) {
-  constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;  // 1 / (2 pi)
-  const double hi = f * kHi;
-  return fraction_of(hi) + fraction_of(fma(f, kLo, fma(f, kHi, -hi)));
-}
 
 // n / d by the magic ceil(2^32 / d): exact while n d < 2^32.
 __device__ __forceinline__ unsigned div_by(unsigned n, unsigned d, unsigned magic, bool exact) {

@@ -336,6 +336,33 @@ dash_status_t dash_rope(const dash_rope_part_t *parts, int nparts, int B, int S,
                         long long pos_stride_b, long long pos_stride_t, long long start,
                         int backward, dash_stream_t stream);
 
+/* Norm of every head of q and k with the rotary turn behind it, v copied:
+ *   y = R(w x rstd(x)),    rstd(x) = (mean(x^2) + eps)^-1/2 over the D elements of a head
+ * parts as in dash_rope: the ones with turn != 0 (one or two) are normed and turned, the others
+ * copied; heads of 512 at most.  weights[0], weights[1]: of the first and the second part that turns,
+ * D elements of the heads' type or of fp32 (NULL: ones).  An output may be its input, as it lies.
+ * Arithmetic in fp32, one rounding at the end. */
+dash_status_t dash_rope_norm_fwd(const dash_rope_part_t *parts, int nparts,
+                                 const void *const weights[2], int B, int S, int rot,
+                                 dash_rope_layout_t layout, dash_dtype_t dtype, dash_dtype_t wdtype,
+                                 const double *inv_freq, float magnitude, float eps,
+                                 const void *positions, int positions64, long long pos_stride_b,
+                                 long long pos_stride_t, long long start, dash_stream_t stream);
+/* Bytes of device workspace of dash_rope_norm_bwd for heads of D elements (0: unsupported). */
+size_t dash_rope_norm_bwd_workspace_bytes(int D);
+/* Gradient of dash_rope_norm_fwd: parts hold the gradients of its outputs (in) and of its inputs
+ * (out); x[i], for the i-th part that turns, the forward's input (in and in_stride; heads and D as in
+ * the part).  dweights[i] receives the weight's gradient in its type (NULL: not wanted; both have
+ * heads of one size), summed in an order that the sizes fix.  A gradient may be written over the one
+ * it comes from, as that lies. */
+dash_status_t dash_rope_norm_bwd(const dash_rope_part_t *parts, const dash_rope_part_t *x, int nparts,
+                                 const void *const weights[2], void *const dweights[2], int B, int S,
+                                 int rot, dash_rope_layout_t layout, dash_dtype_t dtype,
+                                 dash_dtype_t wdtype, const double *inv_freq, float magnitude,
+                                 float eps, const void *positions, int positions64,
+                                 long long pos_stride_b, long long pos_stride_t, long long start,
+                                 void *workspace, size_t workspace_bytes, dash_stream_t stream);
+
 /* Norm of rows, and the join of a residual stream with a branch between two norms.  With
  * rstd(v) = (mean(v^2) + eps)^-1/2 over the C elements of a row:
  *   y = skip_scale * x + branch_scale * gate * (a * rstd(a) * w_post)
@@ -476,6 +503,28 @@ dash_status_t dash_dense_bwd(const dash_dense_bwd_t *args, void *workspace, size
  * product kernel end before its block `block` of 64 contraction elements (-1: of none any more), so
  * that the waits for it run out. */
 dash_status_t dash_dense_withhold(int block);
+
+/* The norm over many gradients, and clipping by it:
+ *   norm = sqrt(sum over all tensors of g^2)      out = g * min(1, max_norm / (norm + eps))
+ * n elements each (0 too), dense in memory, of any type; `grads` is a host array that is read before
+ * the call returns.  Squares are added in fp32 within runs of a few hundred elements and in fp64
+ * beyond, in an order that the sizes fix; magnitudes whose squares fp32 does not hold are scaled.  out
+ * may be in itself; beside that nothing written shares memory with another tensor (a tensor that
+ * occurs twice is refused by dash_grad_clip).  A factor of 1 leaves tensors in place untouched; a norm
+ * that is NaN gives NaN.  dash_grad_clip forms the norm and writes it to `norm`, or takes `given` (then
+ * `norm` may be NULL, and no workspace is needed).  A workspace serves one call at a time. */
+typedef struct {
+  const void *in;
+  void *out; /* not read by dash_grad_norm */
+  long long n;
+  int dtype, unused;
+} dash_grad_t;
+size_t dash_grad_norm_workspace_bytes(int count);
+dash_status_t dash_grad_norm(const dash_grad_t *grads, int count, float *norm, void *workspace,
+                             size_t workspace_bytes, dash_stream_t stream);
+dash_status_t dash_grad_clip(const dash_grad_t *grads, int count, float max_norm, float eps,
+                             const float *given, float *norm, void *workspace,
+                             size_t workspace_bytes, dash_stream_t stream);
 
 /* Human-readable name of a status code (static storage). */
 const char *dash_status_string(dash_status_t status);
