@@ -7,8 +7,8 @@
 // formed again there (x is read anyway).  A group of lanes holds a head in registers, a lane two
 // vectors: the two sides of its pairs, so that the turn needs no exchange, and the norm's sums (of
 // x^2 and of w dz x, from which mean(w dz x^) follows) go through shuffles together.  The lane's
-// cosines and sines stay in registers for the heads of a token that the group goes through, the next
-// head's vectors are on their way while one is worked on.  A CTA takes heads of q, of k or of v only
+// cosines and sines stay in registers for the heads of a token that the group goes through; the next
+// heads are on their way by asynchronous copies into rings of its threads' own.  A CTA takes heads of q, of k or of v only
 // (v is copied), so that a thread has one set of weights and one of sums of dw; the CTAs' sums are
 // added in order by a second kernel, their number follows from the sizes.
 #include "angle.cuh"
@@ -22,6 +22,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxD = 512;
+constexpr int kForwardPerSm = 3, kBackPerSm = 2;  // CTAs, for their registers
 
 struct HeadPart {
   const void *x, *dy, *w;            // w null: ones
@@ -45,15 +46,21 @@ struct HeadParams {
   int pos64, S, rot, nparts, wf32;
 };
 
+// A thread's own copies into shared memory: 16 bytes, or zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(on ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 template <typename T, int V>
-__device__ __forceinline__ Pack<T, V> load_if(const T *p, bool on) {
-  Pack<T, V> r;
-  if constexpr (V == 1)
-    r.e[0] = from_f32<T>(0.f);
-  else
-    *reinterpret_cast<uint4 *>(&r) = make_uint4(0, 0, 0, 0);
-  if (on) r = load_pack<T, V>(p);
-  return r;
+__device__ __forceinline__ void load_if(const T *p, bool on, float (&f)[V]) {
+#pragma unroll
+  for (int e = 0; e < V; ++e) f[e] = on ? to_f32<T>(p[e]) : 0.f;
 }
 
 // The V pairs of two vectors turned by (cos, sin).
@@ -70,29 +77,30 @@ __device__ __forceinline__ void turn_pairs(float (&x)[V], float (&y)[V], const f
   }
 }
 
+// Heads on their way to a group, in a ring of its own in shared memory (single elements are loaded
+// when they are needed).
+template <int V, int R, bool kBack>
+constexpr int kRingStages = V == 1 ? 0 : (kBack ? 4 : 6) / R;
+template <int V, int R, bool kBack>
+constexpr int kRingBytes = kRingStages<V, R, kBack> * (kBack ? 4 : 2) * R * kThreads * 16;
+
 // R pairs of vectors a lane.
 template <typename T, int V, int R, bool kHalf, bool kBack>
-__global__ void __launch_bounds__(kThreads) heads_kernel(const __grid_constant__ HeadParams p) {
+__global__ void __launch_bounds__(kThreads, kBack ? kBackPerSm : kForwardPerSm)
+    heads_kernel(const __grid_constant__ HeadParams p) {
+  constexpr int N = kRingStages<V, R, kBack>, kVecs = (kBack ? 4 : 2) * R;
   extern __shared__ uint4 shared[];
-  u128 *turns = reinterpret_cast<u128 *>(shared);              // [rot / 2]
-  float *by = reinterpret_cast<float *>(turns + p.rot / 2);    // magnitude, NaN for a bad frequency
+  uint4 *ring = shared + threadIdx.x;                                     // [N][kVecs][kThreads]
+  u128 *turns = reinterpret_cast<u128 *>(shared + N * kVecs * kThreads);  // [rot / 2]
+  float *by = reinterpret_cast<float *>(turns + p.rot / 2);  // magnitude, NaN for a bad frequency
   const int cta = blockIdx.x;
   const int k = p.nparts > 2 && cta >= p.part[2].cta0   ? 2
                 : p.nparts > 1 && cta >= p.part[1].cta0 ? 1
                                                         : 0;
   const HeadPart &q = p.part[k];
-  if (q.turn) {
-    for (int i = threadIdx.x; i < p.rot / 2; i += kThreads) {
-      const double f = p.inv_freq[i];
-      turns[i] = turns_of(f);
-      by[i] = isfinite(f) ? p.magnitude : NAN;
-    }
-    __syncthreads();
-  }
   const int G = q.lanes, in_group = threadIdx.x & (G - 1);
   int e0[R], e1[R];
   bool has0[R], has1[R];
-  float w0[R][V], w1[R][V], s0[kBack ? R : 1][V] = {}, s1[kBack ? R : 1][V] = {};
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int u = in_group + r * G;
@@ -101,6 +109,70 @@ __global__ void __launch_bounds__(kThreads) heads_kernel(const __grid_constant__
     e1[r] = across ? p.rot / 2 + u * V : e0[r] + V;
     has0[r] = u < q.units && e0[r] < q.D;
     has1[r] = u < q.units && e1[r] < q.D;
+  }
+  const int per_warp = 32 / G, per_cta = kThreads / G;
+  const long long items = p.tokens * q.blocks, step = (long long)q.ctas * per_cta;
+  // all lanes of a warp go round together, as they meet in the shuffles
+  const long long begin =
+      (long long)(cta - q.cta0) * per_cta + (threadIdx.x >> 5) * per_warp;
+  const int mine = (threadIdx.x & 31) / G;
+
+  // where an item's heads lie; `heads` of them are there
+  struct Place {
+    const T *x, *dy;
+    int heads, b, s;
+  };
+  auto place = [&](long long i0) {
+    const long long item = i0 + mine;
+    Place w{static_cast<const T *>(q.x), static_cast<const T *>(q.dy), 0, 0, 0};
+    if (item < items) {
+      const int tok = (int)(item / q.blocks), h0 = (int)(item - (long long)tok * q.blocks) * q.each;
+      w.b = tok / p.S, w.s = tok - w.b * p.S;
+      w.heads = min(q.each, q.heads - h0);
+      w.x += w.b * q.xb + w.s * q.xt + h0 * q.xh;
+      if constexpr (kBack)
+        if (q.normed) w.dy += w.b * q.gb + w.s * q.gt + h0 * q.gh;
+    }
+    return w;
+  };
+  // the head that is brought in next
+  long long ahead0 = begin;
+  int ahead_h = 0;
+  Place ahead = place(begin);
+  auto bring = [&](int slot) {
+    if constexpr (N > 0) {
+      const bool live = ahead_h < ahead.heads;
+      const uint32_t at =
+          (uint32_t)__cvta_generic_to_shared(ring + slot * kVecs * kThreads);
+      const T *x = ahead.x + ahead_h * q.xh, *dy = ahead.dy + ahead_h * q.gh;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        copy16(at + (2 * r) * kThreads * 16, x + e0[r], live && has0[r]);
+        copy16(at + (2 * r + 1) * kThreads * 16, x + e1[r], live && has1[r]);
+        if constexpr (kBack)
+          if (q.normed) {
+            copy16(at + (2 * R + 2 * r) * kThreads * 16, dy + e0[r], live && has0[r]);
+            copy16(at + (2 * R + 2 * r + 1) * kThreads * 16, dy + e1[r], live && has1[r]);
+          }
+      }
+      copies_end();
+      if (++ahead_h == q.each) ahead_h = 0, ahead0 += step, ahead = place(ahead0);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < N - 1; ++i) bring(i);
+
+  if (q.turn) {
+    for (int i = threadIdx.x; i < p.rot / 2; i += kThreads) {
+      const double f = p.inv_freq[i];
+      turns[i] = turns_of(f);
+      by[i] = isfinite(f) ? p.magnitude : NAN;
+    }
+    __syncthreads();
+  }
+  float w0[R][V], w1[R][V], s0[kBack ? R : 1][V] = {}, s1[kBack ? R : 1][V] = {};
+#pragma unroll
+  for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       w0[r][e] = w1[r][e] = 1.f;
@@ -112,43 +184,19 @@ __global__ void __launch_bounds__(kThreads) heads_kernel(const __grid_constant__
         if (has1[r]) w1[r][e] = to_f32<T>(static_cast<const T *>(q.w)[e1[r] + e]);
       }
     }
-  }
-  const long long items = p.tokens * q.blocks;
-  const int per_warp = 32 / G, per_cta = kThreads / G;
   const float inv_d = 1.f / (float)q.D;
-  // all lanes of a warp go round together, as they meet in the shuffles
-  for (long long i0 = (long long)(cta - q.cta0) * per_cta + (threadIdx.x >> 5) * per_warp; i0 < items;
-       i0 += (long long)q.ctas * per_cta) {
-    const long long item = i0 + (threadIdx.x & 31) / G;
-    const bool on = item < items;
-    const long long tok = on ? item / q.blocks : 0;
-    const int h0 = (int)(on ? item - tok * q.blocks : 0) * q.each;
-    const long long b = tok / p.S, s = tok - b * p.S;
-    const T *x = static_cast<const T *>(q.x) + b * q.xb + s * q.xt + h0 * q.xh;
-    const T *dy = static_cast<const T *>(q.dy) + b * q.gb + s * q.gt + h0 * q.gh;
-    T *out = static_cast<T *>(q.out) + b * q.ob + s * q.ot + h0 * q.oh;
-    const int heads = on ? min(q.each, q.heads - h0) : 0;
-    Pack<T, V> nx0[R], nx1[R], ng0[kBack ? R : 1], ng1[kBack ? R : 1];
-    auto fetch = [&](int h) {
-      const bool live = h < heads;
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        nx0[r] = load_if<T, V>(x + h * q.xh + e0[r], live && has0[r]);
-        nx1[r] = load_if<T, V>(x + h * q.xh + e1[r], live && has1[r]);
-        if constexpr (kBack) {
-          ng0[r] = load_if<T, V>(dy + h * q.gh + e0[r], live && has0[r] && q.normed);
-          ng1[r] = load_if<T, V>(dy + h * q.gh + e1[r], live && has1[r] && q.normed);
-        }
-      }
-    };
-    fetch(0);
+  int slot = 0;
+  for (long long i0 = begin; i0 < items; i0 += step) {
+    const Place at = place(i0);
+    const int h0 = (int)((i0 + mine) % q.blocks) * q.each;
+    T *out = static_cast<T *>(q.out) + at.b * q.ob + at.s * q.ot + h0 * q.oh;
     float2 cs[R][V];
     if (q.turn) {
-      long long pos = p.start + s;
+      long long pos = p.start + at.s;
       if (p.pos) {
-        const long long at = b * p.pos_b + s * p.pos_t;
-        pos = p.pos64 ? static_cast<const long long *>(p.pos)[at]
-                      : (long long)static_cast<const int *>(p.pos)[at];
+        const long long i = at.b * p.pos_b + at.s * p.pos_t;
+        pos = p.pos64 ? static_cast<const long long *>(p.pos)[i]
+                      : (long long)static_cast<const int *>(p.pos)[i];
       }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -168,27 +216,55 @@ __global__ void __launch_bounds__(kThreads) heads_kernel(const __grid_constant__
     }
     for (int h = 0; h < q.each; ++h) {
       float x0[R][V], x1[R][V], g0[kBack ? R : 1][V], g1[kBack ? R : 1][V];
-      Pack<T, V> r0[R], r1[R];
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        r0[r] = nx0[r], r1[r] = nx1[r];
-        unpack<T, V>(nx0[r], x0[r]);
-        unpack<T, V>(nx1[r], x1[r]);
-        if constexpr (kBack) {
-          unpack<T, V>(ng0[r], g0[r]);
-          unpack<T, V>(ng1[r], g1[r]);
-        }
-      }
-      if (h + 1 < q.each) fetch(h + 1);
-      const bool live = h < heads;
+      const bool live = h < at.heads;
       T *row = out + h * q.oh;
-      if (!q.normed) {  // (a part's: the same for the whole CTA)
+      if constexpr (N > 0) {
+        bring(slot == 0 ? N - 1 : slot - 1);
+        copies_wait<N - 1>();
+        const uint4 *v = ring + slot * kVecs * kThreads;
+        slot = slot + 1 == N ? 0 : slot + 1;
+        if (!q.normed) {  // (a part's: the same for the whole CTA)
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            if (live && has0[r]) *reinterpret_cast<uint4 *>(row + e0[r]) = v[2 * r * kThreads];
+            if (live && has1[r]) *reinterpret_cast<uint4 *>(row + e1[r]) = v[(2 * r + 1) * kThreads];
+          }
+          continue;
+        }
+        auto take = [&](int i, float (&f)[V]) {
+          const uint4 raw = v[i * kThreads];
+          unpack<T, V>(*reinterpret_cast<const Pack<T, V> *>(&raw), f);
+        };
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          if (live && has0[r]) store_pack<T, V>(row + e0[r], r0[r]);
-          if (live && has1[r]) store_pack<T, V>(row + e1[r], r1[r]);
+          take(2 * r, x0[r]);
+          take(2 * r + 1, x1[r]);
+          if constexpr (kBack) {
+            take(2 * R + 2 * r, g0[r]);
+            take(2 * R + 2 * r + 1, g1[r]);
+          }
         }
-        continue;
+      } else {
+        const T *x = at.x + h * q.xh;
+        if (!q.normed) {
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+              if (live && has0[r]) row[e0[r] + e] = x[e0[r] + e];
+              if (live && has1[r]) row[e1[r] + e] = x[e1[r] + e];
+            }
+          continue;
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          load_if<T, V>(x + e0[r], live && has0[r], x0[r]);
+          load_if<T, V>(x + e1[r], live && has1[r], x1[r]);
+          if constexpr (kBack) {
+            load_if<T, V>(at.dy + h * q.gh + e0[r], live && has0[r], g0[r]);
+            load_if<T, V>(at.dy + h * q.gh + e1[r], live && has1[r], g1[r]);
+          }
+        }
       }
       float ss = 0.f, sg = 0.f;
 #pragma unroll
@@ -241,6 +317,7 @@ __global__ void __launch_bounds__(kThreads) heads_kernel(const __grid_constant__
     }
   }
   if constexpr (kBack) {
+    if constexpr (N > 0) copies_wait<0>();
     if (!q.dw) return;
     // the groups' sums [group][D], added in order
     float *sums = reinterpret_cast<float *>(shared);
@@ -289,18 +366,20 @@ __global__ void __launch_bounds__(256) heads_sums_kernel(const __grid_constant__
 
 // ------------------------------------------------------------------ host
 constexpr int kSms = 152;  // of a GB300: the number of CTAs, and so dw's sums, follow from the sizes
-constexpr int kCtas = 3 * kSms;
 
 int lanes_of(int units) {
   int g = 1;
   while (g < units && g < 32) g *= 2;
   return g;
 }
-// Shares out the CTAs among the parts and the heads of a token among groups.
-void deal(HeadParams &p, int V) {
-  long long rows = 0;
-  for (int i = 0; i < p.nparts; ++i) rows += p.part[i].heads;
-  const long long all = rows;
+// Shares out the CTAs among the parts, by the bytes that they move, and the heads of a token among
+// groups.
+void deal(HeadParams &p, int V, bool back) {
+  auto cost = [&](const HeadPart &q) {
+    return (long long)q.heads * q.D * (back && q.normed ? 3 : 2);
+  };
+  long long all = 0;
+  for (int i = 0; i < p.nparts; ++i) all += cost(p.part[i]);
   int cta = 0;
   for (int i = 0; i < p.nparts; ++i) {
     HeadPart &q = p.part[i];
@@ -308,7 +387,8 @@ void deal(HeadParams &p, int V) {
     q.units = q.turn + (q.D / V - 2 * q.turn + 1) / 2;
     q.lanes = lanes_of(q.units);
     const int groups = kThreads / q.lanes;
-    const long long share = (kCtas * (long long)q.heads + all - 1) / all;
+    long long share = kSms * (back ? kBackPerSm : kForwardPerSm) * cost(q) / all;
+    if (share < 1) share = 1;
     // as many heads of a token to a group as leave every group something, 16 at most: cosines and
     // sines are formed once for them
     long long each = p.tokens * q.heads / (share * groups);
@@ -326,12 +406,17 @@ int ctas_of(const HeadParams &p) { return p.part[p.nparts - 1].cta0 + p.part[p.n
 
 template <typename T, int V, int R, bool kHalf, bool kBack>
 cudaError_t launch(const HeadParams &p, cudaStream_t s) {
-  size_t smem = (size_t)p.rot / 2 * 20;
+  constexpr int kRing = kRingBytes<V, R, kBack>;
+  size_t smem = kRing + (size_t)p.rot / 2 * 20;
   if (kBack)
     for (int i = 0; i < p.nparts; ++i) {
       const size_t sums = (size_t)(kThreads / p.part[i].lanes) * p.part[i].D * 4;
       if (p.part[i].dw && sums > smem) smem = sums;
     }
+  // (kMaxD / 2 pairs at most)
+  const cudaError_t e =
+      allow_smem<heads_kernel<T, V, R, kHalf, kBack>>(kRing + kMaxD / 2 * 20 + 16384);
+  if (e != cudaSuccess) return e;
   heads_kernel<T, V, R, kHalf, kBack><<<ctas_of(p), kThreads, smem, s>>>(p);
   return cudaGetLastError();
 }
@@ -447,7 +532,7 @@ dash_status_t fill(HeadParams &p, bool &wide, Lay &lay, const dash_rope_part_t *
   p.tokens = (long long)B * S;
   p.S = S, p.rot = rot, p.nparts = nparts;
   p.wf32 = wdtype == DASH_FP32;
-  deal(p, wide ? vec : 1);
+  deal(p, wide ? vec : 1, back);
   return DASH_OK;
 }
 
@@ -487,7 +572,7 @@ dash_status_t dash_rope_norm_fwd(const dash_rope_part_t *parts, int nparts,
 }
 
 size_t dash_rope_norm_bwd_workspace_bytes(int D) {
-  return D > 0 && D <= dash::kMaxD ? (size_t)(dash::kCtas + 2) * D * 4 : 0;
+  return D > 0 && D <= dash::kMaxD ? (size_t)(dash::kSms * dash::kBackPerSm + 3) * D * 4 : 0;
 }
 
 dash_status_t dash_rope_norm_bwd(const dash_rope_part_t *parts, const dash_rope_part_t *x, int nparts,
