@@ -7,10 +7,14 @@
 // formed again there (x is read anyway).  A group of lanes holds a head in registers, a lane two
 // vectors: the two sides of its pairs, so that the turn needs no exchange, and the norm's sums (of
 // x^2 and of w dz x, from which mean(w dz x^) follows) go through shuffles together.  The lane's
-// cosines and sines stay in registers for the heads of a token that the group goes through; the next
-// heads are on their way by asynchronous copies into rings of its threads' own.  A CTA takes heads of q, of k or of v only
-// (v is copied), so that a thread has one set of weights and one of sums of dw; the CTAs' sums are
-// added in order by a second kernel, their number follows from the sizes.
+// cosines and sines stay in registers for the heads of a token, which the group goes through one by
+// one, the weights in shared memory (registers decide how many warps there are); the next heads are
+// on their way by asynchronous copies into rings of its threads' own.  A CTA takes heads of q, of k
+// or of v only (v is copied), so that a thread has one set of sums of dw; the CTAs' sums are added in
+// order by a second kernel, their number follows from the sizes.
+//
+// Measured on 2 x 8192 tokens of 32 + 8 + 8 heads of 128 in bf16: forward 68 us, 5.9 TB/s, 88 % of a
+// plain copy's rate, backward 98 us, 5.8 TB/s; one token 3.9 and 6.2 us, launches.
 #include "angle.cuh"
 #include "common.cuh"
 #include "dash_attn.h"
@@ -20,9 +24,9 @@
 namespace dash {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kMaxD = 512;
-constexpr int kForwardPerSm = 3, kBackPerSm = 2;  // CTAs, for their registers
+constexpr int kForwardPerSm = 6, kBackPerSm = 4;  // CTAs, for their registers
 
 struct HeadPart {
   const void *x, *dy, *w;            // w null: ones
@@ -33,7 +37,9 @@ struct HeadPart {
   int heads, D;
   int units, turn;  // pairs of vectors of a head, the ones that turn
   int lanes;        // of a group
-  int each, blocks; // heads of a token that a group takes at a time, times that
+  int across;       // groups of a warp that share a token
+  int each, blocks; // steps through a token's heads that a warp takes at a time, times that
+  int tokens, dt, dk;  // of a warp's blocks: groups of tokens, and how far on its next one is
   int cta0, ctas;
   int normed;
 };
@@ -57,30 +63,95 @@ template <int N>
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-template <typename T, int V>
-__device__ __forceinline__ void load_if(const T *p, bool on, float (&f)[V]) {
+// The values of a vector: pairs, or a single one.
+template <int V>
+using Values = std::conditional_t<V == 1, float, f2>;
+using dash::f2_sum, dash::fma2, dash::mul2;  // of pairs, beside those of single values
+__device__ __forceinline__ float mul2(float a, float b) { return a * b; }
+__device__ __forceinline__ float fma2(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float f2_sum(float a) { return a; }
+template <typename E>
+__device__ __forceinline__ E both(float a);
+template <>
+__device__ __forceinline__ float both<float>(float a) { return a; }
+template <>
+__device__ __forceinline__ f2 both<f2>(float a) { return f2_of(a, a); }
+__device__ __forceinline__ f2 swapped(f2 v) {
+  float a, b;
+  f2_to(v, a, b);
+  return f2_of(b, a);
+}
+__device__ __forceinline__ float swapped(float v) { return v; }
+template <int V>
+__device__ __forceinline__ void values_of(const float (&f)[V], Values<V> (&v)[V == 1 ? 1 : V / 2]) {
+  if constexpr (V == 1) {
+    v[0] = f[0];
+  } else {
 #pragma unroll
-  for (int e = 0; e < V; ++e) f[e] = on ? to_f32<T>(p[e]) : 0.f;
+    for (int i = 0; i < V / 2; ++i) v[i] = f2_of(f[2 * i], f[2 * i + 1]);
+  }
+}
+// A pair's frequency as the limbs 1 to 3 of the 128-bit fraction of a turn, and the magnitude (NaN for
+// a frequency that is not finite).
+__device__ __forceinline__ uint4 turns_in(const HeadParams &p, int i) {
+  const double f = p.inv_freq[i];
+  const u128 t = turns_of(f);
+  return make_uint4((uint32_t)(t >> 32), (uint32_t)(t >> 64), (uint32_t)(t >> 96),
+                    __float_as_uint(isfinite(f) ? p.magnitude : NAN));
+}
+// Cosine and sine, times the magnitude, of a position's turn.  Of the 192-bit product the bits 96 to
+// 127 are the fraction of a turn; carries from below bit 96 are left out, two units of 2^-32 turns at
+// most.  kShort: the hardware's sine, off by 2^-21, for types that round to 2^-12 and coarser.
+template <bool kShort>
+__device__ __forceinline__ void cos_sin(long long pos, const uint4 &t, float &c, float &s) {
+  const unsigned long long m = pos < 0 ? 0ull - (unsigned long long)pos : (unsigned long long)pos;
+  const uint32_t lo = (uint32_t)m, hi = (uint32_t)(m >> 32);
+  uint32_t turn = lo * t.z + __umulhi(lo, t.y) + hi * t.y + __umulhi(hi, t.x);
+  if (pos < 0) turn = 0u - turn;
+  const float half_turns = (float)(int)turn * (1.0f / 2147483648.0f);
+  if constexpr (kShort) {
+    const float a = half_turns * 3.14159265358979f;
+    c = __cosf(a), s = __sinf(a);
+  } else {
+    sincospif(half_turns, &s, &c);
+  }
+  const float by = __uint_as_float(t.w);
+  c *= by, s *= by;
+}
+template <typename E>
+__device__ __forceinline__ float value_of(const E *v, int e) {
+  if constexpr (sizeof(E) == 4) {
+    return v[e];
+  } else {
+    float x, y;
+    f2_to(v[e >> 1], x, y);
+    return e & 1 ? y : x;
+  }
 }
 
-// The V pairs of two vectors turned by (cos, sin).
-template <int V, bool kHalf>
-__device__ __forceinline__ void turn_pairs(float (&x)[V], float (&y)[V], const float2 (&cs)[V]) {
+// What a turn multiplies a vector pair's values and their partners by: the partner of a value is the
+// other vector's (half layout, single elements) or its neighbour.
+template <int V>
+struct Turn {
+  static constexpr int C = V == 1 ? 1 : V / 2;
+  Values<V> own0[C], other0[C], own1[C], other1[C];
+};
+template <int V, bool kAcross>
+__device__ __forceinline__ void turn_by(const Turn<V> &t, Values<V> (&x)[Turn<V>::C],
+                                        Values<V> (&y)[Turn<V>::C]) {
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-    constexpr bool kAcross = kHalf || V == 1;
-    float &a = kAcross ? x[e] : (2 * e < V ? x[(2 * e) % V] : y[(2 * e) % V]);
-    float &d = kAcross ? y[e] : (2 * e < V ? x[(2 * e + 1) % V] : y[(2 * e + 1) % V]);
-    const float na = fmaf(a, cs[e].x, -__fmul_rn(d, cs[e].y));
-    d = fmaf(d, cs[e].x, __fmul_rn(a, cs[e].y));
-    a = na;
+  for (int i = 0; i < Turn<V>::C; ++i) {
+    const auto a = x[i], b = y[i];
+    x[i] = fma2(kAcross ? b : swapped(a), t.other0[i], mul2(a, t.own0[i]));
+    y[i] = fma2(kAcross ? a : swapped(b), t.other1[i], mul2(b, t.own1[i]));
   }
 }
 
 // Heads on their way to a group, in a ring of its own in shared memory (single elements are loaded
-// when they are needed).
+// when they are needed).  More of them in flight is not faster: of 2 x 8192 tokens the forward takes
+// 70 us with 2 and 80 us with 3, the backward 107 us with 2, 3 and 4.
 template <int V, int R, bool kBack>
-constexpr int kRingStages = V == 1 ? 0 : (kBack ? 4 : 6) / R;
+constexpr int kRingStages = V == 1 ? 0 : kBack ? 3 : 2;
 template <int V, int R, bool kBack>
 constexpr int kRingBytes = kRingStages<V, R, kBack> * (kBack ? 4 : 2) * R * kThreads * 16;
 
@@ -90,9 +161,12 @@ __global__ void __launch_bounds__(kThreads, kBack ? kBackPerSm : kForwardPerSm)
     heads_kernel(const __grid_constant__ HeadParams p) {
   constexpr int N = kRingStages<V, R, kBack>, kVecs = (kBack ? 4 : 2) * R;
   extern __shared__ uint4 shared[];
-  uint4 *ring = shared + threadIdx.x;                                     // [N][kVecs][kThreads]
-  u128 *turns = reinterpret_cast<u128 *>(shared + N * kVecs * kThreads);  // [rot / 2]
-  float *by = reinterpret_cast<float *>(turns + p.rot / 2);  // magnitude, NaN for a bad frequency
+  uint4 *ring = shared + threadIdx.x;                // [N][kVecs][kThreads]
+  // what the lanes need for a token, by element of their vectors and then by lane, so that a warp's
+  // reads meet no bank twice: frequencies of pairs, weights of both vectors
+  uint4 *turns = shared + N * kVecs * kThreads;                   // [V][turning units]
+  float *weights = reinterpret_cast<float *>(turns + p.rot / 2);  // [2][V / W][units][W]
+  constexpr int W = V == 1 ? 1 : 4;
   const int cta = blockIdx.x;
   const int k = p.nparts > 2 && cta >= p.part[2].cta0   ? 2
                 : p.nparts > 1 && cta >= p.part[1].cta0 ? 1
@@ -110,208 +184,242 @@ __global__ void __launch_bounds__(kThreads, kBack ? kBackPerSm : kForwardPerSm)
     has0[r] = u < q.units && e0[r] < q.D;
     has1[r] = u < q.units && e1[r] < q.D;
   }
-  const int per_warp = 32 / G, per_cta = kThreads / G;
-  const long long items = p.tokens * q.blocks, step = (long long)q.ctas * per_cta;
-  // all lanes of a warp go round together, as they meet in the shuffles
-  const long long begin =
-      (long long)(cta - q.cta0) * per_cta + (threadIdx.x >> 5) * per_warp;
-  const int mine = (threadIdx.x & 31) / G;
+  // `across` groups of a warp take neighbouring heads of a token, the others the next tokens; step i
+  // of block k moves them to heads (k each + i) across and behind.  The warps take blocks of tokens in
+  // turn, so that what is under way at a time lies close together in memory.
+  const int per_cta = kThreads / G, mine = (threadIdx.x & 31) / G, my_head = mine & (q.across - 1);
+  const int my_token = mine / q.across, at_once = 32 / G / q.across;
+  const int steps = q.heads / q.across;
+  const long long xstep = q.xh * q.across, gstep = q.gh * q.across, ostep = q.oh * q.across;
 
-  // where an item's heads lie; `heads` of them are there
   struct Place {
     const T *x, *dy;
-    int heads, b, s;
+    int t, k;  // group of tokens and block
+    int left;  // steps
+    int b, s, h;
+    bool on;   // there is such a token
   };
-  auto place = [&](long long i0) {
-    const long long item = i0 + mine;
-    Place w{static_cast<const T *>(q.x), static_cast<const T *>(q.dy), 0, 0, 0};
-    if (item < items) {
-      const int tok = (int)(item / q.blocks), h0 = (int)(item - (long long)tok * q.blocks) * q.each;
-      w.b = tok / p.S, w.s = tok - w.b * p.S;
-      w.heads = min(q.each, q.heads - h0);
-      w.x += w.b * q.xb + w.s * q.xt + h0 * q.xh;
-      if constexpr (kBack)
-        if (q.normed) w.dy += w.b * q.gb + w.s * q.gt + h0 * q.gh;
-    }
-    return w;
+  // (divisions would take longer than a head)
+  auto place = [&](Place &at) {
+    const uint32_t tok = (uint32_t)at.t * at_once + my_token;
+    at.left = min(q.each, steps - at.k * q.each);
+    at.on = at.t < q.tokens && tok < p.tokens;
+    at.b = 0, at.s = at.on ? (int)tok : 0;
+    if (at.s >= p.S) at.b = at.s / p.S, at.s -= at.b * p.S;
+    at.h = at.on ? at.k * q.each * q.across + my_head : 0;
+    at.x = static_cast<const T *>(q.x) + at.b * q.xb + at.s * q.xt + at.h * q.xh;
+    if constexpr (kBack)
+      at.dy = static_cast<const T *>(q.dy) + at.b * q.gb + at.s * q.gt + at.h * q.gh;
   };
+  auto next_block = [&](Place &at) {
+    at.t += q.dt, at.k += q.dk;
+    if (at.k >= q.blocks) at.k -= q.blocks, ++at.t;
+    place(at);
+  };
+  Place first{};
+  first.t = (cta - q.cta0) * (kThreads / 32) + (threadIdx.x >> 5);
+  first.k = first.t % q.blocks, first.t /= q.blocks;
+  place(first);
   // the head that is brought in next
-  long long ahead0 = begin;
-  int ahead_h = 0;
-  Place ahead = place(begin);
-  auto bring = [&](int slot) {
+  Place ahead = first;
+  int filled = 0;  // the slot it goes to
+  auto bring = [&] {
     if constexpr (N > 0) {
-      const bool live = ahead_h < ahead.heads;
       const uint32_t at =
-          (uint32_t)__cvta_generic_to_shared(ring + slot * kVecs * kThreads);
-      const T *x = ahead.x + ahead_h * q.xh, *dy = ahead.dy + ahead_h * q.gh;
+          (uint32_t)__cvta_generic_to_shared(ring + filled * kVecs * kThreads);
+      filled = filled + 1 == N ? 0 : filled + 1;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        copy16(at + (2 * r) * kThreads * 16, x + e0[r], live && has0[r]);
-        copy16(at + (2 * r + 1) * kThreads * 16, x + e1[r], live && has1[r]);
+        copy16(at + (2 * r) * kThreads * 16, ahead.x + e0[r], ahead.on && has0[r]);
+        copy16(at + (2 * r + 1) * kThreads * 16, ahead.x + e1[r], ahead.on && has1[r]);
         if constexpr (kBack)
           if (q.normed) {
-            copy16(at + (2 * R + 2 * r) * kThreads * 16, dy + e0[r], live && has0[r]);
-            copy16(at + (2 * R + 2 * r + 1) * kThreads * 16, dy + e1[r], live && has1[r]);
+            copy16(at + (2 * R + 2 * r) * kThreads * 16, ahead.dy + e0[r], ahead.on && has0[r]);
+            copy16(at + (2 * R + 2 * r + 1) * kThreads * 16, ahead.dy + e1[r], ahead.on && has1[r]);
           }
       }
       copies_end();
-      if (++ahead_h == q.each) ahead_h = 0, ahead0 += step, ahead = place(ahead0);
+      ahead.x += xstep;
+      if constexpr (kBack) ahead.dy += gstep;
+      if (--ahead.left == 0) next_block(ahead);
     }
   };
 #pragma unroll
-  for (int i = 0; i < N - 1; ++i) bring(i);
+  for (int i = 0; i < N - 1; ++i) bring();
 
-  if (q.turn) {
-    for (int i = threadIdx.x; i < p.rot / 2; i += kThreads) {
-      const double f = p.inv_freq[i];
-      turns[i] = turns_of(f);
-      by[i] = isfinite(f) ? p.magnitude : NAN;
+  if (q.normed) {
+    for (int i = threadIdx.x; i < p.rot / 2; i += kThreads)
+      turns[i % V * q.turn + i / V] = turns_in(p, i);
+    for (int i = threadIdx.x; i < 2 * V * q.units; i += kThreads) {
+      const int part = i / (W * q.units), side = part / (V / W);
+      const int u = i / W % q.units, e = part % (V / W) * W + i % W;
+      const bool split = kHalf && u < q.turn;
+      const int at = (split ? u * V + side * (p.rot / 2) : (2 * u + side) * V) + e;
+      weights[i] = at >= q.D ? 0.f
+                   : !q.w    ? 1.f
+                   : p.wf32  ? static_cast<const float *>(q.w)[at]
+                             : to_f32<T>(static_cast<const T *>(q.w)[at]);
     }
     __syncthreads();
   }
-  float w0[R][V], w1[R][V], s0[kBack ? R : 1][V] = {}, s1[kBack ? R : 1][V] = {};
+  constexpr int C = Turn<V>::C;
+  constexpr bool kAcross = kHalf || V == 1;
+  using E = Values<V>;
+  // of a vector of unit u, which the lane may not have
+  auto weights_of = [&](int side, int u, E (&w)[C]) {
+    if constexpr (V == 1) {
+      w[0] = u < q.units ? weights[side * q.units + u] : 0.f;
+    } else {
+      const uint4 *at = reinterpret_cast<const uint4 *>(weights) + side * (V / 4) * q.units +
+                        (u < q.units ? u : 0);
 #pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      w0[r][e] = w1[r][e] = 1.f;
-      if (q.w && p.wf32) {
-        if (has0[r]) w0[r][e] = static_cast<const float *>(q.w)[e0[r] + e];
-        if (has1[r]) w1[r][e] = static_cast<const float *>(q.w)[e1[r] + e];
-      } else if (q.w) {
-        if (has0[r]) w0[r][e] = to_f32<T>(static_cast<const T *>(q.w)[e0[r] + e]);
-        if (has1[r]) w1[r][e] = to_f32<T>(static_cast<const T *>(q.w)[e1[r] + e]);
+      for (int i = 0; i < V / 4; ++i) {
+        const uint4 v = at[i * q.units];
+        w[2 * i] = f2_of(v.x, v.y), w[2 * i + 1] = f2_of(v.z, v.w);
       }
     }
+  };
+  E s0[kBack ? R : 1][C] = {}, s1[kBack ? R : 1][C] = {};
   const float inv_d = 1.f / (float)q.D;
   int slot = 0;
-  for (long long i0 = begin; i0 < items; i0 += step) {
-    const Place at = place(i0);
-    const int h0 = (int)((i0 + mine) % q.blocks) * q.each;
-    T *out = static_cast<T *>(q.out) + at.b * q.ob + at.s * q.ot + h0 * q.oh;
-    float2 cs[R][V];
-    if (q.turn) {
-      long long pos = p.start + at.s;
-      if (p.pos) {
-        const long long i = at.b * p.pos_b + at.s * p.pos_t;
-        pos = p.pos64 ? static_cast<const long long *>(p.pos)[i]
-                      : (long long)static_cast<const int *>(p.pos)[i];
-      }
+  // forward R, backward R^T
+  Turn<V> turn[R];
+  for (Place at = first; at.t < q.tokens; next_block(at)) {
+    T *row = static_cast<T *>(q.out) + at.b * q.ob + at.s * q.ot + at.h * q.oh;
+    {
+      if (q.normed) {
+        long long pos = p.start + at.s;
+        if (p.pos) {
+          const long long i = at.b * p.pos_b + at.s * p.pos_t;
+          pos = p.pos64 ? static_cast<const long long *>(p.pos)[i]
+                        : (long long)static_cast<const int *>(p.pos)[i];
+        }
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int u = in_group + r * G;
+        for (int r = 0; r < R; ++r) {
+          const int u = in_group + r * G;
+          float own[2][V], other[2][V];  // of the two vectors
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          cs[r][e] = make_float2(1.f, 0.f);
-          if (u < q.turn) {
-            const int pair = u * V + e;
-            const int phase = (int)(uint32_t)(((u128)(__int128)pos * turns[pair]) >> 96);
-            float sn, c;
-            sincospif((float)phase * (1.0f / 2147483648.0f), &sn, &c);
-            cs[r][e] = make_float2(c * by[pair], (kBack ? -sn : sn) * by[pair]);
+          for (int e = 0; e < V; ++e) {
+            float c = 1.f, sn = 0.f;
+            if (u < q.turn) {
+              cos_sin<sizeof(T) == 2>(pos, turns[e * q.turn + u], c, sn);
+              if (kBack) sn = -sn;
+            }
+            // pair e, elements a and b: (a, b) -> (c a - sn b, c b + sn a)
+            const int va = kAcross || 2 * e < V ? 0 : 1, vb = kAcross ? 1 : va;
+            const int a = kAcross ? e : (2 * e) % V, b = kAcross ? e : a + 1;
+            own[va][a] = own[vb][b] = c;
+            other[va][a] = -sn, other[vb][b] = sn;
           }
+          values_of<V>(own[0], turn[r].own0);
+          values_of<V>(own[1], turn[r].own1);
+          values_of<V>(other[0], turn[r].other0);
+          values_of<V>(other[1], turn[r].other1);
         }
       }
     }
-    for (int h = 0; h < q.each; ++h) {
-      float x0[R][V], x1[R][V], g0[kBack ? R : 1][V], g1[kBack ? R : 1][V];
-      const bool live = h < at.heads;
-      T *row = out + h * q.oh;
+    for (int left = at.left; left > 0; --left, row += ostep, at.x += xstep, at.dy += gstep) {
+      E x0[R][C], x1[R][C], g0[kBack ? R : 1][C], g1[kBack ? R : 1][C];
       if constexpr (N > 0) {
-        bring(slot == 0 ? N - 1 : slot - 1);
+        bring();
         copies_wait<N - 1>();
         const uint4 *v = ring + slot * kVecs * kThreads;
         slot = slot + 1 == N ? 0 : slot + 1;
         if (!q.normed) {  // (a part's: the same for the whole CTA)
 #pragma unroll
           for (int r = 0; r < R; ++r) {
-            if (live && has0[r]) *reinterpret_cast<uint4 *>(row + e0[r]) = v[2 * r * kThreads];
-            if (live && has1[r]) *reinterpret_cast<uint4 *>(row + e1[r]) = v[(2 * r + 1) * kThreads];
+            if (at.on && has0[r]) *reinterpret_cast<uint4 *>(row + e0[r]) = v[2 * r * kThreads];
+            if (at.on && has1[r]) *reinterpret_cast<uint4 *>(row + e1[r]) = v[(2 * r + 1) * kThreads];
           }
           continue;
         }
-        auto take = [&](int i, float (&f)[V]) {
-          const uint4 raw = v[i * kThreads];
-          unpack<T, V>(*reinterpret_cast<const Pack<T, V> *>(&raw), f);
-        };
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          take(2 * r, x0[r]);
-          take(2 * r + 1, x1[r]);
+          unpack2<T>(v[2 * r * kThreads], x0[r]);
+          unpack2<T>(v[(2 * r + 1) * kThreads], x1[r]);
           if constexpr (kBack) {
-            take(2 * R + 2 * r, g0[r]);
-            take(2 * R + 2 * r + 1, g1[r]);
+            unpack2<T>(v[(2 * R + 2 * r) * kThreads], g0[r]);
+            unpack2<T>(v[(2 * R + 2 * r + 1) * kThreads], g1[r]);
           }
         }
       } else {
-        const T *x = at.x + h * q.xh;
-        if (!q.normed) {
-#pragma unroll
-          for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-              if (live && has0[r]) row[e0[r] + e] = x[e0[r] + e];
-              if (live && has1[r]) row[e1[r] + e] = x[e1[r] + e];
-            }
-          continue;
-        }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          load_if<T, V>(x + e0[r], live && has0[r], x0[r]);
-          load_if<T, V>(x + e1[r], live && has1[r], x1[r]);
+          const bool on0 = at.on && has0[r], on1 = at.on && has1[r];
+          if (!q.normed) {
+            if (on0) row[e0[r]] = at.x[e0[r]];
+            if (on1) row[e1[r]] = at.x[e1[r]];
+            continue;
+          }
+          x0[r][0] = on0 ? to_f32<T>(at.x[e0[r]]) : 0.f;
+          x1[r][0] = on1 ? to_f32<T>(at.x[e1[r]]) : 0.f;
           if constexpr (kBack) {
-            load_if<T, V>(at.dy + h * q.gh + e0[r], live && has0[r], g0[r]);
-            load_if<T, V>(at.dy + h * q.gh + e1[r], live && has1[r], g1[r]);
+            g0[r][0] = on0 ? to_f32<T>(at.dy[e0[r]]) : 0.f;
+            g1[r][0] = on1 ? to_f32<T>(at.dy[e1[r]]) : 0.f;
           }
         }
+        if (!q.normed) continue;
       }
-      float ss = 0.f, sg = 0.f;
+      E ss[2] = {both<E>(0.f), both<E>(0.f)}, sg[2] = {both<E>(0.f), both<E>(0.f)};
 #pragma unroll
       for (int r = 0; r < R; ++r) {
+        E w0[C], w1[C];
         if constexpr (kBack) {
-          if (in_group + r * G < q.turn) turn_pairs<V, kHalf>(g0[r], g1[r], cs[r]);
+          weights_of(0, in_group + r * G, w0), weights_of(1, in_group + r * G, w1);
+          if (in_group + r * G < q.turn) turn_by<V, kAcross>(turn[r], g0[r], g1[r]);
         }
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          ss = fmaf(x0[r][e], x0[r][e], ss);
-          ss = fmaf(x1[r][e], x1[r][e], ss);
+        for (int i = 0; i < C; ++i) {
+          ss[0] = fma2(x0[r][i], x0[r][i], ss[0]);
+          ss[1] = fma2(x1[r][i], x1[r][i], ss[1]);
           if constexpr (kBack) {
-            sg = fmaf(g0[r][e] * w0[r][e], x0[r][e], sg);
-            sg = fmaf(g1[r][e] * w1[r][e], x1[r][e], sg);
+            sg[0] = fma2(mul2(g0[r][i], w0[i]), x0[r][i], sg[0]);
+            sg[1] = fma2(mul2(g1[r][i], w1[i]), x1[r][i], sg[1]);
           }
         }
       }
-      for (int o = G >> 1; o > 0; o >>= 1) {
-        ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if constexpr (kBack) sg += __shfl_xor_sync(0xffffffffu, sg, o);
-      }
-      const float rstd = live ? rsqrtf(fmaf(ss, inv_d, p.eps)) : 0.f;
-      if constexpr (kBack) {
-        const float mean = rstd * rstd * (sg * inv_d);  // mean(w dz x^) rstd, x^ = x rstd
+      float sum = f2_sum(ss[0]) + f2_sum(ss[1]), sum_g = kBack ? f2_sum(sg[0]) + f2_sum(sg[1]) : 0.f;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            s0[r][e] = fmaf(g0[r][e], x0[r][e] * rstd, s0[r][e]);
-            s1[r][e] = fmaf(g1[r][e], x1[r][e] * rstd, s1[r][e]);
-            g0[r][e] = rstd * fmaf(-x0[r][e], mean, g0[r][e] * w0[r][e]);
-            g1[r][e] = rstd * fmaf(-x1[r][e], mean, g1[r][e] * w1[r][e]);
-          }
-          if (live && has0[r]) store_pack<T, V>(row + e0[r], pack<T, V>(g0[r]));
-          if (live && has1[r]) store_pack<T, V>(row + e1[r], pack<T, V>(g1[r]));
+      for (int o = 16; o > 0; o >>= 1)
+        if (o < G) {
+          sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          if constexpr (kBack) sum_g += __shfl_xor_sync(0xffffffffu, sum_g, o);
         }
-      } else {
+      const float rstd = at.on ? rsqrtf(fmaf(sum, inv_d, p.eps)) : 0.f;
+      const E rs = both<E>(rstd);
+      // -mean(w dz x^) rstd, x^ = x rstd
+      const E mean = both<E>(-rstd * rstd * (sum_g * inv_d));
+      auto store = [&](T *to, const E (&f)[C], bool on) {
+        if (!on) return;
+        if constexpr (V == 1)
+          *to = from_f32<T>(f[0]);
+        else
+          *reinterpret_cast<uint4 *>(to) = pack2<T>(f);
+      };
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
+      for (int r = 0; r < R; ++r) {
+        E(&a)[C] = x0[r], (&b)[C] = x1[r], w0[C], w1[C];
+        weights_of(0, in_group + r * G, w0), weights_of(1, in_group + r * G, w1);
+        if constexpr (kBack) {
+          E(&ga)[C] = g0[r], (&gb)[C] = g1[r];
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            x0[r][e] *= rstd * w0[r][e];
-            x1[r][e] *= rstd * w1[r][e];
+          for (int i = 0; i < C; ++i) {
+            s0[r][i] = fma2(ga[i], mul2(a[i], rs), s0[r][i]);
+            s1[r][i] = fma2(gb[i], mul2(b[i], rs), s1[r][i]);
+            ga[i] = mul2(rs, fma2(a[i], mean, mul2(ga[i], w0[i])));
+            gb[i] = mul2(rs, fma2(b[i], mean, mul2(gb[i], w1[i])));
           }
-          if (in_group + r * G < q.turn) turn_pairs<V, kHalf>(x0[r], x1[r], cs[r]);
-          if (live && has0[r]) store_pack<T, V>(row + e0[r], pack<T, V>(x0[r]));
-          if (live && has1[r]) store_pack<T, V>(row + e1[r], pack<T, V>(x1[r]));
+          store(row + e0[r], ga, at.on && has0[r]);
+          store(row + e1[r], gb, at.on && has1[r]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < C; ++i) {
+            a[i] = mul2(mul2(a[i], rs), w0[i]);
+            b[i] = mul2(mul2(b[i], rs), w1[i]);
+          }
+          if (in_group + r * G < q.turn) turn_by<V, kAcross>(turn[r], a, b);
+          store(row + e0[r], a, at.on && has0[r]);
+          store(row + e1[r], b, at.on && has1[r]);
         }
       }
     }
@@ -327,8 +435,8 @@ __global__ void __launch_bounds__(kThreads, kBack ? kBackPerSm : kForwardPerSm)
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        if (has0[r]) sums[group * q.D + e0[r] + e] = s0[r][e];
-        if (has1[r]) sums[group * q.D + e1[r] + e] = s1[r][e];
+        if (has0[r]) sums[group * q.D + e0[r] + e] = value_of(s0[r], e);
+        if (has1[r]) sums[group * q.D + e1[r] + e] = value_of(s1[r], e);
       }
     __syncthreads();
     for (int c = threadIdx.x; c < q.D; c += kThreads) {
@@ -372,8 +480,7 @@ int lanes_of(int units) {
   while (g < units && g < 32) g *= 2;
   return g;
 }
-// Shares out the CTAs among the parts, by the bytes that they move, and the heads of a token among
-// groups.
+// Shares out the CTAs among the parts, by the bytes that they move.
 void deal(HeadParams &p, int V, bool back) {
   auto cost = [&](const HeadPart &q) {
     return (long long)q.heads * q.D * (back && q.normed ? 3 : 2);
@@ -386,18 +493,26 @@ void deal(HeadParams &p, int V, bool back) {
     q.turn = q.normed ? p.rot / (2 * V) : 0;
     q.units = q.turn + (q.D / V - 2 * q.turn + 1) / 2;
     q.lanes = lanes_of(q.units);
-    const int groups = kThreads / q.lanes;
     long long share = kSms * (back ? kBackPerSm : kForwardPerSm) * cost(q) / all;
     if (share < 1) share = 1;
-    // as many heads of a token to a group as leave every group something, 16 at most: cosines and
-    // sines are formed once for them
-    long long each = p.tokens * q.heads / (share * groups);
+    const int per_warp = 32 / q.lanes, warps = kThreads / 32;
+    // neighbouring heads side by side, as far as 8 steps through a token's heads are left: its cosines
+    // and sines serve for them
+    q.across = 1;
+    while (2 * q.across <= per_warp && q.heads % (2 * q.across) == 0 && q.heads / (2 * q.across) >= 8)
+      q.across *= 2;
+    const int steps = q.heads / q.across, at_once = per_warp / q.across;
+    const long long groups = (p.tokens + at_once - 1) / at_once;
+    // as many of them at a time as leave every warp something, 8 at most
+    long long each = groups * steps / (share * warps);
     each = each < 1 ? 1 : each > 16 ? 16 : each;
-    if (each > q.heads) each = q.heads;
-    q.blocks = (int)((q.heads + each - 1) / each);
-    q.each = (q.heads + q.blocks - 1) / q.blocks;
-    const long long want = (p.tokens * q.blocks + groups - 1) / groups;
+    if (each > steps) each = steps;
+    q.blocks = (int)((steps + each - 1) / each);
+    q.each = (int)((steps + q.blocks - 1) / q.blocks);
+    const long long want = (groups * q.blocks + warps - 1) / warps;
+    q.tokens = (int)groups;
     q.ctas = (int)(want < share ? want : share);
+    q.dt = q.ctas * warps / q.blocks, q.dk = q.ctas * warps % q.blocks;
     q.cta0 = cta;
     cta += q.ctas;
   }
@@ -407,7 +522,9 @@ int ctas_of(const HeadParams &p) { return p.part[p.nparts - 1].cta0 + p.part[p.n
 template <typename T, int V, int R, bool kHalf, bool kBack>
 cudaError_t launch(const HeadParams &p, cudaStream_t s) {
   constexpr int kRing = kRingBytes<V, R, kBack>;
-  size_t smem = kRing + (size_t)p.rot / 2 * 20;
+  int units = 0;
+  for (int i = 0; i < p.nparts; ++i) units = p.part[i].units > units ? p.part[i].units : units;
+  size_t smem = kRing + (size_t)p.rot / 2 * 16 + 2 * V * 4 * (size_t)units;
   if (kBack)
     for (int i = 0; i < p.nparts; ++i) {
       const size_t sums = (size_t)(kThreads / p.part[i].lanes) * p.part[i].D * 4;
@@ -415,7 +532,7 @@ cudaError_t launch(const HeadParams &p, cudaStream_t s) {
     }
   // (kMaxD / 2 pairs at most)
   const cudaError_t e =
-      allow_smem<heads_kernel<T, V, R, kHalf, kBack>>(kRing + kMaxD / 2 * 20 + 16384);
+      allow_smem<heads_kernel<T, V, R, kHalf, kBack>>(kRing + kMaxD / 2 * 16 + 16384 + 8 * kMaxD);
   if (e != cudaSuccess) return e;
   heads_kernel<T, V, R, kHalf, kBack><<<ctas_of(p), kThreads, smem, s>>>(p);
   return cudaGetLastError();
@@ -502,7 +619,7 @@ dash_status_t fill(HeadParams &p, bool &wide, Lay &lay, const dash_rope_part_t *
     if (q.D > kMaxD) return DASH_ERR_UNSUPPORTED;
   }
   if (!turned) return DASH_ERR_INVALID;
-  if ((long long)B * S >= (1LL << 31)) return DASH_ERR_UNSUPPORTED;
+  if ((long long)B * S >= (1LL << 31) - (1 << 16)) return DASH_ERR_UNSUPPORTED;
   for (int i = 0; i < nparts; ++i)
     if ((long long)parts[i].heads * parts[i].D >= (1LL << 28)) return DASH_ERR_UNSUPPORTED;
   // an output is its own input (the gradient), as it lies, or what nothing else is
