@@ -70,23 +70,70 @@ Product plan(int M, int N, int K, int parts, int outs, bool gated) {
   double least = 0;
   for (int bn = 256; bn >= 128; bn -= 128) {
     Product p{M, N, K, parts, outs, gated, bn};
-    const long long tiles = p.tiles(), rounds = tiles / kPairs, rest = tiles - rounds * kPairs;
+    const long long tiles = p.tiles(), rounds = tiles / kPairs;
     if (tiles >= (1LL << 28)) continue;
     const int blocks = p.nk() * parts;
     const double block = bn == 256 ? 1.0 : 0.7;
-    p.whole = (int)(rounds * kPairs);
-    for (int s = 1; s <= kMaxSplits && s <= blocks; ++s) {
-      p.per = ceil_div(blocks, s);
-      if (ceil_div(blocks, p.per) != s) continue;  // no split is empty
-      if (s > 1 && (rest == 0 || rest * s > 4 * kPairs)) break;
-      double t = rounds * (blocks * block + 3);
-      t += (rest * s + kPairs - 1) / kPairs * (p.per * block + 3);
-      if (s > 1) t += 10 + 8.0 * rest * s * (M < kDenseM ? M : kDenseM) * bn / 1.8e6;
-      if (least == 0 || t < 0.98 * least) {
-        least = t;
-        best = p;
-        best.splits = s;
+    // whole rounds stay whole, or (a few rounds) every tile is split
+    for (int all = 0; all <= (rounds > 0 && rounds < 4); ++all) {
+      p.whole = all ? 0 : (int)(rounds * kPairs);
+      const long long cut = tiles - p.whole;
+      for (int s = 1; s <= kMaxSplits && s <= blocks; ++s) {
+        p.per = ceil_div(blocks, s);
+        if (ceil_div(blocks, p.per) != s) continue;  // no split is empty
+        if (s > 1 && (cut == 0 || cut * s > 8 * kPairs)) break;
+        double t = (double)(p.whole / kPairs) * (blocks * block + 3);
+        t += (double)((cut * s + kPairs - 1) / kPairs) * (p.per * block + 3);
+        if (s > 1) t += 10 + 8.0 * cut * s * (M < kDenseM ? M : kDenseM) * bn / 1.8e6;
+        if (least == 0 || t < 0.98 * least) {
+          least = t;
+          best = p;
+          best.splits = s;
+        }
       }
+    }
+  }
+  return best;
+}
+
+// How a forward of few rows goes: tiles of 128 outputs, each shared by a cluster.  Counted in blocks of
+// an SM's share: the memory's pace (what the busiest SM would have if all had the same), or what the
+// busiest SM has at the pace of one SM, 1.4 times its share of the memory's (112 SMs reach 6.2 TB/s);
+// 3 for a round of CTAs, 1 for each that an SM holds at once, 2 for sums through a cluster.  Measured, one
+// row x 4096 x 14336 gated: 112 CTAs alone 38 us, 224 in pairs 39, 448 in fours 42 to 55, in eights 71;
+// 17 x 14336 x 4096: 32 CTAs 58, 64 in pairs 32, 128 in fours 23, 256 in eights 22.
+constexpr int kMaxCluster = 8;
+// CTAs that a GB300 holds at once, 1 to 4 on an SM, in clusters of 1, 2, 4 and 8
+// (cudaOccupancyMaxActiveClusters): clusters do not fill every group of SMs.
+constexpr int kFewSlots[4][4] = {
+    {152, 152, 144, 120}, {304, 304, 296, 288}, {456, 456, 440, 408}, {608, 608, 592, 592}};
+struct Few {
+  int split = 0, per, stages, stage, smem, tmem, cols;
+};
+Few plan_few(int M, int N, int K, bool gated) {
+  Few best;
+  const int nk = ceil_div(K, kDenseK), tiles = ceil_div(N, 128);
+  Few f;
+  f.cols = (int)up(M, 16);
+  f.stage = (gated ? 2 : 1) * 128 * kDenseK * 2 + f.cols * 128;
+  f.tmem = 32;
+  while (f.tmem < (gated ? 2 : 1) * f.cols) f.tmem *= 2;
+  const int sums = (gated ? 2 : 1) * f.cols * 512;
+  double least = 0;
+  for (int i = 0; 1 << i <= kMaxCluster && 1 << i <= nk; ++i) {
+    f.split = 1 << i;
+    f.per = ceil_div(nk, f.split);
+    if (ceil_div(nk, f.per) != f.split) continue;  // every CTA has a part
+    const long long ctas = (long long)tiles * f.split;
+    for (int at_once = 1; at_once <= 4 && at_once * f.tmem <= 512; ++at_once) {
+      const int room = 224 * 1024 / at_once - 1536;
+      f.stages = room / f.stage < kFewStages ? room / f.stage : kFewStages;
+      f.smem = f.stages * f.stage > sums ? f.stages * f.stage : sums;
+      if (f.stages < 2 || f.smem > room) break;
+      const long long rounds = (ctas + kFewSlots[at_once - 1][i] - 1) / kFewSlots[at_once - 1][i];
+      const double all = (double)tiles * nk / kFewSlots[0][0], one = rounds * at_once * f.per / 1.4;
+      const double t = (all > one ? all : one) + 3.0 * rounds + at_once + (i > 0 ? 2 : 0);
+      if (least == 0 || t < least) least = t, best = f;
     }
   }
   return best;
@@ -119,7 +166,7 @@ bool place(Rows &r, Arena &arena, cudaStream_t s) {
 // ask for them, otherwise empty).
 dash_status_t launch(const Product &p, const Rows (&a)[2], const Rows (&b)[2], bool a_mn, bool b_mn,
                      bool a_out, bool b_out, const DenseEpilogue &e, void *y1, long long y1s,
-                     float *part, void *workspace, bool f16, int sms, cudaStream_t s) {
+                     float *part, void *workspace, bool clear, bool f16, int sms, cudaStream_t s) {
   CUtensorMap ta[2], tb[2];
   for (int i = 0; i < 2; ++i)
     if (!make_rows_map(&ta[i], a[i].at ? a[i] : a[0], a_mn ? 64 : 128, f16) ||
@@ -130,6 +177,7 @@ dash_status_t launch(const Product &p, const Rows (&a)[2], const Rows (&b)[2], b
   d.y1 = y1, d.y1s = y1s;
   d.part = part;
   d.status = static_cast<uint32_t *>(workspace);
+  d.clear = clear;
   d.wait_ns = g_wait_ns.load();
   d.M = p.M, d.N = p.N;
   d.mt = p.mt(), d.nt = p.nt(), d.bn = p.bn;
@@ -143,7 +191,7 @@ dash_status_t launch(const Product &p, const Rows (&a)[2], const Rows (&b)[2], b
 bool vec_rows(const void *p, long long stride) { return !p || (aligned16(p) && stride % 8 == 0); }
 
 // ------------------------------------------------------------------ forward
-dash_status_t check_fwd(const dash_dense_fwd_t *a, Product &p, Rows &x, Rows (&w)[2]) {
+dash_status_t check_fwd(const dash_dense_fwd_t *a, Product &p, Few &few, Rows &x, Rows (&w)[2]) {
   if (!a || !a->x || !a->w || !a->y || a->M <= 0 || a->K <= 0 || a->N <= 0) return DASH_ERR_INVALID;
   if (a->order != DASH_DENSE_KN && a->order != DASH_DENSE_NK) return DASH_ERR_INVALID;
   if (a->act < DASH_ACT_NONE || a->act > DASH_ACT_SILU) return DASH_ERR_INVALID;
@@ -159,6 +207,10 @@ dash_status_t check_fwd(const dash_dense_fwd_t *a, Product &p, Rows &x, Rows (&w
   if (a->M > kMaxSize || a->K > kMaxSize || a->N > kMaxSize) return DASH_ERR_UNSUPPORTED;
   p = plan(a->M, a->N, a->K, 1, 1, a->w_gate != nullptr);
   if (!sizes_ok(p)) return DASH_ERR_UNSUPPORTED;
+  if (a->M <= kFewRows) {
+    few = plan_few(a->M, a->N, a->K, a->w_gate != nullptr);
+    p.splits = 1;  // (no partial sums in memory)
+  }
   x = Rows(a->x, a->x_stride, a->M, a->K);
   w[0] = Rows(a->w, a->w_stride, kn ? a->K : a->N, kn ? a->N : a->K);
   w[1] = Rows(a->w_gate, a->w_gate_stride, w[0].rows, w[0].cols);
@@ -235,16 +287,18 @@ dash_status_t dash_dense_withhold(int block) {
 
 size_t dash_dense_fwd_workspace_bytes(const dash_dense_fwd_t *args) {
   dash::Product p;
+  dash::Few few;
   dash::Rows x, w[2];
-  return dash::check_fwd(args, p, x, w) == DASH_OK ? dash::need_fwd(p, x, w) : 0;
+  return dash::check_fwd(args, p, few, x, w) == DASH_OK ? dash::need_fwd(p, x, w) : 0;
 }
 
 dash_status_t dash_dense_fwd(const dash_dense_fwd_t *a, void *workspace, size_t workspace_bytes,
                              dash_stream_t stream) {
   using namespace dash;
   Product p;
+  Few few;
   Rows xs, w[2];
-  dash_status_t st = check_fwd(a, p, xs, w);
+  dash_status_t st = check_fwd(a, p, few, xs, w);
   if (st != DASH_OK) return st;
   const size_t need = need_fwd(p, xs, w);
   if (!workspace || !aligned16(workspace) || workspace_bytes < need) return DASH_ERR_WORKSPACE;
@@ -261,7 +315,6 @@ dash_status_t dash_dense_fwd(const dash_dense_fwd_t *a, void *workspace, size_t 
   DevInfo dev;
   if ((st = device_info(&dev)) != DASH_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(workspace, 0, kStatusBytes, s) != cudaSuccess) return DASH_ERR_CUDA;
   Arena arena(workspace);
   if (!place(xs, arena, s) || !place(w[0], arena, s) || !place(w[1], arena, s))
     return DASH_ERR_CUDA;
@@ -273,9 +326,26 @@ dash_status_t dash_dense_fwd(const dash_dense_fwd_t *a, void *workspace, size_t 
   e.act = a->act, e.gated = p.gated;
   e.vec = vec_rows(e.y, e.ys) && vec_rows(e.z, a->N) && vec_rows(e.g, a->N) &&
           vec_rows(e.residual, e.rs) && vec_rows(e.bias, 0) && vec_rows(e.bias_gate, 0);
+  if (few.split) {
+    const bool f16 = a->dtype == DASH_FP16, mn = a->order == DASH_DENSE_KN;
+    CUtensorMap tw[2], tx;
+    for (int i = 0; i < 2; ++i)
+      if (!make_rows_map(&tw[i], w[i].at ? w[i] : w[0], mn ? 64 : 128, f16)) return DASH_ERR_CUDA;
+    if (!make_rows_map(&tx, xs, few.cols, f16)) return DASH_ERR_CUDA;
+    DenseFewParams d{};
+    d.e = e;
+    d.status = static_cast<uint32_t *>(workspace);
+    d.wait_ns = g_wait_ns.load();
+    d.M = p.M, d.N = p.N, d.nk = p.nk();
+    d.cols = few.cols, d.split = few.split, d.per = few.per;
+    d.stages = few.stages, d.stage = few.stage, d.smem = few.smem, d.tmem = few.tmem;
+    d.w_mn = mn;
+    d.withhold = g_dense_withhold.load();
+    return launch_dense_few(f16, tw[0], tw[1], tx, d, s) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
+  }
   const Rows x[2] = {xs, Rows()};
   return launch(p, x, w, false, a->order == DASH_DENSE_KN, false, false, e, nullptr, 0, part,
-                workspace, a->dtype == DASH_FP16, dev.sms, s);
+                workspace, true, a->dtype == DASH_FP16, dev.sms, s);
 }
 
 size_t dash_dense_bwd_workspace_bytes(const dash_dense_bwd_t *args) {
@@ -328,7 +398,6 @@ dash_status_t dash_dense_bwd(const dash_dense_bwd_t *a, void *workspace, size_t 
     if (b.grads) g.z = a->z, g.g = a->gate;
     g.dz = dz_at, g.dg = dg_at;
     g.part = sum, g.part_gate = sum_gate;
-    g.status = static_cast<uint32_t *>(workspace);
     g.dys = b.dy.stride, g.zs = g.gs = a->N, g.ds = up(a->N, 8);
     g.M = a->M, g.N = a->N, g.act = a->act, g.chunk = b.chunk;
     g.vec = a->N % 8 == 0 && vec_rows(a->dy, b.dy.stride) && vec_rows(a->z, a->N) &&
@@ -341,10 +410,9 @@ dash_status_t dash_dense_bwd(const dash_dense_bwd_t *a, void *workspace, size_t 
       dz[0] = Rows(dz_at, g.ds, a->M, a->N);
       dz[1] = Rows(dg_at, g.ds, a->M, a->N);
     }
-  } else if (cudaMemsetAsync(workspace, 0, kStatusBytes, s) != cudaSuccess) {
-    return DASH_ERR_CUDA;
   }
-  if (!a->dx && !a->dw) return DASH_OK;
+  if (!a->dx && !a->dw)  // no product clears the status block
+    return cudaMemsetAsync(workspace, 0, kStatusBytes, s) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
   if (!place(dz[0], arena, s) || !place(b.x, arena, s) || !place(b.w[0], arena, s) ||
       !place(b.w[1], arena, s))
     return DASH_ERR_CUDA;
@@ -352,8 +420,8 @@ dash_status_t dash_dense_bwd(const dash_dense_bwd_t *a, void *workspace, size_t 
     DenseEpilogue e{};
     e.y = a->dx, e.ys = a->dx_stride;
     e.vec = vec_rows(e.y, e.ys);
-    st = launch(b.dx, dz, b.w, false, !kn, false, false, e, nullptr, 0, part, workspace, f16,
-                dev.sms, s);
+    st = launch(b.dx, dz, b.w, false, !kn, false, false, e, nullptr, 0, part, workspace, true,
+                f16, dev.sms, s);
     if (st != DASH_OK) return st;
   }
   if (a->dw) {
@@ -362,9 +430,9 @@ dash_status_t dash_dense_bwd(const dash_dense_bwd_t *a, void *workspace, size_t 
     e.vec = vec_rows(e.y, e.ys) && vec_rows(a->dw_gate, a->dw_gate_stride);
     const Rows x[2] = {b.x, Rows()};
     st = kn ? launch(b.dw, x, dz, true, true, false, gated, e, a->dw_gate, a->dw_gate_stride, part,
-                     workspace, f16, dev.sms, s)
+                     workspace, !a->dx, f16, dev.sms, s)
             : launch(b.dw, dz, x, true, true, gated, false, e, a->dw_gate, a->dw_gate_stride, part,
-                     workspace, f16, dev.sms, s);
+                     workspace, !a->dx, f16, dev.sms, s);
   }
   return st;
 }

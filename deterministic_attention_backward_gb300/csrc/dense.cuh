@@ -30,6 +30,7 @@ struct DenseParams {
   long long y1s;
   float *part;               // fp32 sums of the split tiles: [tile][split][256][bn]
   uint32_t *status;
+  int clear;                 // the status block (the first product of a call does)
   unsigned long long wait_ns;
   int M, N;
   int mt, nt, bn;            // tiles; bn columns of a tile's accumulator (gated: half z, half g)
@@ -40,12 +41,26 @@ struct DenseParams {
   int withhold;              // block at which a CTA's loads end, else -1
 };
 
+// A forward of few rows (outputs as in the epilogue above).
+constexpr int kFewRows = 64, kFewStages = 12, kFewSmem = 224 * 1024;
+struct DenseFewParams {
+  DenseEpilogue e;
+  uint32_t *status;
+  unsigned long long wait_ns;
+  int M, N, nk;
+  int cols;            // M rounded up to 16
+  int split, per;      // CTAs of a cluster, blocks of kDenseK of each
+  int stages, stage;   // their number and bytes
+  int smem, tmem;
+  int w_mn;            // the weights' rows are the contraction
+  int withhold;
+};
+
 // dz = dy g act'(z), dgate = dy act(z) and their sums over rows.
 struct DenseGradParams {
   const void *dy, *z, *g;    // z null: dz = dy (and is not written); g null: not gated
   void *dz, *dg;             // null where only the sums are wanted
   float *part, *part_gate;   // [chunks][N]; null where the sums are not wanted
-  uint32_t *status;          // cleared
   long long dys, zs, gs, ds;
   int M, N, act, chunk;      // rows of a chunk
   int vec;
@@ -53,6 +68,8 @@ struct DenseGradParams {
 
 cudaError_t launch_dense(bool f16, const CUtensorMap (&ta)[2], const CUtensorMap (&tb)[2],
                          const DenseParams &p, int sms, cudaStream_t s);
+cudaError_t launch_dense_few(bool f16, const CUtensorMap &tw0, const CUtensorMap &tw1,
+                             const CUtensorMap &tx, const DenseFewParams &p, cudaStream_t s);
 cudaError_t launch_dense_grad(bool f16, const DenseGradParams &p, int chunks, cudaStream_t s);
 // out[n] = sum over chunks, in order (gate: a second row of sums and its output)
 cudaError_t launch_dense_sums(bool f16, const float *part, const float *part_gate, void *out,

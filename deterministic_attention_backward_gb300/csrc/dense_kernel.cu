@@ -54,12 +54,19 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity)
       : "memory");
   return ok != 0;
 }
-// Warp-wide wait (one answer for the whole warp); the limit runs from the 256th try on.
-__device__ __forceinline__ bool wait_pair(uint64_t *bar, uint32_t parity, const Abort &ab) {
-  if (__all_sync(0xffffffffu, try_wait_cluster(bar, parity))) return true;
+// Warp-wide wait (one answer for the whole warp); the limit runs from the 256th try on.  What is
+// waited for comes from this CTA or its partners in the cluster, so that every wait runs out by itself:
+// the status word is only written (its first CTA clears it, long before any limit).
+template <bool kCluster>
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, const Abort &ab) {
+  auto done = [&] {
+    return __all_sync(0xffffffffu, kCluster ? try_wait_cluster(bar, parity)
+                                            : mbar_try_wait(bar, parity));
+  };
+  if (done()) return true;
   uint64_t t0 = 0;
   for (uint32_t it = 1;; ++it) {
-    if (__all_sync(0xffffffffu, try_wait_cluster(bar, parity))) return true;
+    if (done()) return true;
     if ((it & 15u) == 0) {
       int stop = 0;
       if (lane_id() == 0) {
@@ -67,9 +74,7 @@ __device__ __forceinline__ bool wait_pair(uint64_t *bar, uint32_t parity, const 
           stop = 1;
         } else if ((it & 255u) == 0) {
           if (t0 == 0) t0 = globaltimer();
-          if (ab.poll_global()) {
-            stop = 1;
-          } else if (globaltimer() - t0 > ab.limit_ns) {
+          if (globaltimer() - t0 > ab.limit_ns) {
             ab.raise(kErrMbarTimeout);
             stop = 1;
           }
@@ -78,6 +83,12 @@ __device__ __forceinline__ bool wait_pair(uint64_t *bar, uint32_t parity, const 
       if (__shfl_sync(0xffffffffu, stop, 0)) return false;
     }
   }
+}
+__device__ __forceinline__ bool wait_pair(uint64_t *bar, uint32_t parity, const Abort &ab) {
+  return wait_for<true>(bar, parity, ab);
+}
+__device__ __forceinline__ bool wait_local(uint64_t *bar, uint32_t parity, const Abort &ab) {
+  return wait_for<false>(bar, parity, ab);
 }
 // One box into this CTA's shared memory, its bytes counted on a barrier of either CTA; issued by the
 // lane of a converged warp with `lead` set (a lane on its own takes 85 cycles a box).
@@ -109,6 +120,70 @@ __device__ __forceinline__ void alloc_pair(uint32_t *dst) {
 __device__ __forceinline__ void dealloc_pair(uint32_t at) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(512u)
                : "memory");
+}
+// The same of a CTA alone.
+__device__ __forceinline__ void load_box_alone(uint32_t lead, uint32_t dst, const CUtensorMap *map,
+                                               uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];\n\t}\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void mma_alone(uint32_t lead, uint32_t d, uint64_t a, uint64_t b,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\t"
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void commit_alone(uint32_t lead, uint64_t *bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::
+          "r"(smem_u32(bar)),
+      "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void load16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+// Adds the four values at shared address `at` of the cluster's CTAs, in order.
+__device__ __forceinline__ void add_remote(float (&v)[4], uint32_t at, int ctas) {
+  float r[8][4];
+#pragma unroll
+  for (int c = 0; c < 8; ++c)  // (all on their way before the first is needed)
+    if (c < ctas) {
+      uint32_t there;
+      asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(c));
+      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(r[c][0]), "=f"(r[c][1]), "=f"(r[c][2]), "=f"(r[c][3])
+                   : "r"(there)
+                   : "memory");
+    }
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    if (c < ctas)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] += r[c][k];
 }
 // D[tmem of both] (+)= A B^T, issued by the lane with `lead` set of the leader's warp.
 __device__ __forceinline__ void mma_pair(uint32_t lead, uint32_t d, uint64_t a, uint64_t b,
@@ -359,6 +434,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                  const __grid_constant__ CUtensorMap tb0, const __grid_constant__ CUtensorMap tb1,
                  const __grid_constant__ DenseParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
+  if (p.clear && blockIdx.x == 0 && threadIdx.x < kStatusBytes / 4) p.status[threadIdx.x] = 0;
   // (the same for both CTAs, which leave together)
   if (smem_u32(smem) & 1023u) {
     if (threadIdx.x == 0) atomicOr(p.status, kErrSmemAlign);
@@ -576,6 +652,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
+// The epilogue of 4 columns of a row.
+template <typename T>
+__device__ __forceinline__ void finish4(const DenseEpilogue &e, void *y, long long ys, long long row,
+                                        int n, int N, float (&z)[4], float (&g)[4]) {
+  const int left = N - n;
+  if (e.bias) add_cols<T, 4>(e.bias, n, z, left);
+  if (e.z) store_cols<T, 4>(e.z, row * e.zs + n, z, left);
+  activate(e.act, z);
+  if (e.gated) {
+    if (e.bias_gate) add_cols<T, 4>(e.bias_gate, n, g, left);
+    if (e.g) store_cols<T, 4>(e.g, row * e.gs + n, g, left);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) z[k] *= g[k];
+  }
+  if (e.residual) add_cols<T, 4>(e.residual, row * e.rs + n, z, left);
+  store_cols<T, 4>(y, row * ys + n, z, left);
+}
+
 // The splits' sums of the tiles that were split, added in order, and the epilogue; a thread takes 4
 // columns of a row, a CTA's y one tile.
 template <typename T>
@@ -590,6 +684,7 @@ __global__ void __launch_bounds__(256) dense_finish_kernel(const __grid_constant
   float z[4] = {}, g[4] = {};
   const long long stride = (long long)kDenseM * p.bn;
   const float *src = p.part + w.cut * stride + (long long)r * p.bn + c;
+#pragma unroll 4
   for (int s = 0; s < p.splits; ++s, src += stride) {
     const float4 v = *reinterpret_cast<const float4 *>(src);
     z[0] += v.x, z[1] += v.y, z[2] += v.z, z[3] += v.w;
@@ -598,18 +693,144 @@ __global__ void __launch_bounds__(256) dense_finish_kernel(const __grid_constant
       g[0] += u.x, g[1] += u.y, g[2] += u.z, g[3] += u.w;
     }
   }
-  const int left = p.N - n;
-  if (e.bias) add_cols<T, 4>(e.bias, n, z, left);
-  if (e.z) store_cols<T, 4>(e.z, row * e.zs + n, z, left);
-  activate(e.act, z);
-  if (e.gated) {
-    if (e.bias_gate) add_cols<T, 4>(e.bias_gate, n, g, left);
-    if (e.g) store_cols<T, 4>(e.g, row * e.gs + n, g, left);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) z[k] *= g[k];
+  finish4<T>(e, w.out ? p.y1 : e.y, w.out ? p.y1s : e.ys, row, n, p.N, z, g);
+}
+
+// ------------------------------------------------------------------ few rows
+// Up to 64 rows of x: bound by the weights' way through the SMs.  The weights are the rows of the tensor
+// core's tile here (128 outputs), x its columns, so that nothing but x is read that is not needed.  A
+// cluster shares a tile: every CTA forms the sums over its part of the contraction, leaves them in its
+// shared memory, and finishes its share of the outputs from all CTAs' sums, added in order.
+// 4 warps: 0 brings in the operands, 1 issues the products, 2 holds TMEM; all finish.
+constexpr int kFewThreads = 128;
+template <typename T>
+__global__ void __launch_bounds__(kFewThreads)
+    dense_few_kernel(const __grid_constant__ CUtensorMap tw0, const __grid_constant__ CUtensorMap tw1,
+                     const __grid_constant__ CUtensorMap tx, const __grid_constant__ DenseFewParams p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ uint64_t full[kFewStages], empty[kFewStages], done;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  const int warp = warp_id(), lane = lane_id();
+  const uint32_t rank = cluster_rank();
+  const int tile = blockIdx.x / p.split;
+  if (blockIdx.x == 0 && threadIdx.x < kStatusBytes / 4) p.status[threadIdx.x] = 0;
+  const Abort ab{&s_abort, p.status, p.wait_ns};
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&done, 1);
+    s_abort = smem_u32(smem) & 1023u ? 1 : 0;
+    if (s_abort) atomicOr(p.status, kErrSmemAlign);
+    fence_mbar_init();
   }
-  if (e.residual) add_cols<T, 4>(e.residual, row * e.rs + n, z, left);
-  store_cols<T, 4>(w.out ? p.y1 : e.y, row * (w.out ? p.y1s : e.ys) + n, z, left);
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tw0);
+    tma_prefetch_desc(&tx);
+  }
+  if (warp == 2) {
+    tmem_alloc(&s_tmem, p.tmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  const bool gated = p.e.gated;
+  const int k0 = (int)rank * p.per, k1 = min(k0 + p.per, p.nk);
+  const int n0 = tile * 128;
+  const uint32_t base = smem_u32(smem), xoff = gated ? 2 * kABytes : kABytes;
+
+  bool ok = !s_abort;
+  if (ok && warp == 0) {
+    const uint32_t lead = elect_one(), bytes = xoff + p.cols * 128;
+    int s = 0, it = 0;
+    uint32_t ph = 1;
+    for (int k = k0; k < k1; ++k, ++it) {
+      if (it == p.withhold || !wait_local(&empty[s], ph, ab)) {
+        ok = false;
+        break;
+      }
+      const uint32_t at = base + s * p.stage, bar = smem_u32(&full[s]);
+      expect_l(lead, bar, bytes);
+      for (int g = 0; g <= (int)gated; ++g) {
+        const CUtensorMap *map = g ? &tw1 : &tw0;
+        const uint32_t to = at + g * kABytes;
+        if (p.w_mn) {
+          load_box_alone(lead, to, map, bar, n0, k * kDenseK);
+          load_box_alone(lead, to + kMnBox, map, bar, n0 + 64, k * kDenseK);
+        } else {
+          load_box_alone(lead, to, map, bar, k * kDenseK, n0);
+        }
+      }
+      load_box_alone(lead, at + xoff, &tx, bar, k * kDenseK, 0);
+      if (++s == p.stages) s = 0, ph ^= 1;
+    }
+    if (!ok)  // leave no copy in flight into shared memory
+      for (int j = max(0, it - p.stages); j < it; ++j)
+        mbar_wait_drain(&full[j % p.stages], (j / p.stages) & 1, 100000000ull);
+  } else if (ok && warp == 1) {
+    const uint32_t kind = std::is_same<T, __half>::value ? 0u : (1u << 7) | (1u << 10);
+    const uint32_t idesc = (1u << 4) | kind | ((uint32_t)p.w_mn << 15) |
+                           ((uint32_t)(p.cols >> 3) << 17) | ((128u >> 4) << 24);
+    const uint32_t wstep = (p.w_mn ? 2048 : 32) >> 4, lead = elect_one();
+    int s = 0;
+    uint32_t ph = 0;
+    for (int k = k0; ok && k < k1; ++k) {
+      ok = wait_local(&full[s], ph, ab);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t x = desc_lo(base + s * p.stage + xoff, 16);
+      for (int g = 0; g <= (int)gated; ++g) {
+        const uint32_t w = desc_lo(base + s * p.stage + g * kABytes, p.w_mn ? kMnBox : 16);
+#pragma unroll
+        for (int j = 0; j < kDenseK / 16; ++j)
+          mma_alone(lead, tmem + g * p.cols, desc_of(w + j * wstep), desc_of(x + j * 2), idesc,
+                    (k > k0 || j > 0) ? 1u : 0u);
+      }
+      commit_alone(lead, &empty[s]);
+      if (++s == p.stages) s = 0, ph ^= 1;
+    }
+    commit_alone(lead, &done);
+    mbar_wait_drain(&done, 0, 100000000ull);
+  }
+  __syncwarp();
+  __syncthreads();  // all operands have been read: their place takes the sums
+  tc_fence_after();
+  const bool good = !s_abort;
+  float *sums = reinterpret_cast<float *>(smem);  // [z, g][row][128]
+  if (good) {
+    const uint32_t acc = tmem + ((uint32_t)(warp * 32) << 16);
+    for (int c = 0; c < (gated ? 2 : 1) * p.cols; c += 16) {
+      uint32_t r[16];
+      load16(acc + c, r);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) sums[(c + e) * 128 + threadIdx.x] = __uint_as_float(r[e]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, p.tmem);
+  }
+  cluster_sync();
+  if (good) {
+    // this CTA's groups of 4 outputs of a row
+    const int groups = p.M * 32, each = (groups + p.split - 1) / p.split;
+    const int end = min(groups, ((int)rank + 1) * each);
+    for (int i = (int)rank * each + threadIdx.x; i < end; i += kFewThreads) {
+      const int row = i >> 5, n = n0 + (i & 31) * 4;
+      if (n >= p.N) continue;
+      float z[4] = {}, g[4] = {};
+      add_remote(z, base + i * 16, p.split);
+      if (gated) add_remote(g, base + (p.cols * 32 + i) * 16, p.split);
+      finish4<T>(p.e, p.e.y, p.e.ys, row, n, p.N, z, g);
+    }
+  }
+  cluster_sync();  // the others have read what is here
 }
 
 // ------------------------------------------------------------------ dz, dgate and their sums
@@ -618,8 +839,6 @@ __global__ void __launch_bounds__(256) dense_finish_kernel(const __grid_constant
 template <typename T, int V, int kAct>
 __global__ void __launch_bounds__(256) dense_grad_kernel(const DenseGradParams p) {
   __shared__ float sums[2][8][32 * V + 1];
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < kStatusBytes / 4)
-    p.status[threadIdx.x] = 0;
   const int lane = threadIdx.x & 31, by = threadIdx.x >> 5;
   const int n = (blockIdx.x * 32 + lane) * V;
   const int r1 = min(p.M, (int)(blockIdx.y + 1) * p.chunk);
@@ -710,6 +929,24 @@ cudaError_t launch_t(const CUtensorMap (&ta)[2], const CUtensorMap (&tb)[2], con
   return cudaGetLastError();
 }
 
+template <typename T>
+cudaError_t launch_few_t(const CUtensorMap &tw0, const CUtensorMap &tw1, const CUtensorMap &tx,
+                         const DenseFewParams &p, cudaStream_t s) {
+  const cudaError_t e = allow_smem<dense_few_kernel<T>>(kFewSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((p.N + 127) / 128 * p.split);
+  c.blockDim = dim3(kFewThreads);
+  c.dynamicSmemBytes = p.smem;
+  c.stream = s;
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeClusterDimension;
+  a.val.clusterDim.x = p.split, a.val.clusterDim.y = a.val.clusterDim.z = 1;
+  c.attrs = &a;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, dense_few_kernel<T>, tw0, tw1, tx, p);
+}
+
 template <int kAct>
 cudaError_t launch_grad(bool f16, const DenseGradParams &p, int chunks, cudaStream_t s) {
   const int strip = 32 * (p.vec ? 8 : 1);
@@ -728,6 +965,12 @@ cudaError_t launch_grad(bool f16, const DenseGradParams &p, int chunks, cudaStre
 cudaError_t launch_dense(bool f16, const CUtensorMap (&ta)[2], const CUtensorMap (&tb)[2],
                          const DenseParams &p, int sms, cudaStream_t s) {
   return f16 ? launch_t<__half>(ta, tb, p, sms, s) : launch_t<__nv_bfloat16>(ta, tb, p, sms, s);
+}
+
+cudaError_t launch_dense_few(bool f16, const CUtensorMap &tw0, const CUtensorMap &tw1,
+                             const CUtensorMap &tx, const DenseFewParams &p, cudaStream_t s) {
+  return f16 ? launch_few_t<__half>(tw0, tw1, tx, p, s)
+             : launch_few_t<__nv_bfloat16>(tw0, tw1, tx, p, s);
 }
 
 cudaError_t launch_dense_grad(bool f16, const DenseGradParams &p, int chunks, cudaStream_t s) {

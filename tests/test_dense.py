@@ -202,12 +202,13 @@ def test_workspace_sizes(L):
     assert need(w=2 * at + 2) == 256 + 64 * 128 and need(ws=68) == 256 + 64 * 128
     assert need(K=7, xs=7) == 256 + 256  # 4 rows of 8, as a block of 256
     assert need(N=64, K=64, ws=70, order=1) == 256 + 64 * 128
-    assert need(M=1, K=16384, N=256, ws=256) > 256 + 2 * 256 * 4
+    assert need(M=65, K=16384, N=256, xs=16384, ws=256) > 256 + 2 * 65 * 256 * 4
+    assert need(M=64, K=16384, N=256, xs=16384, ws=256) == 256
     assert need(M=1, x=at, xs=3) == 256  # the stride of a single row has no meaning
 
 
 # M, K, N: one row and element up; tile edges; odd; several tiles a CTA; long sums
-SIZES = [(1, 1, 1), (1, 64, 256), (3, 8, 40), (17, 200, 96), (129, 65, 130), (256, 64, 256),
+SIZES = [(1, 1, 1), (1, 200, 2000), (16, 1000, 700), (64, 4096, 520), (65, 4096, 520), (48, 72, 24), (1, 64, 256), (3, 8, 40), (17, 200, 96), (129, 65, 130), (256, 64, 256),
          (257, 128, 513), (300, 1001, 77), (1, 4096, 1000), (33, 8192, 264), (1237, 96, 1000),
          (2100, 192, 8200)]
 # what stands in the epilogue: act, bias, gate, residual
@@ -322,7 +323,7 @@ def test_no_rows(L):
 @pytest.mark.parametrize("bad", [math.inf, math.nan])
 def test_special_values_stay_in_their_row(L, bad):
     """A row of x that is not finite spoils its own row of y and dx only; a split long sum too."""
-    for M, K, N in ((300, 72, 200), (2, 8192, 64)):
+    for M, K, N in ((300, 72, 200), (2, 8192, 64), (70, 8192, 64)):
         x, w, a, _ = case(M, K, N, "kn", BF, ("silu", False, True, False))
         y, kept = dash.dense_fwd(x, w, **a)
         dy = make((M, N), BF, 3)
@@ -418,15 +419,16 @@ def test_refusals(L):
 
 
 @gpu
-def test_failure_detection(L):
+@pytest.mark.parametrize("M", [700, 5])
+def test_failure_detection(L, M):
     """Loads that end early: the waits for them run out, the call is reported, the next one is right."""
-    M, K, N = 700, 640, 1000
+    M, K, N = M, 640, 1000
     x, w, a, r = case(M, K, N, "nk", BF, ("gelu", True, False, True))
     y, _ = dash.dense_fwd(x, w, residual=r, **a)
     limit = dash.wait_limit()
     dash.set_wait_limit(0.2)
     try:
-        for block in (0, 7):
+        for block in (0, 1):
             assert L.dash_dense_withhold(block) == 0
             with pytest.raises(dash.DashError) as e:
                 dash.dense_fwd(x, w, residual=r, check=True, **a)
