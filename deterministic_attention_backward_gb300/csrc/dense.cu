@@ -162,6 +162,28 @@ bool place(Rows &r, Arena &arena, cudaStream_t s) {
   return true;
 }
 
+// An output that does not lie on 16 bytes is formed in the workspace and copied to its place.
+struct Out {
+  void *to = nullptr, *at = nullptr;
+  long long to_stride = 0, stride = 0;
+  int rows = 0, cols = 0;
+  Out() = default;
+  Out(void *p, long long s, int rows, int cols)
+      : to(p), at(p), to_stride(s), stride(rows > 1 ? s : up(cols, 8)), rows(rows), cols(cols) {}
+  bool pad() const { return to && (!aligned16(to) || stride % 8); }
+  size_t bytes() const { return pad() ? align256((size_t)rows * up(cols, 8) * 2) : 0; }
+  void place(Arena &arena) {
+    if (!pad()) return;
+    const size_t n = bytes();
+    stride = up(cols, 8);
+    at = arena.take(n);
+  }
+  bool finish(cudaStream_t s) const {
+    return at == to ||
+           launch_dense_copy_out(at, stride, to, to_stride, rows, cols, s) == cudaSuccess;
+  }
+};
+
 // Launches a product of rows a[0..1], b[0..1] (the second ones where `parts` or `outs` or a gate
 // ask for them, otherwise empty).
 dash_status_t launch(const Product &p, const Rows (&a)[2], const Rows (&b)[2], bool a_mn, bool b_mn,
@@ -191,7 +213,14 @@ dash_status_t launch(const Product &p, const Rows (&a)[2], const Rows (&b)[2], b
 bool vec_rows(const void *p, long long stride) { return !p || (aligned16(p) && stride % 8 == 0); }
 
 // ------------------------------------------------------------------ forward
-dash_status_t check_fwd(const dash_dense_fwd_t *a, Product &p, Few &few, Rows &x, Rows (&w)[2]) {
+struct Fwd {
+  Product p;
+  Few few;
+  Rows x, w[2], res;
+  Out y, z, g;
+  size_t need;
+};
+dash_status_t check_fwd(const dash_dense_fwd_t *a, Fwd &f) {
   if (!a || !a->x || !a->w || !a->y || a->M <= 0 || a->K <= 0 || a->N <= 0) return DASH_ERR_INVALID;
   if (a->order != DASH_DENSE_KN && a->order != DASH_DENSE_NK) return DASH_ERR_INVALID;
   if (a->act < DASH_ACT_NONE || a->act > DASH_ACT_SILU) return DASH_ERR_INVALID;
@@ -205,25 +234,29 @@ dash_status_t check_fwd(const dash_dense_fwd_t *a, Product &p, Few &few, Rows &x
   if (a->M > 1 && a->y_stride < a->N) return DASH_ERR_INVALID;
   const bool kn = a->order == DASH_DENSE_KN;
   if (a->M > kMaxSize || a->K > kMaxSize || a->N > kMaxSize) return DASH_ERR_UNSUPPORTED;
-  p = plan(a->M, a->N, a->K, 1, 1, a->w_gate != nullptr);
-  if (!sizes_ok(p)) return DASH_ERR_UNSUPPORTED;
-  if (a->M <= kFewRows) {
-    few = plan_few(a->M, a->N, a->K, a->w_gate != nullptr);
-    p.splits = 1;  // (no partial sums in memory)
-  }
-  x = Rows(a->x, a->x_stride, a->M, a->K);
-  w[0] = Rows(a->w, a->w_stride, kn ? a->K : a->N, kn ? a->N : a->K);
-  w[1] = Rows(a->w_gate, a->w_gate_stride, w[0].rows, w[0].cols);
+  const bool gated = a->w_gate != nullptr;
+  f.p = plan(a->M, a->N, a->K, 1, 1, gated);
+  if (!sizes_ok(f.p)) return DASH_ERR_UNSUPPORTED;
+  f.x = Rows(a->x, a->x_stride, a->M, a->K);
+  f.w[0] = Rows(a->w, a->w_stride, kn ? a->K : a->N, kn ? a->N : a->K);
+  f.w[1] = Rows(a->w_gate, a->w_gate_stride, f.w[0].rows, f.w[0].cols);
+  f.res = Rows(a->residual, a->residual_stride, a->M, a->N);
+  f.y = Out(a->y, a->y_stride, a->M, a->N);
+  f.z = Out(a->z, a->N, a->M, a->N);
+  f.g = Out(a->gate, a->N, a->M, a->N);
+  f.need = kStatusBytes + f.x.bytes() + f.w[0].bytes() + f.w[1].bytes();
+  if (a->M <= kFewRows)  // (which needs no more room)
+    f.few = plan_few(a->M, a->N, a->K, gated);
+  else
+    f.need += f.p.part_bytes() + f.res.bytes() + f.y.bytes() + f.z.bytes() + f.g.bytes();
   return DASH_OK;
-}
-size_t need_fwd(const Product &p, const Rows &x, const Rows (&w)[2]) {
-  return kStatusBytes + x.bytes() + w[0].bytes() + w[1].bytes() + p.part_bytes();
 }
 
 // ------------------------------------------------------------------ backward
 struct Bwd {
   Product dx, dw;
   Rows dy, x, w[2];
+  Out out[3];          // dx, dw, dw_gate
   bool grads, pad_dy;  // dz (and dgate) are formed; dy is copied
   int chunks, chunk;
   size_t dz_bytes, sum_bytes, part_bytes, need;
@@ -258,9 +291,9 @@ dash_status_t check_bwd(const dash_dense_bwd_t *a, Bwd &b) {
   b.dw = kn ? plan(a->K, a->N, M, 1, gated ? 2 : 1, false)
             : plan(a->N, a->K, M, 1, gated ? 2 : 1, false);
   if (!sizes_ok(b.dx) || !sizes_ok(b.dw)) return DASH_ERR_UNSUPPORTED;
-  // rows of a chunk: enough chunks for every SM, 64 rows at least
+  // rows of a chunk: four rounds of CTAs or so, 64 rows at least
   const int strips = ceil_div(a->N, 256);
-  b.chunk = ceil_div(M, ceil_div(152 * 8, strips));
+  b.chunk = ceil_div(M, ceil_div(4 * 4 * 152, strips));
   b.chunk = (int)up(b.chunk < 64 ? 64 : b.chunk, 8);
   b.chunks = ceil_div(M, b.chunk);
   b.dz_bytes = b.grads && (a->dx || a->dw) ? align256((size_t)M * up(a->N, 8) * 2) : 0;
@@ -269,7 +302,10 @@ dash_status_t check_bwd(const dash_dense_bwd_t *a, Bwd &b) {
   if (a->dx) b.part_bytes = b.dx.part_bytes();
   if (a->dw && b.dw.part_bytes() > b.part_bytes) b.part_bytes = b.dw.part_bytes();
   b.pad_dy = !b.grads && (a->dx || a->dw) && b.dy.pad;
-  b.need = kStatusBytes + (gated ? 2 : 1) * b.dz_bytes + (a->dbias ? b.sum_bytes : 0) +
+  b.out[0] = Out(a->dx, a->dx_stride, a->M, a->K);
+  b.out[1] = Out(a->dw, a->dw_stride, wr, wc);
+  b.out[2] = Out(a->dw_gate, a->dw_gate_stride, wr, wc);
+  b.need = kStatusBytes + b.out[0].bytes() + b.out[1].bytes() + b.out[2].bytes() + (gated ? 2 : 1) * b.dz_bytes + (a->dbias ? b.sum_bytes : 0) +
            (a->dbias_gate ? b.sum_bytes : 0) + b.part_bytes + (b.pad_dy ? b.dy.bytes() : 0) +
            b.x.bytes() + b.w[0].bytes() + b.w[1].bytes();
   return DASH_OK;
@@ -286,66 +322,66 @@ dash_status_t dash_dense_withhold(int block) {
 }
 
 size_t dash_dense_fwd_workspace_bytes(const dash_dense_fwd_t *args) {
-  dash::Product p;
-  dash::Few few;
-  dash::Rows x, w[2];
-  return dash::check_fwd(args, p, few, x, w) == DASH_OK ? dash::need_fwd(p, x, w) : 0;
+  dash::Fwd f;
+  return dash::check_fwd(args, f) == DASH_OK ? f.need : 0;
 }
 
 dash_status_t dash_dense_fwd(const dash_dense_fwd_t *a, void *workspace, size_t workspace_bytes,
                              dash_stream_t stream) {
   using namespace dash;
-  Product p;
-  Few few;
-  Rows xs, w[2];
-  dash_status_t st = check_fwd(a, p, few, xs, w);
+  Fwd f;
+  dash_status_t st = check_fwd(a, f);
   if (st != DASH_OK) return st;
-  const size_t need = need_fwd(p, xs, w);
-  if (!workspace || !aligned16(workspace) || workspace_bytes < need) return DASH_ERR_WORKSPACE;
-  const Rows y(a->y, a->y_stride, a->M, a->N), res(a->residual, a->residual_stride, a->M, a->N);
+  if (!workspace || !aligned16(workspace) || workspace_bytes < f.need) return DASH_ERR_WORKSPACE;
+  const Rows y(a->y, a->y_stride, a->M, a->N);
   const long long kept = (long long)a->M * a->N;
   const Bytes outs[] = {y.lies(), bytes_of(a->z, 2, kept), bytes_of(a->gate, 2, kept),
-                        bytes_of(workspace, 1, (long long)need)};
-  const Bytes reads[] = {xs.lies(), w[0].lies(), w[1].lies(), bytes_of(a->bias, 2, a->N),
+                        bytes_of(workspace, 1, (long long)f.need)};
+  const Bytes reads[] = {f.x.lies(), f.w[0].lies(), f.w[1].lies(), bytes_of(a->bias, 2, a->N),
                          bytes_of(a->bias_gate, 2, a->N)};
   if (!apart(outs, reads)) return DASH_ERR_INVALID;
   const bool in_place = a->y == a->residual && (a->M == 1 || a->y_stride == a->residual_stride);
   for (int i = in_place ? 1 : 0; i < 4; ++i)
-    if (share(outs[i], res.lies())) return DASH_ERR_INVALID;
+    if (share(outs[i], f.res.lies())) return DASH_ERR_INVALID;
   DevInfo dev;
   if ((st = device_info(&dev)) != DASH_OK) return st;
+  const bool f16 = a->dtype == DASH_FP16, kn = a->order == DASH_DENSE_KN;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   Arena arena(workspace);
-  if (!place(xs, arena, s) || !place(w[0], arena, s) || !place(w[1], arena, s))
+  if (!place(f.x, arena, s) || !place(f.w[0], arena, s) || !place(f.w[1], arena, s))
     return DASH_ERR_CUDA;
-  float *part = static_cast<float *>(arena.take(p.part_bytes()));
   DenseEpilogue e{};
-  e.y = a->y, e.z = a->z, e.g = a->gate;
-  e.bias = a->bias, e.bias_gate = a->bias_gate, e.residual = a->residual;
-  e.ys = a->y_stride, e.zs = e.gs = a->N, e.rs = a->residual_stride;
-  e.act = a->act, e.gated = p.gated;
-  e.vec = vec_rows(e.y, e.ys) && vec_rows(e.z, a->N) && vec_rows(e.g, a->N) &&
-          vec_rows(e.residual, e.rs) && vec_rows(e.bias, 0) && vec_rows(e.bias_gate, 0);
-  if (few.split) {
-    const bool f16 = a->dtype == DASH_FP16, mn = a->order == DASH_DENSE_KN;
+  e.bias = a->bias, e.bias_gate = a->bias_gate;
+  e.act = a->act, e.gated = f.p.gated;
+  if (f.few.split) {
+    e.y = a->y, e.z = a->z, e.g = a->gate, e.residual = a->residual;
+    e.ys = a->y_stride, e.zs = e.gs = a->N, e.rs = a->residual_stride;
     CUtensorMap tw[2], tx;
     for (int i = 0; i < 2; ++i)
-      if (!make_rows_map(&tw[i], w[i].at ? w[i] : w[0], mn ? 64 : 128, f16)) return DASH_ERR_CUDA;
-    if (!make_rows_map(&tx, xs, few.cols, f16)) return DASH_ERR_CUDA;
+      if (!make_rows_map(&tw[i], f.w[i].at ? f.w[i] : f.w[0], kn ? 64 : 128, f16))
+        return DASH_ERR_CUDA;
+    if (!make_rows_map(&tx, f.x, f.few.cols, f16)) return DASH_ERR_CUDA;
     DenseFewParams d{};
     d.e = e;
     d.status = static_cast<uint32_t *>(workspace);
     d.wait_ns = g_wait_ns.load();
-    d.M = p.M, d.N = p.N, d.nk = p.nk();
-    d.cols = few.cols, d.split = few.split, d.per = few.per;
-    d.stages = few.stages, d.stage = few.stage, d.smem = few.smem, d.tmem = few.tmem;
-    d.w_mn = mn;
+    d.M = f.p.M, d.N = f.p.N, d.nk = f.p.nk();
+    d.cols = f.few.cols, d.split = f.few.split, d.per = f.few.per;
+    d.stages = f.few.stages, d.stage = f.few.stage, d.smem = f.few.smem, d.tmem = f.few.tmem;
+    d.w_mn = kn;
     d.withhold = g_dense_withhold.load();
     return launch_dense_few(f16, tw[0], tw[1], tx, d, s) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
   }
-  const Rows x[2] = {xs, Rows()};
-  return launch(p, x, w, false, a->order == DASH_DENSE_KN, false, false, e, nullptr, 0, part,
-                workspace, true, a->dtype == DASH_FP16, dev.sms, s);
+  float *part = static_cast<float *>(arena.take(f.p.part_bytes()));
+  if (!place(f.res, arena, s)) return DASH_ERR_CUDA;
+  for (Out *o : {&f.y, &f.z, &f.g}) o->place(arena);
+  e.y = f.y.at, e.z = f.z.at, e.g = f.g.at, e.residual = f.res.at;
+  e.ys = f.y.stride, e.zs = f.z.stride, e.gs = f.g.stride, e.rs = f.res.stride;
+  const Rows x[2] = {f.x, Rows()};
+  st = launch(f.p, x, f.w, false, kn, false, false, e, nullptr, 0, part, workspace, true, f16,
+              dev.sms, s);
+  if (st != DASH_OK) return st;
+  return f.y.finish(s) && f.z.finish(s) && f.g.finish(s) ? DASH_OK : DASH_ERR_CUDA;
 }
 
 size_t dash_dense_bwd_workspace_bytes(const dash_dense_bwd_t *args) {
@@ -416,25 +452,27 @@ dash_status_t dash_dense_bwd(const dash_dense_bwd_t *a, void *workspace, size_t 
   if (!place(dz[0], arena, s) || !place(b.x, arena, s) || !place(b.w[0], arena, s) ||
       !place(b.w[1], arena, s))
     return DASH_ERR_CUDA;
+  for (Out &o : b.out) o.place(arena);
   if (a->dx) {
     DenseEpilogue e{};
-    e.y = a->dx, e.ys = a->dx_stride;
-    e.vec = vec_rows(e.y, e.ys);
-    st = launch(b.dx, dz, b.w, false, !kn, false, false, e, nullptr, 0, part, workspace, true,
-                f16, dev.sms, s);
+    e.y = b.out[0].at, e.ys = b.out[0].stride;
+    st = launch(b.dx, dz, b.w, false, !kn, false, false, e, nullptr, 0, part, workspace, true, f16,
+                dev.sms, s);
     if (st != DASH_OK) return st;
   }
   if (a->dw) {
     DenseEpilogue e{};
-    e.y = a->dw, e.ys = a->dw_stride;
-    e.vec = vec_rows(e.y, e.ys) && vec_rows(a->dw_gate, a->dw_gate_stride);
+    e.y = b.out[1].at, e.ys = b.out[1].stride;
     const Rows x[2] = {b.x, Rows()};
-    st = kn ? launch(b.dw, x, dz, true, true, false, gated, e, a->dw_gate, a->dw_gate_stride, part,
+    st = kn ? launch(b.dw, x, dz, true, true, false, gated, e, b.out[2].at, b.out[2].stride, part,
                      workspace, !a->dx, f16, dev.sms, s)
-            : launch(b.dw, dz, x, true, true, gated, false, e, a->dw_gate, a->dw_gate_stride, part,
+            : launch(b.dw, dz, x, true, true, gated, false, e, b.out[2].at, b.out[2].stride, part,
                      workspace, !a->dx, f16, dev.sms, s);
+    if (st != DASH_OK) return st;
   }
-  return st;
+  for (const Out &o : b.out)
+    if (!o.finish(s)) return DASH_ERR_CUDA;
+  return DASH_OK;
 }
 
 }  // extern "C"

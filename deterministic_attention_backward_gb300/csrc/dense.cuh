@@ -20,9 +20,8 @@ constexpr int kDenseK = 64;    // contraction elements of a stage
 struct DenseEpilogue {
   void *y, *z, *g;
   const void *bias, *bias_gate, *residual;
-  long long ys, zs, gs, rs;  // row strides in elements
+  long long ys, zs, gs, rs;  // row strides in elements; the product kernel wants 16-byte steps
   int act, gated;
-  int vec;                   // all of them by 16-byte vectors
 };
 struct DenseParams {
   DenseEpilogue e;
@@ -74,8 +73,10 @@ cudaError_t launch_dense_grad(bool f16, const DenseGradParams &p, int chunks, cu
 // out[n] = sum over chunks, in order (gate: a second row of sums and its output)
 cudaError_t launch_dense_sums(bool f16, const float *part, const float *part_gate, void *out,
                               void *out_gate, int chunks, int N, cudaStream_t s);
-// rows of cols elements of two bytes to rows at another stride, cleared up to there
-cudaError_t launch_dense_copy(const void *in, long long is, void *out, long long os,
-                              long long rows, int cols, cudaStream_t s);
+// rows of cols elements of two bytes to rows on 16 bytes, the last vector filled up with zeros; and back
+cudaError_t launch_dense_copy(const void *in, long long is, void *out, long long os, int rows,
+                              int cols, cudaStream_t s);
+cudaError_t launch_dense_copy_out(const void *in, long long is, void *out, long long os, int rows,
+                                  int cols, cudaStream_t s);
 
 }  // namespace dash

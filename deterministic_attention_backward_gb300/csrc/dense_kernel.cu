@@ -287,10 +287,9 @@ __device__ __forceinline__ void add_cols(const void *base, long long at, float (
 }
 // A bias, the same for all rows of a warp.
 template <typename T>
-__device__ __forceinline__ void add_bias(const void *base, int n, float (&v)[32], int left,
-                                         bool vec) {
-  if (vec && left >= 32) {
-    const T *src = static_cast<const T *>(base) + n;
+__device__ __forceinline__ void add_bias(const void *base, int n, float (&v)[32], int left, int lane) {
+  const T *src = static_cast<const T *>(base) + n;
+  if (left >= 32 && (reinterpret_cast<uintptr_t>(base) & 15) == 0) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float f[8];
@@ -298,8 +297,10 @@ __device__ __forceinline__ void add_bias(const void *base, int n, float (&v)[32]
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[8 * i + e] += f[e];
     }
-  } else {
-    add_cols<T, 32>(base, n, v, left);
+  } else {  // a lane brings one column's and hands it round
+    const float b = lane < left ? to_f32<T>(src[lane]) : 0.f;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[e] += __shfl_sync(0xffffffffu, b, e);
   }
 }
 
@@ -331,51 +332,54 @@ __device__ __forceinline__ void turn_add(uint8_t *buf, int lane, float (&v)[32])
     for (int e = 0; e < 8; ++e) v[8 * i + e] += f[e];
   }
 }
-// The buffer to rows [row0, row0 + 32) of a tensor, columns [n, n + left): by 16-byte pieces, four
-// lanes a row, or by elements, a row at a time.
+// The buffer to rows [row0, row0 + rows) of a tensor, columns [n, n + left): by 16-byte pieces, four
+// lanes a row; a piece that ends behind the row by its elements.
 template <typename T>
 __device__ __forceinline__ void turn_store(uint8_t *buf, void *base, long long stride, long long row0,
-                                           int rows, int n, int left, int lane, bool vec) {
+                                           int rows, int n, int left, int lane) {
   T *dst = static_cast<T *>(base) + row0 * stride + n;
-  if (vec && left >= 32) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 8 * i + (lane >> 2), c = lane & 3;
-      if (r < rows)
-        store_pack<T, 8>(dst + r * stride + 8 * c,
-                         load_pack<T, 8>(reinterpret_cast<const T *>(turn_at(buf, r, c))));
-    }
-  } else if (lane < left) {
-    const int c = lane >> 3, e = lane & 7;
-    for (int r = 0; r < rows; ++r)
-      dst[r * stride + lane] = reinterpret_cast<const T *>(turn_at(buf, r, c))[e];
-  }
-}
-// Rows of a tensor into the buffer, the pieces that `fetch` has brought in.
-template <typename T>
-__device__ __forceinline__ void turn_fetch(uint4 (&v)[4], const void *base, long long stride,
-                                           long long row0, int rows, int n, int lane) {
-  const T *src = static_cast<const T *>(base) + row0 * stride + n;
+  const int c = lane & 3, in = left - 8 * c;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int r = 8 * i + (lane >> 2), c = lane & 3;
+    const int r = 8 * i + (lane >> 2);
+    if (r >= rows) continue;
+    const Pack<T, 8> v = load_pack<T, 8>(reinterpret_cast<const T *>(turn_at(buf, r, c)));
+    T *to = dst + r * stride + 8 * c;
+    if (in >= 8) {
+      store_pack<T, 8>(to, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 7; ++e)
+        if (e < in) to[e] = v.e[e];
+    }
+  }
+}
+// The same pieces of a tensor that is read, and into the buffer.
+template <typename T>
+__device__ __forceinline__ void turn_fetch(uint4 (&v)[4], const void *base, long long stride,
+                                           long long row0, int rows, int n, int left, int lane) {
+  const T *src = static_cast<const T *>(base) + row0 * stride + n;
+  const int c = lane & 3, in = left - 8 * c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 2);
     v[i] = make_uint4(0, 0, 0, 0);
-    if (r < rows) v[i] = *reinterpret_cast<const uint4 *>(src + r * stride + 8 * c);
+    if (r >= rows) continue;
+    const T *from = src + r * stride + 8 * c;
+    if (in >= 8) {
+      v[i] = *reinterpret_cast<const uint4 *>(from);
+    } else if (in > 0) {
+      Pack<T, 8> p;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) p.e[e] = e < in ? from[e] : from_f32<T>(0.f);
+      v[i] = *reinterpret_cast<const uint4 *>(&p);
+    }
   }
 }
 __device__ __forceinline__ void turn_fill(uint8_t *buf, const uint4 (&v)[4], int lane) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     *reinterpret_cast<uint4 *>(turn_at(buf, 8 * i + (lane >> 2), lane & 3)) = v[i];
-}
-template <typename T>
-__device__ __forceinline__ void turn_load(uint8_t *buf, const void *base, long long stride,
-                                          long long row0, int rows, int n, int left, int lane) {
-  const T *src = static_cast<const T *>(base) + row0 * stride + n;
-  const int c = lane >> 3, e = lane & 7;
-  if (lane < left)
-    for (int r = 0; r < rows; ++r)
-      reinterpret_cast<T *>(turn_at(buf, r, c))[e] = src[r * stride + lane];
 }
 
 __device__ __forceinline__ void load32(uint32_t taddr, float (&v)[32]) {
@@ -558,7 +562,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int quad = warp & 3, wg = (warp - 4) >> 2;
     uint8_t *turn = smem + kOffTurn + (warp - 4) * 2 * kTurnBytes, *turn2 = turn + kTurnBytes;
     const DenseEpilogue &e = p.e;
-    const bool vec = e.vec;
     const int cols = e.gated ? p.bn / 2 : p.bn;  // output columns of a tile
     const int c0 = wg * (cols / 2), c1 = c0 + cols / 2;
     int n = 0;
@@ -568,10 +571,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int rows = (int)max(0ll, min(32ll, p.M - row0));
       const int n0 = w.n * cols;
       // the residual's pieces are under way while the products are formed
-      const bool fetch = e.residual && vec && w.cut < 0;
       uint4 next[4];
-      if (fetch && n0 + c0 + 32 <= p.N)
-        turn_fetch<T>(next, e.residual, e.rs, row0, rows, n0 + c0, lane);
+      if (e.residual && w.cut < 0 && n0 + c0 < p.N)
+        turn_fetch<T>(next, e.residual, e.rs, row0, rows, n0 + c0, p.N - n0 - c0, lane);
       if (!wait_pair(&acc_full[n & 1], (n >> 1) & 1, ab)) break;
       tc_fence_after();
       const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16) + (n & 1) * 256;
@@ -597,18 +599,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           float z[32], g[32];
           load32(acc + c, z);
           if (e.gated) load32(acc + p.bn / 2 + c, g);
-          if (e.bias) add_bias<T>(e.bias, at, z, left, vec);
+          if (e.bias) add_bias<T>(e.bias, at, z, left, lane);
           if (e.z) {
             turn_put<T>(turn, lane, z);
             __syncwarp();
-            turn_store<T>(turn, e.z, e.zs, row0, rows, at, left, lane, vec);
+            turn_store<T>(turn, e.z, e.zs, row0, rows, at, left, lane);
           }
           if (e.gated) {
-            if (e.bias_gate) add_bias<T>(e.bias_gate, at, g, left, vec);
+            if (e.bias_gate) add_bias<T>(e.bias_gate, at, g, left, lane);
             if (e.g) {
               turn_put<T>(turn2, lane, g);
               __syncwarp();
-              turn_store<T>(turn2, e.g, e.gs, row0, rows, at, left, lane, vec);
+              turn_store<T>(turn2, e.g, e.gs, row0, rows, at, left, lane);
             }
           }
           activate(e.act, z);
@@ -618,19 +620,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
           if (e.residual) {
-            if (fetch && left >= 32) {
-              turn_fill(turn, next, lane);
-              if (c + 32 < c1 && left >= 64)
-                turn_fetch<T>(next, e.residual, e.rs, row0, rows, at + 32, lane);
-            } else {
-              turn_load<T>(turn, e.residual, e.rs, row0, rows, at, left, lane);
-            }
+            turn_fill(turn, next, lane);
+            if (c + 32 < c1 && left > 32)
+              turn_fetch<T>(next, e.residual, e.rs, row0, rows, at + 32, left - 32, lane);
             __syncwarp();
             turn_add<T>(turn, lane, z);
           }
           turn_put<T>(turn2, lane, z);
           __syncwarp();
-          turn_store<T>(turn2, y, ys, row0, rows, at, left, lane, vec);
+          turn_store<T>(turn2, y, ys, row0, rows, at, left, lane);
           __syncwarp();
         }
       }
@@ -836,9 +834,9 @@ __global__ void __launch_bounds__(kFewThreads)
 // ------------------------------------------------------------------ dz, dgate and their sums
 // 32 threads a strip of 32 V columns, 8 rows at a time over a chunk of rows; the eight rows'
 // sums are added in order through shared memory.
-template <typename T, int V, int kAct>
-__global__ void __launch_bounds__(256) dense_grad_kernel(const DenseGradParams p) {
-  __shared__ float sums[2][8][32 * V + 1];
+template <typename T, int V, int kAct, bool kSums>
+__global__ void __launch_bounds__(256, kSums ? 3 : 4)
+    dense_grad_kernel(const __grid_constant__ DenseGradParams p) {
   const int lane = threadIdx.x & 31, by = threadIdx.x >> 5;
   const int n = (blockIdx.x * 32 + lane) * V;
   const int r1 = min(p.M, (int)(blockIdx.y + 1) * p.chunk);
@@ -846,10 +844,14 @@ __global__ void __launch_bounds__(256) dense_grad_kernel(const DenseGradParams p
   if (n < p.N) {
     for (long long r = blockIdx.y * p.chunk + by; r < r1; r += 8) {
       float dy[V], z[V], g[V];
-      unpack<T, V>(load_pack<T, V>(static_cast<const T *>(p.dy) + r * p.dys + n), dy);
+      Pack<T, V> z_, g_;
+      const Pack<T, V> dy_ = load_pack<T, V>(static_cast<const T *>(p.dy) + r * p.dys + n);
+      if (p.z) z_ = load_pack<T, V>(static_cast<const T *>(p.z) + r * p.zs + n);
+      if (p.g) g_ = load_pack<T, V>(static_cast<const T *>(p.g) + r * p.gs + n);
+      unpack<T, V>(dy_, dy);
       if (p.z) {
-        unpack<T, V>(load_pack<T, V>(static_cast<const T *>(p.z) + r * p.zs + n), z);
-        if (p.g) unpack<T, V>(load_pack<T, V>(static_cast<const T *>(p.g) + r * p.gs + n), g);
+        unpack<T, V>(z_, z);
+        if (p.g) unpack<T, V>(g_, g);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           float slope;
@@ -866,28 +868,32 @@ __global__ void __launch_bounds__(256) dense_grad_kernel(const DenseGradParams p
 #pragma unroll
         for (int e = 0; e < V; ++e) z[e] = dy[e];
       }
+      if constexpr (kSums) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        sz[e] += z[e];
-        if (p.g) sg[e] += g[e];
+        for (int e = 0; e < V; ++e) {
+          sz[e] += z[e];
+          if (p.g) sg[e] += g[e];
+        }
       }
     }
   }
-  if (!p.part && !p.part_gate) return;
+  if constexpr (kSums) {
+    __shared__ float sums[2][8][32 * V + 1];
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-    sums[0][by][lane * V + e] = sz[e];
-    sums[1][by][lane * V + e] = sg[e];
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 64 * V; i += 256) {
-    const int which = i / (32 * V), c = i % (32 * V), col = blockIdx.x * 32 * V + c;
-    float *dst = which ? p.part_gate : p.part;
-    if (!dst || col >= p.N) continue;
-    float s = 0.f;
+    for (int e = 0; e < V; ++e) {
+      sums[0][by][lane * V + e] = sz[e];
+      sums[1][by][lane * V + e] = sg[e];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 64 * V; i += 256) {
+      const int which = i / (32 * V), c = i % (32 * V), col = blockIdx.x * 32 * V + c;
+      float *dst = which ? p.part_gate : p.part;
+      if (!dst || col >= p.N) continue;
+      float s = 0.f;
 #pragma unroll
-    for (int b = 0; b < 8; ++b) s += sums[which][b][c];
-    dst[(long long)blockIdx.y * p.N + col] = s;
+      for (int b = 0; b < 8; ++b) s += sums[which][b][c];
+      dst[(long long)blockIdx.y * p.N + col] = s;
+    }
   }
 }
 
@@ -900,18 +906,35 @@ __global__ void __launch_bounds__(128) dense_sums_kernel(const float *part, cons
   T *dst = static_cast<T *>(blockIdx.y ? out_gate : out);
   if (n >= N || !src || !dst) return;
   float s = 0.f;
+#pragma unroll 8
   for (int c = 0; c < chunks; ++c) s += src[(long long)c * N + n];
   dst[n] = from_f32<T>(s);
 }
 
+// A thread writes 16 bytes; a row's reads, which lie on no boundary, meet in L1.
 __global__ void __launch_bounds__(256) dense_copy_kernel(const uint16_t *in, long long is,
-                                                         uint16_t *out, long long os,
-                                                         long long rows, int cols) {
-  const long long stride = (long long)gridDim.x * 256, all = rows * os;
-  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < all; i += stride) {
-    const long long r = i / os, c = i - r * os;
-    out[i] = c < cols ? in[r * is + c] : (uint16_t)0;
+                                                         uint16_t *out, long long os, int rows,
+                                                         int cols) {
+  const int c = (blockIdx.x * 32 + (threadIdx.x & 31)) * 8;
+  if (c >= cols) return;
+  for (long long r = blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.y * 8) {
+    const uint16_t *src = in + r * is + c;
+    Pack<uint16_t, 8> v;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v.e[e] = c + e < cols ? src[e] : (uint16_t)0;
+    store_pack<uint16_t, 8>(out + r * os + c, v);
   }
+}
+
+// The other way: rows that lie on 16 bytes to where a caller's lie.
+__global__ void __launch_bounds__(256) dense_copy_out_kernel(const uint16_t *in, long long is,
+                                                             uint16_t *out, long long os, int rows,
+                                                             int cols) {
+  const int c = blockIdx.x * 128 + (threadIdx.x & 31);
+  for (long long r = blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.y * 8)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + 32 * i < cols) out[r * os + c + 32 * i] = in[r * is + c + 32 * i];
 }
 
 template <typename T>
@@ -947,16 +970,22 @@ cudaError_t launch_few_t(const CUtensorMap &tw0, const CUtensorMap &tw1, const C
   return cudaLaunchKernelEx(&c, dense_few_kernel<T>, tw0, tw1, tx, p);
 }
 
+template <typename T, int V, int kAct>
+void launch_grad_t(const DenseGradParams &p, int chunks, cudaStream_t s) {
+  const dim3 grid((p.N + 32 * V - 1) / (32 * V), chunks);
+  if (p.part || p.part_gate)
+    dense_grad_kernel<T, V, kAct, true><<<grid, 256, 0, s>>>(p);
+  else
+    dense_grad_kernel<T, V, kAct, false><<<grid, 256, 0, s>>>(p);
+}
 template <int kAct>
 cudaError_t launch_grad(bool f16, const DenseGradParams &p, int chunks, cudaStream_t s) {
-  const int strip = 32 * (p.vec ? 8 : 1);
-  const dim3 grid((p.N + strip - 1) / strip, chunks);
   if (f16)
-    p.vec ? dense_grad_kernel<__half, 8, kAct><<<grid, 256, 0, s>>>(p)
-          : dense_grad_kernel<__half, 1, kAct><<<grid, 256, 0, s>>>(p);
+    p.vec ? launch_grad_t<__half, 8, kAct>(p, chunks, s)
+          : launch_grad_t<__half, 1, kAct>(p, chunks, s);
   else
-    p.vec ? dense_grad_kernel<__nv_bfloat16, 8, kAct><<<grid, 256, 0, s>>>(p)
-          : dense_grad_kernel<__nv_bfloat16, 1, kAct><<<grid, 256, 0, s>>>(p);
+    p.vec ? launch_grad_t<__nv_bfloat16, 8, kAct>(p, chunks, s)
+          : launch_grad_t<__nv_bfloat16, 1, kAct>(p, chunks, s);
   return cudaGetLastError();
 }
 
@@ -994,10 +1023,18 @@ cudaError_t launch_dense_sums(bool f16, const float *part, const float *part_gat
   return cudaGetLastError();
 }
 
-cudaError_t launch_dense_copy(const void *in, long long is, void *out, long long os,
-                              long long rows, int cols, cudaStream_t s) {
-  const long long blocks = (rows * os + 255) / 256;
-  dense_copy_kernel<<<(unsigned)(blocks < 8192 ? blocks : 8192), 256, 0, s>>>(
+cudaError_t launch_dense_copy_out(const void *in, long long is, void *out, long long os, int rows,
+                                  int cols, cudaStream_t s) {
+  const int down = (rows + 7) / 8;
+  dense_copy_out_kernel<<<dim3((cols + 127) / 128, down < 16384 ? down : 16384), 256, 0, s>>>(
+      static_cast<const uint16_t *>(in), is, static_cast<uint16_t *>(out), os, rows, cols);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_dense_copy(const void *in, long long is, void *out, long long os, int rows,
+                              int cols, cudaStream_t s) {
+  const int down = (rows + 7) / 8;
+  dense_copy_kernel<<<dim3((cols + 255) / 256, down < 16384 ? down : 16384), 256, 0, s>>>(
       static_cast<const uint16_t *>(in), is, static_cast<uint16_t *>(out), os, rows, cols);
   return cudaGetLastError();
 }
