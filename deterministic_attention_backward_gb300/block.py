@@ -9,13 +9,16 @@ dataset and no optimizer step.  The dense layers use torch matrix products (plum
 the measured path); the attention forward and backward run in this library's kernels.
 
 Options put the operators around the attention in their places, forward and backward in this
-library's kernels too: rotary positions on the way from the qkv product to the attention, norms
-fused with the residual joins (with a norm after each branch as well, if asked for), and
-differential attention with its norm of heads in place of the attention.  Without them the block
-is what it was: no positions, norms and joins in torch operations.
+library's kernels too: rotary positions on the way from the qkv product to the attention, with a norm
+of every head of q and k before the turn if asked for, norms fused with the residual joins (with a norm
+after each branch as well, if asked for), differential attention with its norm of heads in place of the
+attention, the dense products with activation, gate and residual in their epilogues, and after the
+backward the clipping of all gradients by their norm.  Without them the block is what it was: no
+positions, norms, joins and products in torch operations, gradients as they are.
 
     python -m deterministic_attention_backward_gb300.block [--seq 8192] [--batch 1]
-        [--rotary] [--fused-norms] [--post-norms] [--differential]
+        [--rotary] [--qk-norm] [--fused-norms] [--post-norms] [--differential] [--fused-dense]
+        [--clip]
 """
 from __future__ import annotations
 
@@ -74,6 +77,44 @@ def _operator_functions():
         def views(t, heads):
             parts = t.split([h * d for h, d in heads], dim=-1)
             return [p.unflatten(-1, h) for p, h in zip(parts, heads)]
+
+    class NormRotary(torch.autograd.Function):
+        """The same with a norm of every head of q and k before the turn."""
+
+        @staticmethod
+        def forward(ctx, qkv, wq, wk, freqs, q_heads, k_heads, v_heads):
+            ctx.save_for_backward(qkv, wq, wk, freqs)
+            ctx.heads = q_heads, k_heads, v_heads
+            return dash.rope_norm_fwd(*Rotary.views(qkv, ctx.heads), q_weight=wq, k_weight=wk,
+                                      inv_freq=freqs)
+
+        @staticmethod
+        def backward(ctx, *grads):
+            qkv, wq, wk, freqs = ctx.saved_tensors
+            dqkv = torch.empty_like(qkv)
+            *_, dwq, dwk = dash.rope_norm_bwd(
+                *map(dense, grads), *Rotary.views(qkv, ctx.heads)[:2], q_weight=wq, k_weight=wk,
+                inv_freq=freqs, out=Rotary.views(dqkv, ctx.heads))
+            return dqkv, dwq, dwk, None, None, None, None
+
+    class Dense(torch.autograd.Function):
+        """residual + act(x w), or act(x w) (x w_gate): products with their epilogue."""
+
+        @staticmethod
+        def forward(ctx, x, w, w_gate, residual, act):
+            y, kept = dash.dense_fwd(x, w, act=act, w_gate=w_gate, residual=residual)
+            ctx.save_for_backward(x, w, w_gate, kept)
+            ctx.act, ctx.joins = act, residual is not None
+            return y
+
+        @staticmethod
+        def backward(ctx, dy):
+            x, w, w_gate, kept = ctx.saved_tensors
+            dy = dense(dy)
+            dx, dw, _, dw_gate, _ = dash.dense_bwd(
+                dy, x, w, kept, act=ctx.act, w_gate=w_gate, need_dx=ctx.needs_input_grad[0],
+                need_dw=ctx.needs_input_grad[1] or ctx.needs_input_grad[2])
+            return dx, dw, dw_gate, dy if ctx.joins else None, None
 
     class Norm(torch.autograd.Function):
         @staticmethod
@@ -137,7 +178,7 @@ def _operator_functions():
             return *dash.diff_bwd(q, k, v, o, o2, dense(do), lse, lam, causal=ctx.causal,
                                   rest=rest), None
 
-    return Rotary, Norm, PreNorm, Join, Differential
+    return Rotary, Norm, PreNorm, Join, Differential, NormRotary, Dense
 
 
 class Block:
@@ -148,14 +189,19 @@ class Block:
     after each branch.  ``differential``: the first map's weight less ``differential`` times the
     second's in every head, the weight learned per head from there on; the projections are the
     same, a head of q or k becomes a pair of half its size, and the heads' outputs are normed
-    (the schedule has no meaning then: that backward knows one order only)."""
+    (the schedule has no meaning then: that backward knows one order only).  ``qk_norm``: with
+    rotary, heads of q and k normed before the turn.  ``fused_dense``: products in this library's
+    kernels, silu, gate and (without ``fused_norms``, which join by themselves) residual in their
+    epilogues."""
 
     def __init__(self, hidden=4096, heads=32, kv_heads=8, head_dim=128, ffn=14336,
                  device="cuda", seed=0, rotary=None, fused_norms=False, post_norms=False,
-                 differential=None):
+                 differential=None, qk_norm=False, fused_dense=False):
         import torch
         if post_norms and not fused_norms:
             raise ValueError("post_norms needs fused_norms")
+        if qk_norm and rotary is None:
+            raise ValueError("qk_norm needs rotary")
         if differential is not None and head_dim not in (64, 128):
             raise ValueError(f"differential attention needs heads of 64 or 128, got {head_dim}")
         g = torch.Generator(device="cpu").manual_seed(seed)
@@ -171,9 +217,10 @@ class Block:
         self.n1 = torch.ones(hidden, device=device, dtype=torch.bfloat16, requires_grad=True)
         self.n2 = torch.ones(hidden, device=device, dtype=torch.bfloat16, requires_grad=True)
         self.attn = _attention_function()
-        self.Rotary, self.Norm, self.PreNorm, self.Join, self.Differential = _operator_functions()
-        self.fused_norms = fused_norms
-        self.p1 = self.p2 = self.lam = self.nh = self.freqs = None
+        (self.Rotary, self.Norm, self.PreNorm, self.Join, self.Differential, self.NormRotary,
+         self.Dense) = _operator_functions()
+        self.fused_norms, self.fused_dense = fused_norms, fused_dense
+        self.p1 = self.p2 = self.lam = self.nh = self.freqs = self.nq = self.nk = None
 
         def full(n, value, dtype=torch.bfloat16):
             return torch.full((n,), value, device=device, dtype=dtype, requires_grad=True)
@@ -191,6 +238,8 @@ class Block:
         if rotary is not None:
             from .rope import rope_freqs
             self.freqs, _ = rope_freqs(head_dim // pair, base=rotary, device=device)
+        if qk_norm:
+            self.nq, self.nk = full(head_dim // pair, 1.0), full(head_dim // pair, 1.0)
         # when a dict: the attention's inputs and output of the last call are kept there, with
         # their gradients retained (q/k/v.grad = dQ/dK/dV, o.grad = the upstream dO)
         self.capture = None
@@ -208,8 +257,11 @@ class Block:
             x, hid = self.PreNorm.apply(x, self.n1)
         else:
             hid = self._rms(x, self.n1)
-        qkv = hid @ self.wqkv
-        if self.freqs is not None:
+        fused, joins = self.fused_dense, self.fused_norms
+        qkv = self.Dense.apply(hid, self.wqkv, None, None, "none") if fused else hid @ self.wqkv
+        if self.nq is not None:
+            q, k, v = self.NormRotary.apply(qkv, self.nq, self.nk, self.freqs, *self.parts)
+        elif self.freqs is not None:
             q, k, v = self.Rotary.apply(qkv, self.freqs, *self.parts)
         else:
             q, k, v = (t.reshape(B, S, *heads).contiguous() for t, heads in
@@ -224,25 +276,40 @@ class Block:
             self.capture.update(q=q, k=k, v=v, o=o)
         if self.nh is not None:
             o = self.Norm.apply(o, self.nh)
-        a = o.reshape(B, S, self.h * self.d) @ self.wo
-        if self.fused_norms:
+        o = o.reshape(B, S, self.h * self.d)
+        a = self.Dense.apply(o, self.wo, None, None if joins else x, "none") if fused else o @ self.wo
+        if joins:
             x, hid = self.Join.apply(x, a, self.p1, self.n2)
         else:
-            x = x + a
+            x = a if fused else x + a
             hid = self._rms(x, self.n2)
-        m = (F.silu(hid @ self.w1) * (hid @ self.w3)) @ self.w2
-        return self.Join.apply(x, m, self.p2, None) if self.fused_norms else x + m
+        if fused:
+            m = self.Dense.apply(hid, self.w1, self.w3, None, "silu")
+            m = self.Dense.apply(m, self.w2, None, None if joins else x, "none")
+        else:
+            m = (F.silu(hid @ self.w1) * (hid @ self.w3)) @ self.w2
+        if joins:
+            return self.Join.apply(x, m, self.p2, None)
+        return m if fused else x + m
 
     def parameters(self):
         return [p for p in (self.wqkv, self.wo, self.w1, self.w3, self.w2, self.n1, self.n2,
-                            self.p1, self.p2, self.lam, self.nh) if p is not None]
+                            self.p1, self.p2, self.lam, self.nh, self.nq, self.nk)
+                if p is not None]
+
+    def clip(self, max_norm):
+        """Scale the parameters' gradients in place so that their norm is ``max_norm`` at most: the
+        norm they had, an fp32 scalar on the device."""
+        import deterministic_attention_backward_gb300 as dash
+        return dash.grad_clip([p.grad for p in self.parameters()], max_norm)
 
 
 def time_block(seq=8192, batch=1, schedules=("atomic", "serial", "shift_fill", "auto"),
-               steps=10, warmup=3, causal=True, seed=0, **options):
+               steps=10, warmup=3, causal=True, seed=0, clip=None, **options):
     """Median forward+backward time (ms) of one block per schedule, and each
     deterministic schedule's slowdown against ``atomic``.  ``options`` are those of ``Block``;
-    differential attention is timed once, its one order standing for a schedule."""
+    differential attention is timed once, its one order standing for a schedule.  ``clip``: the norm to
+    which a step clips its gradients (None: it does not)."""
     import torch
     blk = Block(seed=seed, **options)
     if blk.lam is not None:
@@ -257,6 +324,8 @@ def time_block(seq=8192, batch=1, schedules=("atomic", "serial", "shift_fill", "
             p.grad = None
         out = blk(x, sched, causal)
         out.backward(gout)
+        if clip is not None:
+            blk.clip(clip)
 
     res = {}
     for sched in schedules:
@@ -282,6 +351,8 @@ def time_block(seq=8192, batch=1, schedules=("atomic", "serial", "shift_fill", "
     out["config"] = {"seq": seq, "batch": batch, "causal": causal, "hidden": 4096,
                      "heads": 32, "kv_heads": 8, "head_dim": 128, "ffn": 14336,
                      "steps": steps, "warmup": warmup, **options}
+    if clip is not None:
+        out["config"]["clip"] = clip
     return out
 
 
@@ -299,12 +370,22 @@ def main():
                     help="with --fused-norms, a norm after each branch as well")
     ap.add_argument("--differential", nargs="?", type=float, const=0.8, metavar="WEIGHT",
                     help="differential attention, the second map's weight to begin with")
+    ap.add_argument("--qk-norm", action="store_true",
+                    help="with --rotary, a norm of every head of q and k before the turn")
+    ap.add_argument("--fused-dense", action="store_true",
+                    help="products with activation, gate and residual in their epilogue")
+    ap.add_argument("--clip", nargs="?", type=float, const=1.0, metavar="NORM",
+                    help="clip the gradients to this norm")
     args = ap.parse_args()
     options = {k: v for k, v in (("rotary", args.rotary), ("fused_norms", args.fused_norms),
                                  ("post_norms", args.post_norms),
-                                 ("differential", args.differential)) if v not in (None, False)}
+                                 ("differential", args.differential),
+                                 ("qk_norm", args.qk_norm), ("fused_dense", args.fused_dense),
+                                 ("clip", args.clip)) if v not in (None, False)}
     if args.post_norms and not args.fused_norms:
         ap.error("--post-norms needs --fused-norms")
+    if args.qk_norm and args.rotary is None:
+        ap.error("--qk-norm needs --rotary")
     print(json.dumps(time_block(args.seq, args.batch, steps=args.steps, warmup=args.warmup,
                                 **options)))
 
