@@ -210,14 +210,12 @@ dash_status_t launch(const Product &p, const Rows (&a)[2], const Rows (&b)[2], b
   return launch_dense(f16, ta, tb, d, sms, s) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
 }
 
-bool vec_rows(const void *p, long long stride) { return !p || (aligned16(p) && stride % 8 == 0); }
-
 // ------------------------------------------------------------------ forward
 struct Fwd {
   Product p;
   Few few;
   Rows x, w[2], res;
-  Out y, z, g;
+  Out y;
   size_t need;
 };
 dash_status_t check_fwd(const dash_dense_fwd_t *a, Fwd &f) {
@@ -226,10 +224,10 @@ dash_status_t check_fwd(const dash_dense_fwd_t *a, Fwd &f) {
   if (a->act < DASH_ACT_NONE || a->act > DASH_ACT_SILU) return DASH_ERR_INVALID;
   if (a->dtype != DASH_BF16 && a->dtype != DASH_FP16)
     return a->dtype == DASH_FP32 ? DASH_ERR_UNSUPPORTED : DASH_ERR_INVALID;
-  const void *all[] = {a->x, a->w, a->w_gate, a->bias, a->bias_gate, a->residual, a->y, a->z,
-                       a->gate};
+  const void *all[] = {a->x, a->w, a->w_gate, a->bias, a->bias_gate, a->residual, a->y};
   for (const void *t : all)
     if (!aligned2(t)) return DASH_ERR_INVALID;
+  if (!aligned16(a->z) || !aligned16(a->gate)) return DASH_ERR_INVALID;
   if ((a->bias_gate || a->gate) && !a->w_gate) return DASH_ERR_INVALID;
   if (a->M > 1 && a->y_stride < a->N) return DASH_ERR_INVALID;
   const bool kn = a->order == DASH_DENSE_KN;
@@ -242,13 +240,11 @@ dash_status_t check_fwd(const dash_dense_fwd_t *a, Fwd &f) {
   f.w[1] = Rows(a->w_gate, a->w_gate_stride, f.w[0].rows, f.w[0].cols);
   f.res = Rows(a->residual, a->residual_stride, a->M, a->N);
   f.y = Out(a->y, a->y_stride, a->M, a->N);
-  f.z = Out(a->z, a->N, a->M, a->N);
-  f.g = Out(a->gate, a->N, a->M, a->N);
   f.need = kStatusBytes + f.x.bytes() + f.w[0].bytes() + f.w[1].bytes();
   if (a->M <= kFewRows)  // (which needs no more room)
     f.few = plan_few(a->M, a->N, a->K, gated);
   else
-    f.need += f.p.part_bytes() + f.res.bytes() + f.y.bytes() + f.z.bytes() + f.g.bytes();
+    f.need += f.p.part_bytes() + f.res.bytes() + f.y.bytes();
   return DASH_OK;
 }
 
@@ -267,10 +263,11 @@ dash_status_t check_bwd(const dash_dense_bwd_t *a, Bwd &b) {
   if (a->act < DASH_ACT_NONE || a->act > DASH_ACT_SILU) return DASH_ERR_INVALID;
   if (a->dtype != DASH_BF16 && a->dtype != DASH_FP16)
     return a->dtype == DASH_FP32 ? DASH_ERR_UNSUPPORTED : DASH_ERR_INVALID;
-  const void *all[] = {a->dy, a->x, a->w, a->w_gate, a->z, a->gate, a->dx, a->dw, a->dw_gate,
-                       a->dbias, a->dbias_gate};
+  const void *all[] = {a->dy, a->x, a->w, a->w_gate, a->dx, a->dw, a->dw_gate, a->dbias,
+                       a->dbias_gate};
   for (const void *t : all)
     if (!aligned2(t)) return DASH_ERR_INVALID;
+  if (!aligned16(a->z) || !aligned16(a->gate)) return DASH_ERR_INVALID;
   const bool kn = a->order == DASH_DENSE_KN, gated = a->gate != nullptr;
   b.grads = a->act != DASH_ACT_NONE || gated;
   if (b.grads && !a->z) return DASH_ERR_INVALID;
@@ -334,8 +331,8 @@ dash_status_t dash_dense_fwd(const dash_dense_fwd_t *a, void *workspace, size_t 
   if (st != DASH_OK) return st;
   if (!workspace || !aligned16(workspace) || workspace_bytes < f.need) return DASH_ERR_WORKSPACE;
   const Rows y(a->y, a->y_stride, a->M, a->N);
-  const long long kept = (long long)a->M * a->N;
-  const Bytes outs[] = {y.lies(), bytes_of(a->z, 2, kept), bytes_of(a->gate, 2, kept),
+  const long long kept = 3LL * a->M * kept_stride(a->N);
+  const Bytes outs[] = {y.lies(), bytes_of(a->z, 1, kept), bytes_of(a->gate, 1, kept),
                         bytes_of(workspace, 1, (long long)f.need)};
   const Bytes reads[] = {f.x.lies(), f.w[0].lies(), f.w[1].lies(), bytes_of(a->bias, 2, a->N),
                          bytes_of(a->bias_gate, 2, a->N)};
@@ -353,9 +350,11 @@ dash_status_t dash_dense_fwd(const dash_dense_fwd_t *a, void *workspace, size_t 
   DenseEpilogue e{};
   e.bias = a->bias, e.bias_gate = a->bias_gate;
   e.act = a->act, e.gated = f.p.gated;
+  e.z = kept_at(a->z, a->M, a->N), e.g = kept_at(a->gate, a->M, a->N);
+  e.ks = kept_stride(a->N);
   if (f.few.split) {
-    e.y = a->y, e.z = a->z, e.g = a->gate, e.residual = a->residual;
-    e.ys = a->y_stride, e.zs = e.gs = a->N, e.rs = a->residual_stride;
+    e.y = a->y, e.residual = a->residual;
+    e.ys = a->y_stride, e.rs = a->residual_stride;
     CUtensorMap tw[2], tx;
     for (int i = 0; i < 2; ++i)
       if (!make_rows_map(&tw[i], f.w[i].at ? f.w[i] : f.w[0], kn ? 64 : 128, f16))
@@ -374,14 +373,14 @@ dash_status_t dash_dense_fwd(const dash_dense_fwd_t *a, void *workspace, size_t 
   }
   float *part = static_cast<float *>(arena.take(f.p.part_bytes()));
   if (!place(f.res, arena, s)) return DASH_ERR_CUDA;
-  for (Out *o : {&f.y, &f.z, &f.g}) o->place(arena);
-  e.y = f.y.at, e.z = f.z.at, e.g = f.g.at, e.residual = f.res.at;
-  e.ys = f.y.stride, e.zs = f.z.stride, e.gs = f.g.stride, e.rs = f.res.stride;
+  f.y.place(arena);
+  e.y = f.y.at, e.residual = f.res.at;
+  e.ys = f.y.stride, e.rs = f.res.stride;
   const Rows x[2] = {f.x, Rows()};
   st = launch(f.p, x, f.w, false, kn, false, false, e, nullptr, 0, part, workspace, true, f16,
               dev.sms, s);
   if (st != DASH_OK) return st;
-  return f.y.finish(s) && f.z.finish(s) && f.g.finish(s) ? DASH_OK : DASH_ERR_CUDA;
+  return f.y.finish(s) ? DASH_OK : DASH_ERR_CUDA;
 }
 
 size_t dash_dense_bwd_workspace_bytes(const dash_dense_bwd_t *args) {
@@ -399,7 +398,7 @@ dash_status_t dash_dense_bwd(const dash_dense_bwd_t *a, void *workspace, size_t 
   const bool kn = a->order == DASH_DENSE_KN, gated = a->gate != nullptr,
              f16 = a->dtype == DASH_FP16;
   const int wr = kn ? a->K : a->N, wc = kn ? a->N : a->K;
-  const long long kept = (long long)a->M * a->N;
+  const long long kept = 3LL * a->M * kept_stride(a->N);
   const Rows dw(a->dw, a->dw_stride, wr, wc), dwg(a->dw_gate, a->dw_gate_stride, wr, wc);
   const Bytes outs[] = {Rows(a->dx, a->dx_stride, a->M, a->K).lies(), dw.lies(), dwg.lies(),
                         bytes_of(a->dbias, 2, a->N), bytes_of(a->dbias_gate, 2, a->N),
@@ -407,7 +406,7 @@ dash_status_t dash_dense_bwd(const dash_dense_bwd_t *a, void *workspace, size_t 
   const Bytes reads[] = {b.dy.lies(), Rows(a->x, a->x_stride, a->M, a->K).lies(),
                          Rows(a->w, a->w_stride, wr, wc).lies(),
                          Rows(a->w_gate, a->w_gate_stride, wr, wc).lies(),
-                         bytes_of(a->z, 2, kept), bytes_of(a->gate, 2, kept)};
+                         bytes_of(a->z, 1, kept), bytes_of(a->gate, 1, kept)};
   if (!apart(outs, reads)) return DASH_ERR_INVALID;
   DevInfo dev;
   if ((st = device_info(&dev)) != DASH_OK) return st;
@@ -431,13 +430,14 @@ dash_status_t dash_dense_bwd(const dash_dense_bwd_t *a, void *workspace, size_t 
   if (b.grads || a->dbias) {
     DenseGradParams g{};
     g.dy = a->dy;
-    if (b.grads) g.z = a->z, g.g = a->gate;
+    if (b.grads)
+      g.z = kept_at(const_cast<void *>(a->z), a->M, a->N),
+      g.g = kept_at(const_cast<void *>(a->gate), a->M, a->N);
     g.dz = dz_at, g.dg = dg_at;
     g.part = sum, g.part_gate = sum_gate;
-    g.dys = b.dy.stride, g.zs = g.gs = a->N, g.ds = up(a->N, 8);
+    g.dys = b.dy.stride, g.ks = kept_stride(a->N), g.ds = up(a->N, 8);
     g.M = a->M, g.N = a->N, g.act = a->act, g.chunk = b.chunk;
-    g.vec = a->N % 8 == 0 && vec_rows(a->dy, b.dy.stride) && vec_rows(a->z, a->N) &&
-            vec_rows(a->gate, a->N);
+    g.vec = aligned16(a->dy) && b.dy.stride % 8 == 0;
     if (launch_dense_grad(f16, g, b.chunks, s) != cudaSuccess) return DASH_ERR_CUDA;
     if ((sum || sum_gate) && launch_dense_sums(f16, sum, sum_gate, a->dbias, a->dbias_gate,
                                                b.chunks, a->N, s) != cudaSuccess)

@@ -15,12 +15,26 @@ namespace dash {
 constexpr int kDenseM = 256;   // rows of a tile, of a pair of CTAs
 constexpr int kDenseK = 64;    // contraction elements of a stage
 
+// What the backward needs of z and g is kept in three bytes an element, the upper 24 bits of the fp32
+// value: with 16 bits their rounding alone would make a third of the gradients' squared error.  Rows of
+// `stride` (N rounded up to 16) 16-bit words, then as many rows of bytes.
+struct DenseKept {
+  uint16_t *hi;  // null: not kept
+  uint8_t *lo;
+};
+inline long long kept_stride(long long N) { return (N + 15) / 16 * 16; }
+inline DenseKept kept_at(void *p, long long M, long long N) {
+  return {static_cast<uint16_t *>(p),
+          p ? static_cast<uint8_t *>(p) + 2 * M * kept_stride(N) : nullptr};
+}
+
 // What follows the product: y = residual + act(z) * g, with z = product + bias (and g likewise,
 // gated); z and g kept where asked for.
 struct DenseEpilogue {
-  void *y, *z, *g;
+  void *y;
+  DenseKept z, g;
   const void *bias, *bias_gate, *residual;
-  long long ys, zs, gs, rs;  // row strides in elements; the product kernel wants 16-byte steps
+  long long ys, ks, rs;  // row strides in elements; the product kernel wants 16-byte steps
   int act, gated;
 };
 struct DenseParams {
@@ -57,12 +71,13 @@ struct DenseFewParams {
 
 // dz = dy g act'(z), dgate = dy act(z) and their sums over rows.
 struct DenseGradParams {
-  const void *dy, *z, *g;    // z null: dz = dy (and is not written); g null: not gated
+  const void *dy;
+  DenseKept z, g;            // no z: dz = dy (and is not written); no g: not gated
   void *dz, *dg;             // null where only the sums are wanted
   float *part, *part_gate;   // [chunks][N]; null where the sums are not wanted
-  long long dys, zs, gs, ds;
+  long long dys, ks, ds;
   int M, N, act, chunk;      // rows of a chunk
-  int vec;
+  int vec;                   // dy lies on 16 bytes
 };
 
 cudaError_t launch_dense(bool f16, const CUtensorMap (&ta)[2], const CUtensorMap (&tb)[2],

@@ -285,6 +285,27 @@ __device__ __forceinline__ void add_cols(const void *base, long long at, float (
   for (int e = 0; e < C; ++e)
     if (e < left) v[e] += to_f32<T>(src[e]);
 }
+// The upper 24 bits of four values: two words of their upper halves and one of the bytes below.
+__device__ __forceinline__ void split24(const float (&v)[4], uint32_t &h0, uint32_t &h1, uint32_t &l) {
+  uint32_t b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(v[i]);
+  h0 = __byte_perm(b[0], b[1], 0x7632);
+  h1 = __byte_perm(b[2], b[3], 0x7632);
+  l = __byte_perm(__byte_perm(b[0], b[1], 0x0051), __byte_perm(b[2], b[3], 0x0051), 0x5410);
+}
+__device__ __forceinline__ float join24(uint32_t hi, uint32_t lo) {
+  return __uint_as_float(hi << 16 | lo << 8);
+}
+// Four values of a row from column n on (rows have room for whole groups of four).
+__device__ __forceinline__ void keep_cols(const DenseKept &k, long long stride, long long row, int n,
+                                          const float (&v)[4]) {
+  uint32_t h0, h1, l;
+  split24(v, h0, h1, l);
+  *reinterpret_cast<uint2 *>(k.hi + row * stride + n) = make_uint2(h0, h1);
+  *reinterpret_cast<uint32_t *>(k.lo + row * stride + n) = l;
+}
+
 // A bias, the same for all rows of a warp.
 template <typename T>
 __device__ __forceinline__ void add_bias(const void *base, int n, float (&v)[32], int left, int lane) {
@@ -380,6 +401,45 @@ __device__ __forceinline__ void turn_fill(uint8_t *buf, const uint4 (&v)[4], int
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     *reinterpret_cast<uint4 *>(turn_at(buf, 8 * i + (lane >> 2), lane & 3)) = v[i];
+}
+
+// 32 rows of 32 values, a thread a row, to rows [row0, row0 + rows) of what is kept, from column n on:
+// the words through one buffer, the bytes (32 a row, in two pieces) through the other.
+__device__ __forceinline__ void turn_keep(uint8_t *words, uint8_t *bytes, const DenseKept &k,
+                                          long long stride, long long row0, int rows, int n, int lane,
+                                          const float (&v)[32]) {
+  uint32_t h[16], l[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float f[4] = {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+    split24(f, h[2 * i], h[2 * i + 1], l[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<uint4 *>(turn_at(words, lane, i)) =
+        make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+  auto byte_at = [&](int row, int piece) { return bytes + row * 32 + ((piece ^ (row >> 2 & 1)) << 4); };
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    *reinterpret_cast<uint4 *>(byte_at(lane, i)) =
+        make_uint4(l[4 * i], l[4 * i + 1], l[4 * i + 2], l[4 * i + 3]);
+  __syncwarp();
+  const int c = lane & 3, room = (int)stride - n;  // (a multiple of 16)
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 2);
+    if (r < rows && 8 * c < room)
+      *reinterpret_cast<uint4 *>(k.hi + (row0 + r) * stride + n + 8 * c) =
+          *reinterpret_cast<const uint4 *>(turn_at(words, r, c));
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = 16 * i + (lane >> 1), d = lane & 1;
+    if (r < rows && 16 * d < room)
+      *reinterpret_cast<uint4 *>(k.lo + (row0 + r) * stride + n + 16 * d) =
+          *reinterpret_cast<const uint4 *>(byte_at(r, d));
+  }
+  __syncwarp();
 }
 
 __device__ __forceinline__ void load32(uint32_t taddr, float (&v)[32]) {
@@ -595,30 +655,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int c = c0; c < c1; c += 32) {
           const int at = n0 + c, left = p.N - at;
           if (left <= 0) break;
-          // (the buffers alternate: a barrier lies between a buffer's reads and its next filling)
+          // (a barrier lies between a buffer's reads and its next filling)
           float z[32], g[32];
           load32(acc + c, z);
           if (e.gated) load32(acc + p.bn / 2 + c, g);
           if (e.bias) add_bias<T>(e.bias, at, z, left, lane);
-          if (e.z) {
-            turn_put<T>(turn, lane, z);
-            __syncwarp();
-            turn_store<T>(turn, e.z, e.zs, row0, rows, at, left, lane);
-          }
+          if (e.z.hi) turn_keep(turn, turn2, e.z, e.ks, row0, rows, at, lane, z);
           if (e.gated) {
             if (e.bias_gate) add_bias<T>(e.bias_gate, at, g, left, lane);
-            if (e.g) {
-              turn_put<T>(turn2, lane, g);
-              __syncwarp();
-              turn_store<T>(turn2, e.g, e.gs, row0, rows, at, left, lane);
-            }
+            if (e.g.hi) turn_keep(turn, turn2, e.g, e.ks, row0, rows, at, lane, g);
           }
           activate(e.act, z);
           if (e.gated) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) z[i] *= g[i];
           }
-          __syncwarp();
           if (e.residual) {
             turn_fill(turn, next, lane);
             if (c + 32 < c1 && left > 32)
@@ -656,11 +707,11 @@ __device__ __forceinline__ void finish4(const DenseEpilogue &e, void *y, long lo
                                         int n, int N, float (&z)[4], float (&g)[4]) {
   const int left = N - n;
   if (e.bias) add_cols<T, 4>(e.bias, n, z, left);
-  if (e.z) store_cols<T, 4>(e.z, row * e.zs + n, z, left);
+  if (e.z.hi) keep_cols(e.z, e.ks, row, n, z);
   activate(e.act, z);
   if (e.gated) {
     if (e.bias_gate) add_cols<T, 4>(e.bias_gate, n, g, left);
-    if (e.g) store_cols<T, 4>(e.g, row * e.gs + n, g, left);
+    if (e.g.hi) keep_cols(e.g, e.ks, row, n, g);
 #pragma unroll
     for (int k = 0; k < 4; ++k) z[k] *= g[k];
   }
@@ -832,38 +883,58 @@ __global__ void __launch_bounds__(kFewThreads)
 }
 
 // ------------------------------------------------------------------ dz, dgate and their sums
-// 32 threads a strip of 32 V columns, 8 rows at a time over a chunk of rows; the eight rows'
-// sums are added in order through shared memory.
-template <typename T, int V, int kAct, bool kSums>
+// 32 threads a strip of 256 columns, 8 rows at a time over a chunk of rows; the eight rows' sums are
+// added in order through shared memory.
+template <typename T, int kAct, bool kSums>
 __global__ void __launch_bounds__(256, kSums ? 3 : 4)
     dense_grad_kernel(const __grid_constant__ DenseGradParams p) {
+  constexpr int V = 8;
   const int lane = threadIdx.x & 31, by = threadIdx.x >> 5;
   const int n = (blockIdx.x * 32 + lane) * V;
   const int r1 = min(p.M, (int)(blockIdx.y + 1) * p.chunk);
+  const bool whole = p.vec && n + V <= p.N;
   float sz[V] = {}, sg[V] = {};
+  auto kept = [&](const DenseKept &k, long long r, uint4 &h, uint2 &l) {
+    h = *reinterpret_cast<const uint4 *>(k.hi + r * p.ks + n);
+    l = *reinterpret_cast<const uint2 *>(k.lo + r * p.ks + n);
+  };
+  auto values = [](const uint4 &h, const uint2 &l, float (&f)[V]) {
+    const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[2] = {l.x, l.y};
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      f[e] = join24(hw[e / 2] >> (16 * (e & 1)), (lw[e / 4] >> (8 * (e & 3))) & 0xffu);
+  };
   if (n < p.N) {
     for (long long r = blockIdx.y * p.chunk + by; r < r1; r += 8) {
       float dy[V], z[V], g[V];
-      Pack<T, V> z_, g_;
-      const Pack<T, V> dy_ = load_pack<T, V>(static_cast<const T *>(p.dy) + r * p.dys + n);
-      if (p.z) z_ = load_pack<T, V>(static_cast<const T *>(p.z) + r * p.zs + n);
-      if (p.g) g_ = load_pack<T, V>(static_cast<const T *>(p.g) + r * p.gs + n);
-      unpack<T, V>(dy_, dy);
-      if (p.z) {
-        unpack<T, V>(z_, z);
-        if (p.g) unpack<T, V>(g_, g);
+      uint4 zh, gh;
+      uint2 zl, gl;
+      Pack<T, V> d;
+      const T *src = static_cast<const T *>(p.dy) + r * p.dys + n;
+      if (whole) {
+        d = load_pack<T, V>(src);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) d.e[e] = n + e < p.N ? src[e] : from_f32<T>(0.f);
+      }
+      if (p.z.hi) kept(p.z, r, zh, zl);
+      if (p.g.hi) kept(p.g, r, gh, gl);
+      unpack<T, V>(d, dy);
+      if (p.z.hi) {
+        values(zh, zl, z);
+        if (p.g.hi) values(gh, gl, g);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           float slope;
           const float a = activation<kAct>(z[e], slope);
           z[e] = dy[e] * slope;
-          if (p.g) {
+          if (p.g.hi) {
             z[e] *= g[e];
             g[e] = dy[e] * a;
           }
         }
         if (p.dz) store_pack<T, V>(static_cast<T *>(p.dz) + r * p.ds + n, pack<T, V>(z));
-        if (p.g && p.dg) store_pack<T, V>(static_cast<T *>(p.dg) + r * p.ds + n, pack<T, V>(g));
+        if (p.g.hi && p.dg) store_pack<T, V>(static_cast<T *>(p.dg) + r * p.ds + n, pack<T, V>(g));
       } else {
 #pragma unroll
         for (int e = 0; e < V; ++e) z[e] = dy[e];
@@ -872,7 +943,7 @@ __global__ void __launch_bounds__(256, kSums ? 3 : 4)
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           sz[e] += z[e];
-          if (p.g) sg[e] += g[e];
+          if (p.g.hi) sg[e] += g[e];
         }
       }
     }
@@ -970,22 +1041,17 @@ cudaError_t launch_few_t(const CUtensorMap &tw0, const CUtensorMap &tw1, const C
   return cudaLaunchKernelEx(&c, dense_few_kernel<T>, tw0, tw1, tx, p);
 }
 
-template <typename T, int V, int kAct>
+template <typename T, int kAct>
 void launch_grad_t(const DenseGradParams &p, int chunks, cudaStream_t s) {
-  const dim3 grid((p.N + 32 * V - 1) / (32 * V), chunks);
+  const dim3 grid((p.N + 255) / 256, chunks);
   if (p.part || p.part_gate)
-    dense_grad_kernel<T, V, kAct, true><<<grid, 256, 0, s>>>(p);
+    dense_grad_kernel<T, kAct, true><<<grid, 256, 0, s>>>(p);
   else
-    dense_grad_kernel<T, V, kAct, false><<<grid, 256, 0, s>>>(p);
+    dense_grad_kernel<T, kAct, false><<<grid, 256, 0, s>>>(p);
 }
 template <int kAct>
 cudaError_t launch_grad(bool f16, const DenseGradParams &p, int chunks, cudaStream_t s) {
-  if (f16)
-    p.vec ? launch_grad_t<__half, 8, kAct>(p, chunks, s)
-          : launch_grad_t<__half, 1, kAct>(p, chunks, s);
-  else
-    p.vec ? launch_grad_t<__nv_bfloat16, 8, kAct>(p, chunks, s)
-          : launch_grad_t<__nv_bfloat16, 1, kAct>(p, chunks, s);
+  f16 ? launch_grad_t<__half, kAct>(p, chunks, s) : launch_grad_t<__nv_bfloat16, kAct>(p, chunks, s);
   return cudaGetLastError();
 }
 

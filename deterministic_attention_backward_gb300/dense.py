@@ -66,6 +66,10 @@ def _weights(x, w, w_gate, act):
     return rows, K, N, order, ws, gs
 
 
+def _kept_bytes(rows, N):
+    return 3 * rows * ((N + 15) // 16 * 16)
+
+
 def _biases(x, N, w_gate, bias, bias_gate):
     for b, n in ((bias, "bias"), (bias_gate, "bias_gate")):
         if b is not None:
@@ -106,9 +110,9 @@ def dense_fwd_workspace_bytes(x, w, *, w_gate=None) -> int:
 def dense_fwd(x, w, bias=None, *, act: str = "none", w_gate=None, bias_gate=None, residual=None,
               keep: bool = True, out=None, workspace=None, stream=None, check: bool = False):
     """y = residual + act(x w + bias), or residual + act(x w + bias) (x w_gate + bias_gate): returns
-    (y [..., N], kept).  ``kept`` is what ``dense_bwd`` needs besides: x w + bias rounded to x's type,
-    [2, ..., N] with x w_gate + bias_gate behind it where there is a gate; None for ``act`` "none"
-    without a gate, or ``keep=False``.  ``out`` may be the residual itself (at its strides).  A
+    (y [..., N], kept).  ``kept`` is what ``dense_bwd`` needs besides, x w + bias and, where there is a
+    gate, x w_gate + bias_gate: 24 bits of each value in a uint8 tensor of the library's layout; None
+    for ``act`` "none" without a gate, or ``keep=False``.  ``out`` may be the residual itself (at its strides).  A
     ``workspace`` serves one call at a time."""
     rows, K, N, order, shape, strides = _fwd_args(x, w, bias, act, w_gate, bias_gate, residual, out,
                                                   keep)
@@ -117,16 +121,16 @@ def dense_fwd(x, w, bias=None, *, act: str = "none", w_gate=None, bias_gate=None
         y = torch.empty(shape, dtype=x.dtype, device=x.device) if out is None else out
         kept = None
         if keep and (act != "none" or w_gate is not None):
-            kept = torch.empty(shape if w_gate is None else (2, *shape), dtype=x.dtype,
-                               device=x.device)
+            kept = torch.empty((1 if w_gate is None else 2, _kept_bytes(rows, N)),
+                               dtype=torch.uint8, device=x.device)
         if rows == 0:
             return y, kept
-        z = kept if w_gate is None or kept is None else kept[0]
-        g = None if w_gate is None or kept is None else kept[1]
+        z = _ptr(kept) or 0
+        g = z + kept.shape[1] if z and w_gate is not None else 0
         L = lib()
         a = _FWD.pack(x.data_ptr(), w.data_ptr(), _ptr(w_gate) or 0, _ptr(bias) or 0,
-                      _ptr(bias_gate) or 0, _ptr(residual) or 0, y.data_ptr(), _ptr(z) or 0,
-                      _ptr(g) or 0, *strides, rows, K, N, order, ACTIVATIONS[act], DTYPES[x.dtype])
+                      _ptr(bias_gate) or 0, _ptr(residual) or 0, y.data_ptr(), z, g, *strides,
+                      rows, K, N, order, ACTIVATIONS[act], DTYPES[x.dtype])
         ws = scratch(L.dash_dense_fwd_workspace_bytes(a) or 256, x, workspace)
         _check(L.dash_dense_fwd(a, ws.data_ptr(), ws.numel() * ws.element_size(), handle),
                "dash_dense_fwd")
@@ -147,7 +151,7 @@ def _bwd_args(dy, x, w, kept, act, w_gate, bias, bias_gate, dx, dw, dw_gate):
     if act != "none" or gated:
         if kept is None:
             raise ValueError("the gradient needs what the forward kept")
-        alike(kept, "kept", x, (2, *shape) if gated else shape)
+        alike(kept, "kept", x, (1 + gated, _kept_bytes(rows, N)), torch.uint8)
         contiguous(kept, "kept")
     dxs = 0 if dx is None else _out(dx, "dx", x)
     dws = dgs = 0
@@ -168,7 +172,8 @@ def _bwd_pack(dy, x, w, kept, act, w_gate, dx, dw, dw_gate, db, dbg, rows, K, N,
     gated = w_gate is not None
     z = g = 0
     if act != "none" or gated:
-        z, g = (kept[0].data_ptr(), kept[1].data_ptr()) if gated else (kept.data_ptr(), 0)
+        z = kept.data_ptr()
+        g = z + kept.shape[1] if gated else 0
     return _BWD.pack(dy.data_ptr(), x.data_ptr(), w.data_ptr(), _ptr(w_gate) or 0, z, g, dx, dw,
                      dw_gate, db, dbg, *strides, rows, K, N, order, ACTIVATIONS[act],
                      DTYPES[x.dtype])

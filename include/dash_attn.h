@@ -459,7 +459,9 @@ dash_status_t dash_diff_withhold(int kernel, int block);
  * without w_gate y = residual + act(z); bias, bias_gate, residual may be NULL.  x [M, K] and y,
  * residual [M, N] are rows at a stride (in elements); w and w_gate are [K, N] rows (DASH_DENSE_KN)
  * or [N, K] rows (DASH_DENSE_NK); biases [N] contiguous, of the rows' type.  z and gate, where not
- * NULL, receive z and g as contiguous [M, N] rows for the backward.  y may be the residual itself
+ * NULL, receive z and g for the backward, the upper 24 bits of their fp32 values: M rows of 16-bit words
+ * (the upper ones), then M rows of bytes, Np elements each, Np = N rounded up to 16 (3 M Np bytes in all,
+ * on 16 bytes).  y may be the residual itself
  * (at its stride); beside that no output shares memory with another tensor of the call.  Sums run
  * in an order that the sizes fix, one rounding at the end.  Operands that do not begin on 16 bytes,
  * or whose stride is no multiple of that, are copied into the workspace first.
@@ -484,7 +486,7 @@ size_t dash_dense_fwd_workspace_bytes(const dash_dense_fwd_t *args);
 dash_status_t dash_dense_fwd(const dash_dense_fwd_t *args, void *workspace, size_t workspace_bytes,
                              dash_stream_t stream);
 /* Gradient: from dy [M, N], x, the weights and what the forward kept (z where act is not NONE or
- * there is a gate, gate with it; both as the forward rounded them)
+ * there is a gate, gate with it; both as the forward kept them)
  *   dz = dy g act'(z)   dgate = dy act(z)
  *   dx = dz w^T + dgate w_gate^T   dw = x^T dz   dw_gate = x^T dgate   dbias, dbias_gate = sums
  * each where its pointer is not NULL (dw and dw_gate in the weights' order).  dz and dgate are

@@ -76,6 +76,14 @@ def weight(K, N, order, dtype, seed):
     return w if order == "kn" else w.t().contiguous().t()
 
 
+def unpacked(kept, rows, N):
+    """What the forward kept, as fp32 [1 or 2, rows, N]: words of the upper 16 bits, bytes below."""
+    Np = (N + 15) // 16 * 16
+    hi = kept[:, :2 * rows * Np].contiguous().view(torch.int16).view(-1, rows, Np).int() << 16
+    lo = kept[:, 2 * rows * Np:].reshape(-1, rows, Np).int() << 8
+    return (hi | lo)[..., :N].contiguous().view(torch.float32)
+
+
 def check_forward(x, w, y, kept, act, bias=None, w_gate=None, bias_gate=None, residual=None):
     dt, K = x.dtype, x.shape[-1]
     X = x.double()
@@ -99,9 +107,11 @@ def check_forward(x, w, y, kept, act, bias=None, w_gate=None, bias_gate=None, re
         ta = ta + 2.0 ** -23 * a.abs()
     inside(y, a, rounded(a, ta, dt), "y")
     if kept is not None:
-        inside(kept[0] if w_gate is not None else kept, z, rounded(z, tz, dt), "z")
+        # cut off after 24 bits: 2^-15 of the value at most
+        k = unpacked(kept, X.shape[0], w.shape[1])
+        inside(k[0], z, tz + 2.0 ** -15 * (z.abs() + tz), "z")
         if w_gate is not None:
-            inside(kept[1], g, rounded(g, tg, dt), "g")
+            inside(k[1], g, tg + 2.0 ** -15 * (g.abs() + tg), "g")
 
 
 def check_backward(dy, x, w, kept, grads, act, bias=None, w_gate=None, bias_gate=None):
@@ -114,13 +124,14 @@ def check_backward(dy, x, w, kept, grads, act, bias=None, w_gate=None, bias_gate
         parts.append((D, torch.zeros_like(D), W, dw, db))
         e = 0.0
     else:
-        z = (kept[0] if w_gate is not None else kept).double().reshape(-1, N)
+        k = unpacked(kept, M, N).double()
+        z = k[0]
         a, slope = act_of(z, act)
         lost = 2.0 ** -19 * D.abs() * (z.abs() + 1) * (act != "none")
         if w_gate is None:
             parts.append((D * slope, lost, W, dw, db))
         else:
-            g = kept[1].double().reshape(-1, N)
+            g = k[1]
             parts.append((D * slope * g, lost * g.abs() + 2.0 ** -22 * (D * slope * g).abs(), W, dw,
                           db))
             parts.append((D * a, lost + 2.0 ** -23 * (D * a).abs(), w_gate.double(), dwg, dbg))
@@ -164,7 +175,7 @@ def test_abi_refusals(L):
         a = _FWD.pack(x, w, wg, b, bg, r, y, z, g, *strides, M, K, N, order, act, dtype)
         return L.dash_dense_fwd(a, ws, bytes, None)
     for bad in (dict(x=0), dict(w=0), dict(y=0), dict(M=0), dict(K=0), dict(N=-1), dict(order=2),
-                dict(act=5), dict(act=-1), dict(dtype=3), dict(x=at + 1), dict(bg=at), dict(g=at),
+                dict(act=5), dict(act=-1), dict(dtype=3), dict(x=at + 1), dict(z=5 * at + 8), dict(bg=at), dict(g=at),
                 dict(strides=(64, 64, 64, 64, 63)), dict(y=at), dict(y=2 * at), dict(y=64 * at),
                 dict(z=3 * at), dict(b=3 * at), dict(r=3 * at, strides=(64, 64, 64, 72, 64)),
                 dict(r=3 * at + 64)):
@@ -285,7 +296,8 @@ def test_views(L, order, offset):
     a["w_gate"] = wide_w(a["w_gate"])[1]
     big, out = wide(torch.zeros_like(y))
     got, kept2 = dash.dense_fwd(xv, wv, residual=rv, out=out, check=True, **a)
-    assert got is out and torch.equal(out, y) and torch.equal(kept2, kept)
+    assert got is out and torch.equal(out, y)
+    assert torch.equal(unpacked(kept2, M, N), unpacked(kept, M, N))
     assert (big == 7).sum() == big.numel() - out.numel() + (out == 7).sum()
     bx, dx = wide(torch.zeros_like(x))
     bw, dw = wide_w(torch.zeros_like(w))
@@ -314,7 +326,7 @@ def test_no_rows(L):
     x, w, a, _ = case(1, 40, 24, "kn", BF, ("gelu", True, True, False))
     x, dy = x[:0], torch.empty(0, 24, dtype=BF, device="cuda")
     y, kept = dash.dense_fwd(x, w, **a)
-    assert y.shape == (0, 24) and kept.shape == (2, 0, 24)
+    assert y.shape == (0, 24) and kept.shape == (2, 0)
     dx, *rest = dash.dense_bwd(dy, x, w, kept, **a)
     assert dx.shape == (0, 40) and all((t == 0).all() for t in rest)
 
@@ -382,7 +394,7 @@ def test_streams_graphs_and_workspaces(L):
         dy.copy_(make((M, N), BF, seed + 5))
         g.replay()
         y1, k1 = dash.dense_fwd(x, w, residual=r, **a)
-        assert torch.equal(y, y1) and torch.equal(kept, k1)
+        assert torch.equal(y, y1) and torch.equal(unpacked(kept, M, N), unpacked(k1, M, N))
         assert all(p is q or torch.equal(p, q)
                    for p, q in zip(got, dash.dense_bwd(dy, x, w, k1, **a)))
     dash.status(ws1), dash.status(ws2)
@@ -405,7 +417,9 @@ def test_refusals(L):
                 lambda: dash.dense_fwd(x, w, workspace=torch.empty(8, device="cuda")),
                 lambda: dash.dense_fwd(x, w[:, :0]), lambda: dash.dense_fwd(x[:, :0], w[:0]),
                 lambda: dash.dense_bwd(dy, x, w, act="silu"),
-                lambda: dash.dense_bwd(dy, x, w, kept[0], act="silu", w_gate=w),
+                lambda: dash.dense_bwd(dy, x, w, kept[:1], act="silu", w_gate=w),
+                lambda: dash.dense_bwd(dy, x, w, kept, act="silu"),
+                lambda: dash.dense_bwd(dy, x, w, kept.char(), act="silu", w_gate=w),
                 lambda: dash.dense_bwd(dy[:3], x, w), lambda: dash.dense_bwd(dy, x, w, dw_gate=w),
                 lambda: dash.dense_bwd(dy, x, w, dw=torch.empty_like(w).t().contiguous().t()),
                 lambda: dash.dense_bwd(dy.half(), x, w)):
