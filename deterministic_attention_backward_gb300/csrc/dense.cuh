@@ -46,6 +46,7 @@ struct DenseParams {
   int clear;                 // the status block (the first product of a call does)
   unsigned long long wait_ns;
   int M, N;
+  int group;                 // rows of tiles that are worked through together
   int mt, nt, bn;            // tiles; bn columns of a tile's accumulator (gated: half z, half g)
   int nk, parts, outs;       // blocks of kDenseK of a part
   int whole, splits, per;    // tiles that are whole; splits of each other tile, blocks of a split

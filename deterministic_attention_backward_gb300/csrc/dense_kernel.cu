@@ -459,7 +459,7 @@ __device__ __forceinline__ void load32(uint32_t taddr, float (&v)[32]) {
 }
 
 // Work items: the first `whole` tiles, then `splits` items for each of the others.  Tiles go in
-// groups of 8 rows of tiles, so that those in flight share their operands in L2.
+// groups of `group` rows of tiles, so that those in flight share their operands in L2.
 struct Item {
   int m, n, out, k0, k1;
   int cut;  // of a split tile: its place in the partial sums, else -1
@@ -479,8 +479,9 @@ __device__ __forceinline__ Item item_of(const DenseParams &p, int t) {
   }
   const int tiles = p.mt * p.nt, r = t % tiles;
   w.out = t / tiles;
-  const int per = 8 * p.nt, g = r / per, in = r - g * per, rows = min(8, p.mt - 8 * g);
-  w.m = (8 * g + in % rows) * kDenseM;
+  const int per = p.group * p.nt, g = r / per, in = r - g * per;
+  const int rows = min(p.group, p.mt - p.group * g);
+  w.m = (p.group * g + in % rows) * kDenseM;
   w.n = in / rows;
   return w;
 }

@@ -32,28 +32,27 @@ def _list(grads, name="grads"):
     if isinstance(grads, Tensor):
         grads = (grads,)
     grads = [t for t in grads if t is not None]
-    device = None
-    for i, t in enumerate(grads):
-        if device is None:
-            tensor(t, f"{name}[{i}]", DTYPES)
-            device = t.device
-        elif not isinstance(t, Tensor) or t.device != device or t.dtype not in DTYPES:
-            tensor(t, f"{name}[{i}]", DTYPES)
-            raise ValueError(f"{name}[{i}] is on {t.device}, expected {device}")
-        if not t.is_contiguous() and not _dense(t):
-            raise ValueError(f"{name}[{i}] must be dense in memory, got strides {tuple(t.stride())}")
     if not grads:
         raise ValueError(f"{name} holds no tensor")
+    tensor(grads[0], f"{name}[0]", DTYPES)
+    device = grads[0].get_device()
+    for i, t in enumerate(grads):
+        if not isinstance(t, Tensor) or t.get_device() != device or t.dtype not in DTYPES:
+            tensor(t, f"{name}[{i}]", DTYPES)
+            raise ValueError(f"{name}[{i}] is on {t.device}, expected {grads[0].device}")
+        if not t.is_contiguous() and not _dense(t):
+            raise ValueError(f"{name}[{i}] must be dense in memory, got strides {tuple(t.stride())}")
     return grads
 
 
-def _pack(grads, outs):
-    buf = bytearray(_GRAD.size * len(grads))
-    at = 0
-    for t, o in zip(grads, outs):
-        _GRAD.pack_into(buf, at, t.data_ptr(), o.data_ptr(), t.numel(), DTYPES[t.dtype], 0)
-        at += _GRAD.size
-    return bytes(buf)
+def _pack(grads, outs=None):
+    """The tensors as an array of dash_grad_t."""
+    if outs is None:
+        rows = [(p, p, t.numel(), DTYPES[t.dtype], 0) for t in grads for p in (t.data_ptr(),)]
+    else:
+        rows = [(t.data_ptr(), o.data_ptr(), t.numel(), DTYPES[t.dtype], 0)
+                for t, o in zip(grads, outs)]
+    return b"".join([_GRAD.pack(*r) for r in rows])
 
 
 def _scalar(t, name, like):
@@ -79,7 +78,7 @@ def grad_norm(grads, *, out=None, workspace=None, stream=None):
         L, n = lib(), len(grads)
         norm = torch.empty((), dtype=torch.float32, device=like.device) if out is None else out
         ws = scratch(L.dash_grad_norm_workspace_bytes(n), like, workspace)
-        _check(L.dash_grad_norm(_pack(grads, grads), n, norm.data_ptr(), ws.data_ptr(),
+        _check(L.dash_grad_norm(_pack(grads), n, norm.data_ptr(), ws.data_ptr(),
                                 ws.numel() * ws.element_size(), handle), "dash_grad_norm")
         return norm
     return run(like, stream, launch)
@@ -97,7 +96,7 @@ def grad_clip(grads, max_norm: float, *, eps: float = 1e-6, norm=None, out=None,
         raise ValueError(f"max_norm and eps must not be negative, got {max_norm} and {eps}")
     if norm is not None:
         _scalar(norm, "norm", like)
-    outs = grads
+    outs = None
     if out is not None:
         outs = [o for o in ((out,) if isinstance(out, Tensor) else out) if o is not None]
         if len(outs) != len(grads):
