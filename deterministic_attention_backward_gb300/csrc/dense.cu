@@ -184,6 +184,13 @@ struct Out {
   }
 };
 
+// The limit of a wait.  A kernel's first CTA clears the status word that a wait which runs out sets: a
+// millisecond at least lies between.
+unsigned long long wait_limit_ns() {
+  const unsigned long long ns = g_wait_ns.load();
+  return ns > 1000000ull ? ns : 1000000ull;
+}
+
 // Launches a product of rows a[0..1], b[0..1] (the second ones where `parts` or `outs` or a gate
 // ask for them, otherwise empty).
 dash_status_t launch(const Product &p, const Rows (&a)[2], const Rows (&b)[2], bool a_mn, bool b_mn,
@@ -200,7 +207,7 @@ dash_status_t launch(const Product &p, const Rows (&a)[2], const Rows (&b)[2], b
   d.part = part;
   d.status = static_cast<uint32_t *>(workspace);
   d.clear = clear;
-  d.wait_ns = g_wait_ns.load();
+  d.wait_ns = wait_limit_ns();
   d.M = p.M, d.N = p.N;
   d.mt = p.mt(), d.nt = p.nt(), d.bn = p.bn;
   // 16 rows of tiles while A's part of them stays in L2 beside the rest (8192 x 4096 x 14336 567 -> 556 us
@@ -366,7 +373,7 @@ dash_status_t dash_dense_fwd(const dash_dense_fwd_t *a, void *workspace, size_t 
     DenseFewParams d{};
     d.e = e;
     d.status = static_cast<uint32_t *>(workspace);
-    d.wait_ns = g_wait_ns.load();
+    d.wait_ns = wait_limit_ns();
     d.M = f.p.M, d.N = f.p.N, d.nk = f.p.nk();
     d.cols = f.few.cols, d.split = f.few.split, d.per = f.few.per;
     d.stages = f.few.stages, d.stage = f.few.stage, d.smem = f.few.smem, d.tmem = f.few.tmem;

@@ -587,7 +587,7 @@ dash_status_t fill(HeadParams &p, bool &wide, Lay &lay, const dash_rope_part_t *
     wide = wide && aligned16(at) && (stride[0] | stride[1] | stride[2]) % vec == 0;
     return true;
   };
-  int turned = 0;
+  int turned = 0, wsizes[2] = {};  // elements of the weights
   for (int i = 0; i < nparts; ++i) {
     const dash_rope_part_t &q = parts[i];
     HeadPart &h = p.part[i];
@@ -613,6 +613,7 @@ dash_status_t fill(HeadParams &p, bool &wide, Lay &lay, const dash_rope_part_t *
     lay.x[i] = lies(from.in, from.in_stride, q.heads, q.D);
     lay.out[i] = lies(q.out, q.out_stride, q.heads, q.D);
     if (q.turn) {
+      wsizes[turned] = q.D;
       h.w = weights[turned++];
       if (reinterpret_cast<uintptr_t>(h.w) & (wsize - 1)) return DASH_ERR_INVALID;
     }
@@ -627,8 +628,7 @@ dash_status_t fill(HeadParams &p, bool &wide, Lay &lay, const dash_rope_part_t *
   const Bytes rest[4] = {
       bytes_of(inv_freq, 8, rot / 2),
       along(along(bytes_of(positions, psize, 1), psize, pos_stride_t, S), psize, pos_stride_b, B),
-      bytes_of(weights[0], wsize, weights[0] ? parts[0].D : 0),
-      bytes_of(weights[1], wsize, weights[1] && nparts > 1 ? parts[1].D : 0)};
+      bytes_of(weights[0], wsize, wsizes[0]), bytes_of(weights[1], wsize, wsizes[1])};
   for (int i = 0; i < nparts; ++i) {
     const dash_rope_part_t &q = parts[i];
     bool in_place = q.in == q.out;

@@ -202,8 +202,8 @@ def rope_bwd(dq, dk=None, dv=None, *, inv_freq, magnitude: float = 1.0, position
     return _rope((dq, dk, dv), inv_freq, magnitude, positions, start, layout, out, stream, True)
 
 
-def _head_weights(q, k, q_weight, k_weight):
-    """Check the norms' weights; returns their type."""
+def _head_weights(q, k, v, q_weight, k_weight):
+    """Check the norms' weights and the heads' size; returns the weights' type."""
     dtype = None
     for name, w, t in (("q_weight", q_weight, q), ("k_weight", k_weight, k)):
         if w is None:
@@ -216,9 +216,9 @@ def _head_weights(q, k, q_weight, k_weight):
                 raise ValueError(f"{name} must be {q.dtype} or torch.float32, got {dtype}")
         alike(w, name, q, t.shape[-1:], dtype)
         contiguous(w, name)
-    for name, t in (("q", q), ("k", k)):
+    for name, t in (("q", q), ("k", k), ("v", v)):
         if t is not None and t.shape[-1] > 512:
-            raise ValueError(f"{name} has heads of {t.shape[-1]}, 512 at most are normed")
+            raise ValueError(f"{name} has heads of {t.shape[-1]}, 512 at most are taken")
     return q.dtype if dtype is None else dtype
 
 
@@ -236,7 +236,7 @@ def rope_norm_fwd(q, k=None, v=None, *, q_weight=None, k_weight=None, inv_freq, 
     parts = (q, k, v)
     tokens, B, S, rot = _frequencies(q, inv_freq, layout)
     out = _parts(parts, out, q, tokens, rot)
-    wtype = _head_weights(q, k, q_weight, k_weight)
+    wtype = _head_weights(q, k, v, q_weight, k_weight)
     where, pos64, pb, pt = _positions(positions, start, q, tokens, S)
 
     def launch(handle):
@@ -283,7 +283,7 @@ def rope_norm_bwd(dq, dk, dv, q, k=None, *, q_weight=None, k_weight=None, inv_fr
         if g is not None:
             alike(x, "qk"[i], dq, g.shape)
             _heads(x, "qk"[i], dq, i, tokens, rot)
-    wtype = _head_weights(q, k, q_weight, k_weight)
+    wtype = _head_weights(q, k, dv, q_weight, k_weight)
     if q_weight is not None and k_weight is not None and q.shape[-1] != k.shape[-1]:
         raise ValueError("heads of q and k with weights must have one size")
     where, pos64, pb, pt = _positions(positions, start, dq, tokens, S)

@@ -127,7 +127,9 @@ def test_abi_refusals(L):
                 dict(parts=part(heads=0)), dict(parts=part(D=0)), dict(parts=part(turn=0)),
                 dict(parts=part(out=at + 32)), dict(parts=part(out=8 * at)),
                 dict(parts=part() + part(out=4 * at) + part(out=6 * at), n=3),
-                dict(parts=part() * 2, n=2), dict(w=(2 * at, 0))):
+                dict(parts=part() * 2, n=2), dict(w=(2 * at, 0)),
+                # the second part's weight in its output, the first being copied
+                dict(parts=part(turn=0) + part(inp=4 * at, out=5 * at), n=2, w=(5 * at, 0))):
         assert fwd(**bad) == 1, bad
     assert fwd(parts=part(D=514)) == 2 and fwd(B=1 << 20, S=1 << 12) == 2
 
