@@ -13,8 +13,9 @@ Layout BSHD, bf16: q/o/do [B,S,H,D], k/v [B,S,Hkv,D] with H % Hkv == 0 (GQA when
 Hkv < H); lse [B,H,S] fp32.
 
 The operators around it in a decoder block have modules of their own and the same manner:
-rotary positions (``rope``), the norms joined with the residual stream (``norms``) and
-differential attention, the difference of two softmax maps (``diff``).
+rotary positions, with norms of the heads before them (``rope``), the norms joined with the residual
+stream (``norms``), differential attention, the difference of two softmax maps (``diff``), and matrix
+products with their epilogue (``dense``).  ``grads`` clips a step's gradients by their norm.
 """
 from __future__ import annotations
 
