@@ -73,7 +73,7 @@ Product plan(int M, int N, int K, int parts, int outs, bool gated) {
     const long long tiles = p.tiles(), rounds = tiles / kPairs;
     if (tiles >= (1LL << 28)) continue;
     const int blocks = p.nk() * parts;
-    const double block = bn == 256 ? 1.0 : 0.7;
+    const double block = bn == 256 ? 1.0 : 0.62;
     // whole rounds stay whole, or (a few rounds) every tile is split
     for (int all = 0; all <= (rounds > 0 && rounds < 4); ++all) {
       p.whole = all ? 0 : (int)(rounds * kPairs);
@@ -191,11 +191,11 @@ unsigned long long wait_limit_ns() {
   return ns > 1000000ull ? ns : 1000000ull;
 }
 
-// Launches a product of rows a[0..1], b[0..1] (the second ones where `parts` or `outs` or a gate
+// Launches a product of rows a[0..1], b[0..1] (the second ones where `pairs`, a second output or a gate
 // ask for them, otherwise empty).
 dash_status_t launch(const Product &p, const Rows (&a)[2], const Rows (&b)[2], bool a_mn, bool b_mn,
-                     bool a_out, bool b_out, const DenseEpilogue &e, void *y1, long long y1s,
-                     float *part, void *workspace, bool clear, bool f16, int sms, cudaStream_t s) {
+                     bool a_out, bool b_out, bool pairs, int a_low, int b_low,
+                     const DenseEpilogue &e, void *y1, long long y1s, float *part, void *workspace, bool clear, bool f16, int sms, cudaStream_t s) {
   CUtensorMap ta[2], tb[2];
   for (int i = 0; i < 2; ++i)
     if (!make_rows_map(&ta[i], a[i].at ? a[i] : a[0], a_mn ? 64 : 128, f16) ||
@@ -216,6 +216,7 @@ dash_status_t launch(const Product &p, const Rows (&a)[2], const Rows (&b)[2], b
   d.nk = p.nk(), d.parts = p.parts, d.outs = p.outs;
   d.whole = p.whole, d.splits = p.splits, d.per = p.per;
   d.a_mn = a_mn, d.b_mn = b_mn, d.a_out = a_out, d.b_out = b_out;
+  d.pairs = pairs, d.a_low = a_low, d.b_low = b_low;
   d.withhold = g_dense_withhold.load();
   return launch_dense(f16, ta, tb, d, sms, s) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
 }
@@ -259,8 +260,13 @@ dash_status_t check_fwd(const dash_dense_fwd_t *a, Fwd &f) {
 }
 
 // ------------------------------------------------------------------ backward
+// dz is rounded for the tensor core, which is off by as much as the rounding of dx and dw: 1.4 times that
+// in all.  Of few elements it may come out well above that, and to multiply what the rounding lost as well
+// costs nothing there.
+constexpr long long kTwoTerms = 1 << 16;  // elements of dz
 struct Bwd {
   Product dx, dw;
+  int terms;
   Rows dy, x, w[2];
   Out out[3];          // dx, dw, dw_gate
   bool grads, pad_dy;  // dz (and dgate) are formed; dy is copied
@@ -294,16 +300,17 @@ dash_status_t check_bwd(const dash_dense_bwd_t *a, Bwd &b) {
   b.w[1] = Rows(a->dx && gated ? a->w_gate : nullptr, a->w_gate_stride, wr, wc);
   if (a->M > kMaxSize || a->K > kMaxSize || a->N > kMaxSize) return DASH_ERR_UNSUPPORTED;
   const int M = a->M ? a->M : 1;
-  b.dx = plan(M, a->K, a->N, gated ? 2 : 1, 1, false);
-  b.dw = kn ? plan(a->K, a->N, M, 1, gated ? 2 : 1, false)
-            : plan(a->N, a->K, M, 1, gated ? 2 : 1, false);
+  b.terms = b.grads && (long long)M * a->N <= kTwoTerms ? 2 : 1;
+  b.dx = plan(M, a->K, a->N, (gated ? 2 : 1) * b.terms, 1, false);
+  b.dw = kn ? plan(a->K, a->N, M, b.terms, gated ? 2 : 1, false)
+            : plan(a->N, a->K, M, b.terms, gated ? 2 : 1, false);
   if (!sizes_ok(b.dx) || !sizes_ok(b.dw)) return DASH_ERR_UNSUPPORTED;
   // rows of a chunk: four rounds of CTAs or so, 64 rows at least
   const int strips = ceil_div(a->N, 256);
   b.chunk = ceil_div(M, ceil_div(4 * 4 * 152, strips));
   b.chunk = (int)up(b.chunk < 64 ? 64 : b.chunk, 8);
   b.chunks = ceil_div(M, b.chunk);
-  b.dz_bytes = b.grads && (a->dx || a->dw) ? align256((size_t)M * up(a->N, 8) * 2) : 0;
+  b.dz_bytes = b.grads && (a->dx || a->dw) ? align256((size_t)b.terms * M * up(a->N, 8) * 2) : 0;
   b.sum_bytes = align256((size_t)b.chunks * a->N * 4);
   b.part_bytes = 0;
   if (a->dx) b.part_bytes = b.dx.part_bytes();
@@ -387,8 +394,8 @@ dash_status_t dash_dense_fwd(const dash_dense_fwd_t *a, void *workspace, size_t 
   e.y = f.y.at, e.residual = f.res.at;
   e.ys = f.y.stride, e.rs = f.res.stride;
   const Rows x[2] = {f.x, Rows()};
-  st = launch(f.p, x, f.w, false, kn, false, false, e, nullptr, 0, part, workspace, true, f16,
-              dev.sms, s);
+  st = launch(f.p, x, f.w, false, kn, false, false, false, 0, 0, e, nullptr, 0, part, workspace, true,
+              f16, dev.sms, s);
   if (st != DASH_OK) return st;
   return f.y.finish(s) ? DASH_OK : DASH_ERR_CUDA;
 }
@@ -444,6 +451,7 @@ dash_status_t dash_dense_bwd(const dash_dense_bwd_t *a, void *workspace, size_t 
       g.z = kept_at(const_cast<void *>(a->z), a->M, a->N),
       g.g = kept_at(const_cast<void *>(a->gate), a->M, a->N);
     g.dz = dz_at, g.dg = dg_at;
+    g.low = b.terms == 2;
     g.part = sum, g.part_gate = sum_gate;
     g.dys = b.dy.stride, g.ks = kept_stride(a->N), g.ds = up(a->N, 8);
     g.M = a->M, g.N = a->N, g.act = a->act, g.chunk = b.chunk;
@@ -453,8 +461,8 @@ dash_status_t dash_dense_bwd(const dash_dense_bwd_t *a, void *workspace, size_t 
                                                b.chunks, a->N, s) != cudaSuccess)
       return DASH_ERR_CUDA;
     if (b.grads) {
-      dz[0] = Rows(dz_at, g.ds, a->M, a->N);
-      dz[1] = Rows(dg_at, g.ds, a->M, a->N);
+      dz[0] = Rows(dz_at, g.ds, b.terms * a->M, a->N);
+      dz[1] = Rows(dg_at, g.ds, b.terms * a->M, a->N);
     }
   }
   if (!a->dx && !a->dw)  // no product clears the status block
@@ -463,21 +471,22 @@ dash_status_t dash_dense_bwd(const dash_dense_bwd_t *a, void *workspace, size_t 
       !place(b.w[1], arena, s))
     return DASH_ERR_CUDA;
   for (Out &o : b.out) o.place(arena);
+  const int low = b.terms == 2 ? a->M : 0;  // (rows of x behind the last are zeros there)
   if (a->dx) {
     DenseEpilogue e{};
     e.y = b.out[0].at, e.ys = b.out[0].stride;
-    st = launch(b.dx, dz, b.w, false, !kn, false, false, e, nullptr, 0, part, workspace, true, f16,
-                dev.sms, s);
+    st = launch(b.dx, dz, b.w, false, !kn, false, false, gated, low, 0, e, nullptr, 0, part,
+                workspace, true, f16, dev.sms, s);
     if (st != DASH_OK) return st;
   }
   if (a->dw) {
     DenseEpilogue e{};
     e.y = b.out[1].at, e.ys = b.out[1].stride;
     const Rows x[2] = {b.x, Rows()};
-    st = kn ? launch(b.dw, x, dz, true, true, false, gated, e, b.out[2].at, b.out[2].stride, part,
-                     workspace, !a->dx, f16, dev.sms, s)
-            : launch(b.dw, dz, x, true, true, gated, false, e, b.out[2].at, b.out[2].stride, part,
-                     workspace, !a->dx, f16, dev.sms, s);
+    st = kn ? launch(b.dw, x, dz, true, true, false, gated, false, 0, low, e, b.out[2].at,
+                     b.out[2].stride, part, workspace, !a->dx, f16, dev.sms, s)
+            : launch(b.dw, dz, x, true, true, gated, false, false, low, 0, e, b.out[2].at,
+                     b.out[2].stride, part, workspace, !a->dx, f16, dev.sms, s);
     if (st != DASH_OK) return st;
   }
   for (const Out &o : b.out)

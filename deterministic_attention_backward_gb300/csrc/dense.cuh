@@ -48,7 +48,9 @@ struct DenseParams {
   int M, N;
   int group;                 // rows of tiles that are worked through together
   int mt, nt, bn;            // tiles; bn columns of a tile's accumulator (gated: half z, half g)
-  int nk, parts, outs;       // blocks of kDenseK of a part
+  int nk, parts, outs;       // blocks of kDenseK of a part; parts, terms counted too
+  int pairs;                 // parts go by pairs of operands (a gated dx): the first pair, the second
+  int a_low, b_low;          // rows behind which an operand's second term begins (0: it has the same)
   int whole, splits, per;    // tiles that are whole; splits of each other tile, blocks of a split
   int a_mn, b_mn;            // the contiguous dimension is M (N), not the contraction
   int a_out, b_out;          // the second output takes the second A (B)
@@ -75,6 +77,7 @@ struct DenseGradParams {
   const void *dy;
   DenseKept z, g;            // no z: dz = dy (and is not written); no g: not gated
   void *dz, *dg;             // null where only the sums are wanted
+  int low;                   // what dz and dg lose by rounding follows them, M rows on
   float *part, *part_gate;   // [chunks][N]; null where the sums are not wanted
   long long dys, ks, ds;
   int M, N, act, chunk;      // rows of a chunk

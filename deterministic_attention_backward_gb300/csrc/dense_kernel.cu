@@ -259,7 +259,8 @@ __device__ __forceinline__ float activation(float z, float &slope) {
   }
   if constexpr (kAct == DASH_ACT_GELU_TANH) {
     const float s = tanh_sigmoid(z);
-    slope = fmaf(s * (1.f - s), 1.5957691216057308f * z * fmaf(0.134145f * z, z, 1.f), s);
+    const float t = s * (1.f - s);  // (0 at both ends, where what it multiplies may be infinite)
+    slope = t > 0.f ? fmaf(t, 1.5957691216057308f * z * fmaf(0.134145f * z, z, 1.f), s) : s;
     return z * s;
   }
   slope = 1.f;
@@ -577,16 +578,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
-        const bool part = k >= p.nk;
-        const int kk = (part ? k - p.nk : k) * kDenseK;
-        const CUtensorMap *map = part || second ? (isb ? &tb1 : &ta1) : (isb ? &tb0 : &ta0);
+        const int q = (k >= p.nk) + (k >= 2 * p.nk) + (k >= 3 * p.nk);
+        const int term = p.pairs ? q >> 1 : q, kk = (k - q * p.nk) * kDenseK;
+        const int low = term * (isb ? p.b_low : p.a_low);
+        const CUtensorMap *map = (p.pairs && (q & 1)) || second ? (isb ? &tb1 : &ta1) : (isb ? &tb0 : &ta0);
         const uint32_t bar = bar0 + 8 * s, dst = base + s * kStageBytes;
         expect_l(signals, own0 + 8 * s, bytes);
         if (mn) {
-          load_box(lead, dst, map, bar, at, kk);
-          if (boxes > 1) load_box(lead, dst + kMnBox, map, bar, at + 64, kk);
+          load_box(lead, dst, map, bar, at, kk + low);
+          if (boxes > 1) load_box(lead, dst + kMnBox, map, bar, at + 64, kk + low);
         } else {
-          load_box(lead, dst, map, bar, kk, at);
+          load_box(lead, dst, map, bar, kk, at + low);
         }
         if (++s == kStages) s = 0, ph ^= 1;
       }
@@ -948,8 +950,22 @@ __global__ void __launch_bounds__(256, kSums ? 3 : 4)
             g[e] = dy[e] * a;
           }
         }
-        if (p.dz) store_pack<T, V>(static_cast<T *>(p.dz) + r * p.ds + n, pack<T, V>(z));
-        if (p.g.hi && p.dg) store_pack<T, V>(static_cast<T *>(p.dg) + r * p.ds + n, pack<T, V>(g));
+        auto put = [&](void *base, const float(&f)[V]) {
+          T *to = static_cast<T *>(base) + r * p.ds + n;
+          const Pack<T, V> v = pack<T, V>(f);
+          store_pack<T, V>(to, v);
+          if (p.low) {
+            float l[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+              l[e] = f[e] - to_f32<T>(v.e[e]);
+              if (!isfinite(l[e])) l[e] = 0.f;
+            }
+            store_pack<T, V>(to + (long long)p.M * p.ds, pack<T, V>(l));
+          }
+        };
+        if (p.dz) put(p.dz, z);
+        if (p.g.hi && p.dg) put(p.dg, g);
       } else {
 #pragma unroll
         for (int e = 0; e < V; ++e) z[e] = dy[e];

@@ -548,8 +548,12 @@ cudaError_t launch_t(const HeadParams &p, bool wide, bool half, bool back, cudaS
   constexpr int V = 16 / sizeof(T);
   int units = 0;
   for (int i = 0; i < p.nparts; ++i) units = p.part[i].units > units ? p.part[i].units : units;
-  if (!wide) return units <= 32 ? launch_v<T, 1, 1>(p, half, back, s)
-                                : launch_v<T, 1, 8>(p, half, back, s);
+  // heads that 16-byte vectors do not fit, element by element: 2 x 8192 tokens of heads of 128 one element
+  // off that grid take 8 times as long as on it
+  if (!wide)
+    return units <= 32   ? launch_v<T, 1, 1>(p, half, back, s)
+           : units <= 64 ? launch_v<T, 1, 2>(p, half, back, s)
+                         : launch_v<T, 1, 8>(p, half, back, s);
   if constexpr (V == 4)
     if (units > 32) return launch_v<T, V, 2>(p, half, back, s);
   return launch_v<T, V, 1>(p, half, back, s);

@@ -96,13 +96,13 @@ def _fwd_args(x, w, bias, act, w_gate, bias_gate, residual, out, keep):
     return rows, K, N, order, shape, (xs, ws, gs, rs, ys or N)
 
 
-def dense_fwd_workspace_bytes(x, w, *, w_gate=None) -> int:
-    """Workspace bytes of ``dense_fwd`` for these operands (as they lie in memory)."""
-    rows, K, N, order, shape, strides = _fwd_args(x, w, None, "none", w_gate, None, None, None, False)
+def dense_fwd_workspace_bytes(x, w, *, w_gate=None, residual=None, out=None) -> int:
+    """Workspace bytes of ``dense_fwd`` for these tensors (as they lie in memory)."""
+    rows, K, N, order, shape, strides = _fwd_args(x, w, None, "none", w_gate, None, residual, out, False)
     if rows == 0:
         return 0
-    # the result's address does not matter to the size
-    a = _FWD.pack(x.data_ptr(), w.data_ptr(), _ptr(w_gate) or 0, 0, 0, 0, x.data_ptr(), 0, 0,
+    y = 1 << 20 if out is None else out.data_ptr()  # (a new one lies on 16 bytes)
+    a = _FWD.pack(x.data_ptr(), w.data_ptr(), _ptr(w_gate) or 0, 0, 0, _ptr(residual) or 0, y, 0, 0,
                   *strides, rows, K, N, order, 0, DTYPES[x.dtype])
     return int(lib().dash_dense_fwd_workspace_bytes(a))
 
@@ -180,14 +180,17 @@ def _bwd_pack(dy, x, w, kept, act, w_gate, dx, dw, dw_gate, db, dbg, rows, K, N,
 
 
 def dense_bwd_workspace_bytes(dy, x, w, kept=None, *, act: str = "none", w_gate=None, bias=None,
-                              bias_gate=None) -> int:
-    """Workspace bytes of ``dense_bwd`` for these operands (as they lie in memory)."""
-    args = _bwd_args(dy, x, w, kept, act, w_gate, bias, bias_gate, None, None, None)
+                              bias_gate=None, dx=None, dw=None, dw_gate=None) -> int:
+    """Workspace bytes of ``dense_bwd`` for these tensors (as they lie in memory), all gradients
+    asked for."""
+    args = _bwd_args(dy, x, w, kept, act, w_gate, bias, bias_gate, dx, dw, dw_gate)
     if args[0] == 0:
         return 256
-    at = 1 << 20  # the results' addresses do not matter to the size
-    a = _bwd_pack(dy, x, w, kept, act, w_gate, at, at, at if w_gate is not None else 0,
-                  0 if bias is None else at, 0 if bias_gate is None else at, *args)
+
+    def at(t, wanted=True):  # (a new one lies on 16 bytes)
+        return t.data_ptr() if t is not None else 1 << 20 if wanted else 0
+    a = _bwd_pack(dy, x, w, kept, act, w_gate, at(dx), at(dw), at(dw_gate, w_gate is not None),
+                  0 if bias is None else at(None), 0 if bias_gate is None else at(None), *args)
     return int(lib().dash_dense_bwd_workspace_bytes(a))
 
 

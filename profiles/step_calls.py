@@ -1,4 +1,4 @@
-"""The calls that step.md profiles: norms of heads with the turn, products with their epilogue,
+"""The calls whose kernels are profiled: norms of heads with the turn, products with their epilogue,
 clipping."""
 import os
 import sys

@@ -176,6 +176,7 @@ def test_special_values(L):
     assert g.isnan().all() and h.isnan().all()
     z = torch.zeros(10, device="cuda")
     assert float(dash.grad_clip([z, torch.empty(0, device="cuda")], 1.0)) == 0 and (z == 0).all()
+    assert float(dash.grad_clip([z], 0.0, eps=0.0)) == 0 and (z == 0).all()
     e = torch.empty(0, device="cuda")
     assert float(dash.grad_norm([e])) == 0 and float(dash.grad_clip([e], 1.0)) == 0
 
