@@ -59,11 +59,13 @@ struct Product {
   }
 };
 
-// The choice follows from the sizes alone, as the order of the sums does (the pairs of SMs are those
-// of a GB300, not of the GPU that runs).  Tiles that fill whole rounds of the pairs stay whole; the
-// rest, which would leave pairs idle, are split along the contraction where that is shorter.  Time is
-// counted in blocks of 64 of a 256-column tile (0.27 us): a block of 128 columns costs 0.7, an item 3
-// beside its blocks, the kernel that adds the splits 10 and the partial sums their way to memory.
+// The choice follows from the sizes alone, as the order of the sums does (the pairs of SMs are those of
+// a GB300, not of the GPU that runs).  Tiles that fill whole rounds of the pairs stay whole; the rest,
+// which would leave pairs idle, are split along the contraction where that is shorter, or, of a few
+// rounds, all of them.  Time is counted in blocks of 64 of a 256-column tile (0.27 us): a block of 128
+// columns costs 0.62 (19456 x 4096 x 4096 402 us against 325; 1237 x 4096 x 4096, where it fills the
+// pairs better, 39 against 40), an item 3 beside its blocks, the kernel that adds the splits 10 and the
+// partial sums their way to memory.
 constexpr int kPairs = 76, kMaxSplits = 64;
 Product plan(int M, int N, int K, int parts, int outs, bool gated) {
   Product best;
@@ -101,7 +103,8 @@ Product plan(int M, int N, int K, int parts, int outs, bool gated) {
 // busiest SM has at the pace of one SM, 1.4 times its share of the memory's (112 SMs reach 6.2 TB/s);
 // 3 for a round of CTAs, 1 for each that an SM holds at once, 2 for sums through a cluster.  Measured, one
 // row x 4096 x 14336 gated: 112 CTAs alone 38 us, 224 in pairs 39, 448 in fours 42 to 55, in eights 71;
-// 17 x 14336 x 4096: 32 CTAs 58, 64 in pairs 32, 128 in fours 23, 256 in eights 22.
+// 17 x 14336 x 4096: 32 CTAs 58, 64 in pairs 32, 128 in fours 23, 256 in eights 22.  At 64 rows x 4096 x
+// 14336 27 us, with the other kernel 65 rows take 27.5.
 constexpr int kMaxCluster = 8;
 // CTAs that a GB300 holds at once, 1 to 4 on an SM, in clusters of 1, 2, 4 and 8
 // (cudaOccupancyMaxActiveClusters): clusters do not fill every group of SMs.
@@ -195,7 +198,8 @@ unsigned long long wait_limit_ns() {
 // ask for them, otherwise empty).
 dash_status_t launch(const Product &p, const Rows (&a)[2], const Rows (&b)[2], bool a_mn, bool b_mn,
                      bool a_out, bool b_out, bool pairs, int a_low, int b_low,
-                     const DenseEpilogue &e, void *y1, long long y1s, float *part, void *workspace, bool clear, bool f16, int sms, cudaStream_t s) {
+                     const DenseEpilogue &e, void *y1, long long y1s, float *part, void *workspace,
+                     bool clear, bool f16, int sms, cudaStream_t s) {
   CUtensorMap ta[2], tb[2];
   for (int i = 0; i < 2; ++i)
     if (!make_rows_map(&ta[i], a[i].at ? a[i] : a[0], a_mn ? 64 : 128, f16) ||
@@ -244,17 +248,20 @@ dash_status_t check_fwd(const dash_dense_fwd_t *a, Fwd &f) {
   const bool kn = a->order == DASH_DENSE_KN;
   if (a->M > kMaxSize || a->K > kMaxSize || a->N > kMaxSize) return DASH_ERR_UNSUPPORTED;
   const bool gated = a->w_gate != nullptr;
-  f.p = plan(a->M, a->N, a->K, 1, 1, gated);
-  if (!sizes_ok(f.p)) return DASH_ERR_UNSUPPORTED;
+  f.p = Product{a->M, a->N, a->K, 1, 1, gated};
+  if (a->M <= kFewRows) {
+    f.few = plan_few(a->M, a->N, a->K, gated);
+  } else {
+    f.p = plan(a->M, a->N, a->K, 1, 1, gated);
+    if (!sizes_ok(f.p)) return DASH_ERR_UNSUPPORTED;
+  }
   f.x = Rows(a->x, a->x_stride, a->M, a->K);
   f.w[0] = Rows(a->w, a->w_stride, kn ? a->K : a->N, kn ? a->N : a->K);
   f.w[1] = Rows(a->w_gate, a->w_gate_stride, f.w[0].rows, f.w[0].cols);
   f.res = Rows(a->residual, a->residual_stride, a->M, a->N);
   f.y = Out(a->y, a->y_stride, a->M, a->N);
   f.need = kStatusBytes + f.x.bytes() + f.w[0].bytes() + f.w[1].bytes();
-  if (a->M <= kFewRows)  // (which needs no more room)
-    f.few = plan_few(a->M, a->N, a->K, gated);
-  else
+  if (!f.few.split)  // (few rows need no more room)
     f.need += f.p.part_bytes() + f.res.bytes() + f.y.bytes();
   return DASH_OK;
 }
@@ -319,7 +326,8 @@ dash_status_t check_bwd(const dash_dense_bwd_t *a, Bwd &b) {
   b.out[0] = Out(a->dx, a->dx_stride, a->M, a->K);
   b.out[1] = Out(a->dw, a->dw_stride, wr, wc);
   b.out[2] = Out(a->dw_gate, a->dw_gate_stride, wr, wc);
-  b.need = kStatusBytes + b.out[0].bytes() + b.out[1].bytes() + b.out[2].bytes() + (gated ? 2 : 1) * b.dz_bytes + (a->dbias ? b.sum_bytes : 0) +
+  b.need = kStatusBytes + b.out[0].bytes() + b.out[1].bytes() + b.out[2].bytes() +
+           (gated ? 2 : 1) * b.dz_bytes + (a->dbias ? b.sum_bytes : 0) +
            (a->dbias_gate ? b.sum_bytes : 0) + b.part_bytes + (b.pad_dy ? b.dy.bytes() : 0) +
            b.x.bytes() + b.w[0].bytes() + b.w[1].bytes();
   return DASH_OK;

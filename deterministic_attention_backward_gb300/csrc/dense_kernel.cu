@@ -344,7 +344,7 @@ __device__ __forceinline__ void add_bias(const void *base, int n, float (&v)[32]
 __device__ __forceinline__ uint8_t *turn_at(uint8_t *buf, int row, int piece) {
   return buf + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
 }
-// (out of) this thread's row
+// This thread's row into the buffer, and what the buffer has of it added.
 template <typename T>
 __device__ __forceinline__ void turn_put(uint8_t *buf, int lane, const float (&v)[32]) {
 #pragma unroll
@@ -581,7 +581,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int q = (k >= p.nk) + (k >= 2 * p.nk) + (k >= 3 * p.nk);
         const int term = p.pairs ? q >> 1 : q, kk = (k - q * p.nk) * kDenseK;
         const int low = term * (isb ? p.b_low : p.a_low);
-        const CUtensorMap *map = (p.pairs && (q & 1)) || second ? (isb ? &tb1 : &ta1) : (isb ? &tb0 : &ta0);
+        const CUtensorMap *map =
+            (p.pairs && (q & 1)) || second ? (isb ? &tb1 : &ta1) : (isb ? &tb0 : &ta0);
         const uint32_t bar = bar0 + 8 * s, dst = base + s * kStageBytes;
         expect_l(signals, own0 + 8 * s, bytes);
         if (mn) {
@@ -899,8 +900,8 @@ __global__ void __launch_bounds__(kFewThreads)
 
 // ------------------------------------------------------------------ dz, dgate and their sums
 // 32 threads a strip of 256 columns, 8 rows at a time over a chunk of rows; the eight rows' sums are
-// added in order through shared memory.  Bound by memory: 8192 x 14336 gated, 14 bytes an element, in
-// about 200 us.  Registers decide how much is on its way: without the sums 4 CTAs are on an SM (two rows
+// added in order through shared memory.  Bound by memory: 8192 x 14336 gated, 12 bytes an element, in
+// 226 us, 6.2 TB/s.  Registers decide how much is on its way: without the sums 4 CTAs are on an SM (two rows
 // at once, 153 registers: twice the time).
 template <typename T, int kAct, bool kSums>
 __global__ void __launch_bounds__(256, kSums ? 3 : 4)

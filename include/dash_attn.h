@@ -491,7 +491,8 @@ dash_status_t dash_dense_fwd(const dash_dense_fwd_t *args, void *workspace, size
  *   dx = dz w^T + dgate w_gate^T   dw = x^T dz   dw_gate = x^T dgate   dbias, dbias_gate = sums
  * each where its pointer is not NULL (dw and dw_gate in the weights' order).  dz and dgate are
  * rounded to the rows' type for the tensor core (where they are few, what that loses is multiplied too),
- * the biases' gradients are sums of the unrounded ones.  The residual's gradient is dy.  Deterministic; M = 0 clears the weights' gradients. */
+ * the biases' gradients are sums of the unrounded ones.  The residual's gradient is dy.  Deterministic;
+ * M = 0 clears the weights' gradients. */
 typedef struct {
   const void *dy, *x, *w, *w_gate, *z, *gate;
   void *dx, *dw, *dw_gate, *dbias, *dbias_gate;
