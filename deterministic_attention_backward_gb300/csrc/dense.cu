@@ -155,14 +155,26 @@ struct Arena {
   }
 };
 
-// Copies an operand that the copy engine cannot read where it lies.
-bool place(Rows &r, Arena &arena, cudaStream_t s) {
-  if (!r.pad) return true;
+// Copies that wait for their launch.
+struct Copies {
+  DenseCopies list{};
+  bool out;
+  explicit Copies(bool out) : out(out) {}
+  void add(const void *in, long long is, void *to, long long os, int rows, int cols) {
+    list.c[list.count++] = {in, to, is, os, rows, cols};
+  }
+  bool run(cudaStream_t s) const {
+    return list.count == 0 || launch_dense_copies(list, out, s) == cudaSuccess;
+  }
+};
+
+// Gives an operand that TMA cannot read where it lies a place in the workspace.
+void place(Rows &r, Arena &arena, Copies &copies) {
+  if (!r.pad) return;
   const long long stride = up(r.cols, 8);
   void *to = arena.take(r.bytes());
-  if (launch_dense_copy(r.at, r.stride, to, stride, r.rows, r.cols, s) != cudaSuccess) return false;
+  copies.add(r.at, r.stride, to, stride, r.rows, r.cols);
   r = Rows(to, stride, r.rows, r.cols);
-  return true;
 }
 
 // An output that does not lie on 16 bytes is formed in the workspace and copied to its place.
@@ -181,9 +193,8 @@ struct Out {
     stride = up(cols, 8);
     at = arena.take(n);
   }
-  bool finish(cudaStream_t s) const {
-    return at == to ||
-           launch_dense_copy_out(at, stride, to, to_stride, rows, cols, s) == cudaSuccess;
+  void finish(Copies &copies) const {
+    if (at != to) copies.add(at, stride, to, to_stride, rows, cols);
   }
 };
 
@@ -312,10 +323,10 @@ dash_status_t check_bwd(const dash_dense_bwd_t *a, Bwd &b) {
   b.dw = kn ? plan(a->K, a->N, M, b.terms, gated ? 2 : 1, false)
             : plan(a->N, a->K, M, b.terms, gated ? 2 : 1, false);
   if (!sizes_ok(b.dx) || !sizes_ok(b.dw)) return DASH_ERR_UNSUPPORTED;
-  // rows of a chunk: four rounds of CTAs or so, 64 rows at least
+  // rows of a chunk: four rounds of CTAs or so, 32 rows at least
   const int strips = ceil_div(a->N, 256);
   b.chunk = ceil_div(M, ceil_div(4 * 4 * 152, strips));
-  b.chunk = (int)up(b.chunk < 64 ? 64 : b.chunk, 8);
+  b.chunk = (int)up(b.chunk < 32 ? 32 : b.chunk, 8);
   b.chunks = ceil_div(M, b.chunk);
   b.dz_bytes = b.grads && (a->dx || a->dw) ? align256((size_t)b.terms * M * up(a->N, 8) * 2) : 0;
   b.sum_bytes = align256((size_t)b.chunks * a->N * 4);
@@ -370,14 +381,15 @@ dash_status_t dash_dense_fwd(const dash_dense_fwd_t *a, void *workspace, size_t 
   const bool f16 = a->dtype == DASH_FP16, kn = a->order == DASH_DENSE_KN;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   Arena arena(workspace);
-  if (!place(f.x, arena, s) || !place(f.w[0], arena, s) || !place(f.w[1], arena, s))
-    return DASH_ERR_CUDA;
+  Copies in(false), out(true);
+  for (Rows *r : {&f.x, &f.w[0], &f.w[1]}) place(*r, arena, in);
   DenseEpilogue e{};
   e.bias = a->bias, e.bias_gate = a->bias_gate;
   e.act = a->act, e.gated = f.p.gated;
   e.z = kept_at(a->z, a->M, a->N), e.g = kept_at(a->gate, a->M, a->N);
   e.ks = kept_stride(a->N);
   if (f.few.split) {
+    if (!in.run(s)) return DASH_ERR_CUDA;
     e.y = a->y, e.residual = a->residual;
     e.ys = a->y_stride, e.rs = a->residual_stride;
     CUtensorMap tw[2], tx;
@@ -397,15 +409,17 @@ dash_status_t dash_dense_fwd(const dash_dense_fwd_t *a, void *workspace, size_t 
     return launch_dense_few(f16, tw[0], tw[1], tx, d, s) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
   }
   float *part = static_cast<float *>(arena.take(f.p.part_bytes()));
-  if (!place(f.res, arena, s)) return DASH_ERR_CUDA;
+  place(f.res, arena, in);
   f.y.place(arena);
+  if (!in.run(s)) return DASH_ERR_CUDA;
   e.y = f.y.at, e.residual = f.res.at;
   e.ys = f.y.stride, e.rs = f.res.stride;
   const Rows x[2] = {f.x, Rows()};
   st = launch(f.p, x, f.w, false, kn, false, false, false, 0, 0, e, nullptr, 0, part, workspace, true,
               f16, dev.sms, s);
   if (st != DASH_OK) return st;
-  return f.y.finish(s) ? DASH_OK : DASH_ERR_CUDA;
+  f.y.finish(out);
+  return out.run(s) ? DASH_OK : DASH_ERR_CUDA;
 }
 
 size_t dash_dense_bwd_workspace_bytes(const dash_dense_bwd_t *args) {
@@ -475,9 +489,9 @@ dash_status_t dash_dense_bwd(const dash_dense_bwd_t *a, void *workspace, size_t 
   }
   if (!a->dx && !a->dw)  // no product clears the status block
     return cudaMemsetAsync(workspace, 0, kStatusBytes, s) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
-  if (!place(dz[0], arena, s) || !place(b.x, arena, s) || !place(b.w[0], arena, s) ||
-      !place(b.w[1], arena, s))
-    return DASH_ERR_CUDA;
+  Copies in(false), out(true);
+  for (Rows *r : {&dz[0], &b.x, &b.w[0], &b.w[1]}) place(*r, arena, in);
+  if (!in.run(s)) return DASH_ERR_CUDA;
   for (Out &o : b.out) o.place(arena);
   const int low = b.terms == 2 ? a->M : 0;  // (rows of x behind the last are zeros there)
   if (a->dx) {
@@ -497,9 +511,8 @@ dash_status_t dash_dense_bwd(const dash_dense_bwd_t *a, void *workspace, size_t 
                      b.out[2].stride, part, workspace, !a->dx, f16, dev.sms, s);
     if (st != DASH_OK) return st;
   }
-  for (const Out &o : b.out)
-    if (!o.finish(s)) return DASH_ERR_CUDA;
-  return DASH_OK;
+  for (const Out &o : b.out) o.finish(out);
+  return out.run(s) ? DASH_OK : DASH_ERR_CUDA;
 }
 
 }  // extern "C"

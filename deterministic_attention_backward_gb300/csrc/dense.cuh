@@ -92,10 +92,18 @@ cudaError_t launch_dense_grad(bool f16, const DenseGradParams &p, int chunks, cu
 // out[n] = sum over chunks, in order (gate: a second row of sums and its output)
 cudaError_t launch_dense_sums(bool f16, const float *part, const float *part_gate, void *out,
                               void *out_gate, int chunks, int N, cudaStream_t s);
-// rows of cols elements of two bytes to rows on 16 bytes, the last vector filled up with zeros; and back
-cudaError_t launch_dense_copy(const void *in, long long is, void *out, long long os, int rows,
-                              int cols, cudaStream_t s);
-cudaError_t launch_dense_copy_out(const void *in, long long is, void *out, long long os, int rows,
-                                  int cols, cudaStream_t s);
+// Up to four copies of rows of cols elements of two bytes in one launch: to rows on 16 bytes, the last
+// vector filled up with zeros, or (out) from there to rows anywhere.
+struct DenseCopy {
+  const void *in;
+  void *out;
+  long long is, os;
+  int rows, cols;
+};
+struct DenseCopies {
+  DenseCopy c[4];
+  int count;
+};
+cudaError_t launch_dense_copies(const DenseCopies &c, bool out, cudaStream_t s);
 
 }  // namespace dash

@@ -1000,44 +1000,52 @@ __global__ void __launch_bounds__(256, kSums ? 3 : 4)
   }
 }
 
+// 8 runs of chunks for each of 32 columns, then the runs, in order.
 template <typename T>
-__global__ void __launch_bounds__(128) dense_sums_kernel(const float *part, const float *part_gate,
+__global__ void __launch_bounds__(256) dense_sums_kernel(const float *part, const float *part_gate,
                                                          void *out, void *out_gate, int chunks,
                                                          int N) {
-  const int n = blockIdx.x * 128 + threadIdx.x;
+  __shared__ float sums[8][32];
+  const int lane = threadIdx.x & 31, run = threadIdx.x >> 5, n = blockIdx.x * 32 + lane;
   const float *src = blockIdx.y ? part_gate : part;
   T *dst = static_cast<T *>(blockIdx.y ? out_gate : out);
-  if (n >= N || !src || !dst) return;
+  if (!src || !dst) return;
+  const int per = (chunks + 7) / 8, end = min(chunks, (run + 1) * per);
   float s = 0.f;
+  if (n < N)
 #pragma unroll 8
-  for (int c = 0; c < chunks; ++c) s += src[(long long)c * N + n];
+    for (int c = run * per; c < end; ++c) s += src[(long long)c * N + n];
+  sums[run][lane] = s;
+  __syncthreads();
+  if (run > 0 || n >= N) return;
+#pragma unroll
+  for (int r = 1; r < 8; ++r) s += sums[r][lane];
   dst[n] = from_f32<T>(s);
 }
 
 // A thread writes 16 bytes; a row's reads, which lie on no boundary, meet in L1.
-__global__ void __launch_bounds__(256) dense_copy_kernel(const uint16_t *in, long long is,
-                                                         uint16_t *out, long long os, int rows,
-                                                         int cols) {
+__global__ void __launch_bounds__(256) dense_copy_kernel(const __grid_constant__ DenseCopies p) {
+  const DenseCopy &q = p.c[blockIdx.z];
   const int c = (blockIdx.x * 32 + (threadIdx.x & 31)) * 8;
-  if (c >= cols) return;
-  for (long long r = blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.y * 8) {
-    const uint16_t *src = in + r * is + c;
+  if (c >= q.cols) return;
+  for (long long r = blockIdx.y * 8 + (threadIdx.x >> 5); r < q.rows; r += gridDim.y * 8) {
+    const uint16_t *src = static_cast<const uint16_t *>(q.in) + r * q.is + c;
     Pack<uint16_t, 8> v;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v.e[e] = c + e < cols ? src[e] : (uint16_t)0;
-    store_pack<uint16_t, 8>(out + r * os + c, v);
+    for (int e = 0; e < 8; ++e) v.e[e] = c + e < q.cols ? src[e] : (uint16_t)0;
+    store_pack<uint16_t, 8>(static_cast<uint16_t *>(q.out) + r * q.os + c, v);
   }
 }
-
-// The other way: rows that lie on 16 bytes to where a caller's lie.
-__global__ void __launch_bounds__(256) dense_copy_out_kernel(const uint16_t *in, long long is,
-                                                             uint16_t *out, long long os, int rows,
-                                                             int cols) {
+__global__ void __launch_bounds__(256) dense_copy_out_kernel(const __grid_constant__ DenseCopies p) {
+  const DenseCopy &q = p.c[blockIdx.z];
   const int c = blockIdx.x * 128 + (threadIdx.x & 31);
-  for (long long r = blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.y * 8)
+  for (long long r = blockIdx.y * 8 + (threadIdx.x >> 5); r < q.rows; r += gridDim.y * 8) {
+    const uint16_t *src = static_cast<const uint16_t *>(q.in) + r * q.is + c;
+    uint16_t *dst = static_cast<uint16_t *>(q.out) + r * q.os + c;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (c + 32 * i < cols) out[r * os + c + 32 * i] = in[r * is + c + 32 * i];
+      if (c + 32 * i < q.cols) dst[32 * i] = src[32 * i];
+  }
 }
 
 template <typename T>
@@ -1112,28 +1120,26 @@ cudaError_t launch_dense_grad(bool f16, const DenseGradParams &p, int chunks, cu
 
 cudaError_t launch_dense_sums(bool f16, const float *part, const float *part_gate, void *out,
                               void *out_gate, int chunks, int N, cudaStream_t s) {
-  const dim3 grid((N + 127) / 128, out_gate ? 2 : 1);
+  const dim3 grid((N + 31) / 32, out_gate ? 2 : 1);
   if (f16)
-    dense_sums_kernel<__half><<<grid, 128, 0, s>>>(part, part_gate, out, out_gate, chunks, N);
+    dense_sums_kernel<__half><<<grid, 256, 0, s>>>(part, part_gate, out, out_gate, chunks, N);
   else
     dense_sums_kernel<__nv_bfloat16>
-        <<<grid, 128, 0, s>>>(part, part_gate, out, out_gate, chunks, N);
+        <<<grid, 256, 0, s>>>(part, part_gate, out, out_gate, chunks, N);
   return cudaGetLastError();
 }
 
-cudaError_t launch_dense_copy_out(const void *in, long long is, void *out, long long os, int rows,
-                                  int cols, cudaStream_t s) {
-  const int down = (rows + 7) / 8;
-  dense_copy_out_kernel<<<dim3((cols + 127) / 128, down < 16384 ? down : 16384), 256, 0, s>>>(
-      static_cast<const uint16_t *>(in), is, static_cast<uint16_t *>(out), os, rows, cols);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_dense_copy(const void *in, long long is, void *out, long long os, int rows,
-                              int cols, cudaStream_t s) {
-  const int down = (rows + 7) / 8;
-  dense_copy_kernel<<<dim3((cols + 255) / 256, down < 16384 ? down : 16384), 256, 0, s>>>(
-      static_cast<const uint16_t *>(in), is, static_cast<uint16_t *>(out), os, rows, cols);
+cudaError_t launch_dense_copies(const DenseCopies &c, bool out, cudaStream_t s) {
+  int rows = 0, cols = 0;
+  for (int i = 0; i < c.count; ++i) {
+    rows = c.c[i].rows > rows ? c.c[i].rows : rows;
+    cols = c.c[i].cols > cols ? c.c[i].cols : cols;
+  }
+  const int down = (rows + 7) / 8 < 16384 ? (rows + 7) / 8 : 16384;
+  if (out)
+    dense_copy_out_kernel<<<dim3((cols + 127) / 128, down, c.count), 256, 0, s>>>(c);
+  else
+    dense_copy_kernel<<<dim3((cols + 255) / 256, down, c.count), 256, 0, s>>>(c);
   return cudaGetLastError();
 }
 

@@ -9,8 +9,8 @@
 // every CTA of the scaling for itself.  Which CTA takes a chunk follows from the sizes: the same bits
 // on every run.
 //
-// Measured (taken in the same order by both, 2 us more): 436 MB in bf16 clipped to other buffers 66 + 134 us, 6.6 TB/s, a copy's rate in both kernels;
-// 3.5 GB in fp32 within the limit 490 us, 7.1 TB/s.
+// Measured: 436 MB in bf16 clipped to other buffers 66 + 134 us, 6.6 TB/s, a copy's rate in both kernels
+// (chunks taken in the same order by both: 2 us more); 3.5 GB in fp32 within the limit 490 us, 7.1 TB/s.
 #include <algorithm>
 #include <cmath>
 #include <vector>
