@@ -781,19 +781,44 @@ __global__ void __launch_bounds__(kFewThreads)
   const int tile = blockIdx.x / p.split;
   if (blockIdx.x == 0 && threadIdx.x < kStatusBytes / 4) p.status[threadIdx.x] = 0;
   const Abort ab{&s_abort, p.status, p.wait_ns};
+  const bool gated = p.e.gated;
+  const int k0 = (int)rank * p.per, k1 = min(k0 + p.per, p.nk);
+  const int n0 = tile * 128;
+  const uint32_t base = smem_u32(smem), xoff = gated ? 2 * kABytes : kABytes;
+  const bool aligned = (base & 1023u) == 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
     mbar_init(&done, 1);
-    s_abort = smem_u32(smem) & 1023u ? 1 : 0;
-    if (s_abort) atomicOr(p.status, kErrSmemAlign);
+    s_abort = aligned ? 0 : 1;
+    if (!aligned) atomicOr(p.status, kErrSmemAlign);
     fence_mbar_init();
   }
-  if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tw0);
-    tma_prefetch_desc(&tx);
+  // the blocks of one filling of the ring are on their way before the others are ready to take them
+  uint32_t lead = 0;
+  auto bring = [&](int k, int s) {
+    const uint32_t at = base + s * p.stage, bar = smem_u32(&full[s]);
+    expect_l(lead, bar, xoff + p.cols * 128);
+    for (int g = 0; g <= (int)gated; ++g) {
+      const CUtensorMap *map = g ? &tw1 : &tw0;
+      const uint32_t to = at + g * kABytes;
+      if (p.w_mn) {
+        load_box_alone(lead, to, map, bar, n0, k * kDenseK);
+        load_box_alone(lead, to + kMnBox, map, bar, n0 + 64, k * kDenseK);
+      } else {
+        load_box_alone(lead, to, map, bar, k * kDenseK, n0);
+      }
+    }
+    load_box_alone(lead, at + xoff, &tx, bar, k * kDenseK, 0);
+  };
+  int it = 0;
+  const int wanted = p.withhold >= 0 && p.withhold < k1 - k0 ? p.withhold : k1 - k0;
+  if (warp == 0 && aligned) {
+    __syncwarp();
+    lead = elect_one();
+    for (; it < wanted && it < p.stages; ++it) bring(k0 + it, it);
   }
   if (warp == 2) {
     tmem_alloc(&s_tmem, p.tmem);
@@ -803,44 +828,28 @@ __global__ void __launch_bounds__(kFewThreads)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  const bool gated = p.e.gated;
-  const int k0 = (int)rank * p.per, k1 = min(k0 + p.per, p.nk);
-  const int n0 = tile * 128;
-  const uint32_t base = smem_u32(smem), xoff = gated ? 2 * kABytes : kABytes;
 
-  bool ok = !s_abort;
+  bool ok = aligned;
   if (ok && warp == 0) {
-    const uint32_t lead = elect_one(), bytes = xoff + p.cols * 128;
-    int s = 0, it = 0;
-    uint32_t ph = 1;
-    for (int k = k0; k < k1; ++k, ++it) {
-      if (it == p.withhold || !wait_local(&empty[s], ph, ab)) {
+    int s = it == p.stages ? 0 : it;
+    uint32_t ph = 0;
+    for (; it < wanted; ++it) {
+      if (!wait_local(&empty[s], ph, ab)) {
         ok = false;
         break;
       }
-      const uint32_t at = base + s * p.stage, bar = smem_u32(&full[s]);
-      expect_l(lead, bar, bytes);
-      for (int g = 0; g <= (int)gated; ++g) {
-        const CUtensorMap *map = g ? &tw1 : &tw0;
-        const uint32_t to = at + g * kABytes;
-        if (p.w_mn) {
-          load_box_alone(lead, to, map, bar, n0, k * kDenseK);
-          load_box_alone(lead, to + kMnBox, map, bar, n0 + 64, k * kDenseK);
-        } else {
-          load_box_alone(lead, to, map, bar, k * kDenseK, n0);
-        }
-      }
-      load_box_alone(lead, at + xoff, &tx, bar, k * kDenseK, 0);
+      bring(k0 + it, s);
       if (++s == p.stages) s = 0, ph ^= 1;
     }
-    if (!ok)  // leave no copy in flight into shared memory
+    if (!ok || wanted < k1 - k0)  // leave no copy in flight into shared memory
       for (int j = max(0, it - p.stages); j < it; ++j)
         mbar_wait_drain(&full[j % p.stages], (j / p.stages) & 1, 100000000ull);
   } else if (ok && warp == 1) {
     const uint32_t kind = std::is_same<T, __half>::value ? 0u : (1u << 7) | (1u << 10);
     const uint32_t idesc = (1u << 4) | kind | ((uint32_t)p.w_mn << 15) |
                            ((uint32_t)(p.cols >> 3) << 17) | ((128u >> 4) << 24);
-    const uint32_t wstep = (p.w_mn ? 2048 : 32) >> 4, lead = elect_one();
+    const uint32_t wstep = (p.w_mn ? 2048 : 32) >> 4;
+    lead = elect_one();
     int s = 0;
     uint32_t ph = 0;
     for (int k = k0; ok && k < k1; ++k) {
