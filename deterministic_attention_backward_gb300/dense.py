@@ -61,8 +61,8 @@ def _weights(x, w, w_gate, act):
         alike(w_gate, "w_gate", x, w.shape)
         _, gs = _order(w_gate, "w_gate", order)
     rows = x.numel() // K
-    if rows >= 1 << 30:
-        raise ValueError(f"x has {rows} rows, 2^30 at most")
+    if max(rows, K, N) > 1 << 30:
+        raise ValueError(f"products of {rows} x {K} x {N} are not taken, 2^30 at most")
     return rows, K, N, order, ws, gs
 
 

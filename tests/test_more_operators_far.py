@@ -80,3 +80,19 @@ def test_grads():
     dash.grad_clip([g], 0.5 * ref)
     assert ((g[-5000:].double() - 0.5 * tail.double()).abs() <=
             (2.0 ** -9 + 2.0 ** -16) * 0.5 * tail.double().abs()).all()
+
+
+def test_sizes_that_do_not_fit():
+    """Sizes behind 2^31 come from views of one element; what would wrap is refused, nothing is formed."""
+    one = torch.ones(1, 1, dtype=BF, device="cuda")
+    with pytest.raises(ValueError, match="2\\^30"):
+        dash.dense_fwd(one.expand(4, 1), one.expand(1, 2 ** 32 + 5))
+    with pytest.raises(ValueError, match="2\\^30"):
+        dash.dense_fwd(one.expand(2 ** 32 + 5, 1), one)
+    f, _ = dash.rope_freqs(2)
+    far = torch.ones(1, 1, 2, dtype=BF, device="cuda").expand(2 ** 32 + 5, 1, 2)
+    for call in (dash.rope_norm_fwd, dash.rope_fwd):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call(far, inv_freq=f)
+        with pytest.raises(ValueError, match="2\\^31"):
+            call(far[:1], None, far[:1, :, :1].expand(1, 2 ** 32 + 5, 1), inv_freq=f)
