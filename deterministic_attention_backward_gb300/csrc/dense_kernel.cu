@@ -9,7 +9,7 @@
 // cuBLAS takes 480 us, 535 to 550 under the power limit.  With gelu 570, gated forward 1160 (2 products),
 // its backward 2500 (4 products, dz).  The epilogue runs beside the next tile's products; by rows through
 // shared memory, so that a warp writes 64 bytes a row (a thread a row: 161 us at K = 512, now 110).
-// Few rows: bound by the weights' bytes, see dense_few_kernel: 1 x 4096 x 14336 gated 38 us, 6.2 TB/s.
+// Few rows: bound by the weights' bytes, see dense_few_kernel: 1 x 4096 x 14336 gated 37.3 us, 6.3 TB/s.
 #include "dense.cuh"
 
 #include "dash_attn.h"
@@ -762,7 +762,7 @@ __global__ void __launch_bounds__(256) dense_finish_kernel(const __grid_constant
 
 // ------------------------------------------------------------------ few rows
 // Up to 64 rows of x: bound by the weights' way through the SMs (with the kernel above one row x 4096 x
-// 14336 gated took 61 us, 17 x 14336 x 4096 31, now 38 and 23).  The weights are the rows of the tensor
+// 14336 gated took 61 us, 17 x 14336 x 4096 31, now 37.3 and 22.4).  The weights are the rows of the tensor
 // core's tile here (128 outputs), x its columns, so that nothing but x is read that is not needed.  A
 // cluster shares a tile: every CTA forms the sums over its part of the contraction, leaves them in its
 // shared memory, and finishes its share of the outputs from all CTAs' sums, added in order.
