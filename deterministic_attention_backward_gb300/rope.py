@@ -86,8 +86,8 @@ def _frequencies(q, inv_freq, layout):
         raise ValueError("inv_freq must be contiguous float64 [rot/2], rot <= 1024")
     tokens = q.shape[:-2]
     B, S = tokens if dims == 4 else (1, tokens[0])
-    if B * S >= 1 << 31 or max(q.shape[-2:]) >= 1 << 31:  # (C integers wrap)
-        raise ValueError(f"q {tuple(q.shape)} has a size of 2^31 or more")
+    if B * S >= 1 << 31:  # (C integers wrap)
+        raise ValueError(f"q {tuple(q.shape)} has 2^31 tokens or more")
     return tokens, B, S, rot
 
 
@@ -98,11 +98,12 @@ def _heads(t, name, q, i, tokens, rot):
         alike(t, name, q)
         if shape[:-2] != tokens or t.dim() != q.dim():
             raise ValueError(f"{name} {tuple(shape)} does not go with q {tuple(q.shape)}")
-        if max(shape[-2:]) >= 1 << 31:
-            raise ValueError(f"{name} {tuple(shape)} has a size of 2^31 or more")
-    if i < 2 and shape[-1] < rot:
-        raise ValueError(f"{name} has heads of {shape[-1]}, fewer than the {rot} that turn")
-    if shape[-1] > 1 and t.stride(-1) != 1:
+    D = shape[-1]
+    if D * shape[-2] >= 1 << 31:
+        raise ValueError(f"{name} {tuple(shape)} has 2^31 elements a token or more")
+    if i < 2 and D < rot:
+        raise ValueError(f"{name} has heads of {D}, fewer than the {rot} that turn")
+    if D > 1 and t.stride(-1) != 1:
         raise ValueError(f"the elements of a head of {name} must be contiguous")
 
 
