@@ -41,7 +41,9 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+// (the aligned form wants whole warps: lanes that come out of a loop one by one meet first)
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 // The shared::cluster address of `p` in the CTA of rank 0.
@@ -708,7 +710,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   // the leader's last arrivals here come in before this CTA can end
   if (!leader && warp == 1) mbar_wait_drain(drain, 0, 100000000ull);
-  __syncwarp();
   cluster_sync();
   if (warp == 2) {
     tc_fence_after();

@@ -470,3 +470,15 @@ def test_failure_detection(L, M):
         dash.set_wait_limit(limit)
     again, _ = dash.dense_fwd(x, w, residual=r, check=True, **a)
     assert torch.equal(again, y)
+
+
+@gpu
+@pytest.mark.parametrize("size", [(1, 8192, 129), (1, 16384, 4), (3, 8192, 130), (2, 4096, 259)], ids=str)
+def test_few_rows_whose_outputs_do_not_fill_a_warp(L, size):
+    """A CTA of a cluster finishes a part of the outputs that is no whole number of warps, some lanes of
+    it behind the last column; they meet again at the cluster's barrier."""
+    x, w, a, r = case(*size, "kn", BF, ("silu", True, True, True))
+    y, kept = dash.dense_fwd(x, w, residual=r, check=True, **a)
+    check_forward(x, w, y, kept, residual=r, **a)
+    for _ in range(20):
+        assert torch.equal(dash.dense_fwd(x, w, residual=r, check=True, **a)[0], y)
