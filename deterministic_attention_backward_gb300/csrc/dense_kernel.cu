@@ -596,7 +596,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (++s == kStages) s = 0, ph ^= 1;
       }
     }
-    if (!ok && leader && !isb)  // leave no copy in flight into shared memory
+    // Leave no copy in flight into shared memory, whichever warp it was that gave up: both producers, as
+    // one may be ahead of the other (the leader's barriers count the other CTA's copies too).
+    if (leader)
       for (int j = max(0, it - kStages); j < it; ++j)
         mbar_wait_drain(&full[j % kStages], (j / kStages) & 1, 100000000ull);
   } else if (warp == 1) {
@@ -842,9 +844,9 @@ __global__ void __launch_bounds__(kFewThreads)
       bring(k0 + it, s);
       if (++s == p.stages) s = 0, ph ^= 1;
     }
-    if (!ok || wanted < k1 - k0)  // leave no copy in flight into shared memory
-      for (int j = max(0, it - p.stages); j < it; ++j)
-        mbar_wait_drain(&full[j % p.stages], (j / p.stages) & 1, 100000000ull);
+    // leave no copy in flight into shared memory, whichever warp it was that gave up
+    for (int j = max(0, it - p.stages); j < it; ++j)
+      mbar_wait_drain(&full[j % p.stages], (j / p.stages) & 1, 100000000ull);
   } else if (ok && warp == 1) {
     const uint32_t kind = std::is_same<T, __half>::value ? 0u : (1u << 7) | (1u << 10);
     const uint32_t idesc = (1u << 4) | kind | ((uint32_t)p.w_mn << 15) |

@@ -482,3 +482,33 @@ def test_few_rows_whose_outputs_do_not_fill_a_warp(L, size):
     check_forward(x, w, y, kept, residual=r, **a)
     for _ in range(20):
         assert torch.equal(dash.dense_fwd(x, w, residual=r, check=True, **a)[0], y)
+
+
+@gpu
+@pytest.mark.parametrize("M,block", [(700, 7), (5, 13)])
+def test_failure_behind_the_first_filling(L, M, block):
+    """The loads end when every place of a ring has been filled once: nothing of the call is under way
+    any more when the next ones, which use the same shared memory, give their usual bits."""
+    K, N = 8192, 1000
+    x, w, a, r = case(M, K, N, "nk", BF, ("silu", False, True, True))
+    y, kept = dash.dense_fwd(x, w, residual=r, **a)
+    dy = make((M, N), BF, 9)
+    grads = dash.dense_bwd(dy, x, w, kept, **a)
+    limit = dash.wait_limit()
+    dash.set_wait_limit(0.05)
+    try:
+        assert L.dash_dense_withhold(block) == 0
+        with pytest.raises(dash.DashError) as e:
+            dash.dense_fwd(x, w, residual=r, check=True, **a)
+        assert e.value.code == 4
+        L.dash_dense_withhold(0)
+        with pytest.raises(dash.DashError) as e:
+            dash.dense_bwd(dy, x, w, kept, check=True, **a)
+        assert e.value.code == 4
+    finally:
+        L.dash_dense_withhold(-1)
+        dash.set_wait_limit(limit)
+    for _ in range(3):
+        assert torch.equal(dash.dense_fwd(x, w, residual=r, check=True, **a)[0], y)
+        again = dash.dense_bwd(dy, x, w, kept, check=True, **a)
+        assert all(p is q or torch.equal(p, q) for p, q in zip(grads, again))
