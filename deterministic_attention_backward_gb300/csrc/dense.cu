@@ -48,6 +48,7 @@ bool make_rows_map(CUtensorMap *m, const Rows &r, int box, bool f16) {
 struct Product {
   int M, N, K, parts, outs;
   bool gated;
+  bool stack = false;  // A's second term in the tile's other 128 rows
   int bn = 256, whole = 0, splits = 1, per = 0;
   int cols() const { return gated ? bn / 2 : bn; }
   int mt() const { return ceil_div(M, kDenseM); }
@@ -55,7 +56,7 @@ struct Product {
   int nk() const { return ceil_div(K, kDenseK); }
   long long tiles() const { return (long long)mt() * nt() * outs; }
   size_t part_bytes() const {
-    return splits > 1 ? (size_t)(tiles() - whole) * splits * kDenseM * bn * 4 : 0;
+    return splits > 1 || stack ? (size_t)(tiles() - whole) * splits * kDenseM * bn * 4 : 0;
   }
 };
 
@@ -67,17 +68,17 @@ struct Product {
 // pairs better, 39 against 40), an item 3 beside its blocks, the kernel that adds the splits 10 and the
 // partial sums their way to memory.
 constexpr int kPairs = 76, kMaxSplits = 64;
-Product plan(int M, int N, int K, int parts, int outs, bool gated) {
+Product plan(int M, int N, int K, int parts, int outs, bool gated, bool stack = false) {
   Product best;
   double least = 0;
   for (int bn = 256; bn >= 128; bn -= 128) {
-    Product p{M, N, K, parts, outs, gated, bn};
+    Product p{M, N, K, parts, outs, gated, stack, bn};
     const long long tiles = p.tiles(), rounds = tiles / kPairs;
     if (tiles >= (1LL << 28)) continue;
     const int blocks = p.nk() * parts;
     const double block = bn == 256 ? 1.0 : 0.62;
-    // whole rounds stay whole, or (a few rounds) every tile is split
-    for (int all = 0; all <= (rounds > 0 && rounds < 4); ++all) {
+    // whole rounds stay whole, or (a few rounds; two terms, which are added behind) every tile is split
+    for (int all = stack; all <= (stack || (rounds > 0 && rounds < 4)); ++all) {
       p.whole = all ? 0 : (int)(rounds * kPairs);
       const long long cut = tiles - p.whole;
       for (int s = 1; s <= kMaxSplits && s <= blocks; ++s) {
@@ -86,7 +87,7 @@ Product plan(int M, int N, int K, int parts, int outs, bool gated) {
         if (s > 1 && (cut == 0 || cut * s > 8 * kPairs)) break;
         double t = (double)(p.whole / kPairs) * (blocks * block + 3);
         t += (double)((cut * s + kPairs - 1) / kPairs) * (p.per * block + 3);
-        if (s > 1) t += 10 + 8.0 * cut * s * (M < kDenseM ? M : kDenseM) * bn / 1.8e6;
+        if (s > 1 || stack) t += 10 + 8.0 * cut * s * (M < kDenseM ? M : kDenseM) * bn / 1.8e6;
         if (least == 0 || t < 0.98 * least) {
           least = t;
           best = p;
@@ -231,7 +232,7 @@ dash_status_t launch(const Product &p, const Rows (&a)[2], const Rows (&b)[2], b
   d.nk = p.nk(), d.parts = p.parts, d.outs = p.outs;
   d.whole = p.whole, d.splits = p.splits, d.per = p.per;
   d.a_mn = a_mn, d.b_mn = b_mn, d.a_out = a_out, d.b_out = b_out;
-  d.pairs = pairs, d.a_low = a_low, d.b_low = b_low;
+  d.pairs = pairs, d.stack = p.stack, d.a_low = a_low, d.b_low = b_low;
   d.withhold = g_dense_withhold.load();
   return launch_dense(f16, ta, tb, d, sms, s) == cudaSuccess ? DASH_OK : DASH_ERR_CUDA;
 }
@@ -279,9 +280,15 @@ dash_status_t check_fwd(const dash_dense_fwd_t *a, Fwd &f) {
 
 // ------------------------------------------------------------------ backward
 // dz is rounded for the tensor core, which is off by as much as the rounding of dx and dw: 1.4 times that
-// in all.  Of few elements it may come out well above that, and to multiply what the rounding lost as well
-// costs nothing there.
+// in all.  Of few elements it may come out well above that, and what the rounding lost is multiplied as
+// well there.  Of dx's rows up to 128 the second term takes the tile's other half, which is empty: every
+// block of the weights is read and multiplied once for both (as a second pass over the weights 8 x 8192 x
+// 8192 took 60 us, now 46, without a second term 44).
 constexpr long long kTwoTerms = 1 << 16;  // elements of dz
+// Such a dx writes all its tiles' sums to the workspace: no more of them than a split would.
+bool stacked(int M, int K) {
+  return M <= kDenseM / 2 && ceil_div(K, 256) <= 8 * kPairs;
+}
 struct Bwd {
   Product dx, dw;
   int terms;
@@ -319,7 +326,8 @@ dash_status_t check_bwd(const dash_dense_bwd_t *a, Bwd &b) {
   if (a->M > kMaxSize || a->K > kMaxSize || a->N > kMaxSize) return DASH_ERR_UNSUPPORTED;
   const int M = a->M ? a->M : 1;
   b.terms = b.grads && (long long)M * a->N <= kTwoTerms ? 2 : 1;
-  b.dx = plan(M, a->K, a->N, (gated ? 2 : 1) * b.terms, 1, false);
+  const bool stack = b.terms == 2 && stacked(M, a->K);
+  b.dx = plan(M, a->K, a->N, (gated ? 2 : 1) * (stack ? 1 : b.terms), 1, false, stack);
   b.dw = kn ? plan(a->K, a->N, M, b.terms, gated ? 2 : 1, false)
             : plan(a->N, a->K, M, b.terms, gated ? 2 : 1, false);
   if (!sizes_ok(b.dx) || !sizes_ok(b.dw)) return DASH_ERR_UNSUPPORTED;

@@ -50,6 +50,7 @@ struct DenseParams {
   int mt, nt, bn;            // tiles; bn columns of a tile's accumulator (gated: half z, half g)
   int nk, parts, outs;       // blocks of kDenseK of a part; parts, terms counted too
   int pairs;                 // parts go by pairs of operands (a gated dx): the first pair, the second
+  int stack;                 // A's second term in rows 128 on of the (only) tile's, added behind
   int a_low, b_low;          // rows behind which an operand's second term begins (0: it has the same)
   int whole, splits, per;    // tiles that are whole; splits of each other tile, blocks of a split
   int a_mn, b_mn;            // the contiguous dimension is M (N), not the contraction

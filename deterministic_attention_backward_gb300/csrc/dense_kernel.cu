@@ -484,7 +484,7 @@ __device__ __forceinline__ Item item_of(const DenseParams &p, int t) {
   w.k0 = 0, w.k1 = p.nk * p.parts;
   if (t >= p.whole) {
     const int j = t - p.whole, tile = j / p.splits;
-    if (p.splits > 1) {
+    if (p.splits > 1 || p.stack) {
       w.cut = j;
       w.k0 = (j - tile * p.splits) * p.per;
       w.k1 = min(w.k0 + p.per, w.k1);
@@ -571,7 +571,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int t = first; ok && t < items; t += step) {
       const Item w = item_of(p, t);
       // gated: the leader brings w's columns of the tile, the other CTA w_gate's
-      const int at = !isb         ? w.m + (int)rank * 128
+      const int at = !isb         ? w.m + (int)rank * (p.stack ? p.a_low : 128)
                      : p.e.gated ? w.n * half
                                  : w.n * p.bn + (int)rank * half;
       const bool second = isb ? (w.out && p.b_out) || (p.e.gated && rank) : w.out && p.a_out;
@@ -582,7 +582,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         const int q = (k >= p.nk) + (k >= 2 * p.nk) + (k >= 3 * p.nk);
         const int term = p.pairs ? q >> 1 : q, kk = (k - q * p.nk) * kDenseK;
-        const int low = term * (isb ? p.b_low : p.a_low);
+        const int low = term * (isb ? p.b_low : p.a_low);  // (0 where terms are stacked)
         const CUtensorMap *map =
             (p.pairs && (q & 1)) || second ? (isb ? &tb1 : &ta1) : (isb ? &tb0 : &ta0);
         const uint32_t bar = bar0 + 8 * s, dst = base + s * kStageBytes;
@@ -646,7 +646,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int n = 0;
     for (int t = first; t < items; t += step, ++n) {
       const Item w = item_of(p, t);
-      const long long row0 = w.m + (int)rank * 128 + quad * 32;
+      const long long row0 = w.m + (p.stack ? 0 : (int)rank * 128) + quad * 32;
       const int rows = (int)max(0ll, min(32ll, p.M - row0));
       const int n0 = w.n * cols;
       // the residual's pieces are under way while the products are formed
@@ -755,11 +755,14 @@ __global__ void __launch_bounds__(256) dense_finish_kernel(const __grid_constant
   for (int s = 0; s < p.splits; ++s, src += stride) {
     const float4 v = *reinterpret_cast<const float4 *>(src);
     z[0] += v.x, z[1] += v.y, z[2] += v.z, z[3] += v.w;
-    if (e.gated) {
-      const float4 u = *reinterpret_cast<const float4 *>(src + p.bn / 2);
+    if (e.gated || p.stack) {
+      const float4 u = *reinterpret_cast<const float4 *>(src + (p.stack ? 128 * p.bn : p.bn / 2));
       g[0] += u.x, g[1] += u.y, g[2] += u.z, g[3] += u.w;
     }
   }
+  if (p.stack)  // the second term
+#pragma unroll
+    for (int k = 0; k < 4; ++k) z[k] += g[k];
   finish4<T>(e, w.out ? p.y1 : e.y, w.out ? p.y1s : e.ys, row, n, p.N, z, g);
 }
 
@@ -1068,7 +1071,7 @@ cudaError_t launch_t(const CUtensorMap (&ta)[2], const CUtensorMap (&tb)[2], con
   const int rest = p.mt * p.nt * p.outs - p.whole, items = p.whole + rest * p.splits;
   const int pairs = items < sms / 2 ? items : sms / 2;
   dense_kernel<T><<<2 * pairs, kThreads, kSmem, s>>>(ta[0], ta[1], tb[0], tb[1], p);
-  if (rest > 0 && p.splits > 1) {
+  if (rest > 0 && (p.splits > 1 || p.stack)) {
     const int rows = p.M < kDenseM ? p.M : kDenseM, cols = p.e.gated ? p.bn / 2 : p.bn;
     dense_finish_kernel<T><<<dim3((rows * (cols / 4) + 255) / 256, rest), 256, 0, s>>>(p);
   }

@@ -512,3 +512,48 @@ def test_failure_behind_the_first_filling(L, M, block):
         assert torch.equal(dash.dense_fwd(x, w, residual=r, check=True, **a)[0], y)
         again = dash.dense_bwd(dy, x, w, kept, check=True, **a)
         assert all(p is q or torch.equal(p, q) for p, q in zip(grads, again))
+
+
+@gpu
+@pytest.mark.parametrize("epilogue", [EPILOGUES[0], EPILOGUES[1], EPILOGUES[3]], ids=lambda e: e[0])
+@pytest.mark.parametrize("size", [(127, 300, 512), (128, 4099, 512), (129, 300, 500), (2, 155648, 24),
+                                  (2, 155649, 24), (1, 520, 20000)], ids=str)
+def test_backward_of_few_rows(L, size, epilogue):
+    """The second term of dz in a tile's other half, and where it does not fit there."""
+    M, K, N = size
+    x, w, a, r = case(*size, "nk", BF, epilogue)
+    _, kept = dash.dense_fwd(x, w, **a)
+    dy = make((M, N), BF, 9)
+    grads = dash.dense_bwd(dy, x, w, kept, check=True, **a)
+    check_backward(dy, x, w, kept, grads, **a)
+    need = dash.dense_bwd_workspace_bytes(dy, x, w, kept, **a)
+    ws = torch.full((need + 64,), 255, dtype=torch.uint8, device="cuda")
+    again = dash.dense_bwd(dy, x, w, kept, workspace=ws[:need], check=True, **a)
+    assert all(p is q or torch.equal(p, q) for p, q in zip(grads, again))
+    assert (ws[need:] == 255).all()
+
+
+@gpu
+def test_the_second_term_reads_the_weights_once(L):
+    """dx of few rows with and without an activation: of weights that L2 does not hold (268 MB, 40 us of
+    memory) a second pass would take half as long again and more."""
+    M, K, N = 8, 16384, 8192
+    x, w, dy = make((M, K), BF, 0), make((K, N), BF, 1, K ** -0.5), make((M, N), BF, 2)
+    _, kept = dash.dense_fwd(x, w, act="relu")
+    time = {}
+    for act in ("none", "relu"):
+        dash.dense_bwd(dy, x, w, kept, act=act, need_dw=False)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(4):
+                dash.dense_bwd(dy, x, w, kept, act=act, need_dw=False)
+        runs = []
+        for _ in range(12):
+            start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            start.record()
+            g.replay()
+            end.record()
+            end.synchronize()
+            runs.append(start.elapsed_time(end))
+        time[act] = sorted(runs)[len(runs) // 2]
+    assert time["relu"] < 1.3 * time["none"], time
