@@ -50,6 +50,7 @@ struct Product {
   bool gated;
   bool stack = false;  // A's second term in the tile's other 128 rows
   int bn = 256, whole = 0, splits = 1, per = 0;
+  double cost = 0;
   int cols() const { return gated ? bn / 2 : bn; }
   int mt() const { return ceil_div(M, kDenseM); }
   int nt() const { return ceil_div(N, cols()); }
@@ -70,7 +71,6 @@ struct Product {
 constexpr int kPairs = 76, kMaxSplits = 64;
 Product plan(int M, int N, int K, int parts, int outs, bool gated, bool stack = false) {
   Product best;
-  double least = 0;
   for (int bn = 256; bn >= 128; bn -= 128) {
     Product p{M, N, K, parts, outs, gated, stack, bn};
     const long long tiles = p.tiles(), rounds = tiles / kPairs;
@@ -88,10 +88,10 @@ Product plan(int M, int N, int K, int parts, int outs, bool gated, bool stack = 
         double t = (double)(p.whole / kPairs) * (blocks * block + 3);
         t += (double)((cut * s + kPairs - 1) / kPairs) * (p.per * block + 3);
         if (s > 1 || stack) t += 10 + 8.0 * cut * s * (M < kDenseM ? M : kDenseM) * bn / 1.8e6;
-        if (least == 0 || t < 0.98 * least) {
-          least = t;
+        if (best.cost == 0 || t < 0.98 * best.cost) {
           best = p;
           best.splits = s;
+          best.cost = t;
         }
       }
     }
@@ -211,7 +211,7 @@ unsigned long long wait_limit_ns() {
 dash_status_t launch(const Product &p, const Rows (&a)[2], const Rows (&b)[2], bool a_mn, bool b_mn,
                      bool a_out, bool b_out, bool pairs, int a_low, int b_low,
                      const DenseEpilogue &e, void *y1, long long y1s, float *part, void *workspace,
-                     bool clear, bool f16, int sms, cudaStream_t s) {
+                     bool clear, bool f16, int sms, cudaStream_t s, uint32_t *special = nullptr) {
   CUtensorMap ta[2], tb[2];
   for (int i = 0; i < 2; ++i)
     if (!make_rows_map(&ta[i], a[i].at ? a[i] : a[0], a_mn ? 64 : 128, f16) ||
@@ -222,6 +222,7 @@ dash_status_t launch(const Product &p, const Rows (&a)[2], const Rows (&b)[2], b
   d.y1 = y1, d.y1s = y1s;
   d.part = part;
   d.status = static_cast<uint32_t *>(workspace);
+  d.special = special;
   d.clear = clear;
   d.wait_ns = wait_limit_ns();
   d.M = p.M, d.N = p.N;
@@ -281,13 +282,17 @@ dash_status_t check_fwd(const dash_dense_fwd_t *a, Fwd &f) {
 // ------------------------------------------------------------------ backward
 // dz is rounded for the tensor core, which is off by as much as the rounding of dx and dw: 1.4 times that
 // in all.  Of few elements it may come out well above that, and what the rounding lost is multiplied as
-// well there.  Of dx's rows up to 128 the second term takes the tile's other half, which is empty: every
-// block of the weights is read and multiplied once for both (as a second pass over the weights 8 x 8192 x
-// 8192 took 60 us, now 46, without a second term 44).
+// well there.
 constexpr long long kTwoTerms = 1 << 16;  // elements of dz
-// Such a dx writes all its tiles' sums to the workspace: no more of them than a split would.
-bool stacked(int M, int K) {
-  return M <= kDenseM / 2 && ceil_div(K, 256) <= 8 * kPairs;
+// dx: a second term is another part of the contraction, or, of up to 128 rows, takes the tile's other half,
+// which is empty: every block of the weights is read and multiplied once for both (8 x 8192 x 8192 46 us,
+// without a second term 44, as another part 60).  That writes all tiles' sums to the workspace (no more of
+// them than a split would), so short contractions go the other way (128 x 4096 x 512 22 us, stacked 25).
+Product plan_dx(int M, int N, int K, int parts, int terms) {
+  const Product p = plan(M, N, K, parts * terms, 1, false);
+  if (terms == 1 || M > kDenseM / 2 || ceil_div(N, 256) > 8 * kPairs) return p;
+  const Product q = plan(M, N, K, parts, 1, false, true);
+  return q.per > 0 && q.cost < p.cost ? q : p;
 }
 struct Bwd {
   Product dx, dw;
@@ -297,6 +302,7 @@ struct Bwd {
   bool grads, pad_dy;  // dz (and dgate) are formed; dy is copied
   int chunks, chunk;
   size_t dz_bytes, sum_bytes, part_bytes, need;
+  size_t special_bytes() const { return terms == 2 ? kStatusBytes : 0; }
 };
 dash_status_t check_bwd(const dash_dense_bwd_t *a, Bwd &b) {
   if (!a || !a->dy || a->M < 0 || a->K <= 0 || a->N <= 0) return DASH_ERR_INVALID;
@@ -326,8 +332,7 @@ dash_status_t check_bwd(const dash_dense_bwd_t *a, Bwd &b) {
   if (a->M > kMaxSize || a->K > kMaxSize || a->N > kMaxSize) return DASH_ERR_UNSUPPORTED;
   const int M = a->M ? a->M : 1;
   b.terms = b.grads && (long long)M * a->N <= kTwoTerms ? 2 : 1;
-  const bool stack = b.terms == 2 && stacked(M, a->K);
-  b.dx = plan(M, a->K, a->N, (gated ? 2 : 1) * (stack ? 1 : b.terms), 1, false, stack);
+  b.dx = plan_dx(M, a->K, a->N, gated ? 2 : 1, b.terms);
   b.dw = kn ? plan(a->K, a->N, M, b.terms, gated ? 2 : 1, false)
             : plan(a->N, a->K, M, b.terms, gated ? 2 : 1, false);
   if (!sizes_ok(b.dx) || !sizes_ok(b.dw)) return DASH_ERR_UNSUPPORTED;
@@ -347,7 +352,7 @@ dash_status_t check_bwd(const dash_dense_bwd_t *a, Bwd &b) {
   b.out[2] = Out(a->dw_gate, a->dw_gate_stride, wr, wc);
   b.need = kStatusBytes + b.out[0].bytes() + b.out[1].bytes() + b.out[2].bytes() +
            (gated ? 2 : 1) * b.dz_bytes + (a->dbias ? b.sum_bytes : 0) +
-           (a->dbias_gate ? b.sum_bytes : 0) + b.part_bytes + (b.pad_dy ? b.dy.bytes() : 0) +
+           (a->dbias_gate ? b.sum_bytes : 0) + b.special_bytes() + b.part_bytes + (b.pad_dy ? b.dy.bytes() : 0) +
            b.x.bytes() + b.w[0].bytes() + b.w[1].bytes();
   return DASH_OK;
 }
@@ -473,6 +478,7 @@ dash_status_t dash_dense_bwd(const dash_dense_bwd_t *a, void *workspace, size_t 
   void *dz_at = arena.take(b.dz_bytes), *dg_at = gated ? arena.take(b.dz_bytes) : nullptr;
   float *sum = static_cast<float *>(arena.take(a->dbias ? b.sum_bytes : 0));
   float *sum_gate = static_cast<float *>(arena.take(a->dbias_gate ? b.sum_bytes : 0));
+  uint32_t *special = static_cast<uint32_t *>(arena.take(b.special_bytes()));
   float *part = static_cast<float *>(arena.take(b.part_bytes));
   if (b.grads || a->dbias) {
     DenseGradParams g{};
@@ -482,6 +488,7 @@ dash_status_t dash_dense_bwd(const dash_dense_bwd_t *a, void *workspace, size_t 
       g.g = kept_at(const_cast<void *>(a->gate), a->M, a->N);
     g.dz = dz_at, g.dg = dg_at;
     g.low = b.terms == 2;
+    g.special = special;
     g.part = sum, g.part_gate = sum_gate;
     g.dys = b.dy.stride, g.ks = kept_stride(a->N), g.ds = up(a->N, 8);
     g.M = a->M, g.N = a->N, g.act = a->act, g.chunk = b.chunk;
@@ -506,7 +513,7 @@ dash_status_t dash_dense_bwd(const dash_dense_bwd_t *a, void *workspace, size_t 
     DenseEpilogue e{};
     e.y = b.out[0].at, e.ys = b.out[0].stride;
     st = launch(b.dx, dz, b.w, false, !kn, false, false, gated, low, 0, e, nullptr, 0, part,
-                workspace, true, f16, dev.sms, s);
+                workspace, true, f16, dev.sms, s, b.dx.stack ? nullptr : special);
     if (st != DASH_OK) return st;
   }
   if (a->dw) {
@@ -514,10 +521,31 @@ dash_status_t dash_dense_bwd(const dash_dense_bwd_t *a, void *workspace, size_t 
     e.y = b.out[1].at, e.ys = b.out[1].stride;
     const Rows x[2] = {b.x, Rows()};
     st = kn ? launch(b.dw, x, dz, true, true, false, gated, false, 0, low, e, b.out[2].at,
-                     b.out[2].stride, part, workspace, !a->dx, f16, dev.sms, s)
+                     b.out[2].stride, part, workspace, !a->dx, f16, dev.sms, s, special)
             : launch(b.dw, dz, x, true, true, gated, false, false, low, 0, e, b.out[2].at,
-                     b.out[2].stride, part, workspace, !a->dx, f16, dev.sms, s);
+                     b.out[2].stride, part, workspace, !a->dx, f16, dev.sms, s, special);
     if (st != DASH_OK) return st;
+  }
+  if (special && (a->dw || !b.dx.stack)) {
+    DenseSpecials sp{};
+    sp.set = special;
+    auto along_row = [](const Rows &r) { return DenseOperand{r.at, r.stride, 1}; };
+    auto along_column = [](const Rows &r) { return DenseOperand{r.at, 1, r.stride}; };
+    if (a->dx && !b.dx.stack) {
+      DenseSpecial &q = sp.s[0];
+      q = {b.out[0].at, b.out[0].stride, a->M, a->K, a->N, gated ? 2 : 1};
+      for (int i = 0; i < q.parts; ++i) {
+        q.a[i] = along_row(dz[i]);
+        q.b[i] = kn ? along_row(b.w[i]) : along_column(b.w[i]);
+      }
+    }
+    for (int i = 0; a->dw && i <= (int)gated; ++i) {
+      DenseSpecial &q = sp.s[1 + i];
+      q = {b.out[1 + i].at, b.out[1 + i].stride, wr, wc, a->M, 1};
+      q.a[0] = along_column(kn ? b.x : dz[i]);
+      q.b[0] = along_column(kn ? dz[i] : b.x);
+    }
+    if (launch_dense_specials(f16, sp, s) != cudaSuccess) return DASH_ERR_CUDA;
   }
   for (const Out &o : b.out) o.finish(out);
   return out.run(s) ? DASH_OK : DASH_ERR_CUDA;

@@ -43,6 +43,7 @@ struct DenseParams {
   long long y1s;
   float *part;               // fp32 sums of the split tiles: [tile][split][256][bn]
   uint32_t *status;
+  uint32_t *special;         // set where a sum is infinite or NaN; null: not asked
   int clear;                 // the status block (the first product of a call does)
   unsigned long long wait_ns;
   int M, N;
@@ -50,7 +51,8 @@ struct DenseParams {
   int mt, nt, bn;            // tiles; bn columns of a tile's accumulator (gated: half z, half g)
   int nk, parts, outs;       // blocks of kDenseK of a part; parts, terms counted too
   int pairs;                 // parts go by pairs of operands (a gated dx): the first pair, the second
-  int stack;                 // A's second term in rows 128 on of the (only) tile's, added behind
+  int stack;                 // A's second term in rows 128 on of the (only) tile's, added behind to sums
+                             // that are finite (see DenseSpecials)
   int a_low, b_low;          // rows behind which an operand's second term begins (0: it has the same)
   int whole, splits, per;    // tiles that are whole; splits of each other tile, blocks of a split
   int a_mn, b_mn;            // the contiguous dimension is M (N), not the contraction
@@ -79,10 +81,30 @@ struct DenseGradParams {
   DenseKept z, g;            // no z: dz = dy (and is not written); no g: not gated
   void *dz, *dg;             // null where only the sums are wanted
   int low;                   // what dz and dg lose by rounding follows them, M rows on
+  uint32_t *special;         // cleared (DenseParams), null: there is none
   float *part, *part_gate;   // [chunks][N]; null where the sums are not wanted
   long long dys, ks, ds;
   int M, N, act, chunk;      // rows of a chunk
   int vec;                   // dy lies on 16 bytes
+};
+
+// A second term of dz is added to the first one's sums in one accumulator.  An infinity in x or a weight is
+// multiplied by both: infinity times a second term that is 0, or of the other sign, would make NaN of what
+// is infinite.  Such elements are formed again from the first term alone, out[r, c] = sum over parts and k
+// of a[r, k] b[c, k], as a call of one term has them.
+struct DenseOperand {
+  const void *at;
+  long long row, k;          // strides in elements
+};
+struct DenseSpecial {
+  void *out;                 // null: nothing to do
+  long long stride;
+  int rows, cols, K, parts;
+  DenseOperand a[2], b[2];
+};
+struct DenseSpecials {
+  DenseSpecial s[3];
+  const uint32_t *set;
 };
 
 cudaError_t launch_dense(bool f16, const CUtensorMap (&ta)[2], const CUtensorMap (&tb)[2],
@@ -90,6 +112,7 @@ cudaError_t launch_dense(bool f16, const CUtensorMap (&ta)[2], const CUtensorMap
 cudaError_t launch_dense_few(bool f16, const CUtensorMap &tw0, const CUtensorMap &tw1,
                              const CUtensorMap &tx, const DenseFewParams &p, cudaStream_t s);
 cudaError_t launch_dense_grad(bool f16, const DenseGradParams &p, int chunks, cudaStream_t s);
+cudaError_t launch_dense_specials(bool f16, const DenseSpecials &p, cudaStream_t s);
 // out[n] = sum over chunks, in order (gate: a second row of sums and its output)
 cudaError_t launch_dense_sums(bool f16, const float *part, const float *part_gate, void *out,
                               void *out_gate, int chunks, int N, cudaStream_t s);

@@ -284,6 +284,15 @@ __device__ __forceinline__ void activate(int act, float (&z)[C]) {
   }
 }
 
+// Sets a word where one of the sums is infinite or NaN.
+template <int C>
+__device__ __forceinline__ void flag_special(uint32_t *set, const float (&v)[C]) {
+  float zero[4] = {};  // (NaN from there on)
+#pragma unroll
+  for (int e = 0; e < C; ++e) zero[e & 3] = fmaf(v[e], 0.f, zero[e & 3]);
+  if ((zero[0] + zero[1]) + (zero[2] + zero[3]) != 0.f) *set = 1;
+}
+
 // C values from column n of a row on, `left` of them inside it.
 template <typename T, int C>
 __device__ __forceinline__ void store_cols(void *base, long long at, const float (&v)[C], int left) {
@@ -678,6 +687,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           float z[32], g[32];
           load32(acc + c, z);
           if (e.gated) load32(acc + p.bn / 2 + c, g);
+          if (p.special) flag_special(p.special, z);
           if (e.bias) add_bias<T>(e.bias, at, z, left, lane);
           if (e.z.hi) turn_keep(turn, turn2, e.z, e.ks, row0, rows, at, lane, z);
           if (e.gated) {
@@ -762,7 +772,9 @@ __global__ void __launch_bounds__(256) dense_finish_kernel(const __grid_constant
   }
   if (p.stack)  // the second term
 #pragma unroll
-    for (int k = 0; k < 4; ++k) z[k] += g[k];
+    for (int k = 0; k < 4; ++k) z[k] = isfinite(z[k]) ? z[k] + g[k] : z[k];
+  else if (p.special)
+    flag_special(p.special, z);
   finish4<T>(e, w.out ? p.y1 : e.y, w.out ? p.y1s : e.ys, row, n, p.N, z, g);
 }
 
@@ -913,6 +925,30 @@ __global__ void __launch_bounds__(kFewThreads)
   cluster_sync();  // the others have read what is here
 }
 
+// ------------------------------------------------------------------ infinities and NaN of two terms
+// A thread an element; ends at once where no product has set the word (the launch and the products' look
+// at their sums take 2 to 5 us: dw of 8 x 14336 x 8192 97 -> 102; sums in accumulators apart, 128 columns a
+// tile, 128).
+template <typename T>
+__global__ void __launch_bounds__(256) dense_specials_kernel(const __grid_constant__ DenseSpecials p) {
+  const DenseSpecial &q = p.s[blockIdx.y];
+  if (!q.out || *p.set == 0) return;
+  const long long count = (long long)q.rows * q.cols;
+  for (long long i = blockIdx.x * 256 + threadIdx.x; i < count; i += gridDim.x * 256) {
+    const long long r = i / q.cols, c = i - r * q.cols;
+    T *out = static_cast<T *>(q.out) + r * q.stride + c;
+    if (isfinite(to_f32<T>(*out))) continue;
+    float sum = 0.f;
+    for (int part = 0; part < q.parts; ++part) {
+      const T *a = static_cast<const T *>(q.a[part].at) + r * q.a[part].row;
+      const T *b = static_cast<const T *>(q.b[part].at) + c * q.b[part].row;
+      for (int k = 0; k < q.K; ++k, a += q.a[part].k, b += q.b[part].k)
+        sum = fmaf(to_f32<T>(*a), to_f32<T>(*b), sum);
+    }
+    *out = from_f32<T>(sum);
+  }
+}
+
 // ------------------------------------------------------------------ dz, dgate and their sums
 // 32 threads a strip of 256 columns, 8 rows at a time over a chunk of rows; the eight rows' sums are
 // added in order through shared memory.  Bound by memory: 8192 x 14336 gated, 12 bytes an element, in
@@ -927,6 +963,7 @@ __global__ void __launch_bounds__(256, kSums ? 3 : 4)
   const int r1 = min(p.M, (int)(blockIdx.y + 1) * p.chunk);
   const bool whole = p.vec && n + V <= p.N;
   float sz[V] = {}, sg[V] = {};
+  if (p.special && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.special = 0;
   auto kept = [&](const DenseKept &k, long long r, uint4 &h, uint2 &l) {
     h = *reinterpret_cast<const uint4 *>(k.hi + r * p.ks + n);
     l = *reinterpret_cast<const uint2 *>(k.lo + r * p.ks + n);
@@ -1131,6 +1168,15 @@ cudaError_t launch_dense_grad(bool f16, const DenseGradParams &p, int chunks, cu
     case DASH_ACT_SILU: return launch_grad<DASH_ACT_SILU>(f16, p, chunks, s);
     default: return launch_grad<DASH_ACT_NONE>(f16, p, chunks, s);
   }
+}
+
+cudaError_t launch_dense_specials(bool f16, const DenseSpecials &p, cudaStream_t s) {
+  const dim3 grid(4 * 152, 3);
+  if (f16)
+    dense_specials_kernel<__half><<<grid, 256, 0, s>>>(p);
+  else
+    dense_specials_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(p);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_dense_sums(bool f16, const float *part, const float *part_gate, void *out,

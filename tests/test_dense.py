@@ -557,3 +557,30 @@ def test_the_second_term_reads_the_weights_once(L):
             runs.append(start.elapsed_time(end))
         time[act] = sorted(runs)[len(runs) // 2]
     assert time["relu"] < 1.3 * time["none"], time
+
+
+@gpu
+@pytest.mark.parametrize("order", ["kn", "nk"])
+@pytest.mark.parametrize("size", [(64, 64, 64), (64, 96, 1000), (200, 300, 300), (2000, 72, 24), (300, 72, 400)],
+                         ids=str)
+def test_infinities_in_the_backwards_operands(L, size, order):
+    """An infinity in x or in a weight is multiplied by dz: what comes out is infinite or NaN as dz's signs
+    and zeros have it, whether dz goes in one term or in two.  (relu, and dy of few bits: dz fits 16 bits,
+    so that a second term is 0.)"""
+    M, K, N = size
+    x, w, a, _ = case(M, K, N, order, BF, ("relu", False, False, False))
+    dy = make((M, N), BF, 9).sign() + 0.25
+    dy[:, N // 2] = 0.0
+    y, kept = dash.dense_fwd(x, w, act="relu")
+    dz = dy.double() * (unpacked(kept, M, N)[0] > 0)
+    assert (dz == dz.to(BF).double()).all()
+    x[M // 2, 3], x[M // 3, K - 1] = math.inf, -math.inf
+    w = w.clone(memory_format=torch.preserve_format)
+    w[5, N // 3], w[K - 2, N - 1], w[7, N // 2] = -math.inf, math.inf, math.inf
+    dx, dw, *_ = dash.dense_bwd(dy, x, w, kept, act="relu")
+    for got, ref in ((dx, dz @ w.double().t()), (dw, x.double().t() @ dz)):
+        got = got.double()
+        assert torch.equal(got.isnan(), ref.isnan())
+        assert torch.equal(got.isinf(), ref.isinf())
+        assert torch.equal(got[ref.isinf()], ref[ref.isinf()])
+        assert ref.isinf().any()
