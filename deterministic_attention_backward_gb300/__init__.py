@@ -57,7 +57,8 @@ EXPORTS = ["dash_attn_fwd_workspace_bytes", "dash_attn_fwd", "dash_attn_bwd_work
            "dash_diff_fwd_workspace_bytes", "dash_diff_fwd", "dash_diff_bwd_workspace_bytes",
            "dash_diff_bwd", "dash_diff_fwd_rest", "dash_diff_bwd_rest", "dash_diff_withhold",
            "dash_dense_fwd_workspace_bytes", "dash_dense_fwd", "dash_dense_bwd_workspace_bytes",
-           "dash_dense_bwd", "dash_dense_withhold", "dash_grad_norm_workspace_bytes",
+           "dash_dense_bwd", "dash_dense_bwd_terms_workspace_bytes", "dash_dense_bwd_terms",
+           "dash_dense_withhold", "dash_grad_norm_workspace_bytes",
            "dash_grad_norm", "dash_grad_clip"]
 
 
@@ -172,6 +173,10 @@ def lib() -> ctypes.CDLL:
             getattr(L, name + "_workspace_bytes").restype = sz
             getattr(L, name).argtypes = [cp, vp, sz, vp]
             getattr(L, name).restype = i
+        L.dash_dense_bwd_terms_workspace_bytes.argtypes = [cp, i]
+        L.dash_dense_bwd_terms_workspace_bytes.restype = sz
+        L.dash_dense_bwd_terms.argtypes = [cp, i, vp, sz, vp]
+        L.dash_dense_bwd_terms.restype = i
         L.dash_dense_withhold.argtypes = [i]
         L.dash_dense_withhold.restype = i
         L.dash_grad_norm_workspace_bytes.argtypes = [i]

@@ -282,7 +282,8 @@ dash_status_t check_fwd(const dash_dense_fwd_t *a, Fwd &f) {
 // ------------------------------------------------------------------ backward
 // dz is rounded for the tensor core, which is off by as much as the rounding of dx and dw: 1.4 times that
 // in all.  Of few elements it may come out well above that, and what the rounding lost is multiplied as
-// well there.
+// well there, unless the caller says otherwise (it doubles the products: 8192 x 4096 x 4096 345 us, 591 with
+// it).
 constexpr long long kTwoTerms = 1 << 16;  // elements of dz
 // dx: a second term is another part of the contraction, or, of up to 128 rows, takes the tile's other half,
 // which is empty: every block of the weights is read and multiplied once for both (8 x 8192 x 8192 46 us,
@@ -304,7 +305,8 @@ struct Bwd {
   size_t dz_bytes, sum_bytes, part_bytes, need;
   size_t special_bytes() const { return terms == 2 ? kStatusBytes : 0; }
 };
-dash_status_t check_bwd(const dash_dense_bwd_t *a, Bwd &b) {
+dash_status_t check_bwd(const dash_dense_bwd_t *a, int terms, Bwd &b) {
+  if (terms < 0 || terms > 2) return DASH_ERR_INVALID;
   if (!a || !a->dy || a->M < 0 || a->K <= 0 || a->N <= 0) return DASH_ERR_INVALID;
   if (a->order != DASH_DENSE_KN && a->order != DASH_DENSE_NK) return DASH_ERR_INVALID;
   if (a->act < DASH_ACT_NONE || a->act > DASH_ACT_SILU) return DASH_ERR_INVALID;
@@ -331,7 +333,8 @@ dash_status_t check_bwd(const dash_dense_bwd_t *a, Bwd &b) {
   b.w[1] = Rows(a->dx && gated ? a->w_gate : nullptr, a->w_gate_stride, wr, wc);
   if (a->M > kMaxSize || a->K > kMaxSize || a->N > kMaxSize) return DASH_ERR_UNSUPPORTED;
   const int M = a->M ? a->M : 1;
-  b.terms = b.grads && (long long)M * a->N <= kTwoTerms ? 2 : 1;
+  b.terms = !b.grads ? 1 : terms ? terms : (long long)M * a->N <= kTwoTerms ? 2 : 1;
+  if (b.terms == 2 && M > kMaxSize / 2) return DASH_ERR_UNSUPPORTED;
   b.dx = plan_dx(M, a->K, a->N, gated ? 2 : 1, b.terms);
   b.dw = kn ? plan(a->K, a->N, M, b.terms, gated ? 2 : 1, false)
             : plan(a->N, a->K, M, b.terms, gated ? 2 : 1, false);
@@ -436,15 +439,24 @@ dash_status_t dash_dense_fwd(const dash_dense_fwd_t *a, void *workspace, size_t 
 }
 
 size_t dash_dense_bwd_workspace_bytes(const dash_dense_bwd_t *args) {
-  dash::Bwd b;
-  return dash::check_bwd(args, b) == DASH_OK ? b.need : 0;
+  return dash_dense_bwd_terms_workspace_bytes(args, 0);
 }
 
-dash_status_t dash_dense_bwd(const dash_dense_bwd_t *a, void *workspace, size_t workspace_bytes,
+dash_status_t dash_dense_bwd(const dash_dense_bwd_t *args, void *workspace, size_t workspace_bytes,
                              dash_stream_t stream) {
+  return dash_dense_bwd_terms(args, 0, workspace, workspace_bytes, stream);
+}
+
+size_t dash_dense_bwd_terms_workspace_bytes(const dash_dense_bwd_t *args, int terms) {
+  dash::Bwd b;
+  return dash::check_bwd(args, terms, b) == DASH_OK ? b.need : 0;
+}
+
+dash_status_t dash_dense_bwd_terms(const dash_dense_bwd_t *a, int terms, void *workspace,
+                                   size_t workspace_bytes, dash_stream_t stream) {
   using namespace dash;
   Bwd b;
-  dash_status_t st = check_bwd(a, b);
+  dash_status_t st = check_bwd(a, terms, b);
   if (st != DASH_OK) return st;
   if (!workspace || !aligned16(workspace) || workspace_bytes < b.need) return DASH_ERR_WORKSPACE;
   const bool kn = a->order == DASH_DENSE_KN, gated = a->gate != nullptr,

@@ -926,26 +926,56 @@ __global__ void __launch_bounds__(kFewThreads)
 }
 
 // ------------------------------------------------------------------ infinities and NaN of two terms
-// A thread an element; ends at once where no product has set the word (the launch and the products' look
-// at their sums take 2 to 5 us: dw of 8 x 14336 x 8192 97 -> 102; sums in accumulators apart, 128 columns a
-// tile, 128).
+// Ends at once where no product has set the word (the launch and the products' look at their sums take 2 to
+// 5 us: dw of 8 x 14336 x 8192 97 -> 102; sums in accumulators apart, 128 columns a tile, 128).  Otherwise
+// the tiles of 64 x 64 that have such an element are summed in fp32, 4 x 4 elements a thread, so that a step
+// whose gradients are all NaN takes 28 ms at 8192 x 4096 x 4096 and no longer.
 template <typename T>
 __global__ void __launch_bounds__(256) dense_specials_kernel(const __grid_constant__ DenseSpecials p) {
   const DenseSpecial &q = p.s[blockIdx.y];
   if (!q.out || *p.set == 0) return;
-  const long long count = (long long)q.rows * q.cols;
-  for (long long i = blockIdx.x * 256 + threadIdx.x; i < count; i += gridDim.x * 256) {
-    const long long r = i / q.cols, c = i - r * q.cols;
-    T *out = static_cast<T *>(q.out) + r * q.stride + c;
-    if (isfinite(to_f32<T>(*out))) continue;
-    float sum = 0.f;
-    for (int part = 0; part < q.parts; ++part) {
-      const T *a = static_cast<const T *>(q.a[part].at) + r * q.a[part].row;
-      const T *b = static_cast<const T *>(q.b[part].at) + c * q.b[part].row;
-      for (int k = 0; k < q.K; ++k, a += q.a[part].k, b += q.b[part].k)
-        sum = fmaf(to_f32<T>(*a), to_f32<T>(*b), sum);
+  constexpr int kTileSide = 64, kDeep = 16;
+  __shared__ float side[2][kDeep][kTileSide + 1];
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const long long across = (q.cols + kTileSide - 1) / kTileSide;
+  const long long tiles = (q.rows + kTileSide - 1) / kTileSide * across;
+  auto at = [&](int r, int c) { return static_cast<T *>(q.out) + r * q.stride + c; };
+  for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const int r0 = (int)(tile / across) * kTileSide, c0 = (int)(tile % across) * kTileSide;
+    uint32_t wanted = 0;
+    for (int i = 0; i < 16; ++i) {
+      const int r = r0 + ty + 16 * (i >> 2), c = c0 + tx + 16 * (i & 3);
+      if (r < q.rows && c < q.cols && !isfinite(to_f32<T>(*at(r, c)))) wanted |= 1u << i;
     }
-    *out = from_f32<T>(sum);
+    if (!__syncthreads_or(wanted != 0)) continue;
+    float sum[4][4] = {};
+    for (int part = 0; part < q.parts; ++part)
+      for (int k0 = 0; k0 < q.K; k0 += kDeep) {
+        for (int which = 0; which < 2; ++which) {
+          const DenseOperand &o = which ? q.b[part] : q.a[part];
+          const int first = which ? c0 : r0, end = which ? q.cols : q.rows;
+          for (int i = threadIdx.x; i < kDeep * kTileSide; i += 256) {  // along its contiguous dimension
+            const int k = o.k == 1 ? i & (kDeep - 1) : i / kTileSide;
+            const int r = o.k == 1 ? i / kDeep : i & (kTileSide - 1);
+            side[which][k][r] =
+                k0 + k < q.K && first + r < end
+                    ? to_f32<T>(static_cast<const T *>(o.at)[(first + r) * o.row + (k0 + k) * o.k])
+                    : 0.f;
+          }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              sum[i][j] = fmaf(side[0][k][ty + 16 * i], side[1][k][tx + 16 * j], sum[i][j]);
+        __syncthreads();
+      }
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (wanted >> i & 1) *at(r0 + ty + 16 * (i >> 2), c0 + tx + 16 * (i & 3)) = from_f32<T>(sum[i >> 2][i & 3]);
   }
 }
 

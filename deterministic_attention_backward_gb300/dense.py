@@ -168,6 +168,14 @@ def _bwd_args(dy, x, w, kept, act, w_gate, bias, bias_gate, dx, dw, dw_gate):
     return rows, K, N, order, (dys, xs, ws, gs, dxs or K, dws or line, dgs or line)
 
 
+def _terms(terms, rows):
+    if terms not in (None, 1, 2):
+        raise ValueError(f"terms must be 1, 2 or None, got {terms}")
+    if terms == 2 and rows > 1 << 29:
+        raise ValueError(f"two terms of {rows} rows are not taken, 2^29 at most")
+    return terms or 0
+
+
 def _bwd_pack(dy, x, w, kept, act, w_gate, dx, dw, dw_gate, db, dbg, rows, K, N, order, strides):
     gated = w_gate is not None
     z = g = 0
@@ -180,10 +188,11 @@ def _bwd_pack(dy, x, w, kept, act, w_gate, dx, dw, dw_gate, db, dbg, rows, K, N,
 
 
 def dense_bwd_workspace_bytes(dy, x, w, kept=None, *, act: str = "none", w_gate=None, bias=None,
-                              bias_gate=None, dx=None, dw=None, dw_gate=None) -> int:
+                              bias_gate=None, dx=None, dw=None, dw_gate=None, terms=None) -> int:
     """Workspace bytes of ``dense_bwd`` for these tensors (as they lie in memory), all gradients
     asked for."""
     args = _bwd_args(dy, x, w, kept, act, w_gate, bias, bias_gate, dx, dw, dw_gate)
+    terms = _terms(terms, args[0])
     if args[0] == 0:
         return 256
 
@@ -191,18 +200,23 @@ def dense_bwd_workspace_bytes(dy, x, w, kept=None, *, act: str = "none", w_gate=
         return t.data_ptr() if t is not None else 1 << 20 if wanted else 0
     a = _bwd_pack(dy, x, w, kept, act, w_gate, at(dx), at(dw), at(dw_gate, w_gate is not None),
                   0 if bias is None else at(None), 0 if bias_gate is None else at(None), *args)
-    return int(lib().dash_dense_bwd_workspace_bytes(a))
+    return int(lib().dash_dense_bwd_terms_workspace_bytes(a, terms))
 
 
 def dense_bwd(dy, x, w, kept=None, *, act: str = "none", w_gate=None, bias=None, bias_gate=None,
-              need_dx: bool = True, need_dw: bool = True, dx=None, dw=None, dw_gate=None,
+              need_dx: bool = True, need_dw: bool = True, dx=None, dw=None, dw_gate=None, terms=None,
               workspace=None, stream=None, check: bool = False):
     """Gradient of ``dense_fwd``: returns (dx, dw, dbias, dw_gate, dbias_gate), None for what is not
     there (``need_dx``, ``need_dw``: not asked for; of the biases only their presence matters).  dw and
-    dw_gate have their weight's layout in memory.  The residual's gradient is dy itself.  The
-    products are formed of dz rounded to x's type."""
+    dw_gate have their weight's layout in memory.  The residual's gradient is dy itself.
+
+    The products take dz = dy act'(z) (and the gate's) rounded to x's type, which is off by as much as
+    the results' own rounding; ``terms=2`` multiplies what that loses too, which doubles the products.
+    Left to itself the call takes two terms of up to 2^16 elements of dz, so ``terms=1`` or ``2`` is
+    for programs whose results must not depend on that.  Infinities and NaN come out as of one term."""
     args = _bwd_args(dy, x, w, kept, act, w_gate, bias, bias_gate, dx, dw, dw_gate)
     rows, K, N, order, strides = args
+    terms = _terms(terms, rows)
     gated = w_gate is not None
 
     def launch(handle):
@@ -228,9 +242,9 @@ def dense_bwd(dy, x, w, kept=None, *, act: str = "none", w_gate=None, bias=None,
         L = lib()
         a = _bwd_pack(dy, x, w, kept, act, w_gate, *(_ptr(t) or 0 for t in (DX, DW, DG, db, dbg)),
                       *args)
-        ws = scratch(L.dash_dense_bwd_workspace_bytes(a) or 256, x, workspace)
-        _check(L.dash_dense_bwd(a, ws.data_ptr(), ws.numel() * ws.element_size(), handle),
-               "dash_dense_bwd")
+        ws = scratch(L.dash_dense_bwd_terms_workspace_bytes(a, terms) or 256, x, workspace)
+        _check(L.dash_dense_bwd_terms(a, terms, ws.data_ptr(), ws.numel() * ws.element_size(), handle),
+               "dash_dense_bwd_terms")
         if check:
             status(ws, torch.cuda.current_stream())
         return DX, DW, db, DG, dbg

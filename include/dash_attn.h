@@ -490,7 +490,7 @@ dash_status_t dash_dense_fwd(const dash_dense_fwd_t *args, void *workspace, size
  *   dz = dy g act'(z)   dgate = dy act(z)
  *   dx = dz w^T + dgate w_gate^T   dw = x^T dz   dw_gate = x^T dgate   dbias, dbias_gate = sums
  * each where its pointer is not NULL (dw and dw_gate in the weights' order).  dz and dgate are
- * rounded to the rows' type for the tensor core (where they are few, what that loses is multiplied too),
+ * rounded to the rows' type for the tensor core (of up to 2^16 elements what that loses is multiplied too),
  * the biases' gradients are sums of the unrounded ones.  The residual's gradient is dy.  Deterministic;
  * M = 0 clears the weights' gradients. */
 typedef struct {
@@ -502,6 +502,12 @@ typedef struct {
 size_t dash_dense_bwd_workspace_bytes(const dash_dense_bwd_t *args);
 dash_status_t dash_dense_bwd(const dash_dense_bwd_t *args, void *workspace, size_t workspace_bytes,
                              dash_stream_t stream);
+/* The same with dz and dgate in one term (rounded to the rows' type) or in two (what that loses as well:
+ * 16 bits and more of them, twice the products), terms = 1 or 2; 0, as above, takes two of up to 2^16 elements
+ * of dz.  Infinities and NaN come out as of one term. */
+size_t dash_dense_bwd_terms_workspace_bytes(const dash_dense_bwd_t *args, int terms);
+dash_status_t dash_dense_bwd_terms(const dash_dense_bwd_t *args, int terms, void *workspace,
+                                   size_t workspace_bytes, dash_stream_t stream);
 /* For tests of failure detection, process-wide: from the next call on the loads of every CTA of the
  * product kernel end before its block `block` of 64 contraction elements (-1: of none any more), so
  * that the waits for it run out. */

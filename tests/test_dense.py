@@ -584,3 +584,85 @@ def test_infinities_in_the_backwards_operands(L, size, order):
         assert torch.equal(got.isinf(), ref.isinf())
         assert torch.equal(got[ref.isinf()], ref[ref.isinf()])
         assert ref.isinf().any()
+
+
+def test_abi_terms(L):
+    at = 1 << 20  # never dereferenced: every call below is refused first
+
+    def bwd(terms, M=4, act=1, ws=0):
+        a = _BWD.pack(at, 2 * at, 3 * at, 0, 6 * at, 0, 4 * at, 5 * at, 0, 0, 0, *(64,) * 7, M, 64, 64, 0,
+                      act, 0)
+        need = L.dash_dense_bwd_terms_workspace_bytes(a, terms)
+        return L.dash_dense_bwd_terms(a, terms, ws, 0, None), need
+    assert bwd(-1) == (1, 0) and bwd(3) == (1, 0)
+    code, one = bwd(1)
+    assert code == 5 and bwd(2)[1] > one and bwd(0) == bwd(2)
+    assert bwd(0, M=1025) == bwd(1, M=1025) and bwd(2, M=1025)[1] > bwd(1, M=1025)[1]
+    assert bwd(2, act=0) == bwd(1, act=0)
+    assert bwd(2, M=(1 << 29) + 1) == (2, 0) and bwd(1, M=(1 << 29) + 1)[0] == 5
+
+
+@gpu
+@pytest.mark.parametrize("order", ["kn", "nk"])
+@pytest.mark.parametrize("epilogue", EPILOGUES[1:], ids=lambda e: e[0])
+@pytest.mark.parametrize("size", [(48, 72, 24), (300, 1001, 277), (700, 264, 1000)], ids=str)
+def test_terms(L, size, epilogue, order):
+    """One term or two as the caller has it, at sizes on both sides of the default's."""
+    M, K, N = size
+    x, w, a, _ = case(*size, order, BF, epilogue)
+    _, kept = dash.dense_fwd(x, w, **a)
+    dy = make((M, N), BF, 9)
+    default, one, two = (dash.dense_bwd(dy, x, w, kept, terms=t, check=True, **a) for t in (None, 1, 2))
+    same = two if M * N <= 1 << 16 else one
+    assert all(p is q or torch.equal(p, q) for p, q in zip(default, same))
+    # (relu without a gate: dz is dy or 0, which 16 bits hold)
+    exact = epilogue[0] == "relu"
+    assert torch.equal(one[1], two[1]) == exact and torch.equal(one[0], two[0]) == exact
+    # in the norm: two terms leave the results' own rounding (as for few elements above)
+    k = unpacked(kept, M, N).double()
+    act, slope = act_of(k[0], a["act"])
+    parts = [(dy.double() * slope * (k[1] if len(k) > 1 else 1.0), w.double(), 1)]
+    if len(k) > 1:
+        parts.append((dy.double() * act, a["w_gate"].double(), 3))
+    e, X = step(BF), x.double()
+
+    def hold(got, ref, size, n):
+        lost = (sums(n) + e * e + 2.0 ** -17) * size.norm()
+        assert (got.double() - ref).norm() <= e / 3 ** 0.5 * ref.norm() + lost or ref.numel() < 1000
+    hold(two[0], sum(d @ u.t() for d, u, _ in parts), sum(d.abs() @ u.abs().t() for d, u, _ in parts),
+         N * len(parts))
+    for d, _, i in parts:
+        hold(two[i], X.t() @ d, X.abs().t() @ d.abs(), M)
+    need = dash.dense_bwd_workspace_bytes(dy, x, w, kept, terms=2, **a)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    again = dash.dense_bwd(dy, x, w, kept, terms=2, workspace=ws, check=True, **a)
+    assert all(p is q or torch.equal(p, q) for p, q in zip(two, again))
+    for bad in (0, 3, "2"):
+        with pytest.raises(ValueError):
+            dash.dense_bwd(dy, x, w, kept, terms=bad, **a)
+
+
+@gpu
+@pytest.mark.parametrize("order", ["kn", "nk"])
+@pytest.mark.parametrize("size", [(100, 200, 300), (700, 264, 1000), (2500, 72, 4099)], ids=str)
+def test_special_values_of_two_terms(L, size, order):
+    """Infinities and NaN in any operand, with dz that two terms are needed for: one term's where one term
+    has them, two terms' bits elsewhere."""
+    M, K, N = size
+    x, w, a, _ = case(*size, order, BF, EPILOGUES[1])
+    _, kept = dash.dense_fwd(x, w, **a)
+    dy = make((M, N), BF, 9)
+    clean = dash.dense_bwd(dy, x, w, kept, terms=2, **a)
+    w, a["w_gate"] = (t.clone(memory_format=torch.preserve_format) for t in (w, a["w_gate"]))
+    x[M // 2, 3], x[M // 3, K - 1], x[M // 3, K // 2] = math.inf, -math.inf, math.nan
+    w[5, N // 3], a["w_gate"][K - 2, N - 1] = -math.inf, math.inf
+    for step_ in range(2):
+        one, two = (dash.dense_bwd(dy, x, w, kept, terms=t, **a) for t in (1, 2))
+        for i in (0, 1, 3):
+            bad = ~one[i].isfinite()
+            assert bad.any() and one[i].isinf().any() and not bad.all()
+            assert torch.equal(two[i].isnan(), one[i].isnan())
+            inf = one[i].isinf()
+            assert torch.equal(two[i][inf], one[i][inf])
+            assert torch.equal(two[i][~bad], clean[i][~bad]) or step_
+        dy[M // 4, N // 2] = math.inf
