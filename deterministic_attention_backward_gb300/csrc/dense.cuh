@@ -15,8 +15,8 @@ namespace dash {
 constexpr int kDenseM = 256;   // rows of a tile, of a pair of CTAs
 constexpr int kDenseK = 64;    // contraction elements of a stage
 
-// What the backward needs of z and g is kept in three bytes an element, the upper 24 bits of the fp32
-// value: with 16 bits their rounding would make a third and more of the gradients' squared error.  Rows of
+// What the backward needs of z and g is kept in three bytes an element, the fp32 value rounded to its upper
+// 24 bits: with 16 bits their rounding would make a third and more of the gradients' squared error.  Rows of
 // `stride` (N rounded up to 16) 16-bit words, then as many rows of bytes.
 struct DenseKept {
   uint16_t *hi;  // null: not kept

@@ -308,11 +308,15 @@ __device__ __forceinline__ void add_cols(const void *base, long long at, float (
   for (int e = 0; e < C; ++e)
     if (e < left) v[e] += to_f32<T>(src[e]);
 }
-// The upper 24 bits of four values: two words of their upper halves and one of the bytes below.
+// Four values rounded to their upper 24 bits, to even between two (a NaN as it is: the addition would carry
+// it over): two words of their upper halves and one of the bytes below.
 __device__ __forceinline__ void split24(const float (&v)[4], uint32_t &h0, uint32_t &h1, uint32_t &l) {
   uint32_t b[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(v[i]);
+  for (int i = 0; i < 4; ++i) {
+    b[i] = __float_as_uint(v[i]);
+    if (v[i] == v[i]) b[i] += 0x7fu + (b[i] >> 8 & 1u);
+  }
   h0 = __byte_perm(b[0], b[1], 0x7632);
   h1 = __byte_perm(b[2], b[3], 0x7632);
   l = __byte_perm(__byte_perm(b[0], b[1], 0x0051), __byte_perm(b[2], b[3], 0x0051), 0x5410);

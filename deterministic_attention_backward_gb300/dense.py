@@ -111,7 +111,7 @@ def dense_fwd(x, w, bias=None, *, act: str = "none", w_gate=None, bias_gate=None
               keep: bool = True, out=None, workspace=None, stream=None, check: bool = False):
     """y = residual + act(x w + bias), or residual + act(x w + bias) (x w_gate + bias_gate): returns
     (y [..., N], kept).  ``kept`` is what ``dense_bwd`` needs besides, x w + bias and, where there is a
-    gate, x w_gate + bias_gate: 24 bits of each value in a uint8 tensor of the library's layout; None
+    gate, x w_gate + bias_gate: each value rounded to 24 bits in a uint8 tensor of the library's layout; None
     for ``act`` "none" without a gate, or ``keep=False``.  ``out`` may be the residual itself (at its strides).  A
     ``workspace`` serves one call at a time."""
     rows, K, N, order, shape, strides = _fwd_args(x, w, bias, act, w_gate, bias_gate, residual, out,

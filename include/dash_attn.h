@@ -459,7 +459,7 @@ dash_status_t dash_diff_withhold(int kernel, int block);
  * without w_gate y = residual + act(z); bias, bias_gate, residual may be NULL.  x [M, K] and y,
  * residual [M, N] are rows at a stride (in elements); w and w_gate are [K, N] rows (DASH_DENSE_KN)
  * or [N, K] rows (DASH_DENSE_NK); biases [N] contiguous, of the rows' type.  z and gate, where not
- * NULL, receive z and g for the backward, the upper 24 bits of their fp32 values: M rows of 16-bit words
+ * NULL, receive z and g for the backward, their fp32 values rounded to the upper 24 bits: M rows of 16-bit words
  * (the upper ones), then M rows of bytes, Np elements each, Np = N rounded up to 16 (3 M Np bytes in all,
  * on 16 bytes).  y may be the residual itself
  * (at its stride); beside that no output shares memory with another tensor of the call.  Sums run

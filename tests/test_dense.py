@@ -666,3 +666,35 @@ def test_special_values_of_two_terms(L, size, order):
             assert torch.equal(two[i][inf], one[i][inf])
             assert torch.equal(two[i][~bad], clean[i][~bad]) or step_
         dy[M // 4, N // 2] = math.inf
+
+
+@gpu
+@pytest.mark.parametrize("size", [(200, 1, 64), (3, 1, 77), (70, 128, 300)], ids=str)
+def test_what_is_kept_is_rounded(L, size):
+    """z and g in 24 bits are off by half a step at most, 2^-16, and as often up as down.  Of one product
+    and a bias z itself is off by 2^-24 of its parts; of a hundred and more what the sums are off is small
+    in the mean."""
+    M, K, N = size
+    x, w, a, _ = case(*size, "kn", BF, EPILOGUES[3])
+    y, kept = dash.dense_fwd(x, w, **a)
+    k = unpacked(kept, M, N).double()
+    for got, u, b in zip(k, (w, a["w_gate"]), (a["bias"], a["bias_gate"])):
+        p = x.double() @ u.double()
+        z = p + b.double()
+        own = sums(K) * (x.double().abs() @ u.double().abs()) if K > 1 else 0.0
+        own = own + 2.0 ** -24 * (p.abs() + b.double().abs() + z.abs())
+        assert ((got - z).abs() <= 2.0 ** -16 * (z.abs() + own) + own).all()
+        # an error spread evenly over a step of 2^-15 has a mean of 0 and a deviation of 2^-15 / sqrt 12
+        # of the value's power of two: five deviations of the mean
+        up = ((got - z) * z.sign() / 2.0 ** z.abs().log2().floor()).mean()
+        assert up.abs() <= 5 * 2.0 ** -15 / 12 ** 0.5 / z.numel() ** 0.5 + 2.0 ** -22
+
+
+@gpu
+def test_special_values_are_kept(L):
+    x = torch.tensor([[math.nan, math.inf, -math.inf, 3.38e38, -0.0, 1e-38]], dtype=BF, device="cuda").t()
+    one = torch.ones(1, 16, dtype=BF, device="cuda")
+    _, kept = dash.dense_fwd(x.contiguous(), one, act="silu")
+    z = unpacked(kept, 6, 16)[0, :, 0]
+    assert z[0].isnan() and z[1] == math.inf and z[2] == -math.inf and z[4] == 0
+    assert z[3] == x[3, 0].float() and abs(z[5] - x[5, 0].float()) <= 2.0 ** -16 * 1e-38
