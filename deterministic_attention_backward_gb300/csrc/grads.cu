@@ -6,8 +6,8 @@
 // are cut into chunks that the CTAs take in turn, and the scaling takes them in the opposite order, so
 // that it begins with what the norm has left in L2.  A thread adds a chunk's squares in fp32, and what
 // it has of all chunks in fp64; the CTAs' sums are added in a fixed order by whoever needs the norm,
-// every CTA of the scaling for itself.  Which CTA takes a chunk follows from the sizes: the same bits
-// on every run.
+// every CTA of the scaling for itself.  Which CTA takes a chunk, and which of its threads an element,
+// follows from the sizes: the same bits on every run and wherever the tensors lie.
 //
 // Measured: 436 MB in bf16 clipped to other buffers 66 + 134 us, 6.6 TB/s, a copy's rate in both kernels
 // (chunks taken in the same order by both: 2 us more); 3.5 GB in fp32 within the limit 490 us, 7.1 TB/s.
@@ -41,35 +41,61 @@ struct GradTable {
   int count, chunks, chunk;
 };
 
-// f(element, its place in its vector) for this thread's share of n elements: single ones up to a
-// 16-byte boundary and behind the last, vectors between, eight on their way at once.
+// 16 bytes from `off` on of two neighbouring vectors.
+__device__ __forceinline__ uint4 shifted(const uint4 &a, const uint4 &b, uint32_t off) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}, bits = 8 * (off & 3);
+  uint32_t x[5];
+#pragma unroll
+  for (int i = 0; i < 5; ++i)
+    x[i] = off < 8 ? (off < 4 ? w[i] : w[i + 1]) : (off < 12 ? w[i + 2] : w[i + 3]);
+  return make_uint4(__funnelshift_r(x[0], x[1], bits), __funnelshift_r(x[1], x[2], bits),
+                    __funnelshift_r(x[2], x[3], bits), __funnelshift_r(x[3], x[4], bits));
+}
+
+// f(element, its place in its vector) for this thread's share of n elements: vectors of 16 bytes from the
+// first element on, eight on their way at once, and single ones behind the last.  Which thread takes an
+// element, and when, follows from its number alone: where the first does not lie on 16 bytes, a vector is
+// put together from two that do (the first and the last from single elements, so that nothing beside the
+// tensor is read; 2^28 elements in bf16 119 us there, on 16 bytes 108).
 template <typename T, typename F>
 __device__ __forceinline__ void each_element(const T *p, long long n, F &&f) {
   constexpr int V = 16 / sizeof(T), U = 8;
-  const long long skip =
-      min(n, (long long)((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / (long long)sizeof(T));
-  const long long vecs = (n - skip) / V;
-  const uint4 *v = reinterpret_cast<const uint4 *>(p + skip);
-  long long i = threadIdx.x;
-  for (; i + (U - 1) * kThreads < vecs; i += U * kThreads) {
-    uint4 r[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) r[u] = v[i + u * kThreads];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const T *e = reinterpret_cast<const T *>(&r[u]);
-#pragma unroll
-      for (int k = 0; k < V; ++k) f(to_f32<T>(e[k]), k);
-    }
-  }
-  for (; i < vecs; i += kThreads) {
-    const uint4 r = v[i];
+  const long long vecs = n / V;
+  const uint32_t off = reinterpret_cast<uintptr_t>(p) & 15;
+  const uint4 *v = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(p) - off);
+  auto take = [&](const uint4 &r) {
     const T *e = reinterpret_cast<const T *>(&r);
 #pragma unroll
     for (int k = 0; k < V; ++k) f(to_f32<T>(e[k]), k);
+  };
+  long long i = threadIdx.x;
+  if (off == 0) {
+    for (; i + (U - 1) * kThreads < vecs; i += U * kThreads) {
+      uint4 r[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) r[u] = v[i + u * kThreads];
+#pragma unroll
+      for (int u = 0; u < U; ++u) take(r[u]);
+    }
+    for (; i < vecs; i += kThreads) take(v[i]);
+  } else {
+    auto single = [&](long long i) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) f(to_f32<T>(p[i * V + k]), k);
+    };
+    if (i == 0 && vecs > 0) single(0), i += kThreads;
+    constexpr int H = U / 2;  // (two loads a vector)
+    for (; i + (H - 1) * kThreads < vecs - 1; i += H * kThreads) {
+      uint4 r[H], q[H];
+#pragma unroll
+      for (int u = 0; u < H; ++u) r[u] = v[i + u * kThreads], q[u] = v[i + u * kThreads + 1];
+#pragma unroll
+      for (int u = 0; u < H; ++u) take(shifted(r[u], q[u], off));
+    }
+    for (; i < vecs - 1; i += kThreads) take(shifted(v[i], v[i + 1], off));
+    if (i == vecs - 1) single(i);
   }
-  if (threadIdx.x < skip) f(to_f32<T>(p[threadIdx.x]), 0);
-  const long long rest = skip + vecs * V + threadIdx.x;
+  const long long rest = vecs * V + threadIdx.x;
   if (rest < n) f(to_f32<T>(p[rest]), 0);
 }
 

@@ -6,7 +6,7 @@
 
 ``grads`` are tensors of one device, bf16, fp16 and fp32 mixed, of any sizes (None is passed over), each
 dense in memory in some order of its dimensions.  Sums run in an order that the sizes fix: the same
-bits on every run.
+bits on every run, wherever the tensors lie.
 """
 from __future__ import annotations
 

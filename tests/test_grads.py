@@ -220,3 +220,30 @@ def test_streams_graphs_and_refusals(L):
         dash.grad_clip([g, g], 1.0)
     with pytest.raises(dash.DashError):
         dash.grad_clip([g, g[:10]], 1.0, out=[torch.empty_like(g), g[10:20]])
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+def test_bits_do_not_depend_on_the_place_in_memory(L, dtype):
+    """A gradient in a flat buffer gives the same norm wherever it begins: its elements are added in the
+    order of their numbers.  One element so large that what is added to it by itself is lost, the others so
+    that it matters which of them are."""
+    bits = {BF: 8, HF: 11, F32: 24}[dtype]
+    for n in (1, 7, 8, 9, 100, 2047, 2048, 2049, 8192, 20001, 300000):
+        for at in {0, 1, n // 2, n - 1}:
+            # squares of 2^-25 and less beside 1: every one is lost alone
+            src = make((n,), F32, n).abs().clamp(0.25, 1) * 2.0 ** -12.5
+            src[min(at, n - 1)] = 1.0 + 2.0 ** (1 - bits)
+            src = src.to(dtype)
+            got = set()
+            for offset in range(9):
+                flat = torch.full((n + 16,), 7.0, dtype=dtype, device="cuda")
+                flat[offset:offset + n] = src
+                norm = dash.grad_norm([flat[offset:offset + n]])
+                got.add(float(norm))
+                out = torch.empty_like(flat)[offset:offset + n]
+                again = dash.grad_clip([flat[offset:offset + n]], 0.5, out=[out])
+                assert torch.equal(again, norm)
+            assert len(got) == 1, (n, at, got)
+            ref = norm_of([src])
+            assert abs(got.pop() - ref) <= (NORM + 2.0 ** -24) * ref
