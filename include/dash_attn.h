@@ -517,8 +517,8 @@ dash_status_t dash_dense_withhold(int block);
  *   norm = sqrt(sum over all tensors of g^2)      out = g * min(1, max_norm / (norm + eps))
  * n elements each (0 too), dense in memory, of any type; `grads` is a host array that is read before
  * the call returns.  Squares are added in fp32 within runs of a few hundred elements and in fp64
- * beyond, in an order that the sizes fix, wherever the tensors lie; magnitudes whose squares fp32 does not hold are scaled.  out
- * may be in itself; beside that nothing written shares memory with another tensor (a tensor that
+ * beyond, in an order that the sizes fix, wherever the tensors lie; magnitudes whose squares fp32 does not
+ * hold are scaled.  out may be in itself; beside that nothing written shares memory with another tensor (a tensor that
  * occurs twice is refused by dash_grad_clip).  A factor of 1 leaves tensors in place untouched; a norm
  * that is NaN gives NaN.  dash_grad_clip forms the norm and writes it to `norm`, or takes `given` (then
  * `norm` may be NULL, and no workspace is needed).  A workspace serves one call at a time. */

@@ -247,3 +247,34 @@ def test_bits_do_not_depend_on_the_place_in_memory(L, dtype):
             assert len(got) == 1, (n, at, got)
             ref = norm_of([src])
             assert abs(got.pop() - ref) <= (NORM + 2.0 ** -24) * ref
+
+
+@gpu
+def test_zeros_are_read_once(L):
+    """The norm of zeros (as gradients of a table's rows are that a step has not met) takes no longer than
+    that of other values; the tensor is larger than L2."""
+    z = torch.zeros(1 << 28, device="cuda")
+    r = make((1 << 28,), F32, 0)
+    time = {}
+    for name, g in (("zeros", [z]), ("values", [r])):
+        out, ws = torch.empty((), device="cuda"), torch.empty(
+            dash.grad_norm_workspace_bytes(1), dtype=torch.uint8, device="cuda")
+        runs = []
+        for _ in range(12):
+            start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            start.record()
+            for _ in range(4):
+                dash.grad_norm(g, out=out, workspace=ws)
+            end.record()
+            end.synchronize()
+            runs.append(start.elapsed_time(end))
+        time[name] = sorted(runs)[len(runs) // 2]
+    assert time["zeros"] < 1.3 * time["values"], time
+    assert float(dash.grad_norm([z])) == 0.0
+    # signed zeros, and a single value of the smallest among them
+    z.neg_()
+    assert float(dash.grad_norm([z])) == 0.0
+    for at in (0, 12345678, z.numel() - 1):
+        z[at] = 2.0 ** -149
+        assert float(dash.grad_norm([z])) == 2.0 ** -149
+        z[at] = 0.0
