@@ -13,8 +13,9 @@
 // or of v only (v is copied), so that a thread has one set of sums of dw; the CTAs' sums are added in
 // order by a second kernel, their number follows from the sizes.
 //
-// Measured on 2 x 8192 tokens of 32 + 8 + 8 heads of 128 in bf16: forward 68 us, 5.9 TB/s, 88 % of a
-// plain copy's rate, backward 98 us, 5.8 TB/s; one token 3.9 and 6.2 us, launches.
+// Measured on 2 x 8192 tokens of 32 + 8 + 8 heads of 128 in bf16: forward 69 us, 5.8 TB/s, 87 % of a
+// plain copy's rate, backward 100 us, 5.7 TB/s; one token 3.9 and 6.2 us, launches.  Off 16 bytes 333 and
+// 581 us: sizes, not places, decide which lane has an element, and with it the sums' order.
 #include "angle.cuh"
 #include "common.cuh"
 #include "dash_attn.h"
@@ -148,15 +149,17 @@ __device__ __forceinline__ void turn_by(const Turn<V> &t, Values<V> (&x)[Turn<V>
 }
 
 // Heads on their way to a group, in a ring of its own in shared memory (single elements are loaded
-// when they are needed).  More of them in flight is not faster: of 2 x 8192 tokens the forward takes
-// 70 us with 2 and 80 us with 3, the backward 107 us with 2, 3 and 4.
+// when they are needed).  Of 2 x 8192 tokens the forward takes 69 us with 2 and 79 us with 3, the backward
+// 102 us with 2, 100 with 3 and 106 with 4.
 template <int V, int R, bool kBack>
 constexpr int kRingStages = V == 1 ? 0 : kBack ? 3 : 2;
 template <int V, int R, bool kBack>
 constexpr int kRingBytes = kRingStages<V, R, kBack> * (kBack ? 4 : 2) * R * kThreads * 16;
 
-// R pairs of vectors a lane.
-template <typename T, int V, int R, bool kHalf, bool kBack>
+// R pairs of vectors a lane.  Where tensors do not lie on 16 bytes (kLoose), a group's lanes bring their head
+// into the ring, and take it out of it, element by element side by side in memory: every lane has the same
+// elements as on 16 bytes, and every sum its order.
+template <typename T, int V, int R, bool kHalf, bool kBack, bool kLoose>
 __global__ void __launch_bounds__(kThreads, kBack ? kBackPerSm : kForwardPerSm)
     heads_kernel(const __grid_constant__ HeadParams p) {
   constexpr int N = kRingStages<V, R, kBack>, kVecs = (kBack ? 4 : 2) * R;
@@ -220,6 +223,36 @@ __global__ void __launch_bounds__(kThreads, kBack ? kBackPerSm : kForwardPerSm)
   first.t = (cta - q.cta0) * (kThreads / 32) + (threadIdx.x >> 5);
   first.k = first.t % q.blocks, first.t /= q.blocks;
   place(first);
+  // where an element of the group's head lies in a slot of the ring
+  auto place_of = [&](int slot, int which, int e) {
+    const int vec = e / V;
+    int u = vec >> 1, side = vec & 1;
+    if (kHalf && vec < 2 * q.turn) side = vec >= q.turn, u = vec - side * q.turn;
+    const int r = R == 1 ? 0 : u / 32;  // (more than one pair: a group is a warp)
+    return reinterpret_cast<T *>(shared + (slot * kVecs + which * 2 * R + 2 * r + side) * kThreads +
+                                 (threadIdx.x & ~(G - 1)) + (u & (G - 1))) +
+           e % V;
+  };
+  // f(element, its value) for this lane's share of a head, eight on their way at once
+  auto each_loose = [&](const T *src, bool on, auto &&f) {
+    constexpr int kAtOnce = 8;
+    for (int first = in_group; first < q.D; first += kAtOnce * G) {
+      T v[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int e = first + i * G;
+        v[i] = on && e < q.D ? src[e] : from_f32<T>(0.f);
+      }
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int e = first + i * G;
+        if (e < q.D) f(e, v[i]);
+      }
+    }
+  };
+  auto bring_loose = [&](int slot, int which, const T *src, bool on) {
+    each_loose(src, on, [&](int e, T v) { *place_of(slot, which, e) = v; });
+  };
   // the head that is brought in next
   Place ahead = first;
   int filled = 0;  // the slot it goes to
@@ -227,7 +260,14 @@ __global__ void __launch_bounds__(kThreads, kBack ? kBackPerSm : kForwardPerSm)
     if constexpr (N > 0) {
       const uint32_t at =
           (uint32_t)__cvta_generic_to_shared(ring + filled * kVecs * kThreads);
+      if constexpr (kLoose)
+        if (q.normed) {
+          __syncwarp();  // what was there has been taken out
+          bring_loose(filled, 0, ahead.x, ahead.on);
+          if constexpr (kBack) bring_loose(filled, 1, ahead.dy, ahead.on);
+        }
       filled = filled + 1 == N ? 0 : filled + 1;
+      if constexpr (!kLoose)
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         copy16(at + (2 * r) * kThreads * 16, ahead.x + e0[r], ahead.on && has0[r]);
@@ -238,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, kBack ? kBackPerSm : kForwardPerSm)
             copy16(at + (2 * R + 2 * r + 1) * kThreads * 16, ahead.dy + e1[r], ahead.on && has1[r]);
           }
       }
-      copies_end();
+      if constexpr (!kLoose) copies_end();
       ahead.x += xstep;
       if constexpr (kBack) ahead.dy += gstep;
       if (--ahead.left == 0) next_block(ahead);
@@ -320,10 +360,21 @@ __global__ void __launch_bounds__(kThreads, kBack ? kBackPerSm : kForwardPerSm)
     }
     for (int left = at.left; left > 0; --left, row += ostep, at.x += xstep, at.dy += gstep) {
       E x0[R][C], x1[R][C], g0[kBack ? R : 1][C], g1[kBack ? R : 1][C];
+      uint4 *v = nullptr;
+      int now = 0;  // this head's slot
       if constexpr (N > 0) {
         bring();
-        copies_wait<N - 1>();
-        const uint4 *v = ring + slot * kVecs * kThreads;
+        if constexpr (kLoose) {
+          if (!q.normed) {
+            if (at.on) each_loose(at.x, true, [&](int e, T v) { row[e] = v; });
+            continue;
+          }
+          __syncwarp();
+        } else {
+          copies_wait<N - 1>();
+        }
+        v = ring + slot * kVecs * kThreads;
+        now = slot;
         slot = slot + 1 == N ? 0 : slot + 1;
         if (!q.normed) {  // (a part's: the same for the whole CTA)
 #pragma unroll
@@ -335,11 +386,14 @@ __global__ void __launch_bounds__(kThreads, kBack ? kBackPerSm : kForwardPerSm)
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          unpack2<T>(v[2 * r * kThreads], x0[r]);
-          unpack2<T>(v[(2 * r + 1) * kThreads], x1[r]);
+          // (copies leave zeros where a lane has no vector, elements nothing)
+          const uint4 none = make_uint4(0, 0, 0, 0);
+          const bool in0 = !kLoose || has0[r], in1 = !kLoose || has1[r];
+          unpack2<T>(in0 ? v[2 * r * kThreads] : none, x0[r]);
+          unpack2<T>(in1 ? v[(2 * r + 1) * kThreads] : none, x1[r]);
           if constexpr (kBack) {
-            unpack2<T>(v[(2 * R + 2 * r) * kThreads], g0[r]);
-            unpack2<T>(v[(2 * R + 2 * r + 1) * kThreads], g1[r]);
+            unpack2<T>(in0 ? v[(2 * R + 2 * r) * kThreads] : none, g0[r]);
+            unpack2<T>(in1 ? v[(2 * R + 2 * r + 1) * kThreads] : none, g1[r]);
           }
         }
       } else {
@@ -389,12 +443,12 @@ __global__ void __launch_bounds__(kThreads, kBack ? kBackPerSm : kForwardPerSm)
       const E rs = both<E>(rstd);
       // -mean(w dz x^) rstd, x^ = x rstd
       const E mean = both<E>(-rstd * rstd * (sum_g * inv_d));
-      auto store = [&](T *to, const E (&f)[C], bool on) {
+      auto store = [&](int vec, int e, const E (&f)[C], bool on) {
         if (!on) return;
         if constexpr (V == 1)
-          *to = from_f32<T>(f[0]);
-        else
-          *reinterpret_cast<uint4 *>(to) = pack2<T>(f);
+          row[e] = from_f32<T>(f[0]);
+        else  // (into the slot that has been read)
+          *(kLoose ? v + vec * kThreads : reinterpret_cast<uint4 *>(row + e)) = pack2<T>(f);
       };
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -409,8 +463,8 @@ __global__ void __launch_bounds__(kThreads, kBack ? kBackPerSm : kForwardPerSm)
             ga[i] = mul2(rs, fma2(a[i], mean, mul2(ga[i], w0[i])));
             gb[i] = mul2(rs, fma2(b[i], mean, mul2(gb[i], w1[i])));
           }
-          store(row + e0[r], ga, at.on && has0[r]);
-          store(row + e1[r], gb, at.on && has1[r]);
+          store(2 * r, e0[r], ga, at.on && has0[r]);
+          store(2 * r + 1, e1[r], gb, at.on && has1[r]);
         } else {
 #pragma unroll
           for (int i = 0; i < C; ++i) {
@@ -418,14 +472,18 @@ __global__ void __launch_bounds__(kThreads, kBack ? kBackPerSm : kForwardPerSm)
             b[i] = mul2(mul2(b[i], rs), w1[i]);
           }
           if (in_group + r * G < q.turn) turn_by<V, kAcross>(turn[r], a, b);
-          store(row + e0[r], a, at.on && has0[r]);
-          store(row + e1[r], b, at.on && has1[r]);
+          store(2 * r, e0[r], a, at.on && has0[r]);
+          store(2 * r + 1, e1[r], b, at.on && has1[r]);
         }
+      }
+      if constexpr (kLoose) {
+        __syncwarp();
+        for (int e = in_group; at.on && e < q.D; e += G) row[e] = *place_of(now, 0, e);
       }
     }
   }
   if constexpr (kBack) {
-    if constexpr (N > 0) copies_wait<0>();
+    if constexpr (N > 0 && !kLoose) copies_wait<0>();
     if (!q.dw) return;
     // the groups' sums [group][D], added in order
     float *sums = reinterpret_cast<float *>(shared);
@@ -503,7 +561,7 @@ void deal(HeadParams &p, int V, bool back) {
       q.across *= 2;
     const int steps = q.heads / q.across, at_once = per_warp / q.across;
     const long long groups = (p.tokens + at_once - 1) / at_once;
-    // as many of them at a time as leave every warp something, 8 at most
+    // as many of them at a time as leave every warp something, 16 at most
     long long each = groups * steps / (share * warps);
     each = each < 1 ? 1 : each > 16 ? 16 : each;
     if (each > steps) each = steps;
@@ -519,7 +577,7 @@ void deal(HeadParams &p, int V, bool back) {
 }
 int ctas_of(const HeadParams &p) { return p.part[p.nparts - 1].cta0 + p.part[p.nparts - 1].ctas; }
 
-template <typename T, int V, int R, bool kHalf, bool kBack>
+template <typename T, int V, int R, bool kHalf, bool kBack, bool kLoose>
 cudaError_t launch(const HeadParams &p, cudaStream_t s) {
   constexpr int kRing = kRingBytes<V, R, kBack>;
   int units = 0;
@@ -532,31 +590,36 @@ cudaError_t launch(const HeadParams &p, cudaStream_t s) {
     }
   // (kMaxD / 2 pairs at most)
   const cudaError_t e =
-      allow_smem<heads_kernel<T, V, R, kHalf, kBack>>(kRing + kMaxD / 2 * 16 + 16384 + 8 * kMaxD);
+      allow_smem<heads_kernel<T, V, R, kHalf, kBack, kLoose>>(kRing + kMaxD / 2 * 16 + 16384 + 8 * kMaxD);
   if (e != cudaSuccess) return e;
-  heads_kernel<T, V, R, kHalf, kBack><<<ctas_of(p), kThreads, smem, s>>>(p);
+  heads_kernel<T, V, R, kHalf, kBack, kLoose><<<ctas_of(p), kThreads, smem, s>>>(p);
   return cudaGetLastError();
 }
-template <typename T, int V, int R>
+template <typename T, int V, int R, bool kLoose = false>
 cudaError_t launch_v(const HeadParams &p, bool half, bool back, cudaStream_t s) {
   if (half)
-    return back ? launch<T, V, R, true, true>(p, s) : launch<T, V, R, true, false>(p, s);
-  return back ? launch<T, V, R, false, true>(p, s) : launch<T, V, R, false, false>(p, s);
+    return back ? launch<T, V, R, true, true, kLoose>(p, s)
+                : launch<T, V, R, true, false, kLoose>(p, s);
+  return back ? launch<T, V, R, false, true, kLoose>(p, s)
+              : launch<T, V, R, false, false, kLoose>(p, s);
 }
+// wide: the sizes are of whole vectors of 16 bytes; loose: they do not lie on 16 bytes
 template <typename T>
-cudaError_t launch_t(const HeadParams &p, bool wide, bool half, bool back, cudaStream_t s) {
+cudaError_t launch_t(const HeadParams &p, bool wide, bool loose, bool half, bool back,
+                     cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
   int units = 0;
   for (int i = 0; i < p.nparts; ++i) units = p.part[i].units > units ? p.part[i].units : units;
-  // heads that 16-byte vectors do not fit, element by element: 2 x 8192 tokens of heads of 128 one
-  // element off that grid take 358 us forward and 670 backward, on it 68 and 98
+  // sizes that 16-byte vectors do not fit, element by element: 2 x 8192 tokens of 32 + 8 + 8 heads of 126
+  // take 376 us forward and 691 backward, of 128 69 and 100
   if (!wide)
     return units <= 32   ? launch_v<T, 1, 1>(p, half, back, s)
            : units <= 64 ? launch_v<T, 1, 2>(p, half, back, s)
                          : launch_v<T, 1, 8>(p, half, back, s);
   if constexpr (V == 4)
-    if (units > 32) return launch_v<T, V, 2>(p, half, back, s);
-  return launch_v<T, V, 1>(p, half, back, s);
+    if (units > 32)
+      return loose ? launch_v<T, V, 2, true>(p, half, back, s) : launch_v<T, V, 2>(p, half, back, s);
+  return loose ? launch_v<T, V, 1, true>(p, half, back, s) : launch_v<T, V, 1>(p, half, back, s);
 }
 
 struct Lay {
@@ -564,7 +627,7 @@ struct Lay {
 };
 
 // Checks and fills everything but the addresses of partial sums.
-dash_status_t fill(HeadParams &p, bool &wide, Lay &lay, const dash_rope_part_t *parts,
+dash_status_t fill(HeadParams &p, bool &wide, bool &loose, Lay &lay, const dash_rope_part_t *parts,
                    const dash_rope_part_t *x, int nparts, const void *const weights[2], int B, int S,
                    int rot, dash_rope_layout_t layout, dash_dtype_t dtype, dash_dtype_t wdtype,
                    const double *inv_freq, const void *positions, int positions64,
@@ -580,6 +643,7 @@ dash_status_t fill(HeadParams &p, bool &wide, Lay &lay, const dash_rope_part_t *
   const int size = dtype == DASH_FP32 ? 4 : 2, vec = 16 / size;
   const int wsize = wdtype == DASH_FP32 ? 4 : 2;
   wide = rot % (2 * vec) == 0;
+  loose = false;
   auto lies = [&](const void *at, const long long *stride, int heads, int D) {
     const long long count[3] = {B, S, heads};
     Bytes b = bytes_of(at, size, D);
@@ -588,7 +652,7 @@ dash_status_t fill(HeadParams &p, bool &wide, Lay &lay, const dash_rope_part_t *
   };
   auto lean = [&](const void *at, const long long *stride) {
     if (reinterpret_cast<uintptr_t>(at) & (size - 1)) return false;
-    wide = wide && aligned16(at) && (stride[0] | stride[1] | stride[2]) % vec == 0;
+    loose = loose || !aligned16(at) || (stride[0] | stride[1] | stride[2]) % vec != 0;
     return true;
   };
   int turned = 0, wsizes[2] = {};  // elements of the weights
@@ -657,11 +721,11 @@ dash_status_t fill(HeadParams &p, bool &wide, Lay &lay, const dash_rope_part_t *
   return DASH_OK;
 }
 
-cudaError_t launch_heads(const HeadParams &p, dash_dtype_t dtype, bool wide, bool half, bool back,
-                         cudaStream_t s) {
-  if (dtype == DASH_BF16) return launch_t<__nv_bfloat16>(p, wide, half, back, s);
-  if (dtype == DASH_FP16) return launch_t<__half>(p, wide, half, back, s);
-  return launch_t<float>(p, wide, half, back, s);
+cudaError_t launch_heads(const HeadParams &p, dash_dtype_t dtype, bool wide, bool loose, bool half,
+                         bool back, cudaStream_t s) {
+  if (dtype == DASH_BF16) return launch_t<__nv_bfloat16>(p, wide, loose, half, back, s);
+  if (dtype == DASH_FP16) return launch_t<__half>(p, wide, loose, half, back, s);
+  return launch_t<float>(p, wide, loose, half, back, s);
 }
 
 }  // namespace
@@ -677,16 +741,16 @@ dash_status_t dash_rope_norm_fwd(const dash_rope_part_t *parts, int nparts,
                                  long long pos_stride_t, long long start, dash_stream_t stream) {
   using namespace dash;
   HeadParams p{};
-  bool wide;
+  bool wide, loose;
   Lay lay;
-  dash_status_t st = fill(p, wide, lay, parts, nullptr, nparts, weights, B, S, rot, layout, dtype,
+  dash_status_t st = fill(p, wide, loose, lay, parts, nullptr, nparts, weights, B, S, rot, layout, dtype,
                           wdtype, inv_freq, positions, positions64, pos_stride_b, pos_stride_t,
                           false);
   if (st != DASH_OK) return st;
   DevInfo dev;
   if ((st = device_info(&dev)) != DASH_OK) return st;
   p.magnitude = magnitude, p.eps = eps, p.start = start;
-  return launch_heads(p, dtype, wide, layout == DASH_ROPE_HALF, false,
+  return launch_heads(p, dtype, wide, loose, layout == DASH_ROPE_HALF, false,
                       reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? DASH_OK
              : DASH_ERR_CUDA;
@@ -705,9 +769,9 @@ dash_status_t dash_rope_norm_bwd(const dash_rope_part_t *parts, const dash_rope_
                                  void *workspace, size_t workspace_bytes, dash_stream_t stream) {
   using namespace dash;
   HeadParams p{};
-  bool wide;
+  bool wide, loose;
   Lay lay;
-  dash_status_t st = fill(p, wide, lay, parts, x, nparts, weights, B, S, rot, layout, dtype, wdtype,
+  dash_status_t st = fill(p, wide, loose, lay, parts, x, nparts, weights, B, S, rot, layout, dtype, wdtype,
                           inv_freq, positions, positions64, pos_stride_b, pos_stride_t, true);
   if (st != DASH_OK) return st;
   if (!dweights) return DASH_ERR_INVALID;
@@ -753,7 +817,7 @@ dash_status_t dash_rope_norm_bwd(const dash_rope_part_t *parts, const dash_rope_
   if ((st = device_info(&dev)) != DASH_OK) return st;
   p.magnitude = magnitude, p.eps = eps, p.start = start;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (launch_heads(p, dtype, wide, layout == DASH_ROPE_HALF, true, s) != cudaSuccess)
+  if (launch_heads(p, dtype, wide, loose, layout == DASH_ROPE_HALF, true, s) != cudaSuccess)
     return DASH_ERR_CUDA;
   if (any) {
     const dim3 grid((sums.D + 31) / 32, 2);

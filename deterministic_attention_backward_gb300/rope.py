@@ -278,7 +278,8 @@ def rope_norm_bwd(dq, dk, dv, q, k=None, *, q_weight=None, k_weight=None, inv_fr
     """Gradient of ``rope_norm_fwd`` from the gradients of its outputs and its inputs q and k:
     returns (dq, dk, dv, dq_weight, dk_weight), None for what is not there.  ``out``: the tensors to
     write the first three to (views of the qkv product's gradient, or the gradients that are given,
-    as they lie).  The weights' gradients are summed in an order that the sizes fix."""
+    as they lie).  The weights' gradients are summed in an order that the sizes fix, wherever the
+    tensors lie."""
     parts, xs = (dq, dk, dv), (q, k)
     tokens, B, S, rot = _frequencies(dq, inv_freq, layout)
     out = _parts(parts, out, dq, tokens, rot)

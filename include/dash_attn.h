@@ -353,7 +353,7 @@ size_t dash_rope_norm_bwd_workspace_bytes(int D);
 /* Gradient of dash_rope_norm_fwd: parts hold the gradients of its outputs (in) and of its inputs
  * (out); x[i], for the i-th part that turns, the forward's input (in and in_stride; heads and D as in
  * the part).  dweights[i] receives the weight's gradient in its type (NULL: not wanted; both have
- * heads of one size), summed in an order that the sizes fix.  A gradient may be written over the one
+ * heads of one size), summed in an order that the sizes fix, wherever tensors lie.  A gradient may be written over the one
  * it comes from, as that lies. */
 dash_status_t dash_rope_norm_bwd(const dash_rope_part_t *parts, const dash_rope_part_t *x, int nparts,
                                  const void *const weights[2], void *const dweights[2], int B, int S,

@@ -348,3 +348,41 @@ def test_refusals(L):
     y = torch.empty_like(q)
     with pytest.raises(dash.DashError):  # over the forward's input
         dash.rope_norm_bwd(y, None, None, q, out=(q, None, None), inv_freq=f)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+@pytest.mark.parametrize("case", [(2, 37, 4, 2, 64, 64, "half"), (1, 513, 4, 1, 128, 128, "interleaved"),
+                                  (1, 300, 8, 8, 128, 32, "half"), (1, 3, 3, 1, 512, 512, "half"),
+                                  (3, 70, 5, 1, 96, 48, "interleaved"), (1, 900, 2, 2, 256, 64, "half"),
+                                  (2, 40, 3, 1, 24, 16, "half"), (1, 50, 3, 1, 50, 24, "half")], ids=str)
+def test_bits_do_not_depend_on_the_place_in_memory(L, case, dtype):
+    """The same heads at other places and strides give the same bits, their weights' gradients too; what
+    lies beside them stays."""
+    B, S, H, Hkv, D, rot, layout = case
+    f, _ = dash.rope_freqs(rot)
+    widths = [H * D, Hkv * D, Hkv * D]
+    wq, wk = (make((D,), dtype, i, 0.2, 1.0) for i in (5, 6))
+    a = dict(q_weight=wq, k_weight=wk, inv_freq=f, start=11, layout=layout)
+
+    def parts(t, at):
+        return tuple(p.unflatten(-1, (-1, D)) for p in
+                     t[..., at:at + sum(widths)].split(widths, dim=-1))
+    x, g = (make((B, S, sum(widths)), dtype, i) for i in (3, 4))
+    want = dash.rope_norm_fwd(*parts(x, 0), **a)
+    gwant = dash.rope_norm_bwd(*parts(g, 0), *parts(x, 0)[:2], **a)
+    for at, room in ((1, 8), (2, 9), (4, 16), (8, 16), (0, 1)):
+        def wide(t):
+            big = torch.full((B, S, sum(widths) + room), 7.0, dtype=dtype, device="cuda")
+            big[..., at:at + sum(widths)] = t
+            return big
+        for fn, args, ref in ((dash.rope_norm_fwd, parts(wide(x), at), want),
+                              (dash.rope_norm_bwd, (*parts(wide(g), at), *parts(wide(x), at)[:2]), gwant)):
+            out = wide(torch.zeros_like(x))
+            assert all(map(torch.equal, fn(*args, **a), ref)), (fn.__name__, at, room)
+            res = fn(*args, out=parts(out, at), **a)
+            assert all(map(torch.equal, res, ref)), (fn.__name__, at, room)
+            assert (out[..., :at] == 7).all() and (out[..., at + sum(widths):] == 7).all()
+            # over the tensors themselves
+            res = fn(*args, out=args[:3], **a)
+            assert all(map(torch.equal, res, ref)), (fn.__name__, at, room)
