@@ -268,7 +268,8 @@ def rope_norm_fwd(q, k=None, v=None, *, q_weight=None, k_weight=None, inv_freq, 
 
 
 def rope_norm_bwd_workspace_bytes(D: int) -> int:
-    """Workspace bytes of ``rope_norm_bwd`` for heads of D elements."""
+    """Workspace bytes of ``rope_norm_bwd`` for heads of D elements (of q or k, whichever has a
+    weight; none is needed where neither has)."""
     return int(lib().dash_rope_norm_bwd_workspace_bytes(D))
 
 
@@ -312,8 +313,8 @@ def rope_norm_bwd(dq, dk, dv, q, k=None, *, q_weight=None, k_weight=None, inv_fr
                 dws[i].zero_()
         if weights:
             L = lib()
-            ws = scratch(L.dash_rope_norm_bwd_workspace_bytes(q.shape[-1]) or 256, q, workspace) \
-                if any(g is not None for g in grads) else None
+            D = max((g.numel() for g in grads if g is not None), default=0)
+            ws = scratch(L.dash_rope_norm_bwd_workspace_bytes(D), q, workspace) if D else None
             none = [None] * (2 - len(weights))
             _check(L.dash_rope_norm_bwd(b"".join(packed), b"".join(packed_x), len(packed),
                                         _two(*weights, *none), _two(*grads, *none), B, S, rot,

@@ -348,7 +348,8 @@ dash_status_t dash_rope_norm_fwd(const dash_rope_part_t *parts, int nparts,
                                  const double *inv_freq, float magnitude, float eps,
                                  const void *positions, int positions64, long long pos_stride_b,
                                  long long pos_stride_t, long long start, dash_stream_t stream);
-/* Bytes of device workspace of dash_rope_norm_bwd for heads of D elements (0: unsupported). */
+/* Bytes of device workspace of dash_rope_norm_bwd for heads of D elements, of the parts whose dweights are
+ * wanted (0: unsupported). */
 size_t dash_rope_norm_bwd_workspace_bytes(int D);
 /* Gradient of dash_rope_norm_fwd: parts hold the gradients of its outputs (in) and of its inputs
  * (out); x[i], for the i-th part that turns, the forward's input (in and in_stride; heads and D as in

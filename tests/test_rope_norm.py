@@ -386,3 +386,26 @@ def test_bits_do_not_depend_on_the_place_in_memory(L, case, dtype):
             # over the tensors themselves
             res = fn(*args, out=args[:3], **a)
             assert all(map(torch.equal, res, ref)), (fn.__name__, at, room)
+
+
+@gpu
+@pytest.mark.parametrize("which", ["q", "k"])
+def test_workspace_is_of_the_heads_that_have_a_weight(L, which):
+    """Heads of q and k of different sizes, a weight for one of them: its size decides."""
+    f, _ = dash.rope_freqs(32)
+    small, large = make((1, 64, 1, 32), BF, 0), make((1, 64, 8, 512), BF, 1)
+    q, k = (large, small) if which == "q" else (small, large)
+    dq, dk = make(q.shape, BF, 2), make(k.shape, BF, 3)
+    w = make((512,), BF, 4, 0.2, 1.0)
+    a = dict(inv_freq=f, **{which + "_weight": w})
+    pos = torch.arange(64, device="cuda")[None]
+    g = dash.rope_norm_bwd(dq, dk, None, q, k, **a)
+    one = torch.ones(32, device="cuda")
+    check_backward(g[0], g[3], dq, q, w if which == "q" else one, f, 1.0, pos, "half")
+    check_backward(g[1], g[4], dk, k, w if which == "k" else one, f, 1.0, pos, "half")
+    need = dash.rope_norm_bwd_workspace_bytes(512)
+    ws = torch.full((need + 64,), 255, dtype=torch.uint8, device="cuda")
+    again = dash.rope_norm_bwd(dq, dk, None, q, k, workspace=ws[:need], **a)
+    assert all(p is r or torch.equal(p, r) for p, r in zip(g, again)) and (ws[need:] == 255).all()
+    with pytest.raises(ValueError, match="workspace"):
+        dash.rope_norm_bwd(dq, dk, None, q, k, workspace=ws[:need - 1], **a)
