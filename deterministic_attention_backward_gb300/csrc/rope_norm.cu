@@ -624,6 +624,7 @@ cudaError_t launch_t(const HeadParams &p, bool wide, bool loose, bool half, bool
 
 struct Lay {
   Bytes x[3], dy[3], out[3];
+  Bytes rest[4];  // frequencies, positions, weights
 };
 
 // Checks and fills everything but the addresses of partial sums.
@@ -693,10 +694,10 @@ dash_status_t fill(HeadParams &p, bool &wide, bool &loose, Lay &lay, const dash_
     if ((long long)parts[i].heads * parts[i].D >= (1LL << 28)) return DASH_ERR_UNSUPPORTED;
   // an output is its own input (the gradient), as it lies, or what nothing else is
   const int psize = positions64 ? 8 : 4;
-  const Bytes rest[4] = {
-      bytes_of(inv_freq, 8, rot / 2),
-      along(along(bytes_of(positions, psize, 1), psize, pos_stride_t, S), psize, pos_stride_b, B),
-      bytes_of(weights[0], wsize, wsizes[0]), bytes_of(weights[1], wsize, wsizes[1])};
+  lay.rest[0] = bytes_of(inv_freq, 8, rot / 2);
+  lay.rest[1] =
+      along(along(bytes_of(positions, psize, 1), psize, pos_stride_t, S), psize, pos_stride_b, B);
+  for (int i = 0; i < 2; ++i) lay.rest[2 + i] = bytes_of(weights[i], wsize, wsizes[i]);
   for (int i = 0; i < nparts; ++i) {
     const dash_rope_part_t &q = parts[i];
     bool in_place = q.in == q.out;
@@ -707,7 +708,7 @@ dash_status_t fill(HeadParams &p, bool &wide, bool &loose, Lay &lay, const dash_
       if (share(lay.out[i], lay.x[k]) && !(own && !(back && q.turn))) return DASH_ERR_INVALID;
       if (share(lay.out[i], lay.dy[k]) && !own) return DASH_ERR_INVALID;
     }
-    for (const Bytes &r : rest)
+    for (const Bytes &r : lay.rest)
       if (share(lay.out[i], r)) return DASH_ERR_INVALID;
   }
   p.inv_freq = inv_freq;
@@ -809,9 +810,8 @@ dash_status_t dash_rope_norm_bwd(const dash_rope_part_t *parts, const dash_rope_
         return DASH_ERR_INVALID;
     for (int k = 0; k < i; ++k)
       if (share(dw[i], dw[k])) return DASH_ERR_INVALID;
-    for (int k = 0; k < 2; ++k)
-      if (share(dw[i], bytes_of(weights[k], wsize, weights[k] ? sums.D : 0)))
-        return DASH_ERR_INVALID;
+    for (const Bytes &r : lay.rest)
+      if (share(dw[i], r)) return DASH_ERR_INVALID;
   }
   DevInfo dev;
   if ((st = device_info(&dev)) != DASH_OK) return st;

@@ -409,3 +409,27 @@ def test_workspace_is_of_the_heads_that_have_a_weight(L, which):
     assert all(p is r or torch.equal(p, r) for p, r in zip(g, again)) and (ws[need:] == 255).all()
     with pytest.raises(ValueError, match="workspace"):
         dash.rope_norm_bwd(dq, dk, None, q, k, workspace=ws[:need - 1], **a)
+
+
+def test_abi_outputs_apart_from_everything_that_is_read(L):
+    """The weights' gradients and the workspace are written while frequencies, positions and both weights
+    are read: they lie apart from all of each, whichever part has a weight."""
+    at = 1 << 20  # never dereferenced: every call below is refused
+
+    def part(inp, out, D):
+        return _PART.pack(inp, out, 2, D, 1, *[4096] * 6)
+
+    def bwd(w=(0, 10 * at), dw=(0, 11 * at), ws=64 * at, bytes=1 << 20, pos=None):
+        wp, dp = _two(None, None), _two(None, None)
+        wp[0], wp[1] = w
+        dp[0], dp[1] = dw
+        return L.dash_rope_norm_bwd(part(at, 2 * at, 512) + part(3 * at, 4 * at, 16),
+                                    part(5 * at, 5 * at, 512) + part(6 * at, 6 * at, 16), 2, wp, dp, 1, 4,
+                                    8, 0, 0, 0, 8 * at, 1.0, 1e-5, pos, 1, 0, 1, 0, ws, bytes, None)
+    assert bwd(bytes=15) == 5  # (as far as the workspace's size nothing is amiss)
+    for bad in (dict(dw=(0, 8 * at + 16)), dict(ws=8 * at), dict(ws=9 * at, pos=9 * at),
+                dict(dw=(0, 9 * at + 8), pos=9 * at), dict(ws=10 * at - 64),
+                # the first part's weight, of 512 elements, behind what the second's gradient has
+                dict(w=(12 * at, 10 * at), dw=(0, 12 * at + 512)),
+                dict(w=(12 * at, 10 * at), ws=12 * at + 512)):
+        assert bwd(**bad) == 1, bad
