@@ -428,7 +428,7 @@ def test_abi_outputs_apart_from_everything_that_is_read(L):
                                     8, 0, 0, 0, 8 * at, 1.0, 1e-5, pos, 1, 0, 1, 0, ws, bytes, None)
     assert bwd(bytes=15) == 5  # (as far as the workspace's size nothing is amiss)
     for bad in (dict(dw=(0, 8 * at + 16)), dict(ws=8 * at), dict(ws=9 * at, pos=9 * at),
-                dict(dw=(0, 9 * at + 8), pos=9 * at), dict(ws=10 * at - 64),
+                dict(dw=(0, 9 * at + 8), pos=9 * at), dict(ws=10 * at - 16),
                 # the first part's weight, of 512 elements, behind what the second's gradient has
                 dict(w=(12 * at, 10 * at), dw=(0, 12 * at + 512)),
                 dict(w=(12 * at, 10 * at), ws=12 * at + 512)):
