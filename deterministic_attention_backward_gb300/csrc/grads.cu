@@ -251,7 +251,7 @@ struct Span {
 // Whether what is written meets nothing else, a tensor's own input in its place apart.
 bool apart_from_all(const dash_grad_t *g, int count, const Bytes (&others)[2], const float *given) {
   std::vector<Span> all;
-  all.reserve(2 * count + 3);
+  all.reserve(2 * (size_t)count + 3);
   auto add = [&](const void *p, long long bytes, int tensor, bool out) {
     const uintptr_t at = reinterpret_cast<uintptr_t>(p);
     if (bytes > 0 && p) all.push_back({at, at + (uintptr_t)bytes, tensor, out});
@@ -324,7 +324,7 @@ extern "C" {
 
 size_t dash_grad_norm_workspace_bytes(int count) {
   using namespace dash;
-  return count >= 0 ? (size_t)((count + kMaxTensors - 1) / kMaxTensors + 1) * kCtas * 8 : 0;
+  return count >= 0 ? (((size_t)count + kMaxTensors - 1) / kMaxTensors + 1) * kCtas * 8 : 0;
 }
 
 dash_status_t dash_grad_norm(const dash_grad_t *grads, int count, float *norm, void *workspace,

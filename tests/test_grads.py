@@ -278,3 +278,8 @@ def test_zeros_are_read_once(L):
         z[at] = 2.0 ** -149
         assert float(dash.grad_norm([z])) == 2.0 ** -149
         z[at] = 0.0
+
+
+def test_workspace_of_the_largest_counts(L):
+    for n in (0, 1, 512, 513, (1 << 31) - 512, (1 << 31) - 511, (1 << 31) - 1):
+        assert L.dash_grad_norm_workspace_bytes(n) == ((n + 511) // 512 + 1) * 608 * 8, n
