@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kThreads)
   const float n = given ? *given : norm_of(part, parts);
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = n;
   float by = n == 0.f ? 1.f : max_norm / (n + eps);
-  if (by > 1.f) by = 1.f;  // (a NaN stays)
+  if (by > 1.f || (max_norm == INFINITY && n == n)) by = 1.f;  // (a NaN stays)
   int t = g.count - 1;
   // a CTA's last chunk first
   const int mine = (g.chunks - 1 - (int)blockIdx.x) / (int)gridDim.x;

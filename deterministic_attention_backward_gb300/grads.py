@@ -89,7 +89,8 @@ def grad_clip(grads, max_norm: float, *, eps: float = 1e-6, norm=None, out=None,
     """Scale the gradients by min(1, max_norm / (norm + eps)), in place or into the tensors ``out``
     (one for each gradient, like it), and return the norm they had.  ``norm``: one that is known
     already, for example over more tensors than these.  Within the limit nothing is written in place.
-    A norm that is NaN makes every gradient NaN; one that is infinite makes the finite ones zero."""
+    A norm that is NaN makes every gradient NaN; one that is infinite makes the finite ones zero.  An
+    infinite ``max_norm`` clips nothing, whatever the norm's value."""
     grads = _list(grads)
     like = grads[0]
     if not max_norm >= 0 or not eps >= 0:

@@ -283,3 +283,18 @@ def test_zeros_are_read_once(L):
 def test_workspace_of_the_largest_counts(L):
     for n in (0, 1, 512, 513, (1 << 31) - 512, (1 << 31) - 511, (1 << 31) - 1):
         assert L.dash_grad_norm_workspace_bytes(n) == ((n + 511) // 512 + 1) * 608 * 8, n
+
+
+@gpu
+def test_an_infinite_limit_clips_nothing(L):
+    g, h = make((1000,), BF, 0), make((3000,), F32, 1)
+    g[77], h[5] = math.inf, -math.inf
+    mine, out = [g.clone(), h.clone()], [torch.empty_like(g), torch.empty_like(h)]
+    assert float(dash.grad_clip(mine, math.inf)) == math.inf
+    dash.grad_clip([g, h], math.inf, out=out)
+    dash.grad_clip(mine, math.inf, norm=torch.tensor(math.inf, device="cuda"))
+    for a, b, ref in zip(mine, out, (g, h)):
+        assert torch.equal(a, ref) and torch.equal(b, ref)
+    g[78] = math.nan
+    assert math.isnan(float(dash.grad_clip([g, h], math.inf)))
+    assert g.isnan().all() and h.isnan().all()
