@@ -526,215 +526,6 @@ dash_status_t dash_dense_withhold(int block);
  * workspace serves one call at a time. */
 typedef struct {
   const void *in;
-  void *out;
-  int heads, D, turn;
-  long long in_stride[3], out_stride[3]; /* batch, token, head */
-} dash_rope_part_t;
-/* Pair p of a head: elements p and p + rot/2 (half), or 2p and 2p + 1 (interleaved). */
-typedef enum { DASH_ROPE_HALF = 0, DASH_ROPE_INTERLEAVED = 1 } dash_rope_layout_t;
-
-/* Pair p (x, y) becomes magnitude * (x cos a - y sin a, y cos a + x sin a) with the angle
- * a = position * inv_freq[p] (radians; device array of rot/2 doubles); backward != 0 turns by
- * -a, which is the gradient.  The angle is formed in 128-bit fixed point modulo one turn and
- * rounded to fp32 there: off by pi 2^-25 at any position.  Positions: device int32
- * (positions64 == 0) or int64, the token's at element b * pos_stride_b + s * pos_stride_t, or NULL
- * for start + s.  Arithmetic in fp32, one rounding at the end.  1 to 3 parts of one element type;
- * rot even, <= 1024. */
-dash_status_t dash_rope(const dash_rope_part_t *parts, int nparts, int B, int S, int rot,
-                        dash_rope_layout_t layout, dash_dtype_t dtype, const double *inv_freq,
-                        float magnitude, const void *positions, int positions64,
-                        long long pos_stride_b, long long pos_stride_t, long long start,
-                        int backward, dash_stream_t stream);
-
-/* Norm of every head of q and k with the rotary turn behind it, v copied:
- *   y = R(w x rstd(x)),    rstd(x) = (mean(x^2) + eps)^-1/2 over the D elements of a head
- * parts as in dash_rope: the ones with turn != 0 (one or two) are normed and turned, the others
- * copied; heads of 512 at most.  weights[0], weights[1]: of the first and the second part that turns,
- * D elements of the heads' type or of fp32 (NULL: ones).  An output may be its input, as it lies.
- * Arithmetic in fp32, one rounding at the end. */
-dash_status_t dash_rope_norm_fwd(const dash_rope_part_t *parts, int nparts,
-                                 const void *const weights[2], int B, int S, int rot,
-                                 dash_rope_layout_t layout, dash_dtype_t dtype, dash_dtype_t wdtype,
-                                 const double *inv_freq, float magnitude, float eps,
-                                 const void *positions, int positions64, long long pos_stride_b,
-                                 long long pos_stride_t, long long start, dash_stream_t stream);
-/* Bytes of device workspace of dash_rope_norm_bwd for heads of D elements, of the parts whose dweights are
- * wanted (0: unsupported). */
-size_t dash_rope_norm_bwd_workspace_bytes(int D);
-/* Gradient of dash_rope_norm_fwd: parts hold the gradients of its outputs (in) and of its inputs
- * (out); x[i], for the i-th part that turns, the forward's input (in and in_stride; heads and D as in
- * the part).  dweights[i] receives the weight's gradient in its type (NULL: not wanted; both have
- * heads of one size), summed in an order that the sizes fix, wherever tensors lie.  A gradient may be written over the one
- * it comes from, as that lies. */
-dash_status_t dash_rope_norm_bwd(const dash_rope_part_t *parts, const dash_rope_part_t *x, int nparts,
-                                 const void *const weights[2], void *const dweights[2], int B, int S,
-                                 int rot, dash_rope_layout_t layout, dash_dtype_t dtype,
-                                 dash_dtype_t wdtype, const double *inv_freq, float magnitude,
-                                 float eps, const void *positions, int positions64,
-                                 long long pos_stride_b, long long pos_stride_t, long long start,
-                                 void *workspace, size_t workspace_bytes, dash_stream_t stream);
-
-/* Norm of rows, and the join of a residual stream with a branch between two norms.  With
- * rstd(v) = (mean(v^2) + eps)^-1/2 over the C elements of a row:
- *   y = skip_scale * x + branch_scale * gate * (a * rstd(a) * w_post)
- *   h = y * rstd(y) * w_next                                        (y before its rounding)
- * a NULL: a plain norm, y = x is not written and h = x rstd(x) w_next.  w_post NULL: the branch
- * is not normed; gate NULL: 1; w_next NULL: no h.  Tensors are `rows` rows of C contiguous
- * elements, the row strides (in elements) of x, a, y, h in `strides`; rstd_a and rstd_y
- * [rows] fp32 are kept for the backward (each written only where its norm is asked for).  The
- * weights [C] are of the rows' type or all fp32; gate is [rows / gate_rows, C], each row of it
- * serving gate_rows consecutive rows.  y and h may each be x or a itself (with the same stride),
- * not both the same.  fp32 arithmetic, one rounding per output.  Tensors are read by whole aligned
- * words of 16 bytes: of rows that 16 bytes do not divide, with up to 15 bytes beside. */
-dash_status_t dash_join_fwd(const void *x, const void *a, const void *w_post, const void *gate,
-                            const void *w_next, void *y, void *h, float *rstd_a, float *rstd_y,
-                            long long rows, int C, long long gate_rows,
-                            const long long strides[4], float skip_scale, float branch_scale,
-                            float eps, dash_dtype_t dtype, dash_dtype_t wdtype,
-                            dash_stream_t stream);
-/* Bytes of device workspace of dash_join_bwd (the CTAs' partial sums of the weight gradients);
- * gate_rows 0 where there is no gate, join 0 for a plain norm; 0 on bad sizes. */
-size_t dash_join_bwd_workspace_bytes(long long rows, int C, long long gate_rows, int join,
-                                     dash_dtype_t dtype);
-/* Gradient of dash_join_fwd: dy, dh are the gradients of y and h (dy may be NULL where nothing
- * else uses y; dh is read where w_next is given), y the forward's output (x for a plain norm,
- * whose dy is added to dx: the gradient of the residual stream beside the norm), a the branch.  y
- * is taken as it is, rounded, where the forward's h came from it unrounded.
- * Writes dx, da and, in the weights' type, dw_post, dgate, dw_next (each where its weight is
- * given).  Row strides of dy, dh, y, a, dx, da in `strides`.  dx and da may each be dy, dh, y or a
- * itself (with the same stride), not both the same.  The weight gradients are summed in an order
- * that the sizes, strides and alignments fix: the same bits on every run. */
-dash_status_t dash_join_bwd(const void *dy, const void *dh, const void *y, const void *a,
-                            const void *w_post, const void *gate, const void *w_next,
-                            const float *rstd_a, const float *rstd_y, void *dx, void *da,
-                            void *dw_post, void *dgate, void *dw_next, long long rows, int C,
-                            long long gate_rows, const long long strides[6], float skip_scale,
-                            float branch_scale, dash_dtype_t dtype, dash_dtype_t wdtype,
-                            void *workspace, size_t workspace_bytes, dash_stream_t stream);
-
-/* Differential attention, the difference of two softmax maps with a learned weight:
- *   O = P1 V - lam P2 V,     Pm = softmax(scale * Qm Km^T + mask)
- *   q [B,S,2H,d]   k [B,S,2Hkv,d]   v, o, o2, dout, dv like them with heads of 2d:
- *   v [B,S,Hkv,2d]   o, o2, dout [B,S,H,2d]   dq like q, dk like k   (bf16, contiguous)
- * Head pair h reads the query maps 2h and 2h+1; with n = h / group, group = H / Hkv, the key
- * maps 2n and 2n+1 and the value head n.  lam: one weight per head pair [H], or per token and
- * head pair [B,S,H] (lam_per_token), bf16 or fp32; any value.  d = 32 or 64 (value heads of 64
- * or 128), any S >= 1, masks and scale as dash_attn_fwd (scale <= 0: 1/sqrt(d)).
- * Forward: writes o, o2 = P2 V and lse [B,2H,S] fp32 (natural log, of map 2h+m at 2h+m), which
- * the backward takes; workspace: its status block, of one call at a time.  No output overlaps an
- * input or another output. */
-size_t dash_diff_fwd_workspace_bytes(int B, int S, int H, int d);
-dash_status_t dash_diff_fwd(const void *q, const void *k, const void *v, const void *lam, void *o,
-                            void *o2, float *lse, int B, int S, int H, int group, int d,
-                            float scale, dash_mask_t mask, dash_dtype_t lam_dtype,
-                            int lam_per_token, void *workspace, size_t workspace_bytes,
-                            dash_stream_t stream);
-/* The same for a forward whose backward follows: also writes rest [2,B,S,H,2d] bf16, what o and o2
- * lose by their rounding (NULL: not written). */
-dash_status_t dash_diff_fwd_rest(const void *q, const void *k, const void *v, const void *lam,
-                                 void *o, void *o2, void *rest, float *lse, int B, int S, int H,
-                                 int group, int d, float scale, dash_mask_t mask,
-                                 dash_dtype_t lam_dtype, int lam_per_token, void *workspace,
-                                 size_t workspace_bytes, dash_stream_t stream);
-/* Backward: dq, dk, dv and dlam (lam's shape and type).  Deterministic: every sum is formed in
- * a fixed order without atomics, bit-identical on every run; dk and dv sum a group's query heads
- * in ascending order (key tiles that the sizes put into pieces: within a piece, then the pieces).
- * The row terms D = dO . Om of dq come from o and o2 as they are given (rounded, which the more
- * peaked the maps are the more of dq's error it makes; dash_diff_bwd_rest adds what the rounding
- * lost); those of dk, and dlam, from the fp32 sums of Pm dP.  Workspace: status block, row
- * vectors of B*H*Sp*20 bytes (Sp = S rounded up to 128), partial sums of dlam and, 80 MB at most,
- * of key tiles that are formed in pieces; dash_attn_status reads either status word. */
-size_t dash_diff_bwd_workspace_bytes(int B, int S, int H, int d);
-dash_status_t dash_diff_bwd(const void *q, const void *k, const void *v, const void *o,
-                            const void *o2, const void *dout, const float *lse, const void *lam,
-                            void *dq, void *dk, void *dv, void *dlam, int B, int S, int H,
-                            int group, int d, float scale, dash_mask_t mask,
-                            dash_dtype_t lam_dtype, int lam_per_token, void *workspace,
-                            size_t workspace_bytes, dash_stream_t stream);
-/* The same with the forward's rest (NULL: none). */
-dash_status_t dash_diff_bwd_rest(const void *q, const void *k, const void *v, const void *o,
-                                 const void *o2, const void *rest, const void *dout,
-                                 const float *lse, const void *lam, void *dq, void *dk, void *dv,
-                                 void *dlam, int B, int S, int H, int group, int d, float scale,
-                                 dash_mask_t mask, dash_dtype_t lam_dtype, int lam_per_token,
-                                 void *workspace, size_t workspace_bytes, dash_stream_t stream);
-
-
-/* For tests of failure detection, process-wide: from the next call on the loads of every CTA of one
- * kernel (1: the forward, 2: dQ's, 3: dK/dV's; 0: of none any more) end before its block `block`
- * (128 keys; 64 queries in dK/dV's), so that the waits for it run out. */
-dash_status_t dash_diff_withhold(int kernel, int block);
-
-/* Matrix product with its epilogue, in bf16 or fp16 with fp32 sums:
- *   z = x w + bias      g = x w_gate + bias_gate      y = residual + act(z) g
- * without w_gate y = residual + act(z); bias, bias_gate, residual may be NULL.  x [M, K] and y,
- * residual [M, N] are rows at a stride (in elements); w and w_gate are [K, N] rows (DASH_DENSE_KN)
- * or [N, K] rows (DASH_DENSE_NK); biases [N] contiguous, of the rows' type.  z and gate, where not
- * NULL, receive z and g for the backward, their fp32 values rounded to the upper 24 bits: M rows of 16-bit words
- * (the upper ones), then M rows of bytes, Np elements each, Np = N rounded up to 16 (3 M Np bytes in all,
- * on 16 bytes).  y may be the residual itself
- * (at its stride); beside that no output shares memory with another tensor of the call.  Sums run
- * in an order that the sizes fix, one rounding at the end.  Operands that do not begin on 16 bytes,
- * or whose stride is no multiple of that, are copied into the workspace first.
- * The workspace holds a status block (dash_attn_status) and serves one call at a time.  Its size
- * follows from the same arguments as the call (pointers' alignment and strides among them); 0 where
- * the call would be refused. */
-typedef enum {
-  DASH_ACT_NONE = 0,
-  DASH_ACT_RELU = 1,
-  DASH_ACT_GELU = 2,      /* z/2 (1 + erf(z / sqrt 2)) */
-  DASH_ACT_GELU_TANH = 3, /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
-  DASH_ACT_SILU = 4
-} dash_act_t;
-typedef enum { DASH_DENSE_KN = 0, DASH_DENSE_NK = 1 } dash_dense_order_t;
-typedef struct {
-  const void *x, *w, *w_gate, *bias, *bias_gate, *residual;
-  void *y, *z, *gate;
-  long long x_stride, w_stride, w_gate_stride, residual_stride, y_stride;
-  int M, K, N, order, act, dtype;
-} dash_dense_fwd_t;
-size_t dash_dense_fwd_workspace_bytes(const dash_dense_fwd_t *args);
-dash_status_t dash_dense_fwd(const dash_dense_fwd_t *args, void *workspace, size_t workspace_bytes,
-                             dash_stream_t stream);
-/* Gradient: from dy [M, N], x, the weights and what the forward kept (z where act is not NONE or
- * there is a gate, gate with it; both as the forward kept them)
- *   dz = dy g act'(z)   dgate = dy act(z)
- *   dx = dz w^T + dgate w_gate^T   dw = x^T dz   dw_gate = x^T dgate   dbias, dbias_gate = sums
- * each where its pointer is not NULL (dw and dw_gate in the weights' order).  dz and dgate are
- * rounded to the rows' type for the tensor core (of up to 2^16 elements what that loses is multiplied too),
- * the biases' gradients are sums of the unrounded ones.  The residual's gradient is dy.  Deterministic;
- * M = 0 clears the weights' gradients. */
-typedef struct {
-  const void *dy, *x, *w, *w_gate, *z, *gate;
-  void *dx, *dw, *dw_gate, *dbias, *dbias_gate;
-  long long dy_stride, x_stride, w_stride, w_gate_stride, dx_stride, dw_stride, dw_gate_stride;
-  int M, K, N, order, act, dtype;
-} dash_dense_bwd_t;
-size_t dash_dense_bwd_workspace_bytes(const dash_dense_bwd_t *args);
-dash_status_t dash_dense_bwd(const dash_dense_bwd_t *args, void *workspace, size_t workspace_bytes,
-                             dash_stream_t stream);
-/* The same with dz and dgate in one term (rounded to the rows' type) or in two (what that loses as well:
- * 16 bits and more of them, twice the products), terms = 1 or 2; 0, as above, takes two of up to 2^16 elements
- * of dz.  Infinities and NaN come out as of one term. */
-size_t dash_dense_bwd_terms_workspace_bytes(const dash_dense_bwd_t *args, int terms);
-dash_status_t dash_dense_bwd_terms(const dash_dense_bwd_t *args, int terms, void *workspace,
-                                   size_t workspace_bytes, dash_stream_t stream);
-/* For tests of failure detection, process-wide: from the next call on the loads of every CTA of the
- * product kernel end before its block `block` of 64 contraction elements (-1: of none any more), so
- * that the waits for it run out. */
-dash_status_t dash_dense_withhold(int block);
-
-/* The norm over many gradients, and clipping by it:
- *   norm = sqrt(sum over all tensors of g^2)      out = g * min(1, max_norm / (norm + eps))
- * n elements each (0 too), dense in memory, of any type; `grads` is a host array that is read before
- * the call returns.  Squares are added in fp32 within runs of a few hundred elements and in fp64
- * beyond, in an order that the sizes fix, wherever the tensors lie; magnitudes whose squares fp32 does not
- * hold are scaled.  out may be in itself; beside that nothing written shares memory with another tensor (a tensor that
- * occurs twice is refused by dash_grad_clip).  A factor of 1 leaves tensors in place untouched (an
- * infinite max_norm's, whatever the norm is); a norm that is NaN gives NaN.  dash_grad_clip forms the norm and writes it to `norm`, or takes `given` (then
- * `norm` may be NULL, and no workspace is needed).  A workspace serves one call at a time. */
-typedef struct {
-  const void *in;
   void *out; /* not read by dash_grad_norm */
   long long n;
   int dtype, unused;
