@@ -100,6 +100,14 @@ def _operator_functions():
     class Dense(torch.autograd.Function):
         """residual + act(x w), or act(x w) (x w_gate): products with their epilogue."""
 
+        @classmethod
+        def call(cls, x, w, w_gate=None, residual=None, act="none"):
+            # (in ``forward`` gradients are off whether a backward is to follow or not)
+            if torch.is_grad_enabled() and any(t is not None and t.requires_grad
+                                               for t in (x, w, w_gate, residual)):
+                return cls.apply(x, w, w_gate, residual, act)
+            return dash.dense_fwd(x, w, act=act, w_gate=w_gate, residual=residual, keep=False)[0]
+
         @staticmethod
         def forward(ctx, x, w, w_gate, residual, act):
             y, kept = dash.dense_fwd(x, w, act=act, w_gate=w_gate, residual=residual)
@@ -258,7 +266,7 @@ class Block:
         else:
             hid = self._rms(x, self.n1)
         fused, joins = self.fused_dense, self.fused_norms
-        qkv = self.Dense.apply(hid, self.wqkv, None, None, "none") if fused else hid @ self.wqkv
+        qkv = self.Dense.call(hid, self.wqkv) if fused else hid @ self.wqkv
         if self.nq is not None:
             q, k, v = self.NormRotary.apply(qkv, self.nq, self.nk, self.freqs, *self.parts)
         elif self.freqs is not None:
@@ -277,15 +285,15 @@ class Block:
         if self.nh is not None:
             o = self.Norm.apply(o, self.nh)
         o = o.reshape(B, S, self.h * self.d)
-        a = self.Dense.apply(o, self.wo, None, None if joins else x, "none") if fused else o @ self.wo
+        a = self.Dense.call(o, self.wo, residual=None if joins else x) if fused else o @ self.wo
         if joins:
             x, hid = self.Join.apply(x, a, self.p1, self.n2)
         else:
             x = a if fused else x + a
             hid = self._rms(x, self.n2)
         if fused:
-            m = self.Dense.apply(hid, self.w1, self.w3, None, "silu")
-            m = self.Dense.apply(m, self.w2, None, None if joins else x, "none")
+            m = self.Dense.call(hid, self.w1, self.w3, act="silu")
+            m = self.Dense.call(m, self.w2, residual=None if joins else x)
         else:
             m = (F.silu(hid @ self.w1) * (hid @ self.w3)) @ self.w2
         if joins:

@@ -258,3 +258,32 @@ def test_block_options_on_the_host():
         assert torch.equal(t, u)
     with pytest.raises(ValueError, match="rotary"):
         block.Block(**sizes, qk_norm=True)
+
+
+def test_block_keeps_nothing_where_no_backward_follows(monkeypatch):
+    """What the backward of a product needs is kept only where gradients are on and one of its operands has
+    one."""
+    asked = []
+
+    def dense_fwd(x, w, *, act, w_gate, residual, keep=True):
+        asked.append(keep)
+        return torch.zeros(*x.shape[:-1], w.shape[1]), None
+    monkeypatch.setattr(dash, "dense_fwd", dense_fwd, raising=False)
+    blk = block.Block(hidden=128, heads=2, kv_heads=1, head_dim=64, ffn=128, device="cpu", fused_dense=True)
+    x = torch.zeros(1, 3, 128)
+    assert blk.Dense.call(x, blk.w1, blk.w3, act="silu").requires_grad and asked.pop()
+    with torch.no_grad():
+        assert not blk.Dense.call(x, blk.w1, blk.w3, act="silu").requires_grad and not asked.pop()
+    assert not blk.Dense.call(x, blk.w1.detach(), blk.w3.detach()).requires_grad and not asked.pop()
+    assert blk.Dense.call(x, blk.w1.detach(), residual=x[..., :128].clone().requires_grad_()).requires_grad
+    assert asked.pop() and not asked
+
+
+@gpu
+def test_block_without_gradients_gives_the_same_bits():
+    for options in (dict(fused_dense=True), dict(rotary=100.0, qk_norm=True, fused_dense=True, fused_norms=True)):
+        blk = block.Block(hidden=512, heads=4, kv_heads=2, head_dim=128, ffn=776, **options)
+        x = torch.linspace(-1, 1, 96 * 512, device="cuda").to(torch.bfloat16).view(1, 96, 512)
+        with torch.no_grad():
+            y = blk(x, "auto")
+        assert not y.requires_grad and torch.equal(blk(x, "auto"), y)
