@@ -698,3 +698,37 @@ def test_special_values_are_kept(L):
     z = unpacked(kept, 6, 16)[0, :, 0]
     assert z[0].isnan() and z[1] == math.inf and z[2] == -math.inf and z[4] == 0
     assert z[3] == x[3, 0].float() and abs(z[5] - x[5, 0].float()) <= 2.0 ** -16 * 1e-38
+
+
+@gpu
+@pytest.mark.parametrize("size", [(40, 256, 300), (300, 264, 200)], ids=str)
+def test_special_values_come_and_go_in_a_captured_backward(L, size):
+    """What flags a sum that is not finite is cleared by every call: replays with and without infinities, and
+    two graphs that share a workspace, one after the other."""
+    M, K, N = size
+    x, w, a, _ = case(*size, "kn", BF, EPILOGUES[1])
+    _, kept = dash.dense_fwd(x, w, **a)
+    dys = [make((M, N), BF, s) for s in (9, 10)]
+    clean = [dash.dense_bwd(dy, x, w, kept, **a) for dy in dys]
+    ws = torch.full((dash.dense_bwd_workspace_bytes(dys[0], x, w, kept, **a),), 255, dtype=torch.uint8,
+                    device="cuda")
+    graphs, outs = [], []
+    for dy in dys:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(dash.dense_bwd(dy, x, w, kept, workspace=ws, **a))
+        graphs.append(g)
+    good = x[1, 2].clone()
+    for bad in (math.inf, 0.0, math.inf, math.nan, 0.0):
+        x[1, 2] = bad if bad else good
+        for g, dy, out, ref in zip(graphs, dys, outs, clean):
+            g.replay()
+            if not bad:
+                assert all(p is q or torch.equal(p, q) for p, q in zip(out, ref))
+                continue
+            one = dash.dense_bwd(dy, x, w, kept, terms=1, **a)
+            for i in (0, 1, 3):
+                assert torch.equal(out[i].isnan(), one[i].isnan())
+                assert torch.equal(out[i].isinf(), one[i].isinf())
+            assert not out[1][2].isfinite().any() and torch.equal(out[1][3], ref[1][3])
+    dash.status(ws)
